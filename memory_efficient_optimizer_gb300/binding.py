@@ -1,5 +1,5 @@
-"""ctypes binding of the C ABI in include/adafactor.h, include/lamb.h and
-include/came.h (argument marshalling only).
+"""ctypes binding of the C ABI in include/adafactor.h, include/lamb.h,
+include/came.h and include/losses.h (argument marshalling only).
 
 Every function here has the name of the C entry point it calls and does no
 arithmetic of the method: all of the step runs in the CUDA library.  Loading
@@ -42,6 +42,16 @@ LAMB_EXPORTS = (
     "lamb_validate", "lamb_workspace_size", "lamb_step", "lamb_trust_ratios", "lamb_profile_enable",
     "lamb_profile_read", "lamb_num_kernels", "lamb_kernel_name",
 )
+
+# Entry points declared in include/losses.h.
+LOSS_EXPORTS = (
+    "loss_workspace_size", "loss_token_logprobs", "loss_token_logprobs_backward", "loss_policy", "loss_preference",
+    "loss_distill", "loss_profile_enable", "loss_profile_read", "loss_num_kernels", "loss_kernel_name",
+)
+LOSS_INT32 = 0
+LOSS_INT64 = 1
+LOSS_MAX_TOP_K = 1024
+LOSS_PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
 
 
 class adaf_tensor(ctypes.Structure):
@@ -97,6 +107,43 @@ class came_hparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("eps1", ctypes.c_double), ("eps2", ctypes.c_double),
                 ("clip_threshold", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("beta3", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
+class loss_logits(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64), ("seq", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("temperature", ctypes.c_double)]
+
+
+class loss_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
+
+
+class loss_targets(ctypes.Structure):
+    _fields_ = [("rows", loss_rows), ("dtype", ctypes.c_int32), ("ignore_index", ctypes.c_int64)]
+
+
+class loss_grad(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("scale", ctypes.c_double)]
+
+
+class loss_policy_args(ctypes.Structure):
+    _fields_ = [("advantages", loss_rows), ("old_logp", loss_rows), ("ref_logp", loss_rows), ("weights", loss_rows),
+                ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("kl_coef", ctypes.c_double)]
+
+
+class loss_preference_args(ctypes.Structure):
+    _fields_ = [("ref_logp", loss_rows), ("pairs", ctypes.c_int64), ("seq_offsets", ctypes.c_void_p),
+                ("offsets_dtype", ctypes.c_int32), ("kind", ctypes.c_int32), ("average", ctypes.c_int32),
+                ("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double), ("margin", ctypes.c_double)]
+
+
+class loss_distill_args(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("ids_dtype", ctypes.c_int32), ("ids_stride_b", ctypes.c_int64),
+                ("ids_stride_s", ctypes.c_int64), ("values", ctypes.c_void_p), ("values_dtype", ctypes.c_int32),
+                ("values_stride_b", ctypes.c_int64), ("values_stride_s", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("lse", loss_rows), ("mask", loss_rows), ("weights", loss_rows)]
 
 
 class AdafactorError(RuntimeError):
@@ -205,6 +252,33 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.lamb_num_kernels.argtypes = []
         lib.lamb_kernel_name.restype = ctypes.c_char_p
         lib.lamb_kernel_name.argtypes = [ctypes.c_int32]
+        lib.loss_workspace_size.restype = ctypes.c_int
+        lib.loss_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int64, P(ctypes.c_size_t)]
+        lib.loss_token_logprobs.restype = ctypes.c_int
+        lib.loss_token_logprobs.argtypes = [P(loss_logits), P(loss_targets), ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p]
+        lib.loss_token_logprobs_backward.restype = ctypes.c_int
+        lib.loss_token_logprobs_backward.argtypes = [P(loss_logits), P(loss_targets), ctypes.c_void_p, P(loss_rows),
+                                                     P(loss_grad), ctypes.c_void_p]
+        lib.loss_policy.restype = ctypes.c_int
+        lib.loss_policy.argtypes = [P(loss_logits), P(loss_targets), P(loss_policy_args), P(loss_grad),
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p]
+        lib.loss_preference.restype = ctypes.c_int
+        lib.loss_preference.argtypes = [P(loss_logits), P(loss_targets), P(loss_preference_args), P(loss_grad),
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.loss_distill.restype = ctypes.c_int
+        lib.loss_distill.argtypes = [P(loss_logits), P(loss_distill_args), P(loss_grad), ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.loss_profile_enable.restype = ctypes.c_int
+        lib.loss_profile_enable.argtypes = [ctypes.c_int32]
+        lib.loss_profile_read.restype = ctypes.c_int
+        lib.loss_profile_read.argtypes = [P(ctypes.c_double), P(ctypes.c_int64), ctypes.c_int32]
+        lib.loss_num_kernels.restype = ctypes.c_int32
+        lib.loss_num_kernels.argtypes = []
+        lib.loss_kernel_name.restype = ctypes.c_char_p
+        lib.loss_kernel_name.argtypes = [ctypes.c_int32]
         _lib = lib
         return lib
 
@@ -411,3 +485,57 @@ def came_profile_read() -> dict:
     launches = (ctypes.c_int64 * nk)()
     _check(load().came_profile_read(ms, launches, nk))
     return {came_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}
+
+
+# ---- losses over a vocabulary (include/losses.h) ------------------------------
+
+def loss_workspace_size(tokens: int, pairs: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().loss_workspace_size(int(tokens), int(pairs), ctypes.byref(out)))
+    return int(out.value)
+
+
+def loss_token_logprobs(x: loss_logits, y: loss_targets, logp: int, stats: int, stream: int) -> None:
+    _check(load().loss_token_logprobs(x, y, logp, stats, stream))
+
+
+def loss_token_logprobs_backward(x: loss_logits, y: loss_targets, stats: int, grad_logp: loss_rows,
+                                 grad: loss_grad, stream: int) -> None:
+    _check(load().loss_token_logprobs_backward(x, y, stats, grad_logp, grad, stream))
+
+
+def loss_policy(x: loss_logits, y: loss_targets, args: loss_policy_args, grad, loss: int, logp: int,
+                token_loss: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().loss_policy(x, y, args, grad, loss, logp, token_loss, workspace, workspace_bytes, stream))
+
+
+def loss_preference(x: loss_logits, y: loss_targets, args: loss_preference_args, grad, loss: int, pair_loss: int,
+                    rewards: int, logp: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().loss_preference(x, y, args, grad, loss, pair_loss, rewards, logp, workspace, workspace_bytes,
+                                  stream))
+
+
+def loss_distill(x: loss_logits, args: loss_distill_args, grad, loss: int, token_loss: int, workspace: int,
+                 workspace_bytes: int, stream: int) -> None:
+    _check(load().loss_distill(x, args, grad, loss, token_loss, workspace, workspace_bytes, stream))
+
+
+def loss_profile_enable(on: bool) -> None:
+    _check(load().loss_profile_enable(1 if on else 0))
+
+
+def loss_num_kernels() -> int:
+    return int(load().loss_num_kernels())
+
+
+def loss_kernel_name(k: int) -> str:
+    return load().loss_kernel_name(int(k)).decode()
+
+
+def loss_profile_read() -> dict:
+    """{kernel name: (total ms, launches)} for the loss events recorded since the last read."""
+    nk = loss_num_kernels()
+    ms = (ctypes.c_double * nk)()
+    launches = (ctypes.c_int64 * nk)()
+    _check(load().loss_profile_read(ms, launches, nk))
+    return {loss_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}
