@@ -10,13 +10,13 @@
 //   k_loss_row      one row: m, s, the operator's scalars, the gradient row
 //   k_loss_grad     gradient rows from kept m, s and the tokens' coefficients
 //   k_loss_pair     a pair's sums over tokens, its loss and its coefficients
-//   k_loss_finish   sum of the tokens' (or pairs') losses in a fixed order
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -28,9 +28,12 @@
 
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kTile = 8192;        // values of a row between two looks at the teacher's entries
-constexpr int kFinishThreads = 1024;
+constexpr int kMaxThreads = 512;   // of a CTA of k_loss_row
+constexpr int kGradThreads = 256;
+constexpr int kPairThreads = 256;
+constexpr int kCountThreads = 1024;
+constexpr int kGroup = 256;        // tokens of a partial sum of the loss
+constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxVocab = (int64_t{1} << 30) - 1;
 constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1;
 
@@ -56,7 +59,11 @@ struct LossArgs {
   float* token_loss;
   float2* stats;                  // [tokens]: m, s
   int64_t* count;                 // counted tokens
-  float* part;                    // [tokens]: w l
+  float* part;                    // [tokens]: w l, or l
+  double* group_part;             // [ceil(tokens / kGroup)]
+  unsigned* tickets;              // [1 + ceil(tokens / kGroup)]; k_loss_pair: [1]
+  int32_t vecs_per_cta;           // k_loss_row: vectors of a row for a CTA
+  int32_t tiles;                  // k_loss_grad: CTAs of a row
   // policy
   Rows adv, old, ref, weights;
   float lo, hi, kl;
@@ -121,63 +128,391 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return t;
 }
 
-struct Soft {
-  float m, s, top;  // largest value, sum of terms (of the words not listed, for distill), sum over the listed words
+// ---- vectors of a row ----------------------------------------------------------
+// A row is read as aligned 16-byte vectors.  Vector i of a row that starts
+// `lead` values after a 16-byte boundary holds its values i kN - lead ..; the
+// first and the last may reach past the row and are then loaded value by
+// value, with -inf outside.
+template <typename T> constexpr int kN = 16 / static_cast<int>(sizeof(T));
+constexpr int kV = 8;               // vectors a thread keeps: 128 bytes of the row
+constexpr uint32_t kNegInf2 = 0xff80ff80u;
+template <typename T> constexpr uint32_t kNegInf = sizeof(T) == 2 ? kNegInf2 : 0xff800000u;
+
+template <typename T>
+struct Row {
+  const T* x;
+  int lead, n, vecs;  // values before the row in its first vector, values, vectors
+  __device__ __forceinline__ Row(const T* p, int vocab) : x(p), n(vocab) {
+    lead = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    vecs = (lead + n + kN<T> - 1) / kN<T>;
+  }
+  __device__ __forceinline__ bool whole(int i) const {
+    const int e = i * kN<T> - lead;
+    return e >= 0 && e + kN<T> <= n;
+  }
+  __device__ __forceinline__ bool ragged() const { return lead != 0 || vecs * kN<T> != lead + n; }
+  __device__ __forceinline__ const uint4* at(int i) const {
+    return reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t{15}) + i;
+  }
 };
-__device__ __forceinline__ Soft join(const Soft& p, const Soft& q, float c) {
-  Soft r;
-  r.m = fmaxf(p.m, q.m);
-  const float sh = shift_of(r.m);
-  const float fp = term(p.m, sh, c), fq = term(q.m, sh, c);
-  r.s = p.s * fp + q.s * fq;
-  r.top = p.top * fp + q.top * fq;
+
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+
+// Value j of a vector, replaced.
+template <typename T>
+__device__ __forceinline__ void put(uint4& w, int j, uint32_t bits) {
+  uint32_t* q = &w.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (sizeof(T) == 4) {
+      if (j == k) q[k] = bits;
+    } else {
+      if (j == 2 * k) q[k] = (q[k] & 0xffff0000u) | bits;
+      if (j == 2 * k + 1) q[k] = (q[k] & 0xffffu) | (bits << 16);
+    }
+  }
+}
+
+// Vectors i = first + k step < last of a row.
+template <typename T>
+__device__ __forceinline__ void load_tile(uint4 (&w)[kV], const Row<T>& r, int first, int step, int last) {
+#pragma unroll
+  for (int k = 0; k < kV; ++k) {
+    const int i = first + k * step;
+    w[k] = make_uint4(kNegInf<T>, kNegInf<T>, kNegInf<T>, kNegInf<T>);
+    if (i < last && r.whole(i)) w[k] = __ldcs(r.at(i));
+  }
+  if (r.ragged()) {
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const int i = first + k * step;
+      if (i < last && !r.whole(i)) {
+#pragma unroll
+        for (int j = 0; j < kN<T>; ++j) {
+          const int e = i * kN<T> - r.lead + j;
+          if (e >= 0 && e < r.n) put<T>(w[k], j, bits_of(r.x[e]));
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// Values of a vector, two at a time.
+template <typename T>
+__device__ __forceinline__ float2 pair_at(const uint4& w, int j) {
+  const uint32_t* q = &w.x;
+  if (sizeof(T) == 4) return make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1]));
+  return pair_of(q[j]);
+}
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+// term() of two values.
+__device__ __forceinline__ float2 terms(float2 x, float m, float c) {
+  const float2 z = __fmul2_rn(__fadd2_rn(x, twice(-m)), twice(c));
+  return make_float2(ex2(z.x), ex2(z.y));
+}
+
+// Largest value of a tile over the warp (NaN is left out: it shows in the sum).
+template <typename T>
+__device__ __forceinline__ float tile_max(const uint4 (&w)[kV]) {
+  float m;
+  if (sizeof(T) == 2) {
+    __nv_bfloat162 a;
+    memcpy(&a, &w[0].x, 4);
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        __nv_bfloat162 b;
+        memcpy(&b, &q[t], 4);
+        a = __hmax2(a, b);
+      }
+    }
+    m = fmaxf(__low2float(a), __high2float(a));
+  } else {
+    m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[k].x), __uint_as_float(w[k].y)),
+                         fmaxf(__uint_as_float(w[k].z), __uint_as_float(w[k].w))));
+  }
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
   return r;
 }
-__device__ __forceinline__ Soft block_join(Soft v, float c, Soft* red) {
+
+// Adds the terms of a tile; with `listed` (a byte a vector, a bit a value) the
+// listed words' terms go to `top`.
+template <typename T, bool LISTED>
+__device__ __forceinline__ void tile_sum(const uint4 (&w)[kV], float m, float c, const uint8_t* listed, int step,
+                                         float& sum, float& top) {
+  float2 acc = make_float2(0.f, 0.f), acc2 = acc;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Soft w;
-    w.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-    w.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-    w.top = __shfl_xor_sync(0xffffffffu, v.top, o);
-    v = join(v, w, c);
+  for (int k = 0; k < kV; ++k) {
+    if (LISTED) {
+      const uint32_t on = listed[k * step];
+      if (on != 0) {
+#pragma unroll
+        for (int j = 0; j < kN<T> / 2; ++j) {
+          const float2 e = terms(pair_at<T>(w[k], j), m, c);
+          sum += (on >> (2 * j) & 1 ? 0.f : e.x) + (on >> (2 * j + 1) & 1 ? 0.f : e.y);
+          top += (on >> (2 * j) & 1 ? e.x : 0.f) + (on >> (2 * j + 1) & 1 ? e.y : 0.f);
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kN<T> / 2; j += 2) {
+      acc = __fadd2_rn(acc, terms(pair_at<T>(w[k], j), m, c));
+      acc2 = __fadd2_rn(acc2, terms(pair_at<T>(w[k], j + 1), m, c));
+    }
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  Soft t = red[0];
-  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) t = join(t, red[w], c);
-  return t;
+  sum += (acc.x + acc.y) + (acc2.x + acc2.y);
+}
+
+// Stores of a gradient row, from vectors in the logits' phase.
+template <typename T>
+struct GradRow {
+  T* g;
+  int n, lead, shift;  // values before the row in its first 16 bytes; that minus the logits' lead, mod kN
+  __device__ __forceinline__ GradRow(T* p, int vocab, int x_lead) : g(p), n(vocab) {
+    lead = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    shift = (lead - x_lead) & (kN<T> - 1);
+  }
+  __device__ __forceinline__ void value(const uint4& w, int e0, int j) const {
+    const int e = e0 + j;
+    if (e < 0 || e >= n) return;
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+    if (sizeof(T) == 4) {
+      reinterpret_cast<uint32_t*>(g)[e] = q[j & 3];
+    } else {
+      reinterpret_cast<uint16_t*>(g)[e] = static_cast<uint16_t>(q[(j >> 1) & 3] >> (16 * (j & 1)));
+    }
+  }
+  // Vector of values e0 .. e0 + kN of the row; `in` false: not this thread's.
+  // Every lane of the warp calls, lanes holding consecutive vectors.
+  __device__ __forceinline__ void store(const uint4& w, int e0, bool in) const {
+    if (shift == 0) {
+      if (!in) return;
+      if (e0 >= 0 && e0 + kN<T> <= n) {
+        __stcs(reinterpret_cast<uint4*>(g + e0), w);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN<T>; ++j) value(w, e0, j);
+      }
+      return;
+    }
+    // The gradient's aligned vectors straddle two of these: each lane joins
+    // its tail to the head of the next lane's and stores that; a warp's first
+    // head and last tail go value by value.
+    const int lane = threadIdx.x & 31, tail = kN<T> - shift;  // first value of the aligned vector that starts here
+    uint32_t q[8] = {w.x, w.y, w.z, w.w, 0, 0, 0, 0};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) q[4 + t] = __shfl_down_sync(0xffffffffu, q[t], 1);
+    const bool next_in = __shfl_down_sync(0xffffffffu, static_cast<int>(in), 1) != 0;
+    const bool joint = in && next_in && lane < 31 && e0 + tail >= 0 && e0 + tail + kN<T> <= n;
+    const bool before = __shfl_up_sync(0xffffffffu, static_cast<int>(joint), 1) != 0 && lane > 0;
+    if (joint) {
+      const int bytes = tail * static_cast<int>(sizeof(T));
+      if (bytes & 8) {
+#pragma unroll
+        for (int t = 0; t < 6; ++t) q[t] = q[t + 2];
+      }
+      if (bytes & 4) {
+#pragma unroll
+        for (int t = 0; t < 5; ++t) q[t] = q[t + 1];
+      }
+      const uint32_t by = 8 * (bytes & 3);
+      const uint4 o = make_uint4(__funnelshift_r(q[0], q[1], by), __funnelshift_r(q[1], q[2], by),
+                                 __funnelshift_r(q[2], q[3], by), __funnelshift_r(q[3], q[4], by));
+      __stcs(reinterpret_cast<uint4*>(g + e0 + tail), o);
+    }
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < kN<T>; ++j) {
+        if (j < tail ? !before : !joint) value(w, e0, j);
+      }
+    }
+  }
+  // The part of the row that CTA `rank` of `ranks` has, as zeros.
+  __device__ __forceinline__ void zero(int rank, int ranks) const {
+    const int vecs = (lead + n + kN<T> - 1) / kN<T>, per = (vecs + ranks - 1) / ranks;
+    const int last = min(vecs, (rank + 1) * per);
+    for (int i = rank * per + threadIdx.x; i < last; i += blockDim.x) {
+      const int e0 = i * kN<T> - lead;
+      if (e0 >= 0 && e0 + kN<T> <= n) {
+        __stcs(reinterpret_cast<uint4*>(g + e0), make_uint4(0, 0, 0, 0));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kN<T>; ++j) value(make_uint4(0, 0, 0, 0), e0, j);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  uint32_t r;
+  memcpy(&r, &b, 4);
+  return r;
+}
+// scale exp((x - m) / T) of a vector, rounded to its type.
+template <typename T>
+__device__ __forceinline__ uint4 scaled_terms(const uint4& w, float m, float c, float scale) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < kN<T> / 2; ++j) {
+    const float2 v = __fmul2_rn(terms(pair_at<T>(w, j), m, c), twice(scale));
+    if (sizeof(T) == 4) {
+      o[2 * j] = __float_as_uint(v.x);
+      o[2 * j + 1] = __float_as_uint(v.y);
+    } else {
+      o[j] = pack2(v);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t rounded_bits(float v) {
+  T t;
+  narrow(t, v);
+  return bits_of(t);
+}
+// The gradient's vectors of a tile: scale exp((x - m) / T), and `at` in place
+// of the value y.
+template <typename T>
+__device__ __forceinline__ void store_tile(const uint4 (&w)[kV], const Row<T>& r, const GradRow<T>& g, int first, int step,
+                                           int last, float m, float c, float scale, int y, float at) {
+#pragma unroll
+  for (int k = 0; k < kV; ++k) {
+    const int i = first + k * step;
+    if (__any_sync(0xffffffffu, i < last)) {
+      const int e0 = i * kN<T> - r.lead;
+      uint4 o = scaled_terms<T>(w[k], m, c, scale);
+      const unsigned j = static_cast<unsigned>(y - e0);
+      if (y >= 0 && j < static_cast<unsigned>(kN<T>)) put<T>(o, static_cast<int>(j), rounded_bits<T>(at));
+      g.store(o, e0, i < last);
+    }
+  }
+}
+
+// ---- clusters --------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void store_remote(const float4* mine, uint32_t rank, float4 v) {
+  const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  uint32_t there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+// Waits for the kernel before this one (launched so that they overlap).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // ---- counted tokens ------------------------------------------------------------
-__global__ void __launch_bounds__(kFinishThreads) k_loss_count(const __grid_constant__ LossArgs a, int op) {
+// Also clears the tickets of the sum over tokens.
+__global__ void __launch_bounds__(kCountThreads) k_loss_count(const __grid_constant__ LossArgs a, int op) {
   __shared__ double red[32];
+  let_next_start();
+  const int groups = (a.tokens + kGroup - 1) / kGroup;
+  for (int i = threadIdx.x; i <= groups; i += kCountThreads) a.tickets[i] = 0;
   int n = 0;
-  for (int64_t t = threadIdx.x; t < a.tokens; t += kFinishThreads) {
-    const int b = static_cast<int>(t / a.seq), s = static_cast<int>(t % a.seq);
-    n += counted(a, op, b, s);
-  }
+#pragma unroll 8
+  for (uint32_t t = threadIdx.x; t < static_cast<uint32_t>(a.tokens); t += kCountThreads)
+    n += counted(a, op, static_cast<int>(t / static_cast<uint32_t>(a.seq)), static_cast<int>(t % static_cast<uint32_t>(a.seq)));
   const double total = block_sum(n, red);  // exact: below 2^53
-  if (threadIdx.x == 0) *a.count = static_cast<int64_t>(total);
+  if (threadIdx.x == 0) {
+    *a.count = static_cast<int64_t>(total);
+    if (a.tokens == 0) *a.loss = 0.f;
+  }
+}
+
+// A token's share of the loss is in a.part: the warp that brings the last of a
+// group of kGroup tokens sums the group, the one that brings the last group
+// sums the groups, each in a fixed order.
+__device__ __forceinline__ void add_to_loss(const LossArgs& a, int row, float share) {
+  const int lane = threadIdx.x & 31;
+  const int group = row / kGroup, groups = (a.tokens + kGroup - 1) / kGroup;
+  const int members = min(kGroup, a.tokens - group * kGroup);
+  int last = 0;
+  if (lane == 0) {
+    a.part[row] = share;
+    __threadfence();
+    last = atomicAdd(&a.tickets[1 + group], 1u) == static_cast<unsigned>(members - 1);
+  }
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  __threadfence();
+  double v = 0.0;
+#pragma unroll
+  for (int k = 0; k < kGroup / 32; ++k)
+    if (k * 32 + lane < members) v += __ldcg(a.part + group * kGroup + k * 32 + lane);
+  v = warp_sum(v);
+  last = 0;
+  if (lane == 0) {
+    a.group_part[group] = v;
+    __threadfence();
+    last = atomicAdd(&a.tickets[0], 1u) == static_cast<unsigned>(groups - 1);
+  }
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  __threadfence();
+  v = 0.0;
+  for (int k = lane; k < groups; k += 32) v += __ldcg(a.group_part + k);
+  v = warp_sum(v);
+  if (lane == 0) {
+    const double n = a.weights.p == nullptr ? static_cast<double>(*a.count) : 1.0;
+    *a.loss = n > 0.0 ? static_cast<float>(v / n) : 0.f;
+  }
 }
 
 // ---- the operators' scalars -----------------------------------------------------
+struct PolicyIn {
+  float adv, old, ref;
+};
 // Loss of a token and its derivative with respect to logp.
 struct Token {
   float loss, d;
 };
-__device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, int b, int s) {
-  const float adv = row_value(a.adv, b, s);
-  const float r = expf(logp - (a.old.p == nullptr ? logp : row_value(a.old, b, s)));
-  const float raw = r * adv;
-  const float cut = fminf(fmaxf(r, a.lo), a.hi) * adv;
+__device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, const PolicyIn& in) {
+  const float r = expf(logp - (a.old.p == nullptr ? logp : in.old));
+  const float raw = r * in.adv;
+  const float cut = fminf(fmaxf(r, a.lo), a.hi) * in.adv;
   Token t;
   const bool free = raw <= cut || isnan(raw);
   t.loss = free ? -raw : -cut;
   t.d = free ? -raw : 0.f;
   if (a.kl != 0.f) {
-    const float far = row_value(a.ref, b, s) - logp;
+    const float far = in.ref - logp;
     const float e = expm1f(far);
     t.loss += a.kl * (e - far);
     t.d -= a.kl * e;
@@ -185,186 +520,326 @@ __device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, int
   return t;
 }
 
-template <typename T>
-__device__ __forceinline__ void zero_row(T* g, int n) {
-  for (int j = threadIdx.x; j < n; j += blockDim.x) narrow(g[j], 0.f);
+// Shared memory of a CTA of k_loss_row: the parts of all warps of the cluster
+// and, for distill, the list's bits (a byte a vector of the tile), ids,
+// probabilities and logits.
+__host__ __device__ constexpr int row_shared(bool distill, int warps, int cluster, int top_k) {
+  const int parts = warps * cluster * static_cast<int>(sizeof(float4));
+  return distill ? parts + warps * 32 * kV + 12 * ((top_k + 3) / 4 * 4) : parts;
 }
 
 // ---- one row -----------------------------------------------------------------
-template <typename T, int OP>
-__global__ void __launch_bounds__(kRowThreads) k_loss_row(const __grid_constant__ LossArgs a) {
-  __shared__ Soft red[kRowThreads / 32];
-  __shared__ double dred[32];
-  __shared__ uint32_t listed[OP == kDistill ? kTile / 32 : 1];
-  __shared__ int32_t id[OP == kDistill ? LOSS_MAX_TOP_K : 1];
-  __shared__ float pk[OP == kDistill ? LOSS_MAX_TOP_K : 1];
-  __shared__ float xk[OP == kDistill ? LOSS_MAX_TOP_K : 1];
-  __shared__ int bad, entries;
-  const int row = blockIdx.x, b = row / a.seq, s = row % a.seq;
-  const T* x = static_cast<const T*>(a.x) + b * a.xsb + s * a.xss;
-  T* g = a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss;
-  const int V = a.vocab, tid = threadIdx.x;
+// A cluster has a row, a CTA a run of a.vecs_per_cta of its vectors.  LONG:
+// more than the threads keep, so the row is read again for the gradient.
+template <typename T, int OP, bool LONG>
+__global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) k_loss_row(const __grid_constant__ LossArgs a) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  __shared__ float4 red[kMaxThreads / 32];
+  __shared__ int bad;
+  constexpr bool kLists = OP == kDistill;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int step = blockDim.x, warps = step >> 5;
+  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int row = blockIdx.x / ranks, b = row / a.seq, s = row % a.seq;
+  float4* parts = reinterpret_cast<float4*>(shared);
+  uint8_t* listed = shared + warps * ranks * sizeof(float4);
+  int32_t* id = reinterpret_cast<int32_t*>(listed + step * kV);
+  const int kpad = (a.top_k + 3) / 4 * 4;
+  float* pk = reinterpret_cast<float*>(id + kpad);
+  float* xk = pk + kpad;
 
-  if (!counted(a, OP, b, s)) {
-    if (g != nullptr) zero_row(g, V);
-    if (tid == 0) {
+  const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
+  const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
+
+  if (OP == kLogprobs) {
+    // k_loss_pair may begin as these CTAs end; its ticket is cleared here
+    let_next_start();
+    if (a.tickets != nullptr && blockIdx.x == 0 && tid == 0) a.tickets[0] = 0;
+  }
+  int64_t y64 = 0;
+  bool in_loss;
+  if (kLists) {
+    in_loss = counted(a, OP, b, s);
+  } else {
+    y64 = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+    in_loss = y64 != a.ignore;
+  }
+  if (!in_loss) {
+    if (a.g != nullptr) g.zero(rank, ranks);
+    if (rank == 0 && tid == 0) {
       if (a.logp != nullptr) a.logp[row] = 0.f;
       if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
       if (a.stats != nullptr) a.stats[row] = make_float2(0.f, 0.f);
-      if (a.part != nullptr) a.part[row] = 0.f;
+      if (a.coef_out != nullptr) a.coef_out[row] = 0.f;
+    }
+    if (OP != kLogprobs && rank == 0 && warp == 0) {
+      wait_for_previous();
+      add_to_loss(a, row, 0.f);
     }
     return;
   }
+  if (ranks > 1) cluster_arrive();  // shared memory of the others may be written once they have all begun
 
-  float sum_p = 0.f, rest = 0.f;  // distill: sum of p, the teacher's mass on other words
-  if (OP == kDistill) {
-    // The teacher's probabilities.  p and rest are the same in every thread.
-    if (tid == 0) bad = entries = 0;
-    __syncthreads();
-    Soft t{-INFINITY, 0.f, 0.f};
-    for (int k = tid; k < a.top_k; k += kRowThreads) {
-      const int64_t e = b * a.isb + s * a.iss + k, f = b * a.tsb + s * a.tss + k;
-      int64_t i = load_index(a.ids, a.idt, e);
-      if (i != -1 && (i < 0 || i >= V)) {
-        bad = 1;
-        i = -1;
-      }
+  const int v0 = rank * a.vecs_per_cta, v1 = min(r.vecs, v0 + a.vecs_per_cta);
+  uint4 w[kV];
+  if (!LONG) load_tile<T>(w, r, v0 + tid, step, v1);
+
+  // Per-token values, while the row is on its way.
+  int y = -1;
+  float x_at = 0.f, weight = 0.f;
+  PolicyIn in{0.f, 0.f, 0.f};
+  if (!kLists && y64 >= 0 && y64 < a.vocab) {
+    y = static_cast<int>(y64);
+    x_at = widen(r.x[y]);
+  }
+  if (OP == kPolicy) {
+    in.adv = row_value(a.adv, b, s);
+    if (a.old.p != nullptr) in.old = row_value(a.old, b, s);
+    if (a.kl != 0.f) in.ref = row_value(a.ref, b, s);
+  }
+  if (OP != kLogprobs && a.weights.p != nullptr) weight = row_value(a.weights, b, s);
+
+  // The teacher: p[k] = pk[k] pscale, their sum and the rest.
+  float pscale = 1.f, sum_p = 0.f, rest = 0.f;
+  if (kLists) {
+    if (tid == 0) bad = 0;
+    if (!LONG)
+      for (int i = tid; i < step * kV / 4; i += step) reinterpret_cast<uint32_t*>(listed)[i] = 0;
+    float top = -INFINITY;
+    int entries = 0, wrong = 0;
+    for (int k = tid; k < a.top_k; k += step) {
+      int64_t i = load_index(a.ids, a.idt, b * a.isb + s * a.iss + k);
+      const int64_t f = b * a.tsb + s * a.tss + k;
       float v = a.tdt == ADAF_BFLOAT16 ? widen(static_cast<const __nv_bfloat16*>(a.tv)[f])
                                        : static_cast<const float*>(a.tv)[f];
-      if (i == -1) v = -INFINITY;
-      if (i >= 0) atomicAdd(&entries, 1);
+      if (i < 0 || i >= a.vocab) {
+        wrong |= i != -1;
+        i = -1;
+        v = -INFINITY;
+      } else {
+        ++entries;
+      }
       id[k] = static_cast<int>(i);
       pk[k] = v;
-      xk[k] = i == -1 ? 0.f : widen(x[i]);
-      t = join(t, Soft{v, i == -1 || v == -INFINITY ? 0.f : 1.f, 0.f}, a.c);
+      top = fmaxf(top, v);
     }
-    t = block_join(t, a.c, red);
-    const float lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
-    double sp = 0.0;
-    for (int k = tid; k < a.top_k; k += kRowThreads) {
-      // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
-      const float p = id[k] < 0 ? 0.f
-                      : a.lse.p == nullptr ? (t.s == 0.f ? 0.f : term(pk[k], shift_of(t.m), a.c) / t.s)
-                                           : expf(pk[k] * a.inv_t - lse);
-      pk[k] = p;
-      sp += p;
+    top = warp_max(top);
+    wrong = __any_sync(0xffffffffu, wrong);
+    entries = __reduce_add_sync(0xffffffffu, entries);
+    if (lane == 0) red[warp] = make_float4(top, __int_as_float(entries), __int_as_float(wrong), 0.f);
+    __syncthreads();
+    entries = wrong = 0;
+    for (int q = 0; q < warps; ++q) {
+      top = fmaxf(top, red[q].x);
+      entries += __float_as_int(red[q].y);
+      wrong |= __float_as_int(red[q].z);
     }
-    sum_p = static_cast<float>(block_sum(sp, dred));
-    if (a.lse.p != nullptr && entries < V) rest = fmaxf(0.f, 1.f - sum_p);
-    if (isnan(sum_p)) rest = sum_p;
-  }
-
-  // m and s, with the listed words apart: their sum is not taken out of the
-  // whole one again, so a small rest keeps its precision.
-  Soft v{-INFINITY, 0.f, 0.f};
-  for (int j0 = 0; j0 < V; j0 += kTile) {
-    if (OP == kDistill) {
-      for (int w = tid; w < kTile / 32; w += kRowThreads) listed[w] = 0;
-      __syncthreads();
-      for (int k = tid; k < a.top_k; k += kRowThreads) {
-        const unsigned at = static_cast<unsigned>(id[k] - j0);
-        if (id[k] >= 0 && at < kTile) {
-          const uint32_t bit = 1u << (at & 31);
-          if (atomicOr(&listed[at >> 5], bit) & bit) bad = 1;
+    if (wrong && tid == 0) bad = 1;
+    const float sh = shift_of(top), lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
+    float sum = 0.f;
+    for (int k = tid; k < a.top_k; k += step) {
+      const int i = id[k];
+      float p = 0.f, x = 0.f;
+      if (i >= 0) {
+        // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
+        p = a.lse.p == nullptr ? term(pk[k], sh, a.c) : expf(pk[k] * a.inv_t - lse);
+        const int at = (i + r.lead) / kN<T> - v0;
+        const bool mine = at >= 0 && at < v1 - v0;
+        if (mine || rank == 0) x = widen(r.x[i]);
+        if (!LONG && mine) {
+          const uint32_t bit = 1u << ((at & 3) * 8 + (i + r.lead) % kN<T>);
+          if (atomicOr(reinterpret_cast<uint32_t*>(listed) + (at >> 2), bit) & bit) bad = 1;
         }
       }
-      __syncthreads();
+      pk[k] = p;
+      xk[k] = x;
+      sum += p;
     }
-    const int j1 = min(V, j0 + kTile);
-    for (int j = j0 + tid; j < j1; j += kRowThreads) {
-      const float xj = widen(x[j]);
-      const float m = fmaxf(v.m, xj), sh = shift_of(m);
-      const float f = term(v.m, sh, a.c), e = term(xj, sh, a.c);
-      const bool on = OP == kDistill && (listed[(j - j0) >> 5] >> ((j - j0) & 31) & 1);
-      v.s = v.s * f + (on ? 0.f : e);
-      v.top = v.top * f + (on ? e : 0.f);
-      v.m = m;
+    sum = warp_sum(sum);
+    __syncthreads();  // red is read, the bits are set
+    if (lane == 0) red[warp].w = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int q = 0; q < warps; ++q) sum += red[q].w;
+    if (a.lse.p == nullptr) {
+      pscale = sum == 0.f ? 0.f : 1.f / sum;
+      sum_p = sum == 0.f ? 0.f : sum == sum ? 1.f : sum;
+    } else {
+      sum_p = sum;
+      if (sum != sum) rest = sum;
+      else if (entries < a.vocab) rest = fmaxf(0.f, 1.f - sum);
     }
-    if (OP == kDistill) __syncthreads();
   }
-  v = block_join(v, a.c, red);
-  const float m = v.m, sum = v.s + v.top;
-  float nan = m == -INFINITY || m == INFINITY ? NAN : 0.f;  // a row without a distribution
 
-  float k_all, k_at;  // gradient: k_all exp((x - m) / T), and k_at more at the target
-  int64_t y = -1;
-  if (OP != kDistill) {
-    y = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
-    if (y < 0 || y >= V) {
-      nan = NAN;
-      y = -1;
+  // m and the sum of the terms; the listed words' apart, so that a small rest
+  // is a sum of its own and keeps its precision.
+  float m = -INFINITY, sum = 0.f, top = 0.f;
+  if (!LONG) {
+    m = tile_max<T>(w);
+    tile_sum<T, kLists>(w, shift_of(m), a.c, listed + tid, step, sum, top);
+  } else {
+    for (int i0 = v0; i0 < v1; i0 += step * kV) {
+      if (kLists) {
+        __syncthreads();
+        for (int i = tid; i < step * kV / 4; i += step) reinterpret_cast<uint32_t*>(listed)[i] = 0;
+        __syncthreads();
+        for (int k = tid; k < a.top_k; k += step) {
+          const int at = (id[k] + r.lead) / kN<T> - i0;
+          if (id[k] >= 0 && at >= 0 && at < min(v1 - i0, step * kV)) {
+            const uint32_t bit = 1u << ((at & 3) * 8 + (id[k] + r.lead) % kN<T>);
+            if (atomicOr(reinterpret_cast<uint32_t*>(listed) + (at >> 2), bit) & bit) bad = 1;
+          }
+        }
+        __syncthreads();
+      }
+      load_tile<T>(w, r, i0 + tid, step, v1);
+      const float m2 = fmaxf(m, tile_max<T>(w));
+      const float sh = shift_of(m2), f = term(m, sh, a.c);
+      sum *= f;
+      top *= f;
+      tile_sum<T, kLists>(w, sh, a.c, listed + tid, step, sum, top);
+      m = m2;
     }
-    const float logp = y < 0 ? NAN : (widen(x[y]) - m) * a.inv_t - logf(sum) + nan;
-    if (tid == 0) {
+  }
+  sum = warp_sum(sum);
+  if (kLists) top = warp_sum(top);
+
+  // Every warp's part to every CTA of the cluster; each warp joins them all.
+  float wrong = 0.f;
+  if (kLists) {
+    __syncthreads();
+    wrong = bad ? NAN : 0.f;
+  }
+  const float4 part = make_float4(m, sum, top, wrong);
+  if (ranks > 1) {
+    cluster_wait();
+    if (lane < ranks) store_remote(parts + rank * warps + warp, lane, part);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    if (lane == 0) parts[warp] = part;
+    __syncthreads();
+  }
+  const int all = warps * ranks;
+  m = -INFINITY;
+  for (int q = lane; q < all; q += 32) m = fmaxf(m, parts[q].x);
+  m = warp_max(m);
+  sum = top = wrong = 0.f;
+  for (int q = lane; q < all; q += 32) {
+    const float4 p = parts[q];
+    const float f = term(p.x, shift_of(m), a.c);
+    sum += p.y * f;
+    top += p.z * f;
+    wrong += p.w;
+  }
+  sum = warp_sum(sum);
+  float off = sum;  // the terms of the words that are not listed
+  if (kLists) {
+    sum += warp_sum(top);
+    wrong = warp_sum(wrong);
+  }
+  if (m == -INFINITY || m == INFINITY) wrong = NAN;  // a row without a distribution
+
+  float scale, at = 0.f;  // gradient: scale exp((x - m) / T), at the target `at`
+  float lead = 0.f, on = 0.f;
+  const bool first = rank == 0 && warp == 0;
+  if (!kLists) {
+    const float logp = y < 0 ? NAN : (x_at - m) * a.inv_t - logf(sum) + wrong;
+    if (first && lane == 0) {
       if (a.logp != nullptr) a.logp[row] = logp;
-      if (a.stats != nullptr) a.stats[row] = make_float2(m + nan, sum + nan);
+      if (a.stats != nullptr) a.stats[row] = make_float2(m + wrong, sum + wrong);
+      if (a.coef_out != nullptr) a.coef_out[row] = 0.f;
     }
     if (OP == kLogprobs) return;
-    const Token t = policy_token(a, logp, b, s);
-    const float w = a.weights.p != nullptr ? row_value(a.weights, b, s)
-                                           : 1.f / static_cast<float>(*a.count);
-    if (tid == 0) {
-      if (a.token_loss != nullptr) a.token_loss[row] = t.loss;
-      a.part[row] = a.weights.p != nullptr ? w * t.loss : t.loss;
+    const Token t = policy_token(a, logp, in);
+    wait_for_previous();
+    if (a.weights.p == nullptr) weight = 1.f / static_cast<float>(*a.count);
+    if (first) {
+      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = t.loss;
+      add_to_loss(a, row, a.weights.p != nullptr ? weight * t.loss : t.loss);
     }
-    k_at = w * a.gscale * a.inv_t * t.d;
-    k_all = -k_at / sum;
+    const float k_at = weight * a.gscale * a.inv_t * t.d;
+    scale = -k_at / sum;
+    at = scale * (y < 0 ? NAN : term(x_at, m, a.c)) + k_at;
   } else {
-    const float log_s = logf(sum);
-    if (bad) nan = NAN;
-    double l = 0.0;
-    for (int k = tid; k < a.top_k; k += kRowThreads)
-      if (pk[k] != 0.f) l += pk[k] * (logf(pk[k]) - ((xk[k] - m) * a.inv_t - log_s));
-    l = block_sum(l, dred);
-    if (rest > 0.f) l += rest * (logf(rest) - (logf(v.s) - log_s));
-    const float t2 = 1.f / (a.inv_t * a.inv_t);
-    const float loss = static_cast<float>(l) * t2 + nan;
-    const float w = a.weights.p != nullptr ? row_value(a.weights, b, s)
-                                           : 1.f / static_cast<float>(*a.count);
-    if (tid == 0) {
-      if (a.token_loss != nullptr) a.token_loss[row] = loss;
-      a.part[row] = a.weights.p != nullptr ? w * loss : loss;
+    wait_for_previous();
+    if (a.weights.p == nullptr) weight = 1.f / static_cast<float>(*a.count);
+    if (first) {
+      const float log_s = logf(sum);
+      float l = 0.f;
+      for (int k = lane; k < a.top_k; k += 32) {
+        const float p = pk[k] * pscale;
+        if (p != 0.f) l += p * (logf(p) - ((xk[k] - m) * a.inv_t - log_s));
+      }
+      l = warp_sum(l);
+      if (rest > 0.f) l += rest * (logf(rest) - (logf(off) - log_s));
+      const float loss = l / (a.inv_t * a.inv_t) + wrong;
+      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
+      add_to_loss(a, row, a.weights.p != nullptr ? weight * loss : loss);
     }
     // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
-    k_at = w * a.gscale / a.inv_t + nan;
-    k_all = k_at * ((sum_p + rest) / sum - (rest > 0.f ? rest / v.s : 0.f));
+    lead = weight * a.gscale / a.inv_t + wrong;
+    on = (sum_p + rest) / sum;
+    scale = lead * (on - (rest > 0.f ? rest / off : 0.f));
   }
-  if (g == nullptr) return;
-  const float at_value = OP == kDistill ? 0.f : k_all * (y < 0 ? NAN : term(widen(x[y]), m, a.c)) + k_at;
-  __syncthreads();  // the target's logit is read before it may be written over
-  for (int j = tid; j < V; j += kRowThreads) narrow(g[j], j == y ? at_value : k_all * term(widen(x[j]), m, a.c));
-  if (OP == kDistill) {
+  if (a.g == nullptr) return;
+  if (!LONG) {
+    store_tile<T>(w, r, g, v0 + tid, step, v1, m, a.c, scale, y, at);
+  } else {
+    for (int i0 = v0; i0 < v1; i0 += step * kV) {
+      load_tile<T>(w, r, i0 + tid, step, v1);
+      store_tile<T>(w, r, g, i0 + tid, step, v1, m, a.c, scale, y, at);
+    }
+  }
+  if (kLists) {
     __syncthreads();  // the listed words' values replace those written above
-    const float on = (sum_p + rest) / sum;
-    for (int k = tid; k < a.top_k; k += kRowThreads)
-      if (id[k] >= 0) narrow(g[id[k]], k_at * (on * term(xk[k], m, a.c) - pk[k]));
+    for (int k = tid; k < a.top_k; k += step) {
+      const int i = id[k], v = (i + r.lead) / kN<T>;
+      if (i >= 0 && v >= v0 && v < v1) narrow(g.g[i], lead * (on * term(xk[k], m, a.c) - pk[k] * pscale));
+    }
   }
 }
 
 // ---- gradient rows from kept statistics ------------------------------------------
+// A CTA has a tile of a row; the last rows come first: of what the forward
+// pass read they are the ones most likely still in L2.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) k_loss_grad(const __grid_constant__ LossArgs a) {
-  const int row = blockIdx.x, b = row / a.seq, s = row % a.seq;
-  const T* x = static_cast<const T*>(a.x) + b * a.xsb + s * a.xss;
-  T* g = static_cast<T*>(a.g) + b * a.gsb + s * a.gss;
+__global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad(const __grid_constant__ LossArgs a) {
+  const int row = a.tokens - 1 - static_cast<int>(blockIdx.x / a.tiles), tile = blockIdx.x % a.tiles;
+  const int b = row / a.seq, s = row % a.seq;
+  const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
+  const GradRow<T> g(static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
   const int64_t y0 = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+  if (a.coef != nullptr) wait_for_previous();
   if (y0 == a.ignore) {
-    zero_row(g, a.vocab);
+    g.zero(tile, a.tiles);
     return;
   }
+  const int first = tile * kGradThreads * kV + threadIdx.x;
+  const int last = min(r.vecs, (tile + 1) * kGradThreads * kV);
+  uint4 w[kV];
+  load_tile<T>(w, r, first, kGradThreads, last);
   const float2 st = a.stats[row];
   const float d = (a.coef != nullptr ? a.coef[row] : row_value(a.dlogp, b, s)) * a.gscale * a.inv_t;
   const bool inside = y0 >= 0 && y0 < a.vocab;
-  const float k_all = inside ? -d / st.y : NAN;
-  for (int j = threadIdx.x; j < a.vocab; j += kRowThreads) {
-    const float e = k_all * term(widen(x[j]), st.x, a.c);
-    narrow(g[j], j == y0 ? e + d : e);
-  }
+  const float scale = inside ? -d / st.y : NAN;
+  const int y = inside ? static_cast<int>(y0) : -1;
+  float at = 0.f;
+  // `at` matters to the thread that holds the target, which alone writes it:
+  // the gradient may lie over the logits.
+  const int v = (y + r.lead) / kN<T>;
+  const bool mine = inside && v >= tile * kGradThreads * kV && v < last;
+  if (mine) at = scale * term(widen(r.x[y]), st.x, a.c) + d;
+  store_tile<T>(w, r, g, first, kGradThreads, last, st.x, a.c, scale, mine ? y : -1, at);
 }
 
 // ---- a pair's loss ---------------------------------------------------------------
-__global__ void __launch_bounds__(kRowThreads) k_loss_pair(const __grid_constant__ LossArgs a) {
+__global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constant__ LossArgs a) {
   __shared__ double red[32];
+  __shared__ int last;
+  let_next_start();
+  wait_for_previous();
   const int64_t pair = blockIdx.x;
   double D[2];
   int64_t from[2], to[2];
@@ -384,7 +859,7 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pair(const __grid_constant
       to[h] = from[h] + a.seq;
     }
     double sum = 0.0, cnt = 0.0;
-    for (int64_t t = from[h] + threadIdx.x; t < to[h]; t += kRowThreads) {
+    for (int64_t t = from[h] + threadIdx.x; t < to[h]; t += kPairThreads) {
       const int b = static_cast<int>(t / a.seq), s = static_cast<int>(t % a.seq);
       if (!counted(a, kLogprobs, b, s)) continue;
       sum += a.logp[t];
@@ -417,6 +892,8 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pair(const __grid_constant
   if (threadIdx.x == 0) {
     if (a.pair_loss != nullptr) a.pair_loss[pair] = static_cast<float>(loss);
     a.pair_part[pair] = loss;
+    __threadfence();
+    last = atomicAdd(a.tickets, 1u) == static_cast<unsigned>(a.pairs - 1);
     if (a.rewards != nullptr) {
       a.rewards[pair] = static_cast<float>(a.beta * D[0]);
       a.rewards[pair + a.pairs] = static_cast<float>(a.beta * D[1]);
@@ -425,26 +902,16 @@ __global__ void __launch_bounds__(kRowThreads) k_loss_pair(const __grid_constant
   for (int q = 0; q < 2; ++q) {
     double c = (q == 0 ? dh : -dh) / static_cast<double>(a.pairs);
     if (a.average) c = n[q] > 0.0 ? c / n[q] : 0.0;
-    for (int64_t t = from[q] + threadIdx.x; t < to[q]; t += kRowThreads) a.coef_out[t] = static_cast<float>(c);
+    for (int64_t t = from[q] + threadIdx.x; t < to[q]; t += kPairThreads) a.coef_out[t] = static_cast<float>(c);
   }
-}
-
-// ---- the loss ------------------------------------------------------------------
-__global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_constant__ LossArgs a) {
-  __shared__ double red[32];
+  __syncthreads();
+  if (!last) return;
+  // the last pair to come sums them all, in order
+  __threadfence();
   double v = 0.0;
-  if (a.pairs > 0) {
-    for (int64_t i = threadIdx.x; i < a.pairs; i += kFinishThreads) v += a.pair_part[i];
-  } else {
-    for (int64_t i = threadIdx.x; i < a.tokens; i += kFinishThreads) v += a.part[i];
-  }
+  for (int64_t k = threadIdx.x; k < a.pairs; k += kPairThreads) v += __ldcg(a.pair_part + k);
   v = block_sum(v, red);
-  if (threadIdx.x == 0) {
-    double n = 1.0;
-    if (a.pairs > 0) n = static_cast<double>(a.pairs);
-    else if (a.weights.p == nullptr) n = static_cast<double>(*a.count);
-    *a.loss = n > 0.0 ? static_cast<float>(v / n) : 0.f;
-  }
+  if (threadIdx.x == 0) *a.loss = static_cast<float>(v / static_cast<double>(a.pairs));
 }
 
 // ---- host side -----------------------------------------------------------------
@@ -535,7 +1002,7 @@ adaf_status check_grad(const loss_logits& x, const loss_grad* g, bool optional) 
 }
 
 struct Layout {
-  size_t off_count = 0, off_part = 0, off_stats = 0, off_logp = 0, off_coef = 0, off_pair = 0, bytes = 0;
+  size_t off_count = 0, off_tickets = 0, off_groups = 0, off_part = 0, off_stats = 0, off_logp = 0, off_coef = 0, off_pair = 0, bytes = 0;
 };
 adaf_status layout(int64_t tokens, int64_t pairs, Layout* L) {
   if (tokens < 0 || pairs < 0) return invalid("tokens or pairs < 0");
@@ -543,9 +1010,13 @@ adaf_status layout(int64_t tokens, int64_t pairs, Layout* L) {
     return fail(ADAF_ERR_UNSUPPORTED, "tokens must be below 2^31, pairs below 2^30");
   size_t o = 0;
   const size_t n = static_cast<size_t>(tokens);
-  L->off_count = o; o = round_up(o + 64, 256);
-  L->off_part = o;  o = round_up(o + sizeof(float) * n, 256);
-  if (pairs > 0) {
+  const size_t groups = (n + kGroup - 1) / kGroup;
+  L->off_count = o;   o += 64;
+  L->off_tickets = o; o = round_up(o + sizeof(unsigned) * (1 + groups), 256);
+  if (pairs == 0) {
+    L->off_groups = o; o = round_up(o + sizeof(double) * groups, 256);
+    L->off_part = o;   o = round_up(o + sizeof(float) * n, 256);
+  } else {
     L->off_stats = o; o = round_up(o + sizeof(float2) * n, 256);
     L->off_logp = o;  o = round_up(o + sizeof(float) * n, 256);
     L->off_coef = o;  o = round_up(o + sizeof(float) * n, 256);
@@ -588,8 +1059,8 @@ LossArgs base_args(const loss_logits& x, const loss_targets* y, const loss_grad*
   return a;
 }
 
-const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_grad", "k_loss_pair", "k_loss_finish"};
-enum Slot { kSlotCount = 0, kSlotRow, kSlotGrad, kSlotPair, kSlotFinish, kNumKernels };
+const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_grad", "k_loss_pair"};
+enum Slot { kSlotCount = 0, kSlotRow, kSlotGrad, kSlotPair, kNumKernels };
 struct ProfRecord {
   int slot;
   cudaEvent_t start, stop;
@@ -598,9 +1069,12 @@ std::mutex g_mu;
 bool g_profile = false;
 std::vector<ProfRecord> g_prof;
 
-// Launches through f(); under profiling between two events.
-template <typename F>
-adaf_status launch(int slot, cudaStream_t s, F f) {
+// Launches a kernel of this file; under profiling between two events.
+// `overlap`: the kernel may begin while the one before it ends (it waits for
+// that one itself, where it needs its results).
+template <typename... Args>
+adaf_status launch(int slot, void (*kernel)(LossArgs, Args...), int64_t grid, int threads, int shared, int cluster,
+                   bool overlap, cudaStream_t s, const LossArgs& a, Args... args) {
   bool prof;
   {
     std::lock_guard<std::mutex> lock(g_mu);
@@ -613,8 +1087,28 @@ adaf_status launch(int slot, cudaStream_t s, F f) {
         (e = cudaEventRecord(rec.start, s)) != cudaSuccess)
       return cuda_fail(e, "profile event");
   }
-  f();
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, kKernelNames[slot]);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(shared);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  cfg.attrs = at;
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+    ++cfg.numAttrs;
+  }
+  if (overlap) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, a, args...)) != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, kKernelNames[slot]);
+  }
   if (prof) {
     if ((e = cudaEventRecord(rec.stop, s)) != cudaSuccess) return cuda_fail(e, "profile event");
     std::lock_guard<std::mutex> lock(g_mu);
@@ -623,29 +1117,55 @@ adaf_status launch(int slot, cudaStream_t s, F f) {
   return ADAF_OK;
 }
 
+static int envi(const char* n, int d) { const char* v = getenv(n); return v ? atoi(v) : d; }
+static int kRowThreads() { return envi("MEO_T", 512); }
+static int kFewCtas() { return envi("MEO_F", 304); }
+// How a row is cut: CTAs, threads of each, vectors of each; `again`: the
+// threads cannot keep the row and read it twice.
+struct Cut {
+  int cluster, threads, vecs;
+  bool again;
+};
+Cut cut_row(int64_t tokens, int64_t vocab, size_t es) {
+  const int64_t per = 16 / static_cast<int64_t>(es), vecs = (vocab + 2 * per - 2) / per;  // the most, at any alignment
+  auto threads_of = [&](int64_t c) { return ((vecs + c - 1) / c + kV * 32 - 1) / (kV * 32) * 32; };
+  int64_t c = 1;
+  const int64_t most = kRowThreads();
+  while (c < kMaxCluster && threads_of(c) > most) c *= 2;
+  while (c < kMaxCluster && tokens * c < kFewCtas() && threads_of(c) > 64) c *= 2;
+  if (tokens * c > kMaxTokens) c = 1;
+  Cut cut;
+  cut.cluster = static_cast<int>(c);
+  cut.threads = static_cast<int>(std::min<int64_t>(threads_of(c), kMaxThreads));
+  cut.vecs = static_cast<int>((vecs + c - 1) / c);
+  cut.again = cut.vecs > cut.threads * kV;
+  return cut;
+}
+
 template <int OP>
-adaf_status launch_rows(const LossArgs& a, int32_t dtype, cudaStream_t s) {
-  return launch(kSlotRow, s, [&] {
-    if (dtype == ADAF_BFLOAT16) k_loss_row<__nv_bfloat16, OP><<<a.tokens, kRowThreads, 0, s>>>(a);
-    else k_loss_row<float, OP><<<a.tokens, kRowThreads, 0, s>>>(a);
-  });
+adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
+  const Cut cut = cut_row(a.tokens, a.vocab, dtype_size(dtype));
+  a.vecs_per_cta = cut.vecs;
+  const int shared = row_shared(OP == kDistill, cut.threads / 32, cut.cluster, a.top_k);
+  const bool bf16 = dtype == ADAF_BFLOAT16;
+  void (*const kernel)(LossArgs) =
+      cut.again ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
+                : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
+  return launch(kSlotRow, kernel, static_cast<int64_t>(a.tokens) * cut.cluster, cut.threads, shared, cut.cluster,
+                OP != kLogprobs, s, a);
 }
-adaf_status launch_grad(const LossArgs& a, int32_t dtype, cudaStream_t s) {
-  return launch(kSlotGrad, s, [&] {
-    if (dtype == ADAF_BFLOAT16) k_loss_grad<__nv_bfloat16><<<a.tokens, kRowThreads, 0, s>>>(a);
-    else k_loss_grad<float><<<a.tokens, kRowThreads, 0, s>>>(a);
-  });
+adaf_status launch_grad(LossArgs a, int32_t dtype, cudaStream_t s) {
+  const int64_t per = 16 / static_cast<int64_t>(dtype_size(dtype)), vecs = (a.vocab + 2 * per - 2) / per;
+  a.tiles = static_cast<int32_t>((vecs + kGradThreads * kV - 1) / (kGradThreads * kV));
+  const int64_t grid = static_cast<int64_t>(a.tokens) * a.tiles;
+  if (grid > kMaxTokens) return fail(ADAF_ERR_UNSUPPORTED, "gradient of more than 2^31 tiles");
+  return launch(kSlotGrad, dtype == ADAF_BFLOAT16 ? k_loss_grad<__nv_bfloat16> : k_loss_grad<float>, grid, kGradThreads,
+                0, 1, a.coef != nullptr, s, a);
 }
-adaf_status launch_finish(const LossArgs& a, cudaStream_t s) {
-  return launch(kSlotFinish, s, [&] { k_loss_finish<<<1, kFinishThreads, 0, s>>>(a); });
-}
-// The loss of no tokens: 0, by the finish kernel with nothing to sum.
 adaf_status launch_mean(const LossArgs& a, int op, int32_t dtype, cudaStream_t s) {
-  adaf_status st = ADAF_OK;
-  st = launch(kSlotCount, s, [&] { k_loss_count<<<1, kFinishThreads, 0, s>>>(a, op); });
-  if (st != ADAF_OK) return st;
-  if (a.tokens > 0) st = op == kPolicy ? launch_rows<kPolicy>(a, dtype, s) : launch_rows<kDistill>(a, dtype, s);
-  return st == ADAF_OK ? launch_finish(a, s) : st;
+  const adaf_status st = launch(kSlotCount, k_loss_count, 1, kCountThreads, 0, 1, false, s, a, op);
+  if (st != ADAF_OK || a.tokens == 0) return st;
+  return op == kPolicy ? launch_rows<kPolicy>(a, dtype, s) : launch_rows<kDistill>(a, dtype, s);
 }
 
 #define LOSS_CHECK(expr)                 \
@@ -729,6 +1249,8 @@ adaf_status loss_policy(const loss_logits* x, const loss_targets* y, const loss_
   a.token_loss = token_loss;
   a.count = reinterpret_cast<int64_t*>(ws + L.off_count);
   a.part = reinterpret_cast<float*>(ws + L.off_part);
+  a.group_part = reinterpret_cast<double*>(ws + L.off_groups);
+  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
   a.adv = rows_of(args->advantages);
   a.old = rows_of(args->old_logp);
   a.ref = rows_of(args->ref_logp);
@@ -790,17 +1312,15 @@ adaf_status loss_preference(const loss_logits* x, const loss_targets* y, const l
   a.beta = args->beta;
   a.smooth = args->label_smoothing;
   a.margin = args->margin;
+  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.tokens > 0) {
-    // A token outside every sequence (bad offsets) has coefficient 0.
-    const cudaError_t e = cudaMemsetAsync(a.coef_out, 0, sizeof(float) * static_cast<size_t>(a.tokens), s);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     LOSS_CHECK(launch_rows<kLogprobs>(a, x->dtype, s));
+  } else {
+    const cudaError_t e = cudaMemsetAsync(a.tickets, 0, sizeof(unsigned), s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   }
-  LOSS_CHECK(launch(kSlotPair, s, [&] {
-    k_loss_pair<<<static_cast<unsigned>(a.pairs), kRowThreads, 0, s>>>(a);
-  }));
-  LOSS_CHECK(launch_finish(a, s));
+  LOSS_CHECK(launch(kSlotPair, k_loss_pair, a.pairs, kPairThreads, 0, 1, a.tokens > 0, s, a));
   if (a.g == nullptr || a.tokens == 0) return ADAF_OK;
   a.coef = a.coef_out;
   return launch_grad(a, x->dtype, s);
@@ -834,6 +1354,8 @@ adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, co
   a.token_loss = token_loss;
   a.count = reinterpret_cast<int64_t*>(ws + L.off_count);
   a.part = reinterpret_cast<float*>(ws + L.off_part);
+  a.group_part = reinterpret_cast<double*>(ws + L.off_groups);
+  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
   a.ids = args->ids;
   a.idt = args->ids_dtype;
   a.isb = args->ids_stride_b;
