@@ -81,7 +81,7 @@ extern "C" {
 typedef struct loss_logits {
     const void* p;
     int32_t dtype;               /* ADAF_FLOAT32 or ADAF_BFLOAT16            */
-    int64_t batch, seq, vocab;   /* batch * seq < 2^31, 1 <= vocab < 2^30    */
+    int64_t batch, seq, vocab;   /* batch * seq <= 2^30, 1 <= vocab <= 2^21  */
     int64_t stride_b, stride_s;  /* elements, >= 0                           */
     double temperature;          /* > 0                                      */
 } loss_logits;

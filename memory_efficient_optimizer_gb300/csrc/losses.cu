@@ -16,7 +16,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -28,16 +27,21 @@
 
 namespace {
 
-constexpr int kMaxThreads = 512;   // of a CTA of k_loss_row
+// CTAs of k_loss_row on an SM, by their threads that sum.
+__host__ __device__ constexpr int row_ctas(int threads, bool lists) { return threads >= 512 ? 1 : threads >= 128 ? 4 : lists ? 10 : 20; }
 constexpr int kGradThreads = 256;
 constexpr int kPairThreads = 256;
 constexpr int kCountThreads = 1024;
-constexpr int kGroup = 256;        // tokens of a partial sum of the loss
+constexpr int kGradVecs = 8;       // vectors of a thread of k_loss_grad
 constexpr int kMaxCluster = 8;
-constexpr int64_t kMaxVocab = (int64_t{1} << 30) - 1;
-constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1;
+constexpr int kNoValue = -(1 << 30);  // a target that no value of a row is
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int64_t kMaxVocab = int64_t{1} << 21;
+constexpr int64_t kMaxTokens = int64_t{1} << 30;
 
-enum Op : int { kLogprobs = 0, kPolicy = 1, kDistill = 2 };
+__host__ __device__ constexpr int div_up(int x, int y) { return (x + y - 1) / y; }
+
+enum Op : int { kLogprobs, kPolicy, kDistill };
 
 struct Rows {
   const void* p;
@@ -49,6 +53,7 @@ struct LossArgs {
   const void* x;
   void* g;                        // NULL: no gradient
   int64_t xsb, xss, gsb, gss;
+  uintptr_t x_begin, x_end;       // the bytes from the logits' first value to their last
   int32_t seq, tokens, vocab;
   float c, inv_t, gscale;         // log2(e) / T, 1 / T, scale of the gradient
   Rows y;
@@ -59,10 +64,10 @@ struct LossArgs {
   float* token_loss;
   float2* stats;                  // [tokens]: m, s
   int64_t* count;                 // counted tokens
-  float* part;                    // [tokens]: w l, or l
-  double* group_part;             // [ceil(tokens / kGroup)]
-  unsigned* tickets;              // [1 + ceil(tokens / kGroup)]; k_loss_pair: [1]
-  int32_t vecs_per_cta;           // k_loss_row: vectors of a row for a CTA
+  double* part;                   // [clusters]: sum of w l, or of l
+  unsigned* ticket;
+  int32_t vecs_per_cta;           // k_loss_row, k_loss_forward: vectors of a row for a CTA
+  int32_t batches, slots;         // k_loss_row: batches of a thread; places of the ring for them
   int32_t tiles;                  // k_loss_grad: CTAs of a row
   // policy
   Rows adv, old, ref, weights;
@@ -103,12 +108,6 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// exp((x - m) / T).  The difference is taken before the scaling: it is exact
-// or rounded once however large x and m are, and two values at the type's
-// lowest give 0, not inf - inf.  m is finite or NaN here.
-__device__ __forceinline__ float term(float x, float m, float c) { return ex2((x - m) * c); }
-// The shift of a part whose largest value is -inf is 0: its terms are 0.
-__device__ __forceinline__ float shift_of(float m) { return m == -INFINITY ? 0.f : m; }
 
 __device__ __forceinline__ bool counted(const LossArgs& a, int op, int b, int s) {
   if (op == kDistill)
@@ -128,32 +127,54 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return t;
 }
 
+// ---- terms -----------------------------------------------------------------------
+// The terms of a sum with the largest value m are 2^(x c - R), c = log2(e) / T
+// and R = m c rounded: one fused multiply-add and one exponential each.  Parts
+// of a row with other m are brought together by 2^(R' - R), and what R is off
+// m c by is put right where ln s leaves the kernel (residue()).  Beyond 2^126
+// R would not be finite (masks at the type's lowest value): there the exponent
+// is (x - m) c, in two roundings.  A part of -inf alone has terms 0 with R = 0.
+struct Ref {
+  float m, R;
+  __device__ __forceinline__ Ref(float m_, float c) {
+    m = m_;
+    R = m_ == -INFINITY ? 0.f : __fmul_rn(m_, c);
+  }
+  __device__ __forceinline__ bool far() const { return fabsf(m) > kFar && m != -INFINITY; }
+  __device__ __forceinline__ float exponent(float x, float c) const { return far() ? (x - m) * c : fmaf(x, c, -R); }
+  // 2^(R' - R) for a part with the largest value m2 <= m
+  __device__ __forceinline__ float factor(float m2, float c) const { return ex2(far() ? (m2 - m) * c : __fsub_rn(__fmul_rn(m2, c), R)); }
+  // m c - R
+  __device__ __forceinline__ float residue(float c) const { return far() || m == -INFINITY ? 0.f : fmaf(m, c, -R); }
+  static constexpr float kFar = 1e37f;
+};
+
 // ---- vectors of a row ----------------------------------------------------------
 // A row is read as aligned 16-byte vectors.  Vector i of a row that starts
-// `lead` values after a 16-byte boundary holds its values i kN - lead ..; the
-// first and the last may reach past the row and are then loaded value by
-// value, with -inf outside.
+// `lead` values after a 16-byte boundary holds its values i kN - lead ..  Of
+// the first, the values before the row (in the same 16 bytes as its first
+// value) are read and replaced by -inf; of the last only the row's are read.
 template <typename T> constexpr int kN = 16 / static_cast<int>(sizeof(T));
-constexpr int kV = 8;               // vectors a thread keeps: 128 bytes of the row
-constexpr uint32_t kNegInf2 = 0xff80ff80u;
-template <typename T> constexpr uint32_t kNegInf = sizeof(T) == 2 ? kNegInf2 : 0xff800000u;
+template <typename T> constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+constexpr int kBatch = 4;           // vectors in registers at a time
 
 template <typename T>
 struct Row {
-  const T* x;
+  uintptr_t base;     // the first vector
   int lead, n, vecs;  // values before the row in its first vector, values, vectors
-  __device__ __forceinline__ Row(const T* p, int vocab) : x(p), n(vocab) {
-    lead = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  __device__ __forceinline__ Row(const T* p, int vocab) : n(vocab) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    base = at & ~uintptr_t{15};
+    lead = static_cast<int>((at & 15) / sizeof(T));
     vecs = (lead + n + kN<T> - 1) / kN<T>;
   }
-  __device__ __forceinline__ bool whole(int i) const {
-    const int e = i * kN<T> - lead;
-    return e >= 0 && e + kN<T> <= n;
-  }
-  __device__ __forceinline__ bool ragged() const { return lead != 0 || vecs * kN<T> != lead + n; }
-  __device__ __forceinline__ const uint4* at(int i) const {
-    return reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(x) & ~uintptr_t{15}) + i;
-  }
+  __device__ __forceinline__ const T* value(int j) const { return reinterpret_cast<const T*>(base) + lead + j; }
+  __device__ __forceinline__ bool ragged(int i) const { return (i == 0 && lead != 0) || (i == vecs - 1 && i * kN<T> + kN<T> > lead + n); }
+  // Vectors [first_whole, past_whole) hold nothing but the row's values.
+  __device__ __forceinline__ int first_whole() const { return lead != 0; }
+  __device__ __forceinline__ int past_whole() const { return (lead + n) / kN<T>; }
+  // Bytes of vector i up to the row's end.
+  __device__ __forceinline__ int bytes(int i) const { return min(16, (lead + n - i * kN<T>) * static_cast<int>(sizeof(T))); }
 };
 
 __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
@@ -162,7 +183,7 @@ __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16
 // Value j of a vector, replaced.
 template <typename T>
 __device__ __forceinline__ void put(uint4& w, int j, uint32_t bits) {
-  uint32_t* q = &w.x;
+  uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (sizeof(T) == 4) {
@@ -172,58 +193,84 @@ __device__ __forceinline__ void put(uint4& w, int j, uint32_t bits) {
       if (j == 2 * k + 1) q[k] = (q[k] & 0xffffu) | (bits << 16);
     }
   }
+  w = make_uint4(q[0], q[1], q[2], q[3]);
 }
-
-// Vectors i = first + k step < last of a row.
+// Value j of a vector.
 template <typename T>
-__device__ __forceinline__ void load_tile(uint4 (&w)[kV], const Row<T>& r, int first, int step, int last) {
+__device__ __forceinline__ float get(const uint4& w, int j) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  float v = 0.f;
 #pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    const int i = first + k * step;
-    w[k] = make_uint4(kNegInf<T>, kNegInf<T>, kNegInf<T>, kNegInf<T>);
-    if (i < last && r.whole(i)) w[k] = __ldcs(r.at(i));
+  for (int k = 0; k < kN<T>; ++k)
+    if (j == k) v = sizeof(T) == 4 ? __uint_as_float(q[k & 3]) : __uint_as_float(k & 1 ? q[k >> 1 & 3] & 0xffff0000u : q[k >> 1 & 3] << 16);
+  return v;
+}
+// -inf outside the row.
+template <typename T>
+__device__ __forceinline__ void trim(uint4& w, const Row<T>& r, int i) {
+#pragma unroll
+  for (int j = 0; j < kN<T>; ++j) {
+    const int e = i * kN<T> - r.lead + j;
+    if (e < 0 || e >= r.n) put<T>(w, j, kNegInf<T> & (sizeof(T) == 2 ? 0xffffu : 0xffffffffu));
   }
-  if (r.ragged()) {
+}
+__device__ __forceinline__ uint4 no_values(uint32_t neg_inf) { return make_uint4(neg_inf, neg_inf, neg_inf, neg_inf); }
+
+// Vector i < last of the row from memory.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const Row<T>& r, int i, int last) {
+  uint4 w = no_values(kNegInf<T>);
+  if (i < last) {
+    if (!r.ragged(i)) {
+      w = __ldcs(reinterpret_cast<const uint4*>(r.base) + i);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const int i = first + k * step;
-      if (i < last && !r.whole(i)) {
-#pragma unroll
-        for (int j = 0; j < kN<T>; ++j) {
-          const int e = i * kN<T> - r.lead + j;
-          if (e >= 0 && e < r.n) put<T>(w[k], j, bits_of(r.x[e]));
-        }
+      for (int j = 0; j < kN<T>; ++j) {
+        const int e = i * kN<T> - r.lead + j;
+        if (e >= 0 && e < r.n) put<T>(w, j, bits_of(*r.value(e)));
       }
     }
   }
+  return w;
+}
+// A warp's batch: vectors i + k NT of lane i - first.  Whether all of them lie
+// in [lo, hi): then nothing is looked at vector by vector.
+template <int NT, int N = kBatch>
+__device__ __forceinline__ bool batch_in(int first, int lo, int hi) { return first >= lo && first + 31 + (N - 1) * NT < hi; }
+template <typename T, int NT, int N>
+__device__ __forceinline__ void load_batch(uint4 (&w)[N], const Row<T>& r, int i, int last) {
+  if (batch_in<NT, N>(i - (threadIdx.x & 31), r.first_whole(), min(r.past_whole(), last))) {
+    const uint4* p = reinterpret_cast<const uint4*>(r.base) + i;
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = __ldcs(p + k * NT);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = load_vec(r, i + k * NT, last);
+  }
 }
 
-__device__ __forceinline__ float2 pair_of(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-// Values of a vector, two at a time.
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+// Two values of a vector.
 template <typename T>
 __device__ __forceinline__ float2 pair_at(const uint4& w, int j) {
-  const uint32_t* q = &w.x;
-  if (sizeof(T) == 4) return make_float2(__uint_as_float(q[2 * j]), __uint_as_float(q[2 * j + 1]));
-  return pair_of(q[j]);
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  if (sizeof(T) == 4) return make_float2(__uint_as_float(q[(2 * j) & 3]), __uint_as_float(q[(2 * j + 1) & 3]));
+  return make_float2(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xffff0000u));
 }
-__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
-// term() of two values.
-__device__ __forceinline__ float2 terms(float2 x, float m, float c) {
-  const float2 z = __fmul2_rn(__fadd2_rn(x, twice(-m)), twice(c));
+template <bool FAR>
+__device__ __forceinline__ float2 terms(float2 x, const Ref& ref, float c) {
+  const float2 z = FAR ? __fmul2_rn(__fadd2_rn(x, twice(-ref.m)), twice(c)) : __ffma2_rn(x, twice(c), twice(-ref.R));
   return make_float2(ex2(z.x), ex2(z.y));
 }
 
-// Largest value of a tile over the warp (NaN is left out: it shows in the sum).
-template <typename T>
-__device__ __forceinline__ float tile_max(const uint4 (&w)[kV]) {
-  float m;
+// Largest value of a batch (NaN is left out: it shows in the sum).
+template <typename T, int N>
+__device__ __forceinline__ float batch_max(const uint4 (&w)[N]) {
   if (sizeof(T) == 2) {
     __nv_bfloat162 a;
     memcpy(&a, &w[0].x, 4);
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
+    for (int k = 0; k < N; ++k) {
       const uint32_t q[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -232,47 +279,62 @@ __device__ __forceinline__ float tile_max(const uint4 (&w)[kV]) {
         a = __hmax2(a, b);
       }
     }
-    m = fmaxf(__low2float(a), __high2float(a));
-  } else {
-    m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kV; ++k)
-      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[k].x), __uint_as_float(w[k].y)),
-                         fmaxf(__uint_as_float(w[k].z), __uint_as_float(w[k].w))));
+    return fmaxf(__low2float(a), __high2float(a));
   }
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
-  return r;
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[k].x), __uint_as_float(w[k].y)),
+                       fmaxf(__uint_as_float(w[k].z), __uint_as_float(w[k].w))));
+  return m;
 }
 
-// Adds the terms of a tile; with `listed` (a byte a vector, a bit a value) the
-// listed words' terms go to `top`.
+// A thread's part of a row: the largest value and the sum of the terms; with
+// LISTED (`on`: a byte a vector, a bit a value) the listed words' terms apart,
+// so that a small rest is a sum of its own and keeps its precision.
 template <typename T, bool LISTED>
-__device__ __forceinline__ void tile_sum(const uint4 (&w)[kV], float m, float c, const uint8_t* listed, int step,
-                                         float& sum, float& top) {
-  float2 acc = make_float2(0.f, 0.f), acc2 = acc;
+struct Part {
+  float m = -INFINITY, s = 0.f, top = 0.f;
+  template <bool FAR, int N>
+  __device__ __forceinline__ void sum(const uint4 (&w)[N], const Ref& ref, float c, uint32_t on) {
+    if (LISTED && on != 0) {
 #pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    if (LISTED) {
-      const uint32_t on = listed[k * step];
-      if (on != 0) {
+      for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int j = 0; j < kN<T> / 2; ++j) {
-          const float2 e = terms(pair_at<T>(w[k], j), m, c);
-          sum += (on >> (2 * j) & 1 ? 0.f : e.x) + (on >> (2 * j + 1) & 1 ? 0.f : e.y);
-          top += (on >> (2 * j) & 1 ? e.x : 0.f) + (on >> (2 * j + 1) & 1 ? e.y : 0.f);
+          const float2 e = terms<FAR>(pair_at<T>(w[k], j), ref, c);
+          const uint32_t at = on >> (8 * k + 2 * j);
+          s += (at & 1 ? 0.f : e.x) + (at & 2 ? 0.f : e.y);
+          top += (at & 1 ? e.x : 0.f) + (at & 2 ? e.y : 0.f);
         }
-        continue;
+      }
+      return;
+    }
+    float2 acc = make_float2(0.f, 0.f), acc2 = acc;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+      for (int j = 0; j < kN<T> / 2; j += 2) {
+        acc = __fadd2_rn(acc, terms<FAR>(pair_at<T>(w[k], j), ref, c));
+        acc2 = __fadd2_rn(acc2, terms<FAR>(pair_at<T>(w[k], j + 1), ref, c));
       }
     }
-#pragma unroll
-    for (int j = 0; j < kN<T> / 2; j += 2) {
-      acc = __fadd2_rn(acc, terms(pair_at<T>(w[k], j), m, c));
-      acc2 = __fadd2_rn(acc2, terms(pair_at<T>(w[k], j + 1), m, c));
-    }
+    s += (acc.x + acc.y) + (acc2.x + acc2.y);
   }
-  sum += (acc.x + acc.y) + (acc2.x + acc2.y);
-}
+  template <int N>
+  __device__ __forceinline__ void add(const uint4 (&w)[N], float c, uint32_t on = 0) {
+    const float m2 = batch_max<T, N>(w);
+    if (m2 > m) {
+      const float f = Ref(m2, c).factor(m, c);
+      s *= f;
+      top *= f;
+      m = m2;
+    }
+    const Ref ref(m, c);
+    if (ref.far()) sum<true>(w, ref, c, on);
+    else sum<false>(w, ref, c, on);
+  }
+};
 
 // Stores of a gradient row, from vectors in the logits' phase.
 template <typename T>
@@ -339,10 +401,10 @@ struct GradRow {
     }
   }
   // The part of the row that CTA `rank` of `ranks` has, as zeros.
-  __device__ __forceinline__ void zero(int rank, int ranks) const {
+  __device__ __forceinline__ void zero(int rank, int ranks, int threads) const {
     const int vecs = (lead + n + kN<T> - 1) / kN<T>, per = (vecs + ranks - 1) / ranks;
     const int last = min(vecs, (rank + 1) * per);
-    for (int i = rank * per + threadIdx.x; i < last; i += blockDim.x) {
+    for (int i = rank * per + threadIdx.x; i < last; i += threads) {
       const int e0 = i * kN<T> - lead;
       if (e0 >= 0 && e0 + kN<T> <= n) {
         __stcs(reinterpret_cast<uint4*>(g + e0), make_uint4(0, 0, 0, 0));
@@ -360,16 +422,16 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
   memcpy(&r, &b, 4);
   return r;
 }
-// scale exp((x - m) / T) of a vector, rounded to its type.
-template <typename T>
-__device__ __forceinline__ uint4 scaled_terms(const uint4& w, float m, float c, float scale) {
+// scale 2^(x c - R) of a vector, rounded to its type.
+template <typename T, bool FAR>
+__device__ __forceinline__ uint4 scaled_terms(const uint4& w, const Ref& ref, float c, float scale) {
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < kN<T> / 2; ++j) {
-    const float2 v = __fmul2_rn(terms(pair_at<T>(w, j), m, c), twice(scale));
+    const float2 v = __fmul2_rn(terms<FAR>(pair_at<T>(w, j), ref, c), twice(scale));
     if (sizeof(T) == 4) {
-      o[2 * j] = __float_as_uint(v.x);
-      o[2 * j + 1] = __float_as_uint(v.y);
+      o[(2 * j) & 3] = __float_as_uint(v.x);
+      o[(2 * j + 1) & 3] = __float_as_uint(v.y);
     } else {
       o[j] = pack2(v);
     }
@@ -382,21 +444,40 @@ __device__ __forceinline__ uint32_t rounded_bits(float v) {
   narrow(t, v);
   return bits_of(t);
 }
-// The gradient's vectors of a tile: scale exp((x - m) / T), and `at` in place
-// of the value y.
+// A vector of the gradient from the logits' vector i: scale 2^(x c - R), and
+// at value y that plus `more`.  Every lane of the warp calls.
 template <typename T>
-__device__ __forceinline__ void store_tile(const uint4 (&w)[kV], const Row<T>& r, const GradRow<T>& g, int first, int step,
-                                           int last, float m, float c, float scale, int y, float at) {
+__device__ __forceinline__ void store_grad(const uint4& w, const Row<T>& r, const GradRow<T>& g, int i, bool in, const Ref& ref,
+                                           float c, float scale, int y, float more) {
+  const int e0 = i * kN<T> - r.lead;
+  uint4 o = ref.far() ? scaled_terms<T, true>(w, ref, c, scale) : scaled_terms<T, false>(w, ref, c, scale);
+  const unsigned j = static_cast<unsigned>(y - e0);
+  if (j < static_cast<unsigned>(kN<T>))
+    put<T>(o, static_cast<int>(j), rounded_bits<T>(scale * ex2(ref.exponent(get<T>(w, static_cast<int>(j)), c)) + more));
+  g.store(o, e0, in);
+}
+
+// The gradient's vectors of a batch, of vectors i + k NT < last; every lane of
+// the warp calls.  `plain`: whole vectors in the logits' phase without the
+// target.
+template <typename T, int NT, int N>
+__device__ __forceinline__ void store_batch(const uint4 (&w)[N], const Row<T>& r, const GradRow<T>& g, int i, int last,
+                                            bool plain, const Ref& ref, float c, float scale, int y, int y_vec, float more) {
+  uint4* p = reinterpret_cast<uint4*>(g.g + (i * kN<T> - r.lead));
+  if (plain) {
 #pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    const int i = first + k * step;
-    if (__any_sync(0xffffffffu, i < last)) {
-      const int e0 = i * kN<T> - r.lead;
-      uint4 o = scaled_terms<T>(w[k], m, c, scale);
-      const unsigned j = static_cast<unsigned>(y - e0);
-      if (y >= 0 && j < static_cast<unsigned>(kN<T>)) put<T>(o, static_cast<int>(j), rounded_bits<T>(at));
-      g.store(o, e0, i < last);
-    }
+    for (int k = 0; k < N; ++k) __stcs(p + k * NT, scaled_terms<T, false>(w[k], ref, c, scale));
+    return;
+  }
+  const int first = i - (threadIdx.x & 31), lo = r.first_whole(), hi = min(r.past_whole(), last);
+  const bool near = g.shift == 0 && !ref.far();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int f = first + k * NT;
+    if (near && batch_in<NT, 1>(f, lo, hi) && static_cast<unsigned>(y_vec - f) >= 32u)
+      __stcs(p + k * NT, scaled_terms<T, false>(w[k], ref, c, scale));
+    else if (f < last)
+      store_grad(w[k], r, g, i + k * NT, i + k * NT < last, ref, c, scale, y, more);
   }
 }
 
@@ -441,12 +522,11 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // ---- counted tokens ------------------------------------------------------------
-// Also clears the tickets of the sum over tokens.
+// Also clears the ticket of the sum over tokens.
 __global__ void __launch_bounds__(kCountThreads) k_loss_count(const __grid_constant__ LossArgs a, int op) {
   __shared__ double red[32];
   let_next_start();
-  const int groups = (a.tokens + kGroup - 1) / kGroup;
-  for (int i = threadIdx.x; i <= groups; i += kCountThreads) a.tickets[i] = 0;
+  if (threadIdx.x == 0) *a.ticket = 0;
   int n = 0;
 #pragma unroll 8
   for (uint32_t t = threadIdx.x; t < static_cast<uint32_t>(a.tokens); t += kCountThreads)
@@ -455,43 +535,6 @@ __global__ void __launch_bounds__(kCountThreads) k_loss_count(const __grid_const
   if (threadIdx.x == 0) {
     *a.count = static_cast<int64_t>(total);
     if (a.tokens == 0) *a.loss = 0.f;
-  }
-}
-
-// A token's share of the loss is in a.part: the warp that brings the last of a
-// group of kGroup tokens sums the group, the one that brings the last group
-// sums the groups, each in a fixed order.
-__device__ __forceinline__ void add_to_loss(const LossArgs& a, int row, float share) {
-  const int lane = threadIdx.x & 31;
-  const int group = row / kGroup, groups = (a.tokens + kGroup - 1) / kGroup;
-  const int members = min(kGroup, a.tokens - group * kGroup);
-  int last = 0;
-  if (lane == 0) {
-    a.part[row] = share;
-    __threadfence();
-    last = atomicAdd(&a.tickets[1 + group], 1u) == static_cast<unsigned>(members - 1);
-  }
-  if (!__shfl_sync(0xffffffffu, last, 0)) return;
-  __threadfence();
-  double v = 0.0;
-#pragma unroll
-  for (int k = 0; k < kGroup / 32; ++k)
-    if (k * 32 + lane < members) v += __ldcg(a.part + group * kGroup + k * 32 + lane);
-  v = warp_sum(v);
-  last = 0;
-  if (lane == 0) {
-    a.group_part[group] = v;
-    __threadfence();
-    last = atomicAdd(&a.tickets[0], 1u) == static_cast<unsigned>(groups - 1);
-  }
-  if (!__shfl_sync(0xffffffffu, last, 0)) return;
-  __threadfence();
-  v = 0.0;
-  for (int k = lane; k < groups; k += 32) v += __ldcg(a.group_part + k);
-  v = warp_sum(v);
-  if (lane == 0) {
-    const double n = a.weights.p == nullptr ? static_cast<double>(*a.count) : 1.0;
-    *a.loss = n > 0.0 ? static_cast<float>(v / n) : 0.f;
   }
 }
 
@@ -520,284 +563,548 @@ __device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, con
   return t;
 }
 
-// Shared memory of a CTA of k_loss_row: the parts of all warps of the cluster
-// and, for distill, the list's bits (a byte a vector of the tile), ids,
-// probabilities and logits.
-__host__ __device__ constexpr int row_shared(bool distill, int warps, int cluster, int top_k) {
-  const int parts = warps * cluster * static_cast<int>(sizeof(float4));
-  return distill ? parts + warps * 32 * kV + 12 * ((top_k + 3) / 4 * 4) : parts;
+// Bulk copies to a warp's own places of the ring, each with a barrier that
+// completes when its bytes are there.
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void init_barrier(uint64_t* bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_at(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
+  if (bytes != 0)
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_at(to)),
+                 "l"(from), "r"(bytes), "r"(shared_at(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(shared_at(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// Waits for a phase; false after meo::kWaitCycles.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  if (phase_done(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!phase_done(bar, parity))
+    if (clock64() - t0 > meo::kWaitCycles) return false;
+  return true;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("barrier.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("barrier.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+enum Barrier : int { kBarRow = 1, kBarListFull = 2, kBarListFree = 4 };  // the list's are two each
+
+constexpr int kChunk = 32 * kBatch;  // vectors of a warp's batch: consecutive ones, lane by lane
+
+// A teacher's list, made by a warp of its own one row ahead (two buffers).
+struct List {
+  uint32_t* bits;  // [batches][threads]: a byte a vector of the batch, a bit a value
+  int32_t* id;     // [top_k]
+  float* p;        // [top_k]: the teacher's probabilities
+  float* x;        // [top_k]: the logits (all in rank 0, the CTA's own elsewhere)
+  float* head;     // sum p, rest, NaN where the list is bad (else 0)
+};
+__host__ __device__ constexpr int list_bytes(int slice, int top_k) {
+  return (slice + 15) / 16 * 16 + 12 * ((top_k + 3) / 4 * 4) + 16;
+}
+__device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) {
+  List l;
+  const int kpad = (top_k + 3) / 4 * 4;
+  l.bits = reinterpret_cast<uint32_t*>(p);
+  l.id = reinterpret_cast<int32_t*>(p + (slice + 15) / 16 * 16);
+  l.p = reinterpret_cast<float*>(l.id + kpad);
+  l.x = l.p + kpad;
+  l.head = l.x + kpad;
+  return l;
 }
 
-// ---- one row -----------------------------------------------------------------
-// A cluster has a row, a CTA a run of a.vecs_per_cta of its vectors.  LONG:
-// more than the threads keep, so the row is read again for the gradient.
-template <typename T, int OP, bool LONG>
-__global__ void __launch_bounds__(kMaxThreads, 1024 / kMaxThreads) k_loss_row(const __grid_constant__ LossArgs a) {
+template <typename T, int NT>
+__device__ __forceinline__ void make_list(const LossArgs& a, const List& l, const Row<T>& r, int b, int s, int v0, int v1,
+                                          int slice, bool all) {
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < slice / kBatch; i += 32) l.bits[i] = 0;
+  __syncwarp();
+  float top = -INFINITY;
+  int entries = 0, wrong = 0;
+  for (int k = lane; k < a.top_k; k += 32) {
+    int64_t i = load_index(a.ids, a.idt, b * a.isb + s * a.iss + k);
+    const int64_t f = b * a.tsb + s * a.tss + k;
+    float v = a.tdt == ADAF_BFLOAT16 ? widen(static_cast<const __nv_bfloat16*>(a.tv)[f])
+                                     : static_cast<const float*>(a.tv)[f];
+    float x = 0.f;
+    if (i < 0 || i >= a.vocab) {
+      wrong |= i != -1;
+      i = -1;
+      v = -INFINITY;
+    } else {
+      ++entries;
+      const int e = static_cast<int>(i) + r.lead, at = e / kN<T> - v0;
+      const bool mine = at >= 0 && at < v1 - v0;
+      if (mine || all) x = widen(*r.value(static_cast<int>(i)));
+      if (mine) {
+        const uint32_t bit = 1u << (at % kChunk / 32 * 8 + e % kN<T>);
+        if (atomicOr(l.bits + at / (NT * kBatch) * NT + at / kChunk * 32 % NT + at % 32, bit) & bit) wrong = 1;
+      }
+    }
+    l.id[k] = static_cast<int>(i);
+    l.p[k] = v;
+    l.x[k] = x;
+    top = fmaxf(top, v);
+  }
+  top = warp_max(top);
+  entries = __reduce_add_sync(0xffffffffu, entries);
+  const bool bad = __any_sync(0xffffffffu, wrong);
+  const float lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
+  const float sh = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  for (int k = lane; k < a.top_k; k += 32) {
+    // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
+    const float p = l.id[k] < 0 ? 0.f : a.lse.p == nullptr ? ex2((l.p[k] - sh) * a.c) : expf(l.p[k] * a.inv_t - lse);
+    l.p[k] = p;
+    sum += p;
+  }
+  sum = warp_sum(sum);
+  float sum_p = sum, rest = 0.f;
+  if (a.lse.p == nullptr) {
+    sum_p = sum == 0.f ? 0.f : sum == sum ? 1.f : sum;
+    const float by = sum == 0.f ? 0.f : 1.f / sum;
+    for (int k = lane; k < a.top_k; k += 32) l.p[k] *= by;
+  } else if (sum != sum) {
+    rest = sum;
+  } else if (entries < a.vocab) {
+    rest = fmaxf(0.f, 1.f - sum);
+  }
+  if (lane == 0) {
+    l.head[0] = sum_p;
+    l.head[1] = rest;
+    l.head[2] = bad ? NAN : 0.f;
+  }
+}
+
+// ---- rows: the sum and the gradient in one read ---------------------------------
+// Clusters of CTAs walk the rows.  A warp copies its chunks of a row to its own
+// places of a ring in shared memory (bulk copies, one row ahead), adds up
+// their terms, and, when the cluster's parts of the row are together, makes the
+// gradient from the same copies; the places that come free take the next row's
+// chunks at once.  LONG: rows that no cluster keeps are read twice.
+template <typename T, int OP, int NT, bool LONG>
+__global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, OP == kDistill))
+    k_loss_row(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
-  __shared__ float4 red[kMaxThreads / 32];
-  __shared__ int bad;
   constexpr bool kLists = OP == kDistill;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int step = blockDim.x, warps = step >> 5;
+  constexpr int warps = NT / 32;  // that sum
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
-  const int row = blockIdx.x / ranks, b = row / a.seq, s = row % a.seq;
-  float4* parts = reinterpret_cast<float4*>(shared);
-  uint8_t* listed = shared + warps * ranks * sizeof(float4);
-  int32_t* id = reinterpret_cast<int32_t*>(listed + step * kV);
-  const int kpad = (a.top_k + 3) / 4 * 4;
-  float* pk = reinterpret_cast<float*>(id + kpad);
-  float* xk = pk + kpad;
+  const int first = static_cast<int>(blockIdx.x) / ranks, stride = static_cast<int>(gridDim.x) / ranks;
+  const int v0 = rank * a.vecs_per_cta, slots = a.slots, batches = a.batches;
+  uint4* const ring = reinterpret_cast<uint4*>(shared) + (LONG ? 0 : warp * slots * kChunk);  // a warp's [slots][kChunk]
+  float4* const parts = reinterpret_cast<float4*>(shared) + (LONG ? 0 : slots * kBatch * NT);  // [2][warps of the cluster]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(parts + 2 * warps * ranks) + warp * slots;  // a warp's [slots]
+  unsigned char* const lists = reinterpret_cast<unsigned char*>(parts + 2 * warps * ranks) + (LONG ? 0 : (warps * slots * 8 + 15) / 16 * 16);
+  const int slice = batches * kBatch * NT, list_size = list_bytes(slice, a.top_k);
 
-  const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
-  const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
-
-  if (OP == kLogprobs) {
-    // k_loss_pair may begin as these CTAs end; its ticket is cleared here
-    let_next_start();
-    if (a.tickets != nullptr && blockIdx.x == 0 && tid == 0) a.tickets[0] = 0;
+  if (ranks > 1) {  // shared memory of the others may be written once they have all begun
+    cluster_arrive();
+    cluster_wait();
   }
-  int64_t y64 = 0;
-  bool in_loss;
-  if (kLists) {
-    in_loss = counted(a, OP, b, s);
-  } else {
-    y64 = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
-    in_loss = y64 != a.ignore;
-  }
-  if (!in_loss) {
-    if (a.g != nullptr) g.zero(rank, ranks);
-    if (rank == 0 && tid == 0) {
-      if (a.logp != nullptr) a.logp[row] = 0.f;
-      if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
-      if (a.stats != nullptr) a.stats[row] = make_float2(0.f, 0.f);
-      if (a.coef_out != nullptr) a.coef_out[row] = 0.f;
+  struct Place {
+    int row, b, s;
+  };
+  const int by_b = stride / a.seq, by_s = stride % a.seq;
+  auto after = [&](Place t) {
+    t.row += stride;
+    t.b += by_b;
+    t.s += by_s;
+    if (t.s >= a.seq) {
+      t.s -= a.seq;
+      ++t.b;
     }
-    if (OP != kLogprobs && rank == 0 && warp == 0) {
-      wait_for_previous();
-      add_to_loss(a, row, 0.f);
+    return t;
+  };
+  auto row_at = [&](const Place& t) { return Row<T>(static_cast<const T*>(a.x) + t.b * a.xsb + t.s * a.xss, a.vocab); };
+  const Place begin{first, first / a.seq, first % a.seq};
+
+  if (kLists && warp == warps) {
+    // The warp that makes the lists.  It arrives at the cluster's barrier of a
+    // row early and makes the next list before it waits there.
+    int q = 0;
+    for (Place t = begin; t.row < a.tokens; t = after(t)) {
+      if (!counted(a, OP, t.b, t.s)) continue;
+      const Row<T> r = row_at(t);
+      if (q >= 2) bar_sync(kBarListFree + (q & 1), NT + 32);
+      make_list<T, NT>(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, t.b, t.s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice,
+                rank == 0);
+      __syncwarp();
+      bar_arrive(kBarListFull + (q & 1), NT + 32);
+      if (ranks > 1) {
+        if (q > 0) cluster_wait();
+        cluster_arrive();
+      }
+      ++q;
+    }
+    if (ranks > 1 && q > 0) cluster_wait();
+    for (int k = max(0, q - 2); k < q; ++k) bar_sync(kBarListFree + (k & 1), NT + 32);
+    return;
+  }
+
+  // Target of a row; ignored rows have none (`kIgnored`).
+  constexpr int64_t kIgnored = INT64_MIN;
+  auto target_at = [&](const Place& t) -> int64_t {
+    if (t.row >= a.tokens) return kIgnored;
+    if (kLists) return counted(a, OP, t.b, t.s) ? 0 : kIgnored;
+    const int64_t y = load_index(a.y.p, a.ydt, t.b * a.y.sb + t.s * a.y.ss);
+    return y == a.ignore ? kIgnored : y;
+  };
+  // The warp's chunks of a row that ends before vector `last`: chunk q starts
+  // at vector `mine` + q kBatch NT.
+  const int mine = v0 + warp * kChunk;
+  auto chunks = [&](int last) { return last <= mine ? 0 : (last - mine - 1) / (kBatch * NT) + 1; };
+  // The granule of 16 bytes at a row's end may hold bytes of its neighbour; at
+  // the tensor's own ends it may reach outside, and is then read value by value.
+  auto copied_from = [&](const Row<T>& r) { return r.base < a.x_begin ? 1 : 0; };
+  auto copied_to = [&](const Row<T>& r) { return r.base + 16 * static_cast<int64_t>(r.vecs) > a.x_end ? r.vecs - 1 : r.vecs; };
+  int fill = 0;  // the place of the ring that the next chunk goes to
+  // Copies chunks [from, to) of a row.
+  auto copy = [&](const Row<T>& r, int from, int to) {
+    const int lo = copied_from(r), hi = min(copied_to(r), v0 + a.vecs_per_cta);
+    for (int q = from; q < to; ++q) {
+      if (lane == 0) {
+        const int i = mine + q * kBatch * NT, i0 = max(i, lo), n = min(i + kChunk, hi) - i0;
+        copy_bulk(ring + fill * kChunk + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + fill);
+      }
+      if (++fill == slots) fill = 0;
+    }
+  };
+  if (!LONG) {
+    if (lane == 0) {
+      for (int k = 0; k < slots; ++k) init_barrier(full + k);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+  }
+
+  Place at{begin};
+  int64_t target = target_at(at), target1 = target_at(after(at));
+  // The ring's place of the row's chunk 0, the parity of its barrier, the
+  // row's chunks and those of the next.
+  int base = 0, n_chunks = 0, n_chunks1 = 0;
+  uint32_t parity = 0;
+  bool dead = false;  // a wait ran out: no more waiting, the loss is NaN
+  if (!LONG && target != kIgnored) {
+    const Row<T> r = row_at(at);
+    copy(r, 0, chunks(min(r.vecs, v0 + a.vecs_per_cta)));
+  }
+  double share = 0.0;  // of the cluster's rows in the loss (rank 0, warp 0)
+  float by_count = 0.f;
+  bool waited = false;
+  int q = 0;  // counted rows so far
+
+  for (; at.row < a.tokens; at = after(at)) {
+    const bool live = target != kIgnored, live1 = target1 != kIgnored;
+    const Place next = after(at);
+    const int row = at.row, b = at.b, s = at.s;
+    const Row<T> r = row_at(at), r1 = row_at(live1 ? next : at);
+    const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
+    const int64_t target2 = target_at(after(next));
+    n_chunks = live ? chunks(min(r.vecs, v0 + a.vecs_per_cta)) : 0;
+    n_chunks1 = live1 ? chunks(min(r1.vecs, v0 + a.vecs_per_cta)) : 0;
+    const int early1 = min(n_chunks1, slots - n_chunks);  // what there is room for before this row's places come free
+    if (!LONG) {
+      __syncwarp();  // the row before has been read
+      copy(r1, 0, early1);
+    }
+    if (!live) {
+      if (a.g != nullptr) g.zero(rank, ranks, NT);
+      if (rank == 0 && tid == 0) {
+        if (a.logp != nullptr) a.logp[row] = 0.f;
+        if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
+      }
+    } else {
+      const int v1 = min(r.vecs, v0 + a.vecs_per_cta);
+      const bool writes = rank == 0 && warp == 0;
+      // Per-token values, while the sum is made.
+      PolicyIn in{0.f, 0.f, 0.f};
+      float weight = 0.f;
+      if (OP == kPolicy) {
+        in.adv = row_value(a.adv, b, s);
+        if (a.old.p != nullptr) in.old = row_value(a.old, b, s);
+        if (a.kl != 0.f) in.ref = row_value(a.ref, b, s);
+      }
+      if (a.weights.p != nullptr) weight = row_value(a.weights, b, s);
+      const List list = list_at(lists + (q & 1) * list_size, slice, a.top_k);
+      if (kLists) bar_sync(kBarListFull + (q & 1), NT + 32);
+
+      // The target's logit, from the thread that has it.
+      int y = kNoValue, y_vec = kNoValue;
+      float x_at = 0.f;
+      bool has = false;
+      if (!kLists && target >= 0 && target < a.vocab) {
+        y = static_cast<int>(target);
+        y_vec = (y + r.lead) / kN<T>;
+        const int v = y_vec - v0;
+        has = y_vec >= v0 && y_vec < v1 && v / kChunk * 32 % NT + v % 32 == tid;
+        if (has) x_at = widen(*r.value(y));
+      }
+
+      // The thread's terms.
+      const int lo = r.first_whole(), hi = min(r.past_whole(), v1);
+      Part<T, kLists> part;
+      int place = base;
+      uint32_t phase = parity;
+      for (int q2 = 0; q2 < n_chunks; ++q2) {
+        const int i = mine + q2 * kBatch * NT + lane;
+        const uint4* const from = ring + place * kChunk + lane;
+        if (!LONG && !dead && !wait_phase(full + place, phase)) dead = true;
+        if (++place == slots) {
+          place = 0;
+          phase ^= 1;
+        }
+        const uint32_t bits = kLists ? list.bits[q2 * NT + tid] : 0;
+        if (batch_in<32>(i - lane, lo, hi)) {
+          uint4 w[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) w[k] = LONG ? __ldcs(reinterpret_cast<const uint4*>(r.base) + i + k * 32) : from[k * 32];
+          part.add(w, a.c, bits);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < kBatch && i - lane + k * 32 < v1; ++k) {
+            const int e = i + k * 32;
+            uint4 w[1] = {no_values(kNegInf<T>)};
+            if (LONG || e < copied_from(r) || e >= copied_to(r)) {
+              w[0] = load_vec(r, e, v1);
+            } else if (e < v1) {
+              w[0] = from[k * 32];
+              if (r.ragged(e)) trim(w[0], r, e);
+            }
+            part.add(w, a.c, bits >> (8 * k) & 0xff);
+          }
+        }
+      }
+
+      // The warp's part to every CTA of the cluster; each warp joins them all.
+      float4 p;
+      p.x = warp_max(part.m);
+      const float f = Ref(p.x, a.c).factor(part.m, a.c);
+      p.y = warp_sum(part.s * f);
+      const unsigned who = __ballot_sync(0xffffffffu, has);
+      if (who != 0) x_at = __shfl_sync(0xffffffffu, x_at, __ffs(static_cast<int>(who)) - 1);
+      p.z = kLists ? warp_sum(part.top * f) : x_at;
+      p.w = kLists && warp == 0 ? list.head[2] : 0.f;
+      float4* const here = parts + (q & 1) * warps * ranks;
+      if (ranks > 1) {
+        if (lane < ranks) store_remote(here + rank * warps + warp, lane, p);
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+      } else {
+        if (lane == 0) here[warp] = p;
+        bar_sync(kBarRow, NT);
+      }
+      const int all = warps * ranks;
+      float m = -INFINITY;
+      for (int k = lane; k < all; k += 32) m = fmaxf(m, here[k].x);
+      const Ref ref(warp_max(m), a.c);
+      float sum = 0.f, z = 0.f, wrong = 0.f;
+      for (int k = lane; k < all; k += 32) {
+        const float4 o = here[k];
+        const float fo = ref.factor(o.x, a.c);
+        sum += o.y * fo;
+        z += kLists ? o.z * fo : o.z;
+        wrong += o.w;
+      }
+      sum = warp_sum(sum);
+      z = warp_sum(z);
+      if (kLists) wrong = warp_sum(wrong);
+      if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
+
+      if (!waited) {
+        wait_for_previous();
+        waited = true;
+        by_count = a.weights.p == nullptr ? 1.f / static_cast<float>(*a.count) : 0.f;
+      }
+      const float w = a.weights.p != nullptr ? weight : by_count;
+      // gradient: scale 2^(x c - R), `more` at the target; for a list, lead (on 2^(x c - R) - p) at its words
+      float scale, more = 0.f, lead = 0.f, on = 0.f;
+      if (!kLists) {
+        const float logp = y < 0 ? NAN : (z - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+        const Token t = policy_token(a, logp, in);
+        if (writes) {
+          if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
+          if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = t.loss;
+          share += a.weights.p != nullptr ? static_cast<double>(w) * t.loss : t.loss;
+        }
+        more = w * a.gscale * a.inv_t * t.d;
+        scale = -more / sum;
+      } else {
+        const float sum_p = list.head[0], rest = list.head[1], off = sum;
+        sum += z;
+        if (writes) {
+          const float log_s = logf(sum), d = ref.residue(a.c) * kLn2;
+          float l = 0.f;
+          for (int k = lane; k < a.top_k; k += 32) {
+            const float pk = list.p[k];
+            if (pk != 0.f) l += pk * (logf(pk) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
+          }
+          l = warp_sum(l);
+          if (rest > 0.f) l += rest * (logf(rest) - (logf(off) - log_s));
+          const float loss = l / (a.inv_t * a.inv_t) + wrong;
+          if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
+          share += a.weights.p != nullptr ? static_cast<double>(w) * loss : loss;
+        }
+        // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
+        lead = w * a.gscale / a.inv_t + wrong;
+        on = (sum_p + rest) / sum;
+        scale = lead * (on - (rest > 0.f ? rest / off : 0.f));
+      }
+
+      // The gradient, and the next row's vectors into the places that come free.
+      if (a.g != nullptr) {
+        const bool near = g.shift == 0 && !ref.far();
+        place = base;
+        for (int q2 = 0; q2 < n_chunks; ++q2) {
+          const int i = mine + q2 * kBatch * NT + lane;
+          uint4 v[kBatch];
+          const bool plain = batch_in<32>(i - lane, lo, hi);
+          if (LONG) {
+            load_batch<T, 32>(v, r, i, v1);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[k] = ring[place * kChunk + k * 32 + lane];  // past the slice: not stored
+            if (!plain) {
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const int e = i + k * 32;
+                if (e < v1 && (e < copied_from(r) || e >= copied_to(r))) v[k] = load_vec(r, e, v1);
+              }
+            }
+          }
+          if (++place == slots) place = 0;
+          store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c, scale,
+                             y, y_vec, more);
+          const int q3 = q2 + slots - n_chunks;
+          if (!LONG && q3 >= early1 && q3 < n_chunks1) {
+            __syncwarp();  // the place has been read
+            copy(r1, q3, q3 + 1);
+          }
+        }
+        if (kLists) {
+          bar_sync(kBarRow, NT);  // the listed words' values replace those written above
+          for (int k = tid; k < a.top_k; k += NT) {
+            const int i = list.id[k], v = (i + r.lead) / kN<T>;
+            if (i >= 0 && v >= v0 && v < v1)
+              narrow(g.g[i], lead * (on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+          }
+        }
+      } else if (!LONG) {
+        __syncwarp();
+        copy(r1, early1, n_chunks1);
+      }
+      if (kLists) bar_arrive(kBarListFree + (q & 1), NT + 32);
+      ++q;
+    }
+    base += n_chunks;
+    if (base >= slots) {
+      base -= slots;
+      parity ^= 1;
+    }
+    target = target1;
+    target1 = target2;
+  }
+  if (__any_sync(0xffffffffu, dead)) {
+    share = NAN;
+    // copies still in flight land before the CTA's memory is given up
+    for (int k = 0; k < slots; ++k) wait_phase(full + k, k < base ? parity : parity ^ 1);
+  }
+
+  // The clusters' shares: the last to come sums them all, in order.
+  if (rank == 0 && warp == 0) {
+    if (!waited) wait_for_previous();
+    int last = 0;
+    if (lane == 0) {
+      a.part[first] = share;
+      __threadfence();
+      last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(stride - 1);
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    double v = 0.0;
+    for (int k = lane; k < stride; k += 32) v += __ldcg(a.part + k);
+    v = warp_sum(v);
+    if (lane == 0) {
+      const double n = a.weights.p == nullptr ? static_cast<double>(*a.count) : 1.0;
+      *a.loss = n > 0.0 ? static_cast<float>(v / n) : 0.f;
+    }
+  }
+}
+
+// ---- log-probabilities --------------------------------------------------------
+// A row is read once and nothing of it is kept: a CTA (or, for a few rows, a
+// cluster) has one, a thread loads a batch while it adds up the one before.
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_loss_forward(const __grid_constant__ LossArgs a) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  float4* parts = reinterpret_cast<float4*>(shared);  // [warps of the cluster]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int warps = NT / 32;
+  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int row = static_cast<int>(blockIdx.x) / ranks, b = row / a.seq, s = row % a.seq;
+  // k_loss_pair may begin as these CTAs end; its ticket is cleared here
+  let_next_start();
+  if (a.ticket != nullptr && blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  const bool writes = rank == 0 && warp == 0;
+  const int64_t target = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+  if (writes && lane == 0 && a.coef_out != nullptr) a.coef_out[row] = 0.f;
+  if (target == a.ignore) {
+    if (writes && lane == 0) {
+      a.logp[row] = 0.f;
+      if (a.stats != nullptr) a.stats[row] = make_float2(0.f, 0.f);
     }
     return;
   }
-  if (ranks > 1) cluster_arrive();  // shared memory of the others may be written once they have all begun
-
+  if (ranks > 1) cluster_arrive();
+  const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
   const int v0 = rank * a.vecs_per_cta, v1 = min(r.vecs, v0 + a.vecs_per_cta);
-  uint4 w[kV];
-  if (!LONG) load_tile<T>(w, r, v0 + tid, step, v1);
-
-  // Per-token values, while the row is on its way.
-  int y = -1;
-  float x_at = 0.f, weight = 0.f;
-  PolicyIn in{0.f, 0.f, 0.f};
-  if (!kLists && y64 >= 0 && y64 < a.vocab) {
-    y = static_cast<int>(y64);
-    x_at = widen(r.x[y]);
+  const bool inside = target >= 0 && target < a.vocab;
+  const float x_at = writes && inside ? widen(*r.value(static_cast<int>(target))) : NAN;
+  Part<T, false> part;
+  uint4 w[kBatch], w1[kBatch];
+  load_batch<T, NT>(w, r, v0 + tid, v1);
+  for (int i = v0 + tid; i - lane < v1; i += kBatch * NT) {
+    load_batch<T, NT>(w1, r, i + kBatch * NT, v1);
+    part.add(w, a.c);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) w[k] = w1[k];
   }
-  if (OP == kPolicy) {
-    in.adv = row_value(a.adv, b, s);
-    if (a.old.p != nullptr) in.old = row_value(a.old, b, s);
-    if (a.kl != 0.f) in.ref = row_value(a.ref, b, s);
-  }
-  if (OP != kLogprobs && a.weights.p != nullptr) weight = row_value(a.weights, b, s);
-
-  // The teacher: p[k] = pk[k] pscale, their sum and the rest.
-  float pscale = 1.f, sum_p = 0.f, rest = 0.f;
-  if (kLists) {
-    if (tid == 0) bad = 0;
-    if (!LONG)
-      for (int i = tid; i < step * kV / 4; i += step) reinterpret_cast<uint32_t*>(listed)[i] = 0;
-    float top = -INFINITY;
-    int entries = 0, wrong = 0;
-    for (int k = tid; k < a.top_k; k += step) {
-      int64_t i = load_index(a.ids, a.idt, b * a.isb + s * a.iss + k);
-      const int64_t f = b * a.tsb + s * a.tss + k;
-      float v = a.tdt == ADAF_BFLOAT16 ? widen(static_cast<const __nv_bfloat16*>(a.tv)[f])
-                                       : static_cast<const float*>(a.tv)[f];
-      if (i < 0 || i >= a.vocab) {
-        wrong |= i != -1;
-        i = -1;
-        v = -INFINITY;
-      } else {
-        ++entries;
-      }
-      id[k] = static_cast<int>(i);
-      pk[k] = v;
-      top = fmaxf(top, v);
-    }
-    top = warp_max(top);
-    wrong = __any_sync(0xffffffffu, wrong);
-    entries = __reduce_add_sync(0xffffffffu, entries);
-    if (lane == 0) red[warp] = make_float4(top, __int_as_float(entries), __int_as_float(wrong), 0.f);
-    __syncthreads();
-    entries = wrong = 0;
-    for (int q = 0; q < warps; ++q) {
-      top = fmaxf(top, red[q].x);
-      entries += __float_as_int(red[q].y);
-      wrong |= __float_as_int(red[q].z);
-    }
-    if (wrong && tid == 0) bad = 1;
-    const float sh = shift_of(top), lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
-    float sum = 0.f;
-    for (int k = tid; k < a.top_k; k += step) {
-      const int i = id[k];
-      float p = 0.f, x = 0.f;
-      if (i >= 0) {
-        // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
-        p = a.lse.p == nullptr ? term(pk[k], sh, a.c) : expf(pk[k] * a.inv_t - lse);
-        const int at = (i + r.lead) / kN<T> - v0;
-        const bool mine = at >= 0 && at < v1 - v0;
-        if (mine || rank == 0) x = widen(r.x[i]);
-        if (!LONG && mine) {
-          const uint32_t bit = 1u << ((at & 3) * 8 + (i + r.lead) % kN<T>);
-          if (atomicOr(reinterpret_cast<uint32_t*>(listed) + (at >> 2), bit) & bit) bad = 1;
-        }
-      }
-      pk[k] = p;
-      xk[k] = x;
-      sum += p;
-    }
-    sum = warp_sum(sum);
-    __syncthreads();  // red is read, the bits are set
-    if (lane == 0) red[warp].w = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int q = 0; q < warps; ++q) sum += red[q].w;
-    if (a.lse.p == nullptr) {
-      pscale = sum == 0.f ? 0.f : 1.f / sum;
-      sum_p = sum == 0.f ? 0.f : sum == sum ? 1.f : sum;
-    } else {
-      sum_p = sum;
-      if (sum != sum) rest = sum;
-      else if (entries < a.vocab) rest = fmaxf(0.f, 1.f - sum);
-    }
-  }
-
-  // m and the sum of the terms; the listed words' apart, so that a small rest
-  // is a sum of its own and keeps its precision.
-  float m = -INFINITY, sum = 0.f, top = 0.f;
-  if (!LONG) {
-    m = tile_max<T>(w);
-    tile_sum<T, kLists>(w, shift_of(m), a.c, listed + tid, step, sum, top);
-  } else {
-    for (int i0 = v0; i0 < v1; i0 += step * kV) {
-      if (kLists) {
-        __syncthreads();
-        for (int i = tid; i < step * kV / 4; i += step) reinterpret_cast<uint32_t*>(listed)[i] = 0;
-        __syncthreads();
-        for (int k = tid; k < a.top_k; k += step) {
-          const int at = (id[k] + r.lead) / kN<T> - i0;
-          if (id[k] >= 0 && at >= 0 && at < min(v1 - i0, step * kV)) {
-            const uint32_t bit = 1u << ((at & 3) * 8 + (id[k] + r.lead) % kN<T>);
-            if (atomicOr(reinterpret_cast<uint32_t*>(listed) + (at >> 2), bit) & bit) bad = 1;
-          }
-        }
-        __syncthreads();
-      }
-      load_tile<T>(w, r, i0 + tid, step, v1);
-      const float m2 = fmaxf(m, tile_max<T>(w));
-      const float sh = shift_of(m2), f = term(m, sh, a.c);
-      sum *= f;
-      top *= f;
-      tile_sum<T, kLists>(w, sh, a.c, listed + tid, step, sum, top);
-      m = m2;
-    }
-  }
-  sum = warp_sum(sum);
-  if (kLists) top = warp_sum(top);
-
-  // Every warp's part to every CTA of the cluster; each warp joins them all.
-  float wrong = 0.f;
-  if (kLists) {
-    __syncthreads();
-    wrong = bad ? NAN : 0.f;
-  }
-  const float4 part = make_float4(m, sum, top, wrong);
+  float4 p;
+  p.x = warp_max(part.m);
+  p.y = warp_sum(part.s * Ref(p.x, a.c).factor(part.m, a.c));
+  p.z = p.w = 0.f;
   if (ranks > 1) {
     cluster_wait();
-    if (lane < ranks) store_remote(parts + rank * warps + warp, lane, part);
+    if (lane == 0) store_remote(parts + rank * warps + warp, 0, p);
     __syncwarp();
     cluster_arrive();
     cluster_wait();
   } else {
-    if (lane == 0) parts[warp] = part;
+    if (lane == 0) parts[warp] = p;
     __syncthreads();
   }
-  const int all = warps * ranks;
-  m = -INFINITY;
-  for (int q = lane; q < all; q += 32) m = fmaxf(m, parts[q].x);
-  m = warp_max(m);
-  sum = top = wrong = 0.f;
-  for (int q = lane; q < all; q += 32) {
-    const float4 p = parts[q];
-    const float f = term(p.x, shift_of(m), a.c);
-    sum += p.y * f;
-    top += p.z * f;
-    wrong += p.w;
-  }
+  if (!writes) return;
+  float m = -INFINITY, sum = 0.f;
+  for (int k = lane; k < warps * ranks; k += 32) m = fmaxf(m, parts[k].x);
+  const Ref ref(warp_max(m), a.c);
+  for (int k = lane; k < warps * ranks; k += 32) sum += parts[k].y * ref.factor(parts[k].x, a.c);
   sum = warp_sum(sum);
-  float off = sum;  // the terms of the words that are not listed
-  if (kLists) {
-    sum += warp_sum(top);
-    wrong = warp_sum(wrong);
-  }
-  if (m == -INFINITY || m == INFINITY) wrong = NAN;  // a row without a distribution
-
-  float scale, at = 0.f;  // gradient: scale exp((x - m) / T), at the target `at`
-  float lead = 0.f, on = 0.f;
-  const bool first = rank == 0 && warp == 0;
-  if (!kLists) {
-    const float logp = y < 0 ? NAN : (x_at - m) * a.inv_t - logf(sum) + wrong;
-    if (first && lane == 0) {
-      if (a.logp != nullptr) a.logp[row] = logp;
-      if (a.stats != nullptr) a.stats[row] = make_float2(m + wrong, sum + wrong);
-      if (a.coef_out != nullptr) a.coef_out[row] = 0.f;
-    }
-    if (OP == kLogprobs) return;
-    const Token t = policy_token(a, logp, in);
-    wait_for_previous();
-    if (a.weights.p == nullptr) weight = 1.f / static_cast<float>(*a.count);
-    if (first) {
-      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = t.loss;
-      add_to_loss(a, row, a.weights.p != nullptr ? weight * t.loss : t.loss);
-    }
-    const float k_at = weight * a.gscale * a.inv_t * t.d;
-    scale = -k_at / sum;
-    at = scale * (y < 0 ? NAN : term(x_at, m, a.c)) + k_at;
-  } else {
-    wait_for_previous();
-    if (a.weights.p == nullptr) weight = 1.f / static_cast<float>(*a.count);
-    if (first) {
-      const float log_s = logf(sum);
-      float l = 0.f;
-      for (int k = lane; k < a.top_k; k += 32) {
-        const float p = pk[k] * pscale;
-        if (p != 0.f) l += p * (logf(p) - ((xk[k] - m) * a.inv_t - log_s));
-      }
-      l = warp_sum(l);
-      if (rest > 0.f) l += rest * (logf(rest) - (logf(off) - log_s));
-      const float loss = l / (a.inv_t * a.inv_t) + wrong;
-      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
-      add_to_loss(a, row, a.weights.p != nullptr ? weight * loss : loss);
-    }
-    // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
-    lead = weight * a.gscale / a.inv_t + wrong;
-    on = (sum_p + rest) / sum;
-    scale = lead * (on - (rest > 0.f ? rest / off : 0.f));
-  }
-  if (a.g == nullptr) return;
-  if (!LONG) {
-    store_tile<T>(w, r, g, v0 + tid, step, v1, m, a.c, scale, y, at);
-  } else {
-    for (int i0 = v0; i0 < v1; i0 += step * kV) {
-      load_tile<T>(w, r, i0 + tid, step, v1);
-      store_tile<T>(w, r, g, i0 + tid, step, v1, m, a.c, scale, y, at);
-    }
-  }
-  if (kLists) {
-    __syncthreads();  // the listed words' values replace those written above
-    for (int k = tid; k < a.top_k; k += step) {
-      const int i = id[k], v = (i + r.lead) / kN<T>;
-      if (i >= 0 && v >= v0 && v < v1) narrow(g.g[i], lead * (on * term(xk[k], m, a.c) - pk[k] * pscale));
-    }
+  const float wrong = fabsf(ref.m) == INFINITY ? NAN : 0.f;  // a row without a distribution
+  if (lane == 0) {
+    a.logp[row] = (x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+    if (a.stats != nullptr) a.stats[row] = make_float2(ref.m, sum + wrong);
   }
 }
 
@@ -810,28 +1117,27 @@ __global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad
   const int b = row / a.seq, s = row % a.seq;
   const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
   const GradRow<T> g(static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
-  const int64_t y0 = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+  const int64_t target = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
   if (a.coef != nullptr) wait_for_previous();
-  if (y0 == a.ignore) {
-    g.zero(tile, a.tiles);
+  if (target == a.ignore) {
+    g.zero(tile, a.tiles, kGradThreads);
     return;
   }
-  const int first = tile * kGradThreads * kV + threadIdx.x;
-  const int last = min(r.vecs, (tile + 1) * kGradThreads * kV);
-  uint4 w[kV];
-  load_tile<T>(w, r, first, kGradThreads, last);
+  const int first = tile * kGradVecs * kGradThreads + threadIdx.x;
+  const int last = min(r.vecs, (tile + 1) * kGradVecs * kGradThreads);
+  uint4 w[kGradVecs];
+  load_batch<T, kGradThreads>(w, r, first, last);
   const float2 st = a.stats[row];
   const float d = (a.coef != nullptr ? a.coef[row] : row_value(a.dlogp, b, s)) * a.gscale * a.inv_t;
-  const bool inside = y0 >= 0 && y0 < a.vocab;
+  const bool inside = target >= 0 && target < a.vocab;
   const float scale = inside ? -d / st.y : NAN;
-  const int y = inside ? static_cast<int>(y0) : -1;
-  float at = 0.f;
-  // `at` matters to the thread that holds the target, which alone writes it:
-  // the gradient may lie over the logits.
-  const int v = (y + r.lead) / kN<T>;
-  const bool mine = inside && v >= tile * kGradThreads * kV && v < last;
-  if (mine) at = scale * term(widen(r.x[y]), st.x, a.c) + d;
-  store_tile<T>(w, r, g, first, kGradThreads, last, st.x, a.c, scale, mine ? y : -1, at);
+  const Ref ref(st.x, a.c);
+  const int y = inside ? static_cast<int>(target) : kNoValue;
+  const int y_vec = inside ? (y + r.lead) / kN<T> : kNoValue;
+  const int lane_first = first - (threadIdx.x & 31), to_y = y_vec - lane_first;
+  const bool plain = batch_in<kGradThreads, kGradVecs>(lane_first, r.first_whole(), min(r.past_whole(), last)) && g.shift == 0 &&
+                     !ref.far() && !(to_y >= 0 && to_y < kGradVecs * kGradThreads && to_y % kGradThreads < 32);
+  store_batch<T, kGradThreads>(w, r, g, first, last, plain, ref, a.c, scale, y, y_vec, d);
 }
 
 // ---- a pair's loss ---------------------------------------------------------------
@@ -893,7 +1199,7 @@ __global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constan
     if (a.pair_loss != nullptr) a.pair_loss[pair] = static_cast<float>(loss);
     a.pair_part[pair] = loss;
     __threadfence();
-    last = atomicAdd(a.tickets, 1u) == static_cast<unsigned>(a.pairs - 1);
+    last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(a.pairs - 1);
     if (a.rewards != nullptr) {
       a.rewards[pair] = static_cast<float>(a.beta * D[0]);
       a.rewards[pair + a.pairs] = static_cast<float>(a.beta * D[1]);
@@ -944,9 +1250,9 @@ adaf_status check_logits(const loss_logits* x) {
   if (x->dtype != ADAF_FLOAT32 && x->dtype != ADAF_BFLOAT16) return invalid("logits: unknown dtype");
   if (x->batch < 0 || x->seq < 0) return invalid("logits: batch or seq < 0");
   if (x->vocab < 1) return invalid("logits: vocab must be >= 1");
-  if (x->vocab > kMaxVocab) return fail(ADAF_ERR_UNSUPPORTED, "logits: vocab must be below 2^30");
+  if (x->vocab > kMaxVocab) return fail(ADAF_ERR_UNSUPPORTED, "logits: vocab must be at most 2^21");
   if (x->batch > kMaxTokens || x->seq > kMaxTokens || x->batch * x->seq > kMaxTokens)
-    return fail(ADAF_ERR_UNSUPPORTED, "logits: batch * seq must be below 2^31");
+    return fail(ADAF_ERR_UNSUPPORTED, "logits: batch * seq must be at most 2^30");
   if (!(x->temperature > 0.0) || !std::isfinite(x->temperature))
     return invalid("invalid temperature (needs 0 < temperature < inf)");
   const double inv = 1.0 / x->temperature;
@@ -1002,20 +1308,18 @@ adaf_status check_grad(const loss_logits& x, const loss_grad* g, bool optional) 
 }
 
 struct Layout {
-  size_t off_count = 0, off_tickets = 0, off_groups = 0, off_part = 0, off_stats = 0, off_logp = 0, off_coef = 0, off_pair = 0, bytes = 0;
+  size_t off_part = 0, off_stats = 0, off_logp = 0, off_coef = 0, off_pair = 0, bytes = 0;
 };
+constexpr int kMaxClusters = 1 << 13;  // of k_loss_row: at most the CTAs that a GPU holds
 adaf_status layout(int64_t tokens, int64_t pairs, Layout* L) {
   if (tokens < 0 || pairs < 0) return invalid("tokens or pairs < 0");
   if (tokens > kMaxTokens || pairs > kMaxTokens / 2)
-    return fail(ADAF_ERR_UNSUPPORTED, "tokens must be below 2^31, pairs below 2^30");
-  size_t o = 0;
+    return fail(ADAF_ERR_UNSUPPORTED, "at most 2^30 tokens and 2^29 pairs");
+  size_t o = 256;  // the count of tokens, the ticket at byte 8
   const size_t n = static_cast<size_t>(tokens);
-  const size_t groups = (n + kGroup - 1) / kGroup;
-  L->off_count = o;   o += 64;
-  L->off_tickets = o; o = round_up(o + sizeof(unsigned) * (1 + groups), 256);
   if (pairs == 0) {
-    L->off_groups = o; o = round_up(o + sizeof(double) * groups, 256);
-    L->off_part = o;   o = round_up(o + sizeof(float) * n, 256);
+    L->off_part = o;
+    o = round_up(o + sizeof(double) * std::min<size_t>(n, kMaxClusters), 256);
   } else {
     L->off_stats = o; o = round_up(o + sizeof(float2) * n, 256);
     L->off_logp = o;  o = round_up(o + sizeof(float) * n, 256);
@@ -1040,6 +1344,7 @@ LossArgs base_args(const loss_logits& x, const loss_targets* y, const loss_grad*
   a.x = x.p;
   a.xsb = x.stride_b;
   a.xss = x.stride_s;
+  if (x.batch * x.seq > 0) extent(x.p, x.batch, x.seq, x.stride_b, x.stride_s, x.vocab, dtype_size(x.dtype), &a.x_begin, &a.x_end);
   a.seq = static_cast<int32_t>(x.seq);
   a.tokens = static_cast<int32_t>(x.batch * x.seq);
   a.vocab = static_cast<int32_t>(x.vocab);
@@ -1059,8 +1364,8 @@ LossArgs base_args(const loss_logits& x, const loss_targets* y, const loss_grad*
   return a;
 }
 
-const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_grad", "k_loss_pair"};
-enum Slot { kSlotCount = 0, kSlotRow, kSlotGrad, kSlotPair, kNumKernels };
+const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_forward", "k_loss_grad", "k_loss_pair"};
+enum Slot { kSlotCount = 0, kSlotRow, kSlotForward, kSlotGrad, kSlotPair, kNumKernels };
 struct ProfRecord {
   int slot;
   cudaEvent_t start, stop;
@@ -1117,48 +1422,116 @@ adaf_status launch(int slot, void (*kernel)(LossArgs, Args...), int64_t grid, in
   return ADAF_OK;
 }
 
-static int envi(const char* n, int d) { const char* v = getenv(n); return v ? atoi(v) : d; }
-static int kRowThreads() { return envi("MEO_T", 512); }
-static int kFewCtas() { return envi("MEO_F", 304); }
-// How a row is cut: CTAs, threads of each, vectors of each; `again`: the
-// threads cannot keep the row and read it twice.
-struct Cut {
-  int cluster, threads, vecs;
-  bool again;
-};
-Cut cut_row(int64_t tokens, int64_t vocab, size_t es) {
-  const int64_t per = 16 / static_cast<int64_t>(es), vecs = (vocab + 2 * per - 2) / per;  // the most, at any alignment
-  auto threads_of = [&](int64_t c) { return ((vecs + c - 1) / c + kV * 32 - 1) / (kV * 32) * 32; };
-  int64_t c = 1;
-  const int64_t most = kRowThreads();
-  while (c < kMaxCluster && threads_of(c) > most) c *= 2;
-  while (c < kMaxCluster && tokens * c < kFewCtas() && threads_of(c) > 64) c *= 2;
-  if (tokens * c > kMaxTokens) c = 1;
-  Cut cut;
-  cut.cluster = static_cast<int>(c);
-  cut.threads = static_cast<int>(std::min<int64_t>(threads_of(c), kMaxThreads));
-  cut.vecs = static_cast<int>((vecs + c - 1) / c);
-  cut.again = cut.vecs > cut.threads * kV;
-  return cut;
+// Vectors of a row, at any alignment that the rows have.
+int row_vecs(const LossArgs& a, int32_t dtype) {
+  const int es = static_cast<int>(dtype_size(dtype)), per = 16 / es;
+  const bool even = a.x_begin % 16 == 0 && a.xsb * es % 16 == 0 && a.xss * es % 16 == 0;
+  return div_up(a.vocab + (even ? 0 : per - 1), per);
 }
+
+// How a row is cut: CTAs, threads of each that sum, vectors of a CTA, batches
+// of a thread, places of the ring (0: the row is read twice).
+struct Cut {
+  int cluster, threads, vecs_per_cta, batches, slots, shared;
+};
+constexpr int kSharedBytes = 227 << 10;  // of an SM; a CTA takes 1 KB more than it asks for
+constexpr int kKeep = 4;                 // batches of a row that a thread keeps
+
+Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
+  Cut c;
+  auto set = [&](int cluster, int keep) {
+    c.cluster = cluster;
+    c.vecs_per_cta = div_up(div_up(vecs, cluster), kChunk) * kChunk;
+    c.threads = c.vecs_per_cta <= kChunk * keep ? 32 : c.vecs_per_cta <= 4 * kChunk * keep ? 128 : 512;
+    c.batches = div_up(c.vecs_per_cta, c.threads * kBatch);
+    c.shared = 2 * c.threads / 32 * cluster * static_cast<int>(sizeof(float4)) +
+               (lists ? 2 * list_bytes(c.batches * kBatch * c.threads, top_k) : 0);
+    const int batch = c.threads * kBatch * 16 + c.threads / 32 * 8;  // places and their barriers
+    for (int ctas = row_ctas(c.threads, lists); ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs
+      const int room = kSharedBytes / ctas - 1024 - 64 - c.shared;
+      c.slots = std::min(2 * c.batches, std::max(0, room / batch));
+      if (c.slots > c.batches) break;
+    }
+    if (c.slots < c.batches) c.slots = 0;  // with 512 threads only: fewer have places enough
+    c.shared += c.slots * c.threads * kBatch * 16 + div_up(c.slots * c.threads / 32 * 8, 16) * 16;
+  };
+  int cluster = 1;
+  set(1, kKeep);
+  while (cluster < kMaxCluster && c.batches > kKeep) set(cluster *= 2, kKeep);
+  while (cluster < kMaxCluster && tokens * cluster < sms && c.vecs_per_cta > 256) set(cluster *= 2, 1);
+  return c;
+}
+
+struct Device {
+  int sms = 0;
+  std::map<std::pair<const void*, int64_t>, int> clusters;  // that run at a time, by kernel and cut
+};
+std::map<int, Device> g_devices;
 
 template <int OP>
 adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
-  const Cut cut = cut_row(a.tokens, a.vocab, dtype_size(dtype));
-  a.vecs_per_cta = cut.vecs;
-  const int shared = row_shared(OP == kDistill, cut.threads / 32, cut.cluster, a.top_k);
+  int device = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::unique_lock<std::mutex> lock(g_mu);
+  Device& dev = g_devices[device];
+  if (dev.sms == 0 && (e = cudaDeviceGetAttribute(&dev.sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
+    return cuda_fail(e, "cudaDeviceGetAttribute");
+  sms = dev.sms;
+  const Cut cut = cut_row(a.tokens, row_vecs(a, dtype), OP == kDistill, a.top_k, sms);
+  const bool bf16 = dtype == ADAF_BFLOAT16, twice_read = cut.slots == 0;
+  void (*kernel)(LossArgs);
+  if (twice_read) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 512, true> : k_loss_row<float, OP, 512, true>;
+  else if (cut.threads == 512) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 512, false> : k_loss_row<float, OP, 512, false>;
+  else if (cut.threads == 128) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 128, false> : k_loss_row<float, OP, 128, false>;
+  else kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 32, false> : k_loss_row<float, OP, 32, false>;
+  const int threads = cut.threads + (OP == kDistill ? 32 : 0);
+  int& most = dev.clusters[{reinterpret_cast<const void*>(kernel),
+                            (static_cast<int64_t>(cut.shared) << 16) + (cut.threads << 4) + cut.cluster}];
+  if (most == 0) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10)) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute");
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(cut.shared);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {static_cast<unsigned>(cut.cluster), 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)) != cudaSuccess)
+      return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    if (n < 1) return fail(ADAF_ERR_CUDA, "no cluster of k_loss_row fits on the device");
+    most = std::min(n, kMaxClusters);
+  }
+  const int64_t clusters = std::min<int64_t>(a.tokens, most);
+  lock.unlock();
+  a.vecs_per_cta = cut.vecs_per_cta;
+  a.batches = cut.batches;
+  a.slots = cut.slots;
+  return launch(kSlotRow, kernel, clusters * cut.cluster, threads, cut.shared, cut.cluster, true, s, a);
+}
+adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
+  const int vecs = row_vecs(a, dtype);
+  int64_t cluster = 1;
+  while (cluster < kMaxCluster && a.tokens * cluster < 304 && div_up(vecs, static_cast<int>(cluster)) > 512) cluster *= 2;
+  a.vecs_per_cta = div_up(vecs, static_cast<int>(cluster));
+  const int threads = a.vecs_per_cta <= 32 * kBatch * 2 ? 32 : a.vecs_per_cta <= 128 * kBatch * 2 ? 128 : 512;
+  const int shared = threads / 32 * static_cast<int>(cluster * sizeof(float4));
   const bool bf16 = dtype == ADAF_BFLOAT16;
   void (*const kernel)(LossArgs) =
-      cut.again ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
-                : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
-  return launch(kSlotRow, kernel, static_cast<int64_t>(a.tokens) * cut.cluster, cut.threads, shared, cut.cluster,
-                OP != kLogprobs, s, a);
+      threads == 512   ? (bf16 ? k_loss_forward<__nv_bfloat16, 512> : k_loss_forward<float, 512>)
+      : threads == 128 ? (bf16 ? k_loss_forward<__nv_bfloat16, 128> : k_loss_forward<float, 128>)
+                       : (bf16 ? k_loss_forward<__nv_bfloat16, 32> : k_loss_forward<float, 32>);
+  return launch(kSlotForward, kernel, a.tokens * cluster, threads, shared, static_cast<int>(cluster), false, s, a);
 }
 adaf_status launch_grad(LossArgs a, int32_t dtype, cudaStream_t s) {
-  const int64_t per = 16 / static_cast<int64_t>(dtype_size(dtype)), vecs = (a.vocab + 2 * per - 2) / per;
-  a.tiles = static_cast<int32_t>((vecs + kGradThreads * kV - 1) / (kGradThreads * kV));
+  a.tiles = div_up(row_vecs(a, dtype), kGradThreads * kGradVecs);
   const int64_t grid = static_cast<int64_t>(a.tokens) * a.tiles;
-  if (grid > kMaxTokens) return fail(ADAF_ERR_UNSUPPORTED, "gradient of more than 2^31 tiles");
+  if (grid > INT32_MAX) return fail(ADAF_ERR_UNSUPPORTED, "gradient of more than 2^31 tiles");
   return launch(kSlotGrad, dtype == ADAF_BFLOAT16 ? k_loss_grad<__nv_bfloat16> : k_loss_grad<float>, grid, kGradThreads,
                 0, 1, a.coef != nullptr, s, a);
 }
@@ -1200,7 +1573,7 @@ adaf_status loss_token_logprobs(const loss_logits* x, const loss_targets* y, flo
   LossArgs a = base_args(*x, y, nullptr);
   a.logp = logp;
   a.stats = reinterpret_cast<float2*>(stats);
-  return launch_rows<kLogprobs>(a, x->dtype, static_cast<cudaStream_t>(stream));
+  return launch_forward(a, x->dtype, static_cast<cudaStream_t>(stream));
 }
 
 adaf_status loss_token_logprobs_backward(const loss_logits* x, const loss_targets* y, const float* stats,
@@ -1247,10 +1620,9 @@ adaf_status loss_policy(const loss_logits* x, const loss_targets* y, const loss_
   a.loss = loss;
   a.logp = logp;
   a.token_loss = token_loss;
-  a.count = reinterpret_cast<int64_t*>(ws + L.off_count);
-  a.part = reinterpret_cast<float*>(ws + L.off_part);
-  a.group_part = reinterpret_cast<double*>(ws + L.off_groups);
-  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
+  a.count = reinterpret_cast<int64_t*>(ws);
+  a.ticket = reinterpret_cast<unsigned*>(ws + 8);
+  a.part = reinterpret_cast<double*>(ws + L.off_part);
   a.adv = rows_of(args->advantages);
   a.old = rows_of(args->old_logp);
   a.ref = rows_of(args->ref_logp);
@@ -1312,12 +1684,12 @@ adaf_status loss_preference(const loss_logits* x, const loss_targets* y, const l
   a.beta = args->beta;
   a.smooth = args->label_smoothing;
   a.margin = args->margin;
-  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
+  a.ticket = reinterpret_cast<unsigned*>(ws + 8);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.tokens > 0) {
-    LOSS_CHECK(launch_rows<kLogprobs>(a, x->dtype, s));
+    LOSS_CHECK(launch_forward(a, x->dtype, s));
   } else {
-    const cudaError_t e = cudaMemsetAsync(a.tickets, 0, sizeof(unsigned), s);
+    const cudaError_t e = cudaMemsetAsync(a.ticket, 0, sizeof(unsigned), s);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
   }
   LOSS_CHECK(launch(kSlotPair, k_loss_pair, a.pairs, kPairThreads, 0, 1, a.tokens > 0, s, a));
@@ -1352,10 +1724,9 @@ adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, co
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.loss = loss;
   a.token_loss = token_loss;
-  a.count = reinterpret_cast<int64_t*>(ws + L.off_count);
-  a.part = reinterpret_cast<float*>(ws + L.off_part);
-  a.group_part = reinterpret_cast<double*>(ws + L.off_groups);
-  a.tickets = reinterpret_cast<unsigned*>(ws + L.off_tickets);
+  a.count = reinterpret_cast<int64_t*>(ws);
+  a.ticket = reinterpret_cast<unsigned*>(ws + 8);
+  a.part = reinterpret_cast<double*>(ws + L.off_part);
   a.ids = args->ids;
   a.idt = args->ids_dtype;
   a.isb = args->ids_stride_b;
