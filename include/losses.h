@@ -50,7 +50,8 @@
  * writes nothing out of range.
  *
  * Logits are fp32 or bf16 and the gradient has their type; everything between
- * is fp32 (sums over tokens fp64), and gradients are rounded once.  The sums
+ * is fp32 (sums over tokens with compensation), and gradients are rounded
+ * once.  The sums
  * run in a fixed order: equal inputs give equal bits.
  *
  * Every call only launches kernels on the caller's stream: it allocates

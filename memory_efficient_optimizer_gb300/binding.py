@@ -495,29 +495,61 @@ def loss_workspace_size(tokens: int, pairs: int = 0) -> int:
     return int(out.value)
 
 
-def loss_token_logprobs(x: loss_logits, y: loss_targets, logp: int, stats: int, stream: int) -> None:
-    _check(load().loss_token_logprobs(x, y, logp, stats, stream))
+# The structs come as ctypes.Structure or packed as bytes (losses.py).  A
+# second set of function objects takes both by address; pointers are ints, 0
+# for NULL.
+_loss_calls = {}
 
 
-def loss_token_logprobs_backward(x: loss_logits, y: loss_targets, stats: int, grad_logp: loss_rows,
-                                 grad: loss_grad, stream: int) -> None:
-    _check(load().loss_token_logprobs_backward(x, y, stats, grad_logp, grad, stream))
+def _loss_call(name: str):
+    f = _loss_calls.get(name)
+    if f is None:
+        f = load()[name]
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_size_t if t is ctypes.c_size_t else ctypes.c_void_p for t in getattr(load(), name).argtypes]
+        _loss_calls[name] = f
+    return f
 
 
-def loss_policy(x: loss_logits, y: loss_targets, args: loss_policy_args, grad, loss: int, logp: int,
-                token_loss: int, workspace: int, workspace_bytes: int, stream: int) -> None:
-    _check(load().loss_policy(x, y, args, grad, loss, logp, token_loss, workspace, workspace_bytes, stream))
+def _by_address(s):
+    return s if s.__class__ is bytes or s is None else ctypes.byref(s)
 
 
-def loss_preference(x: loss_logits, y: loss_targets, args: loss_preference_args, grad, loss: int, pair_loss: int,
-                    rewards: int, logp: int, workspace: int, workspace_bytes: int, stream: int) -> None:
-    _check(load().loss_preference(x, y, args, grad, loss, pair_loss, rewards, logp, workspace, workspace_bytes,
-                                  stream))
+def loss_token_logprobs(x, y, logp: int, stats: int, stream: int) -> None:
+    st = _loss_call("loss_token_logprobs")(_by_address(x), _by_address(y), logp, stats, stream)
+    if st:
+        _check(st)
 
 
-def loss_distill(x: loss_logits, args: loss_distill_args, grad, loss: int, token_loss: int, workspace: int,
-                 workspace_bytes: int, stream: int) -> None:
-    _check(load().loss_distill(x, args, grad, loss, token_loss, workspace, workspace_bytes, stream))
+def loss_token_logprobs_backward(x, y, stats: int, grad_logp, grad, stream: int) -> None:
+    st = _loss_call("loss_token_logprobs_backward")(_by_address(x), _by_address(y), stats, _by_address(grad_logp),
+                                                    _by_address(grad), stream)
+    if st:
+        _check(st)
+
+
+def loss_policy(x, y, args, grad, loss: int, logp: int, token_loss: int, workspace: int, workspace_bytes: int,
+                stream: int) -> None:
+    st = _loss_call("loss_policy")(_by_address(x), _by_address(y), _by_address(args), _by_address(grad), loss, logp,
+                                   token_loss, workspace, workspace_bytes, stream)
+    if st:
+        _check(st)
+
+
+def loss_preference(x, y, args, grad, loss: int, pair_loss: int, rewards: int, logp: int, workspace: int,
+                    workspace_bytes: int, stream: int) -> None:
+    st = _loss_call("loss_preference")(_by_address(x), _by_address(y), _by_address(args), _by_address(grad), loss,
+                                       pair_loss, rewards, logp, workspace, workspace_bytes, stream)
+    if st:
+        _check(st)
+
+
+def loss_distill(x, args, grad, loss: int, token_loss: int, workspace: int, workspace_bytes: int,
+                 stream: int) -> None:
+    st = _loss_call("loss_distill")(_by_address(x), _by_address(args), _by_address(grad), loss, token_loss, workspace,
+                                    workspace_bytes, stream)
+    if st:
+        _check(st)
 
 
 def loss_profile_enable(on: bool) -> None:

@@ -43,6 +43,34 @@ __host__ __device__ constexpr int div_up(int x, int y) { return (x + y - 1) / y;
 
 enum Op : int { kLogprobs, kPolicy, kDistill };
 
+// ---- sums over tokens ------------------------------------------------------------
+// An fp32 sum that carries what its additions round off: as good as an fp64
+// one, whose additions and divisions run at a few per cent of the rate here
+// (the kernels that end a call took 14 to 19 us with them, 3 to 5 without).
+struct Sum {
+  float s = 0.f, rest = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = __fadd_rn(s, x), b = __fsub_rn(t, s);
+    rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.s);
+    rest = __fadd_rn(rest, o.rest);
+  }
+  // Over the lanes of a warp, in a fixed order (equal in all lanes).
+  __device__ __forceinline__ void over_warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Sum p;
+      p.s = __shfl_xor_sync(0xffffffffu, s, o);
+      p.rest = __shfl_xor_sync(0xffffffffu, rest, o);
+      add(p);
+    }
+  }
+  __device__ __forceinline__ float total() const { return fabsf(s) == INFINITY ? s : s + rest; }
+};
+
 struct Rows {
   const void* p;
   int64_t sb, ss;
@@ -63,8 +91,8 @@ struct LossArgs {
   float* logp;
   float* token_loss;
   float2* stats;                  // [tokens]: m, s
-  int64_t* count;                 // counted tokens
-  double* part;                   // [clusters]: sum of w l, or of l
+  int* count;                     // counted tokens
+  Sum* part;                      // [clusters]: sum of w l, or of l
   unsigned* ticket;
   int32_t vecs_per_cta;           // k_loss_row, k_loss_forward: vectors of a row for a CTA
   int32_t batches, slots;         // k_loss_row: batches of a thread; places of the ring for them
@@ -79,10 +107,10 @@ struct LossArgs {
   const void* offsets;
   int32_t odt, kind, average;
   int64_t pairs;
-  double beta, smooth, margin;
+  float beta, smooth, margin;
   float* pair_loss;
   float* rewards;
-  double* pair_part;              // [pairs]
+  float* pair_part;               // [pairs]
   // distill
   const void* ids;
   const void* tv;
@@ -113,18 +141,6 @@ __device__ __forceinline__ bool counted(const LossArgs& a, int op, int b, int s)
   if (op == kDistill)
     return a.mask.p == nullptr || static_cast<const uint8_t*>(a.mask.p)[b * a.mask.sb + s * a.mask.ss] != 0;
   return load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss) != a.ignore;
-}
-
-// ---- sums over a block, in a fixed order ---------------------------------------
-__device__ __forceinline__ double block_sum(double v, double* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double t = 0.0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += red[w];
-  return t;
 }
 
 // ---- terms -----------------------------------------------------------------------
@@ -510,11 +526,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -524,17 +535,22 @@ __device__ __forceinline__ float warp_max(float v) {
 // ---- counted tokens ------------------------------------------------------------
 // Also clears the ticket of the sum over tokens.
 __global__ void __launch_bounds__(kCountThreads) k_loss_count(const __grid_constant__ LossArgs a, int op) {
-  __shared__ double red[32];
+  __shared__ int parts[kCountThreads / 32];
   let_next_start();
   if (threadIdx.x == 0) *a.ticket = 0;
   int n = 0;
 #pragma unroll 8
   for (uint32_t t = threadIdx.x; t < static_cast<uint32_t>(a.tokens); t += kCountThreads)
     n += counted(a, op, static_cast<int>(t / static_cast<uint32_t>(a.seq)), static_cast<int>(t % static_cast<uint32_t>(a.seq)));
-  const double total = block_sum(n, red);  // exact: below 2^53
-  if (threadIdx.x == 0) {
-    *a.count = static_cast<int64_t>(total);
-    if (a.tokens == 0) *a.loss = 0.f;
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    n = __reduce_add_sync(0xffffffffu, parts[threadIdx.x]);
+    if (threadIdx.x == 0) {
+      *a.count = n;
+      if (a.tokens == 0) *a.loss = 0.f;
+    }
   }
 }
 
@@ -800,7 +816,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
     const Row<T> r = row_at(at);
     copy(r, 0, chunks(min(r.vecs, v0 + a.vecs_per_cta)));
   }
-  double share = 0.0;  // of the cluster's rows in the loss (rank 0, warp 0)
+  Sum share;           // of the cluster's rows in the loss (rank 0, warp 0)
   float by_count = 0.f;
   bool waited = false;
   int q = 0;  // counted rows so far
@@ -937,7 +953,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
         if (writes) {
           if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
           if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = t.loss;
-          share += a.weights.p != nullptr ? static_cast<double>(w) * t.loss : t.loss;
+          share.add(a.weights.p != nullptr ? w * t.loss : t.loss);
         }
         more = w * a.gscale * a.inv_t * t.d;
         scale = -more / sum;
@@ -955,7 +971,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
           if (rest > 0.f) l += rest * (logf(rest) - (logf(off) - log_s));
           const float loss = l / (a.inv_t * a.inv_t) + wrong;
           if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
-          share += a.weights.p != nullptr ? static_cast<double>(w) * loss : loss;
+          share.add(a.weights.p != nullptr ? w * loss : loss);
         }
         // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
         lead = w * a.gscale / a.inv_t + wrong;
@@ -1017,7 +1033,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
     target1 = target2;
   }
   if (__any_sync(0xffffffffu, dead)) {
-    share = NAN;
+    share.s = NAN;
     // copies still in flight land before the CTA's memory is given up
     for (int k = 0; k < slots; ++k) wait_phase(full + k, k < base ? parity : parity ^ 1);
   }
@@ -1033,12 +1049,18 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
     }
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
-    double v = 0.0;
-    for (int k = lane; k < stride; k += 32) v += __ldcg(a.part + k);
-    v = warp_sum(v);
+    Sum v;
+    for (int k = lane; k < stride; k += 32) {
+      const float2 o = __ldcg(reinterpret_cast<const float2*>(a.part) + k);
+      Sum p;
+      p.s = o.x;
+      p.rest = o.y;
+      v.add(p);
+    }
+    v.over_warp();
     if (lane == 0) {
-      const double n = a.weights.p == nullptr ? static_cast<double>(*a.count) : 1.0;
-      *a.loss = n > 0.0 ? static_cast<float>(v / n) : 0.f;
+      const float n = a.weights.p == nullptr ? static_cast<float>(*a.count) : 1.f;
+      *a.loss = n > 0.f ? v.total() / n : 0.f;
     }
   }
 }
@@ -1142,14 +1164,13 @@ __global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad
 
 // ---- a pair's loss ---------------------------------------------------------------
 __global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constant__ LossArgs a) {
-  __shared__ double red[32];
-  __shared__ int last;
+  __shared__ Sum sums[2][kPairThreads / 32];
+  __shared__ int counts[2][kPairThreads / 32], last;
   let_next_start();
   wait_for_previous();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t pair = blockIdx.x;
-  double D[2];
   int64_t from[2], to[2];
-  double n[2];
   bool ok = true;
   for (int h = 0; h < 2; ++h) {
     const int64_t q = pair + h * a.pairs;
@@ -1164,60 +1185,77 @@ __global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constan
       from[h] = q * a.seq;
       to[h] = from[h] + a.seq;
     }
-    double sum = 0.0, cnt = 0.0;
-    for (int64_t t = from[h] + threadIdx.x; t < to[h]; t += kPairThreads) {
-      const int b = static_cast<int>(t / a.seq), s = static_cast<int>(t % a.seq);
+    Sum sum;
+    int n = 0;
+#pragma unroll 4
+    for (uint32_t t = static_cast<uint32_t>(from[h]) + threadIdx.x; t < static_cast<uint32_t>(to[h]); t += kPairThreads) {
+      const int b = static_cast<int>(t / static_cast<uint32_t>(a.seq)), s = static_cast<int>(t % static_cast<uint32_t>(a.seq));
       if (!counted(a, kLogprobs, b, s)) continue;
-      sum += a.logp[t];
-      if (a.ref.p != nullptr) sum -= row_value(a.ref, b, s);
-      cnt += 1.0;
+      sum.add(a.logp[t]);
+      if (a.ref.p != nullptr) sum.add(-row_value(a.ref, b, s));
+      ++n;
     }
-    D[h] = block_sum(sum, red);
-    n[h] = block_sum(cnt, red);
-    if (a.average) D[h] = n[h] > 0.0 ? D[h] / n[h] : 0.0;
+    sum.over_warp();
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) {
+      sums[h][warp] = sum;
+      counts[h][warp] = n;
+    }
   }
-  const double h = D[0] - D[1];
-  double loss, dh;  // and its derivative with respect to h
+  __syncthreads();
+  float D[2], n[2];
+  for (int h = 0; h < 2; ++h) {
+    Sum sum;
+    int count = 0;
+    for (int w = 0; w < kPairThreads / 32; ++w) {
+      const Sum p = sums[h][w];
+      sum.add(p);
+      count += counts[h][w];
+    }
+    n[h] = static_cast<float>(count);
+    D[h] = a.average ? (count > 0 ? sum.total() / n[h] : 0.f) : sum.total();
+  }
+  const float h = D[0] - D[1];
+  float loss, dh;  // and its derivative with respect to h
   if (a.kind == LOSS_PREFERENCE_SIGMOID) {
-    const double z = a.beta * h - a.margin, e = exp(-fabs(z)), l = log1p(e);
-    const double neg = l + fmax(-z, 0.0), pos = l + fmax(z, 0.0);  // -ln s(z), -ln s(-z)
-    const double sig = z >= 0.0 ? 1.0 / (1.0 + e) : e / (1.0 + e);
-    const double sig_neg = z >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);
-    loss = (1.0 - a.smooth) * neg + a.smooth * pos;
-    dh = a.beta * (a.smooth * sig - (1.0 - a.smooth) * sig_neg);
+    const float z = a.beta * h - a.margin, e = expf(-fabsf(z)), l = log1pf(e);
+    const float neg = l + fmaxf(-z, 0.f), pos = l + fmaxf(z, 0.f);  // -ln s(z), -ln s(-z)
+    const float big = 1.f / (1.f + e), small = e / (1.f + e);
+    loss = (1.f - a.smooth) * neg + a.smooth * pos;
+    dh = a.beta * (z >= 0.f ? a.smooth * big - (1.f - a.smooth) * small : a.smooth * small - (1.f - a.smooth) * big);
   } else if (a.kind == LOSS_PREFERENCE_HINGE) {
-    const double z = 1.0 + a.margin - a.beta * h;
-    loss = z > 0.0 || isnan(z) ? z : 0.0;
-    dh = z > 0.0 || isnan(z) ? -a.beta + 0.0 * z : 0.0;
+    const float z = 1.f + a.margin - a.beta * h;
+    loss = z > 0.f || isnan(z) ? z : 0.f;
+    dh = z > 0.f ? -a.beta : isnan(z) ? z : 0.f;
   } else {
-    const double z = h - 1.0 / (2.0 * a.beta) - a.margin;
+    const float z = h - 1.f / (2.f * a.beta) - a.margin;
     loss = z * z;
-    dh = 2.0 * z;
+    dh = 2.f * z;
   }
   if (!ok) loss = dh = NAN;
   if (threadIdx.x == 0) {
-    if (a.pair_loss != nullptr) a.pair_loss[pair] = static_cast<float>(loss);
+    if (a.pair_loss != nullptr) a.pair_loss[pair] = loss;
     a.pair_part[pair] = loss;
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(a.pairs - 1);
     if (a.rewards != nullptr) {
-      a.rewards[pair] = static_cast<float>(a.beta * D[0]);
-      a.rewards[pair + a.pairs] = static_cast<float>(a.beta * D[1]);
+      a.rewards[pair] = a.beta * D[0];
+      a.rewards[pair + a.pairs] = a.beta * D[1];
     }
   }
   for (int q = 0; q < 2; ++q) {
-    double c = (q == 0 ? dh : -dh) / static_cast<double>(a.pairs);
-    if (a.average) c = n[q] > 0.0 ? c / n[q] : 0.0;
-    for (int64_t t = from[q] + threadIdx.x; t < to[q]; t += kPairThreads) a.coef_out[t] = static_cast<float>(c);
+    float c = (q == 0 ? dh : -dh) / static_cast<float>(a.pairs);
+    if (a.average) c = n[q] > 0.f ? c / n[q] : 0.f;
+    for (int64_t t = from[q] + threadIdx.x; t < to[q]; t += kPairThreads) a.coef_out[t] = c;
   }
   __syncthreads();
-  if (!last) return;
+  if (!last || warp != 0) return;
   // the last pair to come sums them all, in order
   __threadfence();
-  double v = 0.0;
-  for (int64_t k = threadIdx.x; k < a.pairs; k += kPairThreads) v += __ldcg(a.pair_part + k);
-  v = block_sum(v, red);
-  if (threadIdx.x == 0) *a.loss = static_cast<float>(v / static_cast<double>(a.pairs));
+  Sum v;
+  for (int64_t k = lane; k < a.pairs; k += 32) v.add(__ldcg(a.pair_part + k));
+  v.over_warp();
+  if (lane == 0) *a.loss = v.total() / static_cast<float>(a.pairs);
 }
 
 // ---- host side -----------------------------------------------------------------
@@ -1319,12 +1357,12 @@ adaf_status layout(int64_t tokens, int64_t pairs, Layout* L) {
   const size_t n = static_cast<size_t>(tokens);
   if (pairs == 0) {
     L->off_part = o;
-    o = round_up(o + sizeof(double) * std::min<size_t>(n, kMaxClusters), 256);
+    o = round_up(o + sizeof(Sum) * std::min<size_t>(n, kMaxClusters), 256);
   } else {
     L->off_stats = o; o = round_up(o + sizeof(float2) * n, 256);
     L->off_logp = o;  o = round_up(o + sizeof(float) * n, 256);
     L->off_coef = o;  o = round_up(o + sizeof(float) * n, 256);
-    L->off_pair = o;  o = round_up(o + sizeof(double) * static_cast<size_t>(pairs), 256);
+    L->off_pair = o;  o = round_up(o + sizeof(float) * static_cast<size_t>(pairs), 256);
   }
   L->bytes = o;
   return ADAF_OK;
@@ -1620,9 +1658,9 @@ adaf_status loss_policy(const loss_logits* x, const loss_targets* y, const loss_
   a.loss = loss;
   a.logp = logp;
   a.token_loss = token_loss;
-  a.count = reinterpret_cast<int64_t*>(ws);
+  a.count = reinterpret_cast<int*>(ws);
   a.ticket = reinterpret_cast<unsigned*>(ws + 8);
-  a.part = reinterpret_cast<double*>(ws + L.off_part);
+  a.part = reinterpret_cast<Sum*>(ws + L.off_part);
   a.adv = rows_of(args->advantages);
   a.old = rows_of(args->old_logp);
   a.ref = rows_of(args->ref_logp);
@@ -1674,16 +1712,16 @@ adaf_status loss_preference(const loss_logits* x, const loss_targets* y, const l
   a.logp = logp != nullptr ? logp : reinterpret_cast<float*>(ws + L.off_logp);
   a.stats = reinterpret_cast<float2*>(ws + L.off_stats);
   a.coef_out = reinterpret_cast<float*>(ws + L.off_coef);
-  a.pair_part = reinterpret_cast<double*>(ws + L.off_pair);
+  a.pair_part = reinterpret_cast<float*>(ws + L.off_pair);
   a.pairs = args->pairs;
   a.ref = rows_of(args->ref_logp);
   a.offsets = args->seq_offsets;
   a.odt = args->offsets_dtype;
   a.kind = args->kind;
   a.average = args->average;
-  a.beta = args->beta;
-  a.smooth = args->label_smoothing;
-  a.margin = args->margin;
+  a.beta = static_cast<float>(args->beta);
+  a.smooth = static_cast<float>(args->label_smoothing);
+  a.margin = static_cast<float>(args->margin);
   a.ticket = reinterpret_cast<unsigned*>(ws + 8);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.tokens > 0) {
@@ -1724,9 +1762,9 @@ adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, co
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.loss = loss;
   a.token_loss = token_loss;
-  a.count = reinterpret_cast<int64_t*>(ws);
+  a.count = reinterpret_cast<int*>(ws);
   a.ticket = reinterpret_cast<unsigned*>(ws + 8);
-  a.part = reinterpret_cast<double*>(ws + L.off_part);
+  a.part = reinterpret_cast<Sum*>(ws + L.off_part);
   a.ids = args->ids;
   a.idt = args->ids_dtype;
   a.isb = args->ids_stride_b;

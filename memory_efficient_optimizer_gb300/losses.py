@@ -21,15 +21,38 @@ the header says how bad ones show in the results.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import binding as B
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+# Handle of the current stream of a device (the torch.cuda call that makes a
+# Stream object for it takes twenty times as long).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _DTYPES = {torch.float32: B.ADAF_FLOAT32, torch.bfloat16: B.ADAF_BFLOAT16}
 _INDEX = {torch.int32: B.LOSS_INT32, torch.int64: B.LOSS_INT64}
-_NO_ROWS = B.loss_rows(None, 0, 0)
+_NO_ROWS = (0, 0, 0)
+_FP32 = torch.float32
+
+# The C structs, packed here in one step each (a ctypes.Structure costs several
+# times that, and for a few tokens the host's part is most of a call).
+_LOGITS = struct.Struct("@Piqqqqqd")
+_TARGETS = struct.Struct("@Pqqiq")
+_GRAD = struct.Struct("@Pqqd")
+_ROWS = struct.Struct("@Pqq")
+_POLICY = struct.Struct("@PqqPqqPqqPqqddd")
+_PREFERENCE = struct.Struct("@PqqqPiiiddd")
+_DISTILL = struct.Struct("@PiqqPiqqiPqqPqqPqq")
+for _s, _c in ((_LOGITS, B.loss_logits), (_TARGETS, B.loss_targets), (_GRAD, B.loss_grad), (_ROWS, B.loss_rows),
+               (_POLICY, B.loss_policy_args), (_PREFERENCE, B.loss_preference_args), (_DISTILL, B.loss_distill_args)):
+    assert _s.size == ctypes.sizeof(_c), _c.__name__
 
 
 class TokenLogprobs(NamedTuple):
@@ -58,101 +81,100 @@ class DistillLoss(NamedTuple):
     token_loss: torch.Tensor  # fp32 per token, before the weights
 
 
-class _Call:
-    """The logits of one call, its device and stream."""
+def _context(logits, stream):
+    """What to enter so that the logits' device and the call's stream are
+    current (the library launches on the current device, and outputs and
+    workspace are allocated for the stream that uses them); None if they are."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if isinstance(logits, torch.Tensor) and logits.is_cuda and logits.get_device() != _current_device():
+        return torch.cuda.device(logits.device)
+    return None
 
-    def __init__(self, logits, temperature, stream):
-        if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES:
-            raise ValueError("logits must be a float32 or bfloat16 tensor")
-        dim = logits.dim()
-        if dim not in (2, 3):
-            raise ValueError("logits must be [tokens, vocab] or [batch, seq, vocab]")
-        shape, st = logits.shape, logits.stride()
-        if st[-1] != 1 and shape[-1] != 1:
-            raise ValueError("logits: the innermost stride must be 1")
-        if logits.device.type != "cuda":
-            raise ValueError("logits must be on a CUDA device")
-        self.logits, self.device, self.shape = logits, logits.device, shape[:-1]
-        if dim == 2:
-            self.x = B.loss_logits(logits.data_ptr() or None, _DTYPES[logits.dtype], 1, shape[0], shape[1], 0, st[0],
-                                   temperature)
-        else:
-            self.x = B.loss_logits(logits.data_ptr() or None, _DTYPES[logits.dtype], shape[0], shape[1], shape[2],
-                                   st[0], st[1], temperature)
-        self.tokens = self.x.batch * self.x.seq
-        self._given = stream
 
-    def _strides(self, t):
-        st = t.stride()
-        return (0, st[0]) if len(self.shape) == 1 else (st[0], st[1])
+def _logits(logits, temperature):
+    """The packed logits, the tokens' shape, their device's index."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES:
+        raise ValueError("logits must be a float32 or bfloat16 tensor")
+    shape, st = logits.shape, logits.stride()
+    if len(shape) == 2:
+        batch, sb, ss = 1, 0, st[0]
+    elif len(shape) == 3:
+        batch, sb, ss = shape[0], st[0], st[1]
+    else:
+        raise ValueError("logits must be [tokens, vocab] or [batch, seq, vocab]")
+    if st[-1] != 1 and shape[-1] != 1:
+        raise ValueError("logits: the innermost stride must be 1")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    return (_LOGITS.pack(logits.data_ptr(), _DTYPES[logits.dtype], batch, shape[-2], shape[-1], sb, ss, temperature),
+            shape[:-1], logits.get_device())
 
-    def rows(self, name, t, dtype=torch.float32):
-        """A per-token argument, with any strides."""
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-            raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor")
-        if t.device != self.device or t.shape != self.shape:
-            raise ValueError(f"{name} must have shape {list(self.shape)} on the logits' device")
-        return B.loss_rows(t.data_ptr() or None, *self._strides(t))
 
-    def optional(self, name, t, dtype=torch.float32):
-        return _NO_ROWS if t is None else self.rows(name, t, dtype)
+def _strides(t, shape):
+    st = t.stride()
+    return (0, st[0]) if len(shape) == 1 else (st[0], st[1])
 
-    def targets(self, t, ignore_index):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _INDEX:
-            raise ValueError("targets must be an int32 or int64 tensor")
-        return B.loss_targets(self.rows("targets", t, t.dtype), _INDEX[t.dtype], ignore_index)
 
-    def grad(self, grad, need_grad, scale):
-        """(tensor or None, descriptor or None) of the gradient."""
-        if grad is None:
-            if not need_grad:
-                return None, None
-            grad = torch.empty(self.logits.shape, dtype=self.logits.dtype, device=self.device)
-        else:
-            if not need_grad:
-                raise ValueError("grad was given with need_grad=False")
-            if not isinstance(grad, torch.Tensor) or grad.dtype != self.logits.dtype:
-                raise ValueError("grad must have the logits' dtype")
-            if grad.device != self.device or grad.shape != self.logits.shape:
-                raise ValueError("grad must have the logits' shape and device")
-            if grad.stride(-1) != 1 and grad.shape[-1] != 1:
-                raise ValueError("grad: the innermost stride must be 1")
-        return grad, B.loss_grad(grad.data_ptr() or None, *self._strides(grad), scale)
+def _rows(name, t, shape, device, dtype=_FP32):
+    """A per-token argument, with any strides: (pointer, stride_b, stride_s)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype:
+        if t.shape == shape and t.get_device() == device:
+            st = t.stride()
+            return (t.data_ptr(), 0, st[0]) if len(st) == 1 else (t.data_ptr(), st[0], st[1])
+        raise ValueError(f"{name} must have shape {list(shape)} on the logits' device")
+    raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor")
 
-    def empty(self, *shape):
-        return torch.empty(shape, dtype=torch.float32, device=self.device)
 
-    def workspace(self, pairs=0):
-        n = B.loss_workspace_size(self.tokens, pairs)
-        return torch.empty(n, dtype=torch.uint8, device=self.device), n
+def _targets(t, shape, device, ignore_index):
+    code = _INDEX.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise ValueError("targets must be an int32 or int64 tensor")
+    return _TARGETS.pack(*_rows("targets", t, shape, device, t.dtype), code, ignore_index)
 
-    def __enter__(self):
-        """Makes the logits' device and the call's stream current: the library
-        launches on the current device, and outputs and workspace are allocated
-        for the stream that uses them."""
-        self._before = None
-        if self._given is not None:
-            self._before = torch.cuda.stream(self._given)
-        elif torch.cuda.current_device() != self.device.index:
-            self._before = torch.cuda.device(self.device)
-        if self._before is not None:
-            self._before.__enter__()
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream
-        return self
 
-    def __exit__(self, *exc):
-        if self._before is not None:
-            self._before.__exit__(*exc)
+def _gradient(logits, grad, need_grad, scale, device):
+    """(tensor or None, packed or None) of the gradient."""
+    if grad is None:
+        if not need_grad:
+            return None, None
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    else:
+        if not need_grad:
+            raise ValueError("grad was given with need_grad=False")
+        if not isinstance(grad, torch.Tensor) or grad.dtype != logits.dtype:
+            raise ValueError("grad must have the logits' dtype")
+        if grad.shape != logits.shape or grad.get_device() != device:
+            raise ValueError("grad must have the logits' shape and device")
+        if grad.stride(-1) != 1 and grad.shape[-1] != 1:
+            raise ValueError("grad: the innermost stride must be 1")
+    st = grad.stride()
+    return grad, _GRAD.pack(grad.data_ptr(), st[0] if len(st) == 3 else 0, st[-2], scale)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(tokens, pairs):
+    return B.loss_workspace_size(tokens, pairs)
+
+
+def _workspace(shape, device, pairs=0):
+    n = _workspace_bytes(shape.numel(), pairs)
+    return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
 def token_logprobs(logits, targets, *, temperature: float = 1.0, ignore_index: int = -100,
                    stream=None) -> TokenLogprobs:
     """Log-probability of each target under softmax(logits / temperature)."""
-    c = _Call(logits, temperature, stream)
-    y = c.targets(targets, ignore_index)
-    with c:
-        logp, stats = c.empty(*c.shape), c.empty(*c.shape, 2)
-        B.loss_token_logprobs(c.x, y, logp.data_ptr(), stats.data_ptr(), c.stream)
+    ctx = _context(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return token_logprobs(logits, targets, temperature=temperature, ignore_index=ignore_index)
+    x, shape, dev = _logits(logits, temperature)
+    y = _targets(targets, shape, dev, ignore_index)
+    device = logits.device
+    logp = torch.empty(shape, dtype=_FP32, device=device)
+    stats = torch.empty((*shape, 2), dtype=_FP32, device=device)
+    B.loss_token_logprobs(x, y, logp.data_ptr(), stats.data_ptr(), _raw_stream(dev))
     return TokenLogprobs(logp, stats)
 
 
@@ -161,15 +183,19 @@ def token_logprobs_backward(logits, targets, stats, grad_logp, *, temperature: f
     """Gradient of the logits, given that of the log-probabilities: the
     backward pass of token_logprobs under any loss.  ``stats`` is the forward
     pass's; targets, temperature and ignore_index are the same as there."""
-    c = _Call(logits, temperature, stream)
-    y = c.targets(targets, ignore_index)
-    if (not isinstance(stats, torch.Tensor) or stats.dtype != torch.float32 or stats.device != c.device
-            or stats.shape != (*c.shape, 2) or not stats.is_contiguous()):
-        raise ValueError(f"stats must be contiguous float32 {[*c.shape, 2]} on the logits' device")
-    d = c.rows("grad_logp", grad_logp)
-    with c:
-        out, g = c.grad(grad, True, grad_scale)
-        B.loss_token_logprobs_backward(c.x, y, stats.data_ptr(), d, g, c.stream)
+    ctx = _context(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return token_logprobs_backward(logits, targets, stats, grad_logp, temperature=temperature,
+                                           ignore_index=ignore_index, grad=grad, grad_scale=grad_scale)
+    x, shape, dev = _logits(logits, temperature)
+    y = _targets(targets, shape, dev, ignore_index)
+    if (not isinstance(stats, torch.Tensor) or stats.dtype != _FP32 or stats.get_device() != dev
+            or stats.shape != (*shape, 2) or not stats.is_contiguous()):
+        raise ValueError(f"stats must be contiguous float32 {[*shape, 2]} on the logits' device")
+    d = _ROWS.pack(*_rows("grad_logp", grad_logp, shape, dev))
+    out, g = _gradient(logits, grad, True, grad_scale, dev)
+    B.loss_token_logprobs_backward(x, y, stats.data_ptr(), d, g, _raw_stream(dev))
     return out
 
 
@@ -189,17 +215,27 @@ def policy_loss(logits, targets, advantages, old_logp=None, ref_logp=None, *, cl
     shape and any strides: ``advantages[:, None].expand(batch, seq)`` gives a
     sequence one advantage.
     """
-    c = _Call(logits, temperature, stream)
-    y = c.targets(targets, ignore_index)
-    args = B.loss_policy_args(c.rows("advantages", advantages), c.optional("old_logp", old_logp),
-                              c.optional("ref_logp", ref_logp), c.optional("weights", weights),
-                              clip_low, clip_high, kl_coef)
-    with c:
-        out, g = c.grad(grad, need_grad, grad_scale)
-        loss, logp, token = c.empty(), c.empty(*c.shape), c.empty(*c.shape)
-        ws, n = c.workspace()
-        B.loss_policy(c.x, y, args, g, loss.data_ptr(), logp.data_ptr() or None, token.data_ptr() or None,
-                      ws.data_ptr(), n, c.stream)
+    ctx = _context(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return policy_loss(logits, targets, advantages, old_logp, ref_logp, clip_low=clip_low, clip_high=clip_high,
+                               kl_coef=kl_coef, weights=weights, temperature=temperature, ignore_index=ignore_index,
+                               grad=grad, grad_scale=grad_scale, need_grad=need_grad)
+    x, shape, dev = _logits(logits, temperature)
+    y = _targets(targets, shape, dev, ignore_index)
+    args = _POLICY.pack(*_rows("advantages", advantages, shape, dev),
+                        *(_NO_ROWS if old_logp is None else _rows("old_logp", old_logp, shape, dev)),
+                        *(_NO_ROWS if ref_logp is None else _rows("ref_logp", ref_logp, shape, dev)),
+                        *(_NO_ROWS if weights is None else _rows("weights", weights, shape, dev)),
+                        clip_low, clip_high, kl_coef)
+    out, g = _gradient(logits, grad, need_grad, grad_scale, dev)
+    device = logits.device
+    loss = torch.empty((), dtype=_FP32, device=device)
+    logp = torch.empty(shape, dtype=_FP32, device=device)
+    token = torch.empty(shape, dtype=_FP32, device=device)
+    ws, n = _workspace(shape, device)
+    B.loss_policy(x, y, args, g, loss.data_ptr(), logp.data_ptr(), token.data_ptr(), ws.data_ptr(), n,
+                  _raw_stream(dev))
     return PolicyLoss(loss, out, logp, token)
 
 
@@ -220,33 +256,44 @@ def preference_loss(logits, targets, ref_logp=None, *, seq_offsets=None, beta: f
         "hinge"     max(0, 1 + margin - beta h)
         "squared"   (h - 1 / (2 beta) - margin)^2
     """
-    c = _Call(logits, temperature, stream)
-    y = c.targets(targets, ignore_index)
+    ctx = _context(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return preference_loss(logits, targets, ref_logp, seq_offsets=seq_offsets, beta=beta,
+                                   label_smoothing=label_smoothing, kind=kind, margin=margin, average=average,
+                                   temperature=temperature, ignore_index=ignore_index, grad=grad,
+                                   grad_scale=grad_scale, need_grad=need_grad)
+    x, shape, dev = _logits(logits, temperature)
+    y = _targets(targets, shape, dev, ignore_index)
     code = B.LOSS_PREFERENCE_KINDS.get(kind)
     if code is None:
         raise ValueError(f"unknown kind {kind!r}: one of {sorted(B.LOSS_PREFERENCE_KINDS)}")
     if seq_offsets is None:
-        if len(c.shape) != 2 or c.shape[0] < 2 or c.shape[0] % 2:
+        if len(shape) != 2 or shape[0] < 2 or shape[0] % 2:
             raise ValueError("without seq_offsets the logits must be [2 pairs, seq, vocab]")
-        pairs, at, odt = c.shape[0] // 2, None, B.LOSS_INT64
+        pairs, at, odt = shape[0] // 2, 0, B.LOSS_INT64
     else:
-        if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dtype not in _INDEX:
+        odt = _INDEX.get(seq_offsets.dtype) if isinstance(seq_offsets, torch.Tensor) else None
+        if odt is None:
             raise ValueError("seq_offsets must be an int32 or int64 tensor")
         n = seq_offsets.numel()
-        if (seq_offsets.dim() != 1 or n < 3 or n % 2 == 0 or seq_offsets.device != c.device
+        if (seq_offsets.dim() != 1 or n < 3 or n % 2 == 0 or seq_offsets.get_device() != dev
                 or not seq_offsets.is_contiguous()):
             raise ValueError("seq_offsets must be contiguous [2 pairs + 1] on the logits' device")
-        if len(c.shape) != 1:
+        if len(shape) != 1:
             raise ValueError("with seq_offsets the logits must be [tokens, vocab]")
-        pairs, at, odt = (n - 1) // 2, seq_offsets.data_ptr(), _INDEX[seq_offsets.dtype]
-    args = B.loss_preference_args(c.optional("ref_logp", ref_logp), pairs, at, odt, code, 1 if average else 0,
-                                  beta, label_smoothing, margin)
-    with c:
-        out, g = c.grad(grad, need_grad, grad_scale)
-        loss, pair, rewards, logp = c.empty(), c.empty(pairs), c.empty(2 * pairs), c.empty(*c.shape)
-        ws, n = c.workspace(pairs)
-        B.loss_preference(c.x, y, args, g, loss.data_ptr(), pair.data_ptr(), rewards.data_ptr(),
-                          logp.data_ptr() or None, ws.data_ptr(), n, c.stream)
+        pairs, at = (n - 1) // 2, seq_offsets.data_ptr()
+    args = _PREFERENCE.pack(*(_NO_ROWS if ref_logp is None else _rows("ref_logp", ref_logp, shape, dev)), pairs, at,
+                            odt, code, 1 if average else 0, beta, label_smoothing, margin)
+    out, g = _gradient(logits, grad, need_grad, grad_scale, dev)
+    device = logits.device
+    loss = torch.empty((), dtype=_FP32, device=device)
+    pair = torch.empty(pairs, dtype=_FP32, device=device)
+    rewards = torch.empty(2 * pairs, dtype=_FP32, device=device)
+    logp = torch.empty(shape, dtype=_FP32, device=device)
+    ws, n = _workspace(shape, device, pairs)
+    B.loss_preference(x, y, args, g, loss.data_ptr(), pair.data_ptr(), rewards.data_ptr(), logp.data_ptr(),
+                      ws.data_ptr(), n, _raw_stream(dev))
     return PreferenceLoss(loss, out, pair, rewards, logp)
 
 
@@ -264,30 +311,33 @@ def distill_loss(logits, teacher_ids, teacher_logits, teacher_lse=None, *, mask=
     ``mask`` (bool) leaves tokens out; the loss is the mean over the others, or
     sum(weights * l).
     """
-    c = _Call(logits, temperature, stream)
+    ctx = _context(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return distill_loss(logits, teacher_ids, teacher_logits, teacher_lse, mask=mask, weights=weights,
+                                temperature=temperature, grad=grad, grad_scale=grad_scale, need_grad=need_grad)
+    x, shape, dev = _logits(logits, temperature)
     for name, t, types in (("teacher_ids", teacher_ids, _INDEX), ("teacher_logits", teacher_logits, _DTYPES)):
         if not isinstance(t, torch.Tensor) or t.dtype not in types:
             raise ValueError(f"{name} must be a tensor of {' or '.join(str(d)[6:] for d in types)}")
-        if t.device != c.device or t.dim() != len(c.shape) + 1 or t.shape[:-1] != c.shape:
-            raise ValueError(f"{name} must have shape {[*c.shape, 'k']} on the logits' device")
+        if t.shape[:-1] != shape or t.get_device() != dev or t.dim() == len(shape):
+            raise ValueError(f"{name} must have shape {[*shape, 'k']} on the logits' device")
         if t.stride(-1) != 1 and t.shape[-1] != 1:
             raise ValueError(f"{name}: the innermost stride must be 1")
     k = teacher_ids.shape[-1]
     if teacher_logits.shape[-1] != k:
         raise ValueError("teacher_ids and teacher_logits must have the same shape")
-    if mask is not None and isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
-        mask = mask.view(torch.uint8)
-    elif mask is not None:
-        raise ValueError("mask must be a bool tensor")
-    args = B.loss_distill_args(teacher_ids.data_ptr() or None, _INDEX[teacher_ids.dtype], *c._strides(teacher_ids),
-                               teacher_logits.data_ptr() or None, _DTYPES[teacher_logits.dtype],
-                               *c._strides(teacher_logits), k, c.optional("teacher_lse", teacher_lse),
-                               c.optional("mask", mask, torch.uint8), c.optional("weights", weights))
-    with c:
-        out, g = c.grad(grad, need_grad, grad_scale)
-        loss, token = c.empty(), c.empty(*c.shape)
-        ws, n = c.workspace()
-        B.loss_distill(c.x, args, g, loss.data_ptr(), token.data_ptr() or None, ws.data_ptr(), n, c.stream)
+    args = _DISTILL.pack(teacher_ids.data_ptr(), _INDEX[teacher_ids.dtype], *_strides(teacher_ids, shape),
+                         teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], *_strides(teacher_logits, shape), k,
+                         *(_NO_ROWS if teacher_lse is None else _rows("teacher_lse", teacher_lse, shape, dev)),
+                         *(_NO_ROWS if mask is None else _rows("mask", mask, shape, dev, torch.bool)),
+                         *(_NO_ROWS if weights is None else _rows("weights", weights, shape, dev)))
+    out, g = _gradient(logits, grad, need_grad, grad_scale, dev)
+    device = logits.device
+    loss = torch.empty((), dtype=_FP32, device=device)
+    token = torch.empty(shape, dtype=_FP32, device=device)
+    ws, n = _workspace(shape, device)
+    B.loss_distill(x, args, g, loss.data_ptr(), token.data_ptr(), ws.data_ptr(), n, _raw_stream(dev))
     return DistillLoss(loss, out, token)
 
 
