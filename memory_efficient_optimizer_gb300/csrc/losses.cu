@@ -20,6 +20,7 @@
 #include <map>
 #include <mutex>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "adafactor_internal.h"
@@ -27,13 +28,13 @@
 
 namespace {
 
-// CTAs of k_loss_row on an SM, by their threads that sum.
-__host__ __device__ constexpr int row_ctas(int threads, bool lists) { return threads >= 512 ? 1 : threads >= 128 ? 4 : lists ? 10 : 20; }
+constexpr int kMaxWarps = 16;      // of a CTA of k_loss_row that sum
 constexpr int kGradThreads = 256;
 constexpr int kPairThreads = 256;
 constexpr int kCountThreads = 1024;
 constexpr int kGradVecs = 8;       // vectors of a thread of k_loss_grad
 constexpr int kMaxCluster = 8;
+constexpr int kKeep = 4;           // chunks of a row that a warp keeps
 constexpr int kNoValue = -(1 << 30);  // a target that no value of a row is
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int64_t kMaxVocab = int64_t{1} << 21;
@@ -95,7 +96,7 @@ struct LossArgs {
   Sum* part;                      // [clusters]: sum of w l, or of l
   unsigned* ticket;
   int32_t vecs_per_cta;           // k_loss_row, k_loss_forward: vectors of a row for a CTA
-  int32_t batches, slots;         // k_loss_row: batches of a thread; places of the ring for them
+  int32_t slots;                  // k_loss_row: places of a warp in the ring
   int32_t tiles;                  // k_loss_grad: CTAs of a row
   // policy
   Rows adv, old, ref, weights;
@@ -172,7 +173,8 @@ struct Ref {
 // value) are read and replaced by -inf; of the last only the row's are read.
 template <typename T> constexpr int kN = 16 / static_cast<int>(sizeof(T));
 template <typename T> constexpr uint32_t kNegInf = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-constexpr int kBatch = 4;           // vectors in registers at a time
+constexpr int kBatch = 4;           // vectors of a lane in a warp's chunk of a row
+constexpr int kForwardBatch = 4;    // vectors in flight in k_loss_forward, twice
 
 template <typename T>
 struct Row {
@@ -312,14 +314,14 @@ template <typename T, bool LISTED>
 struct Part {
   float m = -INFINITY, s = 0.f, top = 0.f;
   template <bool FAR, int N>
-  __device__ __forceinline__ void sum(const uint4 (&w)[N], const Ref& ref, float c, uint32_t on) {
+  __device__ __forceinline__ void sum(const uint4 (&w)[N], const Ref& ref, float c, uint64_t on) {
     if (LISTED && on != 0) {
 #pragma unroll
       for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int j = 0; j < kN<T> / 2; ++j) {
           const float2 e = terms<FAR>(pair_at<T>(w[k], j), ref, c);
-          const uint32_t at = on >> (8 * k + 2 * j);
+          const uint32_t at = static_cast<uint32_t>(on >> (8 * k + 2 * j));
           s += (at & 1 ? 0.f : e.x) + (at & 2 ? 0.f : e.y);
           top += (at & 1 ? e.x : 0.f) + (at & 2 ? e.y : 0.f);
         }
@@ -338,7 +340,7 @@ struct Part {
     s += (acc.x + acc.y) + (acc2.x + acc2.y);
   }
   template <int N>
-  __device__ __forceinline__ void add(const uint4 (&w)[N], float c, uint32_t on = 0) {
+  __device__ __forceinline__ void add(const uint4 (&w)[N], float c, uint64_t on = 0) {
     const float m2 = batch_max<T, N>(w);
     if (m2 > m) {
       const float f = Ref(m2, c).factor(m, c);
@@ -614,13 +616,28 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 __device__ __forceinline__ void bar_arrive(int id, int threads) {
   asm volatile("barrier.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
+}
+// 16 bytes to the same place in another CTA of the cluster, counted by its
+// barrier there.  Unlike the cluster's own barrier this waits for no store to
+// global memory before it.
+__device__ __forceinline__ void send(const float4* mine, uint32_t rank, float4 v, uint64_t* bar) {
+  uint32_t to, there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(shared_at(mine)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(shared_at(bar)), "r"(rank));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(there)
+               : "memory");
+}
 enum Barrier : int { kBarRow = 1, kBarListFull = 2, kBarListFree = 4 };  // the list's are two each
 
 constexpr int kChunk = 32 * kBatch;  // vectors of a warp's batch: consecutive ones, lane by lane
 
 // A teacher's list, made by a warp of its own one row ahead (two buffers).
+using Bits = std::conditional<kBatch == 8, uint64_t, uint32_t>::type;
 struct List {
-  uint32_t* bits;  // [batches][threads]: a byte a vector of the batch, a bit a value
+  Bits* bits;      // [chunks of a warp][threads]: a byte a vector of the lane's, a bit a value
   int32_t* id;     // [top_k]
   float* p;        // [top_k]: the teacher's probabilities
   float* x;        // [top_k]: the logits (all in rank 0, the CTA's own elsewhere)
@@ -632,7 +649,7 @@ __host__ __device__ constexpr int list_bytes(int slice, int top_k) {
 __device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) {
   List l;
   const int kpad = (top_k + 3) / 4 * 4;
-  l.bits = reinterpret_cast<uint32_t*>(p);
+  l.bits = reinterpret_cast<Bits*>(p);
   l.id = reinterpret_cast<int32_t*>(p + (slice + 15) / 16 * 16);
   l.p = reinterpret_cast<float*>(l.id + kpad);
   l.x = l.p + kpad;
@@ -640,7 +657,7 @@ __device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) 
   return l;
 }
 
-template <typename T, int NT>
+template <typename T>
 __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, const Row<T>& r, int b, int s, int v0, int v1,
                                           int slice, bool all) {
   const int lane = threadIdx.x & 31;
@@ -664,8 +681,10 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
       const bool mine = at >= 0 && at < v1 - v0;
       if (mine || all) x = widen(*r.value(static_cast<int>(i)));
       if (mine) {
-        const uint32_t bit = 1u << (at % kChunk / 32 * 8 + e % kN<T>);
-        if (atomicOr(l.bits + at / (NT * kBatch) * NT + at / kChunk * 32 % NT + at % 32, bit) & bit) wrong = 1;
+        const int k = at % kChunk / 32;
+        const uint32_t bit = 1u << (k % 4 * 8 + e % kN<T>);
+        uint32_t* const word = reinterpret_cast<uint32_t*>(l.bits + at / kChunk * 32 + at % 32) + k / 4;
+        if (atomicOr(word, bit) & bit) wrong = 1;
       }
     }
     l.id[k] = static_cast<int>(i);
@@ -709,24 +728,37 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
 // their terms, and, when the cluster's parts of the row are together, makes the
 // gradient from the same copies; the places that come free take the next row's
 // chunks at once.  LONG: rows that no cluster keeps are read twice.
-template <typename T, int OP, int NT, bool LONG>
-__global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, OP == kDistill))
-    k_loss_row(const __grid_constant__ LossArgs a) {
+template <typename T, int OP, bool LONG>
+__global__ void __launch_bounds__(kMaxWarps * 32 + (OP == kDistill ? 32 : 0), 1) k_loss_row(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
+  __shared__ uint64_t together[2];
   constexpr bool kLists = OP == kDistill;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int warps = NT / 32;  // that sum
+  const int warps = (blockDim.x >> 5) - (kLists ? 1 : 0), NT = 32 * warps;  // that sum
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int first = static_cast<int>(blockIdx.x) / ranks, stride = static_cast<int>(gridDim.x) / ranks;
-  const int v0 = rank * a.vecs_per_cta, slots = a.slots, batches = a.batches;
+  const int v0 = rank * a.vecs_per_cta, slots = a.slots;
   uint4* const ring = reinterpret_cast<uint4*>(shared) + (LONG ? 0 : warp * slots * kChunk);  // a warp's [slots][kChunk]
-  float4* const parts = reinterpret_cast<float4*>(shared) + (LONG ? 0 : slots * kBatch * NT);  // [2][warps of the cluster]
+  float4* const parts = reinterpret_cast<float4*>(shared) + (LONG ? 0 : warps * slots * kChunk);  // [2][warps of the cluster]
   uint64_t* const full = reinterpret_cast<uint64_t*>(parts + 2 * warps * ranks) + warp * slots;  // a warp's [slots]
   unsigned char* const lists = reinterpret_cast<unsigned char*>(parts + 2 * warps * ranks) + (LONG ? 0 : (warps * slots * 8 + 15) / 16 * 16);
-  const int slice = batches * kBatch * NT, list_size = list_bytes(slice, a.top_k);
+  const int slice = a.vecs_per_cta, list_size = list_bytes(slice, a.top_k);
 
-  if (ranks > 1) {  // shared memory of the others may be written once they have all begun
-    cluster_arrive();
+  // A barrier for the parts of each of the two rows; warp 0 expects the next
+  // but one row's as soon as a row's are there, before it sends its own of the
+  // next row: nobody can be further than that.
+  
+  const uint32_t row_bytes = 16 * warps * ranks;
+  if (ranks > 1) {
+    if (tid == 0) {
+      for (int k = 0; k < 2; ++k) {
+        init_barrier(together + k);
+        expect_bytes(together + k, row_bytes);
+      }
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    cluster_arrive();  // shared memory of the others may be written once they have all begun
     cluster_wait();
   }
   struct Place {
@@ -747,25 +779,23 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
   const Place begin{first, first / a.seq, first % a.seq};
 
   if (kLists && warp == warps) {
-    // The warp that makes the lists.  It arrives at the cluster's barrier of a
-    // row early and makes the next list before it waits there.
+    // The warp that makes the lists, up to two rows ahead.
     int q = 0;
     for (Place t = begin; t.row < a.tokens; t = after(t)) {
       if (!counted(a, OP, t.b, t.s)) continue;
       const Row<T> r = row_at(t);
       if (q >= 2) bar_sync(kBarListFree + (q & 1), NT + 32);
-      make_list<T, NT>(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, t.b, t.s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice,
+      make_list(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, t.b, t.s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice,
                 rank == 0);
       __syncwarp();
       bar_arrive(kBarListFull + (q & 1), NT + 32);
-      if (ranks > 1) {
-        if (q > 0) cluster_wait();
-        cluster_arrive();
-      }
       ++q;
     }
-    if (ranks > 1 && q > 0) cluster_wait();
     for (int k = max(0, q - 2); k < q; ++k) bar_sync(kBarListFree + (k & 1), NT + 32);
+    if (ranks > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
     return;
   }
 
@@ -807,15 +837,14 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
 
   Place at{begin};
   int64_t target = target_at(at), target1 = target_at(after(at));
-  // The ring's place of the row's chunk 0, the parity of its barrier, the
-  // row's chunks and those of the next.
-  int base = 0, n_chunks = 0, n_chunks1 = 0;
+  const bool gradient = a.g != nullptr;
+  Row<T> r = row_at(at);
+  // The row's chunks, the ring's place of its first and the parity of that
+  // one's barrier.
+  int n_chunks = target != kIgnored ? chunks(min(r.vecs, v0 + a.vecs_per_cta)) : 0, base = 0;
   uint32_t parity = 0;
   bool dead = false;  // a wait ran out: no more waiting, the loss is NaN
-  if (!LONG && target != kIgnored) {
-    const Row<T> r = row_at(at);
-    copy(r, 0, chunks(min(r.vecs, v0 + a.vecs_per_cta)));
-  }
+  if (!LONG) copy(r, 0, n_chunks);
   Sum share;           // of the cluster's rows in the loss (rank 0, warp 0)
   float by_count = 0.f;
   bool waited = false;
@@ -825,18 +854,17 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
     const bool live = target != kIgnored, live1 = target1 != kIgnored;
     const Place next = after(at);
     const int row = at.row, b = at.b, s = at.s;
-    const Row<T> r = row_at(at), r1 = row_at(live1 ? next : at);
-    const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
+    const Row<T> r1 = live1 ? row_at(next) : r;
+    const GradRow<T> g(!gradient ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
     const int64_t target2 = target_at(after(next));
-    n_chunks = live ? chunks(min(r.vecs, v0 + a.vecs_per_cta)) : 0;
-    n_chunks1 = live1 ? chunks(min(r1.vecs, v0 + a.vecs_per_cta)) : 0;
+    const int n_chunks1 = live1 ? chunks(min(r1.vecs, v0 + a.vecs_per_cta)) : 0;
     const int early1 = min(n_chunks1, slots - n_chunks);  // what there is room for before this row's places come free
     if (!LONG) {
       __syncwarp();  // the row before has been read
       copy(r1, 0, early1);
     }
     if (!live) {
-      if (a.g != nullptr) g.zero(rank, ranks, NT);
+      if (gradient) g.zero(rank, ranks, NT);
       if (rank == 0 && tid == 0) {
         if (a.logp != nullptr) a.logp[row] = 0.f;
         if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
@@ -864,7 +892,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
         y = static_cast<int>(target);
         y_vec = (y + r.lead) / kN<T>;
         const int v = y_vec - v0;
-        has = y_vec >= v0 && y_vec < v1 && v / kChunk * 32 % NT + v % 32 == tid;
+        has = y_vec >= v0 && y_vec < v1 && v / kChunk % warps == warp && v % 32 == lane;
         if (has) x_at = widen(*r.value(y));
       }
 
@@ -881,7 +909,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
           place = 0;
           phase ^= 1;
         }
-        const uint32_t bits = kLists ? list.bits[q2 * NT + tid] : 0;
+        const Bits bits = kLists ? list.bits[(q2 * warps + warp) * 32 + lane] : 0;
         if (batch_in<32>(i - lane, lo, hi)) {
           uint4 w[kBatch];
 #pragma unroll
@@ -914,20 +942,22 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
       p.w = kLists && warp == 0 ? list.head[2] : 0.f;
       float4* const here = parts + (q & 1) * warps * ranks;
       if (ranks > 1) {
-        if (lane < ranks) store_remote(here + rank * warps + warp, lane, p);
+        if (lane < ranks) send(here + rank * warps + warp, lane, p, together + (q & 1));
+        if (!dead && !wait_phase(together + (q & 1), q >> 1 & 1)) dead = true;
         __syncwarp();
-        cluster_arrive();
-        cluster_wait();
+        if (tid == 0) expect_bytes(together + (q & 1), row_bytes);
       } else {
         if (lane == 0) here[warp] = p;
         bar_sync(kBarRow, NT);
       }
       const int all = warps * ranks;
-      float m = -INFINITY;
-      for (int k = lane; k < all; k += 32) m = fmaxf(m, here[k].x);
+      const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f), mine0 = lane < all ? here[lane] : none;
+      float m = mine0.x;
+      for (int k = lane + 32; k < all; k += 32) m = fmaxf(m, here[k].x);
       const Ref ref(warp_max(m), a.c);
-      float sum = 0.f, z = 0.f, wrong = 0.f;
-      for (int k = lane; k < all; k += 32) {
+      const float f0 = ref.factor(mine0.x, a.c);
+      float sum = mine0.y * f0, z = kLists ? mine0.z * f0 : mine0.z, wrong = mine0.w;
+      for (int k = lane + 32; k < all; k += 32) {
         const float4 o = here[k];
         const float fo = ref.factor(o.x, a.c);
         sum += o.y * fo;
@@ -956,7 +986,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
           share.add(a.weights.p != nullptr ? w * t.loss : t.loss);
         }
         more = w * a.gscale * a.inv_t * t.d;
-        scale = -more / sum;
+        scale = __fdividef(-more, sum);
       } else {
         const float sum_p = list.head[0], rest = list.head[1], off = sum;
         sum += z;
@@ -980,7 +1010,7 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
       }
 
       // The gradient, and the next row's vectors into the places that come free.
-      if (a.g != nullptr) {
+      if (gradient) {
         const bool near = g.shift == 0 && !ref.far();
         place = base;
         for (int q2 = 0; q2 < n_chunks; ++q2) {
@@ -1029,6 +1059,8 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
       base -= slots;
       parity ^= 1;
     }
+    n_chunks = n_chunks1;
+    r = live1 || next.row >= a.tokens ? r1 : row_at(next);
     target = target1;
     target1 = target2;
   }
@@ -1036,6 +1068,11 @@ __global__ void __launch_bounds__(NT + (OP == kDistill ? 32 : 0), row_ctas(NT, O
     share.s = NAN;
     // copies still in flight land before the CTA's memory is given up
     for (int k = 0; k < slots; ++k) wait_phase(full + k, k < base ? parity : parity ^ 1);
+  }
+
+  if (ranks > 1) {  // nobody leaves while others may write here
+    cluster_arrive();
+    cluster_wait();
   }
 
   // The clusters' shares: the last to come sums them all, in order.
@@ -1095,13 +1132,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_loss_forward(const __grid_con
   const bool inside = target >= 0 && target < a.vocab;
   const float x_at = writes && inside ? widen(*r.value(static_cast<int>(target))) : NAN;
   Part<T, false> part;
-  uint4 w[kBatch], w1[kBatch];
+  uint4 w[kForwardBatch], w1[kForwardBatch];
   load_batch<T, NT>(w, r, v0 + tid, v1);
-  for (int i = v0 + tid; i - lane < v1; i += kBatch * NT) {
-    load_batch<T, NT>(w1, r, i + kBatch * NT, v1);
+  for (int i = v0 + tid; i - lane < v1; i += kForwardBatch * NT) {
+    load_batch<T, NT>(w1, r, i + kForwardBatch * NT, v1);
     part.add(w, a.c);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) w[k] = w1[k];
+    for (int k = 0; k < kForwardBatch; ++k) w[k] = w1[k];
   }
   float4 p;
   p.x = warp_max(part.m);
@@ -1467,36 +1504,37 @@ int row_vecs(const LossArgs& a, int32_t dtype) {
   return div_up(a.vocab + (even ? 0 : per - 1), per);
 }
 
-// How a row is cut: CTAs, threads of each that sum, vectors of a CTA, batches
-// of a thread, places of the ring (0: the row is read twice).
+// How a row is cut: CTAs, warps of each that sum, vectors of a CTA, places of
+// a warp in the ring (0: the row is read twice).
 struct Cut {
-  int cluster, threads, vecs_per_cta, batches, slots, shared;
+  int cluster, warps, vecs_per_cta, slots, shared;
 };
 constexpr int kSharedBytes = 227 << 10;  // of an SM; a CTA takes 1 KB more than it asks for
-constexpr int kKeep = 4;                 // batches of a row that a thread keeps
 
 Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
+  const int chunks = div_up(vecs, kChunk);
   Cut c;
+  // `keep`: chunks of a row for a warp
   auto set = [&](int cluster, int keep) {
+    const int mine = div_up(chunks, cluster);
     c.cluster = cluster;
-    c.vecs_per_cta = div_up(div_up(vecs, cluster), kChunk) * kChunk;
-    c.threads = c.vecs_per_cta <= kChunk * keep ? 32 : c.vecs_per_cta <= 4 * kChunk * keep ? 128 : 512;
-    c.batches = div_up(c.vecs_per_cta, c.threads * kBatch);
-    c.shared = 2 * c.threads / 32 * cluster * static_cast<int>(sizeof(float4)) +
-               (lists ? 2 * list_bytes(c.batches * kBatch * c.threads, top_k) : 0);
-    const int batch = c.threads * kBatch * 16 + c.threads / 32 * 8;  // places and their barriers
-    for (int ctas = row_ctas(c.threads, lists); ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs
+    c.vecs_per_cta = mine * kChunk;
+    c.warps = std::min(kMaxWarps, div_up(mine, keep));
+    const int n = div_up(mine, c.warps);
+    c.shared = 2 * c.warps * cluster * static_cast<int>(sizeof(float4)) + (lists ? 2 * list_bytes(c.vecs_per_cta, top_k) : 0);
+    const int place = kChunk * 16 + 8;  // and its barrier
+    for (int ctas = kMaxWarps / c.warps; ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs of an SM
       const int room = kSharedBytes / ctas - 1024 - 64 - c.shared;
-      c.slots = std::min(2 * c.batches, std::max(0, room / batch));
-      if (c.slots > c.batches) break;
+      c.slots = std::min(2 * n, std::max(0, room / (c.warps * place)));
+      if (c.slots > n) break;
     }
-    if (c.slots < c.batches) c.slots = 0;  // with 512 threads only: fewer have places enough
-    c.shared += c.slots * c.threads * kBatch * 16 + div_up(c.slots * c.threads / 32 * 8, 16) * 16;
+    if (c.slots < n) c.slots = 0;
+    c.shared += c.warps * c.slots * kChunk * 16 + div_up(c.warps * c.slots * 8, 16) * 16;
   };
   int cluster = 1;
   set(1, kKeep);
-  while (cluster < kMaxCluster && c.batches > kKeep) set(cluster *= 2, kKeep);
-  while (cluster < kMaxCluster && tokens * cluster < sms && c.vecs_per_cta > 256) set(cluster *= 2, 1);
+  while (cluster < kMaxCluster && c.vecs_per_cta > kMaxWarps * kKeep * kChunk) set(cluster *= 2, kKeep);
+  while (cluster < kMaxCluster && tokens * cluster < sms && c.vecs_per_cta > kChunk) set(cluster *= 2, 1);
   return c;
 }
 
@@ -1518,16 +1556,13 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   sms = dev.sms;
   const Cut cut = cut_row(a.tokens, row_vecs(a, dtype), OP == kDistill, a.top_k, sms);
   const bool bf16 = dtype == ADAF_BFLOAT16, twice_read = cut.slots == 0;
-  void (*kernel)(LossArgs);
-  if (twice_read) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 512, true> : k_loss_row<float, OP, 512, true>;
-  else if (cut.threads == 512) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 512, false> : k_loss_row<float, OP, 512, false>;
-  else if (cut.threads == 128) kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 128, false> : k_loss_row<float, OP, 128, false>;
-  else kernel = bf16 ? k_loss_row<__nv_bfloat16, OP, 32, false> : k_loss_row<float, OP, 32, false>;
-  const int threads = cut.threads + (OP == kDistill ? 32 : 0);
+  void (*const kernel)(LossArgs) = twice_read ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
+                                              : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
+  const int threads = 32 * (cut.warps + (OP == kDistill ? 1 : 0));
   int& most = dev.clusters[{reinterpret_cast<const void*>(kernel),
-                            (static_cast<int64_t>(cut.shared) << 16) + (cut.threads << 4) + cut.cluster}];
+                            (static_cast<int64_t>(cut.shared) << 16) + (cut.warps << 4) + cut.cluster}];
   if (most == 0) {
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 << 10)) != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - 1024)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute");
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
@@ -1548,7 +1583,6 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   const int64_t clusters = std::min<int64_t>(a.tokens, most);
   lock.unlock();
   a.vecs_per_cta = cut.vecs_per_cta;
-  a.batches = cut.batches;
   a.slots = cut.slots;
   return launch(kSlotRow, kernel, clusters * cut.cluster, threads, cut.shared, cut.cluster, true, s, a);
 }
@@ -1557,7 +1591,7 @@ adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
   int64_t cluster = 1;
   while (cluster < kMaxCluster && a.tokens * cluster < 304 && div_up(vecs, static_cast<int>(cluster)) > 512) cluster *= 2;
   a.vecs_per_cta = div_up(vecs, static_cast<int>(cluster));
-  const int threads = a.vecs_per_cta <= 32 * kBatch * 2 ? 32 : a.vecs_per_cta <= 128 * kBatch * 2 ? 128 : 512;
+  const int threads = a.vecs_per_cta <= 32 * kForwardBatch * 2 ? 32 : a.vecs_per_cta <= 128 * kForwardBatch * 2 ? 128 : 512;
   const int shared = threads / 32 * static_cast<int>(cluster * sizeof(float4));
   const bool bf16 = dtype == ADAF_BFLOAT16;
   void (*const kernel)(LossArgs) =
