@@ -20,7 +20,6 @@
 #include <map>
 #include <mutex>
 #include <string>
-#include <type_traits>
 #include <vector>
 
 #include "adafactor_internal.h"
@@ -28,7 +27,7 @@
 
 namespace {
 
-constexpr int kMaxWarps = 16;      // of a CTA of k_loss_row that sum
+constexpr int kMaxWarps = 8;       // of a CTA of k_loss_row that sum
 constexpr int kGradThreads = 256;
 constexpr int kPairThreads = 256;
 constexpr int kCountThreads = 1024;
@@ -97,6 +96,7 @@ struct LossArgs {
   unsigned* ticket;
   int32_t vecs_per_cta;           // k_loss_row, k_loss_forward: vectors of a row for a CTA
   int32_t slots;                  // k_loss_row: places of a warp in the ring
+  int32_t stall;                  // k_loss_row: make no copies (a test)
   int32_t tiles;                  // k_loss_grad: CTAs of a row
   // policy
   Rows adv, old, ref, weights;
@@ -307,27 +307,12 @@ __device__ __forceinline__ float batch_max(const uint4 (&w)[N]) {
   return m;
 }
 
-// A thread's part of a row: the largest value and the sum of the terms; with
-// LISTED (`on`: a byte a vector, a bit a value) the listed words' terms apart,
-// so that a small rest is a sum of its own and keeps its precision.
-template <typename T, bool LISTED>
+// A thread's part of a row: the largest value and the sum of the terms.
+template <typename T>
 struct Part {
-  float m = -INFINITY, s = 0.f, top = 0.f;
+  float m = -INFINITY, s = 0.f;
   template <bool FAR, int N>
-  __device__ __forceinline__ void sum(const uint4 (&w)[N], const Ref& ref, float c, uint64_t on) {
-    if (LISTED && on != 0) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-#pragma unroll
-        for (int j = 0; j < kN<T> / 2; ++j) {
-          const float2 e = terms<FAR>(pair_at<T>(w[k], j), ref, c);
-          const uint32_t at = static_cast<uint32_t>(on >> (8 * k + 2 * j));
-          s += (at & 1 ? 0.f : e.x) + (at & 2 ? 0.f : e.y);
-          top += (at & 1 ? e.x : 0.f) + (at & 2 ? e.y : 0.f);
-        }
-      }
-      return;
-    }
+  __device__ __forceinline__ void sum(const uint4 (&w)[N], const Ref& ref, float c) {
     float2 acc = make_float2(0.f, 0.f), acc2 = acc;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -340,17 +325,15 @@ struct Part {
     s += (acc.x + acc.y) + (acc2.x + acc2.y);
   }
   template <int N>
-  __device__ __forceinline__ void add(const uint4 (&w)[N], float c, uint64_t on = 0) {
+  __device__ __forceinline__ void add(const uint4 (&w)[N], float c) {
     const float m2 = batch_max<T, N>(w);
     if (m2 > m) {
-      const float f = Ref(m2, c).factor(m, c);
-      s *= f;
-      top *= f;
+      s *= Ref(m2, c).factor(m, c);
       m = m2;
     }
     const Ref ref(m, c);
-    if (ref.far()) sum<true>(w, ref, c, on);
-    else sum<false>(w, ref, c, on);
+    if (ref.far()) sum<true>(w, ref, c);
+    else sum<false>(w, ref, c);
   }
 };
 
@@ -584,12 +567,18 @@ __device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, con
 // Bulk copies to a warp's own places of the ring, each with a barrier that
 // completes when its bytes are there.
 __device__ __forceinline__ uint32_t shared_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void init_barrier(uint64_t* bar) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_at(bar)) : "memory");
+__device__ __forceinline__ void init_barrier(uint64_t* bar, int arrivals) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(arrivals) : "memory");
 }
-__device__ __forceinline__ void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar) {
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_at(bar)) : "memory");
+}
+// Before copies to places that threads have written to.
+__device__ __forceinline__ void writes_before_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// `stall`: the copy is expected and not made (a test of the waits).
+__device__ __forceinline__ void copy_bulk(void* to, const void* from, uint32_t bytes, uint64_t* bar, bool stall) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
-  if (bytes != 0)
+  if (bytes != 0 && !stall)
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(shared_at(to)),
                  "l"(from), "r"(bytes), "r"(shared_at(bar))
                  : "memory");
@@ -602,19 +591,15 @@ __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
-// Waits for a phase; false after meo::kWaitCycles.
+// Waits for a phase; false, in the whole warp, after meo::kWaitCycles.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
-  if (phase_done(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!phase_done(bar, parity))
-    if (clock64() - t0 > meo::kWaitCycles) return false;
-  return true;
-}
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("barrier.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(int id, int threads) {
-  asm volatile("barrier.arrive.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
+  bool ok = phase_done(bar, parity);
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!(ok = phase_done(bar, parity)))
+      if (clock64() - t0 > meo::kWaitCycles) break;
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
@@ -630,18 +615,17 @@ __device__ __forceinline__ void send(const float4* mine, uint32_t rank, float4 v
                "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(there)
                : "memory");
 }
-enum Barrier : int { kBarRow = 1, kBarListFull = 2, kBarListFree = 4 };  // the list's are two each
-
 constexpr int kChunk = 32 * kBatch;  // vectors of a warp's batch: consecutive ones, lane by lane
 
 // A teacher's list, made by a warp of its own one row ahead (two buffers).
-using Bits = std::conditional<kBatch == 8, uint64_t, uint32_t>::type;
+using Bits = uint32_t;
+static_assert(sizeof(Bits) == kBatch, "a byte for each vector of a lane: list_bytes() counts on it");
 struct List {
   Bits* bits;      // [chunks of a warp][threads]: a byte a vector of the lane's, a bit a value
   int32_t* id;     // [top_k]
   float* p;        // [top_k]: the teacher's probabilities
-  float* x;        // [top_k]: the logits (all in rank 0, the CTA's own elsewhere)
-  float* head;     // sum p, rest, NaN where the list is bad (else 0)
+  float* x;        // [top_k]: the logits
+  float* head;     // sum p, rest, NaN where the list is bad (else 0), the largest of x
 };
 __host__ __device__ constexpr int list_bytes(int slice, int top_k) {
   return (slice + 15) / 16 * 16 + 12 * ((top_k + 3) / 4 * 4) + 16;
@@ -659,11 +643,11 @@ __device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) 
 
 template <typename T>
 __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, const Row<T>& r, int b, int s, int v0, int v1,
-                                          int slice, bool all) {
+                                          int slice) {
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < slice / kBatch; i += 32) l.bits[i] = 0;
   __syncwarp();
-  float top = -INFINITY;
+  float top = -INFINITY, most = -INFINITY;
   int entries = 0, wrong = 0;
   for (int k = lane; k < a.top_k; k += 32) {
     int64_t i = load_index(a.ids, a.idt, b * a.isb + s * a.iss + k);
@@ -679,12 +663,11 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
       ++entries;
       const int e = static_cast<int>(i) + r.lead, at = e / kN<T> - v0;
       const bool mine = at >= 0 && at < v1 - v0;
-      if (mine || all) x = widen(*r.value(static_cast<int>(i)));
+      x = widen(*r.value(static_cast<int>(i)));
+      most = fmaxf(most, x);
       if (mine) {
-        const int k = at % kChunk / 32;
-        const uint32_t bit = 1u << (k % 4 * 8 + e % kN<T>);
-        uint32_t* const word = reinterpret_cast<uint32_t*>(l.bits + at / kChunk * 32 + at % 32) + k / 4;
-        if (atomicOr(word, bit) & bit) wrong = 1;
+        const uint32_t bit = 1u << (at % kChunk / 32 * 8 + e % kN<T>);
+        if (atomicOr(l.bits + at / kChunk * 32 + at % 32, bit) & bit) wrong = 1;
       }
     }
     l.id[k] = static_cast<int>(i);
@@ -693,6 +676,7 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
     top = fmaxf(top, v);
   }
   top = warp_max(top);
+  most = warp_max(most);
   entries = __reduce_add_sync(0xffffffffu, entries);
   const bool bad = __any_sync(0xffffffffu, wrong);
   const float lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
@@ -719,22 +703,110 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
     l.head[0] = sum_p;
     l.head[1] = rest;
     l.head[2] = bad ? NAN : 0.f;
+    l.head[3] = most;
   }
 }
 
 // ---- rows: the sum and the gradient in one read ---------------------------------
+// A row of the walk, as the managing warp tells it to the others.
+struct RowInfo {
+  uintptr_t x, g;           // the first value of the logits' and of the gradient's row
+  int32_t live;             // 0: there is no further row
+  int32_t y;                // the target, kNoValue without one
+  int32_t ignored, n_ignored;  // rows before it (every `stride`) whose gradient is 0
+};
+// What the gradient needs: scale 2^(x c - R) with R of m, `more` at the target;
+// for a list, lead (on 2^(x c - R) - p) at its words.
+struct RowScale {
+  float m, scale, more, lead, on;
+};
+
+// The rows first, first + stride, .. of a cluster, 32 at a time: a lane looks
+// one up, and its per-token values with it, so that none of them is waited for
+// row by row.
+template <typename T, int OP>
+struct Walk {
+  const LossArgs& a;
+  int stride, base, off = 32;      // row of lane 0 one window back; next lane to look at
+  unsigned live = 0, valid = 0;
+  int64_t target = 0;
+  PolicyIn in{0.f, 0.f, 0.f};
+  float weight = 0.f, x_at = 0.f;
+  __device__ __forceinline__ Walk(const LossArgs& args, int first, int step) : a(args), stride(step), base(first - 32 * step) {}
+  // `values`: look the token's values up too, and write the results of ignored tokens (`writes`)
+  __device__ __forceinline__ void window(bool values, bool writes) {
+    const int lane = threadIdx.x & 31;
+    base += 32 * stride;
+    off = 0;
+    const int64_t row64 = base + static_cast<int64_t>(lane) * stride;
+    const bool is = row64 < a.tokens;
+    bool counts = false;
+    if (is) {
+      const int row = static_cast<int>(row64), b = row / a.seq, s = row % a.seq;
+      if (OP == kDistill) {
+        counts = counted(a, OP, b, s);
+      } else {
+        target = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+        counts = target != a.ignore;
+      }
+      if (values && counts) {
+        if (OP == kPolicy) {
+          in.adv = row_value(a.adv, b, s);
+          if (a.old.p != nullptr) in.old = row_value(a.old, b, s);
+          if (a.kl != 0.f) in.ref = row_value(a.ref, b, s);
+          if (target >= 0 && target < a.vocab) x_at = widen((static_cast<const T*>(a.x) + b * a.xsb + s * a.xss)[target]);
+        }
+        if (a.weights.p != nullptr) weight = row_value(a.weights, b, s);
+      }
+      if (writes && !counts) {
+        if (a.logp != nullptr) a.logp[row] = 0.f;
+        if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
+      }
+    }
+    valid = __ballot_sync(0xffffffffu, is);
+    live = __ballot_sync(0xffffffffu, counts);
+  }
+  // The lane that has the next counted row, -1 at the end; `ignored`: first and
+  // number of the rows passed over.
+  __device__ __forceinline__ int next(bool values, bool writes, int& ignored, int& n_ignored) {
+    n_ignored = 0;
+    while (true) {
+      if (off == 32) {
+        if (base + 32 * static_cast<int64_t>(stride) >= a.tokens) return -1;
+        window(values, writes);
+      }
+      const unsigned left = live >> off;
+      const int skip = left != 0 ? __ffs(static_cast<int>(left)) - 1 : __popc(valid >> off);
+      if (skip > 0 && n_ignored == 0) ignored = base + off * stride;
+      n_ignored += skip;
+      if (left != 0) {
+        off += skip + 1;
+        return off - 1;
+      }
+      off = 32;
+    }
+  }
+};
+
 // Clusters of CTAs walk the rows.  A warp copies its chunks of a row to its own
 // places of a ring in shared memory (bulk copies, one row ahead), adds up
 // their terms, and, when the cluster's parts of the row are together, makes the
 // gradient from the same copies; the places that come free take the next row's
-// chunks at once.  LONG: rows that no cluster keeps are read twice.
+// chunks at once.  One more warp manages: it looks the rows up ahead of the
+// others, joins the parts and works out the row's scalars, so that these cost
+// the others nothing (16 warps doing so themselves took 2300 cycles to begin a
+// row and 2500 from its sum to its gradient, of 13,500 in all).  For lists a
+// second one makes those.  LONG: rows that no cluster keeps are read twice.
 template <typename T, int OP, bool LONG>
-__global__ void __launch_bounds__(kMaxWarps * 32 + (OP == kDistill ? 32 : 0), 1) k_loss_row(const __grid_constant__ LossArgs a) {
+__global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 32, 2)
+    k_loss_row(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
-  __shared__ uint64_t together[2];
+  __shared__ RowInfo info[3];
+  __shared__ RowScale scales[2];
+  __shared__ uint64_t together[2], info_full[3], scale_full[2], list_full[2], list_free[2], written;
   constexpr bool kLists = OP == kDistill;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int warps = (blockDim.x >> 5) - (kLists ? 1 : 0), NT = 32 * warps;  // that sum
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = (blockDim.x >> 5) - (kLists ? 2 : 1);  // that sum
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int first = static_cast<int>(blockIdx.x) / ranks, stride = static_cast<int>(gridDim.x) / ranks;
   const int v0 = rank * a.vecs_per_cta, slots = a.slots;
@@ -743,178 +815,288 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + (OP == kDistill ? 32 : 0), 1)
   uint64_t* const full = reinterpret_cast<uint64_t*>(parts + 2 * warps * ranks) + warp * slots;  // a warp's [slots]
   unsigned char* const lists = reinterpret_cast<unsigned char*>(parts + 2 * warps * ranks) + (LONG ? 0 : (warps * slots * 8 + 15) / 16 * 16);
   const int slice = a.vecs_per_cta, list_size = list_bytes(slice, a.top_k);
-
-  // A barrier for the parts of each of the two rows; warp 0 expects the next
-  // but one row's as soon as a row's are there, before it sends its own of the
-  // next row: nobody can be further than that.
-  
+  // Bytes that a row's parts are; the manager expects the next but one row's
+  // as soon as a row's are there, and only then its scalars let anybody go on.
   const uint32_t row_bytes = 16 * warps * ranks;
-  if (ranks > 1) {
-    if (tid == 0) {
-      for (int k = 0; k < 2; ++k) {
-        init_barrier(together + k);
-        expect_bytes(together + k, row_bytes);
-      }
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k) {
+      init_barrier(together + k, ranks > 1 ? 1 : warps);
+      if (ranks > 1) expect_bytes(together + k, row_bytes);
+      init_barrier(scale_full + k, 1);
+      init_barrier(list_full + k, 1);
+      init_barrier(list_free + k, warps + 1);
     }
-    __syncthreads();
-    cluster_arrive();  // shared memory of the others may be written once they have all begun
+    for (int k = 0; k < 3; ++k) init_barrier(info_full + k, 1);
+    init_barrier(&written, warps);
+  }
+  if (!LONG && warp < warps && lane == 0)
+    for (int k = 0; k < slots; ++k) init_barrier(full + k, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();
+  if (ranks > 1) {  // shared memory of the others may be written once they have all begun
+    cluster_arrive();
     cluster_wait();
   }
-  struct Place {
-    int row, b, s;
-  };
-  const int by_b = stride / a.seq, by_s = stride % a.seq;
-  auto after = [&](Place t) {
-    t.row += stride;
-    t.b += by_b;
-    t.s += by_s;
-    if (t.s >= a.seq) {
-      t.s -= a.seq;
-      ++t.b;
-    }
-    return t;
-  };
-  auto row_at = [&](const Place& t) { return Row<T>(static_cast<const T*>(a.x) + t.b * a.xsb + t.s * a.xss, a.vocab); };
-  const Place begin{first, first / a.seq, first % a.seq};
-
-  if (kLists && warp == warps) {
-    // The warp that makes the lists, up to two rows ahead.
-    int q = 0;
-    for (Place t = begin; t.row < a.tokens; t = after(t)) {
-      if (!counted(a, OP, t.b, t.s)) continue;
-      const Row<T> r = row_at(t);
-      if (q >= 2) bar_sync(kBarListFree + (q & 1), NT + 32);
-      make_list(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, t.b, t.s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice,
-                rank == 0);
-      __syncwarp();
-      bar_arrive(kBarListFull + (q & 1), NT + 32);
-      ++q;
-    }
-    for (int k = max(0, q - 2); k < q; ++k) bar_sync(kBarListFree + (k & 1), NT + 32);
-    if (ranks > 1) {
-      cluster_arrive();
-      cluster_wait();
-    }
-    return;
-  }
-
-  // Target of a row; ignored rows have none (`kIgnored`).
-  constexpr int64_t kIgnored = INT64_MIN;
-  auto target_at = [&](const Place& t) -> int64_t {
-    if (t.row >= a.tokens) return kIgnored;
-    if (kLists) return counted(a, OP, t.b, t.s) ? 0 : kIgnored;
-    const int64_t y = load_index(a.y.p, a.ydt, t.b * a.y.sb + t.s * a.y.ss);
-    return y == a.ignore ? kIgnored : y;
-  };
-  // The warp's chunks of a row that ends before vector `last`: chunk q starts
-  // at vector `mine` + q kBatch NT.
-  const int mine = v0 + warp * kChunk;
-  auto chunks = [&](int last) { return last <= mine ? 0 : (last - mine - 1) / (kBatch * NT) + 1; };
-  // The granule of 16 bytes at a row's end may hold bytes of its neighbour; at
-  // the tensor's own ends it may reach outside, and is then read value by value.
-  auto copied_from = [&](const Row<T>& r) { return r.base < a.x_begin ? 1 : 0; };
-  auto copied_to = [&](const Row<T>& r) { return r.base + 16 * static_cast<int64_t>(r.vecs) > a.x_end ? r.vecs - 1 : r.vecs; };
-  int fill = 0;  // the place of the ring that the next chunk goes to
-  // Copies chunks [from, to) of a row.
-  auto copy = [&](const Row<T>& r, int from, int to) {
-    const int lo = copied_from(r), hi = min(copied_to(r), v0 + a.vecs_per_cta);
-    for (int q = from; q < to; ++q) {
-      if (lane == 0) {
-        const int i = mine + q * kBatch * NT, i0 = max(i, lo), n = min(i + kChunk, hi) - i0;
-        copy_bulk(ring + fill * kChunk + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + fill);
-      }
-      if (++fill == slots) fill = 0;
-    }
-  };
-  if (!LONG) {
-    if (lane == 0) {
-      for (int k = 0; k < slots; ++k) init_barrier(full + k);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncwarp();
-  }
-
-  Place at{begin};
-  int64_t target = target_at(at), target1 = target_at(after(at));
-  const bool gradient = a.g != nullptr;
-  Row<T> r = row_at(at);
-  // The row's chunks, the ring's place of its first and the parity of that
-  // one's barrier.
-  int n_chunks = target != kIgnored ? chunks(min(r.vecs, v0 + a.vecs_per_cta)) : 0, base = 0;
-  uint32_t parity = 0;
   bool dead = false;  // a wait ran out: no more waiting, the loss is NaN
-  if (!LONG) copy(r, 0, n_chunks);
-  Sum share;           // of the cluster's rows in the loss (rank 0, warp 0)
-  float by_count = 0.f;
-  bool waited = false;
-  int q = 0;  // counted rows so far
 
-  for (; at.row < a.tokens; at = after(at)) {
-    const bool live = target != kIgnored, live1 = target1 != kIgnored;
-    const Place next = after(at);
-    const int row = at.row, b = at.b, s = at.s;
-    const Row<T> r1 = live1 ? row_at(next) : r;
-    const GradRow<T> g(!gradient ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
-    const int64_t target2 = target_at(after(next));
-    const int n_chunks1 = live1 ? chunks(min(r1.vecs, v0 + a.vecs_per_cta)) : 0;
-    const int early1 = min(n_chunks1, slots - n_chunks);  // what there is room for before this row's places come free
-    if (!LONG) {
-      __syncwarp();  // the row before has been read
-      copy(r1, 0, early1);
+  if (kLists && warp == warps + 1) {
+    // The warp that makes the lists, up to two rows ahead.
+    Walk<T, OP> walk(a, first, stride);
+    int q = 0, none, n_none;
+    for (int at = walk.next(false, false, none, n_none); at >= 0; at = walk.next(false, false, none, n_none), ++q) {
+      const int row = walk.base + at * stride, b = row / a.seq, s = row % a.seq;
+      const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
+      if (q >= 2 && !wait_phase(list_free + (q & 1), (q - 2) >> 1 & 1)) break;
+      make_list(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, b, s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice);
+      __syncwarp();
+      if (lane == 0) arrive(list_full + (q & 1));
     }
-    if (!live) {
-      if (gradient) g.zero(rank, ranks, NT);
-      if (rank == 0 && tid == 0) {
-        if (a.logp != nullptr) a.logp[row] = 0.f;
-        if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
+  } else if (warp == warps) {
+    // The manager.
+    Walk<T, OP> walk(a, first, stride);
+    struct Values {
+      int row, y;
+      bool live;
+      PolicyIn in;
+      float weight, x_at;
+    };
+    int told = 0;
+    auto tell_next = [&] {
+      RowInfo i;
+      Values v;
+      int ignored = 0;
+      const int at = walk.next(true, rank == 0, ignored, i.n_ignored);
+      const int from = max(at, 0);
+      v.live = at >= 0;
+      v.row = walk.base + from * stride;
+      const int64_t target = __shfl_sync(0xffffffffu, walk.target, from);
+      v.y = !kLists && target >= 0 && target < a.vocab ? static_cast<int>(target) : kNoValue;
+      v.in.adv = __shfl_sync(0xffffffffu, walk.in.adv, from);
+      v.in.old = __shfl_sync(0xffffffffu, walk.in.old, from);
+      v.in.ref = __shfl_sync(0xffffffffu, walk.in.ref, from);
+      v.weight = __shfl_sync(0xffffffffu, walk.weight, from);
+      v.x_at = __shfl_sync(0xffffffffu, walk.x_at, from);
+      const int b = v.row / a.seq, s = v.row % a.seq;
+      i.x = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss);
+      i.g = a.g == nullptr ? 0 : reinterpret_cast<uintptr_t>(static_cast<T*>(a.g) + b * a.gsb + s * a.gss);
+      i.live = v.live;
+      i.y = v.y;
+      i.ignored = ignored;
+      if (lane == 0) {
+        info[told % 3] = i;
+        arrive(info_full + told % 3);
       }
-    } else {
-      const int v1 = min(r.vecs, v0 + a.vecs_per_cta);
-      const bool writes = rank == 0 && warp == 0;
-      // Per-token values, while the sum is made.
-      PolicyIn in{0.f, 0.f, 0.f};
-      float weight = 0.f;
-      if (OP == kPolicy) {
-        in.adv = row_value(a.adv, b, s);
-        if (a.old.p != nullptr) in.old = row_value(a.old, b, s);
-        if (a.kl != 0.f) in.ref = row_value(a.ref, b, s);
-      }
-      if (a.weights.p != nullptr) weight = row_value(a.weights, b, s);
+      ++told;
+      return v;
+    };
+    Values v = tell_next(), v1 = v;
+    if (v.live) v1 = tell_next();
+    Sum share;  // of the cluster's rows in the loss
+    float by_count = 0.f;
+    bool waited = false;
+    for (int q = 0; v.live; ++q) {
       const List list = list_at(lists + (q & 1) * list_size, slice, a.top_k);
-      if (kLists) bar_sync(kBarListFull + (q & 1), NT + 32);
-
-      // The target's logit, from the thread that has it.
-      int y = kNoValue, y_vec = kNoValue;
-      float x_at = 0.f;
-      bool has = false;
-      if (!kLists && target >= 0 && target < a.vocab) {
-        y = static_cast<int>(target);
-        y_vec = (y + r.lead) / kN<T>;
-        const int v = y_vec - v0;
-        has = y_vec >= v0 && y_vec < v1 && v / kChunk % warps == warp && v % 32 == lane;
-        if (has) x_at = widen(*r.value(y));
+      if (kLists && !wait_phase(list_full + (q & 1), q >> 1 & 1)) dead = true;
+      if (dead || !wait_phase(together + (q & 1), q >> 1 & 1)) dead = true;
+      if (dead) break;
+      const float4* const here = parts + (q & 1) * warps * ranks;
+      const int all = warps * ranks;
+      const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f), mine = lane < all ? here[lane] : none;
+      float m = kLists ? fmaxf(mine.x, list.head[3]) : mine.x;
+      for (int k = lane + 32; k < all; k += 32) m = fmaxf(m, here[k].x);
+      const Ref ref(warp_max(m), a.c);
+      float sum = mine.y * ref.factor(mine.x, a.c), wrong = mine.w, top = 0.f;
+      for (int k = lane + 32; k < all; k += 32) {
+        const float4 o = here[k];
+        sum += o.y * ref.factor(o.x, a.c);
+        wrong += o.w;
       }
+      if (kLists)
+        for (int k = lane; k < a.top_k; k += 32) top += list.id[k] < 0 ? 0.f : ex2(ref.exponent(list.x[k], a.c));
+      sum = warp_sum(sum);
+      if (kLists) {
+        top = warp_sum(top);
+        wrong = warp_sum(wrong);
+      }
+      if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
+      __syncwarp();
+      if (ranks > 1 && lane == 0) expect_bytes(together + (q & 1), row_bytes);
 
-      // The thread's terms.
-      const int lo = r.first_whole(), hi = min(r.past_whole(), v1);
-      Part<T, kLists> part;
+      if (!waited) {
+        wait_for_previous();
+        waited = true;
+        by_count = a.weights.p == nullptr ? 1.f / static_cast<float>(*a.count) : 0.f;
+      }
+      const float w = a.weights.p != nullptr ? v.weight : by_count;
+      RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f};
+      float logp = 0.f, loss = 0.f;
+      const float d = ref.residue(a.c) * kLn2;
+      if (!kLists) {
+        logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + d + wrong;
+        const Token t = policy_token(a, logp, v.in);
+        loss = t.loss;
+        out.more = w * a.gscale * a.inv_t * t.d;
+        out.scale = __fdividef(-out.more, sum);
+      } else {
+        // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
+        const float rest = list.head[1];
+        out.lead = w * a.gscale / a.inv_t + wrong;
+        out.on = (list.head[0] + rest) / (sum + top);
+        out.scale = out.lead * (out.on - (rest > 0.f ? rest / sum : 0.f));
+      }
+      if (lane == 0) {
+        scales[q & 1] = out;
+        arrive(scale_full + (q & 1));
+      }
+      __syncwarp();
+      // The others make the gradient from here on.
+      if (kLists && rank == 0) {
+        const float log_s = logf(sum + top), rest = list.head[1];
+        for (int k = lane; k < a.top_k; k += 32) {
+          const float pk = list.p[k];
+          if (pk != 0.f) loss += pk * (logf(pk) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
+        }
+        loss = warp_sum(loss);
+        if (rest > 0.f) loss += rest * (logf(rest) - (logf(sum) - log_s));
+        loss = loss / (a.inv_t * a.inv_t) + wrong;
+      }
+      if (rank == 0) {
+        if (lane == 0 && a.logp != nullptr) a.logp[v.row] = logp;
+        if (lane == 0 && a.token_loss != nullptr) a.token_loss[v.row] = loss;
+        share.add(a.weights.p != nullptr ? w * loss : loss);
+      }
+      if (kLists) {
+        __syncwarp();
+        if (lane == 0) arrive(list_free + (q & 1));
+      }
+      v = v1;
+      if (v.live) v1 = tell_next();
+    }
+    if (dead) share.s = NAN;
+
+    // The clusters' shares: the last to come sums them all, in order.
+    if (rank == 0) {
+      if (!waited) wait_for_previous();
+      int last = 0;
+      if (lane == 0) {
+        a.part[first] = share;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(stride - 1);
+      }
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        __threadfence();
+        Sum sum;
+        for (int k = lane; k < stride; k += 32) {
+          const float2 o = __ldcg(reinterpret_cast<const float2*>(a.part) + k);
+          Sum p;
+          p.s = o.x;
+          p.rest = o.y;
+          sum.add(p);
+        }
+        sum.over_warp();
+        if (lane == 0) {
+          const float n = a.weights.p == nullptr ? static_cast<float>(*a.count) : 1.f;
+          *a.loss = n > 0.f ? sum.total() / n : 0.f;
+        }
+      }
+    }
+  } else {
+    // A warp that sums.  Its chunks of a row that ends before vector `last`:
+    // chunk q starts at vector `mine` + q * between.
+    const int mine = v0 + warp * kChunk, between = warps * kChunk;
+    auto chunks = [&](const Row<T>& r) {
+      const int last = min(r.vecs, v0 + a.vecs_per_cta);
+      return last <= mine ? 0 : (last - mine - 1) / between + 1;
+    };
+    // The granule of 16 bytes at a row's end may hold bytes of its neighbour; at
+    // the tensor's own ends it may reach outside, and is then read value by value.
+    auto copied_from = [&](const Row<T>& r) { return r.base < a.x_begin ? 1 : 0; };
+    auto copied_to = [&](const Row<T>& r) { return r.base + 16 * static_cast<int64_t>(r.vecs) > a.x_end ? r.vecs - 1 : r.vecs; };
+    int fill = 0;  // the place of the ring that the next chunk goes to
+    // Copies chunks [from, to) of a row.
+    auto copy = [&](const Row<T>& r, int from, int to) {
+      for (int q = from; q < to; ++q) {
+        if (lane == 0) {
+          const int i = mine + q * between, i0 = max(i, copied_from(r));
+          const int n = min(i + kChunk, min(copied_to(r), v0 + a.vecs_per_cta)) - i0;
+          copy_bulk(ring + fill * kChunk + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + fill,
+                    a.stall != 0);
+        }
+        if (++fill == slots) fill = 0;
+      }
+    };
+    const bool gradient = a.g != nullptr;
+    int told = 0, told_parity = 0;
+    auto next_info = [&] {
+      if (!wait_phase(info_full + told, told_parity)) dead = true;
+      RowInfo i = info[told];
+      if (dead) i.live = i.n_ignored = 0;
+      if (++told == 3) {
+        told = 0;
+        told_parity ^= 1;
+      }
+      return i;
+    };
+    RowInfo now = next_info();
+    Row<T> r(reinterpret_cast<const T*>(now.x), a.vocab);
+    // The row's chunks, the ring's place of its first and the parity of that
+    // one's barrier.
+    int n_chunks = now.live ? chunks(r) : 0, base = 0;
+    uint32_t parity = 0;
+    if (!LONG) copy(r, 0, n_chunks);
+    for (int q = 0;; ++q) {
+      if (gradient && now.n_ignored > 0) {
+        for (int k = 0; k < now.n_ignored; ++k) {
+          const int row = now.ignored + k * stride, b = row / a.seq, s = row % a.seq;
+          GradRow<T>(static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, 0).zero(rank, ranks, 32 * warps);
+        }
+      }
+      if (!now.live) break;
+      const RowInfo then = next_info();
+      if (dead) break;
+      const Row<T> r1(reinterpret_cast<const T*>(then.x), a.vocab);
+      const int n_chunks1 = then.live ? chunks(r1) : 0;
+      const int early1 = min(n_chunks1, slots - n_chunks);  // what there is room for before this row's places come free
+      if (!LONG) {
+        if (kLists) writes_before_copies();
+        __syncwarp();  // the row before has been read
+        copy(r1, 0, early1);
+      }
+      const List list = list_at(lists + (q & 1) * list_size, slice, a.top_k);
+      if (kLists && !wait_phase(list_full + (q & 1), q >> 1 & 1)) dead = true;
+      if (dead) break;
+
+      // The warp's terms.
+      const int v1 = min(r.vecs, v0 + a.vecs_per_cta), lo = r.first_whole(), hi = min(r.past_whole(), v1);
+      Part<T> part;
       int place = base;
       uint32_t phase = parity;
       for (int q2 = 0; q2 < n_chunks; ++q2) {
-        const int i = mine + q2 * kBatch * NT + lane;
-        const uint4* const from = ring + place * kChunk + lane;
-        if (!LONG && !dead && !wait_phase(full + place, phase)) dead = true;
+        const int i = mine + q2 * between + lane;
+        uint4* const from = ring + place * kChunk + lane;
+        if (!LONG && !wait_phase(full + place, phase)) {
+          dead = true;
+          break;
+        }
         if (++place == slots) {
           place = 0;
           phase ^= 1;
         }
-        const Bits bits = kLists ? list.bits[(q2 * warps + warp) * 32 + lane] : 0;
-        if (batch_in<32>(i - lane, lo, hi)) {
+        // The listed words leave the copy: their terms are summed apart, and
+        // their gradients written after the others'.
+        Bits on = kLists ? list.bits[(q2 * warps + warp) * 32 + lane] : 0;
+        if (!LONG) {
+          for (; on != 0; on &= on - 1) {
+            const int bit = __ffs(static_cast<int>(on)) - 1;
+            T* const x = reinterpret_cast<T*>(from + bit / 8 * 32) + bit % 8;
+            narrow(*x, -INFINITY);
+          }
+        }
+        if (batch_in<32>(i - lane, lo, hi) && !(LONG && kLists)) {
           uint4 w[kBatch];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) w[k] = LONG ? __ldcs(reinterpret_cast<const uint4*>(r.base) + i + k * 32) : from[k * 32];
-          part.add(w, a.c, bits);
+          part.add(w, a.c);
         } else {
 #pragma unroll 1
           for (int k = 0; k < kBatch && i - lane + k * 32 < v1; ++k) {
@@ -922,99 +1104,47 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + (OP == kDistill ? 32 : 0), 1)
             uint4 w[1] = {no_values(kNegInf<T>)};
             if (LONG || e < copied_from(r) || e >= copied_to(r)) {
               w[0] = load_vec(r, e, v1);
+              const uint32_t out = kLists ? static_cast<uint32_t>(list.bits[(q2 * warps + warp) * 32 + lane] >> (8 * k)) : 0;
+#pragma unroll
+              for (int j = 0; j < kN<T>; ++j)
+                if (kLists && (out >> j & 1)) put<T>(w[0], j, sizeof(T) == 2 ? 0xff80u : 0xff800000u);
             } else if (e < v1) {
               w[0] = from[k * 32];
               if (r.ragged(e)) trim(w[0], r, e);
             }
-            part.add(w, a.c, bits >> (8 * k) & 0xff);
+            part.add(w, a.c);
           }
         }
       }
 
-      // The warp's part to every CTA of the cluster; each warp joins them all.
+      if (dead) break;
+
+      // The warp's part, to every CTA of the cluster.
       float4 p;
       p.x = warp_max(part.m);
-      const float f = Ref(p.x, a.c).factor(part.m, a.c);
-      p.y = warp_sum(part.s * f);
-      const unsigned who = __ballot_sync(0xffffffffu, has);
-      if (who != 0) x_at = __shfl_sync(0xffffffffu, x_at, __ffs(static_cast<int>(who)) - 1);
-      p.z = kLists ? warp_sum(part.top * f) : x_at;
+      p.y = warp_sum(part.s * Ref(p.x, a.c).factor(part.m, a.c));
+      p.z = 0.f;
       p.w = kLists && warp == 0 ? list.head[2] : 0.f;
       float4* const here = parts + (q & 1) * warps * ranks;
       if (ranks > 1) {
         if (lane < ranks) send(here + rank * warps + warp, lane, p, together + (q & 1));
-        if (!dead && !wait_phase(together + (q & 1), q >> 1 & 1)) dead = true;
-        __syncwarp();
-        if (tid == 0) expect_bytes(together + (q & 1), row_bytes);
-      } else {
-        if (lane == 0) here[warp] = p;
-        bar_sync(kBarRow, NT);
+      } else if (lane == 0) {
+        here[warp] = p;
+        arrive(together + (q & 1));
       }
-      const int all = warps * ranks;
-      const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f), mine0 = lane < all ? here[lane] : none;
-      float m = mine0.x;
-      for (int k = lane + 32; k < all; k += 32) m = fmaxf(m, here[k].x);
-      const Ref ref(warp_max(m), a.c);
-      const float f0 = ref.factor(mine0.x, a.c);
-      float sum = mine0.y * f0, z = kLists ? mine0.z * f0 : mine0.z, wrong = mine0.w;
-      for (int k = lane + 32; k < all; k += 32) {
-        const float4 o = here[k];
-        const float fo = ref.factor(o.x, a.c);
-        sum += o.y * fo;
-        z += kLists ? o.z * fo : o.z;
-        wrong += o.w;
-      }
-      sum = warp_sum(sum);
-      z = warp_sum(z);
-      if (kLists) wrong = warp_sum(wrong);
-      if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
+      if (!wait_phase(scale_full + (q & 1), q >> 1 & 1)) dead = true;
+      if (dead) break;
+      const RowScale by = scales[q & 1];
+      const Ref ref(by.m, a.c);
 
-      if (!waited) {
-        wait_for_previous();
-        waited = true;
-        by_count = a.weights.p == nullptr ? 1.f / static_cast<float>(*a.count) : 0.f;
-      }
-      const float w = a.weights.p != nullptr ? weight : by_count;
-      // gradient: scale 2^(x c - R), `more` at the target; for a list, lead (on 2^(x c - R) - p) at its words
-      float scale, more = 0.f, lead = 0.f, on = 0.f;
-      if (!kLists) {
-        const float logp = y < 0 ? NAN : (z - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
-        const Token t = policy_token(a, logp, in);
-        if (writes) {
-          if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
-          if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = t.loss;
-          share.add(a.weights.p != nullptr ? w * t.loss : t.loss);
-        }
-        more = w * a.gscale * a.inv_t * t.d;
-        scale = __fdividef(-more, sum);
-      } else {
-        const float sum_p = list.head[0], rest = list.head[1], off = sum;
-        sum += z;
-        if (writes) {
-          const float log_s = logf(sum), d = ref.residue(a.c) * kLn2;
-          float l = 0.f;
-          for (int k = lane; k < a.top_k; k += 32) {
-            const float pk = list.p[k];
-            if (pk != 0.f) l += pk * (logf(pk) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
-          }
-          l = warp_sum(l);
-          if (rest > 0.f) l += rest * (logf(rest) - (logf(off) - log_s));
-          const float loss = l / (a.inv_t * a.inv_t) + wrong;
-          if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
-          share.add(a.weights.p != nullptr ? w * loss : loss);
-        }
-        // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
-        lead = w * a.gscale / a.inv_t + wrong;
-        on = (sum_p + rest) / sum;
-        scale = lead * (on - (rest > 0.f ? rest / off : 0.f));
-      }
-
-      // The gradient, and the next row's vectors into the places that come free.
+      // The gradient, and the next row's chunks into the places that come free.
       if (gradient) {
+        const GradRow<T> g(reinterpret_cast<T*>(now.g), a.vocab, r.lead);
         const bool near = g.shift == 0 && !ref.far();
+        const int y_vec = now.y >= 0 ? (now.y + r.lead) / kN<T> : kNoValue;
         place = base;
         for (int q2 = 0; q2 < n_chunks; ++q2) {
-          const int i = mine + q2 * kBatch * NT + lane;
+          const int i = mine + q2 * between + lane;
           uint4 v[kBatch];
           const bool plain = batch_in<32>(i - lane, lo, hi);
           if (LONG) {
@@ -1031,74 +1161,53 @@ __global__ void __launch_bounds__(kMaxWarps * 32 + (OP == kDistill ? 32 : 0), 1)
             }
           }
           if (++place == slots) place = 0;
-          store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c, scale,
-                             y, y_vec, more);
+          store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c,
+                             by.scale, now.y, y_vec, by.more);
           const int q3 = q2 + slots - n_chunks;
           if (!LONG && q3 >= early1 && q3 < n_chunks1) {
+            if (kLists) writes_before_copies();
             __syncwarp();  // the place has been read
             copy(r1, q3, q3 + 1);
           }
         }
         if (kLists) {
-          bar_sync(kBarRow, NT);  // the listed words' values replace those written above
-          for (int k = tid; k < a.top_k; k += NT) {
+          __syncwarp();
+          if (lane == 0) arrive(&written);
+          if (!wait_phase(&written, q & 1)) dead = true;  // the listed words' values replace those written above
+          if (dead) break;
+          for (int k = threadIdx.x; k < a.top_k; k += 32 * warps) {
             const int i = list.id[k], v = (i + r.lead) / kN<T>;
             if (i >= 0 && v >= v0 && v < v1)
-              narrow(g.g[i], lead * (on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+              narrow(g.g[i], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
           }
         }
       } else if (!LONG) {
+        if (kLists) writes_before_copies();
         __syncwarp();
         copy(r1, early1, n_chunks1);
       }
-      if (kLists) bar_arrive(kBarListFree + (q & 1), NT + 32);
-      ++q;
+      if (kLists) {
+        __syncwarp();
+        if (lane == 0) arrive(list_free + (q & 1));
+      }
+      base += n_chunks;
+      if (base >= slots) {
+        base -= slots;
+        parity ^= 1;
+      }
+      n_chunks = n_chunks1;
+      r = r1;
+      now = then;
     }
-    base += n_chunks;
-    if (base >= slots) {
-      base -= slots;
-      parity ^= 1;
-    }
-    n_chunks = n_chunks1;
-    r = live1 || next.row >= a.tokens ? r1 : row_at(next);
-    target = target1;
-    target1 = target2;
+    // Copies still in flight land before the CTA's memory is given up.
+    if (dead)
+      for (int k = 0; k < slots; ++k)
+        if (!wait_phase(full + k, k < base ? parity : parity ^ 1)) break;
   }
-  if (__any_sync(0xffffffffu, dead)) {
-    share.s = NAN;
-    // copies still in flight land before the CTA's memory is given up
-    for (int k = 0; k < slots; ++k) wait_phase(full + k, k < base ? parity : parity ^ 1);
-  }
-
   if (ranks > 1) {  // nobody leaves while others may write here
+    __syncwarp();
     cluster_arrive();
     cluster_wait();
-  }
-
-  // The clusters' shares: the last to come sums them all, in order.
-  if (rank == 0 && warp == 0) {
-    if (!waited) wait_for_previous();
-    int last = 0;
-    if (lane == 0) {
-      a.part[first] = share;
-      __threadfence();
-      last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(stride - 1);
-    }
-    if (!__shfl_sync(0xffffffffu, last, 0)) return;
-    __threadfence();
-    Sum v;
-    for (int k = lane; k < stride; k += 32) {
-      const float2 o = __ldcg(reinterpret_cast<const float2*>(a.part) + k);
-      Sum p;
-      p.s = o.x;
-      p.rest = o.y;
-      v.add(p);
-    }
-    v.over_warp();
-    if (lane == 0) {
-      const float n = a.weights.p == nullptr ? static_cast<float>(*a.count) : 1.f;
-      *a.loss = n > 0.f ? v.total() / n : 0.f;
-    }
   }
 }
 
@@ -1131,7 +1240,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_loss_forward(const __grid_con
   const int v0 = rank * a.vecs_per_cta, v1 = min(r.vecs, v0 + a.vecs_per_cta);
   const bool inside = target >= 0 && target < a.vocab;
   const float x_at = writes && inside ? widen(*r.value(static_cast<int>(target))) : NAN;
-  Part<T, false> part;
+  Part<T> part;
   uint4 w[kForwardBatch], w1[kForwardBatch];
   load_batch<T, NT>(w, r, v0 + tid, v1);
   for (int i = v0 + tid; i - lane < v1; i += kForwardBatch * NT) {
@@ -1523,8 +1632,8 @@ Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
     const int n = div_up(mine, c.warps);
     c.shared = 2 * c.warps * cluster * static_cast<int>(sizeof(float4)) + (lists ? 2 * list_bytes(c.vecs_per_cta, top_k) : 0);
     const int place = kChunk * 16 + 8;  // and its barrier
-    for (int ctas = kMaxWarps / c.warps; ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs of an SM
-      const int room = kSharedBytes / ctas - 1024 - 64 - c.shared;
+    for (int ctas = 2 * kMaxWarps / c.warps; ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs of an SM
+      const int room = kSharedBytes / ctas - 1024 - 512 - c.shared;
       c.slots = std::min(2 * n, std::max(0, room / (c.warps * place)));
       if (c.slots > n) break;
     }
@@ -1558,7 +1667,7 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   const bool bf16 = dtype == ADAF_BFLOAT16, twice_read = cut.slots == 0;
   void (*const kernel)(LossArgs) = twice_read ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
                                               : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
-  const int threads = 32 * (cut.warps + (OP == kDistill ? 1 : 0));
+  const int threads = 32 * (cut.warps + (OP == kDistill ? 2 : 1));
   int& most = dev.clusters[{reinterpret_cast<const void*>(kernel),
                             (static_cast<int64_t>(cut.shared) << 16) + (cut.warps << 4) + cut.cluster}];
   if (most == 0) {
