@@ -55,7 +55,9 @@
  * run in a fixed order: equal inputs give equal bits.
  *
  * Every call only launches kernels on the caller's stream: it allocates
- * nothing, waits for nothing and may be captured in a graph.  The workspace
+ * nothing on the device, waits for nothing and may be captured in a graph.
+ * Every wait inside a kernel is bounded; if one runs out, which no input
+ * brings about, the call ends with a loss of NaN.  The workspace
  * needs no initialisation.  Calls on different streams may run at the same
  * time if each has its own workspace.  Status codes, dtypes and the message
  * slot are shared with adafactor.h; every argument check runs before the
@@ -180,6 +182,11 @@ adaf_status loss_preference(const loss_logits* x, const loss_targets* y, const l
 /* loss [1], token_loss [batch * seq] (may be NULL). */
 adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, const loss_grad* grad, float* loss,
                          float* token_loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Testing hook: while on, the bulk copies of loss_policy and loss_distill are
+ * expected but not made, so that the kernel's waits for them run out (after
+ * about a second each); the loss of such a call is NaN. */
+void loss_debug_stall_copies(int32_t on);
 
 /* Per-kernel CUDA-event timing, as in adafactor.h. */
 adaf_status loss_profile_enable(int32_t on);

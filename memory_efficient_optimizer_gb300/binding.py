@@ -46,7 +46,8 @@ LAMB_EXPORTS = (
 # Entry points declared in include/losses.h.
 LOSS_EXPORTS = (
     "loss_workspace_size", "loss_token_logprobs", "loss_token_logprobs_backward", "loss_policy", "loss_preference",
-    "loss_distill", "loss_profile_enable", "loss_profile_read", "loss_num_kernels", "loss_kernel_name",
+    "loss_distill", "loss_debug_stall_copies", "loss_profile_enable", "loss_profile_read", "loss_num_kernels",
+    "loss_kernel_name",
 )
 LOSS_INT32 = 0
 LOSS_INT64 = 1
@@ -271,6 +272,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.loss_distill.restype = ctypes.c_int
         lib.loss_distill.argtypes = [P(loss_logits), P(loss_distill_args), P(loss_grad), ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.loss_debug_stall_copies.restype = None
+        lib.loss_debug_stall_copies.argtypes = [ctypes.c_int32]
         lib.loss_profile_enable.restype = ctypes.c_int
         lib.loss_profile_enable.argtypes = [ctypes.c_int32]
         lib.loss_profile_read.restype = ctypes.c_int
@@ -550,6 +553,11 @@ def loss_distill(x, args, grad, loss: int, token_loss: int, workspace: int, work
                                     workspace_bytes, stream)
     if st:
         _check(st)
+
+
+def loss_debug_stall_copies(on: bool) -> None:
+    """Testing hook: the copies of the next calls are expected but not made (see the header)."""
+    load().loss_debug_stall_copies(1 if on else 0)
 
 
 def loss_profile_enable(on: bool) -> None:

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -91,7 +92,7 @@ struct LossArgs {
   float* logp;
   float* token_loss;
   float2* stats;                  // [tokens]: m, s
-  int* count;                     // counted tokens
+  int* count;                     // counted tokens; NULL: k_loss_row counts them itself
   Sum* part;                      // [clusters]: sum of w l, or of l
   unsigned* ticket;
   int32_t vecs_per_cta;           // k_loss_row, k_loss_forward: vectors of a row for a CTA
@@ -892,8 +893,21 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     Values v = tell_next(), v1 = v;
     if (v.live) v1 = tell_next();
     Sum share;  // of the cluster's rows in the loss
-    float by_count = 0.f;
+    int n_counted = 0;
     bool waited = false;
+    if (a.count == nullptr) {
+#pragma unroll 4
+      for (int t = lane; t < a.tokens; t += 32) n_counted += counted(a, OP, t / a.seq, t % a.seq);
+      n_counted = __reduce_add_sync(0xffffffffu, n_counted);
+      waited = true;
+    }
+    // The counting kernel's result and its clearing of the ticket.
+    auto wait_for_count = [&] {
+      if (waited) return;
+      wait_for_previous();
+      waited = true;
+      n_counted = *a.count;
+    };
     for (int q = 0; v.live; ++q) {
       const List list = list_at(lists + (q & 1) * list_size, slice, a.top_k);
       if (kLists && !wait_phase(list_full + (q & 1), q >> 1 & 1)) dead = true;
@@ -922,12 +936,8 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
       __syncwarp();
       if (ranks > 1 && lane == 0) expect_bytes(together + (q & 1), row_bytes);
 
-      if (!waited) {
-        wait_for_previous();
-        waited = true;
-        by_count = a.weights.p == nullptr ? 1.f / static_cast<float>(*a.count) : 0.f;
-      }
-      const float w = a.weights.p != nullptr ? v.weight : by_count;
+      wait_for_count();
+      const float w = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
       RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f};
       float logp = 0.f, loss = 0.f;
       const float d = ref.residue(a.c) * kLn2;
@@ -976,7 +986,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
 
     // The clusters' shares: the last to come sums them all, in order.
     if (rank == 0) {
-      if (!waited) wait_for_previous();
+      wait_for_count();
       int last = 0;
       if (lane == 0) {
         a.part[first] = share;
@@ -995,8 +1005,9 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
         }
         sum.over_warp();
         if (lane == 0) {
-          const float n = a.weights.p == nullptr ? static_cast<float>(*a.count) : 1.f;
+          const float n = a.weights.p == nullptr ? static_cast<float>(n_counted) : 1.f;
           *a.loss = n > 0.f ? sum.total() / n : 0.f;
+          if (a.count == nullptr) *a.ticket = 0;  // for the stream's next call
         }
       }
     }
@@ -1556,6 +1567,7 @@ struct ProfRecord {
 };
 std::mutex g_mu;
 bool g_profile = false;
+std::atomic<bool> g_stall{false};
 std::vector<ProfRecord> g_prof;
 
 // Launches a kernel of this file; under profiling between two events.
@@ -1649,6 +1661,8 @@ Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
 
 struct Device {
   int sms = 0;
+  unsigned* tickets = nullptr;           // g_tickets on this device
+  std::map<cudaStream_t, int> streams;   // of the streams that have one
   std::map<std::pair<const void*, int64_t>, int> clusters;  // that run at a time, by kernel and cut
 };
 std::map<int, Device> g_devices;
@@ -1693,7 +1707,8 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   lock.unlock();
   a.vecs_per_cta = cut.vecs_per_cta;
   a.slots = cut.slots;
-  return launch(kSlotRow, kernel, clusters * cut.cluster, threads, cut.shared, cut.cluster, true, s, a);
+  a.stall = g_stall.load() ? 1 : 0;
+  return launch(kSlotRow, kernel, clusters * cut.cluster, threads, cut.shared, cut.cluster, a.count != nullptr, s, a);
 }
 adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
   const int vecs = row_vecs(a, dtype);
@@ -1716,9 +1731,49 @@ adaf_status launch_grad(LossArgs a, int32_t dtype, cudaStream_t s) {
   return launch(kSlotGrad, dtype == ADAF_BFLOAT16 ? k_loss_grad<__nv_bfloat16> : k_loss_grad<float>, grid, kGradThreads,
                 0, 1, a.coef != nullptr, s, a);
 }
-adaf_status launch_mean(const LossArgs& a, int op, int32_t dtype, cudaStream_t s) {
-  const adaf_status st = launch(kSlotCount, k_loss_count, 1, kCountThreads, 0, 1, false, s, a, op);
-  if (st != ADAF_OK || a.tokens == 0) return st;
+// A call for a few tokens is one launch: the managing warps count the tokens
+// themselves, and the ticket is one that the library keeps for the stream (the
+// last CTA leaves it at 0; calls on one stream follow one another).  For 8
+// tokens the host spends 5 us less than with k_loss_count before it; from some
+// hundred tokens on counting holds the first row up.  A captured call may be
+// replayed on any stream and so takes the workspace's ticket.
+constexpr int kFewTokens = 512;
+constexpr int kTickets = 1024;
+__device__ unsigned g_tickets[kTickets];
+
+unsigned* stream_ticket(cudaStream_t s) {
+  if (s == cudaStreamPerThread) return nullptr;  // a handle for many streams
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capturing) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  int device = 0;
+  if (capturing != cudaStreamCaptureStatusNone || cudaGetDevice(&device) != cudaSuccess) return nullptr;
+  std::lock_guard<std::mutex> lock(g_mu);
+  Device& dev = g_devices[device];
+  if (dev.tickets == nullptr && cudaGetSymbolAddress(reinterpret_cast<void**>(&dev.tickets), g_tickets) != cudaSuccess) {
+    cudaGetLastError();
+    dev.tickets = nullptr;
+    return nullptr;
+  }
+  const auto at = dev.streams.find(s);
+  if (at != dev.streams.end()) return dev.tickets + at->second;
+  const int slot = static_cast<int>(dev.streams.size());
+  if (slot >= kTickets) return nullptr;
+  dev.streams[s] = slot;
+  return dev.tickets + slot;
+}
+
+adaf_status launch_mean(LossArgs a, int op, int32_t dtype, cudaStream_t s) {
+  unsigned* const ticket = a.tokens > 0 && a.tokens <= kFewTokens ? stream_ticket(s) : nullptr;
+  if (ticket != nullptr) {
+    a.ticket = ticket;
+    a.count = nullptr;
+  } else {
+    const adaf_status st = launch(kSlotCount, k_loss_count, 1, kCountThreads, 0, 1, false, s, a, op);
+    if (st != ADAF_OK || a.tokens == 0) return st;
+  }
   return op == kPolicy ? launch_rows<kPolicy>(a, dtype, s) : launch_rows<kDistill>(a, dtype, s);
 }
 
@@ -1922,6 +1977,8 @@ adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, co
   a.weights = rows_of(args->weights);
   return launch_mean(a, kDistill, x->dtype, static_cast<cudaStream_t>(stream));
 }
+
+void loss_debug_stall_copies(int32_t on) { g_stall = on != 0; }
 
 adaf_status loss_profile_enable(int32_t on) {
   std::lock_guard<std::mutex> lock(g_mu);

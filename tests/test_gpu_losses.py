@@ -525,6 +525,60 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert torch.equal(out.loss, w.loss) and torch.equal(out.grad, w.grad)
 
+def test_calls_for_few_tokens_on_several_streams_and_in_graphs():
+    """Calls for few tokens end by a counter that the library keeps for the
+    stream; captured ones by their workspace's.  Interleaved, each is right."""
+    cases = []
+    for tokens in (1, 7, 200, 512, 513):
+        x, y = make(tokens, 300, BF16, tokens, ignore=(0,) if tokens > 1 else ())
+        adv = per_token(tokens, 1)
+        n = o.policy(f64(x), y.cpu().numpy(), f64(adv))
+        cases.append((x, y, adv, n))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs = []
+    for x, y, adv, n in cases[:4]:
+        meo.policy_loss(x, y, adv)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = meo.policy_loss(x, y, adv)
+        graphs.append((g, out, n))
+    torch.cuda.synchronize()
+    got = []
+    for k in range(30):
+        x, y, adv, n = cases[k % 5]
+        got.append((meo.policy_loss(x, y, adv, stream=streams[k % 3]).loss, n))
+        if k % 4 == 0:
+            g, out, n = graphs[k // 4 % 4]
+            with torch.cuda.stream(streams[(k + 1) % 3]):
+                g.replay()
+    torch.cuda.synchronize()
+    for loss, n in got + [(out.loss, n) for _, out, n in graphs]:
+        check("loss", f64(loss), n[0], 2e-6 * np.mean(np.abs(n[1])))
+
+
+def test_a_copy_that_never_lands_ends_the_call():
+    """Every wait in the kernel is bounded: with the copies expected but not
+    made the call ends, the loss says so, and the next call is right."""
+    from memory_efficient_optimizer_gb300 import binding as B
+    for tokens, vocab in ((3, 1000), (3, 128256), (600, 5000)):
+        x, y = make(tokens, vocab, BF16, 4)
+        adv = per_token(tokens, 1)
+        ids, t = distill_inputs(tokens, vocab, 8, 3)
+        calls = [lambda: meo.policy_loss(x, y, adv), lambda: meo.distill_loss(x, ids, t)]
+        want = [c() for c in calls]
+        for c, w in zip(calls, want):
+            torch.cuda.synchronize()
+            B.loss_debug_stall_copies(True)
+            try:
+                out = c()
+            finally:
+                B.loss_debug_stall_copies(False)
+            torch.cuda.synchronize()
+            assert out.loss.isnan()
+            again = c()
+            assert torch.equal(again.loss, w.loss) and torch.equal(again.grad, w.grad)
+
 
 def test_front_end_refusals():
     x, y = make(4, 10, BF16)
