@@ -8,6 +8,8 @@
 //
 //   k_loss_count    number of counted tokens, the denominator of the mean
 //   k_loss_row      one row: m, s, the operator's scalars, the gradient row
+//   k_loss_short    the same where a warp keeps a row
+//   k_loss_forward  m, s and the target's log-probability of a row
 //   k_loss_grad     gradient rows from kept m, s and the tokens' coefficients
 //   k_loss_pair     a pair's sums over tokens, its loss and its coefficients
 #include <cuda_bf16.h>
@@ -403,10 +405,10 @@ struct GradRow {
     }
   }
   // The part of the row that CTA `rank` of `ranks` has, as zeros.
-  __device__ __forceinline__ void zero(int rank, int ranks, int threads) const {
+  __device__ __forceinline__ void zero(int rank, int ranks, int threads, int thread) const {
     const int vecs = (lead + n + kN<T> - 1) / kN<T>, per = (vecs + ranks - 1) / ranks;
     const int last = min(vecs, (rank + 1) * per);
-    for (int i = rank * per + threadIdx.x; i < last; i += threads) {
+    for (int i = rank * per + thread; i < last; i += threads) {
       const int e0 = i * kN<T> - lead;
       if (e0 >= 0 && e0 + kN<T> <= n) {
         __stcs(reinterpret_cast<uint4*>(g + e0), make_uint4(0, 0, 0, 0));
@@ -708,6 +710,91 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
   }
 }
 
+// What the gradient needs: scale 2^(x c - R) with R of m, `more` at the target;
+// for a list, lead (on 2^(x c - R) - p) at its words.
+struct RowScale {
+  float m, scale, more, lead, on;
+};
+// A token's own values.
+struct Values {
+  int row, y;
+  bool live;
+  PolicyIn in;
+  float weight, x_at;
+};
+// The row's scalars from its sum (of the words not listed) and, for a list, the
+// listed words' (`top`).  `loss` of a policy is done; of a list it is what
+// list_loss() makes of the row.
+template <int OP>
+__device__ __forceinline__ RowScale row_scale(const LossArgs& a, const Values& v, const List& list, const Ref& ref, float sum,
+                                              float top, float wrong, float w, float& logp, float& loss) {
+  RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f};
+  if (OP != kDistill) {
+    logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+    const Token t = policy_token(a, logp, v.in);
+    loss = t.loss;
+    out.more = w * a.gscale * a.inv_t * t.d;
+    out.scale = __fdividef(-out.more, sum);
+  } else {
+    // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
+    const float rest = list.head[1];
+    out.lead = w * a.gscale / a.inv_t + wrong;
+    out.on = (list.head[0] + rest) / (sum + top);
+    out.scale = out.lead * (out.on - (rest > 0.f ? rest / sum : 0.f));
+  }
+  return out;
+}
+// By a whole warp.
+__device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, const Ref& ref, float sum, float top, float wrong) {
+  const float log_s = logf(sum + top), rest = list.head[1], d = ref.residue(a.c) * kLn2;
+  float loss = 0.f;
+  for (int k = threadIdx.x & 31; k < a.top_k; k += 32) {
+    const float p = list.p[k];
+    if (p != 0.f) loss += p * (logf(p) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
+  }
+  loss = warp_sum(loss);
+  if (rest > 0.f) loss += rest * (logf(rest) - (logf(sum) - log_s));
+  return loss / (a.inv_t * a.inv_t) + wrong;
+}
+__device__ __forceinline__ float list_terms(const LossArgs& a, const List& list, const Ref& ref) {
+  float top = 0.f;
+  for (int k = threadIdx.x & 31; k < a.top_k; k += 32) top += list.id[k] < 0 ? 0.f : ex2(ref.exponent(list.x[k], a.c));
+  return warp_sum(top);
+}
+// The loss from `n` parts, by the warp that adds the last: in a fixed order.
+__device__ __forceinline__ void add_part(const LossArgs& a, int part, int n, const Sum& share, int n_counted) {
+  const int lane = threadIdx.x & 31;
+  int last = 0;
+  if (lane == 0) {
+    a.part[part] = share;
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(n - 1);
+  }
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
+  __threadfence();
+  Sum sum;
+  for (int k = lane; k < n; k += 32) {
+    const float2 o = __ldcg(reinterpret_cast<const float2*>(a.part) + k);
+    Sum p;
+    p.s = o.x;
+    p.rest = o.y;
+    sum.add(p);
+  }
+  sum.over_warp();
+  if (lane == 0) {
+    const float c = a.weights.p == nullptr ? static_cast<float>(n_counted) : 1.f;
+    *a.loss = c > 0.f ? sum.total() / c : 0.f;
+    if (a.count == nullptr) *a.ticket = 0;  // for the stream's next call
+  }
+}
+// Counted tokens, by a warp that has them from no other kernel.
+__device__ __forceinline__ int count_tokens(const LossArgs& a, int op) {
+  int n = 0;
+#pragma unroll 4
+  for (int t = threadIdx.x & 31; t < a.tokens; t += 32) n += counted(a, op, t / a.seq, t % a.seq);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
 // ---- rows: the sum and the gradient in one read ---------------------------------
 // A row of the walk, as the managing warp tells it to the others.
 struct RowInfo {
@@ -716,12 +803,6 @@ struct RowInfo {
   int32_t y;                // the target, kNoValue without one
   int32_t ignored, n_ignored;  // rows before it (every `stride`) whose gradient is 0
 };
-// What the gradient needs: scale 2^(x c - R) with R of m, `more` at the target;
-// for a list, lead (on 2^(x c - R) - p) at its words.
-struct RowScale {
-  float m, scale, more, lead, on;
-};
-
 // The rows first, first + stride, .. of a cluster, 32 at a time: a lane looks
 // one up, and its per-token values with it, so that none of them is waited for
 // row by row.
@@ -855,12 +936,6 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
   } else if (warp == warps) {
     // The manager.
     Walk<T, OP> walk(a, first, stride);
-    struct Values {
-      int row, y;
-      bool live;
-      PolicyIn in;
-      float weight, x_at;
-    };
     int told = 0;
     auto tell_next = [&] {
       RowInfo i;
@@ -896,9 +971,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     int n_counted = 0;
     bool waited = false;
     if (a.count == nullptr) {
-#pragma unroll 4
-      for (int t = lane; t < a.tokens; t += 32) n_counted += counted(a, OP, t / a.seq, t % a.seq);
-      n_counted = __reduce_add_sync(0xffffffffu, n_counted);
+      n_counted = count_tokens(a, OP);
       waited = true;
     }
     // The counting kernel's result and its clearing of the ticket.
@@ -925,11 +998,9 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
         sum += o.y * ref.factor(o.x, a.c);
         wrong += o.w;
       }
-      if (kLists)
-        for (int k = lane; k < a.top_k; k += 32) top += list.id[k] < 0 ? 0.f : ex2(ref.exponent(list.x[k], a.c));
       sum = warp_sum(sum);
       if (kLists) {
-        top = warp_sum(top);
+        top = list_terms(a, list, ref);
         wrong = warp_sum(wrong);
       }
       if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
@@ -938,38 +1009,15 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
 
       wait_for_count();
       const float w = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
-      RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f};
       float logp = 0.f, loss = 0.f;
-      const float d = ref.residue(a.c) * kLn2;
-      if (!kLists) {
-        logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + d + wrong;
-        const Token t = policy_token(a, logp, v.in);
-        loss = t.loss;
-        out.more = w * a.gscale * a.inv_t * t.d;
-        out.scale = __fdividef(-out.more, sum);
-      } else {
-        // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
-        const float rest = list.head[1];
-        out.lead = w * a.gscale / a.inv_t + wrong;
-        out.on = (list.head[0] + rest) / (sum + top);
-        out.scale = out.lead * (out.on - (rest > 0.f ? rest / sum : 0.f));
-      }
+      const RowScale out = row_scale<OP>(a, v, list, ref, sum, top, wrong, w, logp, loss);
       if (lane == 0) {
         scales[q & 1] = out;
         arrive(scale_full + (q & 1));
       }
       __syncwarp();
       // The others make the gradient from here on.
-      if (kLists && rank == 0) {
-        const float log_s = logf(sum + top), rest = list.head[1];
-        for (int k = lane; k < a.top_k; k += 32) {
-          const float pk = list.p[k];
-          if (pk != 0.f) loss += pk * (logf(pk) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
-        }
-        loss = warp_sum(loss);
-        if (rest > 0.f) loss += rest * (logf(rest) - (logf(sum) - log_s));
-        loss = loss / (a.inv_t * a.inv_t) + wrong;
-      }
+      if (kLists && rank == 0) loss = list_loss(a, list, ref, sum, top, wrong);
       if (rank == 0) {
         if (lane == 0 && a.logp != nullptr) a.logp[v.row] = logp;
         if (lane == 0 && a.token_loss != nullptr) a.token_loss[v.row] = loss;
@@ -987,29 +1035,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     // The clusters' shares: the last to come sums them all, in order.
     if (rank == 0) {
       wait_for_count();
-      int last = 0;
-      if (lane == 0) {
-        a.part[first] = share;
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(stride - 1);
-      }
-      if (__shfl_sync(0xffffffffu, last, 0)) {
-        __threadfence();
-        Sum sum;
-        for (int k = lane; k < stride; k += 32) {
-          const float2 o = __ldcg(reinterpret_cast<const float2*>(a.part) + k);
-          Sum p;
-          p.s = o.x;
-          p.rest = o.y;
-          sum.add(p);
-        }
-        sum.over_warp();
-        if (lane == 0) {
-          const float n = a.weights.p == nullptr ? static_cast<float>(n_counted) : 1.f;
-          *a.loss = n > 0.f ? sum.total() / n : 0.f;
-          if (a.count == nullptr) *a.ticket = 0;  // for the stream's next call
-        }
-      }
+      add_part(a, first, stride, share, n_counted);
     }
   } else {
     // A warp that sums.  Its chunks of a row that ends before vector `last`:
@@ -1059,7 +1085,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
       if (gradient && now.n_ignored > 0) {
         for (int k = 0; k < now.n_ignored; ++k) {
           const int row = now.ignored + k * stride, b = row / a.seq, s = row % a.seq;
-          GradRow<T>(static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, 0).zero(rank, ranks, 32 * warps);
+          GradRow<T>(static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, 0).zero(rank, ranks, 32 * warps, threadIdx.x);
         }
       }
       if (!now.live) break;
@@ -1182,9 +1208,12 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
           }
         }
         if (kLists) {
+          // The listed words' values replace those written above, once all
+          // warps have (each looking for its own among the ids instead: 421 us
+          // for 410 with 64 ids, 508 for 436 with 256).
           __syncwarp();
           if (lane == 0) arrive(&written);
-          if (!wait_phase(&written, q & 1)) dead = true;  // the listed words' values replace those written above
+          if (!wait_phase(&written, q & 1)) dead = true;
           if (dead) break;
           for (int k = threadIdx.x; k < a.top_k; k += 32 * warps) {
             const int i = list.id[k], v = (i + r.lead) / kN<T>;
@@ -1220,6 +1249,116 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     cluster_arrive();
     cluster_wait();
   }
+}
+
+// ---- short rows -------------------------------------------------------------------
+// A warp has a row and keeps it in registers; nothing is handed from warp to
+// warp.  (16384 rows of 1000 bf16 values take 33 us; k_loss_row, whose
+// rows pass through three warps and two barriers, 70.)
+constexpr int kShortVecs = 8;     // of a lane
+constexpr int kShortWarps = 8;    // of a CTA
+template <typename T, int OP>
+__global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid_constant__ LossArgs a) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  __shared__ Sum shares[kShortWarps];
+  constexpr bool kLists = OP == kDistill;
+  constexpr int kSlice = 32 * kShortVecs;
+  static_assert(kSlice % kChunk == 0, "a list's bits are by chunks");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const List list = list_at(shared + warp * (kLists ? list_bytes(kSlice, a.top_k) : 0), kSlice, a.top_k);
+  int n_counted = 0;
+  bool waited = false;
+  if (a.count == nullptr) {
+    n_counted = count_tokens(a, OP);
+    waited = true;
+  }
+  auto wait_for_count = [&] {
+    if (waited) return;
+    wait_for_previous();
+    waited = true;
+    n_counted = *a.count;
+  };
+  Sum share;
+  for (int row = static_cast<int>(blockIdx.x) * kShortWarps + warp; row < a.tokens; row += gridDim.x * kShortWarps) {
+    const int b = row / a.seq, s = row % a.seq;
+    const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
+    const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
+    // Read before it is known whether the row counts: one wait, not two.
+    uint4 w[kShortVecs];
+    load_batch<T, 32>(w, r, lane, r.vecs);
+    Values v{row, kNoValue, true, {0.f, 0.f, 0.f}, 0.f, 0.f};
+    bool live;
+    if (kLists) {
+      live = counted(a, OP, b, s);
+    } else {
+      const int64_t target = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
+      live = target != a.ignore;
+      if (live && target >= 0 && target < a.vocab) {
+        v.y = static_cast<int>(target);
+        v.x_at = widen(*r.value(v.y));
+      }
+    }
+    if (!live) {
+      if (a.g != nullptr) g.zero(0, 1, 32, lane);
+      if (lane == 0 && a.logp != nullptr) a.logp[row] = 0.f;
+      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = 0.f;
+      continue;
+    }
+    if (OP == kPolicy) {
+      v.in.adv = row_value(a.adv, b, s);
+      if (a.old.p != nullptr) v.in.old = row_value(a.old, b, s);
+      if (a.kl != 0.f) v.in.ref = row_value(a.ref, b, s);
+    }
+    if (a.weights.p != nullptr) v.weight = row_value(a.weights, b, s);
+    if (kLists) {
+      __syncwarp();
+      make_list(a, list, r, b, s, 0, r.vecs, kSlice);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kShortVecs; ++k) {
+        const uint32_t on = list.bits[k / kBatch * 32 + lane] >> (k % kBatch * 8) & 0xff;
+        if (on != 0) {
+#pragma unroll
+          for (int j = 0; j < kN<T>; ++j)
+            if (on >> j & 1) put<T>(w[k], j, sizeof(T) == 2 ? 0xff80u : 0xff800000u);
+        }
+      }
+    }
+    Part<T> part;
+    part.add(w, a.c);
+    const Ref ref(warp_max(kLists ? fmaxf(part.m, list.head[3]) : part.m), a.c);
+    const float sum = warp_sum(part.s * ref.factor(part.m, a.c));
+    const float top = kLists ? list_terms(a, list, ref) : 0.f;
+    const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(ref.m) == INFINITY ? NAN : 0.f);
+    wait_for_count();
+    const float weight = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
+    float logp = 0.f, loss = 0.f;
+    const RowScale by = row_scale<OP>(a, v, list, ref, sum, top, wrong, weight, logp, loss);
+    if (a.g != nullptr) {
+      const int y_vec = v.y >= 0 ? (v.y + r.lead) / kN<T> : kNoValue;
+      const bool plain = batch_in<32, kShortVecs>(0, r.first_whole(), r.past_whole()) && g.shift == 0 && !ref.far() && y_vec < 0;
+      store_batch<T, 32>(w, r, g, lane, r.vecs, plain, ref, a.c, by.scale, v.y, y_vec, by.more);
+      if (kLists) {
+        __syncwarp();  // the listed words' values replace those written above
+        for (int k = lane; k < a.top_k; k += 32)
+          if (list.id[k] >= 0) narrow(g.g[list.id[k]], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+      }
+    }
+    if (kLists) loss = list_loss(a, list, ref, sum, top, wrong);
+    if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
+    if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
+    share.add(a.weights.p != nullptr ? weight * loss : loss);
+  }
+  if (lane == 0) shares[warp] = share;
+  __syncthreads();
+  if (warp != 0) return;
+  wait_for_count();
+  Sum all;
+  for (int k = 0; k < kShortWarps; ++k) {
+    const Sum p = shares[k];
+    all.add(p);
+  }
+  add_part(a, blockIdx.x, gridDim.x, all, n_counted);
 }
 
 // ---- log-probabilities --------------------------------------------------------
@@ -1290,8 +1429,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_loss_forward(const __grid_con
 // ---- gradient rows from kept statistics ------------------------------------------
 // A CTA has a tile of a row; the last rows come first: of what the forward
 // pass read they are the ones most likely still in L2.
-template <typename T>
-__global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad(const __grid_constant__ LossArgs a) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_loss_grad(const __grid_constant__ LossArgs a) {
   const int row = a.tokens - 1 - static_cast<int>(blockIdx.x / a.tiles), tile = blockIdx.x % a.tiles;
   const int b = row / a.seq, s = row % a.seq;
   const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
@@ -1299,13 +1438,13 @@ __global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad
   const int64_t target = load_index(a.y.p, a.ydt, b * a.y.sb + s * a.y.ss);
   if (a.coef != nullptr) wait_for_previous();
   if (target == a.ignore) {
-    g.zero(tile, a.tiles, kGradThreads);
+    g.zero(tile, a.tiles, NT, threadIdx.x);
     return;
   }
-  const int first = tile * kGradVecs * kGradThreads + threadIdx.x;
-  const int last = min(r.vecs, (tile + 1) * kGradVecs * kGradThreads);
+  const int first = tile * kGradVecs * NT + threadIdx.x;
+  const int last = min(r.vecs, (tile + 1) * kGradVecs * NT);
   uint4 w[kGradVecs];
-  load_batch<T, kGradThreads>(w, r, first, last);
+  load_batch<T, NT>(w, r, first, last);
   const float2 st = a.stats[row];
   const float d = (a.coef != nullptr ? a.coef[row] : row_value(a.dlogp, b, s)) * a.gscale * a.inv_t;
   const bool inside = target >= 0 && target < a.vocab;
@@ -1314,9 +1453,9 @@ __global__ void __launch_bounds__(kGradThreads, 1024 / kGradThreads) k_loss_grad
   const int y = inside ? static_cast<int>(target) : kNoValue;
   const int y_vec = inside ? (y + r.lead) / kN<T> : kNoValue;
   const int lane_first = first - (threadIdx.x & 31), to_y = y_vec - lane_first;
-  const bool plain = batch_in<kGradThreads, kGradVecs>(lane_first, r.first_whole(), min(r.past_whole(), last)) && g.shift == 0 &&
-                     !ref.far() && !(to_y >= 0 && to_y < kGradVecs * kGradThreads && to_y % kGradThreads < 32);
-  store_batch<T, kGradThreads>(w, r, g, first, last, plain, ref, a.c, scale, y, y_vec, d);
+  const bool plain = batch_in<NT, kGradVecs>(lane_first, r.first_whole(), min(r.past_whole(), last)) && g.shift == 0 &&
+                     !ref.far() && !(to_y >= 0 && to_y < kGradVecs * NT && to_y % NT < 32);
+  store_batch<T, NT>(w, r, g, first, last, plain, ref, a.c, scale, y, y_vec, d);
 }
 
 // ---- a pair's loss ---------------------------------------------------------------
@@ -1559,8 +1698,8 @@ LossArgs base_args(const loss_logits& x, const loss_targets* y, const loss_grad*
   return a;
 }
 
-const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_forward", "k_loss_grad", "k_loss_pair"};
-enum Slot { kSlotCount = 0, kSlotRow, kSlotForward, kSlotGrad, kSlotPair, kNumKernels };
+const char* const kKernelNames[] = {"k_loss_count", "k_loss_row", "k_loss_short", "k_loss_forward", "k_loss_grad", "k_loss_pair"};
+enum Slot { kSlotCount = 0, kSlotRow, kSlotShort, kSlotForward, kSlotGrad, kSlotPair, kNumKernels };
 struct ProfRecord {
   int slot;
   cudaEvent_t start, stop;
@@ -1666,23 +1805,42 @@ struct Device {
   std::map<std::pair<const void*, int64_t>, int> clusters;  // that run at a time, by kernel and cut
 };
 std::map<int, Device> g_devices;
+// The current device's, with g_mu held.
+Device* current_device(cudaError_t* e) {
+  int device = 0;
+  if ((*e = cudaGetDevice(&device)) != cudaSuccess) return nullptr;
+  Device& dev = g_devices[device];
+  if (dev.sms == 0 && (*e = cudaDeviceGetAttribute(&dev.sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
+    return nullptr;
+  return &dev;
+}
 
 template <int OP>
 adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
-  int device = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  cudaError_t e = cudaSuccess;
+  int sms = 0;
   std::unique_lock<std::mutex> lock(g_mu);
-  Device& dev = g_devices[device];
-  if (dev.sms == 0 && (e = cudaDeviceGetAttribute(&dev.sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
-    return cuda_fail(e, "cudaDeviceGetAttribute");
-  sms = dev.sms;
-  const Cut cut = cut_row(a.tokens, row_vecs(a, dtype), OP == kDistill, a.top_k, sms);
-  const bool bf16 = dtype == ADAF_BFLOAT16, twice_read = cut.slots == 0;
+  Device* const dev = current_device(&e);
+  if (dev == nullptr) return cuda_fail(e, "current device");
+  sms = dev->sms;
+  const int vecs = row_vecs(a, dtype);
+  const bool bf16 = dtype == ADAF_BFLOAT16;
+  if (vecs <= 32 * kShortVecs) {
+    lock.unlock();
+    const int shared = OP == kDistill ? kShortWarps * list_bytes(32 * kShortVecs, a.top_k) : 0;
+    void (*const kernel)(LossArgs) = bf16 ? k_loss_short<__nv_bfloat16, OP> : k_loss_short<float, OP>;
+    if (shared > (48 << 10) &&
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - 1024)) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute");
+    const int grid = std::min(div_up(a.tokens, kShortWarps), 2 * sms);
+    return launch(kSlotShort, kernel, grid, 32 * kShortWarps, shared, 1, a.count != nullptr, s, a);
+  }
+  const Cut cut = cut_row(a.tokens, vecs, OP == kDistill, a.top_k, sms);
+  const bool twice_read = cut.slots == 0;
   void (*const kernel)(LossArgs) = twice_read ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
                                               : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
   const int threads = 32 * (cut.warps + (OP == kDistill ? 2 : 1));
-  int& most = dev.clusters[{reinterpret_cast<const void*>(kernel),
+  int& most = dev->clusters[{reinterpret_cast<const void*>(kernel),
                             (static_cast<int64_t>(cut.shared) << 16) + (cut.warps << 4) + cut.cluster}];
   if (most == 0) {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - 1024)) != cudaSuccess)
@@ -1712,10 +1870,22 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
 }
 adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
   const int vecs = row_vecs(a, dtype);
+  int sms = 0;
+  {
+    cudaError_t e = cudaSuccess;
+    std::lock_guard<std::mutex> lock(g_mu);
+    const Device* const dev = current_device(&e);
+    if (dev == nullptr) return cuda_fail(e, "current device");
+    sms = dev->sms;
+  }
   int64_t cluster = 1;
-  while (cluster < kMaxCluster && a.tokens * cluster < 304 && div_up(vecs, static_cast<int>(cluster)) > 512) cluster *= 2;
+  auto threads_of = [](int mine) { return mine <= 32 * kForwardBatch * 2 ? 32 : mine <= 128 * kForwardBatch * 2 ? 128 : 512; };
+  // Few rows are cut among a cluster's CTAs.  (Cutting them where that would
+  // only fill the last wave of CTAs better costs more than it gives: 999 rows
+  // of 50257 fp32 values 38 us whole, 47 cut in two.)
+  while (cluster < kMaxCluster && a.tokens * cluster < 2 * sms && div_up(vecs, static_cast<int>(cluster)) > 512) cluster *= 2;
   a.vecs_per_cta = div_up(vecs, static_cast<int>(cluster));
-  const int threads = a.vecs_per_cta <= 32 * kForwardBatch * 2 ? 32 : a.vecs_per_cta <= 128 * kForwardBatch * 2 ? 128 : 512;
+  const int threads = threads_of(a.vecs_per_cta);
   const int shared = threads / 32 * static_cast<int>(cluster * sizeof(float4));
   const bool bf16 = dtype == ADAF_BFLOAT16;
   void (*const kernel)(LossArgs) =
@@ -1725,11 +1895,17 @@ adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
   return launch(kSlotForward, kernel, a.tokens * cluster, threads, shared, static_cast<int>(cluster), false, s, a);
 }
 adaf_status launch_grad(LossArgs a, int32_t dtype, cudaStream_t s) {
-  a.tiles = div_up(row_vecs(a, dtype), kGradThreads * kGradVecs);
+  // A tile is 256 threads' or, for rows that fill no such tile, a warp's:
+  // 16384 rows of 1000 bf16 values take 61 us in CTAs of 256 threads.
+  const int vecs = row_vecs(a, dtype), threads = vecs <= 4 * 32 * kGradVecs ? 32 : kGradThreads;
+  const bool bf16 = dtype == ADAF_BFLOAT16;
+  a.tiles = div_up(vecs, threads * kGradVecs);
   const int64_t grid = static_cast<int64_t>(a.tokens) * a.tiles;
   if (grid > INT32_MAX) return fail(ADAF_ERR_UNSUPPORTED, "gradient of more than 2^31 tiles");
-  return launch(kSlotGrad, dtype == ADAF_BFLOAT16 ? k_loss_grad<__nv_bfloat16> : k_loss_grad<float>, grid, kGradThreads,
-                0, 1, a.coef != nullptr, s, a);
+  void (*const kernel)(LossArgs) =
+      threads == 32 ? (bf16 ? k_loss_grad<__nv_bfloat16, 32> : k_loss_grad<float, 32>)
+                    : (bf16 ? k_loss_grad<__nv_bfloat16, kGradThreads> : k_loss_grad<float, kGradThreads>);
+  return launch(kSlotGrad, kernel, grid, threads, 0, 1, a.coef != nullptr, s, a);
 }
 // A call for a few tokens is one launch: the managing warps count the tokens
 // themselves, and the ticket is one that the library keeps for the stream (the

@@ -133,12 +133,26 @@ def _targets(t, shape, device, ignore_index):
     return _TARGETS.pack(*_rows("targets", t, shape, device, t.dtype), code, ignore_index)
 
 
+def _is_cut(shape, st):
+    """Whole rows of sequences that are a few tokens longer."""
+    return st[1] == shape[2] and shape[1] * shape[2] < st[0] <= 2 * shape[1] * shape[2]
+
+
 def _gradient(logits, grad, need_grad, scale, device):
     """(tensor or None, packed or None) of the gradient."""
     if grad is None:
         if not need_grad:
             return None, None
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        shape, st = logits.shape, logits.stride()
+        if len(shape) == 3 and shape[0] > 1 and shape[2] * logits.element_size() % 16 and _is_cut(shape, st):
+            # Views such as logits[:, :-1] of rows that are no multiple of 16
+            # bytes: a gradient with the same strides has its rows' 16-byte
+            # boundaries where the logits' are (a contiguous one of 999 rows of
+            # 50257 fp32 values takes 71 us in the backward pass, this 59).
+            whole = torch.empty((shape[0] - 1) * st[0] + shape[1] * shape[2], dtype=logits.dtype, device=logits.device)
+            grad = whole.as_strided(shape, st)
+        else:
+            grad = torch.empty(shape, dtype=logits.dtype, device=logits.device)
     else:
         if not need_grad:
             raise ValueError("grad was given with need_grad=False")
