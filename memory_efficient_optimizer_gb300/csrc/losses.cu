@@ -870,17 +870,19 @@ struct Walk {
   }
 };
 
-// Clusters of CTAs walk the rows.  A warp copies its chunks of a row to its own
-// places of a ring in shared memory (bulk copies, one row ahead), adds up
-// their terms, and, when the cluster's parts of the row are together, makes the
-// gradient from the same copies; the places that come free take the next row's
-// chunks at once.  One more warp manages: it looks the rows up ahead of the
+// Clusters of CTAs walk the rows; a CTA has a run of a row's vectors and its
+// warps share that in rounds of a chunk each.  One warp copies rounds into a
+// ring in shared memory as places come free (bulk copies, so that the next row
+// is on its way while this one is worked on).  The warps add up their terms,
+// and, when the cluster's parts of the row are together, make the gradient from
+// the same copies.  Another warp manages: it looks the rows up ahead of the
 // others, joins the parts and works out the row's scalars, so that these cost
 // the others nothing (16 warps doing so themselves took 2300 cycles to begin a
-// row and 2500 from its sum to its gradient, of 13,500 in all).  For lists a
-// second one makes those.  LONG: rows that no cluster keeps are read twice.
+// row and 2500 from its sum to its gradient, of 13,500 in all).  For lists
+// there is one more, which makes those.  LONG: rows that no cluster keeps are
+// read twice, from global memory.
 template <typename T, int OP, bool LONG>
-__global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 32, 2)
+__global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 32, 2)
     k_loss_row(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
   __shared__ RowInfo info[3];
@@ -888,14 +890,16 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
   __shared__ uint64_t together[2], info_full[3], scale_full[2], list_full[2], list_free[2], written;
   constexpr bool kLists = OP == kDistill;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = (blockDim.x >> 5) - (kLists ? 2 : 1);  // that sum
+  const int warps = (blockDim.x >> 5) - (kLists ? 3 : 2);  // that sum
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int first = static_cast<int>(blockIdx.x) / ranks, stride = static_cast<int>(gridDim.x) / ranks;
   const int v0 = rank * a.vecs_per_cta, slots = a.slots;
-  uint4* const ring = reinterpret_cast<uint4*>(shared) + (LONG ? 0 : warp * slots * kChunk);  // a warp's [slots][kChunk]
-  float4* const parts = reinterpret_cast<float4*>(shared) + (LONG ? 0 : warps * slots * kChunk);  // [2][warps of the cluster]
-  uint64_t* const full = reinterpret_cast<uint64_t*>(parts + 2 * warps * ranks) + warp * slots;  // a warp's [slots]
-  unsigned char* const lists = reinterpret_cast<unsigned char*>(parts + 2 * warps * ranks) + (LONG ? 0 : (warps * slots * 8 + 15) / 16 * 16);
+  const int round = warps * kChunk;                                  // vectors
+  uint4* const ring = reinterpret_cast<uint4*>(shared);              // [slots][round]
+  float4* const parts = reinterpret_cast<float4*>(shared) + slots * round;  // [2][warps of the cluster]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(parts + 2 * warps * ranks);  // [slots]
+  uint64_t* const empty = full + slots;                              // [slots]
+  unsigned char* const lists = reinterpret_cast<unsigned char*>(empty + slots);
   const int slice = a.vecs_per_cta, list_size = list_bytes(slice, a.top_k);
   // Bytes that a row's parts are; the manager expects the next but one row's
   // as soon as a row's are there, and only then its scalars let anybody go on.
@@ -911,8 +915,10 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     for (int k = 0; k < 3; ++k) init_barrier(info_full + k, 1);
     init_barrier(&written, warps);
   }
-  if (!LONG && warp < warps && lane == 0)
-    for (int k = 0; k < slots; ++k) init_barrier(full + k, 1);
+  if (threadIdx.x < slots) {
+    init_barrier(full + threadIdx.x, 1);
+    init_barrier(empty + threadIdx.x, warps);
+  }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __syncthreads();
   if (ranks > 1) {  // shared memory of the others may be written once they have all begun
@@ -920,8 +926,48 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
     cluster_wait();
   }
   bool dead = false;  // a wait ran out: no more waiting, the loss is NaN
+  // The granule of 16 bytes at a row's end may hold bytes of its neighbour; at
+  // the tensor's own ends it may reach outside, and is then read value by value.
+  auto copied_from = [&](const Row<T>& r) { return r.base < a.x_begin ? 1 : 0; };
+  auto copied_to = [&](const Row<T>& r) { return r.base + 16 * static_cast<int64_t>(r.vecs) > a.x_end ? r.vecs - 1 : r.vecs; };
 
-  if (kLists && warp == warps + 1) {
+  if (warp == warps + 1) {
+    // The warp that copies.
+    if (!LONG) {
+      Walk<T, OP> walk(a, first, stride);
+      int place = 0, none, n_none, copies = 0;
+      uint32_t parity = 1;  // of the place's last reading; the first waits return at once
+      for (int at = walk.next(false, false, none, n_none); at >= 0 && !dead; at = walk.next(false, false, none, n_none)) {
+        const int row = walk.base + at * stride, b = row / a.seq, s = row % a.seq;
+        const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
+        const int v1 = min(r.vecs, v0 + a.vecs_per_cta), lo = copied_from(r), hi = min(copied_to(r), v1);
+        for (int i = v0; i < v1; i += round) {
+          if (!wait_phase(empty + place, parity)) {
+            dead = true;
+            break;
+          }
+          if (lane == 0) {
+            const int i0 = max(i, lo), n = min(i + round, hi) - i0;
+            copy_bulk(ring + place * round + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + place,
+                      a.stall != 0);
+          }
+          ++copies;
+          if (++place == slots) {
+            place = 0;
+            parity ^= 1;
+          }
+        }
+      }
+      // The last copies land before the CTA's memory is given up.
+      for (int k = min(copies, slots); k > 0; --k) {
+        if (--place < 0) {
+          place = slots - 1;
+          parity ^= 1;
+        }
+        if (!wait_phase(full + place, parity ^ 1)) break;
+      }
+    }
+  } else if (kLists && warp == warps + 2) {
     // The warp that makes the lists, up to two rows ahead.
     Walk<T, OP> walk(a, first, stride);
     int q = 0, none, n_none;
@@ -1038,50 +1084,20 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
       add_part(a, first, stride, share, n_counted);
     }
   } else {
-    // A warp that sums.  Its chunks of a row that ends before vector `last`:
-    // chunk q starts at vector `mine` + q * between.
-    const int mine = v0 + warp * kChunk, between = warps * kChunk;
-    auto chunks = [&](const Row<T>& r) {
-      const int last = min(r.vecs, v0 + a.vecs_per_cta);
-      return last <= mine ? 0 : (last - mine - 1) / between + 1;
-    };
-    // The granule of 16 bytes at a row's end may hold bytes of its neighbour; at
-    // the tensor's own ends it may reach outside, and is then read value by value.
-    auto copied_from = [&](const Row<T>& r) { return r.base < a.x_begin ? 1 : 0; };
-    auto copied_to = [&](const Row<T>& r) { return r.base + 16 * static_cast<int64_t>(r.vecs) > a.x_end ? r.vecs - 1 : r.vecs; };
-    int fill = 0;  // the place of the ring that the next chunk goes to
-    // Copies chunks [from, to) of a row.
-    auto copy = [&](const Row<T>& r, int from, int to) {
-      for (int q = from; q < to; ++q) {
-        if (lane == 0) {
-          const int i = mine + q * between, i0 = max(i, copied_from(r));
-          const int n = min(i + kChunk, min(copied_to(r), v0 + a.vecs_per_cta)) - i0;
-          copy_bulk(ring + fill * kChunk + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + fill,
-                    a.stall != 0);
-        }
-        if (++fill == slots) fill = 0;
-      }
-    };
+    // A warp that sums: in a round, chunk `mine` + k round.
+    const int mine = v0 + warp * kChunk;
     const bool gradient = a.g != nullptr;
     int told = 0, told_parity = 0;
-    auto next_info = [&] {
-      if (!wait_phase(info_full + told, told_parity)) dead = true;
-      RowInfo i = info[told];
-      if (dead) i.live = i.n_ignored = 0;
+    // The ring's place of the row's first round and the parity of its barrier.
+    int base = 0;
+    uint32_t parity = 0;
+    for (int q = 0;; ++q) {
+      if (!wait_phase(info_full + told, told_parity)) break;
+      const RowInfo now = info[told];
       if (++told == 3) {
         told = 0;
         told_parity ^= 1;
       }
-      return i;
-    };
-    RowInfo now = next_info();
-    Row<T> r(reinterpret_cast<const T*>(now.x), a.vocab);
-    // The row's chunks, the ring's place of its first and the parity of that
-    // one's barrier.
-    int n_chunks = now.live ? chunks(r) : 0, base = 0;
-    uint32_t parity = 0;
-    if (!LONG) copy(r, 0, n_chunks);
-    for (int q = 0;; ++q) {
       if (gradient && now.n_ignored > 0) {
         for (int k = 0; k < now.n_ignored; ++k) {
           const int row = now.ignored + k * stride, b = row / a.seq, s = row % a.seq;
@@ -1089,39 +1105,25 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
         }
       }
       if (!now.live) break;
-      const RowInfo then = next_info();
-      if (dead) break;
-      const Row<T> r1(reinterpret_cast<const T*>(then.x), a.vocab);
-      const int n_chunks1 = then.live ? chunks(r1) : 0;
-      const int early1 = min(n_chunks1, slots - n_chunks);  // what there is room for before this row's places come free
-      if (!LONG) {
-        if (kLists) writes_before_copies();
-        __syncwarp();  // the row before has been read
-        copy(r1, 0, early1);
-      }
+      const Row<T> r(reinterpret_cast<const T*>(now.x), a.vocab);
       const List list = list_at(lists + (q & 1) * list_size, slice, a.top_k);
-      if (kLists && !wait_phase(list_full + (q & 1), q >> 1 & 1)) dead = true;
-      if (dead) break;
+      if (kLists && !wait_phase(list_full + (q & 1), q >> 1 & 1)) break;
 
       // The warp's terms.
       const int v1 = min(r.vecs, v0 + a.vecs_per_cta), lo = r.first_whole(), hi = min(r.past_whole(), v1);
       Part<T> part;
       int place = base;
       uint32_t phase = parity;
-      for (int q2 = 0; q2 < n_chunks; ++q2) {
-        const int i = mine + q2 * between + lane;
-        uint4* const from = ring + place * kChunk + lane;
+      for (int i = mine + lane, i0 = v0; i0 < v1; i += round, i0 += round) {
+        uint4* const from = ring + place * round + warp * kChunk + lane;
         if (!LONG && !wait_phase(full + place, phase)) {
           dead = true;
           break;
         }
-        if (++place == slots) {
-          place = 0;
-          phase ^= 1;
-        }
         // The listed words leave the copy: their terms are summed apart, and
         // their gradients written after the others'.
-        Bits on = kLists ? list.bits[(q2 * warps + warp) * 32 + lane] : 0;
+        const int chunk = (i - lane - v0) / kChunk;
+        Bits on = kLists && i - lane < v1 ? list.bits[chunk * 32 + lane] : 0;
         if (!LONG) {
           for (; on != 0; on &= on - 1) {
             const int bit = __ffs(static_cast<int>(on)) - 1;
@@ -1141,7 +1143,7 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
             uint4 w[1] = {no_values(kNegInf<T>)};
             if (LONG || e < copied_from(r) || e >= copied_to(r)) {
               w[0] = load_vec(r, e, v1);
-              const uint32_t out = kLists ? static_cast<uint32_t>(list.bits[(q2 * warps + warp) * 32 + lane] >> (8 * k)) : 0;
+              const uint32_t out = kLists ? list.bits[chunk * 32 + lane] >> (8 * k) : 0;
 #pragma unroll
               for (int j = 0; j < kN<T>; ++j)
                 if (kLists && (out >> j & 1)) put<T>(w[0], j, sizeof(T) == 2 ? 0xff80u : 0xff800000u);
@@ -1152,8 +1154,18 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
             part.add(w, a.c);
           }
         }
+        if (!LONG) {
+          if (!gradient) {
+            if (kLists) writes_before_copies();
+            __syncwarp();  // the place has been read
+            if (lane == 0) arrive(empty + place);
+          }
+          if (++place == slots) {
+            place = 0;
+            phase ^= 1;
+          }
+        }
       }
-
       if (dead) break;
 
       // The warp's part, to every CTA of the cluster.
@@ -1169,26 +1181,23 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
         here[warp] = p;
         arrive(together + (q & 1));
       }
-      if (!wait_phase(scale_full + (q & 1), q >> 1 & 1)) dead = true;
-      if (dead) break;
+      if (!wait_phase(scale_full + (q & 1), q >> 1 & 1)) break;
       const RowScale by = scales[q & 1];
       const Ref ref(by.m, a.c);
 
-      // The gradient, and the next row's chunks into the places that come free.
       if (gradient) {
         const GradRow<T> g(reinterpret_cast<T*>(now.g), a.vocab, r.lead);
         const bool near = g.shift == 0 && !ref.far();
         const int y_vec = now.y >= 0 ? (now.y + r.lead) / kN<T> : kNoValue;
         place = base;
-        for (int q2 = 0; q2 < n_chunks; ++q2) {
-          const int i = mine + q2 * between + lane;
+        for (int i = mine + lane, i0 = v0; i0 < v1; i += round, i0 += round) {
           uint4 v[kBatch];
           const bool plain = batch_in<32>(i - lane, lo, hi);
           if (LONG) {
             load_batch<T, 32>(v, r, i, v1);
           } else {
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) v[k] = ring[place * kChunk + k * 32 + lane];  // past the slice: not stored
+            for (int k = 0; k < kBatch; ++k) v[k] = ring[place * round + warp * kChunk + k * 32 + lane];  // past the slice: not stored
             if (!plain) {
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) {
@@ -1196,16 +1205,13 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
                 if (e < v1 && (e < copied_from(r) || e >= copied_to(r))) v[k] = load_vec(r, e, v1);
               }
             }
-          }
-          if (++place == slots) place = 0;
-          store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c,
-                             by.scale, now.y, y_vec, by.more);
-          const int q3 = q2 + slots - n_chunks;
-          if (!LONG && q3 >= early1 && q3 < n_chunks1) {
             if (kLists) writes_before_copies();
             __syncwarp();  // the place has been read
-            copy(r1, q3, q3 + 1);
+            if (lane == 0) arrive(empty + place);
+            if (++place == slots) place = 0;
           }
+          store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c,
+                             by.scale, now.y, y_vec, by.more);
         }
         if (kLists) {
           // The listed words' values replace those written above, once all
@@ -1213,36 +1219,26 @@ __global__ void __launch_bounds__((kMaxWarps + 1 + (OP == kDistill ? 1 : 0)) * 3
           // for 410 with 64 ids, 508 for 436 with 256).
           __syncwarp();
           if (lane == 0) arrive(&written);
-          if (!wait_phase(&written, q & 1)) dead = true;
-          if (dead) break;
+          if (!wait_phase(&written, q & 1)) break;
           for (int k = threadIdx.x; k < a.top_k; k += 32 * warps) {
             const int i = list.id[k], v = (i + r.lead) / kN<T>;
             if (i >= 0 && v >= v0 && v < v1)
               narrow(g.g[i], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
           }
         }
-      } else if (!LONG) {
-        if (kLists) writes_before_copies();
-        __syncwarp();
-        copy(r1, early1, n_chunks1);
       }
       if (kLists) {
         __syncwarp();
         if (lane == 0) arrive(list_free + (q & 1));
       }
-      base += n_chunks;
-      if (base >= slots) {
-        base -= slots;
-        parity ^= 1;
+      if (!LONG) {
+        base += max(0, v1 - v0 + round - 1) / round;
+        if (base >= slots) {
+          base -= slots;
+          parity ^= 1;
+        }
       }
-      n_chunks = n_chunks1;
-      r = r1;
-      now = then;
     }
-    // Copies still in flight land before the CTA's memory is given up.
-    if (dead)
-      for (int k = 0; k < slots; ++k)
-        if (!wait_phase(full + k, k < base ? parity : parity ^ 1)) break;
   }
   if (ranks > 1) {  // nobody leaves while others may write here
     __syncwarp();
@@ -1782,14 +1778,14 @@ Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
     c.warps = std::min(kMaxWarps, div_up(mine, keep));
     const int n = div_up(mine, c.warps);
     c.shared = 2 * c.warps * cluster * static_cast<int>(sizeof(float4)) + (lists ? 2 * list_bytes(c.vecs_per_cta, top_k) : 0);
-    const int place = kChunk * 16 + 8;  // and its barrier
+    const int place = c.warps * kChunk * 16 + 16;  // and its two barriers
     for (int ctas = 2 * kMaxWarps / c.warps; ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs of an SM
       const int room = kSharedBytes / ctas - 1024 - 512 - c.shared;
-      c.slots = std::min(2 * n, std::max(0, room / (c.warps * place)));
+      c.slots = std::min(2 * n, std::max(0, room / place));
       if (c.slots > n) break;
     }
     if (c.slots < n) c.slots = 0;
-    c.shared += c.warps * c.slots * kChunk * 16 + div_up(c.warps * c.slots * 8, 16) * 16;
+    c.shared += c.slots * place;
   };
   int cluster = 1;
   set(1, kKeep);
@@ -1839,7 +1835,7 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   const bool twice_read = cut.slots == 0;
   void (*const kernel)(LossArgs) = twice_read ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
                                               : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
-  const int threads = 32 * (cut.warps + (OP == kDistill ? 2 : 1));
+  const int threads = 32 * (cut.warps + (OP == kDistill ? 3 : 2));
   int& most = dev->clusters[{reinterpret_cast<const void*>(kernel),
                             (static_cast<int64_t>(cut.shared) << 16) + (cut.warps << 4) + cut.cluster}];
   if (most == 0) {
