@@ -8,7 +8,7 @@
 //
 //   k_loss_count    number of counted tokens, the denominator of the mean
 //   k_loss_row      one row: m, s, the operator's scalars, the gradient row
-//   k_loss_short    the same where a warp keeps a row
+//   k_loss_short    the same where a few warps keep a row
 //   k_loss_forward  m, s and the target's log-probability of a row
 //   k_loss_grad     gradient rows from kept m, s and the tokens' coefficients
 //   k_loss_pair     a pair's sums over tokens, its loss and its coefficients
@@ -1125,11 +1125,13 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
         const int chunk = (i - lane - v0) / kChunk;
         Bits on = kLists && i - lane < v1 ? list.bits[chunk * 32 + lane] : 0;
         if (!LONG) {
+          const bool some = on != 0;
           for (; on != 0; on &= on - 1) {
             const int bit = __ffs(static_cast<int>(on)) - 1;
             T* const x = reinterpret_cast<T*>(from + bit / 8 * 32) + bit % 8;
             narrow(*x, -INFINITY);
           }
+          if (some) writes_before_copies();
         }
         if (batch_in<32>(i - lane, lo, hi) && !(LONG && kLists)) {
           uint4 w[kBatch];
@@ -1156,7 +1158,6 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
         }
         if (!LONG) {
           if (!gradient) {
-            if (kLists) writes_before_copies();
             __syncwarp();  // the place has been read
             if (lane == 0) arrive(empty + place);
           }
@@ -1205,7 +1206,6 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
                 if (e < v1 && (e < copied_from(r) || e >= copied_to(r))) v[k] = load_vec(r, e, v1);
               }
             }
-            if (kLists) writes_before_copies();
             __syncwarp();  // the place has been read
             if (lane == 0) arrive(empty + place);
             if (++place == slots) place = 0;
@@ -1248,20 +1248,28 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
 }
 
 // ---- short rows -------------------------------------------------------------------
-// A warp has a row and keeps it in registers; nothing is handed from warp to
-// warp.  (16384 rows of 1000 bf16 values take 33 us; k_loss_row, whose
-// rows pass through three warps and two barriers, 70.)
+// TEAM warps have a row and keep it in registers.  Nothing is handed to other
+// warps but the team's parts: 16384 rows of 1000 bf16 values take 33 us, 70 in
+// k_loss_row, whose rows pass through three warps and two barriers; 4096 rows
+// of 8192 37 us for 45.  Teams of eight no longer gain: 4096 rows of 12000 63 us
+// for 59, with a teacher's 64 entries of 16000 88 us for 73.
 constexpr int kShortVecs = 8;     // of a lane
 constexpr int kShortWarps = 8;    // of a CTA
-template <typename T, int OP>
+constexpr int kMaxTeam = 4;
+template <typename T, int OP, int TEAM>
 __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
   __shared__ Sum shares[kShortWarps];
+  __shared__ float2 parts[2][kShortWarps];
   constexpr bool kLists = OP == kDistill;
-  constexpr int kSlice = 32 * kShortVecs;
-  static_assert(kSlice % kChunk == 0, "a list's bits are by chunks");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const List list = list_at(shared + warp * (kLists ? list_bytes(kSlice, a.top_k) : 0), kSlice, a.top_k);
+  constexpr int kOwn = 32 * kShortVecs, kSlice = kOwn * TEAM, kTeams = kShortWarps / TEAM;
+  static_assert(kOwn % kChunk == 0, "a list's bits are by chunks");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / TEAM, member = warp % TEAM;
+  auto team_sync = [&] {
+    if (TEAM == 1) __syncwarp();
+    else asm volatile("barrier.sync.aligned %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
+  };
+  const List list = list_at(shared + team * (kLists ? list_bytes(kSlice, a.top_k) : 0), kSlice, a.top_k);
   int n_counted = 0;
   bool waited = false;
   if (a.count == nullptr) {
@@ -1275,13 +1283,15 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     n_counted = *a.count;
   };
   Sum share;
-  for (int row = static_cast<int>(blockIdx.x) * kShortWarps + warp; row < a.tokens; row += gridDim.x * kShortWarps) {
+  int q = 0;
+  for (int row = static_cast<int>(blockIdx.x) * kTeams + team; row < a.tokens; row += gridDim.x * kTeams) {
     const int b = row / a.seq, s = row % a.seq;
     const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
     const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
+    const int first = member * kOwn + lane;
     // Read before it is known whether the row counts: one wait, not two.
     uint4 w[kShortVecs];
-    load_batch<T, 32>(w, r, lane, r.vecs);
+    load_batch<T, 32>(w, r, first, r.vecs);
     Values v{row, kNoValue, true, {0.f, 0.f, 0.f}, 0.f, 0.f};
     bool live;
     if (kLists) {
@@ -1295,9 +1305,11 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
       }
     }
     if (!live) {
-      if (a.g != nullptr) g.zero(0, 1, 32, lane);
-      if (lane == 0 && a.logp != nullptr) a.logp[row] = 0.f;
-      if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = 0.f;
+      if (a.g != nullptr) g.zero(member, TEAM, 32, lane);
+      if (member == 0 && lane == 0) {
+        if (a.logp != nullptr) a.logp[row] = 0.f;
+        if (a.token_loss != nullptr) a.token_loss[row] = 0.f;
+      }
       continue;
     }
     if (OP == kPolicy) {
@@ -1307,12 +1319,12 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     }
     if (a.weights.p != nullptr) v.weight = row_value(a.weights, b, s);
     if (kLists) {
-      __syncwarp();
-      make_list(a, list, r, b, s, 0, r.vecs, kSlice);
-      __syncwarp();
+      team_sync();  // the list before has been read
+      if (member == 0) make_list(a, list, r, b, s, 0, r.vecs, kSlice);
+      team_sync();
 #pragma unroll
       for (int k = 0; k < kShortVecs; ++k) {
-        const uint32_t on = list.bits[k / kBatch * 32 + lane] >> (k % kBatch * 8) & 0xff;
+        const uint32_t on = list.bits[(member * (kOwn / kChunk) + k / kBatch) * 32 + lane] >> (k % kBatch * 8) & 0xff;
         if (on != 0) {
 #pragma unroll
           for (int j = 0; j < kN<T>; ++j)
@@ -1322,24 +1334,45 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     }
     Part<T> part;
     part.add(w, a.c);
-    const Ref ref(warp_max(kLists ? fmaxf(part.m, list.head[3]) : part.m), a.c);
-    const float sum = warp_sum(part.s * ref.factor(part.m, a.c));
+    // (the target's logit, and a list's, are read before anything is written)
+    float m = warp_max(part.m);
+    float sum = warp_sum(part.s * Ref(m, a.c).factor(part.m, a.c));
+    if (TEAM > 1) {
+      if (lane == 0) parts[q & 1][warp] = make_float2(m, sum);
+      team_sync();
+      const float2* const here = parts[q & 1] + team * TEAM;
+      for (int k = 0; k < TEAM; ++k) m = fmaxf(m, here[k].x);
+      if (kLists) m = fmaxf(m, list.head[3]);
+      sum = 0.f;
+      for (int k = 0; k < TEAM; ++k) sum += here[k].y * Ref(m, a.c).factor(here[k].x, a.c);
+    } else if (kLists) {
+      const float m2 = fmaxf(m, list.head[3]);
+      sum *= Ref(m2, a.c).factor(m, a.c);
+      m = m2;
+    }
+    ++q;
+    const Ref ref(m, a.c);
     const float top = kLists ? list_terms(a, list, ref) : 0.f;
-    const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(ref.m) == INFINITY ? NAN : 0.f);
+    const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(m) == INFINITY ? NAN : 0.f);
     wait_for_count();
     const float weight = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
     float logp = 0.f, loss = 0.f;
     const RowScale by = row_scale<OP>(a, v, list, ref, sum, top, wrong, weight, logp, loss);
     if (a.g != nullptr) {
       const int y_vec = v.y >= 0 ? (v.y + r.lead) / kN<T> : kNoValue;
-      const bool plain = batch_in<32, kShortVecs>(0, r.first_whole(), r.past_whole()) && g.shift == 0 && !ref.far() && y_vec < 0;
-      store_batch<T, 32>(w, r, g, lane, r.vecs, plain, ref, a.c, by.scale, v.y, y_vec, by.more);
+      const bool plain = batch_in<32, kShortVecs>(first - lane, r.first_whole(), r.past_whole()) && g.shift == 0 && !ref.far() &&
+                         static_cast<unsigned>(y_vec - (first - lane)) >= kOwn;
+      store_batch<T, 32>(w, r, g, first, r.vecs, plain, ref, a.c, by.scale, v.y, y_vec, by.more);
       if (kLists) {
-        __syncwarp();  // the listed words' values replace those written above
-        for (int k = lane; k < a.top_k; k += 32)
-          if (list.id[k] >= 0) narrow(g.g[list.id[k]], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+        __syncwarp();  // the listed words' values replace those that this warp wrote
+        for (int k = lane; k < a.top_k; k += 32) {
+          const int i = list.id[k];
+          if (i >= 0 && (i + r.lead) / kN<T> / kOwn == member)
+            narrow(g.g[i], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+        }
       }
     }
+    if (member != 0) continue;
     if (kLists) loss = list_loss(a, list, ref, sum, top, wrong);
     if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
     if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
@@ -1821,14 +1854,19 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   sms = dev->sms;
   const int vecs = row_vecs(a, dtype);
   const bool bf16 = dtype == ADAF_BFLOAT16;
-  if (vecs <= 32 * kShortVecs) {
+  if (vecs <= 32 * kShortVecs * kMaxTeam) {
     lock.unlock();
-    const int shared = OP == kDistill ? kShortWarps * list_bytes(32 * kShortVecs, a.top_k) : 0;
-    void (*const kernel)(LossArgs) = bf16 ? k_loss_short<__nv_bfloat16, OP> : k_loss_short<float, OP>;
-    if (shared > (48 << 10) &&
+    int team = 1;
+    while (32 * kShortVecs * team < vecs) team *= 2;
+    const int teams = kShortWarps / team;
+    const int shared = OP == kDistill ? teams * list_bytes(32 * kShortVecs * team, a.top_k) : 0;
+    void (*const kernel)(LossArgs) = team == 1   ? (bf16 ? k_loss_short<__nv_bfloat16, OP, 1> : k_loss_short<float, OP, 1>)
+                                     : team == 2 ? (bf16 ? k_loss_short<__nv_bfloat16, OP, 2> : k_loss_short<float, OP, 2>)
+                                                 : (bf16 ? k_loss_short<__nv_bfloat16, OP, 4> : k_loss_short<float, OP, 4>);
+    if (shared > (48 << 10) - 512 &&
         (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - 1024)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute");
-    const int grid = std::min(div_up(a.tokens, kShortWarps), 2 * sms);
+    const int grid = std::min(div_up(a.tokens, teams), 2 * sms);
     return launch(kSlotShort, kernel, grid, 32 * kShortWarps, shared, 1, a.count != nullptr, s, a);
   }
   const Cut cut = cut_row(a.tokens, vecs, OP == kDistill, a.top_k, sms);

@@ -561,7 +561,7 @@ def test_a_copy_that_never_lands_ends_the_call():
     """Every wait in the kernel is bounded: with the copies expected but not
     made the call ends, the loss says so, and the next call is right."""
     from memory_efficient_optimizer_gb300 import binding as B
-    for tokens, vocab in ((3, 3000), (3, 128256), (600, 5000)):  # shorter rows take no copies
+    for tokens, vocab in ((3, 40000), (3, 128256), (600, 40000)):  # short rows take no copies
         x, y = make(tokens, vocab, BF16, 4)
         adv = per_token(tokens, 1)
         ids, t = distill_inputs(tokens, vocab, 8, 3)
