@@ -47,7 +47,8 @@
  * with nothing but -inf, answers NaN in its own values, and so does a row
  * whose target (or a listed teacher id) lies outside the vocabulary, and one
  * whose teacher lists an id twice: bad data shows in the loss and reads or
- * writes nothing out of range.
+ * writes nothing out of range.  Of the 16 bytes that hold a row's first or last
+ * value all are read where they lie within the logits' extent.
  *
  * Logits are fp32 or bf16 and the gradient has their type; everything between
  * is fp32 (sums over tokens with compensation), and gradients are rounded
@@ -159,8 +160,9 @@ typedef struct loss_distill_args {
 adaf_status loss_workspace_size(int64_t tokens, int64_t pairs, size_t* bytes);
 
 /* logp [batch * seq] fp32 and, if not NULL, stats [batch * seq][2] fp32: the
- * row's largest logit and sum exp((x - largest) / temperature), which the
- * backward pass takes.  Stats of ignored tokens are 0. */
+ * row's largest logit and sum exp((x - largest) / temperature) as the backward
+ * pass takes them (the sum is relative to a rounded exponent, so no value to
+ * compute with).  Stats of ignored tokens are 0. */
 adaf_status loss_token_logprobs(const loss_logits* x, const loss_targets* y, float* logp, float* stats, void* stream);
 
 /* grad from the stats of the forward pass on the same logits, and grad_logp

@@ -385,6 +385,29 @@ def test_masked_words_and_lowest_values(vocab, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [5, 300, 9000, 128256])
+@pytest.mark.parametrize("tau", [1e-3, 1e-2, 1e20])
+def test_large_logits_and_far_temperatures(vocab, tau, dtype):
+    """Logits whose product with 1 / T leaves fp32: a row of equal ones, one
+    word far above the others, and two words a little apart."""
+    x = torch.full((4, vocab), 2e36, dtype=dtype).cuda()
+    x[1, 2:] = -3e38
+    x[2, 0] = 3e36
+    x[3] = 7.0 if tau < 1 else -1e38
+    y = torch.zeros(4, dtype=torch.int64).cuda()
+    adv = torch.tensor([1.0, -1.0, 2.0, 0.5]).cuda()
+    xn, yn, an = f64(x), y.cpu().numpy(), f64(adv)
+    r = meo.token_logprobs(x, y, temperature=tau)
+    check_logp(f64(r.logp), o.token_logprobs(xn, yn, tau), vocab)
+    g = meo.token_logprobs_backward(x, y, r.stats, adv, temperature=tau)
+    check_grad(f64(g), o.logprobs_grad(xn, yn, an, tau), an / tau, vocab, dtype)
+    out = meo.policy_loss(x, y, adv, temperature=tau)
+    n = o.policy(xn, yn, an, temperature=tau)
+    check_logp(f64(out.logp), n[2], vocab)
+    check_grad(f64(out.grad), n[3], n[4] / tau, vocab, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("vocab", [5, 300, 128256])
 def test_rows_without_a_distribution_answer_nan_alone(vocab, dtype):
     x, y = make(6, vocab, dtype, 3)
@@ -603,3 +626,28 @@ def test_front_end_refusals():
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [300, 40000])
+def test_parts_of_a_row_on_both_sides_of_the_exponent_forms(vocab, dtype):
+    """Logits about 65536 T / log2(e), where warps of one row take either form
+    of the exponent; half of the row is some steps lower."""
+    at = 65536 / 1.4426950408889634
+    x = torch.full((3, vocab), 0.0)
+    for k, low in enumerate((0.0, 256.0, 1.0 if dtype is FP32 else 512.0)):
+        x[k] = at + 2
+        x[k, : vocab // 2] = at + 2 - low
+    x[0, ::3] += 512
+    x, y = x.to(dtype).cuda(), torch.tensor([0, vocab - 1, 1]).cuda()
+    adv = torch.tensor([1.0, -1.0, 2.0]).cuda()
+    for tau in (1.0, 256.0):
+        z = (x.float() * (tau if tau > 1 else 1)).to(dtype)
+        n = o.policy(f64(z), y.cpu().numpy(), f64(adv), temperature=tau)
+        out = meo.policy_loss(z, y, adv, temperature=tau)
+        check_logp(f64(out.logp), n[2], vocab)
+        check_grad(f64(out.grad), n[3], n[4] / tau, vocab, dtype)
+        r = meo.token_logprobs(z, y, temperature=tau)
+        check_logp(f64(r.logp), n[2], vocab)
+        g = meo.token_logprobs_backward(z, y, r.stats, adv, temperature=tau)
+        check_grad(f64(g), o.logprobs_grad(f64(z), y.cpu().numpy(), f64(adv), tau), f64(adv) / tau, vocab, dtype)
