@@ -167,9 +167,15 @@ struct Ref {
   __device__ __forceinline__ float residue(float c) const { return far() || m == -INFINITY ? 0.f : fmaf(m, c, -R); }
   // What the sum of a part with the largest value m2 <= m is multiplied by.
   __device__ __forceinline__ float factor(float m2, float c) const {
-    const Ref part(m2, c);
-    if (!far() && !part.far()) return ex2(__fsub_rn(__fmul_rn(m2, c), R));
-    return ex2((m2 - m) * c + residue(c) - part.residue(c));
+    const float R2 = __fmul_rn(m2, c);
+    if (!far() && (R2 >= -kFar || R2 < R - 512.f)) return ex2(__fsub_rn(R2, R));  // (0 where the part is far below)
+    return far_factor(m2, m, R, c);
+  }
+  static __device__ __noinline__ float far_factor(float m2, float m, float R, float c) {
+    const float R2 = m2 == -INFINITY ? 0.f : __fmul_rn(m2, c);
+    const float off = fabsf(R) > kFar ? 0.f : fmaf(m, c, -R);
+    const float off2 = fabsf(R2) > kFar || m2 == -INFINITY ? 0.f : fmaf(m2, c, -R2);
+    return ex2((m2 - m) * c + off - off2);
   }
   static constexpr float kFar = 65536.f;
 };
@@ -635,11 +641,11 @@ struct List {
   Bits* bits;      // [chunks of the CTA's part][lanes]: a byte a vector, a bit a value
   int32_t* id;     // [top_k]
   float* p;        // [top_k]: the teacher's probabilities
-  float* x;        // [top_k]: the logits
-  float* head;     // sum p, rest, NaN where the list is bad (else 0), the largest of x
+  float* x;        // [top_k]: the logits (of all in rank 0, of the CTA's own elsewhere)
+  float* head;     // sum p, rest, NaN where the list is bad (else 0); of its own: the largest of x, sum of terms
 };
 __host__ __device__ constexpr int list_bytes(int slice, int top_k) {
-  return (slice + 15) / 16 * 16 + 12 * ((top_k + 3) / 4 * 4) + 16;
+  return (slice + 15) / 16 * 16 + 12 * ((top_k + 3) / 4 * 4) + 32;
 }
 __device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) {
   List l;
@@ -654,7 +660,7 @@ __device__ __forceinline__ List list_at(unsigned char* p, int slice, int top_k) 
 
 template <typename T>
 __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, const Row<T>& r, int b, int s, int v0, int v1,
-                                          int slice) {
+                                          int slice, bool all) {
   const int lane = threadIdx.x & 31;
   const float lse = a.lse.p == nullptr ? 0.f : row_value(a.lse, b, s);
   const int64_t ids = b * a.isb + s * a.iss, values = b * a.tsb + s * a.tss;
@@ -683,7 +689,8 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
     for (int u = 0; u < kAtOnce; ++u) {
       x[u] = 0.f;
       if (i[u] >= 0 && i[u] < a.vocab) {
-        x[u] = widen(*r.value(static_cast<int>(i[u])));
+        const int at = (static_cast<int>(i[u]) + r.lead) / kN<T> - v0;
+        if (all || (at >= 0 && at < v1 - v0)) x[u] = widen(*r.value(static_cast<int>(i[u])));
       } else {
         wrong |= i[u] != -1;
         i[u] = -1;
@@ -696,10 +703,10 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
       if (k >= a.top_k) continue;
       if (i[u] >= 0) {
         ++entries;
-        most = fmaxf(most, x[u]);
         top = fmaxf(top, v[u]);
         const int e = static_cast<int>(i[u]) + r.lead, at = e / kN<T> - v0;
         if (at >= 0 && at < v1 - v0) {
+          most = fmaxf(most, x[u]);
           const uint32_t bit = 1u << (at % kChunk / 32 * 8 + e % kN<T>);
           if (atomicOr(l.bits + at / kChunk * 32 + at % 32, bit) & bit) wrong = 1;
         }
@@ -714,14 +721,18 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
   entries = __reduce_add_sync(0xffffffffu, entries);
   const bool bad = __any_sync(0xffffffffu, wrong);
   const float sh = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
+  const Ref ref(most, a.c);
+  float sum = 0.f, own = 0.f;
   for (int k = lane; k < a.top_k; k += 32) {
+    const int at = (l.id[k] + r.lead) / kN<T> - v0;
+    if (l.id[k] >= 0 && at >= 0 && at < v1 - v0) own += ex2(ref.exponent(l.x[k], a.c));
     // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
     const float p = l.id[k] < 0 ? 0.f : a.lse.p == nullptr ? ex2((l.p[k] - sh) * a.c) : expf(l.p[k] * a.inv_t - lse);
     l.p[k] = p;
     sum += p;
   }
   sum = warp_sum(sum);
+  own = warp_sum(own);
   float sum_p = sum, rest = 0.f;
   if (a.lse.p == nullptr) {
     sum_p = sum == 0.f ? 0.f : sum == sum ? 1.f : sum;
@@ -737,6 +748,7 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
     l.head[1] = rest;
     l.head[2] = bad ? NAN : 0.f;
     l.head[3] = most;
+    l.head[4] = own;
   }
 }
 
@@ -785,11 +797,6 @@ __device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, 
   loss = warp_sum(loss);
   if (rest > 0.f) loss += rest * (logf(rest) - (logf(sum) - log_s));
   return loss / (a.inv_t * a.inv_t) + wrong;
-}
-__device__ __forceinline__ float list_terms(const LossArgs& a, const List& list, const Ref& ref) {
-  float top = 0.f;
-  for (int k = threadIdx.x & 31; k < a.top_k; k += 32) top += list.id[k] < 0 ? 0.f : ex2(ref.exponent(list.x[k], a.c));
-  return warp_sum(top);
 }
 // The loss from `n` parts, by the warp that adds the last: in a fixed order.
 __device__ __forceinline__ void add_part(const LossArgs& a, int part, int n, const Sum& share, int n_counted) {
@@ -909,17 +916,18 @@ struct Walk {
 // others, joins the parts and works out the row's scalars, so that these cost
 // the others nothing (16 warps doing so themselves took 2300 cycles to begin a
 // row and 2500 from its sum to its gradient, of 13,500 in all).  For lists
-// there is one more, which makes those, two rows at a time.  LONG: rows that no
+// there is one more, which makes those up to two rows ahead.  LONG: rows that no
 // cluster keeps are read twice, from global memory.
 //
-// Bound by memory where rows are many: 8192 x 128256 bf16 values take 648 us,
-// 6.49 TB/s or 0.955 of the copy rate (ring of 6 x 16 KB a CTA, two CTAs an SM,
+// Bound by memory where rows are many: 8192 x 128256 bf16 values take 660 us,
+// 6.36 TB/s or 0.94 of the copy rate (ring of 6 x 16 KB a CTA, two CTAs an SM,
 // four CTAs a row); 3000 x 50256 fp32 191 us, 0.93; 4096 x 32000 bf16 93 us,
 // 0.83.  What it took: one CTA of 16 warps an SM 716 us; the parts exchanged
 // under the cluster's own barrier, whose release waits for every store before
 // it, 748; registers in place of the ring 1075.  With a list of 64 entries 4096
-// rows take 390 us, 0.79: making the lists costs 21 of them, their words' own
-// gradients and waiting to write these 12, leaving them out of the sum 8.
+// rows take 406 us, 0.76 (336 without), with 8 entries 379: reading the listed
+// words' logits and writing their gradients takes sectors of their own.  Two
+// warps that make lists in turn: 418, but 653 for 794 with 500 entries.
 // 100 rows take 22 us, bound by one row's way through the warps (11 us).
 template <typename T, int OP, bool LONG>
 __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 32, 2)
@@ -1015,7 +1023,8 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
       const int row = walk.base + at * stride, b = row / a.seq, s = row % a.seq;
       const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
       if (q >= 2 && !wait_phase(list_free + (q & 1), (q - 2) >> 1 & 1)) break;
-      make_list(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, b, s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice);
+      make_list(a, list_at(lists + (q & 1) * list_size, slice, a.top_k), r, b, s, v0, min(r.vecs, v0 + a.vecs_per_cta), slice,
+                rank == 0);
       __syncwarp();
       if (lane == 0) arrive(list_full + (q & 1));
     }
@@ -1075,18 +1084,21 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
       const float4* const here = parts + (q & 1) * warps * ranks;
       const int all = warps * ranks;
       const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f), mine = lane < all ? here[lane] : none;
-      float m = kLists ? fmaxf(mine.x, list.head[3]) : mine.x;
+      float m = mine.x;
       for (int k = lane + 32; k < all; k += 32) m = fmaxf(m, here[k].x);
       const Ref ref(warp_max(m), a.c);
-      float sum = mine.y * ref.factor(mine.x, a.c), wrong = mine.w, top = 0.f;
+      const float f = ref.factor(mine.x, a.c);
+      float sum = mine.y * f, top = mine.z * f, wrong = mine.w;
       for (int k = lane + 32; k < all; k += 32) {
         const float4 o = here[k];
-        sum += o.y * ref.factor(o.x, a.c);
+        const float fo = ref.factor(o.x, a.c);
+        sum += o.y * fo;
+        top += o.z * fo;
         wrong += o.w;
       }
       sum = warp_sum(sum);
       if (kLists) {
-        top = list_terms(a, list, ref);
+        top = warp_sum(top);
         wrong = warp_sum(wrong);
       }
       if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
@@ -1204,9 +1216,13 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
       // The warp's part, to every CTA of the cluster.
       float4 p;
       p.x = warp_max(part.m);
+      p.z = p.w = 0.f;
+      if (kLists && warp == 0) {  // with the CTA's listed words
+        p.x = fmaxf(p.x, list.head[3]);
+        p.z = list.head[4] * Ref(p.x, a.c).factor(list.head[3], a.c);
+        p.w = list.head[2];
+      }
       p.y = warp_sum(part.s * Ref(p.x, a.c).factor(part.m, a.c));
-      p.z = 0.f;
-      p.w = kLists && warp == 0 ? list.head[2] : 0.f;
       float4* const here = parts + (q & 1) * warps * ranks;
       if (ranks > 1) {
         if (lane < ranks) send(here + rank * warps + warp, lane, p, together + (q & 1));
@@ -1247,8 +1263,9 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
         }
         if (kLists) {
           // The listed words' values replace those written above, once all
-          // warps have (each looking for its own among the ids instead: 421 us
-          // for 410 with 64 ids, 508 for 436 with 256).
+          // warps have (each looking for its own among the ids instead: 3 % more
+          // time with 64 ids, 16 % with 256; the warp that makes the lists
+          // writing them: 4 % more).
           __syncwarp();
           if (lane == 0) arrive(&written);
           if (!wait_phase(&written, q & 1)) break;
@@ -1352,7 +1369,7 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     if (a.weights.p != nullptr) v.weight = row_value(a.weights, b, s);
     if (kLists) {
       team_sync();  // the list before has been read
-      if (member == 0) make_list(a, list, r, b, s, 0, r.vecs, kSlice);
+      if (member == 0) make_list(a, list, r, b, s, 0, r.vecs, kSlice, true);
       team_sync();
 #pragma unroll
       for (int k = 0; k < kShortVecs; ++k)
@@ -1378,7 +1395,7 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     }
     ++q;
     const Ref ref(m, a.c);
-    const float top = kLists ? list_terms(a, list, ref) : 0.f;
+    const float top = kLists ? list.head[4] * ref.factor(list.head[3], a.c) : 0.f;
     const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(m) == INFINITY ? NAN : 0.f);
     wait_for_count();
     const float weight = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
@@ -1944,17 +1961,24 @@ adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
     sms = dev->sms;
   }
   int64_t cluster = 1;
-  auto threads_of = [](int mine) { return mine <= 32 * kForwardBatch * 2 ? 32 : mine <= 128 * kForwardBatch * 2 ? 128 : 512; };
   // Few rows are cut among a cluster's CTAs.  (Cutting them where that would
   // only fill the last wave of CTAs better costs more than it gives: 999 rows
   // of 50257 fp32 values 38 us whole, 47 cut in two.)
   while (cluster < kMaxCluster && a.tokens * cluster < 2 * sms && div_up(vecs, static_cast<int>(cluster)) > 512) cluster *= 2;
   a.vecs_per_cta = div_up(vecs, static_cast<int>(cluster));
-  const int threads = threads_of(a.vecs_per_cta);
+  // Small CTAs keep the SMs' loads apart in time, and with many rows their ends
+  // too; few rows want more threads each.  In CTAs of 32, 128, 256, 512:
+  //   16384 x 1000 bf16       18, 39 us
+  //   4096 x 8192             13, 17
+  //   8192 x 128256          299, 295, 299, 304
+  //   600 x 128256                 29,  25,  27
+  //   100 x 128256 (4 CTAs)   21, 9.4, 7.7, 10.8
+  const int64_t ctas = a.tokens * cluster;
+  const int threads = a.vecs_per_cta <= 1024 ? (ctas >= 16 * sms ? 32 : 128) : ctas >= 8 * sms ? 128 : 256;
   const int shared = threads / 32 * static_cast<int>(cluster * sizeof(float4));
   const bool bf16 = dtype == ADAF_BFLOAT16;
   void (*const kernel)(LossArgs) =
-      threads == 512   ? (bf16 ? k_loss_forward<__nv_bfloat16, 512> : k_loss_forward<float, 512>)
+      threads == 256   ? (bf16 ? k_loss_forward<__nv_bfloat16, 256> : k_loss_forward<float, 256>)
       : threads == 128 ? (bf16 ? k_loss_forward<__nv_bfloat16, 128> : k_loss_forward<float, 128>)
                        : (bf16 ? k_loss_forward<__nv_bfloat16, 32> : k_loss_forward<float, 32>);
   return launch(kSlotForward, kernel, a.tokens * cluster, threads, shared, static_cast<int>(cluster), false, s, a);
