@@ -7,7 +7,7 @@ three stages, each a few steps on a batch of synthetic token sequences:
   preference   to prefer the sequences that follow a rule to ones that do not
   policy       with rewards for sampled tokens, clipped against the policy that
                sampled them, and a KL term that holds it near the model of the
-               stage before
+               stage before (its loss begins at 0 with each new set of samples)
 
 Reference and old log-probabilities come from ``token_logprobs``.  The gradient
 of the logits is written over them (``grad=logits``), so a step keeps one
@@ -115,10 +115,13 @@ def main(argv=None):
     frozen = Model(args.vocab, args.width, 0).cuda()
     torch.manual_seed(2)
     results = {}
-    for name, stage in (("distill", lambda: distill(model, teacher, opt, args.steps, *size)),
-                        ("preference", lambda: preference(model, frozen, opt, args.steps, *size)),
-                        ("policy", lambda: policy(model, frozen, opt, args.steps, *size))):
+    # a preference adds up a sequence's tokens: at the first stage's rate one step goes past its minimum
+    for name, lr, stage in (("distill", 3e-3, lambda: distill(model, teacher, opt, args.steps, *size)),
+                            ("preference", 1e-4, lambda: preference(model, frozen, opt, args.steps, *size)),
+                            ("policy", 1e-4, lambda: policy(model, frozen, opt, args.steps, *size))):
         frozen.load_state_dict(model.state_dict())
+        for group in opt.param_groups:
+            group["lr"] = lr
         losses = torch.stack(list(stage())).tolist()
         results[name] = losses
         print(f"{name:11s} " + " ".join(f"{v:8.4f}" for v in losses))
