@@ -31,6 +31,11 @@
 namespace {
 
 constexpr int kMaxWarps = 8;       // of a CTA of k_loss_row that sum
+// Lists of so many entries are made by two warps of a CTA in turn.  By one, two
+// warps 4096 rows of 128256 bf16 values take, with 64 entries 406, 417 us, 256
+// 508, 498, 320 585, 540, 500 799, 653, 1000 1451, 966; rows of 32000 with 256
+// 143, 147 us, 384 173, 166.
+constexpr int kTwoListers = 320;
 constexpr int kGradThreads = 256;
 constexpr int kPairThreads = 256;
 constexpr int kCountThreads = 1024;
@@ -916,8 +921,8 @@ struct Walk {
 // others, joins the parts and works out the row's scalars, so that these cost
 // the others nothing (16 warps doing so themselves took 2300 cycles to begin a
 // row and 2500 from its sum to its gradient, of 13,500 in all).  For lists
-// there is one more, which makes those up to two rows ahead.  LONG: rows that no
-// cluster keeps are read twice, from global memory.
+// there are one or two more (LISTERS), which make those up to two rows ahead.
+// LONG: rows that no cluster keeps are read twice, from global memory.
 //
 // Bound by memory where rows are many: 8192 x 128256 bf16 values take 660 us,
 // 6.36 TB/s or 0.94 of the copy rate (ring of 6 x 16 KB a CTA, two CTAs an SM,
@@ -925,12 +930,12 @@ struct Walk {
 // 0.83.  What it took: one CTA of 16 warps an SM 716 us; the parts exchanged
 // under the cluster's own barrier, whose release waits for every store before
 // it, 748; registers in place of the ring 1075.  With a list of 64 entries 4096
-// rows take 406 us, 0.76 (the policy loss 336), with 8 entries 379: reading the listed
-// words' logits and writing their gradients takes sectors of their own.  Two
-// warps that make lists in turn: 418, but 653 for 794 with 500 entries.
+// rows take 406 us, 0.76 (the policy loss 336), with 8 entries 379, with 1000
+// 966: reading the listed words' logits and writing their gradients takes
+// sectors of their own, and long lists are bound by the warps that make them.
 // 100 rows take 22 us, bound by one row's way through the warps (11 us).
-template <typename T, int OP, bool LONG>
-__global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 32, 2)
+template <typename T, int OP, bool LONG, int LISTERS = OP == kDistill ? 1 : 0>
+__global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
     k_loss_row(const __grid_constant__ LossArgs a) {
   extern __shared__ __align__(16) unsigned char shared[];
   __shared__ RowInfo info[3];
@@ -938,7 +943,7 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
   __shared__ uint64_t together[2], info_full[3], scale_full[2], list_full[2], list_free[2], written;
   constexpr bool kLists = OP == kDistill;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int warps = (blockDim.x >> 5) - (kLists ? 3 : 2);  // that sum
+  const int warps = (blockDim.x >> 5) - 2 - LISTERS;  // that sum
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int first = static_cast<int>(blockIdx.x) / ranks, stride = static_cast<int>(gridDim.x) / ranks;
   const int v0 = rank * a.vecs_per_cta, slots = a.slots;
@@ -1015,11 +1020,13 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + (OP == kDistill ? 1 : 0)) * 3
         if (!wait_phase(full + place, parity ^ 1)) break;
       }
     }
-  } else if (kLists && warp == warps + 2) {
-    // The warp that makes the lists, up to two rows ahead.
+  } else if (kLists && warp >= warps + 2) {
+    // A warp that makes lists, up to two rows ahead: every row's, or of two such
+    // warps every other row's.
     Walk<T, OP> walk(a, first, stride);
     int q = 0, none, n_none;
     for (int at = walk.next(false, false, none, n_none); at >= 0; at = walk.next(false, false, none, n_none), ++q) {
+      if (LISTERS == 2 && (q & 1) != warp - warps - 2) continue;
       const int row = walk.base + at * stride, b = row / a.seq, s = row % a.seq;
       const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
       if (q >= 2 && !wait_phase(list_free + (q & 1), (q - 2) >> 1 & 1)) break;
@@ -1863,7 +1870,10 @@ Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
     for (int ctas = 2 * kMaxWarps / c.warps; ctas >= 1; ctas /= 2) {  // long lists: fewer CTAs of an SM
       const int room = kSharedBytes / ctas - 1024 - 512 - c.shared;
       c.slots = std::min(2 * n, std::max(0, room / place));
-      if (c.slots > n) break;
+      // places for a row and more; beside long lists for one row: a second CTA
+      // that makes lists is worth more (4096 x 128256, 1000 entries, one such warp
+      // in each: 1451 us, 2486 with one CTA an SM)
+      if (c.slots > n || (lists && c.slots == n)) break;
     }
     if (c.slots < n) c.slots = 0;
     c.shared += c.slots * place;
@@ -1919,9 +1929,13 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   }
   const Cut cut = cut_row(a.tokens, vecs, OP == kDistill, a.top_k, sms);
   const bool twice_read = cut.slots == 0;
-  void (*const kernel)(LossArgs) = twice_read ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
-                                              : (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>);
-  const int threads = 32 * (cut.warps + (OP == kDistill ? 3 : 2));
+  constexpr int kFew = OP == kDistill ? 1 : 0, kMany = 2 * kFew;
+  const int listers = kFew == 1 && !twice_read && a.top_k >= kTwoListers ? 2 : kFew;
+  void (*const kernel)(LossArgs) =
+      twice_read    ? (bf16 ? k_loss_row<__nv_bfloat16, OP, true> : k_loss_row<float, OP, true>)
+      : listers < 2 ? (bf16 ? k_loss_row<__nv_bfloat16, OP, false> : k_loss_row<float, OP, false>)
+                    : (bf16 ? k_loss_row<__nv_bfloat16, OP, false, kMany> : k_loss_row<float, OP, false, kMany>);
+  const int threads = 32 * (cut.warps + 2 + listers);
   int& most = dev->clusters[{reinterpret_cast<const void*>(kernel),
                             (static_cast<int64_t>(cut.shared) << 16) + (cut.warps << 4) + cut.cluster}];
   if (most == 0) {

@@ -218,6 +218,43 @@ def test_distill(vocab, k, dtype, rest):
     check("loss", f64(alone.loss), n[0], tau * tau * (2 * ds(vocab) + 8 * U * 60), 8 * U)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens,vocab,k", [(2400, 9001, 319), (2400, 9001, 320), (250, 128256, 1000), (250, 131073, 1024)])
+def test_distill_long_lists_over_many_rows(tokens, vocab, k, dtype):
+    """Each cluster takes several rows, some of them not counted: lists of 320
+    entries and more are made by two warps in turn, those of about 1000 leave
+    the ring one row's places."""
+    x, _ = make(tokens, vocab, dtype, 7)
+    ids, t = distill_inputs(tokens, vocab, k, 8)
+    lse = torch.logsumexp(t, 1) + 0.2
+    ids[1, 5:300] = -1
+    ids[2] = -1
+    mask = torch.rand(tokens, generator=torch.Generator().manual_seed(9)) < 0.8
+    out = meo.distill_loss(x, ids, t, lse, mask=mask.cuda())
+    n = o.distill(f64(x), ids.cpu().numpy(), f64(t), f64(lse), mask.numpy())
+    check_distill(out, n[0], n[1], n[2], n[3], x, 1.0, vocab, dtype)
+    assert not out.grad[~mask.cuda()].any()
+    again = meo.distill_loss(x, ids, t, lse, mask=mask.cuda())
+    assert torch.equal(again.loss, out.loss) and torch.equal(again.grad, out.grad)
+
+
+def test_a_copy_that_never_lands_ends_a_call_with_long_lists():
+    from memory_efficient_optimizer_gb300 import binding as B
+    x, _ = make(600, 40000, BF16, 4)
+    ids, t = distill_inputs(600, 40000, 400, 3)
+    want = meo.distill_loss(x, ids, t)
+    torch.cuda.synchronize()
+    B.loss_debug_stall_copies(True)
+    try:
+        out = meo.distill_loss(x, ids, t)
+    finally:
+        B.loss_debug_stall_copies(False)
+    torch.cuda.synchronize()
+    assert out.loss.isnan()
+    again = meo.distill_loss(x, ids, t)
+    assert torch.equal(again.loss, want.loss) and torch.equal(again.grad, want.grad)
+
+
 def test_distill_types_weights_and_strides():
     x, _ = make(6, 777, BF16, 4)
     ids, t = distill_inputs(6, 777, 12, 1, bf16=True)
