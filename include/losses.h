@@ -43,7 +43,8 @@
  * row is written as 0.  With no token left the loss is 0.  A token whose
  * teacher lists nothing (every id -1) counts, with loss and gradient 0.
  *
- * Values.  Logits of -inf have probability 0.  A row with NaN or +inf, or
+ * Values.  Logits of -inf have probability 0; a term whose factor is 0 counts
+ * as 0 beside the infinite logarithm of one.  A row with NaN or +inf, or
  * with nothing but -inf, answers NaN in its own values, and so does a row
  * whose target (or a listed teacher id) lies outside the vocabulary, and one
  * whose teacher lists an id twice: bad data shows in the loss and reads or

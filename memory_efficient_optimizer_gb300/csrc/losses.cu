@@ -1601,7 +1601,8 @@ __global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constan
     const float z = a.beta * h - a.margin, e = expf(-fabsf(z)), l = log1pf(e);
     const float neg = l + fmaxf(-z, 0.f), pos = l + fmaxf(z, 0.f);  // -ln s(z), -ln s(-z)
     const float big = 1.f / (1.f + e), small = e / (1.f + e);
-    loss = (1.f - a.smooth) * neg + a.smooth * pos;
+    // (pos is infinite where the rejected side has probability 0: with e = 0 it is no term)
+    loss = (1.f - a.smooth) * neg + (a.smooth != 0.f ? a.smooth * pos : 0.f);
     dh = a.beta * (z >= 0.f ? a.smooth * big - (1.f - a.smooth) * small : a.smooth * small - (1.f - a.smooth) * big);
   } else if (a.kind == LOSS_PREFERENCE_HINGE) {
     const float z = 1.f + a.margin - a.beta * h;

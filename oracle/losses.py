@@ -81,8 +81,9 @@ def preference(x, y, sequences, ref=None, beta=0.1, label_smoothing=0.0, kind="s
         h = D[i] - D[i + pairs]
         if kind == "sigmoid":
             z, e = beta * h - margin, label_smoothing
-            pair[i] = (1 - e) * np.logaddexp(0, -z) + e * np.logaddexp(0, z)
-            dh = beta * (e - 1 + 1 / (1 + np.exp(-z)))
+            pair[i] = (1 - e) * np.logaddexp(0, -z) + (e * np.logaddexp(0, z) if e else 0.0)
+            with np.errstate(over="ignore"):
+                dh = beta * (e - 1 + 1 / (1 + np.exp(-z)))
         elif kind == "hinge":
             z = 1 + margin - beta * h
             pair[i], dh = max(0.0, z), -beta if z > 0 else 0.0

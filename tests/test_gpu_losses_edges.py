@@ -1,0 +1,46 @@
+"""GPU parity of the losses (include/losses.h) at the edges of their formulas
+and of their arguments, and what one call may see of another.  The bars are
+those of test_gpu_losses.py, which derives them."""
+import numpy as np
+import pytest
+import torch
+
+import memory_efficient_optimizer_gb300 as meo
+from oracle import losses as o
+from test_gpu_losses import (BF16, DTYPES, FP32, U, _built, check, check_grad, check_logp, ds, f64, flat, make,  # noqa: F401
+                             per_token)
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+# ---- words of probability 0 -----------------------------------------------------
+
+def two_sides(vocab, dtype, masked):
+    """A chosen and a rejected sequence of three tokens; one target of the
+    `masked` side has probability 0."""
+    x, y = make(6, vocab, dtype, vocab + 3)
+    t = 1 if masked == "chosen" else 4
+    x[t, y[t]] = -INF
+    return x, y
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [7, 1000, 50257])
+@pytest.mark.parametrize("masked", ["chosen", "rejected"])
+@pytest.mark.parametrize("smooth", [0.0, 0.1])
+def test_preference_with_a_side_of_probability_zero(masked, smooth, vocab, dtype):
+    """h = -inf or +inf: -(1 - e) ln s(beta h) is inf or 0, the other side's
+    term 0 or inf where e > 0 and nothing where e = 0; the derivative is finite."""
+    x, y = two_sides(vocab, dtype, masked)
+    at = torch.tensor([0, 3, 6]).cuda()
+    out = meo.preference_loss(x, y, seq_offsets=at, beta=0.3, label_smoothing=smooth)
+    want, pair, rewards, lp, grad, d = o.preference(f64(x), y.cpu().numpy(), [(0, 3), (3, 6)], beta=0.3,
+                                                    label_smoothing=smooth)
+    assert want == (0.0 if masked == "rejected" and smooth == 0 else INF)
+    check("loss", f64(out.loss), want, 0.0)
+    check("pair_loss", f64(out.pair_loss), pair, 0.0)
+    e = 3 * (ds(vocab) + 4 * U * 60)
+    check("rewards", f64(out.rewards), rewards, 0.3 * e, 4 * U)
+    # the logistic function is 0 or 1 there, so the coefficient beta (e - 1), beta e is one rounding off
+    check_grad(f64(out.grad), grad, d, vocab, dtype)
