@@ -572,7 +572,8 @@ struct Token {
   float loss, d;
 };
 __device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, const PolicyIn& in) {
-  const float r = expf(logp - (a.old.p == nullptr ? logp : in.old));
+  // Without old_logp the ratio is 1, for a word of probability 0 too (NaN stays).
+  const float r = a.old.p != nullptr ? expf(logp - in.old) : isnan(logp) ? logp : 1.f;
   const float raw = r * in.adv;
   const float cut = fminf(fmaxf(r, a.lo), a.hi) * in.adv;
   Token t;

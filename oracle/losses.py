@@ -51,7 +51,7 @@ def policy(x, y, adv, old=None, ref=None, clip_low=0.2, clip_high=0.2, kl_coef=0
     for t in range(len(y)):
         if y[t] == ignore:
             continue
-        r = np.exp(logp[t] - (logp[t] if old is None else old[t]))
+        r = np.exp(logp[t] - old[t]) if old is not None else 1.0 if not np.isnan(logp[t]) else np.nan
         raw, cut = r * adv[t], np.clip(r, 1 - clip_low, 1 + clip_high) * adv[t]
         token[t] = -min(raw, cut)
         d[t] = -raw if raw <= cut else 0.0

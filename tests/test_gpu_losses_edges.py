@@ -44,3 +44,26 @@ def test_preference_with_a_side_of_probability_zero(masked, smooth, vocab, dtype
     check("rewards", f64(out.rewards), rewards, 0.3 * e, 4 * U)
     # the logistic function is 0 or 1 there, so the coefficient beta (e - 1), beta e is one rounding off
     check_grad(f64(out.grad), grad, d, vocab, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [7, 1000, 50257])
+def test_policy_first_step_on_a_word_of_probability_zero(vocab, dtype):
+    """Without old_logp the ratio is 1, whatever the target's probability is."""
+    x, y = make(5, vocab, dtype, vocab + 4)
+    x[1, y[1]] = -INF
+    x[2, y[2]] = -INF
+    adv = torch.tensor([1.0, 0.7, -1.5, 0.4, -1.0]).cuda()
+    out = meo.policy_loss(x, y, adv)
+    want, token, lp, grad, d = o.policy(f64(x), y.cpu().numpy(), f64(adv))
+    assert np.isneginf(lp[1:3]).all() and np.array_equal(token, -f64(adv))
+    check_logp(f64(out.logp), lp, vocab)
+    check("token_loss", f64(out.token_loss), token, 0.0, 2 * U)
+    check("loss", f64(out.loss), want, 0.0, 8 * U)
+    check_grad(f64(out.grad), grad, d, vocab, dtype)
+    # a row without a distribution still answers NaN
+    y[3] = vocab
+    x[4, 0] = float("nan")
+    out = meo.policy_loss(x, y, adv)
+    assert out.token_loss[3:].isnan().all() and out.grad[3:].isnan().all() and out.grad[:3].isfinite().all()
+    assert out.token_loss[:3].isfinite().all()

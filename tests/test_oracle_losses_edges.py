@@ -24,3 +24,13 @@ def test_preference_with_a_side_of_probability_zero(t, smooth, want):
     assert rewards[0 if t < 2 else 1] == -INF and np.isfinite(grad).all()
     # the limit of the derivative beta (e - 1 + s(beta h)) at h = -inf, +inf
     assert d[0] == pytest.approx(0.3 * (smooth - 1 if t < 2 else smooth)) and d[2] == -d[0]
+
+
+def test_policy_first_step_on_a_word_of_probability_zero():
+    x, y = masked(2)
+    loss, token, logp, grad, d = o.policy(x, y, [1.0, 1.0, -2.0, 3.0])
+    assert logp[2] == -INF and np.array_equal(token, [-1.0, -1.0, 2.0, -3.0]) and loss == pytest.approx(-0.75)
+    assert np.isfinite(grad).all() and np.array_equal(d * 4, token)
+    # a target outside the vocabulary is no word: NaN
+    y[0] = 9
+    assert np.isnan(o.policy(x, y, [1.0] * 4)[1][0])
