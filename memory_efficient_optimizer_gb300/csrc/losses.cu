@@ -583,7 +583,7 @@ __device__ __forceinline__ Token policy_token(const LossArgs& a, float logp, con
   if (a.kl != 0.f) {
     const float far = in.ref - logp;
     const float e = expm1f(far);
-    t.loss += a.kl * (e - far);
+    t.loss += a.kl * (far == INFINITY ? far : e - far);  // (a word of probability 0: not inf - inf)
     t.d -= a.kl * e;
   }
   return t;

@@ -38,7 +38,8 @@ def logprobs_grad(x, y, d, temperature=1.0, ignore=-100):
             g[t] = np.nan
             continue
         q = np.exp(log_softmax(x[t] / temperature))
-        g[t] = -q * d[t] / temperature
+        with np.errstate(invalid="ignore"):  # (an infinite d times a word of probability 0)
+            g[t] = -q * d[t] / temperature
         g[t, y[t]] += d[t] / temperature
     return g
 
@@ -57,7 +58,7 @@ def policy(x, y, adv, old=None, ref=None, clip_low=0.2, clip_high=0.2, kl_coef=0
         d[t] = -raw if raw <= cut else 0.0
         if kl_coef:
             far = ref[t] - logp[t]
-            token[t] += kl_coef * (np.expm1(far) - far)
+            token[t] += kl_coef * (np.expm1(far) - far if far != np.inf else np.inf)
             d[t] -= kl_coef * np.expm1(far)
     w = np.full(len(y), 1.0 / max(n, 1)) if weights is None else np.asarray(weights, dtype=np.float64)
     w = np.where(y != ignore, w, 0.0)

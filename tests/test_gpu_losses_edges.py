@@ -67,3 +67,28 @@ def test_policy_first_step_on_a_word_of_probability_zero(vocab, dtype):
     out = meo.policy_loss(x, y, adv)
     assert out.token_loss[3:].isnan().all() and out.grad[3:].isnan().all() and out.grad[:3].isfinite().all()
     assert out.token_loss[:3].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [7, 1000, 50257])
+def test_policy_kl_term_of_a_word_of_probability_zero(vocab, dtype):
+    """exp(d) - d - 1 grows without bound on both sides: inf where the policy
+    gives the word probability 0, and where the reference does."""
+    x, y = make(4, vocab, dtype, vocab + 5)
+    x[1, y[1]] = -INF
+    lp = o.token_logprobs(f64(x), y.cpu().numpy())
+    ref = torch.tensor(np.float32(np.where(np.isfinite(lp), lp, -5) - 0.3)).cuda()
+    ref[2] = -INF
+    old = torch.tensor(np.float32(np.where(np.isfinite(lp), lp, -5) + 0.1)).cuda()
+    adv = torch.tensor([1.0, 1.0, -1.0, 0.5]).cuda()
+    for args in ((None, ref), (old, ref)):
+        out = meo.policy_loss(x, y, adv, *args, kl_coef=0.05)
+        want, token, _, grad, d = o.policy(f64(x), y.cpu().numpy(), f64(adv), *(None if a is None else f64(a) for a in args),
+                                           kl_coef=0.05)
+        assert want == INF and np.isposinf(token[1:3]).all()
+        err = 4 * (6 * ds(vocab) + 8 * U * 40)
+        check("token_loss", f64(out.token_loss), token, err, err)
+        check("loss", f64(out.loss), want, 0.0)
+        keep = [0, 2, 3]     # (the derivative of token 1 is infinite)
+        check("grad", f64(out.grad)[keep], grad[keep], 3 * ds(vocab) * np.abs(d[keep])[:, None] + 1e-37,
+              err + (2 ** -8 if dtype is BF16 else 0))

@@ -34,3 +34,10 @@ def test_policy_first_step_on_a_word_of_probability_zero():
     # a target outside the vocabulary is no word: NaN
     y[0] = 9
     assert np.isnan(o.policy(x, y, [1.0] * 4)[1][0])
+
+
+def test_policy_kl_term_of_a_word_of_probability_zero():
+    x, y = masked(2)
+    ref = np.array([-1.0, -INF, -2.0, -3.0])
+    token = o.policy(x, y, [1.0] * 4, ref=ref, kl_coef=0.1)[1]
+    assert token[1] == INF and token[2] == INF and np.isfinite(token[[0, 3]]).all()
