@@ -606,6 +606,10 @@ __device__ __forceinline__ void copy_bulk(void* to, const void* from, uint32_t b
                  "l"(from), "r"(bytes), "r"(shared_at(bar))
                  : "memory");
 }
+// Orders what a thread has read (or has waited for others to read) before a bulk
+// copy that it makes to the same place: barriers alone order them with ordinary
+// stores, not with a copy, which goes by another way.
+__device__ __forceinline__ void reads_before_copies() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ bool phase_done(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -1001,6 +1005,7 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
             break;
           }
           if (lane == 0) {
+            reads_before_copies();
             const int i0 = max(i, lo), n = min(i + round, hi) - i0;
             copy_bulk(ring + place * round + (i0 - i), reinterpret_cast<const uint4*>(r.base) + i0, n > 0 ? 16 * n : 0, full + place,
                       a.stall != 0);
@@ -1210,7 +1215,8 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
         }
         if (!LONG) {
           if (!gradient) {
-            __syncwarp();  // the place has been read
+            reads_before_copies();  // (no store waits for them here)
+            __syncwarp();
             if (lane == 0) arrive(empty + place);
           }
           if (++place == slots) {
@@ -1262,12 +1268,20 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
                 if (e < v1 && (e < copied_from(r) || e >= copied_to(r))) v[k] = load_vec(r, e, v1);
               }
             }
-            __syncwarp();  // the place has been read
-            if (lane == 0) arrive(empty + place);
-            if (++place == slots) place = 0;
           }
           store_batch<T, 32>(v, r, g, i, v1, plain && near && static_cast<unsigned>(y_vec - (i - lane)) >= kChunk, ref, a.c,
                              by.scale, now.y, y_vec, by.more);
+          if (!LONG) {
+            // The place is given back when the stores have taken what was read
+            // from it.  Given back once its reads were merely begun, it was
+            // seen overwritten by the next row's copy before the last of them
+            // where stores to global memory held them up.  8192 x 128256 bf16
+            // values take 658 us with either, 670 with a fence by every warp
+            // here, 679 with one before the stores.
+            __syncwarp();
+            if (lane == 0) arrive(empty + place);
+            if (++place == slots) place = 0;
+          }
         }
         if (kLists) {
           // The listed words' values replace those written above, once all

@@ -92,3 +92,37 @@ def test_policy_kl_term_of_a_word_of_probability_zero(vocab, dtype):
         keep = [0, 2, 3]     # (the derivative of token 1 is infinite)
         check("grad", f64(out.grad)[keep], grad[keep], 3 * ds(vocab) * np.abs(d[keep])[:, None] + 1e-37,
               err + (2 ** -8 if dtype is BF16 else 0))
+
+
+# ---- state between rows and between calls ---------------------------------------------
+
+def ring_case(op, tokens, vocab, k, dtype):
+    from test_gpu_losses import distill_inputs
+    x, y = make(tokens, vocab, dtype, 7, ignore=range(3, tokens, 7))
+    if op == "policy":
+        adv = per_token(tokens, 5)
+        return lambda **kw: meo.policy_loss(x, y, adv, **kw), lambda: o.policy(f64(x), y.cpu().numpy(), f64(adv))
+    ids, t = distill_inputs(tokens, vocab, k, 8)
+    lse = torch.logsumexp(t, 1) + 0.2
+    mask = y != -100
+    return (lambda **kw: meo.distill_loss(x, ids, t, lse, mask=mask, **kw),
+            lambda: o.distill(f64(x), ids.cpu().numpy(), f64(t), f64(lse), mask.cpu().numpy()))
+
+
+@pytest.mark.parametrize("op,tokens,vocab,k,dtype", [
+    ("distill", 2400, 20001, 300, FP32), ("distill", 2400, 9001, 319, FP32), ("distill", 1200, 50257, 500, BF16),
+    ("distill", 800, 128256, 1000, BF16), ("policy", 2400, 20001, 0, FP32), ("policy", 1200, 50257, 0, BF16)])
+def test_a_row_in_the_ring_is_not_overwritten_while_it_is_read(op, tokens, vocab, k, dtype):
+    """The next row's copies wait for places that this row's gradient is made
+    from: with lists the ring has one place more than a row's, or none.  Every
+    word of every row is right, in each of several passes."""
+    call, oracle = ring_case(op, tokens, vocab, k, dtype)
+    outs = [call() for _ in range(8)]
+    want = oracle()
+    grad, w = (want[3], want[4]) if op == "policy" else (want[2], want[3])
+    check("grad", f64(outs[0].grad), grad, 6 * ds(vocab) * np.abs(w)[:, None] + 1e-37,
+          6 * ds(vocab) + (2 ** -8 if dtype is BF16 else 4 * U))
+    loss_alone = call(need_grad=False)
+    assert torch.equal(loss_alone.token_loss, outs[0].token_loss) and torch.equal(loss_alone.loss, outs[0].loss)
+    for out in outs[1:]:
+        assert torch.equal(out.grad, outs[0].grad) and torch.equal(out.token_loss, outs[0].token_loss)
