@@ -652,7 +652,7 @@ struct List {
   int32_t* id;     // [top_k]
   float* p;        // [top_k]: the teacher's probabilities
   float* x;        // [top_k]: the logits (of all in rank 0, of the CTA's own elsewhere)
-  float* head;     // sum p, rest, NaN where the list is bad (else 0); of its own: the largest of x, sum of terms
+  float* head;     // sum p, rest, NaN where the list is bad (else 0); of the CTA's own: the largest of x, sum of terms
 };
 __host__ __device__ constexpr int list_bytes(int slice, int top_k) {
   return (slice + 15) / 16 * 16 + 12 * ((top_k + 3) / 4 * 4) + 32;
@@ -763,9 +763,9 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
 }
 
 // What the gradient needs: scale 2^(x c - R) with R of m, `more` at the target;
-// for a list, lead (on 2^(x c - R) - p) at its words.
+// for a list, with R of m_on, lead (on 2^(x c - R) - p) at its words.
 struct RowScale {
-  float m, scale, more, lead, on;
+  float m, scale, more, m_on, lead, on;
 };
 // A token's own values.
 struct Values {
@@ -774,38 +774,47 @@ struct Values {
   PolicyIn in;
   float weight, x_at;
 };
-// The row's scalars from its sum (of the words not listed) and, for a list, the
-// listed words' (`top`).  `loss` of a policy is done; of a list it is what
-// list_loss() makes of the row.
-template <int OP>
-__device__ __forceinline__ RowScale row_scale(const LossArgs& a, const Values& v, const List& list, const Ref& ref, float sum,
-                                              float top, float wrong, float w, float& logp, float& loss) {
-  RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f};
-  if (OP != kDistill) {
-    logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
-    const Token t = policy_token(a, logp, v.in);
-    loss = t.loss;
-    out.more = w * a.gscale * a.inv_t * t.d;
-    out.scale = __fdividef(-out.more, sum);
-  } else {
-    // off the list q (P + u) - u q / (rest of q); on it q (P + u) - p
-    const float rest = list.head[1];
-    out.lead = w * a.gscale / a.inv_t + wrong;
-    out.on = (list.head[0] + rest) / (sum + top);
-    out.scale = out.lead * (out.on - (rest > 0.f ? rest / sum : 0.f));
-  }
+// A row with a list has two sums.  That of the words not listed is relative to
+// the largest of them: their shares among themselves are needed too, and beside
+// the listed words they may all be too small for fp32 (logits 88 T below).
+// (Rows that need no such care on a path of their own: 415 us for 417 of 4096 x
+// 128256 bf16 values, with one sum and no care 408.)
+struct ListSums {
+  Ref off, whole;              // of the words not listed, of all
+  float factor, off_sum, sum;  // from `off` to `whole`; the two sums
+};
+// The row's scalars from its sum.  The policy's loss is done with them.
+__device__ __forceinline__ RowScale policy_scale(const LossArgs& a, const Values& v, const Ref& ref, float sum, float wrong, float w,
+                                                 float& logp, float& loss) {
+  RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f, 0.f};
+  logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+  const Token t = policy_token(a, logp, v.in);
+  loss = t.loss;
+  out.more = w * a.gscale * a.inv_t * t.d;
+  out.scale = __fdividef(-out.more, sum);
+  return out;
+}
+// Off the list q (P + u) - u share, share = q / (sum of such q); on it q (P + u) - p.
+__device__ __forceinline__ RowScale list_scale(const LossArgs& a, const List& list, const ListSums& s, float wrong, float w) {
+  RowScale out{s.off.m, 0.f, 0.f, s.whole.m, 0.f, 0.f};
+  const float rest = list.head[1];
+  out.lead = w * a.gscale / a.inv_t + wrong;
+  out.on = (list.head[0] + rest) / s.sum;
+  out.scale = out.lead * (out.on * s.factor - (rest > 0.f ? rest / s.off_sum : 0.f));
   return out;
 }
 // By a whole warp.
-__device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, const Ref& ref, float sum, float top, float wrong) {
-  const float log_s = logf(sum + top), rest = list.head[1], d = ref.residue(a.c) * kLn2;
+__device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, const ListSums& s, float wrong) {
+  const Ref& ref = s.whole;
+  const float log_s = logf(s.sum), rest = list.head[1], d = ref.residue(a.c) * kLn2;
   float loss = 0.f;
   for (int k = threadIdx.x & 31; k < a.top_k; k += 32) {
     const float p = list.p[k];
     if (p != 0.f) loss += p * (logf(p) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
   }
   loss = warp_sum(loss);
-  if (rest > 0.f) loss += rest * (logf(rest) - (logf(sum) - log_s));
+  if (rest > 0.f)
+    loss += rest * (logf(rest) - ((s.off.m - ref.m) * a.inv_t + (logf(s.off_sum) - s.off.residue(a.c) * kLn2) - (log_s - d)));
   return loss / (a.inv_t * a.inv_t) + wrong;
 }
 // The loss from `n` parts, by the warp that adds the last: in a fixed order.
@@ -1096,39 +1105,40 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
       if (dead) break;
       const float4* const here = parts + (q & 1) * warps * ranks;
       const int all = warps * ranks;
-      const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f), mine = lane < all ? here[lane] : none;
-      float m = mine.x;
-      for (int k = lane + 32; k < all; k += 32) m = fmaxf(m, here[k].x);
-      const Ref ref(warp_max(m), a.c);
-      const float f = ref.factor(mine.x, a.c);
-      float sum = mine.y * f, top = mine.z * f, wrong = mine.w;
+      const float4 none = make_float4(-INFINITY, 0.f, -INFINITY, 0.f), mine = lane < all ? here[lane] : none;
+      float m = mine.x, m_whole = fmaxf(mine.x, mine.z);
       for (int k = lane + 32; k < all; k += 32) {
         const float4 o = here[k];
-        const float fo = ref.factor(o.x, a.c);
-        sum += o.y * fo;
-        top += o.z * fo;
-        wrong += o.w;
+        m = fmaxf(m, o.x);
+        m_whole = fmaxf(m_whole, fmaxf(o.x, o.z));
       }
+      const Ref ref(warp_max(m), a.c), whole(kLists ? warp_max(m_whole) : ref.m, a.c);
+      float sum = mine.y * ref.factor(mine.x, a.c), top = kLists ? mine.w * whole.factor(mine.z, a.c) : 0.f;
+      for (int k = lane + 32; k < all; k += 32) {
+        const float4 o = here[k];
+        sum += o.y * ref.factor(o.x, a.c);
+        if (kLists) top += o.w * whole.factor(o.z, a.c);
+      }
+      const float f = kLists ? whole.factor(ref.m, a.c) : 1.f;
       sum = warp_sum(sum);
-      if (kLists) {
-        top = warp_sum(top);
-        wrong = warp_sum(wrong);
-      }
-      if (fabsf(ref.m) == INFINITY) wrong = NAN;  // a row without a distribution
+      if (kLists) top = warp_sum(top);
+      // A row without a distribution, and a bad list, whose sum is NaN.
+      const float wrong = fabsf(whole.m) == INFINITY || isnan(top) ? NAN : 0.f;
       __syncwarp();
       if (ranks > 1 && lane == 0) expect_bytes(together + (q & 1), row_bytes);
 
       wait_for_count();
       const float w = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
       float logp = 0.f, loss = 0.f;
-      const RowScale out = row_scale<OP>(a, v, list, ref, sum, top, wrong, w, logp, loss);
+      const ListSums both{ref, whole, f, sum, sum * f + top};
+      const RowScale out = kLists ? list_scale(a, list, both, wrong, w) : policy_scale(a, v, ref, sum, wrong, w, logp, loss);
       if (lane == 0) {
         scales[q & 1] = out;
         arrive(scale_full + (q & 1));
       }
       __syncwarp();
       // The others make the gradient from here on.
-      if (kLists && rank == 0) loss = list_loss(a, list, ref, sum, top, wrong);
+      if (kLists && rank == 0) loss = list_loss(a, list, both, wrong);
       if (rank == 0) {
         if (lane == 0 && a.logp != nullptr) a.logp[v.row] = logp;
         if (lane == 0 && a.token_loss != nullptr) a.token_loss[v.row] = loss;
@@ -1227,14 +1237,15 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
       }
       if (dead) break;
 
-      // The warp's part, to every CTA of the cluster.
+      // The warp's part, to every CTA of the cluster: the largest value and the
+      // sum, and in the first warp's those of the CTA's listed words.
       float4 p;
       p.x = warp_max(part.m);
-      p.z = p.w = 0.f;
-      if (kLists && warp == 0) {  // with the CTA's listed words
-        p.x = fmaxf(p.x, list.head[3]);
-        p.z = list.head[4] * Ref(p.x, a.c).factor(list.head[3], a.c);
-        p.w = list.head[2];
+      p.z = -INFINITY;
+      p.w = 0.f;
+      if (kLists && warp == 0) {
+        p.z = list.head[3];
+        p.w = list.head[4] + list.head[2];
       }
       p.y = warp_sum(part.s * Ref(p.x, a.c).factor(part.m, a.c));
       float4* const here = parts + (q & 1) * warps * ranks;
@@ -1291,10 +1302,11 @@ __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
           __syncwarp();
           if (lane == 0) arrive(&written);
           if (!wait_phase(&written, q & 1)) break;
+          const Ref on(by.m_on, a.c);
           for (int k = threadIdx.x; k < a.top_k; k += 32 * warps) {
             const int i = list.id[k], v = (i + r.lead) / kN<T>;
             if (i >= 0 && v >= v0 && v < v1)
-              narrow(g.g[i], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+              narrow(g.g[i], by.lead * (by.on * ex2(on.exponent(list.x[k], a.c)) - list.p[k]));
           }
         }
       }
@@ -1407,22 +1419,19 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
       team_sync();
       const float2* const here = parts[q & 1] + team * TEAM;
       for (int k = 0; k < TEAM; ++k) m = fmaxf(m, here[k].x);
-      if (kLists) m = fmaxf(m, list.head[3]);
       sum = 0.f;
       for (int k = 0; k < TEAM; ++k) sum += here[k].y * Ref(m, a.c).factor(here[k].x, a.c);
-    } else if (kLists) {
-      const float m2 = fmaxf(m, list.head[3]);
-      sum *= Ref(m2, a.c).factor(m, a.c);
-      m = m2;
     }
     ++q;
     const Ref ref(m, a.c);
-    const float top = kLists ? list.head[4] * ref.factor(list.head[3], a.c) : 0.f;
-    const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(m) == INFINITY ? NAN : 0.f);
+    const Ref whole(kLists ? fmaxf(m, list.head[3]) : m, a.c);
+    const float f = kLists ? whole.factor(m, a.c) : 1.f;
+    const ListSums both{ref, whole, f, sum, kLists ? sum * f + list.head[4] * whole.factor(list.head[3], a.c) : sum};
+    const float wrong = (kLists ? list.head[2] : 0.f) + (fabsf(whole.m) == INFINITY ? NAN : 0.f);
     wait_for_count();
     const float weight = a.weights.p != nullptr ? v.weight : 1.f / static_cast<float>(n_counted);
     float logp = 0.f, loss = 0.f;
-    const RowScale by = row_scale<OP>(a, v, list, ref, sum, top, wrong, weight, logp, loss);
+    const RowScale by = kLists ? list_scale(a, list, both, wrong, weight) : policy_scale(a, v, ref, sum, wrong, weight, logp, loss);
     if (a.g != nullptr) {
       const int y_vec = v.y >= 0 ? (v.y + r.lead) / kN<T> : kNoValue;
       const bool plain = batch_in<32, kShortVecs>(first - lane, r.first_whole(), r.past_whole()) && g.shift == 0 && !ref.far() &&
@@ -1433,12 +1442,12 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
         for (int k = lane; k < a.top_k; k += 32) {
           const int i = list.id[k];
           if (i >= 0 && (i + r.lead) / kN<T> / kOwn == member)
-            narrow(g.g[i], by.lead * (by.on * ex2(ref.exponent(list.x[k], a.c)) - list.p[k]));
+            narrow(g.g[i], by.lead * (by.on * ex2(whole.exponent(list.x[k], a.c)) - list.p[k]));
         }
       }
     }
     if (member != 0) continue;
-    if (kLists) loss = list_loss(a, list, ref, sum, top, wrong);
+    if (kLists) loss = list_loss(a, list, both, wrong);
     if (lane == 0 && a.logp != nullptr) a.logp[row] = logp;
     if (lane == 0 && a.token_loss != nullptr) a.token_loss[row] = loss;
     share.add(a.weights.p != nullptr ? weight * loss : loss);

@@ -126,3 +126,89 @@ def test_a_row_in_the_ring_is_not_overwritten_while_it_is_read(op, tokens, vocab
     assert torch.equal(loss_alone.token_loss, outs[0].token_loss) and torch.equal(loss_alone.loss, outs[0].loss)
     for out in outs[1:]:
         assert torch.equal(out.grad, outs[0].grad) and torch.equal(out.token_loss, outs[0].token_loss)
+
+
+# ---- a student far from its teacher ------------------------------------------------
+
+def check_distill_far(out, x, ids, t, lse, tau, dtype):
+    """Against the oracle, word by word.  With L the largest |ln| of a listed
+    word's or of the other words' probability, ln q and ln(others) are good to
+    ds + 4u L; a teacher's p to dp = 2^-22 + 4u (|t / T| + |lse|), and so is its
+    rest, absolutely.  The gradient on the list is T w (q (P + u) - p), off it
+    T w (q (P + u) - u share), share a word's part of the unlisted mass: each
+    product has its factors' relative errors and share u also the rest's."""
+    xn, ids, t, lse = f64(x), ids.cpu().numpy(), f64(t), f64(lse)
+    vocab = xn.shape[1]
+    want, token, grad, w = o.distill(xn, ids, t, lse, temperature=tau)
+    e_token, bar = np.zeros(len(token)), np.zeros(xn.shape)
+    for i in range(len(token)):
+        lq = o.log_softmax(xn[i] / tau)
+        p = np.exp(t[i] / tau - lse[i])
+        off = np.ones(vocab, dtype=bool)
+        off[ids[i]] = False
+        l_off = np.logaddexp.reduce(lq[off])
+        rest = max(0.0, 1 - p.sum())
+        far = max(np.abs(lq[ids[i]]).max(), abs(l_off))
+        dp = 2.0 ** -22 + 4 * U * (np.abs(t[i] / tau).max() + abs(lse[i])) + 32 * U
+        rel = 6 * ds(vocab) + 4 * U * far
+        e_token[i] = tau ** 2 * (2 * rel + dp * (far + 20))
+        share = np.where(off, np.exp(lq - l_off), 0.0)
+        bar[i] = np.exp(lq) * (p.sum() + rest + dp) * (rel + dp) + share * (rest * rel + dp)
+        bar[i, ids[i]] += p * (rel + dp)
+    check("token_loss", f64(out.token_loss), token, e_token, 8 * U)
+    check("loss", f64(out.loss), want, np.sum(w * e_token), 8 * U)
+    if out.grad is not None:
+        check("grad", f64(out.grad), grad, tau * w[:, None] * bar + 1e-36, 2.0 ** -8 if dtype is BF16 else 4 * U)
+
+
+def far_student(vocab, k, tau, gap, dtype):
+    """Listed words `gap` nats above the others; below them; one above and the
+    others below; above them, and a teacher whose rest is rounding alone."""
+    g = torch.Generator().manual_seed(vocab)
+    x = torch.randn(4, vocab, generator=g) * 2 * tau
+    ids = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(4)])
+    for row, move in ((0, gap), (1, -gap), (2, -gap), (3, gap)):
+        x[row, ids[row]] += move * tau
+    x[2, ids[2, 0]] += 2 * gap * tau
+    t = torch.randn(4, k, generator=g) * 2 * tau
+    lse = torch.logsumexp(t / tau, 1) + torch.tensor([0.3, 0.3, 0.3, 0.0])
+    return x.to(dtype).cuda(), ids.cuda(), t.cuda(), lse.cuda()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab,k", [(300, 5), (1000, 20), (8000, 64), (50257, 64), (128256, 400), (600011, 20)])
+@pytest.mark.parametrize("tau,gap", [(1.0, 25), (1.0, 120), (0.2, 100), (0.1, 250)])
+def test_distill_of_a_student_far_from_its_teacher(tau, gap, vocab, k, dtype):
+    """The unlisted words' mass is far below what fp32 holds beside the listed
+    words', or the other way about: loss and gradient are finite."""
+    x, ids, t, lse = far_student(vocab, k, tau, gap, dtype)
+    out = meo.distill_loss(x, ids, t, lse, temperature=tau)
+    assert out.loss.isfinite() and out.grad.isfinite().all()
+    check_distill_far(out, x, ids, t, lse, tau, dtype)
+    check_distill_far(meo.distill_loss(x, ids, t, lse, temperature=tau, need_grad=False), x, ids, t, lse, tau, dtype)
+
+
+def test_distill_small_rest_at_a_low_temperature():
+    x = torch.full((1, 1000), -12.0)
+    x[0, 5], x[0, 700] = 9.0, 8.5
+    x, ids, t = x.cuda(), torch.tensor([[5, 700]]).cuda(), torch.tensor([[2.0, 1.0]]).cuda()
+    lse = torch.logsumexp(t / 0.2, 1) + 0.2
+    out = meo.distill_loss(x, ids, t, lse, temperature=0.2)
+    check_distill_far(out, x, ids, t, lse, 0.2, FP32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab,k", [(1000, 20), (50257, 64)])
+def test_distill_far_students_in_many_rows_a_cluster(vocab, k, dtype):
+    """Far and near rows in turn through the same places of the ring."""
+    rows = [far_student(vocab, k, 0.5, gap, dtype) for gap in (0, 150)]
+    x, ids, t, lse = (torch.cat([torch.stack([a, b], 1).flatten(0, 1)] * 200) for a, b in zip(*rows))
+    first = meo.distill_loss(x[:8], ids[:8], t[:8], lse[:8], temperature=0.5)
+    check_distill_far(first, x[:8], ids[:8], t[:8], lse[:8], 0.5, dtype)
+    w = torch.full((1600,), 1 / 8.0, device="cuda")
+    out = meo.distill_loss(x, ids, t, lse, temperature=0.5, weights=w)
+    some = meo.distill_loss(x[800:1600], ids[800:1600], t[800:1600], lse[800:1600], temperature=0.5, weights=w[800:])
+    assert torch.equal(out.grad[:800], out.grad[800:]) and torch.equal(out.grad[:800], some.grad)
+    assert torch.equal(out.token_loss[:8].repeat(200), out.token_loss)
+    again = out.grad[:8].double() - first.grad.double()
+    assert again.abs().max() <= 2.0 ** -7 * first.grad.double().abs().max()
