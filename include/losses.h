@@ -132,7 +132,9 @@ typedef struct loss_preference_args {
     const void* seq_offsets;     /* device [2 pairs + 1], non-decreasing from
                                     0 to seq, with batch = 1: sequence n has
                                     the tokens offsets[n] .. offsets[n + 1];
-                                    a pair with a bad offset answers NaN.
+                                    a pair with a bad offset answers NaN (its
+                                    loss and both rewards; a bad sequence has
+                                    no tokens to give a gradient to).
                                     NULL: batch = 2 pairs, one per sequence  */
     int32_t offsets_dtype;       /* LOSS_INT32 or LOSS_INT64                 */
     int32_t kind;                /* LOSS_PREFERENCE_*                        */

@@ -1644,8 +1644,8 @@ __global__ void __launch_bounds__(kPairThreads) k_loss_pair(const __grid_constan
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == static_cast<unsigned>(a.pairs - 1);
     if (a.rewards != nullptr) {
-      a.rewards[pair] = a.beta * D[0];
-      a.rewards[pair + a.pairs] = a.beta * D[1];
+      a.rewards[pair] = ok ? a.beta * D[0] : NAN;
+      a.rewards[pair + a.pairs] = ok ? a.beta * D[1] : NAN;
     }
   }
   for (int q = 0; q < 2; ++q) {

@@ -212,3 +212,23 @@ def test_distill_far_students_in_many_rows_a_cluster(vocab, k, dtype):
     assert torch.equal(out.token_loss[:8].repeat(200), out.token_loss)
     again = out.grad[:8].double() - first.grad.double()
     assert again.abs().max() <= 2.0 ** -7 * first.grad.double().abs().max()
+
+
+# ---- bad offsets -----------------------------------------------------------------
+
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_pairs_with_a_bad_offset_answer_nan_in_every_value(average):
+    x, y = make(16, 100, FP32)
+    ref = per_token(16, 1)
+    # sequences 0 .. 3; of the pairs (0, 2) and (1, 3) the second has a bad end
+    for at in ([0, 4, 8, 12, 11], [0, 4, 8, 12, 17]):
+        out = meo.preference_loss(x, y, ref, seq_offsets=torch.tensor(at).cuda(), average=average)
+        assert out.loss.isnan() and out.pair_loss.isnan().tolist() == [False, True]
+        assert out.rewards.isnan().tolist() == [False, True, False, True]
+        good = meo.preference_loss(x[[0, 1, 2, 3, 8, 9, 10, 11]], y[[0, 1, 2, 3, 8, 9, 10, 11]],
+                                   ref[[0, 1, 2, 3, 8, 9, 10, 11]], seq_offsets=torch.tensor([0, 4, 8]).cuda(), average=average)
+        assert torch.equal(out.rewards[::2], good.rewards) and torch.equal(out.pair_loss[:1], good.pair_loss)
+        assert torch.equal(out.logp[:4], good.logp[:4]) and out.grad[[0, 1, 2, 3, 8, 9, 10, 11]].isfinite().all()
+    # the first sequence's beginning
+    out = meo.preference_loss(x, y, ref, seq_offsets=torch.tensor([-1, 4, 8, 12, 16]).cuda(), average=average)
+    assert out.rewards.isnan().tolist() == [True, False, True, False]
