@@ -79,6 +79,20 @@ struct Sum {
   __device__ __forceinline__ float total() const { return fabsf(s) == INFINITY ? s : s + rest; }
 };
 
+// 1 / T as the sum of two fp32 numbers: one alone is off by up to 2^-24 of it, and
+// every ln q would lean by that times z[y] - max z the same way, which sums over
+// tokens collect.  Both are positive, so that an infinity stays one.
+//
+// log2(e) / T of the terms is one number.  For it the mean of ln q is off by up to
+// 4e-7 (over 48 temperatures by 1e-7, as in fp32 torch operations), at T = 1 by
+// 3e-8 to 7e-8, where the exponential's own mean error of -5e-8 goes the other
+// way; a ln q is rounded to 5e-7.  A second multiply-add a term leaves a fifth of
+// it over the temperatures, twice as much at T = 1, and costs the policy loss 2.5 %.
+struct PerT {
+  float hi, lo;
+};
+__device__ __forceinline__ float over_t(float v, const PerT& t) { return fmaf(v, t.hi, v * t.lo); }
+
 struct Rows {
   const void* p;
   int64_t sb, ss;
@@ -92,6 +106,7 @@ struct LossArgs {
   uintptr_t x_begin, x_end;       // the bytes from the logits' first value to their last
   int32_t seq, tokens, vocab;
   float c, inv_t, gscale;         // log2(e) / T, 1 / T, scale of the gradient
+  PerT per_t;
   Rows y;
   int32_t ydt;
   int64_t ignore;
@@ -737,7 +752,7 @@ __device__ __forceinline__ void make_list(const LossArgs& a, const List& l, cons
     const int at = (l.id[k] + r.lead) / kN<T> - v0;
     if (l.id[k] >= 0 && at >= 0 && at < v1 - v0) own += ex2(ref.exponent(l.x[k], a.c));
     // renormalised: exp((t - max) / T) / sum; with lse: exp(t / T - lse)
-    const float p = l.id[k] < 0 ? 0.f : a.lse.p == nullptr ? ex2((l.p[k] - sh) * a.c) : expf(l.p[k] * a.inv_t - lse);
+    const float p = l.id[k] < 0 ? 0.f : a.lse.p == nullptr ? ex2((l.p[k] - sh) * a.c) : expf(over_t(l.p[k], a.per_t) - lse);
     l.p[k] = p;
     sum += p;
   }
@@ -787,7 +802,7 @@ struct ListSums {
 __device__ __forceinline__ RowScale policy_scale(const LossArgs& a, const Values& v, const Ref& ref, float sum, float wrong, float w,
                                                  float& logp, float& loss) {
   RowScale out{ref.m, 0.f, 0.f, 0.f, 0.f, 0.f};
-  logp = v.y < 0 ? NAN : (v.x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+  logp = v.y < 0 ? NAN : over_t(v.x_at - ref.m, a.per_t) - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
   const Token t = policy_token(a, logp, v.in);
   loss = t.loss;
   out.more = w * a.gscale * a.inv_t * t.d;
@@ -810,11 +825,11 @@ __device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, 
   float loss = 0.f;
   for (int k = threadIdx.x & 31; k < a.top_k; k += 32) {
     const float p = list.p[k];
-    if (p != 0.f) loss += p * (logf(p) - ((list.x[k] - ref.m) * a.inv_t + d - log_s));
+    if (p != 0.f) loss += p * (logf(p) - (over_t(list.x[k] - ref.m, a.per_t) + d - log_s));
   }
   loss = warp_sum(loss);
   if (rest > 0.f)
-    loss += rest * (logf(rest) - ((s.off.m - ref.m) * a.inv_t + (logf(s.off_sum) - s.off.residue(a.c) * kLn2) - (log_s - d)));
+    loss += rest * (logf(rest) - (over_t(s.off.m - ref.m, a.per_t) + (logf(s.off_sum) - s.off.residue(a.c) * kLn2) - (log_s - d)));
   return loss / (a.inv_t * a.inv_t) + wrong;
 }
 // The loss from `n` parts, by the warp that adds the last: in a fixed order.
@@ -1527,7 +1542,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_loss_forward(const __grid_con
   sum = warp_sum(sum);
   const float wrong = fabsf(ref.m) == INFINITY ? NAN : 0.f;  // a row without a distribution
   if (lane == 0) {
-    a.logp[row] = (x_at - ref.m) * a.inv_t - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
+    a.logp[row] = over_t(x_at - ref.m, a.per_t) - logf(sum) + ref.residue(a.c) * kLn2 + wrong;
     if (a.stats != nullptr) a.stats[row] = make_float2(ref.m, sum + wrong);
   }
 }
@@ -1792,7 +1807,10 @@ LossArgs base_args(const loss_logits& x, const loss_targets* y, const loss_grad*
   a.tokens = static_cast<int32_t>(x.batch * x.seq);
   a.vocab = static_cast<int32_t>(x.vocab);
   a.c = static_cast<float>(1.4426950408889634 / x.temperature);
-  a.inv_t = static_cast<float>(1.0 / x.temperature);
+  const double per_t = 1.0 / x.temperature;
+  a.inv_t = a.per_t.hi = static_cast<float>(per_t);
+  if (per_t - a.per_t.hi < per_t * 0x1p-30) a.per_t.hi = std::nextafterf(a.per_t.hi, 0.f);
+  a.per_t.lo = static_cast<float>(per_t - a.per_t.hi);
   if (g != nullptr && g->p != nullptr) {
     a.g = g->p;
     a.gsb = g->stride_b;

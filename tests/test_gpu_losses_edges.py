@@ -232,3 +232,39 @@ def test_preference_pairs_with_a_bad_offset_answer_nan_in_every_value(average):
     # the first sequence's beginning
     out = meo.preference_loss(x, y, ref, seq_offsets=torch.tensor([-1, 4, 8, 12, 16]).cuda(), average=average)
     assert out.rewards.isnan().tolist() == [True, False, True, False]
+
+
+# ---- rounding that does not average out ---------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [1000, 8192, 50257])
+def test_log_probabilities_do_not_lean_with_the_rounding_of_1_over_t(vocab, dtype):
+    """1 / T held as one fp32 number would be off by a relative d that is the
+    same in every row: ln q would lean by d (z_y - m), and sums over tokens would
+    collect it.  Over 48 temperatures the mean error of 768 tokens (each rounded
+    by at most 5e-7, so the mean scatters by 1e-8) is fitted with that and with
+    what the rounding of log2(e) / T makes of the exponents.  d scatters by 3e-8
+    and z_y - m is 4 to 10: leaning would show as a slope of 1 with an error of
+    0.01 to 0.03.  The bar is 0.2."""
+    x, y = make(768, vocab, dtype, 11)
+    adv = torch.ones(768).cuda()
+    xd = x.double()
+    fits = {"token_logprobs": [], "policy_loss": []}
+    for k in range(48):
+        tau = 0.7 + 0.9 * (k * 0.6180339887498949 % 1.0)
+        z = xd / tau
+        lq = torch.log_softmax(z, 1)
+        want = lq.gather(1, y[:, None])[:, 0]
+        m = z.amax(1)
+        below = (lq.exp() * (m[:, None] - z)).sum(1).mean().item()
+        at = (z.gather(1, y[:, None])[:, 0] - m).mean().item()
+        c = np.log2(np.e) / tau
+        lean = [(np.float64(np.float32(c)) / c - 1) * below, (np.float64(np.float32(1 / tau)) * tau - 1) * at]
+        for name, got in (("token_logprobs", meo.token_logprobs(x, y, temperature=tau).logp),
+                          ("policy_loss", meo.policy_loss(x, y, adv, temperature=tau, need_grad=False).logp)):
+            fits[name].append([(got.double() - want).mean().item()] + lean)
+    for name, rows in fits.items():
+        rows = np.array(rows)
+        a = np.column_stack([np.ones(48), rows[:, 1:]])
+        slope = np.linalg.lstsq(a, rows[:, 0], rcond=None)[0][2]
+        assert abs(slope) < 0.2, (name, slope)
