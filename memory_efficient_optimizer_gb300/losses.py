@@ -134,8 +134,9 @@ def _targets(t, shape, device, ignore_index):
 
 
 def _is_cut(shape, st):
-    """Whole rows of sequences that are a few tokens longer."""
-    return st[1] == shape[2] and shape[1] * shape[2] < st[0] <= 2 * shape[1] * shape[2]
+    """Whole rows of sequences that are a few tokens longer: at most 4, and at
+    most an eighth, which is what a gradient with the gaps takes in memory."""
+    return st[1] == shape[2] and shape[1] * shape[2] < st[0] <= (shape[1] + min(4, shape[1] // 8)) * shape[2]
 
 
 def _gradient(logits, grad, need_grad, scale, device):

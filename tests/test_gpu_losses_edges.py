@@ -268,3 +268,39 @@ def test_log_probabilities_do_not_lean_with_the_rounding_of_1_over_t(vocab, dtyp
         a = np.column_stack([np.ones(48), rows[:, 1:]])
         slope = np.linalg.lstsq(a, rows[:, 0], rcond=None)[0][2]
         assert abs(slope) < 0.2, (name, slope)
+
+
+# ---- what the front end allocates, refuses and tells autograd ---------------------------
+
+def views(dtype, vocab):
+    """Logits as callers cut them out of a longer tensor, and whether the
+    default gradient may take the gaps' memory too."""
+    def buf(*shape):
+        g = torch.Generator().manual_seed(vocab)
+        return (torch.randn(*shape, vocab, generator=g) * 3).to(dtype).cuda()
+    return {"next token": (buf(3, 33)[:, :-1], True), "first half": (buf(3, 32)[:, :16], False),
+            "all but nine": (buf(3, 33)[:, :24], False), "one of two": (buf(3, 2)[:, :1], False),
+            "transposed": (buf(9, 3).transpose(0, 1), False), "whole": (buf(3, 9), False), "flat": (buf(9), False),
+            "repeated": (buf(1, 9).expand(3, 9, vocab), False)}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [64, 1001, 50257])
+def test_the_default_gradient_of_any_view(vocab, dtype):
+    """Right, and no larger than the logits' rows but for the few rows that a
+    next-token view leaves out."""
+    for name, (x, gaps) in views(dtype, vocab).items():
+        shape = x.shape[:-1]
+        tokens = shape.numel()
+        g = torch.Generator().manual_seed(2)
+        y = torch.randint(0, vocab, shape, generator=g).cuda()
+        d = torch.randn(shape, generator=g).cuda()
+        xn, yn, dn = f64(x).reshape(tokens, vocab), y.cpu().numpy().reshape(-1), flat(d)
+        r = meo.token_logprobs(x, y)
+        pol = o.policy(xn, yn, dn)
+        for got, ref, lead in ((meo.token_logprobs_backward(x, y, r.stats, d), o.logprobs_grad(xn, yn, dn), dn),
+                               (meo.policy_loss(x, y, d).grad, pol[3], pol[4])):
+            assert got.shape == x.shape, name
+            check_grad(f64(got).reshape(tokens, vocab), ref, lead, vocab, dtype)
+            rows = got.untyped_storage().nbytes() / (vocab * got.element_size())
+            assert rows <= tokens + (len(shape) * 4 if gaps else 0) + 1, (name, rows)
