@@ -11,7 +11,8 @@ respect to the logits, so that a training step is::
 ``grad=logits.detach()`` writes the gradient over the logits: then the step
 holds one tensor of that size where elementary operations hold several in fp32
 (autograd must not need the logits' values any more, which a linear layer does
-not).  ``need_grad=False`` gives the loss alone.
+not; where it does, as behind a tanh, ``backward`` raises as after any change
+in place).  ``need_grad=False`` gives the loss alone.
 
 As elsewhere in this package PyTorch only provides memory and streams: these
 functions check and marshal arguments, allocate the outputs and the workspace,
@@ -167,6 +168,12 @@ def _gradient(logits, grad, need_grad, scale, device):
     return grad, _GRAD.pack(grad.data_ptr(), st[0] if len(st) == 3 else 0, st[-2], scale)
 
 
+def _written(grad):
+    """Tells autograd of a caller's tensor that it has other values now."""
+    if grad is not None:
+        torch.autograd.graph.increment_version(grad)
+
+
 @functools.lru_cache(maxsize=4096)
 def _workspace_bytes(tokens, pairs):
     return B.loss_workspace_size(tokens, pairs)
@@ -211,6 +218,7 @@ def token_logprobs_backward(logits, targets, stats, grad_logp, *, temperature: f
     d = _ROWS.pack(*_rows("grad_logp", grad_logp, shape, dev))
     out, g = _gradient(logits, grad, True, grad_scale, dev)
     B.loss_token_logprobs_backward(x, y, stats.data_ptr(), d, g, _raw_stream(dev))
+    _written(grad)
     return out
 
 
@@ -251,6 +259,7 @@ def policy_loss(logits, targets, advantages, old_logp=None, ref_logp=None, *, cl
     ws, n = _workspace(shape, device)
     B.loss_policy(x, y, args, g, loss.data_ptr(), logp.data_ptr(), token.data_ptr(), ws.data_ptr(), n,
                   _raw_stream(dev))
+    _written(grad)
     return PolicyLoss(loss, out, logp, token)
 
 
@@ -309,6 +318,7 @@ def preference_loss(logits, targets, ref_logp=None, *, seq_offsets=None, beta: f
     ws, n = _workspace(shape, device, pairs)
     B.loss_preference(x, y, args, g, loss.data_ptr(), pair.data_ptr(), rewards.data_ptr(), logp.data_ptr(),
                       ws.data_ptr(), n, _raw_stream(dev))
+    _written(grad)
     return PreferenceLoss(loss, out, pair, rewards, logp)
 
 
@@ -353,6 +363,7 @@ def distill_loss(logits, teacher_ids, teacher_logits, teacher_lse=None, *, mask=
     token = torch.empty(shape, dtype=_FP32, device=device)
     ws, n = _workspace(shape, device)
     B.loss_distill(x, args, g, loss.data_ptr(), token.data_ptr(), ws.data_ptr(), n, _raw_stream(dev))
+    _written(grad)
     return DistillLoss(loss, out, token)
 
 

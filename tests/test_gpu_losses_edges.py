@@ -1,6 +1,8 @@
 """GPU parity of the losses (include/losses.h) at the edges of their formulas
 and of their arguments, and what one call may see of another.  The bars are
 those of test_gpu_losses.py, which derives them."""
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -304,3 +306,38 @@ def test_the_default_gradient_of_any_view(vocab, dtype):
             check_grad(f64(got).reshape(tokens, vocab), ref, lead, vocab, dtype)
             rows = got.untyped_storage().nbytes() / (vocab * got.element_size())
             assert rows <= tokens + (len(shape) * 4 if gaps else 0) + 1, (name, rows)
+
+
+def test_autograd_sees_that_the_logits_were_written():
+    """A model whose last operation keeps its output gets an error, not the
+    gradients of other values; one that does not, its gradients."""
+    y = torch.tensor([[1, 2], [3, -100]]).cuda()
+    a = torch.ones(2, 2).cuda()
+    ids = torch.tensor([[[1, 5], [2, 6]], [[3, 7], [4, 8]]]).cuda()
+    t = torch.tensor([1.0, 2.0]).cuda().expand(2, 2, 2)
+    calls = [lambda x, g: meo.policy_loss(x, y, a, grad=g), lambda x, g: meo.preference_loss(x, y, grad=g),
+             lambda x, g: meo.distill_loss(x, ids, t, grad=g),
+             lambda x, g: types.SimpleNamespace(grad=meo.token_logprobs_backward(x, y, meo.token_logprobs(x, y).stats, a,
+                                                                                 grad=g))]
+    weight = torch.randn(11, 6, generator=torch.Generator().manual_seed(1)).cuda()
+    hidden = torch.randn(2, 2, 6, generator=torch.Generator().manual_seed(2)).cuda()
+    for call in calls:
+        for cap in (False, True):
+            def logits():
+                w = weight.clone().requires_grad_(True)
+                x = torch.nn.functional.linear(hidden, w)
+                return w, torch.tanh(x) if cap else x
+            w, x = logits()
+            x.backward(call(x.detach(), None).grad)
+            want = w.grad
+            w, x = logits()
+            out = call(x.detach(), x.detach())
+            if cap:
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    x.backward(out.grad)
+            else:
+                x.backward(out.grad)
+                assert torch.equal(w.grad, want)
+    with torch.inference_mode():  # tensors without a version
+        x = torch.zeros(4, 10, device="cuda")
+        assert meo.policy_loss(x, y.view(-1), a.view(-1), grad=x).grad.isfinite().all()
