@@ -87,6 +87,8 @@ def _context(logits, stream):
     current (the library launches on the current device, and outputs and
     workspace are allocated for the stream that uses them); None if they are."""
     if stream is not None:
+        if isinstance(logits, torch.Tensor) and logits.is_cuda and stream.device.index != logits.get_device():
+            raise ValueError(f"stream is of {stream.device}, the logits are on {logits.device}")
         return torch.cuda.stream(stream)
     if isinstance(logits, torch.Tensor) and logits.is_cuda and logits.get_device() != _current_device():
         return torch.cuda.device(logits.device)

@@ -341,3 +341,16 @@ def test_autograd_sees_that_the_logits_were_written():
     with torch.inference_mode():  # tensors without a version
         x = torch.zeros(4, 10, device="cuda")
         assert meo.policy_loss(x, y.view(-1), a.view(-1), grad=x).grad.isfinite().all()
+
+
+def test_a_stream_of_another_device_is_refused():
+    x, y = make(4, 10, BF16)
+    a = torch.zeros(4).cuda()
+    other = types.SimpleNamespace(device=torch.device("cuda", 1), device_index=1)
+    for call in (lambda: meo.token_logprobs(x, y, stream=other), lambda: meo.policy_loss(x, y, a, stream=other),
+                 lambda: meo.token_logprobs_backward(x, y, torch.zeros(4, 2).cuda(), a, stream=other),
+                 lambda: meo.preference_loss(x[:, None], y[:, None], stream=other),
+                 lambda: meo.distill_loss(x, y[:, None], a[:, None], stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert meo.policy_loss(x, y, a, stream=torch.cuda.current_stream()).loss.isfinite()
