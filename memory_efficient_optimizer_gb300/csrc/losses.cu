@@ -1931,7 +1931,7 @@ Cut cut_row(int64_t tokens, int vecs, bool lists, int top_k, int sms) {
 struct Device {
   int sms = 0;
   unsigned* tickets = nullptr;           // g_tickets on this device
-  std::map<cudaStream_t, int> streams;   // of the streams that have one
+  std::map<unsigned long long, int> streams;  // of the streams that have one, by the stream's id
   std::map<std::pair<const void*, int64_t>, int> clusters;  // that run at a time, by kernel and cut
 };
 std::map<int, Device> g_devices;
@@ -2058,8 +2058,10 @@ adaf_status launch_grad(LossArgs a, int32_t dtype, cudaStream_t s) {
 // last CTA leaves it at 0; calls on one stream follow one another).  A call of
 // 400 tokens of 500 words takes 21.8 us so, 24.0 us with k_loss_count before
 // it, host time for the most part; beyond some hundred tokens a warp's counting
-// would hold the first row up.  A captured call may be replayed on any stream
-// and so takes the workspace's ticket.
+// would hold the first row up.  A stream is known by its id, which no other gets:
+// its handle may be another's once it is destroyed, while its last call still
+// runs.  Streams beyond the first 1024 and captured calls, which may be replayed
+// on any stream, take the workspace's ticket.
 constexpr int kFewTokens = 512;
 constexpr int kTickets = 1024;
 __device__ unsigned g_tickets[kTickets];
@@ -2072,7 +2074,12 @@ unsigned* stream_ticket(cudaStream_t s) {
     return nullptr;
   }
   int device = 0;
-  if (capturing != cudaStreamCaptureStatusNone || cudaGetDevice(&device) != cudaSuccess) return nullptr;
+  unsigned long long id = 0;
+  if (capturing != cudaStreamCaptureStatusNone) return nullptr;
+  if (cudaGetDevice(&device) != cudaSuccess || cudaStreamGetId(s, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
   std::lock_guard<std::mutex> lock(g_mu);
   Device& dev = g_devices[device];
   if (dev.tickets == nullptr && cudaGetSymbolAddress(reinterpret_cast<void**>(&dev.tickets), g_tickets) != cudaSuccess) {
@@ -2080,11 +2087,11 @@ unsigned* stream_ticket(cudaStream_t s) {
     dev.tickets = nullptr;
     return nullptr;
   }
-  const auto at = dev.streams.find(s);
+  const auto at = dev.streams.find(id);
   if (at != dev.streams.end()) return dev.tickets + at->second;
   const int slot = static_cast<int>(dev.streams.size());
   if (slot >= kTickets) return nullptr;
-  dev.streams[s] = slot;
+  dev.streams[id] = slot;
   return dev.tickets + slot;
 }
 

@@ -1,6 +1,7 @@
 """GPU parity of the losses (include/losses.h) at the edges of their formulas
 and of their arguments, and what one call may see of another.  The bars are
 those of test_gpu_losses.py, which derives them."""
+import ctypes
 import types
 
 import numpy as np
@@ -354,3 +355,37 @@ def test_a_stream_of_another_device_is_refused():
         with pytest.raises(ValueError, match="stream"):
             call()
     assert meo.policy_loss(x, y, a, stream=torch.cuda.current_stream()).loss.isfinite()
+
+
+def test_streams_that_come_and_go():
+    """A call for few tokens ends by a counter that is its stream's alone: a
+    stream destroyed with its call still waiting, new ones that may get its
+    handle, and more streams than there are counters."""
+    from memory_efficient_optimizer_gb300 import binding as B
+    cu = ctypes.CDLL("libcuda.so.1")
+    tokens, vocab = 40, 500
+    x, y = make(tokens, vocab, FP32, 3)
+    adv = per_token(tokens, 4)
+    want = meo.policy_loss(x, y, adv, need_grad=False).loss
+    n = B.loss_workspace_size(tokens)
+    calls = 1200
+    loss = torch.full((calls,), float("nan"), device="cuda")
+    work = torch.empty(calls, (n + 255) // 256 * 256, dtype=torch.uint8, device="cuda")
+    logits = B.loss_logits(x.data_ptr(), B.ADAF_FLOAT32, 1, tokens, vocab, 0, vocab, 1.0)
+    targets = B.loss_targets(B.loss_rows(y.data_ptr(), 0, 1), B.LOSS_INT64, -100)
+    none = B.loss_rows(None, 0, 0)
+    args = B.loss_policy_args(B.loss_rows(adv.data_ptr(), 0, 1), none, none, none, 0.2, 0.2, 0.0)
+    torch.cuda.synchronize()
+    handles = set()
+    for k in range(calls):
+        stream = ctypes.c_void_p()
+        assert cu.cuStreamCreate(ctypes.byref(stream), 1) == 0
+        handles.add(stream.value)
+        if k % 50 == 0:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream.value)):
+                torch.cuda._sleep(2000000)
+        B.loss_policy(logits, targets, args, B.loss_grad(None, 0, 0, 1.0), loss[k].data_ptr(), None, None,
+                      work[k].data_ptr(), n, stream.value)
+        assert cu.cuStreamDestroy_v2(stream) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(loss, want.expand(calls)), (len(handles), loss[loss != want][:4])
