@@ -188,9 +188,10 @@ adaf_status loss_preference(const loss_logits* x, const loss_targets* y, const l
 adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, const loss_grad* grad, float* loss,
                          float* token_loss, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Testing hook: while on, the bulk copies of loss_policy and loss_distill are
- * expected but not made, so that the kernel's waits for them run out (after
- * about a second each); the loss of such a call is NaN. */
+/* Testing hook: while on, the bulk copies of loss_policy and loss_distill calls
+ * of the calling thread are expected but not made, so that the kernel's waits
+ * for them run out (after about a second each); the loss of such a call is NaN.
+ * Other threads' calls are as ever. */
 void loss_debug_stall_copies(int32_t on);
 
 /* Per-kernel CUDA-event timing, as in adafactor.h. */

@@ -556,7 +556,7 @@ def loss_distill(x, args, grad, loss: int, token_loss: int, workspace: int, work
 
 
 def loss_debug_stall_copies(on: bool) -> None:
-    """Testing hook: the copies of the next calls are expected but not made (see the header)."""
+    """Testing hook: the copies of this thread's next calls are expected but not made (see the header)."""
     load().loss_debug_stall_copies(1 if on else 0)
 
 

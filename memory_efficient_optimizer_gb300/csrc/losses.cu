@@ -16,7 +16,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -1833,7 +1832,7 @@ struct ProfRecord {
 };
 std::mutex g_mu;
 bool g_profile = false;
-std::atomic<bool> g_stall{false};
+thread_local bool t_stall = false;
 std::vector<ProfRecord> g_prof;
 
 // Launches a kernel of this file; under profiling between two events.
@@ -2004,7 +2003,7 @@ adaf_status launch_rows(LossArgs a, int32_t dtype, cudaStream_t s) {
   lock.unlock();
   a.vecs_per_cta = cut.vecs_per_cta;
   a.slots = cut.slots;
-  a.stall = g_stall.load() ? 1 : 0;
+  a.stall = t_stall ? 1 : 0;
   return launch(kSlotRow, kernel, clusters * cut.cluster, threads, cut.shared, cut.cluster, a.count != nullptr, s, a);
 }
 adaf_status launch_forward(LossArgs a, int32_t dtype, cudaStream_t s) {
@@ -2308,7 +2307,7 @@ adaf_status loss_distill(const loss_logits* x, const loss_distill_args* args, co
   return launch_mean(a, kDistill, x->dtype, static_cast<cudaStream_t>(stream));
 }
 
-void loss_debug_stall_copies(int32_t on) { g_stall = on != 0; }
+void loss_debug_stall_copies(int32_t on) { t_stall = on != 0; }
 
 adaf_status loss_profile_enable(int32_t on) {
   std::lock_guard<std::mutex> lock(g_mu);

@@ -2,6 +2,7 @@
 and of their arguments, and what one call may see of another.  The bars are
 those of test_gpu_losses.py, which derives them."""
 import ctypes
+import threading
 import types
 
 import numpy as np
@@ -389,3 +390,21 @@ def test_streams_that_come_and_go():
         assert cu.cuStreamDestroy_v2(stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(loss, want.expand(calls)), (len(handles), loss[loss != want][:4])
+
+
+def test_a_test_of_stalled_copies_stays_in_its_thread():
+    from memory_efficient_optimizer_gb300 import binding as B
+    x, y = make(3, 40000, BF16, 4)
+    adv = per_token(3, 1)
+    want = meo.policy_loss(x, y, adv)
+    torch.cuda.synchronize()
+    got = []
+    B.loss_debug_stall_copies(True)
+    try:
+        other = threading.Thread(target=lambda: got.append(meo.policy_loss(x, y, adv)))
+        other.start()
+        other.join()
+    finally:
+        B.loss_debug_stall_copies(False)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0].loss, want.loss) and torch.equal(got[0].grad, want.grad)
