@@ -134,16 +134,19 @@ def test_a_row_in_the_ring_is_not_overwritten_while_it_is_read(op, tokens, vocab
 
 # ---- a student far from its teacher ------------------------------------------------
 
-def check_distill_far(out, x, ids, t, lse, tau, dtype):
-    """Against the oracle, word by word.  With L the largest |ln| of a listed
+def check_distill_words(out, x, ids, t, lse, tau, dtype, w=None):
+    """Against the oracle, word by word (without `lse` the rest is 0 and the
+    entries' own sum stands for it).  With L the largest |ln| of a listed
     word's or of the other words' probability, ln q and ln(others) are good to
-    ds + 4u L; a teacher's p to dp = 2^-22 + 4u (|t / T| + |lse|), and so is its
-    rest, absolutely.  The gradient on the list is T w (q (P + u) - p), off it
+    ds + 4u L; a teacher's p to dp = 2^-22 + 4u (|t / T| + |lse|) and the roundings
+    of a warp's sum of k entries, and so is its rest, absolutely.  The gradient on the list is T w (q (P + u) - p), off it
     T w (q (P + u) - u share), share a word's part of the unlisted mass: each
     product has its factors' relative errors and share u also the rest's."""
-    xn, ids, t, lse = f64(x), ids.cpu().numpy(), f64(t), f64(lse)
+    xn, ids, t, lse = f64(x), ids.cpu().numpy(), f64(t), None if lse is None else f64(lse)
     vocab = xn.shape[1]
-    want, token, grad, w = o.distill(xn, ids, t, lse, temperature=tau)
+    want, token, grad, w = o.distill(xn, ids, t, lse, temperature=tau, weights=None if w is None else f64(w))
+    rests = lse is not None
+    lse = lse if rests else np.logaddexp.reduce(t / tau, axis=1)
     e_token, bar = np.zeros(len(token)), np.zeros(xn.shape)
     for i in range(len(token)):
         lq = o.log_softmax(xn[i] / tau)
@@ -151,12 +154,12 @@ def check_distill_far(out, x, ids, t, lse, tau, dtype):
         off = np.ones(vocab, dtype=bool)
         off[ids[i]] = False
         l_off = np.logaddexp.reduce(lq[off])
-        rest = max(0.0, 1 - p.sum())
+        rest = max(0.0, 1 - p.sum()) if rests else 0.0
         far = max(np.abs(lq[ids[i]]).max(), abs(l_off))
-        dp = 2.0 ** -22 + 4 * U * (np.abs(t[i] / tau).max() + abs(lse[i])) + 32 * U
+        dp = 2.0 ** -22 + 4 * U * (np.abs(t[i] / tau).max() + abs(lse[i])) + (p.size / 32 + 24) * U
         rel = 6 * ds(vocab) + 4 * U * far
         e_token[i] = tau ** 2 * (2 * rel + dp * (far + 20))
-        share = np.where(off, np.exp(lq - l_off), 0.0)
+        share = np.where(off, np.exp(lq - l_off), 0.0) if rests else 0.0
         bar[i] = np.exp(lq) * (p.sum() + rest + dp) * (rel + dp) + share * (rest * rel + dp)
         bar[i, ids[i]] += p * (rel + dp)
     check("token_loss", f64(out.token_loss), token, e_token, 8 * U)
@@ -188,8 +191,8 @@ def test_distill_of_a_student_far_from_its_teacher(tau, gap, vocab, k, dtype):
     x, ids, t, lse = far_student(vocab, k, tau, gap, dtype)
     out = meo.distill_loss(x, ids, t, lse, temperature=tau)
     assert out.loss.isfinite() and out.grad.isfinite().all()
-    check_distill_far(out, x, ids, t, lse, tau, dtype)
-    check_distill_far(meo.distill_loss(x, ids, t, lse, temperature=tau, need_grad=False), x, ids, t, lse, tau, dtype)
+    check_distill_words(out, x, ids, t, lse, tau, dtype)
+    check_distill_words(meo.distill_loss(x, ids, t, lse, temperature=tau, need_grad=False), x, ids, t, lse, tau, dtype)
 
 
 def test_distill_small_rest_at_a_low_temperature():
@@ -198,7 +201,7 @@ def test_distill_small_rest_at_a_low_temperature():
     x, ids, t = x.cuda(), torch.tensor([[5, 700]]).cuda(), torch.tensor([[2.0, 1.0]]).cuda()
     lse = torch.logsumexp(t / 0.2, 1) + 0.2
     out = meo.distill_loss(x, ids, t, lse, temperature=0.2)
-    check_distill_far(out, x, ids, t, lse, 0.2, FP32)
+    check_distill_words(out, x, ids, t, lse, 0.2, FP32)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -208,7 +211,7 @@ def test_distill_far_students_in_many_rows_a_cluster(vocab, k, dtype):
     rows = [far_student(vocab, k, 0.5, gap, dtype) for gap in (0, 150)]
     x, ids, t, lse = (torch.cat([torch.stack([a, b], 1).flatten(0, 1)] * 200) for a, b in zip(*rows))
     first = meo.distill_loss(x[:8], ids[:8], t[:8], lse[:8], temperature=0.5)
-    check_distill_far(first, x[:8], ids[:8], t[:8], lse[:8], 0.5, dtype)
+    check_distill_words(first, x[:8], ids[:8], t[:8], lse[:8], 0.5, dtype)
     w = torch.full((1600,), 1 / 8.0, device="cuda")
     out = meo.distill_loss(x, ids, t, lse, temperature=0.5, weights=w)
     some = meo.distill_loss(x[800:1600], ids[800:1600], t[800:1600], lse[800:1600], temperature=0.5, weights=w[800:])
@@ -408,3 +411,118 @@ def test_a_test_of_stalled_copies_stays_in_its_thread():
         B.loss_debug_stall_copies(False)
     torch.cuda.synchronize()
     assert torch.equal(got[0].loss, want.loss) and torch.equal(got[0].grad, want.grad)
+
+
+# ---- every word, and every row of many -------------------------------------------------
+
+def check_words(got, ref, x, y, d, dtype, coef=0.0, d_rel=0.0, tau=1.0):
+    """The gradient d (1[j = y] - q) word by word: off the target relative to d q,
+    which has q's error (6 ds) and d's (`d_rel`, or `coef` of d absolutely); at
+    the target, where 1 - q cancels, 3 ds of d more."""
+    vocab = ref.shape[1]
+    q = np.exp(np.stack([o.log_softmax(row / tau) for row in f64(x)]))
+    q[y < 0] = 0.0
+    rows = np.flatnonzero(y >= 0)
+    part = q.copy()
+    part[rows, y[rows]] = 1 - q[rows, y[rows]]
+    bar = coef * part + 1e-37
+    bar[rows, y[rows]] += 3 * ds(vocab) * np.abs(d[rows])
+    check("grad", got, ref, bar, 6 * ds(vocab) + d_rel + (2 ** -8 if dtype is BF16 else 4 * U))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [33, 1000, 4099, 8193, 20011, 50257, 128256, 600011])
+def test_gradients_word_by_word(vocab, dtype):
+    x, y = make(6, vocab, dtype, vocab + 6, ignore=(2,))
+    xn, yn = f64(x), y.cpu().numpy()
+    d = per_token(6, 3)
+    r = meo.token_logprobs(x, y, temperature=1.3)
+    back = meo.token_logprobs_backward(x, y, r.stats, d, temperature=1.3)
+    check_words(f64(back), o.logprobs_grad(xn, yn, f64(d), 1.3), x, yn, f64(d) / 1.3, dtype, tau=1.3)
+    logp = o.token_logprobs(xn, yn)
+    old = torch.tensor(np.float32(logp - np.array([0.1, 0.6, 0, -0.5, -0.05, 0.1]))).cuda()
+    ref = torch.tensor(np.float32(logp + np.array([0.3, -0.2, 0, 0.5, -0.4, 0.01]))).cuda()
+    out = meo.policy_loss(x, y, d, old, ref, kl_coef=0.05)
+    n = o.policy(xn, yn, f64(d), f64(old), f64(ref), kl_coef=0.05)
+    # -r A + kl (1 - exp(ref - logp)): each part has the absolute error of logp
+    err = ds(vocab) + 4 * U * (2 * 40 + 40)
+    part = 1.5 * (2 * np.abs(f64(d)) + 0.05 * 2) * err / 5
+    check_words(f64(out.grad), n[3], x, yn, n[4], dtype, coef=part[:, None])
+    at = torch.tensor([0, 2, 4, 5, 6]).cuda()
+    out = meo.preference_loss(x, y, ref, seq_offsets=at, beta=0.3)
+    n = o.preference(xn, yn, [(0, 2), (2, 4), (4, 5), (5, 6)], f64(ref), beta=0.3)
+    # the coefficient moves by beta^2 / 4 of h's error, over two pairs
+    check_words(f64(out.grad), n[4], x, yn, n[5], dtype, coef=0.3 ** 2 / 4 / 2 * 4 * err)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab,k", [(33, 8), (1000, 20), (8193, 64), (20011, 319), (50257, 320), (128256, 64), (131073, 1024),
+                                     (600011, 20)])
+@pytest.mark.parametrize("tau,rest", [(1.0, True), (2.0, True), (0.7, False)])
+def test_distill_gradient_word_by_word(vocab, k, tau, rest, dtype):
+    x, ids, t, lse = far_student(vocab, k, tau, 0, dtype)
+    lse = lse if rest else None
+    check_distill_words(meo.distill_loss(x, ids, t, lse, temperature=tau), x, ids, t, lse, tau, dtype)
+
+
+MANY = [(2500, 1001, 9, BF16), (2500, 4099, 20, FP32), (2000, 20001, 300, FP32), (1500, 50257, 64, BF16), (900, 50257, 400, FP32),
+        (700, 128257, 64, BF16)]
+
+
+@pytest.mark.parametrize("tokens,vocab,k,dtype", MANY)
+def test_many_rows_in_place(tokens, vocab, k, dtype):
+    """Rows that share 16-byte granules with their neighbours, several to each
+    cluster, overwritten while the next ones are being copied."""
+    from test_gpu_losses import distill_inputs
+    x, y = make(tokens, vocab, dtype, 7, ignore=range(3, tokens, 7))
+    d = per_token(tokens, 5)
+    ids, t = distill_inputs(tokens, vocab, k, 8)
+    lse = torch.logsumexp(t, 1) + 0.2
+    for call in (lambda v, g: meo.policy_loss(v, y, d, grad=g),
+                 lambda v, g: meo.distill_loss(v, ids, t, lse, mask=y != -100, grad=g)):
+        want = call(x, None)
+        for _ in range(3):
+            z = x.clone()
+            got = call(z, z)
+            assert torch.equal(z, want.grad) and torch.equal(got.token_loss, want.token_loss)
+    r = meo.token_logprobs(x, y)
+    want = meo.token_logprobs_backward(x, y, r.stats, d)
+    z = x.clone()
+    assert torch.equal(meo.token_logprobs_backward(z, y, r.stats, d, grad=z), want)
+    at = torch.tensor([0, tokens // 3, tokens]).cuda()
+    want = meo.preference_loss(x, y, seq_offsets=at).grad
+    z = x.clone()
+    assert torch.equal(meo.preference_loss(z, y, seq_offsets=at, grad=z).grad, want)
+
+
+@pytest.mark.parametrize("tokens,vocab,k,dtype", MANY)
+def test_rows_of_a_large_call_are_those_of_smaller_ones(tokens, vocab, k, dtype):
+    """With weights a row's results hang on no other row: bit for bit in calls
+    that cut rows alike (short rows always, others from a CTA an SM on), and
+    within the bars in calls of a single row."""
+    from test_gpu_losses import distill_inputs
+    x, y = make(tokens, vocab, dtype, 7, ignore=range(3, tokens, 7))
+    d, w = per_token(tokens, 5), per_token(tokens, 6).abs()
+    ids, t = distill_inputs(tokens, vocab, k, 8)
+    lse = torch.logsumexp(t, 1) + 0.2
+    def policy(s):
+        return meo.policy_loss(x[s], y[s], d[s], weights=w[s])
+    def distill(s):
+        return meo.distill_loss(x[s], ids[s], t[s], lse[s], weights=w[s])
+    half = tokens // 2
+    for call in (policy, distill):
+        whole = call(slice(0, tokens))
+        for s in (slice(0, half), slice(half, tokens)):
+            part = call(s)
+            assert torch.equal(part.grad, whole.grad[s]) and torch.equal(part.token_loss, whole.token_loss[s])
+        for row in (0, 5, half - 1, tokens - 2):
+            one = call(slice(row, row + 1))
+            if vocab <= 8192 // (2 if dtype is FP32 else 1) - 8:
+                assert torch.equal(one.grad[0], whole.grad[row]) and torch.equal(one.token_loss[0], whole.token_loss[row])
+    for row in (0, 5, tokens - 2):
+        s = slice(row, row + 1)
+        one, n = policy(s), o.policy(f64(x[s]), y[s].cpu().numpy(), f64(d[s]), weights=f64(w[s]))
+        check_logp(f64(one.logp), n[2], vocab)
+        check_words(f64(one.grad), n[3], x[s], y[s].cpu().numpy(), n[4], dtype)
+        check_words(f64(policy(slice(0, tokens)).grad[s]), n[3], x[s], y[s].cpu().numpy(), n[4], dtype)
+        check_distill_words(distill(s), x[s], ids[s], t[s], lse[s], 1.0, dtype, w=w[s])
