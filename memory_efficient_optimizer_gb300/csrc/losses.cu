@@ -31,9 +31,9 @@ namespace {
 
 constexpr int kMaxWarps = 8;       // of a CTA of k_loss_row that sum
 // Lists of so many entries are made by two warps of a CTA in turn.  By one, two
-// warps 4096 rows of 128256 bf16 values take, with 64 entries 406, 417 us, 256
-// 508, 498, 320 585, 540, 500 799, 653, 1000 1451, 966; rows of 32000 with 256
-// 143, 147 us, 384 173, 166.
+// warps 4096 rows of 128256 bf16 values take, with 64 entries 420, 428 us, 256
+// 517, 509, 320 598, 551, 500 803, 662, 1000 1412, 957; rows of 32000 with 256
+// 150, 150 us, 384 181, 169.
 constexpr int kTwoListers = 320;
 constexpr int kGradThreads = 256;
 constexpr int kPairThreads = 256;
@@ -827,8 +827,13 @@ __device__ __forceinline__ float list_loss(const LossArgs& a, const List& list, 
     if (p != 0.f) loss += p * (logf(p) - (over_t(list.x[k] - ref.m, a.per_t) + d - log_s));
   }
   loss = warp_sum(loss);
-  if (rest > 0.f)
-    loss += rest * (logf(rest) - (over_t(s.off.m - ref.m, a.per_t) + (logf(s.off_sum) - s.off.residue(a.c) * kLn2) - (log_s - d)));
+  if (rest > 0.f) {
+    // The unlisted words' part of the row: one logarithm where fp32 holds it
+    // (the sum of four is rounded at their size, which showed in the loss).
+    const float part = s.off_sum * s.factor / s.sum;
+    loss += rest * (logf(rest) - (part > 1e-30f ? logf(part) : over_t(s.off.m - ref.m, a.per_t) +
+                                                                 (logf(s.off_sum) - s.off.residue(a.c) * kLn2) - (log_s - d)));
+  }
   return loss / (a.inv_t * a.inv_t) + wrong;
 }
 // The loss from `n` parts, by the warp that adds the last: in a fixed order.
@@ -952,16 +957,16 @@ struct Walk {
 // there are one or two more (LISTERS), which make those up to two rows ahead.
 // LONG: rows that no cluster keeps are read twice, from global memory.
 //
-// Bound by memory where rows are many: 8192 x 128256 bf16 values take 660 us,
-// 6.36 TB/s or 0.94 of the copy rate (ring of 6 x 16 KB a CTA, two CTAs an SM,
-// four CTAs a row); 3000 x 50256 fp32 191 us, 0.93; 4096 x 32000 bf16 93 us,
-// 0.83.  What it took: one CTA of 16 warps an SM 716 us; the parts exchanged
+// Bound by memory where rows are many: 8192 x 128256 bf16 values take 652 us,
+// 6.44 TB/s or 0.95 of the copy rate (ring of 6 x 16 KB a CTA, two CTAs an SM,
+// four CTAs a row); 3000 x 50256 fp32 195 us, 0.91; 4096 x 32000 bf16 95 us,
+// 0.82.  What it took: one CTA of 16 warps an SM 716 us; the parts exchanged
 // under the cluster's own barrier, whose release waits for every store before
 // it, 748; registers in place of the ring 1075.  With a list of 64 entries 4096
-// rows take 406 us, 0.76 (the policy loss 336), with 8 entries 379, with 1000
-// 966: reading the listed words' logits and writing their gradients takes
+// rows take 418 us, 0.74 (the policy loss 334), with 8 entries 389, with 1000
+// 963: reading the listed words' logits and writing their gradients takes
 // sectors of their own, and long lists are bound by the warps that make them.
-// 100 rows take 22 us, bound by one row's way through the warps (11 us).
+// 100 rows take 23 us, bound by one row's way through the warps (11 us).
 template <typename T, int OP, bool LONG, int LISTERS = OP == kDistill ? 1 : 0>
 __global__ void __launch_bounds__((kMaxWarps + 2 + LISTERS) * 32, 2)
     k_loss_row(const __grid_constant__ LossArgs a) {
@@ -1386,7 +1391,8 @@ __global__ void __launch_bounds__(32 * kShortWarps, 2) k_loss_short(const __grid
     const Row<T> r(static_cast<const T*>(a.x) + b * a.xsb + s * a.xss, a.vocab);
     const GradRow<T> g(a.g == nullptr ? nullptr : static_cast<T*>(a.g) + b * a.gsb + s * a.gss, a.vocab, r.lead);
     const int first = member * kOwn + lane;
-    // Read before it is known whether the row counts: one wait, not two.
+    // Read before it is known whether the row counts: one wait, not two.  (What
+    // is read of a row that does not is left alone.)
     uint4 w[kShortVecs];
     load_batch<T, 32>(w, r, first, r.vecs);
     Values v{row, kNoValue, true, {0.f, 0.f, 0.f}, 0.f, 0.f};
