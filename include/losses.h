@@ -39,8 +39,9 @@
  * element's own size is accepted.  2D logits are batch = 1.
  *
  * Tokens that do not count.  Where the target is ignore_index (or mask is 0)
- * the logits are not read, the token's loss and logp are 0 and its gradient
- * row is written as 0.  With no token left the loss is 0.  A token whose
+ * the logits may hold anything (rows of up to 1024 vectors of 16 bytes are read
+ * all the same, by policy and distill, longer ones are not), the token's loss
+ * and logp are 0 and its gradient row is written as 0.  With no token left the loss is 0.  A token whose
  * teacher lists nothing (every id -1) counts, with loss and gradient 0.
  *
  * Values.  Logits of -inf have probability 0; a term whose factor is 0 counts
@@ -48,13 +49,13 @@
  * with nothing but -inf, answers NaN in its own values, and so does a row
  * whose target (or a listed teacher id) lies outside the vocabulary, and one
  * whose teacher lists an id twice: bad data shows in the loss and reads or
- * writes nothing out of range.  Of the 16 bytes that hold a row's first or last
+ * writes nothing out of range.  A teacher's rest for which the student leaves
+ * nothing (no unlisted logit above -inf) is a loss of inf.  Of the 16 bytes that hold a row's first or last
  * value all are read where they lie within the logits' extent.
  *
  * Logits are fp32 or bf16 and the gradient has their type; everything between
  * is fp32 (sums over tokens with compensation), and gradients are rounded
- * once.  The sums
- * run in a fixed order: equal inputs give equal bits.
+ * once.  The sums run in a fixed order: equal inputs give equal bits.
  *
  * Every call only launches kernels on the caller's stream: it allocates
  * nothing on the device, waits for nothing and may be captured in a graph.
