@@ -16,11 +16,13 @@ from .came import Came, CameStep, came_step, init_came_state, make_came_hparams 
 from .lamb import Lamb, LambStep, init_lamb_state, lamb_step, make_lamb_hparams  # noqa: F401
 from .losses import (DistillLoss, PolicyLoss, PreferenceLoss, TokenLogprobs, distill_loss,  # noqa: F401
                      policy_loss, preference_loss, token_logprobs, token_logprobs_backward)
+from .muon import Muon, MuonStep, init_muon_state, make_muon_hparams, muon_step, orthogonalize  # noqa: F401
 from .optim import (Adafactor, AdafactorShardStep, AdafactorStep, adafactor_step,  # noqa: F401
                     init_state, make_hparams)
 
 __all__ = ["Adafactor", "AdafactorStep", "AdafactorShardStep", "AdafactorError", "adafactor_step", "init_state",
            "make_hparams", "library_path", "Lamb", "LambStep", "lamb_step", "init_lamb_state",
            "make_lamb_hparams", "Came", "CameStep", "came_step", "init_came_state", "make_came_hparams",
+           "Muon", "MuonStep", "muon_step", "init_muon_state", "make_muon_hparams", "orthogonalize",
            "TokenLogprobs", "PolicyLoss", "PreferenceLoss", "DistillLoss", "token_logprobs",
            "token_logprobs_backward", "policy_loss", "preference_loss", "distill_loss"]

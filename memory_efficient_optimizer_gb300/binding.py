@@ -49,6 +49,14 @@ LOSS_EXPORTS = (
     "loss_distill", "loss_debug_stall_copies", "loss_profile_enable", "loss_profile_read", "loss_num_kernels",
     "loss_kernel_name",
 )
+# Entry points declared in include/muon.h.
+MUON_EXPORTS = (
+    "muon_default_iteration", "muon_validate", "muon_validate_iteration", "muon_workspace_size",
+    "muon_orthogonalize_workspace_size", "muon_step", "muon_orthogonalize", "muon_device_status",
+    "muon_debug_stall_copies", "muon_profile_enable", "muon_profile_read", "muon_num_kernels", "muon_kernel_name",
+)
+MUON_MAX_STEPS = 16
+MUON_ADJUST = {"original": 0, "match_rms": 1}
 LOSS_INT32 = 0
 LOSS_INT64 = 1
 LOSS_MAX_TOP_K = 1024
@@ -145,6 +153,26 @@ class loss_distill_args(ctypes.Structure):
                 ("ids_stride_s", ctypes.c_int64), ("values", ctypes.c_void_p), ("values_dtype", ctypes.c_int32),
                 ("values_stride_b", ctypes.c_int64), ("values_stride_s", ctypes.c_int64), ("top_k", ctypes.c_int32),
                 ("lse", loss_rows), ("mask", loss_rows), ("weights", loss_rows)]
+
+
+class muon_tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("grad_dtype", ctypes.c_int32),
+                ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("momentum", ctypes.c_void_p)]
+
+
+class muon_iteration(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("coef", (ctypes.c_double * 3) * MUON_MAX_STEPS), ("eps", ctypes.c_double)]
+
+
+class muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("nesterov", ctypes.c_int32), ("adjust_lr", ctypes.c_int32), ("iteration", muon_iteration)]
+
+
+class muon_matrices(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("stride_b", ctypes.c_int64), ("stride_r", ctypes.c_int64)]
 
 
 class AdafactorError(RuntimeError):
@@ -282,6 +310,35 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.loss_num_kernels.argtypes = []
         lib.loss_kernel_name.restype = ctypes.c_char_p
         lib.loss_kernel_name.argtypes = [ctypes.c_int32]
+        lib.muon_default_iteration.restype = None
+        lib.muon_default_iteration.argtypes = [P(muon_iteration)]
+        lib.muon_validate.restype = ctypes.c_int
+        lib.muon_validate.argtypes = [P(muon_hparams)]
+        lib.muon_validate_iteration.restype = ctypes.c_int
+        lib.muon_validate_iteration.argtypes = [P(muon_iteration)]
+        lib.muon_workspace_size.restype = ctypes.c_int
+        lib.muon_workspace_size.argtypes = [P(muon_tensor), ctypes.c_int32, P(ctypes.c_size_t)]
+        lib.muon_orthogonalize_workspace_size.restype = ctypes.c_int
+        lib.muon_orthogonalize_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                          P(ctypes.c_size_t)]
+        lib.muon_step.restype = ctypes.c_int
+        lib.muon_step.argtypes = [P(muon_tensor), ctypes.c_int32, P(muon_hparams), ctypes.c_void_p, ctypes.c_size_t,
+                                  ctypes.c_void_p]
+        lib.muon_orthogonalize.restype = ctypes.c_int
+        lib.muon_orthogonalize.argtypes = [P(muon_matrices), P(muon_iteration), ctypes.c_void_p, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.muon_device_status.restype = ctypes.c_int
+        lib.muon_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, P(ctypes.c_int32)]
+        lib.muon_debug_stall_copies.restype = None
+        lib.muon_debug_stall_copies.argtypes = [ctypes.c_int32]
+        lib.muon_profile_enable.restype = ctypes.c_int
+        lib.muon_profile_enable.argtypes = [ctypes.c_int32]
+        lib.muon_profile_read.restype = ctypes.c_int
+        lib.muon_profile_read.argtypes = [P(ctypes.c_double), P(ctypes.c_int64), ctypes.c_int32]
+        lib.muon_num_kernels.restype = ctypes.c_int32
+        lib.muon_num_kernels.argtypes = []
+        lib.muon_kernel_name.restype = ctypes.c_char_p
+        lib.muon_kernel_name.argtypes = [ctypes.c_int32]
         _lib = lib
         return lib
 
@@ -579,3 +636,71 @@ def loss_profile_read() -> dict:
     launches = (ctypes.c_int64 * nk)()
     _check(load().loss_profile_read(ms, launches, nk))
     return {loss_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}
+
+
+def muon_default_iteration() -> muon_iteration:
+    it = muon_iteration()
+    load().muon_default_iteration(ctypes.byref(it))
+    return it
+
+
+def muon_validate(hp: muon_hparams) -> None:
+    _check(load().muon_validate(ctypes.byref(hp)))
+
+
+def muon_validate_iteration(it: muon_iteration) -> None:
+    _check(load().muon_validate_iteration(ctypes.byref(it)))
+
+
+def muon_workspace_size(tensors, n: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().muon_workspace_size(tensors, n, ctypes.byref(out)))
+    return int(out.value)
+
+
+def muon_orthogonalize_workspace_size(batch: int, rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().muon_orthogonalize_workspace_size(batch, rows, cols, ctypes.byref(out)))
+    return int(out.value)
+
+
+def muon_step(tensors, n: int, hp: muon_hparams, workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(load().muon_step(tensors, n, ctypes.byref(hp), workspace, workspace_bytes, stream))
+
+
+def muon_orthogonalize(x: muon_matrices, it: muon_iteration, out: int, out_dtype: int, workspace: int,
+                       workspace_bytes: int, stream: int) -> None:
+    _check(load().muon_orthogonalize(ctypes.byref(x), ctypes.byref(it), out, out_dtype, workspace, workspace_bytes,
+                                     stream))
+
+
+def muon_device_status(workspace: int, stream: int) -> int:
+    out = ctypes.c_int32()
+    _check(load().muon_device_status(workspace, stream, ctypes.byref(out)))
+    return int(out.value)
+
+
+def muon_debug_stall_copies(on: bool) -> None:
+    """Testing hook: the copies of this thread's next calls are expected but not made (see the header)."""
+    load().muon_debug_stall_copies(1 if on else 0)
+
+
+def muon_profile_enable(on: bool) -> None:
+    _check(load().muon_profile_enable(1 if on else 0))
+
+
+def muon_num_kernels() -> int:
+    return int(load().muon_num_kernels())
+
+
+def muon_kernel_name(k: int) -> str:
+    return load().muon_kernel_name(int(k)).decode()
+
+
+def muon_profile_read() -> dict:
+    """{kernel name: (total ms, launches)} for the Muon events recorded since the last read."""
+    nk = muon_num_kernels()
+    ms = (ctypes.c_double * nk)()
+    launches = (ctypes.c_int64 * nk)()
+    _check(load().muon_profile_read(ms, launches, nk))
+    return {muon_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}

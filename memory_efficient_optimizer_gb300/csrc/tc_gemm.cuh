@@ -1,0 +1,419 @@
+// Products of matrices on the tensor cores of sm_103a, with the work on each
+// result tile given by the caller (the "ending").
+//
+//   D[b][i, j] = sum over k of A[b][i, k] B[b][j, k]
+//
+// A and B are 16-bit (both fp16 or both bf16), each either with k innermost
+// ("K-major") or with i or j innermost ("MN-major"); sums are fp32.
+//
+// Layout.  A tile of the result is 128 CG rows by BN columns, CG = 2: the two
+// CTAs of a cluster work on one tile with tcgen05 instructions that read both
+// CTAs' shared memory, so each CTA loads its own 128 rows of A and half of the
+// tile's columns of B, half of what two CTAs apart would.  A persistent grid
+// walks the tiles.  In a CTA
+//
+//   warp 0     copies the operands' tiles of 64 k values into a ring of
+//              stages (TMA, 128-byte swizzle; it also zero-fills what lies
+//              beyond the matrices, so no size has to be a multiple of anything)
+//   warp 1     issues the products (one thread, of the cluster's first CTA)
+//   warp 2     holds the tensor memory
+//   warps 4..  take the finished tile out of tensor memory (the ending), while
+//              the next tile is summed in the other half of it
+//
+// What bounds it: at 256 x 256 x 64 a CTA's stage is 32 KB for 512 cycles of
+// the tensor cores, 64 bytes a cycle, which L2 just gives; smaller tiles are
+// bound by those copies and are taken where there are too few large ones.
+//
+// Every wait is bounded.  One that runs out sets the kernel's status word and
+// the CTA's flag: its tiles' values are NaN from then on, nothing more is
+// waited for, and the CTA ends after its copies have had time to land.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace meo {
+namespace tc {
+namespace {
+
+constexpr int kBlockK = 64;        // k values of a stage: 128 bytes, the swizzle's width
+constexpr int kTileM = 128;        // rows of a CTA
+constexpr int kEndWarps = 8;       // two groups of four warps, each half of the columns
+constexpr int kThreads = 128 + 32 * kEndWarps;
+constexpr long long kWaitCycles = 2000000000LL;   // about a second
+
+__device__ __forceinline__ uint32_t shared_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t arrivals) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_at(bar)), "r"(arrivals) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_at(bar)), "r"(bytes) : "memory");
+}
+// Address of the same place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(shared_at(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- tcgen05 ------------------------------------------------------------------------
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_at(where)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_at(where)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  const uint32_t p = add ? 1u : 0u;
+  if constexpr (CG == 2)
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(p)
+                 : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(p)
+                 : "memory");
+}
+// `bar` (of both CTAs of a pair) gets one arrival when the products issued before are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     shared_at(bar)),
+                 "h"(static_cast<uint16_t>(3))
+                 : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_at(bar)) : "memory");
+}
+// 32 columns of the warp's 32 lanes (rows).
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+      "%26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Descriptor of an operand in shared memory, 128-byte swizzle: rows of 128 bytes,
+// groups of 8 rows 1024 bytes apart (`sbo`).  K-major: a row is 64 k values of one
+// i or j.  MN-major: a row is 64 i or j of one k; blocks of 64 i or j `lbo` apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            to),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     to),
+                 "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+                 : "memory");
+}
+
+// ---- the product --------------------------------------------------------------------
+struct Shape {
+  int32_t m, n, k;         // of one matrix of the batch
+  int32_t batch;
+  int32_t splits;          // parts of k, each a result of its own
+  int32_t group;           // tiles are walked in groups of so many rows of tiles
+  const int32_t* m_live;   // not NULL: the rows that count (on the device) are *m_live - first, at most m
+  const int32_t* k_live;   // the same for k
+  int32_t first;
+  int32_t* status;         // bit 0: a wait ran out
+  int32_t stall;           // testing: make no copies
+};
+
+struct Tile {
+  int32_t batch, split, m0, n0;   // the cluster tile's first row and column
+  bool mirror;                    // symmetric results: the tile above the diagonal stands for the one below too
+};
+
+// What an ending is given: a row of the result a thread, and the columns of its group.
+struct Part {
+  Tile tile;
+  int32_t row;            // of the result
+  int32_t col, cols;      // its columns: col, ..., col + cols - 1 (a multiple of 32)
+  int32_t m, n;
+  uint32_t tmem;
+  bool zero, bad;         // there was nothing to sum; a wait ran out
+  __device__ __forceinline__ void load(int c, float (&v)[32]) const {
+    tmem_load(tmem + c, v);
+    if (zero || bad) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = bad ? __int_as_float(0x7fc00000) : 0.f;
+    }
+  }
+};
+
+__device__ __forceinline__ int live(const int32_t* p, int32_t first, int32_t most) {
+  if (p == nullptr) return most;
+  const int n = *p - first;
+  return n < 0 ? 0 : n < most ? n : most;
+}
+
+// The tile of number i; false beyond the last.
+template <bool SYM>
+__device__ __forceinline__ bool tile_of(int64_t i, int mt, int nt, const Shape& s, int tm, int tn, Tile* t) {
+  const int64_t per = SYM ? static_cast<int64_t>(mt) * (mt + 1) / 2 : static_cast<int64_t>(mt) * nt * s.splits;
+  if (per == 0 || i >= per * s.batch) return false;
+  t->batch = static_cast<int>(i / per);
+  int r = static_cast<int>(i - t->batch * per);
+  if constexpr (SYM) {
+    // column by column of the upper triangle: column c holds rows 0 .. c
+    int c = static_cast<int>((sqrtf(8.f * static_cast<float>(r) + 1.f) - 1.f) * 0.5f);
+    while (c * (c + 1) / 2 > r) --c;
+    while ((c + 1) * (c + 2) / 2 <= r) ++c;
+    r -= c * (c + 1) / 2;
+    t->m0 = r * tm;
+    t->n0 = c * tn;
+    t->split = 0;
+    t->mirror = r != c;
+  } else {
+    t->split = r / (mt * nt);
+    r -= t->split * (mt * nt);
+    const int g = r / (s.group * nt);            // group of rows of tiles
+    const int left = mt - g * s.group, high = left < s.group ? left : s.group;
+    r -= g * s.group * nt;
+    t->n0 = r / high * tn;
+    t->m0 = (g * s.group + r % high) * tm;
+    t->mirror = false;
+  }
+  return true;
+}
+
+template <int CG, int BN, int STAGES>
+struct Shared {
+  static constexpr int kA = kTileM * kBlockK * 2;        // bytes of a stage of a CTA
+  static constexpr int kB = BN / CG * kBlockK * 2;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kBars = 2 * STAGES + 4;
+  static constexpr int bytes = STAGES * kStage + kBars * 8 + 64 + 1024;   // and the alignment to 1024
+};
+
+// End: what is done with a result tile.
+//   static constexpr bool kSym; struct Args; static __device__ void part(const Args&, const Part&)
+template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape s,
+              const typename End::Args end) {
+  using S = Shared<CG, BN, STAGES>;
+  constexpr uint32_t kCols = 2 * BN;      // two accumulators
+  constexpr int kBCta = BN / CG;          // rows of B (columns of the result) that a CTA loads
+  extern __shared__ unsigned char raw[];
+  unsigned char* ring = raw + ((1024 - (shared_at(raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + STAGES * S::kStage);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sum_full = empty + STAGES;
+  uint64_t* sum_empty = sum_full + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sum_empty + 2);
+  volatile int* off = reinterpret_cast<volatile int*>(tmem_at + 1);   // a wait of this CTA ran out
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int m = live(s.m_live, s.first, s.m), k_all = live(s.k_live, s.first, s.k);
+  const int mt = (m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
+  const int blocks = (k_all + kBlockK - 1) / kBlockK, per_split = (blocks + s.splits - 1) / s.splits;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(full + i, 1);
+      bar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(sum_full + i, 1);
+      bar_init(sum_empty + i, CG * kEndWarps);
+    }
+    *off = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  // False if the wait ran out, or another of the CTA's had before.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (bar_try(bar, parity)) return true;
+    const long long from = clock64();
+    while (!bar_try(bar, parity)) {
+      if (*off != 0) return false;
+      if (clock64() - from > kWaitCycles) {
+        *off = 1;
+        atomicOr(s.status, 1);
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- copies
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Tile t;
+      for (int64_t i = first; ok && tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &t); i += step) {
+        const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
+        const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
+        for (int kb = b0; kb < b1; ++kb) {
+          if (!(ok = wait(empty + stage, phase ^ 1))) break;
+          const uint32_t a = shared_at(ring + stage * S::kStage), b = a + S::kA;
+          uint32_t bar = shared_at(full + stage);
+          if (rank == 0) bar_expect(full + stage, S::kStage * CG);
+          if constexpr (CG == 2) bar = at_rank(bar, 0);
+          const int k = kb * kBlockK;
+          if (s.stall == 0) {
+            if constexpr (A_MN) {
+#pragma unroll
+              for (int j = 0; j < kTileM / 64; ++j) tma_load<CG>(a + j * 64 * kBlockK * 2, &map_a, am + j * 64, k, t.batch, bar);
+            } else {
+              tma_load<CG>(a, &map_a, k, am, t.batch, bar);
+            }
+            if constexpr (B_MN) {
+#pragma unroll
+              for (int j = 0; j < kBCta / 64; ++j) tma_load<CG>(b + j * 64 * kBlockK * 2, &map_b, bn + j * 64, k, t.batch, bar);
+            } else {
+              tma_load<CG>(b, &map_b, k, bn, t.batch, bar);
+            }
+          }
+          if (++stage == STAGES) stage = 0, phase ^= 1;
+        }
+      }
+      // The products' last arrivals have to find this CTA's barriers there.
+      for (int i = 0; ok && i < STAGES; ++i) {
+        ok = wait(empty + stage, phase ^ 1);
+        if (++stage == STAGES) stage = 0, phase ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---- products
+      constexpr uint32_t idesc = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((A_MN ? 1u : 0u) << 15) |
+                                 ((B_MN ? 1u : 0u) << 16) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
+      constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;   // bytes of 16 k values
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      Tile t;
+      for (int64_t i = first; ok && tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &t); i += step) {
+        const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
+        if (!(ok = wait(sum_empty + acc, acc_phase ^ 1))) break;
+        fence_after();
+        for (int kb = b0; kb < b1; ++kb) {
+          if (!(ok = wait(full + stage, phase))) break;
+          fence_after();
+          const uint32_t a = shared_at(ring + stage * S::kStage), b = a + S::kA;
+#pragma unroll
+          for (int j = 0; j < kBlockK / 16; ++j)
+            mma<CG>(tmem + acc * BN, operand(a + j * a_step, A_MN ? 64 * kBlockK * 2 : 16, 1024),
+                    operand(b + j * b_step, B_MN ? 64 * kBlockK * 2 : 16, 1024), idesc, kb > b0 || j > 0);
+          commit<CG>(empty + stage);
+          if (++stage == STAGES) stage = 0, phase ^= 1;
+        }
+        if (!ok) break;
+        commit<CG>(sum_full + acc);
+        if (++acc == 2) acc = 0, acc_phase ^= 1;
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- endings
+    const int group = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    Part p;
+    p.m = m;
+    p.n = s.n;
+    p.bad = false;
+    for (int64_t i = first; tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &p.tile); i += step) {
+      const int b0 = p.tile.split * per_split;
+      const bool ok = wait(sum_full + acc, acc_phase);
+      p.bad = __any_sync(0xffffffffu, !ok) || p.bad;
+      fence_after();
+      p.zero = min(blocks, b0 + per_split) <= b0;
+      p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
+      p.cols = BN / 2;
+      p.col = p.tile.n0 + group * p.cols;
+      p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
+      End::part(end, p);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
+      if (++acc == 2) acc = 0, acc_phase ^= 1;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (*off != 0 && threadIdx.x == 0) {
+    // Copies and products that were under way when a wait ran out: they are done in microseconds.
+    const long long from = clock64();
+    while (clock64() - from < 2000000) {
+    }
+  }
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 2) tmem_free<CG>(tmem, kCols);
+}
+
+}  // namespace
+}  // namespace tc
+}  // namespace meo
