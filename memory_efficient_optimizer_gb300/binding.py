@@ -1,5 +1,6 @@
 """ctypes binding of the C ABI in include/adafactor.h, include/lamb.h,
-include/came.h and include/losses.h (argument marshalling only).
+include/came.h, include/losses.h, include/muon.h and include/linear_ce.h
+(argument marshalling only).
 
 Every function here has the name of the C entry point it calls and does no
 arithmetic of the method: all of the step runs in the CUDA library.  Loading
@@ -54,6 +55,11 @@ MUON_EXPORTS = (
     "muon_default_iteration", "muon_validate", "muon_validate_iteration", "muon_workspace_size",
     "muon_orthogonalize_workspace_size", "muon_step", "muon_orthogonalize", "muon_device_status",
     "muon_debug_stall_copies", "muon_profile_enable", "muon_profile_read", "muon_num_kernels", "muon_kernel_name",
+)
+# Entry points declared in include/linear_ce.h.
+LINEAR_CE_EXPORTS = (
+    "linear_ce_workspace_size", "linear_ce", "linear_ce_debug_stall_copies", "linear_ce_profile_enable",
+    "linear_ce_profile_read", "linear_ce_num_kernels", "linear_ce_kernel_name",
 )
 MUON_MAX_STEPS = 16
 MUON_ADJUST = {"original": 0, "match_rms": 1}
@@ -173,6 +179,21 @@ class muon_hparams(ctypes.Structure):
 class muon_matrices(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("stride_b", ctypes.c_int64), ("stride_r", ctypes.c_int64)]
+
+
+class linear_ce_hidden(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64), ("seq", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64)]
+
+
+class linear_ce_weight(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int64),
+                ("stride_v", ctypes.c_int64), ("accumulate", ctypes.c_int32)]
+
+
+class linear_ce_args(ctypes.Structure):
+    _fields_ = [("weights", loss_rows), ("temperature", ctypes.c_double), ("z_loss", ctypes.c_double),
+                ("grad_scale", ctypes.c_double)]
 
 
 class AdafactorError(RuntimeError):
@@ -339,6 +360,23 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.muon_num_kernels.argtypes = []
         lib.muon_kernel_name.restype = ctypes.c_char_p
         lib.muon_kernel_name.argtypes = [ctypes.c_int32]
+        lib.linear_ce_workspace_size.restype = ctypes.c_int
+        lib.linear_ce_workspace_size.argtypes = [P(linear_ce_hidden), P(linear_ce_weight), P(linear_ce_hidden),
+                                                 P(linear_ce_weight), P(ctypes.c_size_t)]
+        lib.linear_ce.restype = ctypes.c_int
+        lib.linear_ce.argtypes = [P(linear_ce_hidden), P(linear_ce_weight), P(loss_targets), P(linear_ce_args),
+                                  P(linear_ce_hidden), P(linear_ce_weight), ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        lib.linear_ce_debug_stall_copies.restype = None
+        lib.linear_ce_debug_stall_copies.argtypes = [ctypes.c_int32]
+        lib.linear_ce_profile_enable.restype = ctypes.c_int
+        lib.linear_ce_profile_enable.argtypes = [ctypes.c_int32]
+        lib.linear_ce_profile_read.restype = ctypes.c_int
+        lib.linear_ce_profile_read.argtypes = [P(ctypes.c_double), P(ctypes.c_int64), ctypes.c_int32]
+        lib.linear_ce_num_kernels.restype = ctypes.c_int32
+        lib.linear_ce_num_kernels.argtypes = []
+        lib.linear_ce_kernel_name.restype = ctypes.c_char_p
+        lib.linear_ce_kernel_name.argtypes = [ctypes.c_int32]
         _lib = lib
         return lib
 
@@ -704,3 +742,41 @@ def muon_profile_read() -> dict:
     launches = (ctypes.c_int64 * nk)()
     _check(load().muon_profile_read(ms, launches, nk))
     return {muon_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}
+
+
+def linear_ce_workspace_size(hidden, weight, grad_hidden=None, grad_weight=None) -> int:
+    out = ctypes.c_size_t()
+    _check(load().linear_ce_workspace_size(hidden, weight, grad_hidden, grad_weight, ctypes.byref(out)))
+    return int(out.value)
+
+
+def linear_ce(hidden, weight, targets, args, grad_hidden, grad_weight, loss: int, logp: int, lse: int, workspace: int,
+              workspace_bytes: int, stream: int) -> None:
+    _check(load().linear_ce(hidden, weight, targets, args, grad_hidden, grad_weight, loss, logp, lse, workspace,
+                            workspace_bytes, stream))
+
+
+def linear_ce_debug_stall_copies(on: bool) -> None:
+    """Testing hook: the copies of this thread's next calls are expected but not made (see the header)."""
+    load().linear_ce_debug_stall_copies(1 if on else 0)
+
+
+def linear_ce_profile_enable(on: bool) -> None:
+    _check(load().linear_ce_profile_enable(1 if on else 0))
+
+
+def linear_ce_num_kernels() -> int:
+    return int(load().linear_ce_num_kernels())
+
+
+def linear_ce_kernel_name(k: int) -> str:
+    return load().linear_ce_kernel_name(int(k)).decode()
+
+
+def linear_ce_profile_read() -> dict:
+    """{kernel name: (total ms, launches)} for the events of linear_ce recorded since the last read."""
+    nk = linear_ce_num_kernels()
+    ms = (ctypes.c_double * nk)()
+    launches = (ctypes.c_int64 * nk)()
+    _check(load().linear_ce_profile_read(ms, launches, nk))
+    return {linear_ce_kernel_name(k): (float(ms[k]), int(launches[k])) for k in range(nk)}

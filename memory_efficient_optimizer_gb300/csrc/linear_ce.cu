@@ -1,0 +1,881 @@
+// Cross entropy of a linear output layer for sm_103a, with the gradients of the
+// hidden states and the weight: the C ABI of include/linear_ce.h.
+//
+//   k_lce_scan         which tokens count, in order; how many
+//   k_lce_gather       their hidden states side by side, in bf16; zeros for the others' gradients
+//   k_lce_weight       the weight as the products read it, where it is not already
+//   then for every piece of tokens
+//   k_lce_logits       x = h W^T.  The ending reduces a row's 128 words to a power of two 2^I >= their
+//                      largest exponential and s = sum 2^(x c - I) over the words but the target, and
+//                      keeps 2^(x c - I) in fp16 (c = log2(e) / T); the logits themselves are not kept
+//   k_lce_rows         a token's I and s over the vocabulary, its lse and logp, and dx in bf16 over
+//                      the exponentials: one read and one write of them
+//   k_lce_grad_hidden  dx W, in parts of the vocabulary where there are few tiles
+//   k_lce_join         the parts' sum
+//   k_lce_grad_weight  dx^T h
+//   k_lce_loss         the tokens' sum
+//
+// Why exponentials are kept and not computed again: the products are all but the
+// whole time (2 T D V flops each), and to compute x twice is a fourth beside the
+// three that have to be; keeping 16 bits of it costs 4 bytes a word and token of
+// memory traffic (0.6 of 16 ms at 8192 tokens of 128256 words).
+//
+// Rounding.  An exponential is kept as 2^(x c - I + 15) in fp16: 2^-12 relative
+// down to 2^-29 of the largest of its 128 words, and below that an error of 2^-40
+// of it.  A power of two moves it to the row's scale exactly.  dx is rounded to
+// bf16 once; under a mean it is kept without the mean's factor, whose rounding
+// would lean the same way in every token's target (the gradients were up to
+// 3.3e-3 off for it, 2.1e-3 without).  The sum over the words without the target,
+// R, is kept apart from the target's exponential E: its own dx is -R / (R + E), not
+// 1 less a rounded q, and logp = -ln(1 + R / E), so a token that is nearly certain
+// has both to the last bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "adafactor_internal.h"
+#include "linear_ce.h"
+#include "tc_host.cuh"
+
+namespace {
+
+using meo::tc::Part;
+using meo::tc::Shape;
+
+constexpr int64_t kMaxTokens = int64_t{1} << 26, kMaxDim = int64_t{1} << 16, kMaxVocab = int64_t{1} << 21;
+constexpr int64_t kPieceBytes = int64_t{1} << 31;   // of a piece's exponentials
+constexpr int kSpan = 128;                          // words of one I and s
+constexpr int kScanThreads = 1024, kScanEach = 8;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1e30f;                     // I of a span without words
+constexpr int kIgnored = -1, kBad = -2;
+
+struct Rows {
+  const void* p;
+  int64_t sb, ss;
+};
+
+struct CeArgs {
+  const void* h;
+  int32_t h_bf16, g_bf16;
+  int64_t hsb, hss, gsb, gss;
+  void* g;                   // the hidden states' gradient; NULL: none
+  Rows y;
+  int32_t y64;
+  int64_t ignore;
+  Rows w;                    // NULL: the mean
+  int32_t tokens, seq, dim, vocab;
+  int32_t ldh, lde, spans;   // of the gathered hidden states, of the exponentials; spans of a row
+  int32_t first, rows;       // the piece: its first row, rows that it has room for
+  float c_hi, c_lo, inv_t, z_loss, scale;
+  int32_t* count;            // tokens that count
+  int32_t* status;
+  int32_t* token;            // [rows] which token a row is
+  int32_t* target;           // [rows]
+  __nv_bfloat16* hc;         // [rows][ldh]
+  float* xt;                 // [rows of a piece]: the target's logit
+  float2* stat;              // [rows of a piece][spans]
+  unsigned short* e;         // [rows of a piece][lde]; NULL: no gradient
+  float* part;               // [rows] w (z_loss lse^2 - logp)
+  float* loss;
+  float* logp;
+  float* lse;
+};
+
+__device__ __forceinline__ int64_t place(int t, int seq, int64_t sb, int64_t ss) {
+  const int b = t / seq;
+  return b * sb + (t - b * seq) * ss;
+}
+__device__ __forceinline__ int target_of(const CeArgs& a, int t) {
+  const int64_t at = place(t, a.seq, a.y.sb, a.y.ss);
+  const int64_t y = a.y64 ? static_cast<const int64_t*>(a.y.p)[at] : static_cast<const int32_t*>(a.y.p)[at];
+  return y == a.ignore ? kIgnored : y < 0 || y >= a.vocab ? kBad : static_cast<int>(y);
+}
+
+// ---- tokens ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kScanThreads) k_lce_scan(const CeArgs a) {
+  __shared__ int warps[32];
+  __shared__ int total;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += kScanThreads * kScanEach) {
+    int y[kScanEach], n = 0;
+    const int64_t mine = t0 + threadIdx.x * kScanEach;
+#pragma unroll
+    for (int i = 0; i < kScanEach; ++i) {
+      y[i] = mine + i < a.tokens ? target_of(a, static_cast<int>(mine + i)) : kIgnored;
+      n += y[i] != kIgnored;
+    }
+    int up = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += v;
+    }
+    if (lane == 31) warps[warp] = up;
+    __syncthreads();
+    if (warp == 0) {
+      int v = warps[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      warps[lane] = v;
+      if (lane == 31) total = v;
+    }
+    __syncthreads();
+    int at = base + (warp ? warps[warp - 1] : 0) + up - n;
+#pragma unroll
+    for (int i = 0; i < kScanEach; ++i)
+      if (y[i] != kIgnored) {
+        a.token[at] = static_cast<int>(mine + i);
+        a.target[at++] = y[i];
+      }
+    base += total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    *a.count = base;
+    *a.status = 0;
+  }
+}
+
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+  const __nv_bfloat162 two = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&two);
+}
+
+// Row i of the gathered hidden states, up to a multiple of 64 rows (zeros beyond the
+// last token), and what an ignored token i is answered.
+__global__ void __launch_bounds__(128) k_lce_gather(const CeArgs a) {
+  const int i = blockIdx.x;
+  const int n = *a.count;
+  if (i < ((n + 63) & ~63)) {
+    __nv_bfloat16* const to = a.hc + static_cast<int64_t>(i) * a.ldh;
+    if (i < n) {
+      const int64_t at = place(a.token[i], a.seq, a.hsb, a.hss);
+      if (a.h_bf16) {
+        const __nv_bfloat16* const from = static_cast<const __nv_bfloat16*>(a.h) + at;
+        int d = 0;
+        if (reinterpret_cast<uintptr_t>(from) % 16 == 0) {
+          d = a.dim & ~7;
+          for (int k = threadIdx.x; k < a.dim >> 3; k += 128)
+            reinterpret_cast<uint4*>(to)[k] = reinterpret_cast<const uint4*>(from)[k];
+        }
+        for (int k = d + threadIdx.x; k < a.dim; k += 128) to[k] = from[k];
+      } else {
+        const float* const from = static_cast<const float*>(a.h) + at;
+        for (int k = threadIdx.x; k < a.dim; k += 128) to[k] = __float2bfloat16_rn(from[k]);
+      }
+      for (int k = a.dim + threadIdx.x; k < a.ldh; k += 128) to[k] = __float2bfloat16_rn(0.f);
+    } else {
+      for (int k = threadIdx.x; k < a.ldh; k += 128) to[k] = __float2bfloat16_rn(0.f);
+    }
+  }
+  if (i < a.tokens && target_of(a, i) == kIgnored) {
+    if (threadIdx.x == 0) {
+      if (a.logp != nullptr) a.logp[i] = 0.f;
+      if (a.lse != nullptr) a.lse[i] = 0.f;
+    }
+    if (a.g != nullptr) {
+      const int64_t at = place(i, a.seq, a.gsb, a.gss);
+      for (int k = threadIdx.x; k < a.dim; k += 128) {
+        if (a.g_bf16)
+          static_cast<__nv_bfloat16*>(a.g)[at + k] = __float2bfloat16_rn(0.f);
+        else
+          static_cast<float*>(a.g)[at + k] = 0.f;
+      }
+    }
+  }
+}
+
+// The weight in bf16 with rows of a multiple of 8 values.
+__global__ void __launch_bounds__(256) k_lce_weight(const void* w, int32_t bf16, int64_t stride, int32_t vocab, int32_t dim, int32_t ld,
+                                                    __nv_bfloat16* to) {
+  for (int v = blockIdx.x; v < vocab; v += gridDim.x) {
+    const int64_t at = v * stride;
+    for (int k = threadIdx.x; k < ld; k += 256) {
+      float x = 0.f;
+      if (k < dim) x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at + k]) : static_cast<const float*>(w)[at + k];
+      to[static_cast<int64_t>(v) * ld + k] = __float2bfloat16_rn(x);
+    }
+  }
+}
+
+// ---- logits to exponentials --------------------------------------------------------------
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool KEEP>
+struct LogitsEnd {
+  static constexpr bool kSym = false;
+  struct Args {
+    float c_hi, c_lo;
+    const int32_t* target;   // of the piece
+    float* xt;
+    float2* stat;
+    unsigned short* e;
+    int32_t lde, spans;
+  };
+  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+    // the columns of a group are one span: 128 words
+    static_assert(kSpan == 128, "half of a tile's columns");
+    if (p.col >= p.n) return;
+    const bool mine = p.row < p.m;
+    const int at = mine ? a.target[p.row] - p.col : -1;
+    float top = -INFINITY;
+    for (int c = 0; c < kSpan && p.col + c < p.n; c += 32) {
+      float v[32];
+      p.load(c, v);
+      if (p.col + c + 32 <= p.n) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (p.col + c + i < p.n) top = fmaxf(top, v[i]);
+      }
+      if (at >= c && at < c + 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i == at) a.xt[p.row] = v[i];
+      }
+    }
+    // (nothing but -inf or NaN leaves top at -inf: the sum is NaN or 0 then)
+    const float I = top > -INFINITY ? ceilf(fmaf(top, a.c_hi, top * a.c_lo)) : kNone;
+    const float shift = 15.f - I;
+    float sum = 0.f;
+    for (int c = 0; c < kSpan && p.col + c < p.n; c += 32) {
+      float v[32], some = 0.f;
+      p.load(c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = exp2_approx(fmaf(v[i], a.c_lo, fmaf(v[i], a.c_hi, shift)));
+        if (p.col + c + i < p.n) some += v[i];
+      }
+      if (at >= c && at < c + 32) {
+        some = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (p.col + c + i < p.n && c + i != at) some += v[i];
+      }
+      sum += some;
+      if (KEEP && mine) {
+        unsigned short* const to = a.e + static_cast<int64_t>(p.row) * a.lde + p.col + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p.col + c + 8 * i >= a.lde) break;
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const __half2 two = __floats2half2_rn(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]);
+            w[q] = *reinterpret_cast<const uint32_t*>(&two);
+          }
+          *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (mine) a.stat[static_cast<int64_t>(p.row) * a.spans + p.col / kSpan] = make_float2(I, sum);
+  }
+};
+
+// ---- a token's softmax, and dx ---------------------------------------------------------------
+__device__ __forceinline__ float power_of_two(float d) {   // 2^d for a whole d <= 0
+  return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
+}
+
+constexpr int kRowThreads = 256;
+
+__global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
+  __shared__ float s_max[kRowThreads / 32], s_sum[kRowThreads / 32];
+  const int r = blockIdx.x;
+  const int n = *a.count, live = min(a.rows, n - a.first);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint4* const e = a.e != nullptr ? reinterpret_cast<uint4*>(a.e + static_cast<int64_t>(r) * a.lde) : nullptr;
+  const int vecs = a.lde >> 3;
+  if (r >= live) {
+    // rows up to a multiple of 64 count as zeros in the weight's gradient
+    if (live > 0 && r < ((live + 63) & ~63) && e != nullptr)
+      for (int i = threadIdx.x; i < vecs; i += kRowThreads) e[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float2* const stat = a.stat + static_cast<int64_t>(r) * a.spans;
+  float top = -INFINITY;
+  for (int i = threadIdx.x; i < a.spans; i += kRowThreads) top = fmaxf(top, stat[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_max[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, s_max[w]);
+  float sum = 0.f;
+  for (int i = threadIdx.x; i < a.spans; i += kRowThreads) {
+    const float2 s = stat[i];
+    sum = fmaf(s.y, power_of_two(s.x - top), sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) sum += s_sum[w];
+
+  const int i = a.first + r, t = a.token[i], y = a.target[i];
+  const float nan = __int_as_float(0x7fc00000);
+  // rest: the words without the target; own: the target (both over 2^top)
+  const float rest = sum * 0x1p-15f;
+  float own = 0.f, far = 0.f;
+  if (y >= 0) {
+    const float x = a.xt[r];
+    far = fmaf(x, a.c_lo, fmaf(x, a.c_hi, -top));
+    own = exp2f(far);
+  }
+  const float all = rest + own;
+  const float log_s = log2f(all);
+  const float lse = kLn2 * (top + log_s);
+  const float logp = y < 0 ? nan : own > rest ? -log1pf(rest / own) : kLn2 * (far - log_s);
+  const float w = a.w.p != nullptr ? static_cast<const float*>(a.w.p)[place(t, a.seq, a.w.sb, a.w.ss)] : 1.f / static_cast<float>(n);
+  if (threadIdx.x == 0) {
+    a.part[i] = w * (a.z_loss * lse * lse - logp);
+    if (a.logp != nullptr) a.logp[t] = logp;
+    if (a.lse != nullptr) a.lse[t] = lse;
+  }
+  if (e == nullptr) return;
+  // (the mean's factor is the endings': see Factor)
+  const float d = a.w.p != nullptr ? w * a.scale * a.inv_t : 1.f, z = 2.f * a.z_loss * lse;
+  // (a target outside the vocabulary makes the whole row NaN)
+  const float factor = y >= 0 ? d * (1.f + z) / (all * 32768.f) : nan;
+  const float at_target = d * (z * own - rest) / all;
+  for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
+    const float f = factor * power_of_two(stat[v >> 4].x - top);
+    const uint4 q = e[v];
+    const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&in[k]));
+      const int j = 8 * v + 2 * k;
+      out[k] = pack(j == y ? at_target : x.x * f, j + 1 == y ? at_target : x.y * f);
+    }
+    e[v] = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// ---- gradients --------------------------------------------------------------------------------
+// What the products of dx still have to be multiplied by: under a mean, scale / (T count).
+struct Factor {
+  const int32_t* count;      // NULL: nothing
+  float scale;
+  __device__ __forceinline__ float value() const { return count == nullptr ? 1.f : scale / static_cast<float>(max(1, *count)); }
+  __device__ __forceinline__ void apply(float (&v)[32]) const {
+    if (count == nullptr) return;
+    const float f = value();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+  }
+};
+
+// Writes 32 values of a row of a result, fp32 or bf16; load: adds what is there first.
+__device__ __forceinline__ void store32(void* out, bool bf16, bool wide, bool load, int64_t at, int left, float (&v)[32]) {
+  if (bf16) {
+    __nv_bfloat16* const q = static_cast<__nv_bfloat16*>(out) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (wide && 8 * i + 8 <= left) {
+        if (load) {
+          const uint4 r = *reinterpret_cast<const uint4*>(q + 8 * i);
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+            v[8 * i + 2 * k] += x.x;
+            v[8 * i + 2 * k + 1] += x.y;
+          }
+        }
+        *reinterpret_cast<uint4*>(q + 8 * i) = make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]),
+                                                          pack(v[8 * i + 4], v[8 * i + 5]), pack(v[8 * i + 6], v[8 * i + 7]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (8 * i + k < left) q[8 * i + k] = __float2bfloat16_rn(v[8 * i + k] + (load ? __bfloat162float(q[8 * i + k]) : 0.f));
+      }
+    }
+  } else {
+    float* const q = static_cast<float*>(out) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (wide && 4 * i + 4 <= left) {
+        float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (load) {
+          const float4 o = *reinterpret_cast<const float4*>(q + 4 * i);
+          x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+        }
+        *reinterpret_cast<float4*>(q + 4 * i) = x;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (4 * i + k < left) q[4 * i + k] = v[4 * i + k] + (load ? q[4 * i + k] : 0.f);
+      }
+    }
+  }
+}
+
+struct HiddenEnd {
+  static constexpr bool kSym = false;
+  struct Args {
+    const int32_t* token;     // of the piece
+    void* out;
+    int64_t sb, ss;
+    int32_t seq, bf16, wide;
+    float* parts;             // not NULL: [splits][rows][dim], summed by k_lce_join
+    int32_t rows;
+    Factor factor;
+  };
+  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+    const bool mine = p.row < p.m;
+    int64_t at = 0;
+    if (mine)
+      at = a.parts != nullptr ? (static_cast<int64_t>(p.tile.split) * a.rows + p.row) * p.n : place(a.token[p.row], a.seq, a.sb, a.ss);
+    for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
+      float v[32];
+      p.load(c, v);
+      if (!mine) continue;
+      a.factor.apply(v);
+      if (a.parts != nullptr)
+        store32(a.parts, false, p.n % 4 == 0, false, at + p.col + c, p.n - p.col - c, v);
+      else
+        store32(a.out, a.bf16, a.wide, false, at + p.col + c, p.n - p.col - c, v);
+    }
+  }
+};
+
+// A token's hidden gradient from its parts, in their order.
+__global__ void __launch_bounds__(256) k_lce_join(const float* parts, int32_t splits, int32_t rows, int32_t dim, const int32_t* count,
+                                                  int32_t first, const HiddenEnd::Args o) {
+  const int r = blockIdx.x;
+  if (r >= *count - first) return;
+  const int64_t at = place(o.token[r], o.seq, o.sb, o.ss);
+  for (int k = blockIdx.y * 256 + threadIdx.x; k < dim; k += gridDim.y * 256) {
+    float v = 0.f;
+    for (int s = 0; s < splits; ++s) v += parts[(static_cast<int64_t>(s) * rows + r) * dim + k];
+    if (o.bf16)
+      static_cast<__nv_bfloat16*>(o.out)[at + k] = __float2bfloat16_rn(v);
+    else
+      static_cast<float*>(o.out)[at + k] = v;
+  }
+}
+
+struct WeightEnd {
+  static constexpr bool kSym = false;
+  struct Args {
+    void* out;
+    int64_t stride;
+    int32_t bf16, wide;
+    float* sum;                // [vocab][dim] over the pieces; NULL: there is one, or the result is fp32
+    int32_t load_sum, load_out, last;
+    Factor factor;
+  };
+  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+    const bool mine = p.row < p.m;
+    if (p.zero && !a.last && (a.sum != nullptr ? a.load_sum : a.load_out)) return;   // nothing to add
+    for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
+      float v[32];
+      p.load(c, v);
+      if (!mine) continue;
+      a.factor.apply(v);
+      const int left = p.n - p.col - c;
+      if (a.sum != nullptr) {
+        const int64_t at = static_cast<int64_t>(p.row) * p.n + p.col + c;
+        if (!a.last) {
+          store32(a.sum, false, p.n % 4 == 0, a.load_sum, at, left, v);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) v[i] += a.sum[at + i];
+      }
+      store32(a.out, a.bf16, a.wide, a.load_out, p.row * a.stride + p.col + c, left, v);
+    }
+  }
+};
+
+// An fp32 sum that carries what its additions round off.
+struct Sum {
+  float s = 0.f, rest = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = __fadd_rn(s, x), b = __fsub_rn(t, s);
+    rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    s = t;
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.s);
+    rest = __fadd_rn(rest, o.rest);
+  }
+  __device__ __forceinline__ float total() const { return fabsf(s) == INFINITY ? s : s + rest; }
+};
+
+__global__ void __launch_bounds__(1024) k_lce_loss(const CeArgs a) {
+  __shared__ Sum warps[32];
+  const int n = *a.count;
+  Sum s;
+  for (int i = threadIdx.x; i < n; i += 1024) s.add(a.part[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum other;
+    other.s = __shfl_down_sync(0xffffffffu, s.s, o);
+    other.rest = __shfl_down_sync(0xffffffffu, s.rest, o);
+    s.add(other);
+  }
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    Sum all;
+    for (int w = 0; w < 32; ++w) all.add(warps[w]);
+    *a.loss = *a.status != 0 ? __int_as_float(0x7fc00000) : all.total();
+  }
+}
+
+// ---- host side ------------------------------------------------------------------------------
+adaf_status fail(adaf_status st, const std::string& msg) { return meo::set_last_error(st, ("linear_ce: " + msg).c_str()); }
+adaf_status invalid(const std::string& msg) { return fail(ADAF_ERR_INVALID_ARGUMENT, msg); }
+adaf_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
+  return fail(ADAF_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(a) == 0; }
+int64_t size_of(int32_t dtype) { return dtype == ADAF_BFLOAT16 ? 2 : 4; }
+bool known(int32_t dtype) { return dtype == ADAF_BFLOAT16 || dtype == ADAF_FLOAT32; }
+
+const char* const kKernelNames[] = {"k_lce_scan", "k_lce_gather", "k_lce_weight",      "k_lce_logits", "k_lce_rows", "k_lce_grad_hidden",
+                                    "k_lce_join", "k_lce_grad_weight", "k_lce_loss"};
+constexpr int kNumKernels = 9;
+enum Slot { kSlotScan, kSlotGather, kSlotWeight, kSlotLogits, kSlotRows, kSlotGradHidden, kSlotJoin, kSlotGradWeight, kSlotLoss };
+meo::tc::Profile g_profile;
+thread_local bool t_stall = false;
+
+constexpr int64_t kMaxStride = int64_t{1} << 40;
+
+// [p, end) of a tensor's bytes.
+struct Extent {
+  uintptr_t from, to;
+  bool meets(const Extent& o) const { return from < o.to && o.from < to; }
+};
+Extent extent(const linear_ce_hidden& h) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(h.p);
+  return {p, p + static_cast<uintptr_t>(((h.batch - 1) * h.stride_b + (h.seq - 1) * h.stride_s + h.dim) * size_of(h.dtype))};
+}
+Extent extent(const linear_ce_weight& w, int64_t dim) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(w.p);
+  return {p, p + static_cast<uintptr_t>(((w.vocab - 1) * w.stride_v + dim) * size_of(w.dtype))};
+}
+
+adaf_status check_sizes(const linear_ce_hidden* h, const linear_ce_weight* w, const linear_ce_hidden* gh, const linear_ce_weight* gw) {
+  if (h == nullptr || w == nullptr) return invalid("hidden or weight is NULL");
+  if (!known(h->dtype)) return invalid("hidden: unknown dtype");
+  if (!known(w->dtype)) return invalid("weight: unknown dtype");
+  if (h->batch < 0 || h->seq < 0) return invalid("hidden: negative batch or seq");
+  if (h->dim < 1) return invalid("hidden: dim must be at least 1");
+  if (w->vocab < 1) return invalid("weight: vocab must be at least 1");
+  if (h->dim > kMaxDim || w->vocab > kMaxVocab) return fail(ADAF_ERR_UNSUPPORTED, "dim above 2^16 or vocab above 2^21");
+  if (h->batch > kMaxTokens || h->seq > kMaxTokens || h->batch * h->seq > kMaxTokens) return fail(ADAF_ERR_UNSUPPORTED, "more than 2^26 tokens");
+  if (w->stride_v < 0 || w->stride_v > kMaxStride || (w->vocab > 1 && w->stride_v < h->dim)) return invalid("weight: rows overlap (stride)");
+  if (gh != nullptr) {
+    if (!known(gh->dtype)) return invalid("grad_hidden: unknown dtype");
+    if (gh->batch != h->batch || gh->seq != h->seq || gh->dim != h->dim) return invalid("grad_hidden: not the hidden states' size");
+  }
+  if (gw != nullptr) {
+    if (!known(gw->dtype)) return invalid("grad_weight: unknown dtype");
+    if (gw->vocab != w->vocab) return invalid("grad_weight: not the weight's size");
+  }
+  return ADAF_OK;
+}
+
+// How a call is cut, and where things are in the workspace.
+struct Plan {
+  int64_t tokens, room, rows, pieces;   // room: rows of the gathered hidden states; rows: of a piece
+  int64_t ldh, lde, ldw, spans;
+  int splits;                           // of the hidden gradient's sums
+  bool packed;                          // the weight is copied
+  size_t token, target, part, hc, xt, stat, e, w, parts, sum, bytes;
+};
+
+Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_hidden* gh, const linear_ce_weight* gw) {
+  Plan P{};
+  const bool grad = gh != nullptr || gw != nullptr;
+  P.tokens = h.batch * h.seq;
+  P.room = round_up(P.tokens, 64);
+  P.ldh = round_up(h.dim, 8);
+  P.lde = round_up(w.vocab, 64);
+  P.spans = (w.vocab + kSpan - 1) / kSpan;
+  P.rows = std::min(P.room, std::max<int64_t>(256, kPieceBytes / (P.lde * 2) / 256 * 256));
+  P.pieces = (P.tokens + P.rows - 1) / P.rows;
+  P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || w.stride_v % 8 != 0;
+  P.ldw = P.packed ? P.ldh : w.stride_v;
+  const int64_t tiles = ((P.rows + 255) / 256) * ((h.dim + 255) / 256), blocks = (w.vocab + 63) / 64;
+  P.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({152 / tiles, blocks / 16, 32})));
+  size_t o = 256;
+  auto take = [&](int64_t bytes) {
+    const size_t at = o;
+    o = static_cast<size_t>(round_up(static_cast<int64_t>(o) + bytes, 256));
+    return at;
+  };
+  P.token = take(P.tokens * 4);
+  P.target = take(P.tokens * 4);
+  P.part = take(P.tokens * 4);
+  P.hc = take(P.room * P.ldh * 2);
+  P.xt = take(P.rows * 4);
+  P.stat = take(P.rows * P.spans * 8);
+  if (grad) P.e = take(P.rows * P.lde * 2);
+  if (P.packed) P.w = take(w.vocab * P.ldw * 2);
+  if (gh != nullptr && P.splits > 1) P.parts = take(P.splits * P.rows * h.dim * 4);
+  if (gw != nullptr && P.pieces > 1 && gw->dtype == ADAF_BFLOAT16) P.sum = take(w.vocab * h.dim * 4);
+  P.bytes = o;
+  return P;
+}
+
+#define LCE_TRY(expr, what)                           \
+  do {                                                \
+    const cudaError_t e_ = (expr);                    \
+    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+adaf_status linear_ce_workspace_size(const linear_ce_hidden* hidden, const linear_ce_weight* weight, const linear_ce_hidden* grad_hidden,
+                                     const linear_ce_weight* grad_weight, size_t* bytes) {
+  if (bytes == nullptr) return invalid("bytes is NULL");
+  const adaf_status st = check_sizes(hidden, weight, grad_hidden, grad_weight);
+  if (st != ADAF_OK) return st;
+  *bytes = plan(*hidden, *weight, grad_hidden, grad_weight).bytes;
+  return ADAF_OK;
+}
+
+adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* weight, const loss_targets* targets,
+                      const linear_ce_args* args, const linear_ce_hidden* grad_hidden, const linear_ce_weight* grad_weight, float* loss,
+                      float* logp, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const linear_ce_hidden* const gh = grad_hidden != nullptr && grad_hidden->p != nullptr ? grad_hidden : nullptr;
+  const linear_ce_weight* const gw = grad_weight != nullptr && grad_weight->p != nullptr ? grad_weight : nullptr;
+  const adaf_status st = check_sizes(hidden, weight, gh, gw);
+  if (st != ADAF_OK) return st;
+  if (targets == nullptr || args == nullptr) return invalid("targets or args is NULL");
+  const linear_ce_hidden& h = *hidden;
+  const linear_ce_weight& w = *weight;
+  const int64_t tokens = h.batch * h.seq;
+  auto bad_stride = [](int64_t s) { return s < 0 || s > kMaxStride; };
+  if (bad_stride(h.stride_b) || bad_stride(h.stride_s)) return invalid("hidden: strides must be 0 to 2^40");
+  if (tokens > 0 && h.p == nullptr) return invalid("hidden is NULL");
+  if (w.p == nullptr) return invalid("weight is NULL");
+  if (!aligned(h.p, size_of(h.dtype))) return invalid("hidden is not element-aligned");
+  if (!aligned(w.p, size_of(w.dtype))) return invalid("weight is not element-aligned");
+  if (targets->dtype != LOSS_INT32 && targets->dtype != LOSS_INT64) return invalid("targets: unknown dtype");
+  if (tokens > 0 && targets->rows.p == nullptr) return invalid("targets is NULL");
+  if (!aligned(targets->rows.p, targets->dtype == LOSS_INT64 ? 8 : 4)) return invalid("targets is not element-aligned");
+  if (bad_stride(targets->rows.stride_b) || bad_stride(targets->rows.stride_s)) return invalid("targets: strides must be 0 to 2^40");
+  if (!aligned(args->weights.p, 4)) return invalid("weights is not element-aligned");
+  if (args->weights.p != nullptr && (bad_stride(args->weights.stride_b) || bad_stride(args->weights.stride_s)))
+    return invalid("weights: strides must be 0 to 2^40");
+  const double inv_t = 1.0 / args->temperature;
+  if (!(args->temperature > 0.0) || !std::isfinite(args->temperature) || !std::isfinite(static_cast<float>(inv_t * 1.5)) ||
+      static_cast<float>(inv_t) < FLT_MIN)
+    return invalid("temperature must be positive, and 1 / temperature a normal fp32 number");
+  if (!(args->z_loss >= 0.0) || !std::isfinite(static_cast<float>(args->z_loss))) return invalid("z_loss must be >= 0");
+  if (!std::isfinite(static_cast<float>(args->grad_scale))) return invalid("grad_scale must be finite");
+  if (loss == nullptr) return invalid("loss is NULL");
+  if (!aligned(loss, 4) || !aligned(logp, 4) || !aligned(lse, 4)) return invalid("loss, logp or lse is not element-aligned");
+  if (gh != nullptr && tokens > 0) {
+    if (bad_stride(gh->stride_b) || bad_stride(gh->stride_s)) return invalid("grad_hidden: strides must be 0 to 2^40");
+    if (!aligned(gh->p, size_of(gh->dtype))) return invalid("grad_hidden is not element-aligned");
+    if ((gh->seq > 1 && gh->stride_s < gh->dim) || (gh->batch > 1 && gh->stride_b < (gh->seq - 1) * gh->stride_s + gh->dim))
+      return invalid("grad_hidden: rows overlap");
+    const bool same = gh->p == h.p && gh->dtype == h.dtype && (h.batch == 1 || gh->stride_b == h.stride_b) &&
+                      (h.seq == 1 || gh->stride_s == h.stride_s);
+    if (!same && extent(*gh).meets(extent(h))) return invalid("grad_hidden overlaps the hidden states, and is not in their place");
+    if (extent(*gh).meets(extent(w, h.dim))) return invalid("grad_hidden overlaps the weight");
+  }
+  if (gw != nullptr) {
+    if (!aligned(gw->p, size_of(gw->dtype))) return invalid("grad_weight is not element-aligned");
+    if (bad_stride(gw->stride_v) || (gw->vocab > 1 && gw->stride_v < h.dim)) return invalid("grad_weight: rows overlap (stride)");
+    if (extent(*gw, h.dim).meets(extent(w, h.dim))) return invalid("grad_weight overlaps the weight");
+    if (tokens > 0 && extent(*gw, h.dim).meets(extent(h))) return invalid("grad_weight overlaps the hidden states");
+    if (tokens > 0 && gh != nullptr && extent(*gw, h.dim).meets(extent(*gh))) return invalid("grad_weight overlaps grad_hidden");
+  }
+  const Plan P = plan(h, w, gh, gw);
+  if (workspace == nullptr || !aligned(workspace, 256)) return invalid("workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < P.bytes) return fail(ADAF_ERR_WORKSPACE_TOO_SMALL, "workspace needs " + std::to_string(P.bytes) + " bytes");
+
+  unsigned char* const ws = static_cast<unsigned char*>(workspace);
+  cudaStream_t const s = static_cast<cudaStream_t>(stream);
+  const bool grad = gh != nullptr || gw != nullptr;
+  CeArgs a{};
+  a.h = h.p;
+  a.h_bf16 = h.dtype == ADAF_BFLOAT16;
+  a.hsb = h.stride_b;
+  a.hss = h.stride_s;
+  if (gh != nullptr) {
+    a.g = gh->p;
+    a.g_bf16 = gh->dtype == ADAF_BFLOAT16;
+    a.gsb = gh->stride_b;
+    a.gss = gh->stride_s;
+  }
+  a.y = {targets->rows.p, targets->rows.stride_b, targets->rows.stride_s};
+  a.y64 = targets->dtype == LOSS_INT64;
+  a.ignore = targets->ignore_index;
+  a.w = {args->weights.p, args->weights.stride_b, args->weights.stride_s};
+  a.tokens = static_cast<int32_t>(tokens);
+  a.seq = static_cast<int32_t>(std::max<int64_t>(1, h.seq));
+  a.dim = static_cast<int32_t>(h.dim);
+  a.vocab = static_cast<int32_t>(w.vocab);
+  a.ldh = static_cast<int32_t>(P.ldh);
+  a.lde = static_cast<int32_t>(P.lde);
+  a.spans = static_cast<int32_t>(P.spans);
+  a.rows = static_cast<int32_t>(P.rows);
+  const double c = 1.4426950408889634 * inv_t;
+  a.c_hi = static_cast<float>(c);
+  a.c_lo = static_cast<float>(c - static_cast<double>(a.c_hi));
+  a.inv_t = static_cast<float>(inv_t);
+  a.z_loss = static_cast<float>(args->z_loss);
+  a.scale = static_cast<float>(args->grad_scale);
+  a.count = reinterpret_cast<int32_t*>(ws);
+  a.status = a.count + 1;
+  a.token = reinterpret_cast<int32_t*>(ws + P.token);
+  a.target = reinterpret_cast<int32_t*>(ws + P.target);
+  a.part = reinterpret_cast<float*>(ws + P.part);
+  a.hc = reinterpret_cast<__nv_bfloat16*>(ws + P.hc);
+  a.xt = reinterpret_cast<float*>(ws + P.xt);
+  a.stat = reinterpret_cast<float2*>(ws + P.stat);
+  a.e = grad ? reinterpret_cast<unsigned short*>(ws + P.e) : nullptr;
+  a.loss = loss;
+  a.logp = logp;
+  a.lse = lse;
+
+  LCE_TRY(g_profile.run(kSlotScan, s, [&] { k_lce_scan<<<1, kScanThreads, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_scan");
+  if (P.room > 0)
+    LCE_TRY(g_profile.run(kSlotGather, s, [&] { k_lce_gather<<<static_cast<unsigned>(P.room), 128, 0, s>>>(a); return cudaGetLastError(); }),
+            "k_lce_gather");
+  const void* wp = w.p;
+  if (P.packed && tokens > 0) {
+    wp = ws + P.w;
+    LCE_TRY(g_profile.run(kSlotWeight, s, [&] {
+      k_lce_weight<<<static_cast<unsigned>(std::min<int64_t>(w.vocab, 152 * 8)), 256, 0, s>>>(
+          w.p, w.dtype == ADAF_BFLOAT16, w.stride_v, a.vocab, a.dim, static_cast<int32_t>(P.ldw), reinterpret_cast<__nv_bfloat16*>(ws + P.w));
+      return cudaGetLastError();
+    }), "k_lce_weight");
+  }
+  const Factor factor{a.w.p != nullptr ? nullptr : a.count, a.scale * a.inv_t};
+  const int nt_d = static_cast<int>((h.dim + 255) / 256);
+  // without tokens one piece remains, which writes the weight's gradient
+  for (int64_t piece = 0; piece < std::max<int64_t>(P.pieces, gw != nullptr ? 1 : 0); ++piece) {
+    a.first = static_cast<int32_t>(piece * P.rows);
+    const int64_t rows = std::min(P.rows, std::max<int64_t>(tokens - a.first, 0));
+    __nv_bfloat16* const hc = a.hc + static_cast<int64_t>(a.first) * P.ldh;
+    const int64_t room = std::max<int64_t>(P.room - a.first, 64), e_rows = std::max<int64_t>(P.rows, 64);
+    Shape shape{};
+    shape.batch = 1;
+    shape.splits = 1;
+    shape.first = a.first;
+    shape.status = a.status;
+    shape.stall = t_stall ? 1 : 0;
+    using namespace meo::tc;
+    CUtensorMap h_k, w_k, e_k, w_n, e_m, h_n;
+    bool ok = true;
+    if (rows > 0) {
+      ok = make_map(&h_k, hc, true, room, h.dim, P.ldh, 1, room * P.ldh, kBoxK) &&
+           make_map(&w_k, wp, true, w.vocab, h.dim, P.ldw, 1, w.vocab * P.ldw, kBoxK);
+      if (!ok) return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+      Shape x = shape;
+      x.m = static_cast<int32_t>(rows);
+      x.n = a.vocab;
+      x.k = a.dim;
+      x.group = 32;
+      x.m_live = a.count;
+      cudaError_t e;
+      if (grad) {
+        const LogitsEnd<true>::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
+        e = g_profile.run(kSlotLogits, s, [&] { return launch_product<2, 256, 6, false, false, true, LogitsEnd<true>>(h_k, w_k, x, end, s); });
+      } else {
+        const LogitsEnd<false>::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
+        e = g_profile.run(kSlotLogits, s, [&] { return launch_product<2, 256, 6, false, false, true, LogitsEnd<false>>(h_k, w_k, x, end, s); });
+      }
+      LCE_TRY(e, "k_lce_logits");
+      LCE_TRY(g_profile.run(kSlotRows, s, [&] {
+        k_lce_rows<<<static_cast<unsigned>(grad ? round_up(rows, 64) : rows), kRowThreads, 0, s>>>(a);
+        return cudaGetLastError();
+      }), "k_lce_rows");
+    }
+    if (gh != nullptr && rows > 0) {
+      ok = make_map(&e_k, a.e, true, e_rows, w.vocab, P.lde, 1, e_rows * P.lde, kBoxK) &&
+           make_map(&w_n, wp, true, w.vocab, h.dim, P.ldw, 1, w.vocab * P.ldw, kBoxMN);
+      if (!ok) return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+      const int64_t es = size_of(gh->dtype);
+      const bool wide = aligned(gh->p, 16) && (h.batch == 1 || gh->stride_b * es % 16 == 0) && (h.seq == 1 || gh->stride_s * es % 16 == 0);
+      const HiddenEnd::Args end{a.token + a.first, gh->p, gh->stride_b, gh->stride_s, a.seq, a.g_bf16, wide,
+                                P.splits > 1 ? reinterpret_cast<float*>(ws + P.parts) : nullptr, static_cast<int32_t>(P.rows), factor};
+      Shape x = shape;
+      x.m = static_cast<int32_t>(rows);
+      x.n = a.dim;
+      x.k = a.vocab;
+      x.splits = P.splits;
+      x.group = 8;
+      x.m_live = a.count;
+      LCE_TRY(g_profile.run(kSlotGradHidden, s, [&] { return launch_product<2, 256, 6, false, true, true, HiddenEnd>(e_k, w_n, x, end, s); }),
+              "k_lce_grad_hidden");
+      if (P.splits > 1)
+        LCE_TRY(g_profile.run(kSlotJoin, s, [&] {
+          k_lce_join<<<dim3(static_cast<unsigned>(rows), static_cast<unsigned>(std::min<int64_t>((h.dim + 255) / 256, 16))), 256, 0, s>>>(
+              end.parts, P.splits, end.rows, a.dim, a.count, a.first, end);
+          return cudaGetLastError();
+        }), "k_lce_join");
+    }
+    if (gw != nullptr) {
+      ok = make_map(&e_m, P.e != 0 ? static_cast<void*>(a.e) : ws, true, e_rows, w.vocab, P.lde, 1, e_rows * P.lde, kBoxMN) &&
+           make_map(&h_n, hc, true, room, h.dim, P.ldh, 1, room * P.ldh, kBoxMN);
+      if (!ok) return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+      const int64_t es = size_of(gw->dtype);
+      const bool wide = aligned(gw->p, 16) && gw->stride_v * es % 16 == 0;
+      const bool last = piece + 1 >= P.pieces, more = P.pieces > 1 && gw->dtype == ADAF_FLOAT32;
+      // over several pieces: an fp32 result is summed in place, a bf16 one beside it
+      const WeightEnd::Args end{gw->p, gw->stride_v, gw->dtype == ADAF_BFLOAT16, wide,
+                                P.sum != 0 ? reinterpret_cast<float*>(ws + P.sum) : nullptr, piece > 0,
+                                gw->accumulate != 0 || (more && piece > 0), last, factor};
+      Shape x = shape;
+      x.m = a.vocab;
+      x.n = a.dim;
+      x.k = static_cast<int32_t>(rows);
+      x.group = std::max(1, 76 / nt_d);
+      x.k_live = a.count;
+      LCE_TRY(g_profile.run(kSlotGradWeight, s, [&] { return launch_product<2, 256, 6, true, true, true, WeightEnd>(e_m, h_n, x, end, s); }),
+              "k_lce_grad_weight");
+    }
+  }
+  LCE_TRY(g_profile.run(kSlotLoss, s, [&] { k_lce_loss<<<1, 1024, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_loss");
+  return ADAF_OK;
+}
+
+void linear_ce_debug_stall_copies(int32_t on) { t_stall = on != 0; }
+
+adaf_status linear_ce_profile_enable(int32_t on) {
+  g_profile.on = on != 0;
+  return ADAF_OK;
+}
+adaf_status linear_ce_profile_read(double* ms, int64_t* launches, int32_t nk) {
+  const cudaError_t e = g_profile.read(ms, launches, nk);
+  return e == cudaSuccess ? ADAF_OK : cuda_fail(e, "profile event");
+}
+int32_t linear_ce_num_kernels(void) { return kNumKernels; }
+const char* linear_ce_kernel_name(int32_t k) { return k >= 0 && k < kNumKernels ? kKernelNames[k] : ""; }
+
+}  // extern "C"
