@@ -91,9 +91,9 @@ void muon_default_iteration(muon_iteration* it);
 adaf_status muon_validate(const muon_hparams* hp);
 adaf_status muon_validate_iteration(const muon_iteration* it);
 
-/* Bytes of workspace (host only).  Matrices of one shape are worked on together,
- * up to 2^28 values at a time.  ADAF_ERR_UNSUPPORTED for a matrix with a side
- * above 2^20 or more than 2^31 - 1 values, or more than 2^24 matrices. */
+/* Bytes of workspace (host only).  Matrices are worked on together, up to 48 of
+ * them or 2^28 values at a time.  ADAF_ERR_UNSUPPORTED for a matrix with a side
+ * above 2^20 or more than 2^31 - 1 values, or more than 2^20 matrices. */
 adaf_status muon_workspace_size(const muon_tensor* tensors, int32_t n, size_t* bytes);
 adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t* bytes);
 

@@ -219,6 +219,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 template <bool KEEP>
 struct LogitsEnd {
   static constexpr bool kSym = false;
+  static constexpr int kChunk = 8;   // sums of 512 values: see k_product
   struct Args {
     float c_hi, c_lo;
     const int32_t* target;   // of the piece
@@ -227,62 +228,57 @@ struct LogitsEnd {
     unsigned short* e;
     int32_t lde, spans;
   };
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    // the columns of a group are one span: 128 words
-    static_assert(kSpan == 128, "half of a tile's columns");
+  // the columns of a group are one span: 128 words
+  static __device__ __forceinline__ void whole(const Args& a, const Part& p, float (&v)[kSpan]) {
     if (p.col >= p.n) return;
     const bool mine = p.row < p.m;
-    const int at = mine ? a.target[p.row] - p.col : -1;
+    const int at = mine ? a.target[p.row] - p.col : -1, left = p.n - p.col;
     float top = -INFINITY;
-    for (int c = 0; c < kSpan && p.col + c < p.n; c += 32) {
-      float v[32];
-      p.load(c, v);
-      if (p.col + c + 32 <= p.n) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-      } else {
+    for (int i = 0; i < kSpan; ++i) {
+      if (i >= left) v[i] = -INFINITY;
+      top = fmaxf(top, v[i]);
+    }
+    if (at >= 0 && at < kSpan) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (p.col + c + i < p.n) top = fmaxf(top, v[i]);
-      }
-      if (at >= c && at < c + 32) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i == at) a.xt[p.row] = v[i];
-      }
+      for (int i = 0; i < kSpan; ++i)
+        if (i == at) a.xt[p.row] = v[i];
     }
     // (nothing but -inf or NaN leaves top at -inf: the sum is NaN or 0 then)
     const float I = top > -INFINITY ? ceilf(fmaf(top, a.c_hi, top * a.c_lo)) : kNone;
     const float shift = 15.f - I;
     float sum = 0.f;
-    for (int c = 0; c < kSpan && p.col + c < p.n; c += 32) {
-      float v[32], some = 0.f;
-      p.load(c, v);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[i] = exp2_approx(fmaf(v[i], a.c_lo, fmaf(v[i], a.c_hi, shift)));
-        if (p.col + c + i < p.n) some += v[i];
+    for (int c = 0; c < kSpan; c += 32) {
+      float some = 0.f;
+#pragma unroll
+      for (int i = c; i < c + 32; ++i) {
+        // (a word beyond the vocabulary: -inf, and c_lo may be 0)
+        v[i] = i < left ? exp2_approx(fmaf(v[i], a.c_lo, fmaf(v[i], a.c_hi, shift))) : 0.f;
+        some += v[i];
       }
       if (at >= c && at < c + 32) {
         some = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (p.col + c + i < p.n && c + i != at) some += v[i];
+        for (int i = c; i < c + 32; ++i)
+          if (i != at) some += v[i];
       }
       sum += some;
-      if (KEEP && mine) {
-        unsigned short* const to = a.e + static_cast<int64_t>(p.row) * a.lde + p.col + c;
+      if (KEEP && c < left) {
+        uint4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (p.col + c + 8 * i >= a.lde) break;
-          uint32_t w[4];
+          uint32_t k[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const __half2 two = __floats2half2_rn(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]);
-            w[q] = *reinterpret_cast<const uint32_t*>(&two);
+            const __half2 two = __floats2half2_rn(v[c + 8 * i + 2 * q], v[c + 8 * i + 2 * q + 1]);
+            k[q] = *reinterpret_cast<const uint32_t*>(&two);
           }
-          *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          w[i] = make_uint4(k[0], k[1], k[2], k[3]);
         }
+        p.ex.to_memory(w);
+        p.ex.put(a.e + static_cast<int64_t>(p.row0()) * a.lde + p.col + c, static_cast<int64_t>(a.lde) * 2, p.m - p.row0(),
+                 (a.lde - p.col - c) * 2, w);
       }
     }
     if (mine) a.stat[static_cast<int64_t>(p.row) * a.spans + p.col / kSpan] = make_float2(I, sum);
@@ -386,46 +382,66 @@ struct Factor {
   }
 };
 
-// Writes 32 values of a row of a result, fp32 or bf16; load: adds what is there first.
-__device__ __forceinline__ void store32(void* out, bool bf16, bool wide, bool load, int64_t at, int left, float (&v)[32]) {
-  if (bf16) {
-    __nv_bfloat16* const q = static_cast<__nv_bfloat16*>(out) + at;
+// Writes the warp's 32 rows of 32 values of a result, fp32 or bf16: row i at out + row(i), of
+// which `left` values are there; load: adds what is there first.
+template <class RowAt>
+__device__ __forceinline__ void store32(const Part& p, void* out, bool bf16, bool wide, bool load, RowAt&& row_at, int left, float (&v)[32]) {
+  const meo::tc::Exchange& x = p.ex;
+  const int rows = p.m - p.row0();
+  if (bf16 && !load) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]), pack(v[8 * i + 4], v[8 * i + 5]),
+                        pack(v[8 * i + 6], v[8 * i + 7]));
+    x.to_memory(w);
+    const int j = x.place() / 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (wide && 8 * i + 8 <= left) {
-        if (load) {
-          const uint4 r = *reinterpret_cast<const uint4*>(q + 8 * i);
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
-            v[8 * i + 2 * k] += x.x;
-            v[8 * i + 2 * k + 1] += x.y;
-          }
-        }
-        *reinterpret_cast<uint4*>(q + 8 * i) = make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]),
-                                                          pack(v[8 * i + 4], v[8 * i + 5]), pack(v[8 * i + 6], v[8 * i + 7]));
+      if (x.row(i) >= rows || j >= left) continue;
+      __nv_bfloat16* const q = static_cast<__nv_bfloat16*>(out) + row_at(i) + j;
+      if (wide && j + 8 <= left) {
+        *reinterpret_cast<uint4*>(q) = w[i];
       } else {
+        const __nv_bfloat16* const k = reinterpret_cast<const __nv_bfloat16*>(&w[i]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (8 * i + k < left) q[8 * i + k] = __float2bfloat16_rn(v[8 * i + k] + (load ? __bfloat162float(q[8 * i + k]) : 0.f));
+        for (int e = 0; e < 8; ++e)
+          if (j + e < left) q[e] = k[e];
       }
     }
-  } else {
-    float* const q = static_cast<float*>(out) + at;
+    return;
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (wide && 4 * i + 4 <= left) {
-        float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  for (int half = 0; half < 2; ++half) {
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = make_uint4(__float_as_uint(v[16 * half + 4 * i]), __float_as_uint(v[16 * half + 4 * i + 1]),
+                        __float_as_uint(v[16 * half + 4 * i + 2]), __float_as_uint(v[16 * half + 4 * i + 3]));
+    x.to_memory(w);
+    const int j = 16 * half + x.place() / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (x.row(i) >= rows || j >= left) continue;
+      float r[4] = {__uint_as_float(w[i].x), __uint_as_float(w[i].y), __uint_as_float(w[i].z), __uint_as_float(w[i].w)};
+      if (bf16) {   // added to what is there
+        __nv_bfloat16* const q = static_cast<__nv_bfloat16*>(out) + row_at(i) + j;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < left) q[e] = __float2bfloat16_rn(r[e] + __bfloat162float(q[e]));
+        continue;
+      }
+      float* const q = static_cast<float*>(out) + row_at(i) + j;
+      if (wide && j + 4 <= left) {
         if (load) {
-          const float4 o = *reinterpret_cast<const float4*>(q + 4 * i);
-          x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+          const float4 o = *reinterpret_cast<const float4*>(q);
+          r[0] += o.x, r[1] += o.y, r[2] += o.z, r[3] += o.w;
         }
-        *reinterpret_cast<float4*>(q + 4 * i) = x;
+        *reinterpret_cast<float4*>(q) = make_float4(r[0], r[1], r[2], r[3]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (4 * i + k < left) q[4 * i + k] = v[4 * i + k] + (load ? q[4 * i + k] : 0.f);
+        for (int e = 0; e < 4; ++e)
+          if (j + e < left) q[e] = r[e] + (load ? q[e] : 0.f);
       }
     }
   }
@@ -433,6 +449,7 @@ __device__ __forceinline__ void store32(void* out, bool bf16, bool wide, bool lo
 
 struct HiddenEnd {
   static constexpr bool kSym = false;
+  static constexpr int kChunk = 0;
   struct Args {
     const int32_t* token;     // of the piece
     void* out;
@@ -443,19 +460,21 @@ struct HiddenEnd {
     Factor factor;
   };
   static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    const bool mine = p.row < p.m;
-    int64_t at = 0;
-    if (mine)
-      at = a.parts != nullptr ? (static_cast<int64_t>(p.tile.split) * a.rows + p.row) * p.n : place(a.token[p.row], a.seq, a.sb, a.ss);
+    int64_t at[4];   // of the rows that this lane writes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = p.row0() + p.ex.row(i);
+      at[i] = r >= p.m ? 0 : a.parts != nullptr ? (static_cast<int64_t>(p.tile.split) * a.rows + r) * p.n : place(a.token[r], a.seq, a.sb, a.ss);
+    }
     for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
       float v[32];
       p.load(c, v);
-      if (!mine) continue;
       a.factor.apply(v);
+      const int j = p.col + c;
       if (a.parts != nullptr)
-        store32(a.parts, false, p.n % 4 == 0, false, at + p.col + c, p.n - p.col - c, v);
+        store32(p, a.parts, false, p.n % 4 == 0, false, [&](int i) { return at[i] + j; }, p.n - j, v);
       else
-        store32(a.out, a.bf16, a.wide, false, at + p.col + c, p.n - p.col - c, v);
+        store32(p, a.out, a.bf16, a.wide, false, [&](int i) { return at[i] + j; }, p.n - j, v);
     }
   }
 };
@@ -478,6 +497,7 @@ __global__ void __launch_bounds__(256) k_lce_join(const float* parts, int32_t sp
 
 struct WeightEnd {
   static constexpr bool kSym = false;
+  static constexpr int kChunk = 0;
   struct Args {
     void* out;
     int64_t stride;
@@ -487,25 +507,25 @@ struct WeightEnd {
     Factor factor;
   };
   static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    const bool mine = p.row < p.m;
     if (p.zero && !a.last && (a.sum != nullptr ? a.load_sum : a.load_out)) return;   // nothing to add
     for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
       float v[32];
       p.load(c, v);
-      if (!mine) continue;
       a.factor.apply(v);
-      const int left = p.n - p.col - c;
+      const int j = p.col + c, left = p.n - j;
       if (a.sum != nullptr) {
-        const int64_t at = static_cast<int64_t>(p.row) * p.n + p.col + c;
+        const auto sum_at = [&](int i) { return static_cast<int64_t>(p.row0() + p.ex.row(i)) * p.n + j; };
         if (!a.last) {
-          store32(a.sum, false, p.n % 4 == 0, a.load_sum, at, left, v);
+          store32(p, a.sum, false, p.n % 4 == 0, a.load_sum, sum_at, left, v);
           continue;
         }
+        if (p.row < p.m) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < left) v[i] += a.sum[at + i];
+          for (int i = 0; i < 32; ++i)
+            if (i < left) v[i] += a.sum[static_cast<int64_t>(p.row) * p.n + j + i];
+        }
       }
-      store32(a.out, a.bf16, a.wide, a.load_out, p.row * a.stride + p.col + c, left, v);
+      store32(p, a.out, a.bf16, a.wide, a.load_out, [&](int i) { return (p.row0() + p.ex.row(i)) * a.stride + j; }, left, v);
     }
   }
 };

@@ -1,16 +1,16 @@
 // Multi-tensor Muon step and its orthogonalisation for sm_103a: the C ABI of
 // include/muon.h.
 //
-// Matrices of one shape (with the smaller side as m, the larger as n; a taller
-// matrix is worked on transposed) go through a sequence of launches together:
+// The matrices of a list (with the smaller side as m, the larger as n; a taller
+// matrix is worked on transposed) go through three launches together:
 //
 //   k_muon_moment   m = mu m + g; sum u^2 of every matrix, in parts
 //   k_muon_pack     x = u / max(||u||, eps), in the layout of the products
-//   then per step of the iteration three products (tc_gemm.cuh), which do
-//   everything else in their endings:
-//   k_muon_gram     A = x x^T          (only tiles on or above the diagonal)
-//   k_muon_poly     B = b A + c A A    (the same)
-//   k_muon_apply    x = a x + B x; the last one updates p, or writes the result
+//   k_muon_iterate  the steps of the iteration; each is three phases of products,
+//                   which do everything else in their endings:
+//                     A = x x^T          (only tiles on or above the diagonal)
+//                     B = b A + c A A    (the same)
+//                     x = a x + B x; the last one updates p, or writes the result
 //
 // Numbers.  The factors of the products are fp16, scaled by powers of two: an
 // element of x is at most its largest singular value, 1.21, so x 2^15 fits, and
@@ -53,38 +53,38 @@
 
 namespace {
 
-using meo::tc::Part;
-using meo::tc::Shape;
-
-constexpr int kMaxGroup = 64;                      // matrices of a launch
-constexpr int64_t kGroupValues = int64_t{1} << 28;  // and their values, unless one alone has more
+constexpr int kMaxGroup = 48;                      // matrices of a launch
+constexpr int kFew = 8;                            // a launch of few matrices has smaller arguments
+constexpr int64_t kGroupValues = int64_t{1} << 28;  // their values, unless one alone has more
 constexpr int kMaxParts = 256;                     // of a matrix's sum of squares
 constexpr int kPartValues = 8192;                  // values of a part, at least
 constexpr int64_t kMaxSide = int64_t{1} << 20;
+constexpr int64_t kMaxMatrices = int64_t{1} << 20;
 constexpr float kLoScale = 2048.f, kLoUnscale = 1.f / 2048.f;
 
-enum Flag : unsigned char { kTurned = 1, kBf16 = 2 };   // x is u^T; u is bf16
+enum Flag : int32_t { kTurned = 1, kBf16 = 2 };   // x is u^T; u is bf16
 
-// A launch's matrices.  u: the gradient, or the matrix to orthogonalise; p: the
-// parameter, or the result.
-struct Group {
-  float* p[kMaxGroup];
-  const void* u[kMaxGroup];
-  float* mom[kMaxGroup];
-  float rate[kMaxGroup];           // p = keep p - rate o
-  unsigned char flags[kMaxGroup];
+// A matrix as the passes before the products see it.
+struct Item {
+  const void* u;                   // the gradient, or the matrix to orthogonalise
+  float* mom;
+  __half* hi;
+  __half* lo;
+  int32_t rows, cols;              // of u
+  int32_t m, n, ldx;               // of x: m <= n
+  int32_t flags;
+  int32_t parts, part0, tile0;     // parts of its sum of squares; its first part and tile of the launches
 };
 
 struct MuonArgs {
-  int32_t m, n, ldx, lda;          // of x, and row lengths of x and of A and B in memory
-  int32_t parts;
+  int32_t count;
   int64_t stride_r;                // of u
   float mu, nesterov_mu, eps;      // u = g + nesterov_mu m, or m itself (nesterov_mu < 0)
-  float* part;                     // [matrices][kMaxParts]
-  __half* hi;
-  __half* lo;
+  float* part;                     // [parts of all matrices]
   int32_t* status;
+  unsigned* barrier;
   int32_t clear;                   // this launch clears the status word
+  Item item[kMaxGroup];
 };
 
 // ---- norm and layout ------------------------------------------------------------------
@@ -114,20 +114,38 @@ __device__ __forceinline__ float update_of(float g, float m, const MuonArgs& a) 
   return a.nesterov_mu < 0.f ? m : fmaf(a.nesterov_mu, m, g);
 }
 
+// Matrix of a launch that has block `at` of those that `first` counts.
+template <class First>
+__device__ __forceinline__ int owner(int count, int at, First&& first) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first(mid) <= at)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
 // One part of a matrix a CTA.  STEP: the momentum is brought up to date too.
 // Read 2 or 4 + 4 bytes a value, write 4: bound by memory.
 template <bool STEP>
-__global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Group grp, const MuonArgs a, int32_t rows, int32_t cols) {
+__global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ MuonArgs a) {
   __shared__ float scratch[8];
-  const int b = blockIdx.y;
-  if (a.clear != 0 && blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *a.status = 0;
-  const bool bf16 = grp.flags[b] & kBf16;
-  const void* u = grp.u[b];
-  float* mom = grp.mom[b];
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (a.clear != 0) *a.status = 0;
+    *a.barrier = 0;
+  }
+  const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].part0; })];
+  const bool bf16 = t.flags & kBf16;
+  const void* const u = t.u;
+  float* const mom = t.mom;
+  const int cols = t.cols;
   const bool flat = STEP || a.stride_r == cols;
-  const int64_t numel = static_cast<int64_t>(rows) * cols;
-  const int64_t per = ((numel + a.parts - 1) / a.parts + 3) & ~int64_t{3};
-  const int64_t e0 = per * blockIdx.x, e1 = min(numel, e0 + per);
+  const int64_t numel = static_cast<int64_t>(t.rows) * cols;
+  const int64_t per = ((numel + t.parts - 1) / t.parts + 3) & ~int64_t{3};
+  const int64_t e0 = per * (blockIdx.x - t.part0), e1 = min(numel, e0 + per);
   float sum = 0.f;
   if (flat) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(u) % (bf16 ? 8 : 16) | (STEP ? reinterpret_cast<uintptr_t>(mom) % 16 : 0);
@@ -167,7 +185,7 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Gro
     }
   }
   sum = block_sum(sum, scratch);
-  if (threadIdx.x == 0) a.part[b * kMaxParts + blockIdx.x] = sum;
+  if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
 __device__ __forceinline__ void split(float x, __half* hi, __half* lo) {
@@ -178,25 +196,26 @@ __device__ __forceinline__ void split(float x, __half* hi, __half* lo) {
 // x of a matrix, 64 x 64 values a CTA, through shared memory so that both u and
 // x are walked along their rows where x is u^T.
 template <bool STEP>
-__global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ Group grp, const MuonArgs a, int32_t rows, int32_t cols) {
+__global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[64][65];
   __shared__ float scratch[8];
-  const int b = blockIdx.z;
-  const float sum = block_sum(static_cast<int>(threadIdx.x) < a.parts ? a.part[b * kMaxParts + threadIdx.x] : 0.f, scratch);
+  const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].tile0; })];
+  const int rows = t.m, cols = t.n, ldx = t.ldx;
+  const int across = (cols + 63) >> 6, at_tile = blockIdx.x - t.tile0;
+  const int by = at_tile / across, bx = at_tile - by * across;
+  const float sum = block_sum(static_cast<int>(threadIdx.x) < t.parts ? a.part[t.part0 + threadIdx.x] : 0.f, scratch);
   const float norm = sqrtf(sum);
   // (a norm that is not finite makes x NaN)
   const float scale = norm <= FLT_MAX ? 32768.f / fmaxf(norm, a.eps) : __int_as_float(0x7fc00000);
-  const bool bf16 = grp.flags[b] & kBf16, turned = grp.flags[b] & kTurned;
-  const void* u = grp.u[b];
-  const float* mom = grp.mom[b];
-  // rows and cols are those of x; u has them the other way round if turned
-  const int ur = turned ? cols : rows, uc = turned ? rows : cols;
-  const int r0 = (turned ? blockIdx.x : blockIdx.y) * 64, c0 = (turned ? blockIdx.y : blockIdx.x) * 64;
+  const bool bf16 = t.flags & kBf16, turned = t.flags & kTurned;
+  const void* const u = t.u;
+  const float* const mom = t.mom;
+  const int r0 = (turned ? bx : by) * 64, c0 = (turned ? by : bx) * 64;   // of u
   for (int i = threadIdx.x; i < 64 * 64; i += 256) {
     const int r = r0 + (i >> 6), c = c0 + (i & 63);
     float v = 0.f;
-    if (r < ur && c < uc) {
-      const int64_t at = static_cast<int64_t>(r) * (STEP ? uc : a.stride_r) + c;
+    if (r < t.rows && c < t.cols) {
+      const int64_t at = static_cast<int64_t>(r) * (STEP ? t.cols : a.stride_r) + c;
       v = value_at(u, bf16, at);
       if (STEP) v = update_of(v, mom[at], a);
       v *= scale;
@@ -204,19 +223,17 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ Group
     tile[i >> 6][i & 63] = v;
   }
   __syncthreads();
-  const int x0 = blockIdx.y * 64, y0 = blockIdx.x * 64;   // of x
-  __half* const hi = a.hi + static_cast<int64_t>(b) * rows * a.ldx;
-  __half* const lo = a.lo + static_cast<int64_t>(b) * rows * a.ldx;
+  const int x0 = by * 64, y0 = bx * 64;   // of x
   for (int i = threadIdx.x; i < 64 * 32; i += 256) {
     const int r = i >> 5, c = (i & 31) * 2;
-    if (x0 + r >= rows || y0 + c >= a.ldx) continue;
+    if (x0 + r >= rows || y0 + c >= ldx) continue;
     const float v0 = turned ? tile[c][r] : tile[r][c], v1 = turned ? tile[c + 1][r] : tile[r][c + 1];
     __half2 h, l;
     split(v0, &h.x, &l.x);
     split(v1, &h.y, &l.y);
-    const int64_t at = static_cast<int64_t>(x0 + r) * a.ldx + y0 + c;
-    *reinterpret_cast<__half2*>(hi + at) = h;
-    *reinterpret_cast<__half2*>(lo + at) = l;
+    const int64_t at = static_cast<int64_t>(x0 + r) * ldx + y0 + c;
+    *reinterpret_cast<__half2*>(t.hi + at) = h;
+    *reinterpret_cast<__half2*>(t.lo + at) = l;
   }
 }
 
@@ -228,253 +245,528 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 __device__ __forceinline__ float2 unpack(uint32_t r) { return __half22float2(*reinterpret_cast<const __half2*>(&r)); }
 
 // 32 values of a row of a symmetric matrix s [m][ld] (values beyond column m are 0 and
-// go up to ld), and their mirror image in column `row`.
-__device__ __forceinline__ void store_symmetric(__half* s, int ld, int m, int row, int col, bool mirror, const float (&v)[32]) {
-  uint32_t h[16];
+// go up to ld), and their mirror image in column p.row.
+__device__ __forceinline__ void store_symmetric(__half* s, int ld, const meo::tc::Part& p, int col, const float (&v)[32]) {
+  uint4 w[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) h[i] = pack(v[2 * i], v[2 * i + 1]);
-  if (row < m) {
-    uint4* const to = reinterpret_cast<uint4*>(s + static_cast<int64_t>(row) * ld + col);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (col + 8 * i < ld) to[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-  }
-  if (mirror) {
+  for (int i = 0; i < 4; ++i)
+    w[i] = make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]), pack(v[8 * i + 4], v[8 * i + 5]),
+                      pack(v[8 * i + 6], v[8 * i + 7]));
+  if (p.tile.mirror) {
     // Two lanes swap halves, so that each stores two values side by side.
-    const bool odd = row & 1;
+    const bool odd = p.row & 1;
+    const int c = p.row & ~1;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       // column col + 2i has (mine.low, theirs.low), column col + 2i + 1 the high ones
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, h[i], 1);
-      const uint32_t pair = odd ? __byte_perm(other, h[i], 0x7632) : __byte_perm(h[i], other, 0x5410);
-      const int r = col + 2 * i + (odd ? 1 : 0), c = row & ~1;
-      if (r < m && c < ld) *reinterpret_cast<uint32_t*>(s + static_cast<int64_t>(r) * ld + c) = pair;
+      const uint32_t mine = i % 4 == 0 ? w[i / 4].x : i % 4 == 1 ? w[i / 4].y : i % 4 == 2 ? w[i / 4].z : w[i / 4].w;
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+      const uint32_t pair = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+      const int r = col + 2 * i + (odd ? 1 : 0);
+      if (r < p.m && c < ld) *reinterpret_cast<uint32_t*>(s + static_cast<int64_t>(r) * ld + c) = pair;
     }
+  }
+  p.ex.to_memory(w);
+  p.ex.put(s + static_cast<int64_t>(p.row0()) * ld + col, static_cast<int64_t>(ld) * 2, p.m - p.row0(), (ld - col) * 2, w);
+}
+
+// A matrix as the products see it.  (Its address in the arguments is that of the tensor maps.)
+struct Matrix {
+  CUtensorMap x;         // hi [2][m][n]: of this step and of the next
+  CUtensorMap s;         // [2][m][m]: F and E
+  __half* hi;
+  __half* lo;            // read and written in place: nobody else needs a tile's values
+  __half* fe;
+  float* dg;             // [2][lda]: D and G
+  float* p;              // the parameter, or the result
+  int32_t m, n, ldx, lda;
+  int32_t flags;
+  float rate;            // p = keep p - rate o
+  int32_t sym0, app0;    // its first tile of the symmetric products and of the others
+};
+
+enum Out : int32_t { kUpdate, kFp32, kBf16Out };
+
+template <int COUNT>
+struct IterateArgs {
+  Matrix mat[COUNT];
+  float coef[MUON_MAX_STEPS][3];
+  int32_t count, steps, sym_tiles, app_tiles;
+  int32_t out;
+  float keep;
+  int32_t stall;
+  int32_t* status;
+  unsigned* barrier;     // arrivals of the grid's CTAs
+};
+
+using meo::tc::Part;
+
+// A = x x^T: F = A without its diagonal (scaled by 2^15), D the diagonal.
+__device__ __forceinline__ void end_gram(const Matrix& t, const Part& p) {
+  for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
+    float v[32];
+    p.load(c, v);
+    const int diag = p.row - (p.col + c);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] *= 0x1p-15f;
+      if (i == diag) {
+        if (p.row < p.m) t.dg[p.row] = v[i] * 0x1p-15f;
+        v[i] = 0.f;
+      }
+    }
+    store_symmetric(t.fe, t.lda, p, p.col + c, v);
   }
 }
 
-// A = x x^T: F = A without its diagonal (scaled by 2^15), D the diagonal.
-struct GramEnd {
-  static constexpr bool kSym = true;
-  struct Args {
-    __half* f;
-    float* d;
-    int32_t ld;
-  };
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    __half* const f = a.f + static_cast<int64_t>(p.tile.batch) * p.m * a.ld;
-    float* const d = a.d + static_cast<int64_t>(p.tile.batch) * a.ld;
-    for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
-      float v[32];
-      p.load(c, v);
-      const int diag = p.row - (p.col + c);
+// What an ending reads beside the sums: the tile's part of one or two 16-bit matrices, 64 bytes
+// of a row a word.  It is asked for before the sums are there: behind the ring's copies, which
+// keep the SM's port to L2 full, an answer takes two microseconds, and a tile's four in a row
+// took longer than its products.
+template <int CHUNKS>
+struct Ahead {
+  uint4 w[CHUNKS][4];
+  __device__ __forceinline__ void fetch(const Part& p, const __half* from, int ld) {
+    const __half* const rows = from + static_cast<int64_t>(p.row0()) * ld + p.col;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        v[i] *= 0x1p-15f;
-        if (i == diag) {
-          if (p.row < p.m) d[p.row] = v[i] * 0x1p-15f;
-          v[i] = 0.f;
-        }
-      }
-      store_symmetric(f, a.ld, p.m, p.row, p.col + c, p.tile.mirror, v);
-    }
+    for (int c = 0; c < CHUNKS; ++c) p.ex.fetch(rows + 32 * c, static_cast<int64_t>(ld) * 2, p.m - p.row0(), (ld - p.col - 32 * c) * 2, w[c]);
   }
 };
 
 // B = b A + c A A: E without the diagonal (scaled by 2^14), G the diagonal.
-struct PolyEnd {
-  static constexpr bool kSym = true;
-  struct Args {
-    const __half* f;
-    const float* d;
-    __half* e;
-    float* g;
-    int32_t ld;
-    float b, c;
-  };
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    const int64_t at = static_cast<int64_t>(p.tile.batch) * p.m * a.ld;
-    const float* const d = a.d + static_cast<int64_t>(p.tile.batch) * a.ld;
-    const float di = p.row < p.m ? d[p.row] : 0.f;
-    for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
-      const int j0 = p.col + c;
-      float v[32];
-      p.load(c, v);
-      const int diag = p.row - j0;
+template <int CHUNKS>
+__device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, Ahead<CHUNKS>& f, float cb, float cc) {
+  const float* const d = t.dg;
+  const float di = p.row < p.m ? d[p.row] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (j0 + 8 * i >= a.ld) {
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int j0 = p.col + 32 * c;
+    if (j0 >= p.m) break;
+    p.ex.to_rows(f.w[c]);
+    float v[32];
+    p.load(32 * c, v);
+    const int diag = p.row - j0;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[8 * i + q] = 0.f;
-          continue;
-        }
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (p.row < p.m) r = *reinterpret_cast<const uint4*>(a.f + at + static_cast<int64_t>(p.row) * a.ld + j0 + 8 * i);
-        const float4 d0 = *reinterpret_cast<const float4*>(d + j0 + 8 * i), d1 = *reinterpret_cast<const float4*>(d + j0 + 8 * i + 4);
-        const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    for (int i = 0; i < 4; ++i) {
+      if (j0 + 8 * i >= t.lda) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 two = unpack(w[q >> 1]);
-          const float f = (q & 1) ? two.y : two.x;   // F 2^15
-          float& x = v[8 * i + q];                   // (F F) 2^30
-          if (8 * i + q == diag) {
-            if (p.row < p.m) a.g[static_cast<int64_t>(p.tile.batch) * a.ld + p.row] = fmaf(a.c, fmaf(di, di, x * 0x1p-30f), a.b * di);
-            x = 0.f;
-          } else {
-            x = fmaf(f * 0.5f, fmaf(a.c, di + dj[q], a.b), a.c * (x * 0x1p-16f));
-          }
+        for (int q = 0; q < 8; ++q) v[8 * i + q] = 0.f;
+        continue;
+      }
+      const uint4 r = f.w[c][i];
+      const float4 d0 = *reinterpret_cast<const float4*>(d + j0 + 8 * i), d1 = *reinterpret_cast<const float4*>(d + j0 + 8 * i + 4);
+      const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float2 two = unpack(w[q >> 1]);
+        const float x16 = (q & 1) ? two.y : two.x;   // F 2^15
+        float& x = v[8 * i + q];                     // (F F) 2^30
+        if (8 * i + q == diag) {
+          if (p.row < p.m) t.dg[t.lda + p.row] = fmaf(cc, fmaf(di, di, x * 0x1p-30f), cb * di);
+          x = 0.f;
+        } else {
+          x = fmaf(x16 * 0.5f, fmaf(cc, di + dj[q], cb), cc * (x * 0x1p-16f));
         }
       }
-      if (p.row >= p.m) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (j0 + i >= p.m) v[i] = 0.f;
-      store_symmetric(a.e + at, a.ld, p.m, p.row, j0, p.tile.mirror, v);
     }
+    if (p.row >= p.m) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (j0 + i >= p.m) v[i] = 0.f;
+    store_symmetric(t.fe + static_cast<int64_t>(p.m) * t.lda, t.lda, p, j0, v);
   }
-};
+}
 
-// x = (a + G) x + E x.  LAST: the update of p, or the result.
-enum Last : int { kNext, kUpdate, kResult };
-template <int LAST>
-struct ApplyEnd {
-  static constexpr bool kSym = false;
-  struct Args {
-    const __half* hi;
-    __half* lo;            // read and written in place: nobody else needs these values
-    __half* hi_next;
-    const float* g;
-    int32_t ldx, lda;
-    float a, keep;
-    int32_t out_bf16;
-    const int32_t* status;
-  };
-};
-
-__device__ __forceinline__ void applied(const Part& p, int c, const __half* hi, const __half* lo, int64_t at, int ldx, float factor,
-                                        float (&v)[32]) {
+// 32 columns of (a + G) x + E x, scaled by 2^15.
+__device__ __forceinline__ void applied(const Part& p, int c, uint4 (&h)[4], uint4 (&l)[4], float factor, float (&v)[32]) {
+  p.ex.to_rows(h);
+  p.ex.to_rows(l);
   p.load(c, v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (p.row < p.m && p.col + c + 8 * i < ldx) {
-      const uint4 h = *reinterpret_cast<const uint4*>(hi + at + c + 8 * i), l = *reinterpret_cast<const uint4*>(lo + at + c + 8 * i);
-      const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+    const uint32_t hw[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, lw[4] = {l[i].x, l[i].y, l[i].z, l[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 a = unpack(hw[q]), b = unpack(lw[q]);
+      v[8 * i + 2 * q] = fmaf(factor, fmaf(b.x, kLoUnscale, a.x), v[8 * i + 2 * q] * 0x1p-14f);
+      v[8 * i + 2 * q + 1] = fmaf(factor, fmaf(b.y, kLoUnscale, a.y), v[8 * i + 2 * q + 1] * 0x1p-14f);
+    }
+  }
+}
+
+// x of the next step.
+template <int CHUNKS>
+__device__ __forceinline__ void end_next(const Matrix& t, const Part& p, Ahead<CHUNKS>& ah, Ahead<CHUNKS>& al, int slab, float ca) {
+  const float factor = ca + (p.row < p.m ? t.dg[t.lda + p.row] : 0.f);
+  const int64_t pitch = static_cast<int64_t>(t.ldx) * 2;
+  __half* const next = t.hi + (slab ^ 1) * (static_cast<int64_t>(p.m) * t.ldx) + static_cast<int64_t>(p.row0()) * t.ldx + p.col;
+  __half* const lo = t.lo + static_cast<int64_t>(p.row0()) * t.ldx + p.col;
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    const int c = 32 * k;
+    if (p.col + c >= p.n) break;
+    float v[32];
+    applied(p, c, ah.w[k], al.w[k], factor, v);
+    uint4 h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t hw[4], lw[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float2 x = unpack(hw[q]), y = unpack(lw[q]);
-        v[8 * i + 2 * q] = fmaf(factor, fmaf(y.x, kLoUnscale, x.x), v[8 * i + 2 * q] * 0x1p-14f);
-        v[8 * i + 2 * q + 1] = fmaf(factor, fmaf(y.y, kLoUnscale, x.y), v[8 * i + 2 * q + 1] * 0x1p-14f);
+        const float a = v[8 * i + 2 * q], b = v[8 * i + 2 * q + 1];
+        hw[q] = pack(a, b);
+        const float2 r = unpack(hw[q]);
+        lw[q] = pack((a - r.x) * kLoScale, (b - r.y) * kLoScale);
+      }
+      h[i] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      l[i] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    }
+    const int left = (t.ldx - p.col - c) * 2;
+    p.ex.to_memory(h);
+    p.ex.put(next + c, pitch, p.m - p.row0(), left, h);
+    p.ex.to_memory(l);
+    p.ex.put(lo + c, pitch, p.m - p.row0(), left, l);
+  }
+}
+
+// The last step: the update of p, or the result.
+template <int CHUNKS>
+__device__ __forceinline__ void end_last(const Matrix& t, const Part& p, Ahead<CHUNKS>& ah, Ahead<CHUNKS>& al, float ca, int out, float keep,
+                                         const int32_t* status) {
+  if (out == kUpdate && (p.bad || *reinterpret_cast<const volatile int32_t*>(status) != 0)) return;   // p stays as it is
+  const float factor = ca + (p.row < p.m ? t.dg[t.lda + p.row] : 0.f);
+  const bool turned = t.flags & kTurned;
+  const bool wide = p.n % (out == kBf16Out ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(t.p) % 16 == 0;
+  const float rate = t.rate * 0x1p-15f;
+  const int rows = p.m - p.row0();
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    const int c = 32 * k;
+    if (p.col + c >= p.n) break;
+    float v[32];
+    applied(p, c, ah.w[k], al.w[k], factor, v);
+    const int j0 = p.col + c;
+    if (turned) {
+      // down a column of the parameter: the warp's lanes lie side by side there
+      if (p.row >= p.m) continue;
+      const int64_t to = static_cast<int64_t>(j0) * p.m + p.row;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (j0 + i >= p.n) break;
+        const int64_t q = to + static_cast<int64_t>(i) * p.m;
+        if (out == kUpdate)
+          t.p[q] = fmaf(-rate, v[i], keep * t.p[q]);
+        else if (out == kBf16Out)
+          reinterpret_cast<__nv_bfloat16*>(t.p)[q] = __float2bfloat16_rn(v[i] * 0x1p-15f);
+        else
+          t.p[q] = v[i] * 0x1p-15f;
+      }
+    } else if (out == kBf16Out) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t k[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * i + 2 * q] * 0x1p-15f, v[8 * i + 2 * q + 1] * 0x1p-15f);
+          k[q] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        w[i] = make_uint4(k[0], k[1], k[2], k[3]);
+      }
+      p.ex.to_memory(w);
+      __nv_bfloat16* const q = reinterpret_cast<__nv_bfloat16*>(t.p) + static_cast<int64_t>(p.row0()) * p.n + j0;
+      if (wide) {
+        p.ex.put(q, static_cast<int64_t>(p.n) * 2, rows, (p.n - j0) * 2, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p.ex.row(i) >= rows) continue;
+          const __nv_bfloat16* const k = reinterpret_cast<const __nv_bfloat16*>(&w[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int j = p.ex.place() / 2 + e;
+            if (j0 + j < p.n) q[static_cast<int64_t>(p.ex.row(i)) * p.n + j] = k[e];
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // 16 columns, 64 bytes
+        uint4 w[4], old[4];
+        float* const q = t.p + static_cast<int64_t>(p.row0()) * p.n + j0 + 16 * half;
+        const int left = p.n - j0 - 16 * half;
+        if (out == kUpdate && wide) p.ex.fetch(q, static_cast<int64_t>(p.n) * 4, rows, left * 4, old);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = make_uint4(__float_as_uint(v[16 * half + 4 * i]), __float_as_uint(v[16 * half + 4 * i + 1]),
+                            __float_as_uint(v[16 * half + 4 * i + 2]), __float_as_uint(v[16 * half + 4 * i + 3]));
+        p.ex.to_memory(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float r[4] = {__uint_as_float(w[i].x), __uint_as_float(w[i].y), __uint_as_float(w[i].z), __uint_as_float(w[i].w)};
+          const float o[4] = {__uint_as_float(old[i].x), __uint_as_float(old[i].y), __uint_as_float(old[i].z), __uint_as_float(old[i].w)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (wide) {
+              r[e] = out == kUpdate ? fmaf(-rate, r[e], keep * o[e]) : r[e] * 0x1p-15f;
+            } else if (p.ex.row(i) < rows && p.ex.place() / 4 + e < left) {
+              float* const one = q + static_cast<int64_t>(p.ex.row(i)) * p.n + p.ex.place() / 4 + e;
+              *one = out == kUpdate ? fmaf(-rate, r[e], keep * *one) : r[e] * 0x1p-15f;
+            }
+          }
+          w[i] = make_uint4(__float_as_uint(r[0]), __float_as_uint(r[1]), __float_as_uint(r[2]), __float_as_uint(r[3]));
+        }
+        if (wide) p.ex.put(q, static_cast<int64_t>(p.n) * 4, rows, left * 4, w);
       }
     }
   }
 }
 
-struct NextEnd : ApplyEnd<kNext> {
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    const int64_t at = (static_cast<int64_t>(p.tile.batch) * p.m + p.row) * a.ldx + p.col;
-    const float factor = a.a + (p.row < p.m ? a.g[static_cast<int64_t>(p.tile.batch) * a.lda + p.row] : 0.f);
-    for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
-      float v[32];
-      applied(p, c, a.hi, a.lo, at, a.ldx, factor, v);
-      if (p.row >= p.m) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (p.col + c + 8 * i >= a.ldx) continue;
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float x = v[8 * i + 2 * q], y = v[8 * i + 2 * q + 1];
-          h[q] = pack(x, y);
-          const float2 r = unpack(h[q]);
-          l[q] = pack((x - r.x) * kLoScale, (y - r.y) * kLoScale);
-        }
-        *reinterpret_cast<uint4*>(a.hi_next + at + c + 8 * i) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(a.lo + at + c + 8 * i) = make_uint4(l[0], l[1], l[2], l[3]);
-      }
-    }
-  }
-};
+// ---- the iteration ------------------------------------------------------------------------
+// All steps for all matrices of a group, in one launch: a step is three phases
+// (x x^T, the polynomial, its product with x), each over the tiles of all
+// matrices, and between phases the grid's CTAs wait for one another (they are
+// launched together: a cooperative launch).  Fifteen launches in a row took 11 us
+// each on a matrix of 256 x 512, of which the copies and products are one or two,
+// and every matrix shape had its own.  The roles of the warps and the ring are
+// k_product's; they go on from phase to phase.
+enum Phase : int { kGram, kPoly, kApply };
 
-template <int LAST>
-struct LastEnd : ApplyEnd<LAST> {
-  struct Args : ApplyEnd<LAST>::Args {
-    Group grp;
+// Tile number i of a phase; `at` is the matrix that the number before fell in.
+template <int CG, int BN, int COUNT>
+__device__ __forceinline__ bool find_tile(const IterateArgs<COUNT>& a, int phase, int i, int* at, meo::tc::Tile* t) {
+  const bool sym = phase != kApply;
+  if (i >= (sym ? a.sym_tiles : a.app_tiles)) return false;
+  int k = *at;
+  while (k + 1 < a.count && i >= (sym ? a.mat[k + 1].sym0 : a.mat[k + 1].app0)) ++k;
+  *at = k;
+  const Matrix& m = a.mat[k];
+  meo::tc::Shape s{};
+  s.batch = 1;
+  s.splits = 1;
+  s.group = 8;
+  const int mt = (m.m + meo::tc::kTileM * CG - 1) / (meo::tc::kTileM * CG), nt = (m.n + BN - 1) / BN;
+  if (sym) return meo::tc::tile_of<true>(i - m.sym0, mt, mt, s, meo::tc::kTileM * CG, BN, t);
+  return meo::tc::tile_of<false>(i - m.app0, mt, nt, s, meo::tc::kTileM * CG, BN, t);
+}
+
+template <int CG, int BN, int STAGES, int COUNT>
+__global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __grid_constant__ IterateArgs<COUNT> a) {
+  using namespace meo::tc;
+  using S = Shared<CG, BN, STAGES>;
+  constexpr uint32_t kCols = 2 * BN;
+  constexpr int kBCta = BN / CG;
+  static_assert(kTileM * CG == BN, "square tiles");
+  extern __shared__ unsigned char raw[];
+  unsigned char* ring = raw + ((1024 - (shared_at(raw) & 1023)) & 1023);
+  unsigned char* const exchange = ring + STAGES * S::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(exchange + kEndWarps * kExchange);
+  uint64_t* empty = full + STAGES;
+  uint64_t* sum_full = empty + STAGES;
+  uint64_t* sum_empty = sum_full + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sum_empty + 2);
+  volatile int* off = reinterpret_cast<volatile int*>(tmem_at + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      bar_init(full + i, 1);
+      bar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(sum_full + i, 1);
+      bar_init(sum_empty + i, CG * kEndWarps);
+    }
+    *off = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = *tmem_at;
+
+  auto gave_up = [&] {
+    *off = 1;
+    atomicOr(a.status, 1);
   };
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
-    if (LAST == kUpdate && (p.bad || *reinterpret_cast<const volatile int32_t*>(a.status) != 0)) return;   // p stays as it is
-    const int b = p.tile.batch;
-    const int64_t at = (static_cast<int64_t>(b) * p.m + p.row) * a.ldx + p.col;
-    const float factor = a.a + (p.row < p.m ? a.g[static_cast<int64_t>(b) * a.lda + p.row] : 0.f);
-    const bool turned = a.grp.flags[b] & kTurned;
-    const bool wide = !turned && p.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.grp.p[b]) % 16 == 0;
-    for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
-      float v[32];
-      applied(p, c, a.hi, a.lo, at, a.ldx, factor, v);
-      if (p.row >= p.m) continue;
-      const int j0 = p.col + c;
-      // value i of p's or the result's memory: along its row, or down its column
-      const int64_t to = turned ? static_cast<int64_t>(j0) * p.m + p.row : static_cast<int64_t>(p.row) * p.n + j0;
-      const int64_t step = turned ? p.m : 1;
-      if (LAST == kUpdate) {
-        float* const q = a.grp.p[b] + to;
-        const float rate = a.grp.rate[b] * 0x1p-15f;
-        if (wide) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (j0 + 4 * i >= p.n) break;
-            float4 x = *reinterpret_cast<const float4*>(q + 4 * i);
-            x.x = fmaf(-rate, v[4 * i], a.keep * x.x);
-            x.y = fmaf(-rate, v[4 * i + 1], a.keep * x.y);
-            x.z = fmaf(-rate, v[4 * i + 2], a.keep * x.z);
-            x.w = fmaf(-rate, v[4 * i + 3], a.keep * x.w);
-            *reinterpret_cast<float4*>(q + 4 * i) = x;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (j0 + i < p.n) q[i * step] = fmaf(-rate, v[i], a.keep * q[i * step]);
-        }
-      } else if (a.out_bf16) {
-        __nv_bfloat16* const q = reinterpret_cast<__nv_bfloat16*>(a.grp.p[b]) + to;
-        if (wide) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (j0 + 8 * i >= p.n) break;
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * i + 2 * k] * 0x1p-15f, v[8 * i + 2 * k + 1] * 0x1p-15f);
-              w[k] = *reinterpret_cast<const uint32_t*>(&two);
-            }
-            *reinterpret_cast<uint4*>(q + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (j0 + i < p.n) q[i * step] = __float2bfloat16_rn(v[i] * 0x1p-15f);
-        }
-      } else {
-        float* const q = a.grp.p[b] + to;
-        if (wide) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (j0 + 4 * i >= p.n) break;
-            *reinterpret_cast<float4*>(q + 4 * i) = make_float4(v[4 * i] * 0x1p-15f, v[4 * i + 1] * 0x1p-15f,
-                                                                v[4 * i + 2] * 0x1p-15f, v[4 * i + 3] * 0x1p-15f);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (j0 + i < p.n) q[i * step] = v[i] * 0x1p-15f;
-        }
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (bar_try(bar, parity)) return true;
+    const long long from = clock64();
+    while (!bar_try(bar, parity)) {
+      if (*off != 0) return false;
+      if (clock64() - from > kWaitCycles) {
+        gave_up();
+        return false;
       }
     }
+    return true;
+  };
+
+  const int phases = 3 * a.steps;
+  // After a phase: the grid's CTAs wait for one another.
+  auto block_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
+  auto next_phase = [&](int ph) {
+    __syncwarp();
+    block_barrier();
+    if (ph + 1 == phases) return;
+    if (threadIdx.x == 0) {
+      const unsigned all = static_cast<unsigned>(ph + 1) * gridDim.x;
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.barrier) : "memory");
+      const long long from = clock64();
+      unsigned seen;
+      for (;;) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.barrier) : "memory");
+        if (seen >= all || *off != 0) break;
+        if (clock64() - from > 4 * kWaitCycles) gave_up();
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+    }
+    __syncwarp();
+    block_barrier();
+  };
+  if (warp < 4) {
+    fewer_registers();
+    int stage = 0, acc = 0;
+    uint32_t phase_bit = 0, acc_bit = 0;
+    bool ok = true;
+    for (int ph = 0; ph < phases; ++ph) {
+      const int kind = ph % 3, slab = ph / 3 & 1;
+      int at = 0;
+      Tile t;
+      if (warp == 0 && lane == 0) {
+        // ---- copies
+        for (int i = first; ok && find_tile<CG, BN>(a, kind, i, &at, &t); i += step) {
+          const Matrix& m = a.mat[at];
+          const CUtensorMap* const map_a = kind == kGram ? &m.x : &m.s;
+          const CUtensorMap* const map_b = kind == kPoly ? &m.s : &m.x;
+          const int za = kind == kGram ? slab : kind == kPoly ? 0 : 1, zb = kind == kPoly ? 0 : slab;
+          const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+          const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
+          for (int kb = 0; kb < blocks; ++kb) {
+            if (!(ok = wait(empty + stage, phase_bit ^ 1))) break;
+            const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
+            uint32_t bar = shared_at(full + stage);
+            if (rank == 0) bar_expect(full + stage, S::kStage * CG);
+            if constexpr (CG == 2) bar = at_rank(bar, 0);
+            const int k = kb * kBlockK;
+            if (a.stall == 0) {
+#pragma unroll
+              for (int j = 0; j < kTileM / 64; ++j) tma_load<CG>(pa + j * 8192, map_a, k, am + j * 64, za, bar);
+#pragma unroll
+              for (int j = 0; j < kBCta / 64; ++j) {
+                if (kind == kApply)
+                  tma_load<CG>(pb + j * 8192, map_b, bn + j * 64, k, zb, bar);
+                else
+                  tma_load<CG>(pb + j * 8192, map_b, k, bn + j * 64, zb, bar);
+              }
+            }
+            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+          }
+        }
+        if (ph + 1 == phases)
+          for (int i = 0; ok && i < STAGES; ++i) {   // the products' last arrivals have to find the barriers there
+            ok = wait(empty + stage, phase_bit ^ 1);
+            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+          }
+      }
+      if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- products
+        const uint32_t idesc = (1u << 4) | ((kind == kApply ? 1u : 0u) << 16) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
+        const uint32_t b_step = kind == kApply ? 16 * 128 : 32, b_lbo = kind == kApply ? 8192 : 16;
+        for (int i = first; ok && find_tile<CG, BN>(a, kind, i, &at, &t); i += step) {
+          const Matrix& m = a.mat[at];
+          const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+          if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
+          fence_after();
+          for (int kb = 0; kb < blocks; ++kb) {
+            if (!(ok = wait(full + stage, phase_bit))) break;
+            fence_after();
+            const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
+#pragma unroll
+            for (int j = 0; j < kBlockK / 16; ++j)
+              mma<CG>(tmem + acc * BN, operand(pa + j * 32, 16, 1024), operand(pb + j * b_step, b_lbo, 1024), idesc, kb > 0 || j > 0);
+            commit<CG>(empty + stage);
+            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+          }
+          if (!ok) break;
+          commit<CG>(sum_full + acc);
+          if (++acc == 2) acc = 0, acc_bit ^= 1;
+        }
+      }
+      next_phase(ph);
+    }
+  } else {
+    // ---- endings
+    more_registers();
+    const int group = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32;
+    int acc = 0;
+    uint32_t acc_bit = 0;
+    Part p;
+    p.zero = p.bad = false;
+    p.cols = BN / 2;
+    p.ex = {exchange + (warp - 4) * kExchange, lane};
+    for (int ph = 0; ph < phases; ++ph) {
+      const int kind = ph % 3, k_step = ph / 3, slab = k_step & 1;
+      int at = 0;
+      for (int i = first; find_tile<CG, BN>(a, kind, i, &at, &p.tile); i += step) {
+        const Matrix& m = a.mat[at];
+        p.m = m.m;
+        p.n = m.n;
+        p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
+        p.col = p.tile.n0 + group * p.cols;
+        p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
+        auto arrived = [&] {
+          const bool there = wait(sum_full + acc, acc_bit);
+          p.bad = __any_sync(0xffffffffu, !there) || p.bad;
+          fence_after();
+        };
+        if (kind == kGram) {
+          arrived();
+          end_gram(m, p);
+        } else if (kind == kPoly) {
+          Ahead<BN / 64> f;
+          f.fetch(p, m.fe, m.lda);
+          arrived();
+          end_poly(m, p, f, a.coef[k_step][1], a.coef[k_step][2]);
+        } else {
+          Ahead<BN / 64> h, l;
+          h.fetch(p, m.hi + slab * (static_cast<int64_t>(m.m) * m.ldx), m.ldx);
+          l.fetch(p, m.lo, m.ldx);
+          arrived();
+          if (k_step + 1 < a.steps)
+            end_next(m, p, h, l, slab, a.coef[k_step][0]);
+          else
+            end_last(m, p, h, l, a.coef[k_step][0], a.out, a.keep, a.status);
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
+        if (++acc == 2) acc = 0, acc_bit ^= 1;
+      }
+      // what was written here is read by other CTAs' bulk copies after the barrier
+      asm volatile("fence.proxy.async;" ::: "memory");
+      next_phase(ph);
+    }
   }
-};
+  if (*off != 0 && threadIdx.x == 0) {
+    // Copies and products that were under way when a wait ran out: they are done in microseconds.
+    const long long from = clock64();
+    while (clock64() - from < 2000000) {
+    }
+  }
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 2) tmem_free<CG>(tmem, kCols);
+}
 
 // ---- host side ------------------------------------------------------------------------
 adaf_status fail(adaf_status st, const std::string& msg) { return meo::set_last_error(st, ("muon: " + msg).c_str()); }
@@ -486,9 +778,9 @@ adaf_status cuda_fail(cudaError_t e, const char* what) {
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-const char* const kKernelNames[] = {"k_muon_moment", "k_muon_pack", "k_muon_gram", "k_muon_poly", "k_muon_apply"};
-constexpr int kNumKernels = 5;
-enum Slot { kSlotMoment, kSlotPack, kSlotGram, kSlotPoly, kSlotApply };
+const char* const kKernelNames[] = {"k_muon_moment", "k_muon_pack", "k_muon_iterate"};
+constexpr int kNumKernels = 3;
+enum Slot { kSlotMoment, kSlotPack, kSlotIterate };
 meo::tc::Profile g_profile;
 thread_local bool t_stall = false;
 
@@ -528,13 +820,13 @@ adaf_status check_hp(const muon_hparams* hp) {
 }
 
 // One matrix of the list.
-struct Matrix {
+struct Listed {
   int64_t m, n;
   int64_t rows, cols;
   float* p;
   const void* u;
   float* mom;
-  unsigned char flags;
+  int32_t flags;
 };
 
 adaf_status check_size(int64_t batch, int64_t rows, int64_t cols, const std::string& who) {
@@ -542,58 +834,55 @@ adaf_status check_size(int64_t batch, int64_t rows, int64_t cols, const std::str
   if (batch == 0 || rows == 0 || cols == 0) return ADAF_OK;
   if (rows > kMaxSide || cols > kMaxSide || rows * cols > INT32_MAX)
     return fail(ADAF_ERR_UNSUPPORTED, who + "a side above 2^20 or more than 2^31 - 1 values a matrix");
-  if (batch > (1 << 24)) return fail(ADAF_ERR_UNSUPPORTED, who + "more than 2^24 matrices");
+  if (batch > kMaxMatrices) return fail(ADAF_ERR_UNSUPPORTED, who + "more than 2^20 matrices");
   return ADAF_OK;
 }
 
-int group_size(int64_t m, int64_t n, int64_t count) {
-  return static_cast<int>(std::min<int64_t>({count, kMaxGroup, std::max<int64_t>(1, kGroupValues / (m * n))}));
-}
-
+// Bytes of a matrix in the workspace, and where its parts are.
 struct Layout {
-  size_t part, hi0, hi1, lo, f, e, d, g, bytes;
+  size_t hi, lo, fe, dg, bytes;
 };
-Layout layout(int64_t m, int64_t n, int64_t count) {
+Layout layout(int64_t m, int64_t n) {
   const int64_t ldx = round_up(n, 8), lda = round_up(m, 8);
   Layout L{};
-  size_t o = 256;   // the status word
-  auto take = [&](size_t bytes) {
-    const size_t at = o;
-    o = static_cast<size_t>(round_up(static_cast<int64_t>(o + bytes), 256));
+  auto take = [&](int64_t bytes) {
+    const size_t at = L.bytes;
+    L.bytes += static_cast<size_t>(round_up(bytes, 256));
     return at;
   };
-  const size_t x = static_cast<size_t>(count) * m * ldx * 2, s = static_cast<size_t>(count) * m * lda * 2;
-  L.part = take(static_cast<size_t>(count) * kMaxParts * 4);
-  L.hi0 = take(x);
-  L.hi1 = take(x);
-  L.lo = take(x);
-  L.f = take(s);
-  L.e = take(s);
-  L.d = take(static_cast<size_t>(count) * lda * 4);
-  L.g = take(static_cast<size_t>(count) * lda * 4);
-  L.bytes = o;
+  L.hi = take(2 * m * ldx * 2);
+  L.lo = take(m * ldx * 2);
+  L.fe = take(2 * m * lda * 2);
+  L.dg = take(2 * lda * 4);
   return L;
 }
-
-// Bytes for all groups of a sorted list of (m, n), one after another in the same memory.
-size_t bytes_of(std::vector<std::pair<std::pair<int64_t, int64_t>, int64_t>>& sizes) {
-  std::sort(sizes.begin(), sizes.end());
-  size_t most = 256;
-  for (size_t i = 0; i < sizes.size();) {
-    int64_t count = 0;
-    size_t j = i;
-    for (; j < sizes.size() && sizes[j].first == sizes[i].first; ++j) count += sizes[j].second;
-    const int64_t m = sizes[i].first.first, n = sizes[i].first.second;
-    most = std::max(most, layout(m, n, group_size(m, n, count)).bytes);
-    i = j;
-  }
-  return most;
+int32_t parts_of(int64_t m, int64_t n) {
+  return static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
 }
+constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4;   // the status word, the barrier, the sums' parts
+
+// Matrices are worked on in the order of their sizes, the longest sums first; a
+// group ends at so many matrices or values.
+using Size = std::pair<int64_t, int64_t>;   // n, m
+bool before(const Size& x, const Size& y) { return x > y; }
+struct Grouping {
+  int64_t count = 0, values = 0;
+  size_t bytes = kHead, most = 0;
+  // Whether a group that goes on with this matrix would be too large.
+  bool full(const Size& z) const { return count == kMaxGroup || (count > 0 && values + z.first * z.second > kGroupValues); }
+  void add(const Size& z) {
+    if (full(z)) *this = Grouping{0, 0, kHead, most};
+    ++count;
+    values += z.first * z.second;
+    bytes += layout(z.second, z.first).bytes;
+    most = std::max(most, bytes);
+  }
+};
 
 adaf_status check_tensors(const muon_tensor* tensors, int32_t n, size_t* bytes) {
   if (n < 0) return invalid("n < 0");
   if (n > 0 && tensors == nullptr) return invalid("tensors is NULL");
-  std::vector<std::pair<std::pair<int64_t, int64_t>, int64_t>> sizes;
+  std::vector<std::pair<Size, int64_t>> sizes;
   int64_t total = 0;
   for (int32_t i = 0; i < n; ++i) {
     const muon_tensor& t = tensors[i];
@@ -602,10 +891,14 @@ adaf_status check_tensors(const muon_tensor* tensors, int32_t n, size_t* bytes) 
     if (st != ADAF_OK) return st;
     if (t.grad_dtype != ADAF_FLOAT32 && t.grad_dtype != ADAF_BFLOAT16) return invalid(who + "unknown grad_dtype");
     if (t.batch == 0 || t.rows == 0 || t.cols == 0) continue;
-    if ((total += t.batch) > (1 << 24)) return fail(ADAF_ERR_UNSUPPORTED, "more than 2^24 matrices");
-    sizes.push_back({{std::min(t.rows, t.cols), std::max(t.rows, t.cols)}, t.batch});
+    if ((total += t.batch) > kMaxMatrices) return fail(ADAF_ERR_UNSUPPORTED, "more than 2^20 matrices");
+    sizes.push_back({{std::max(t.rows, t.cols), std::min(t.rows, t.cols)}, t.batch});
   }
-  *bytes = sizes.empty() ? 0 : bytes_of(sizes);
+  std::stable_sort(sizes.begin(), sizes.end(), [](const auto& x, const auto& y) { return before(x.first, y.first); });
+  Grouping g;
+  for (const auto& z : sizes)
+    for (int64_t b = 0; b < z.second; ++b) g.add(z.first);
+  *bytes = g.most;
   return ADAF_OK;
 }
 
@@ -620,16 +913,10 @@ struct Call {
   const muon_iteration* it;
   const muon_hparams* hp;      // NULL: orthogonalise
   int64_t stride_r;
-  int32_t out_bf16;
+  int32_t out;
   unsigned char* ws;
   cudaStream_t s;
 };
-
-template <int CG, int BN, int STAGES, bool B_MN, class End>
-cudaError_t product(int slot, const CUtensorMap& a, const CUtensorMap& b, const Shape& s, const typename End::Args& end,
-                    cudaStream_t stream) {
-  return g_profile.run(slot, stream, [&] { return meo::tc::launch_product<CG, BN, STAGES, false, B_MN, false, End>(a, b, s, end, stream); });
-}
 
 #define MUON_TRY(expr, what)                          \
   do {                                                \
@@ -637,125 +924,148 @@ cudaError_t product(int slot, const CUtensorMap& a, const CUtensorMap& b, const 
     if (e_ != cudaSuccess) return cuda_fail(e_, what); \
   } while (0)
 
-// The iteration on one group; x is packed in hi0, lo.
-template <int CG, int BN, int STAGES>
-adaf_status iterate(const Call& c, const Layout& L, const Group& grp, int64_t m, int64_t n, int count, float keep) {
-  unsigned char* const ws = c.ws;
-  const int64_t ldx = round_up(n, 8), lda = round_up(m, 8);
-  __half* hi[2] = {reinterpret_cast<__half*>(ws + L.hi0), reinterpret_cast<__half*>(ws + L.hi1)};
-  __half* const lo = reinterpret_cast<__half*>(ws + L.lo);
-  __half* const f = reinterpret_cast<__half*>(ws + L.f);
-  __half* const e = reinterpret_cast<__half*>(ws + L.e);
-  float* const d = reinterpret_cast<float*>(ws + L.d);
-  float* const g = reinterpret_cast<float*>(ws + L.g);
-  CUtensorMap xk[2], xn[2], fk, ek;
-  bool ok = true;
-  for (int i = 0; i < 2; ++i) {
-    ok = ok && meo::tc::make_map(&xk[i], hi[i], false, m, n, ldx, count, m * ldx, meo::tc::kBoxK);
-    ok = ok && meo::tc::make_map(&xn[i], hi[i], false, m, n, ldx, count, m * ldx, meo::tc::kBoxMN);
-  }
-  ok = ok && meo::tc::make_map(&fk, f, false, m, m, lda, count, m * lda, meo::tc::kBoxK);
-  ok = ok && meo::tc::make_map(&ek, e, false, m, m, lda, count, m * lda, meo::tc::kBoxK);
-  if (!ok) return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  Shape sq{};
-  sq.m = sq.n = static_cast<int32_t>(m);
-  sq.batch = count;
-  sq.splits = 1;
-  sq.group = 8;
-  sq.status = reinterpret_cast<int32_t*>(ws);
-  sq.stall = t_stall ? 1 : 0;
-  for (int k = 0; k < c.it->steps; ++k) {
-    const float ca = static_cast<float>(c.it->coef[k][0]), cb = static_cast<float>(c.it->coef[k][1]),
-                cc = static_cast<float>(c.it->coef[k][2]);
-    Shape s = sq;
-    s.k = static_cast<int32_t>(n);
-    MUON_TRY((product<CG, BN, STAGES, false, GramEnd>(kSlotGram, xk[k & 1], xk[k & 1], s, {f, d, static_cast<int32_t>(lda)}, c.s)), "k_muon_gram");
-    s.k = static_cast<int32_t>(m);
-    MUON_TRY((product<CG, BN, STAGES, false, PolyEnd>(kSlotPoly, fk, fk, s, {f, d, e, g, static_cast<int32_t>(lda), cb, cc}, c.s)), "k_muon_poly");
-    s.n = static_cast<int32_t>(n);
-    ApplyEnd<kNext>::Args next{hi[k & 1], lo, hi[(k + 1) & 1], g, static_cast<int32_t>(ldx), static_cast<int32_t>(lda), ca, keep, c.out_bf16, sq.status};
-    if (k + 1 < c.it->steps) {
-      MUON_TRY((product<CG, BN, STAGES, true, NextEnd>(kSlotApply, ek, xn[k & 1], s, next, c.s)), "k_muon_apply");
-    } else if (c.hp != nullptr) {
-      LastEnd<kUpdate>::Args last;
-      std::memcpy(static_cast<ApplyEnd<kUpdate>::Args*>(&last), &next, sizeof next);
-      last.grp = grp;
-      MUON_TRY((product<CG, BN, STAGES, true, LastEnd<kUpdate>>(kSlotApply, ek, xn[k & 1], s, last, c.s)), "k_muon_apply");
-    } else {
-      LastEnd<kResult>::Args last;
-      std::memcpy(static_cast<ApplyEnd<kResult>::Args*>(&last), &next, sizeof next);
-      last.grp = grp;
-      MUON_TRY((product<CG, BN, STAGES, true, LastEnd<kResult>>(kSlotApply, ek, xn[k & 1], s, last, c.s)), "k_muon_apply");
+template <int CG, int BN, int STAGES, int COUNT>
+adaf_status iterate(const Call& c, const Listed* mats, int count) {
+  using namespace meo::tc;
+  auto* const kernel = k_muon_iterate<CG, BN, STAGES, COUNT>;
+  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes;
+  IterateArgs<COUNT> a;
+  std::memset(&a, 0, sizeof a);
+  a.count = count;
+  a.steps = c.it->steps;
+  for (int k = 0; k < a.steps; ++k)
+    for (int q = 0; q < 3; ++q) a.coef[k][q] = static_cast<float>(c.it->coef[k][q]);
+  a.out = c.out;
+  a.keep = c.hp != nullptr ? static_cast<float>(1.0 - c.hp->lr * c.hp->weight_decay) : 1.f;
+  a.stall = t_stall ? 1 : 0;
+  a.status = reinterpret_cast<int32_t*>(c.ws);
+  a.barrier = reinterpret_cast<unsigned*>(c.ws) + 1;
+  unsigned char* at = c.ws + kHead;
+  for (int i = 0; i < count; ++i) {
+    const Listed& z = mats[i];
+    const Layout L = layout(z.m, z.n);
+    Matrix& m = a.mat[i];
+    m.hi = reinterpret_cast<__half*>(at + L.hi);
+    m.lo = reinterpret_cast<__half*>(at + L.lo);
+    m.fe = reinterpret_cast<__half*>(at + L.fe);
+    m.dg = reinterpret_cast<float*>(at + L.dg);
+    at += L.bytes;
+    m.p = z.p;
+    m.m = static_cast<int32_t>(z.m);
+    m.n = static_cast<int32_t>(z.n);
+    m.ldx = static_cast<int32_t>(round_up(z.n, 8));
+    m.lda = static_cast<int32_t>(round_up(z.m, 8));
+    m.flags = z.flags;
+    if (c.hp != nullptr) {
+      const double h = static_cast<double>(z.rows), w = static_cast<double>(z.cols);
+      const bool original = c.hp->adjust_lr == MUON_ADJUST_ORIGINAL;
+      m.rate = static_cast<float>(c.hp->lr * (original ? std::sqrt(std::max(1.0, h / w)) : 0.2 * std::sqrt(std::max(h, w))));
     }
+    if (!make_map(&m.x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
+        !make_map(&m.s, m.fe, false, z.m, z.m, m.lda, 2, z.m * m.lda, 64))
+      return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    const int64_t mt = (z.m + BN - 1) / BN, nt = (z.n + BN - 1) / BN;
+    m.sym0 = a.sym_tiles;
+    m.app0 = a.app_tiles;
+    a.sym_tiles += static_cast<int32_t>(mt * (mt + 1) / 2);
+    a.app_tiles += static_cast<int32_t>(mt * nt);
   }
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.stream = c.s;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {CG, 1, 1};
+  cfg.numAttrs = CG > 1 ? 2 : 1;
+  // Clusters that can be there together, which the barrier needs: asked for once a device.
+  static std::atomic<int> together[64];
+  int device = 0, sms = 0;
+  MUON_TRY(sm_count(&device, &sms), "current device");
+  int most = device < 64 ? together[device].load() : 0;
+  if (most == 0) {
+    MUON_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes), "k_muon_iterate");
+    most = sms;
+    if (CG > 1) {
+      cfg.gridDim = dim3(static_cast<unsigned>(sms / CG * CG));
+      MUON_TRY(cudaOccupancyMaxActiveClusters(&most, kernel, &cfg), "k_muon_iterate");
+    }
+    if (most < 1) return fail(ADAF_ERR_CUDA, "k_muon_iterate does not fit this device");
+    if (device < 64) together[device] = most;
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(most, std::max(a.sym_tiles, a.app_tiles)) * CG));
+  MUON_TRY(g_profile.run(kSlotIterate, c.s, [&] { return cudaLaunchKernelEx(&cfg, kernel, a); }), "k_muon_iterate");
   return ADAF_OK;
 }
 
 template <bool STEP>
-adaf_status run_group(const Call& c, const Matrix* mats, int count, bool first) {
-  const int64_t m = mats[0].m, n = mats[0].n;
-  const Layout L = layout(m, n, count);
-  Group grp;
-  std::memset(&grp, 0, sizeof grp);
-  for (int i = 0; i < count; ++i) {
-    grp.p[i] = mats[i].p;
-    grp.u[i] = mats[i].u;
-    grp.mom[i] = mats[i].mom;
-    grp.flags[i] = mats[i].flags;
-    if (STEP) {
-      const double h = static_cast<double>(mats[i].rows), w = static_cast<double>(mats[i].cols);
-      const bool original = c.hp->adjust_lr == MUON_ADJUST_ORIGINAL;
-      grp.rate[i] = static_cast<float>(c.hp->lr * (original ? std::sqrt(std::max(1.0, h / w)) : 0.2 * std::sqrt(std::max(h, w))));
-    }
-  }
-  MuonArgs a{};
-  a.m = static_cast<int32_t>(m);
-  a.n = static_cast<int32_t>(n);
-  a.ldx = static_cast<int32_t>(round_up(n, 8));
-  a.lda = static_cast<int32_t>(round_up(m, 8));
-  a.parts = static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
+adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) {
+  MuonArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.count = count;
   a.stride_r = c.stride_r;
   a.eps = static_cast<float>(c.it->eps);
   if (STEP) {
     a.mu = static_cast<float>(c.hp->momentum);
     a.nesterov_mu = c.hp->nesterov != 0 ? a.mu : -1.f;
   }
-  a.part = reinterpret_cast<float*>(c.ws + L.part);
-  a.hi = reinterpret_cast<__half*>(c.ws + L.hi0);
-  a.lo = reinterpret_cast<__half*>(c.ws + L.lo);
   a.status = reinterpret_cast<int32_t*>(c.ws);
+  a.barrier = reinterpret_cast<unsigned*>(c.ws) + 1;
+  a.part = reinterpret_cast<float*>(c.ws + 256);
   a.clear = first ? 1 : 0;
-  // (rows and columns as u has them only matter where its rows have gaps: then there is one shape)
+  unsigned char* at = c.ws + kHead;
+  int32_t parts = 0, tiles = 0;
+  int64_t big = 0;
+  for (int i = 0; i < count; ++i) {
+    const Listed& z = mats[i];
+    const Layout L = layout(z.m, z.n);
+    Item& t = a.item[i];
+    t.u = z.u;
+    t.mom = z.mom;
+    t.hi = reinterpret_cast<__half*>(at + L.hi);
+    t.lo = reinterpret_cast<__half*>(at + L.lo);
+    at += L.bytes;
+    t.rows = static_cast<int32_t>(z.rows);
+    t.cols = static_cast<int32_t>(z.cols);
+    t.m = static_cast<int32_t>(z.m);
+    t.n = static_cast<int32_t>(z.n);
+    t.ldx = static_cast<int32_t>(round_up(z.n, 8));
+    t.flags = z.flags;
+    t.parts = parts_of(z.m, z.n);
+    t.part0 = parts;
+    t.tile0 = tiles;
+    parts += t.parts;
+    tiles += static_cast<int32_t>(((z.m + 63) / 64) * ((z.n + 63) / 64));
+    const int64_t mt = (z.m + 255) / 256;
+    big += mt * (mt + 1) / 2;
+  }
   MUON_TRY(g_profile.run(kSlotMoment, c.s, [&] {
-    k_muon_moment<STEP><<<dim3(a.parts, count), 256, 0, c.s>>>(grp, a, static_cast<int32_t>(mats[0].rows), static_cast<int32_t>(mats[0].cols));
+    k_muon_moment<STEP><<<static_cast<unsigned>(parts), 256, 0, c.s>>>(a);
     return cudaGetLastError();
   }), "k_muon_moment");
   MUON_TRY(g_profile.run(kSlotPack, c.s, [&] {
-    k_muon_pack<STEP><<<dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), count), 256, 0, c.s>>>(
-        grp, a, static_cast<int32_t>(m), static_cast<int32_t>(n));
+    k_muon_pack<STEP><<<static_cast<unsigned>(tiles), 256, 0, c.s>>>(a);
     return cudaGetLastError();
   }), "k_muon_pack");
-  const float keep = STEP ? static_cast<float>(1.0 - c.hp->lr * c.hp->weight_decay) : 1.f;
-  const int64_t big = ((m + 255) / 256) * ((m + 255) / 256 + 1) / 2 * count;
-  if (big >= 64) return iterate<2, 256, 6>(c, L, grp, m, n, count, keep);
-  return iterate<1, 128, 6>(c, L, grp, m, n, count, keep);
+  if (big >= 64) return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count) : iterate<2, 256, 6, kMaxGroup>(c, mats, count);
+  return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count) : iterate<1, 128, 6, kMaxGroup>(c, mats, count);
 }
 
 template <bool STEP>
-adaf_status run(const Call& c, std::vector<Matrix>& mats) {
-  // matrices of the same sides, tall and wide ones, are worked on together
-  std::stable_sort(mats.begin(), mats.end(),
-                   [](const Matrix& x, const Matrix& y) { return std::make_pair(x.m, x.n) < std::make_pair(y.m, y.n); });
+adaf_status run(const Call& c, std::vector<Listed>& mats) {
+  std::stable_sort(mats.begin(), mats.end(), [](const Listed& x, const Listed& y) { return before({x.n, x.m}, {y.n, y.m}); });
   bool first = true;
   for (size_t i = 0; i < mats.size();) {
+    Grouping g;
     size_t j = i;
-    while (j < mats.size() && mats[j].m == mats[i].m && mats[j].n == mats[i].n) ++j;
-    const int most = group_size(mats[i].m, mats[i].n, static_cast<int64_t>(j - i));
-    for (; i < j; i += static_cast<size_t>(most)) {
-      const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(std::min<size_t>(static_cast<size_t>(most), j - i)), first);
-      if (st != ADAF_OK) return st;
-      first = false;
-    }
+    for (; j < mats.size() && !g.full({mats[j].n, mats[j].m}); ++j) g.add({mats[j].n, mats[j].m});
+    const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(j - i), first);
+    if (st != ADAF_OK) return st;
+    first = false;
     i = j;
   }
   return ADAF_OK;
@@ -789,9 +1099,10 @@ adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64
   if (bytes == nullptr) return invalid("bytes is NULL");
   const adaf_status st = check_size(batch, rows, cols, "");
   if (st != ADAF_OK) return st;
-  std::vector<std::pair<std::pair<int64_t, int64_t>, int64_t>> sizes;
-  if (batch > 0 && rows > 0 && cols > 0) sizes.push_back({{std::min(rows, cols), std::max(rows, cols)}, batch});
-  *bytes = sizes.empty() ? 0 : bytes_of(sizes);
+  Grouping g;
+  if (rows > 0 && cols > 0)
+    for (int64_t b = 0; b < batch; ++b) g.add({std::max(rows, cols), std::min(rows, cols)});
+  *bytes = g.most;
   return ADAF_OK;
 }
 
@@ -801,7 +1112,7 @@ adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams*
   if (st != ADAF_OK) return st;
   size_t need = 0;
   if ((st = check_tensors(tensors, n, &need)) != ADAF_OK) return st;
-  std::vector<Matrix> mats;
+  std::vector<Listed> mats;
   for (int32_t i = 0; i < n; ++i) {
     const muon_tensor& t = tensors[i];
     if (t.batch == 0 || t.rows == 0 || t.cols == 0) continue;
@@ -813,11 +1124,11 @@ adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams*
     for (int64_t b = 0; b < t.batch; ++b)
       mats.push_back({std::min(t.rows, t.cols), std::max(t.rows, t.cols), t.rows, t.cols, t.p + b * numel,
                       static_cast<const char*>(t.g) + static_cast<size_t>(b * numel) * es, t.momentum + b * numel,
-                      static_cast<unsigned char>((t.rows > t.cols ? kTurned : 0) | (es == 2 ? kBf16 : 0))});
+                      (t.rows > t.cols ? kTurned : 0) | (es == 2 ? kBf16 : 0)});
   }
   if (mats.empty()) return ADAF_OK;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ADAF_OK) return st;
-  const Call c{&hp->iteration, hp, 0, 0, static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream)};
+  const Call c{&hp->iteration, hp, 0, kUpdate, static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream)};
   return run<true>(c, mats);
 }
 
@@ -843,14 +1154,14 @@ adaf_status muon_orthogonalize(const muon_matrices* x, const muon_iteration* it,
   const bool same = x0 == o0 && es == os && (x->rows == 1 || x->stride_r == x->cols) && (x->batch == 1 || x->stride_b == numel);
   if (!same && x0 < o1 && o0 < x1) return invalid("out overlaps x, and is not x itself");
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ADAF_OK) return st;
-  std::vector<Matrix> mats;
+  std::vector<Listed> mats;
   for (int64_t b = 0; b < x->batch; ++b)
     mats.push_back({std::min(x->rows, x->cols), std::max(x->rows, x->cols), x->rows, x->cols,
                     reinterpret_cast<float*>(static_cast<char*>(out) + static_cast<size_t>(b * numel) * os),
                     static_cast<const char*>(x->x) + static_cast<size_t>(b * x->stride_b) * es, nullptr,
-                    static_cast<unsigned char>((x->rows > x->cols ? kTurned : 0) | (es == 2 ? kBf16 : 0))});
-  const Call c{it, nullptr, x->rows == 1 ? x->cols : x->stride_r, os == 2 ? 1 : 0, static_cast<unsigned char*>(workspace),
-               static_cast<cudaStream_t>(stream)};
+                    (x->rows > x->cols ? kTurned : 0) | (es == 2 ? kBf16 : 0)});
+  const Call c{it, nullptr, x->rows == 1 ? x->cols : x->stride_r, os == 2 ? kBf16Out : kFp32,
+               static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream)};
   return run<false>(c, mats);
 }
 

@@ -60,18 +60,25 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// (relaxed: what it tells of is tensor memory, which the tcgen05 fences order; a release at
+// cluster scope waits for the thread's global stores, a microsecond or two at every tile)
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(shared_at(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
+// The endings' warps take registers over from the first four (at launch all have 168: 384
+// threads of 65536): 128 x 64 + 256 x 216 = 63488 of the 64512 that the block holds.  Each is
+// called by all warps of its kind at the head of their branch.
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -142,6 +149,18 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // Descriptor of an operand in shared memory, 128-byte swizzle: rows of 128 bytes,
 // groups of 8 rows 1024 bytes apart (`sbo`).  K-major: a row is 64 k values of one
 // i or j.  MN-major: a row is 64 i or j of one k; blocks of 64 i or j `lbo` apart.
@@ -164,6 +183,52 @@ __device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, in
                  "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
                  : "memory");
 }
+
+// ---- a tile's rows and memory --------------------------------------------------------
+// In an ending a lane holds a row of the result, 64 bytes of it at a time.  Read or
+// written that way, an instruction touches 32 rows, 16 bytes of each, and a tile of
+// 128 x 256 took 5 us (bf16) to 15 us (two fp16 in, two out).  Through 2.5 KB of
+// shared memory a warp, four lanes side by side hold a row's 64 bytes.
+constexpr int kPitch = 80;                       // of a row in shared memory
+constexpr int kExchange = 32 * kPitch;           // bytes of a warp
+
+struct Exchange {
+  unsigned char* at;
+  int lane;
+  __device__ __forceinline__ void to_rows(uint4 (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + (8 * i + (lane >> 2)) * kPitch + (lane & 3) * 16) = w[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(at + lane * kPitch + 16 * i);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void to_memory(uint4 (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(at + lane * kPitch + 16 * i) = w[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4*>(at + (8 * i + (lane >> 2)) * kPitch + (lane & 3) * 16);
+    __syncwarp();
+  }
+  // In memory order: lane l has 16 bytes from byte place() of rows row(0) .. row(3) of the warp's.
+  __device__ __forceinline__ int row(int i) const { return 8 * i + (lane >> 2); }
+  __device__ __forceinline__ int place() const { return (lane & 3) * 16; }
+  // 64 bytes of each of `rows` rows from p on, `pitch` bytes apart, of which `left` (a multiple
+  // of 16) are there; zeros beyond.
+  __device__ __forceinline__ void fetch(const void* p, int64_t pitch, int rows, int left, uint4 (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (row(i) < rows && place() < left) w[i] = *reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) + row(i) * pitch + place());
+    }
+  }
+  __device__ __forceinline__ void put(void* p, int64_t pitch, int rows, int left, const uint4 (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row(i) < rows && place() < left) *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p) + row(i) * pitch + place()) = w[i];
+  }
+};
 
 // ---- the product --------------------------------------------------------------------
 struct Shape {
@@ -190,7 +255,9 @@ struct Part {
   int32_t col, cols;      // its columns: col, ..., col + cols - 1 (a multiple of 32)
   int32_t m, n;
   uint32_t tmem;
+  Exchange ex;            // of the warp
   bool zero, bad;         // there was nothing to sum; a wait ran out
+  __device__ __forceinline__ int row0() const { return row - ex.lane; }   // the warp's first row
   __device__ __forceinline__ void load(int c, float (&v)[32]) const {
     tmem_load(tmem + c, v);
     if (zero || bad) {
@@ -242,11 +309,16 @@ struct Shared {
   static constexpr int kB = BN / CG * kBlockK * 2;
   static constexpr int kStage = kA + kB;
   static constexpr int kBars = 2 * STAGES + 4;
-  static constexpr int bytes = STAGES * kStage + kBars * 8 + 64 + 1024;   // and the alignment to 1024
+  static constexpr int bytes = STAGES * kStage + kEndWarps * kExchange + kBars * 8 + 64 + 1024;   // and the alignment to 1024
 };
 
 // End: what is done with a result tile.
-//   static constexpr bool kSym; struct Args; static __device__ void part(const Args&, const Part&)
+//   static constexpr bool kSym; struct Args;
+//   static constexpr int kChunk = 0;   static __device__ void part(const Args&, const Part&)
+// or, with kChunk > 0, static __device__ void whole(const Args&, const Part&, float (&v)[BN / 2]):
+// the sums are taken out of tensor memory every kChunk stages and added up in registers.  The
+// tensor cores cut off what does not fit a sum's 24 bits, so a long sum is off toward zero by
+// 2^-25 of itself for each of its steps of 16 values; parts of 256 values leave next to nothing.
 template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
 __global__ void __launch_bounds__(kThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape s,
@@ -256,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kBCta = BN / CG;          // rows of B (columns of the result) that a CTA loads
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024 - (shared_at(raw) & 1023)) & 1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + STAGES * S::kStage);
+  unsigned char* const exchange = ring + STAGES * S::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(exchange + kEndWarps * kExchange);
   uint64_t* empty = full + STAGES;
   uint64_t* sum_full = empty + STAGES;
   uint64_t* sum_empty = sum_full + 2;
@@ -304,8 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    fewer_registers();
+    if (warp == 0 && lane == 0) {
       // ---- copies
       int stage = 0;
       uint32_t phase = 0;
@@ -344,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == STAGES) stage = 0, phase ^= 1;
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (warp == 1 && lane == 0 && rank == 0) {
       // ---- products
       constexpr uint32_t idesc = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((A_MN ? 1u : 0u) << 15) |
                                  ((B_MN ? 1u : 0u) << 16) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
@@ -358,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
         if (!(ok = wait(sum_empty + acc, acc_phase ^ 1))) break;
         fence_after();
+        bool fresh = true;   // nothing summed yet
         for (int kb = b0; kb < b1; ++kb) {
           if (!(ok = wait(full + stage, phase))) break;
           fence_after();
@@ -365,17 +439,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kBlockK / 16; ++j)
             mma<CG>(tmem + acc * BN, operand(a + j * a_step, A_MN ? 64 * kBlockK * 2 : 16, 1024),
-                    operand(b + j * b_step, B_MN ? 64 * kBlockK * 2 : 16, 1024), idesc, kb > b0 || j > 0);
+                    operand(b + j * b_step, B_MN ? 64 * kBlockK * 2 : 16, 1024), idesc, !fresh || j > 0);
+          fresh = false;
           commit<CG>(empty + stage);
           if (++stage == STAGES) stage = 0, phase ^= 1;
+          if (End::kChunk > 0 && kb + 1 < b1 && (kb + 1 - b0) % max(End::kChunk, 1) == 0) {
+            commit<CG>(sum_full + acc);
+            if (++acc == 2) acc = 0, acc_phase ^= 1;
+            if (!(ok = wait(sum_empty + acc, acc_phase ^ 1))) break;
+            fence_after();
+            fresh = true;
+          }
         }
         if (!ok) break;
         commit<CG>(sum_full + acc);
         if (++acc == 2) acc = 0, acc_phase ^= 1;
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ---- endings
+    more_registers();
     const int group = (warp - 4) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32;
     int acc = 0;
@@ -384,21 +467,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.m = m;
     p.n = s.n;
     p.bad = false;
+    p.ex = {exchange + (warp - 4) * kExchange, lane};
     for (int64_t i = first; tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &p.tile); i += step) {
-      const int b0 = p.tile.split * per_split;
-      const bool ok = wait(sum_full + acc, acc_phase);
-      p.bad = __any_sync(0xffffffffu, !ok) || p.bad;
-      fence_after();
-      p.zero = min(blocks, b0 + per_split) <= b0;
+      const int b0 = p.tile.split * per_split, b1 = min(blocks, b0 + per_split);
+      p.zero = b1 <= b0;
       p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
       p.cols = BN / 2;
       p.col = p.tile.n0 + group * p.cols;
-      p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
-      End::part(end, p);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
-      if (++acc == 2) acc = 0, acc_phase ^= 1;
+      auto arrived = [&] {
+        const bool ok = wait(sum_full + acc, acc_phase);
+        p.bad = __any_sync(0xffffffffu, !ok) || p.bad;
+        fence_after();
+        p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
+      };
+      auto release = [&] {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
+        if (++acc == 2) acc = 0, acc_phase ^= 1;
+      };
+      if constexpr (End::kChunk > 0) {
+        float v[BN / 2];
+        for (int kb = b0; kb == b0 || kb < b1; kb += End::kChunk) {
+          arrived();
+#pragma unroll
+          for (int j = 0; j < BN / 2; j += 16) {
+            float w[16];
+            tmem_load16(p.tmem + j, w);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[j + q] = kb == b0 ? w[q] : v[j + q] + w[q];
+          }
+          release();
+        }
+        if (p.zero || p.bad) {
+#pragma unroll
+          for (int j = 0; j < BN / 2; ++j) v[j] = p.bad ? __int_as_float(0x7fc00000) : 0.f;
+        }
+        End::whole(end, p, v);
+      } else {
+        arrived();
+        End::part(end, p);
+        release();
+      }
     }
   }
   __syncwarp();
