@@ -18,7 +18,7 @@
  * from any above 0.01 of the largest sum.
  *
  * Precision.  Products run on the tensor cores with fp16 factors and fp32 sums.
- * x is carried to 22 bits, and the diagonals of A and of b A + c A A, where
+ * x is carried in fp32, and the diagonals of A and of b A + c A A, where
  * most of their size is, are kept in fp32 and multiplied apart, so a rounding
  * is relative to what a step changes and small singular values are not lost in
  * the large ones' roundings: the result is within 1e-3 of the formula

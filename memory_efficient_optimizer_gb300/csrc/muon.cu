@@ -22,8 +22,8 @@
 //     2^-12 or so, and a small singular value stays as accurate as a large one;
 //   - rounding of x where it is carried to the next step adds noise at the level
 //     of the large singular values, which the small ones drown in (they grow by
-//     3.44 a step, and the noise with them).  So x is carried as hi + lo 2^-11,
-//     two fp16 numbers with 22 bits, of which hi is the factor of the products;
+//     3.44 a step, and the noise with them).  So x is carried in fp32, beside the
+//     fp16 copy that is the factor of the products;
 //   - as x comes near orthogonal, A comes near a multiple of I, and a rounding of
 //     the diagonal would weigh most.  With A = D + F, B = G + E (D, G diagonal,
 //     in fp32), A A = F F + D F + F D + D D and a x + B x = (a + G) x + E x: only
@@ -60,7 +60,6 @@ constexpr int kMaxParts = 256;                     // of a matrix's sum of squar
 constexpr int kPartValues = 8192;                  // values of a part, at least
 constexpr int64_t kMaxSide = int64_t{1} << 20;
 constexpr int64_t kMaxMatrices = int64_t{1} << 20;
-constexpr float kLoScale = 2048.f, kLoUnscale = 1.f / 2048.f;
 
 enum Flag : int32_t { kTurned = 1, kBf16 = 2 };   // x is u^T; u is bf16
 
@@ -69,7 +68,7 @@ struct Item {
   const void* u;                   // the gradient, or the matrix to orthogonalise
   float* mom;
   __half* hi;
-  __half* lo;
+  float* x;
   int32_t rows, cols;              // of u
   int32_t m, n, ldx;               // of x: m <= n
   int32_t flags;
@@ -188,9 +187,11 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
-__device__ __forceinline__ void split(float x, __half* hi, __half* lo) {
-  *hi = __float2half_rn(x);
-  *lo = __float2half_rn((x - __half2float(*hi)) * kLoScale);
+// Values that only endings read and write again are kept in the order in which a warp holds them:
+// blocks of 32 x 32, lane l has row l, and word i (16 bytes) of all lanes lies side by side.
+// Then a warp's accesses are whole lines, with nothing to exchange between lanes.
+__device__ __forceinline__ int64_t block_at(int row, int col, int n) {
+  return (static_cast<int64_t>(row >> 5) * ((n + 31) >> 5) + (col >> 5)) << 10;   // values
 }
 
 // x of a matrix, 64 x 64 values a CTA, through shared memory so that both u and
@@ -228,12 +229,18 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonA
     const int r = i >> 5, c = (i & 31) * 2;
     if (x0 + r >= rows || y0 + c >= ldx) continue;
     const float v0 = turned ? tile[c][r] : tile[r][c], v1 = turned ? tile[c + 1][r] : tile[r][c + 1];
-    __half2 h, l;
-    split(v0, &h.x, &l.x);
-    split(v1, &h.y, &l.y);
-    const int64_t at = static_cast<int64_t>(x0 + r) * ldx + y0 + c;
-    *reinterpret_cast<__half2*>(t.hi + at) = h;
-    *reinterpret_cast<__half2*>(t.lo + at) = l;
+    *reinterpret_cast<__half2*>(t.hi + static_cast<int64_t>(x0 + r) * ldx + y0 + c) = __floats2half2_rn(v0, v1);
+  }
+  // four blocks of 32 x 32, two warps each
+  const int blk = threadIdx.x >> 6, r0x = (blk >> 1) * 32, c0x = (blk & 1) * 32, lane = threadIdx.x & 31;
+  if (x0 + r0x < rows && y0 + c0x < cols) {
+    float4* const to = reinterpret_cast<float4*>(t.x + block_at(x0 + r0x, y0 + c0x, cols)) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = i * 2 + ((threadIdx.x >> 5) & 1), r = r0x + lane, c = c0x + 4 * w;
+      to[32 * w] = turned ? make_float4(tile[c][r], tile[c + 1][r], tile[c + 2][r], tile[c + 3][r])
+                          : make_float4(tile[r][c], tile[r][c + 1], tile[r][c + 2], tile[r][c + 3]);
+    }
   }
 }
 
@@ -244,39 +251,25 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float2 unpack(uint32_t r) { return __half22float2(*reinterpret_cast<const __half2*>(&r)); }
 
-// 32 values of a row of a symmetric matrix s [m][ld] (values beyond column m are 0 and
-// go up to ld), and their mirror image in column p.row.
-__device__ __forceinline__ void store_symmetric(__half* s, int ld, const meo::tc::Part& p, int col, const float (&v)[32]) {
-  uint4 w[4];
+// 32 fp16 values a row of a matrix with rows of ld values, from column col on (values beyond the
+// last column are 0 and go up to ld).
+__device__ __forceinline__ void store_rows(__half* to, int ld, const meo::tc::Part& p, int col, uint4 (&w)[4]) {
+  p.ex.to_memory(w);
+  p.ex.put(to + static_cast<int64_t>(p.row0()) * ld + col, static_cast<int64_t>(ld) * 2, p.m - p.row0(), (ld - col) * 2, w);
+}
+__device__ __forceinline__ void pack32(const float (&v)[32], uint4 (&w)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     w[i] = make_uint4(pack(v[8 * i], v[8 * i + 1]), pack(v[8 * i + 2], v[8 * i + 3]), pack(v[8 * i + 4], v[8 * i + 5]),
                       pack(v[8 * i + 6], v[8 * i + 7]));
-  if (p.tile.mirror) {
-    // Two lanes swap halves, so that each stores two values side by side.
-    const bool odd = p.row & 1;
-    const int c = p.row & ~1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      // column col + 2i has (mine.low, theirs.low), column col + 2i + 1 the high ones
-      const uint32_t mine = i % 4 == 0 ? w[i / 4].x : i % 4 == 1 ? w[i / 4].y : i % 4 == 2 ? w[i / 4].z : w[i / 4].w;
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-      const uint32_t pair = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-      const int r = col + 2 * i + (odd ? 1 : 0);
-      if (r < p.m && c < ld) *reinterpret_cast<uint32_t*>(s + static_cast<int64_t>(r) * ld + c) = pair;
-    }
-  }
-  p.ex.to_memory(w);
-  p.ex.put(s + static_cast<int64_t>(p.row0()) * ld + col, static_cast<int64_t>(ld) * 2, p.m - p.row0(), (ld - col) * 2, w);
 }
 
-// A matrix as the products see it.  (Its address in the arguments is that of the tensor maps.)
+// A matrix as the products see it.
 struct Matrix {
-  CUtensorMap x;         // hi [2][m][n]: of this step and of the next
-  CUtensorMap s;         // [2][m][m]: F and E
-  __half* hi;
-  __half* lo;            // read and written in place: nobody else needs a tile's values
-  __half* fe;
+  __half* hi;            // [2][m][ldx]: of this step and of the next
+  float* xb;             // x in blocks (block_at), updated in place
+  __half* fe;            // [2][m][lda]: F and E, the tiles on and above the diagonal
+  __half* fb;            // F in blocks
   float* dg;             // [2][lda]: D and G
   float* p;              // the parameter, or the result
   int32_t m, n, ldx, lda;
@@ -289,7 +282,11 @@ enum Out : int32_t { kUpdate, kFp32, kBf16Out };
 
 template <int COUNT>
 struct IterateArgs {
-  Matrix mat[COUNT];
+  struct {
+    CUtensorMap x, s;    // hi and fe
+  } map[COUNT];
+  Matrix mat[COUNT];     // (copied to shared memory first: at every phase's first tile the constants
+                         // would be asked for anew, a microsecond or two each)
   float coef[MUON_MAX_STEPS][3];
   int32_t count, steps, sym_tiles, app_tiles;
   int32_t out;
@@ -303,153 +300,145 @@ using meo::tc::Part;
 
 // A = x x^T: F = A without its diagonal (scaled by 2^15), D the diagonal.
 __device__ __forceinline__ void end_gram(const Matrix& t, const Part& p) {
+#pragma unroll 1
   for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
+    const int j0 = p.col + c;
     float v[32];
     p.load(c, v);
-    const int diag = p.row - (p.col + c);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] *= 0x1p-15f;
-      if (i == diag) {
-        if (p.row < p.m) t.dg[p.row] = v[i] * 0x1p-15f;
-        v[i] = 0.f;
+    for (int i = 0; i < 32; ++i) v[i] *= 0x1p-15f;
+    if (p.row0() == j0) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        d = i == p.ex.lane ? v[i] : d;
+        v[i] = i == p.ex.lane ? 0.f : v[i];
       }
+      if (p.row < p.m) t.dg[p.row] = d * 0x1p-15f;
     }
-    store_symmetric(t.fe, t.lda, p, p.col + c, v);
+    uint4 w[4];
+    pack32(v, w);
+    if (p.row0() < p.m) {
+      uint4* const to = reinterpret_cast<uint4*>(t.fb + block_at(p.row0(), j0, p.m)) + p.ex.lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[32 * i] = w[i];
+    }
+    store_rows(t.fe, t.lda, p, j0, w);
   }
 }
 
-// What an ending reads beside the sums: the tile's part of one or two 16-bit matrices, 64 bytes
-// of a row a word.  It is asked for before the sums are there: behind the ring's copies, which
-// keep the SM's port to L2 full, an answer takes two microseconds, and a tile's four in a row
-// took longer than its products.
-template <int CHUNKS>
+// What an ending reads beside the sums.  It is asked for before the sums are there: behind the
+// ring's copies, which keep the SM's port to L2 full, an answer takes two microseconds, and a
+// tile's four in a row took longer than its products.
+template <int WORDS, int CHUNKS>
 struct Ahead {
-  uint4 w[CHUNKS][4];
-  __device__ __forceinline__ void fetch(const Part& p, const __half* from, int ld) {
-    const __half* const rows = from + static_cast<int64_t>(p.row0()) * ld + p.col;
+  uint4 w[CHUNKS][WORDS];
+  // `from`: the block of the warp's first row and first column; `left`: columns that are there
+  __device__ __forceinline__ void fetch(const Part& p, const void* from, bool rows, int left) {
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) p.ex.fetch(rows + 32 * c, static_cast<int64_t>(ld) * 2, p.m - p.row0(), (ld - p.col - 32 * c) * 2, w[c]);
+    for (int c = 0; c < CHUNKS; ++c) {
+      const uint4* const at = static_cast<const uint4*>(from) + c * 32 * WORDS + p.ex.lane;
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[c][i] = rows && 32 * c < left ? at[32 * i] : make_uint4(0, 0, 0, 0);
+    }
   }
 };
 
-// B = b A + c A A: E without the diagonal (scaled by 2^14), G the diagonal.
+// B = b A + c A A: E without the diagonal (scaled by 2^14), G the diagonal.  di, dj: D of the row,
+// and of the columns (in the warp's shared memory).
 template <int CHUNKS>
-__device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, Ahead<CHUNKS>& f, float cb, float cc) {
-  const float* const d = t.dg;
-  const float di = p.row < p.m ? d[p.row] : 0.f;
+__device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, const Ahead<4, CHUNKS>& f, float di, const float* dj, float cb,
+                                         float cc) {
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int j0 = p.col + 32 * c;
     if (j0 >= p.m) break;
-    p.ex.to_rows(f.w[c]);
     float v[32];
     p.load(32 * c, v);
-    const int diag = p.row - j0;
+    if (p.row0() == j0) {
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x = i == p.ex.lane ? v[i] : x;
+      if (p.row < p.m) t.dg[t.lda + p.row] = fmaf(cc, fmaf(di, di, x * 0x1p-30f), cb * di);
+    }
+    // ((b + c (d_i + d_j)) F + c F F) 2^14, two columns at a time; F is scaled by 2^15, F F by 2^30
+    const float2 own = make_float2(0.5f * (cb + cc * di), 0.5f * (cb + cc * di)), half_c = make_float2(0.5f * cc, 0.5f * cc),
+                 small_c = make_float2(cc * 0x1p-16f, cc * 0x1p-16f);
+    uint4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (j0 + 8 * i >= t.lda) {
+      const uint32_t r[4] = {f.w[c][i].x, f.w[c][i].y, f.w[c][i].z, f.w[c][i].w};
+      uint32_t o[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[8 * i + q] = 0.f;
-        continue;
+      for (int q = 0; q < 4; ++q) {
+        const float2 d = *reinterpret_cast<const float2*>(dj + 32 * c + 8 * i + 2 * q);
+        const float2 x = __fmul2_rn(small_c, make_float2(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]));
+        const float2 e = __ffma2_rn(unpack(r[q]), __ffma2_rn(half_c, d, own), x);
+        o[q] = pack(e.x, e.y);
       }
-      const uint4 r = f.w[c][i];
-      const float4 d0 = *reinterpret_cast<const float4*>(d + j0 + 8 * i), d1 = *reinterpret_cast<const float4*>(d + j0 + 8 * i + 4);
-      const float dj[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      w[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (p.row0() == j0) {
+      // the diagonal is G's
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float2 two = unpack(w[q >> 1]);
-        const float x16 = (q & 1) ? two.y : two.x;   // F 2^15
-        float& x = v[8 * i + q];                     // (F F) 2^30
-        if (8 * i + q == diag) {
-          if (p.row < p.m) t.dg[t.lda + p.row] = fmaf(cc, fmaf(di, di, x * 0x1p-30f), cb * di);
-          x = 0.f;
-        } else {
-          x = fmaf(x16 * 0.5f, fmaf(cc, di + dj[q], cb), cc * (x * 0x1p-16f));
-        }
+      for (int i = 0; i < 16; ++i) {
+        uint32_t& x = i % 4 == 0 ? w[i / 4].x : i % 4 == 1 ? w[i / 4].y : i % 4 == 2 ? w[i / 4].z : w[i / 4].w;
+        if (p.ex.lane == 2 * i) x &= 0xffff0000u;
+        if (p.ex.lane == 2 * i + 1) x &= 0xffffu;
       }
     }
-    if (p.row >= p.m) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (j0 + i >= p.m) v[i] = 0.f;
-    store_symmetric(t.fe + static_cast<int64_t>(p.m) * t.lda, t.lda, p, j0, v);
+    store_rows(t.fe + static_cast<int64_t>(p.m) * t.lda, t.lda, p, j0, w);
   }
 }
 
 // 32 columns of (a + G) x + E x, scaled by 2^15.
-__device__ __forceinline__ void applied(const Part& p, int c, uint4 (&h)[4], uint4 (&l)[4], float factor, float (&v)[32]) {
-  p.ex.to_rows(h);
-  p.ex.to_rows(l);
+__device__ __forceinline__ void applied(const Part& p, int c, const uint4 (&x)[8], float factor, float (&v)[32]) {
   p.load(c, v);
+  const float2 f = make_float2(factor, factor), s = make_float2(0x1p-14f, 0x1p-14f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t hw[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, lw[4] = {l[i].x, l[i].y, l[i].z, l[i].w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 a = unpack(hw[q]), b = unpack(lw[q]);
-      v[8 * i + 2 * q] = fmaf(factor, fmaf(b.x, kLoUnscale, a.x), v[8 * i + 2 * q] * 0x1p-14f);
-      v[8 * i + 2 * q + 1] = fmaf(factor, fmaf(b.y, kLoUnscale, a.y), v[8 * i + 2 * q + 1] * 0x1p-14f);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = __ffma2_rn(f, make_float2(__uint_as_float(x[i].x), __uint_as_float(x[i].y)), __fmul2_rn(s, make_float2(v[4 * i], v[4 * i + 1])));
+    const float2 b = __ffma2_rn(f, make_float2(__uint_as_float(x[i].z), __uint_as_float(x[i].w)), __fmul2_rn(s, make_float2(v[4 * i + 2], v[4 * i + 3])));
+    v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = b.x, v[4 * i + 3] = b.y;
   }
 }
 
 // x of the next step.
 template <int CHUNKS>
-__device__ __forceinline__ void end_next(const Matrix& t, const Part& p, Ahead<CHUNKS>& ah, Ahead<CHUNKS>& al, int slab, float ca) {
-  const float factor = ca + (p.row < p.m ? t.dg[t.lda + p.row] : 0.f);
-  const int64_t pitch = static_cast<int64_t>(t.ldx) * 2;
+__device__ __forceinline__ void end_next(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, int slab, float factor) {
   __half* const next = t.hi + (slab ^ 1) * (static_cast<int64_t>(p.m) * t.ldx) + static_cast<int64_t>(p.row0()) * t.ldx + p.col;
-  __half* const lo = t.lo + static_cast<int64_t>(p.row0()) * t.ldx + p.col;
+  uint4* const xb = reinterpret_cast<uint4*>(t.xb + block_at(p.row0(), p.col, p.n)) + p.ex.lane;
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k) {
-    const int c = 32 * k;
-    if (p.col + c >= p.n) break;
+    if (p.col + 32 * k >= p.n) break;
     float v[32];
-    applied(p, c, ah.w[k], al.w[k], factor, v);
-    uint4 h[4], l[4];
+    applied(p, 32 * k, x.w[k], factor, v);
+    if (p.row0() < p.m) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t hw[4], lw[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float a = v[8 * i + 2 * q], b = v[8 * i + 2 * q + 1];
-        hw[q] = pack(a, b);
-        const float2 r = unpack(hw[q]);
-        lw[q] = pack((a - r.x) * kLoScale, (b - r.y) * kLoScale);
-      }
-      h[i] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      l[i] = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      for (int i = 0; i < 8; ++i)
+        xb[k * 256 + 32 * i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                                          __float_as_uint(v[4 * i + 3]));
     }
-    const int left = (t.ldx - p.col - c) * 2;
+    uint4 h[4];
+    pack32(v, h);
     p.ex.to_memory(h);
-    p.ex.put(next + c, pitch, p.m - p.row0(), left, h);
-    p.ex.to_memory(l);
-    p.ex.put(lo + c, pitch, p.m - p.row0(), left, l);
+    p.ex.put(next + 32 * k, static_cast<int64_t>(t.ldx) * 2, p.m - p.row0(), (t.ldx - p.col - 32 * k) * 2, h);
   }
 }
 
 // The last step: the update of p, or the result.
 template <int CHUNKS>
-__device__ __forceinline__ void end_last(const Matrix& t, const Part& p, Ahead<CHUNKS>& ah, Ahead<CHUNKS>& al, float ca, int out, float keep,
-                                         const int32_t* status) {
-  if (out == kUpdate && (p.bad || *reinterpret_cast<const volatile int32_t*>(status) != 0)) return;   // p stays as it is
-  const float factor = ca + (p.row < p.m ? t.dg[t.lda + p.row] : 0.f);
+__device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, float factor, int out, float keep) {
   const bool turned = t.flags & kTurned;
   const bool wide = p.n % (out == kBf16Out ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(t.p) % 16 == 0;
   const float rate = t.rate * 0x1p-15f;
   const int rows = p.m - p.row0();
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k) {
-    const int c = 32 * k;
-    if (p.col + c >= p.n) break;
+    const int c = 32 * k, j0 = p.col + c;
+    if (j0 >= p.n) break;
     float v[32];
-    applied(p, c, ah.w[k], al.w[k], factor, v);
-    const int j0 = p.col + c;
+    applied(p, c, x.w[k], factor, v);
     if (turned) {
       // down a column of the parameter: the warp's lanes lie side by side there
       if (p.row >= p.m) continue;
@@ -469,13 +458,13 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, Ahead<C
       uint4 w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t k[4];
+        uint32_t two[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const __nv_bfloat162 two = __floats2bfloat162_rn(v[8 * i + 2 * q] * 0x1p-15f, v[8 * i + 2 * q + 1] * 0x1p-15f);
-          k[q] = *reinterpret_cast<const uint32_t*>(&two);
+          const __nv_bfloat162 r = __floats2bfloat162_rn(v[8 * i + 2 * q] * 0x1p-15f, v[8 * i + 2 * q + 1] * 0x1p-15f);
+          two[q] = *reinterpret_cast<const uint32_t*>(&r);
         }
-        w[i] = make_uint4(k[0], k[1], k[2], k[3]);
+        w[i] = make_uint4(two[0], two[1], two[2], two[3]);
       }
       p.ex.to_memory(w);
       __nv_bfloat16* const q = reinterpret_cast<__nv_bfloat16*>(t.p) + static_cast<int64_t>(p.row0()) * p.n + j0;
@@ -485,11 +474,11 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, Ahead<C
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (p.ex.row(i) >= rows) continue;
-          const __nv_bfloat16* const k = reinterpret_cast<const __nv_bfloat16*>(&w[i]);
+          const __nv_bfloat16* const one = reinterpret_cast<const __nv_bfloat16*>(&w[i]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int j = p.ex.place() / 2 + e;
-            if (j0 + j < p.n) q[static_cast<int64_t>(p.ex.row(i)) * p.n + j] = k[e];
+            if (j0 + j < p.n) q[static_cast<int64_t>(p.ex.row(i)) * p.n + j] = one[e];
           }
         }
       }
@@ -537,14 +526,14 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, Ahead<C
 enum Phase : int { kGram, kPoly, kApply };
 
 // Tile number i of a phase; `at` is the matrix that the number before fell in.
-template <int CG, int BN, int COUNT>
-__device__ __forceinline__ bool find_tile(const IterateArgs<COUNT>& a, int phase, int i, int* at, meo::tc::Tile* t) {
+template <int CG, int BN>
+__device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int tiles, int phase, int i, int* at, meo::tc::Tile* t) {
   const bool sym = phase != kApply;
-  if (i >= (sym ? a.sym_tiles : a.app_tiles)) return false;
+  if (i >= tiles) return false;
   int k = *at;
-  while (k + 1 < a.count && i >= (sym ? a.mat[k + 1].sym0 : a.mat[k + 1].app0)) ++k;
+  while (k + 1 < count && i >= (sym ? mat[k + 1].sym0 : mat[k + 1].app0)) ++k;
   *at = k;
-  const Matrix& m = a.mat[k];
+  const Matrix& m = mat[k];
   meo::tc::Shape s{};
   s.batch = 1;
   s.splits = 1;
@@ -564,7 +553,10 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024 - (shared_at(raw) & 1023)) & 1023);
   unsigned char* const exchange = ring + STAGES * S::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(exchange + kEndWarps * kExchange);
+  float* const columns = reinterpret_cast<float*>(exchange + kEndWarps * kExchange);   // of each warp: BN / 2 values
+  Matrix* const mat = reinterpret_cast<Matrix*>(columns + kEndWarps * (BN / 2));
+  float* const coef = reinterpret_cast<float*>(mat + COUNT);
+  uint64_t* full = reinterpret_cast<uint64_t*>(coef + 3 * MUON_MAX_STEPS);
   uint64_t* empty = full + STAGES;
   uint64_t* sum_full = empty + STAGES;
   uint64_t* sum_empty = sum_full + 2;
@@ -574,6 +566,11 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int count = a.count, steps = a.steps, sym_tiles = a.sym_tiles, app_tiles = a.app_tiles, out = a.out;
+  const float keep = a.keep;
+  for (int i = threadIdx.x; i < count * static_cast<int>(sizeof(Matrix) / 4); i += kThreads)
+    reinterpret_cast<uint32_t*>(mat)[i] = reinterpret_cast<const uint32_t*>(a.mat)[i];
+  for (int i = threadIdx.x; i < 3 * steps; i += kThreads) coef[i] = a.coef[i / 3][i % 3];
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       bar_init(full + i, 1);
@@ -610,7 +607,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     return true;
   };
 
-  const int phases = 3 * a.steps;
+  const int phases = 3 * steps;
   // After a phase: the grid's CTAs wait for one another.
   auto block_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   auto next_phase = [&](int ph) {
@@ -638,15 +635,15 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     uint32_t phase_bit = 0, acc_bit = 0;
     bool ok = true;
     for (int ph = 0; ph < phases; ++ph) {
-      const int kind = ph % 3, slab = ph / 3 & 1;
+      const int kind = ph % 3, slab = ph / 3 & 1, tiles = kind == kApply ? app_tiles : sym_tiles;
       int at = 0;
       Tile t;
       if (warp == 0 && lane == 0) {
         // ---- copies
-        for (int i = first; ok && find_tile<CG, BN>(a, kind, i, &at, &t); i += step) {
-          const Matrix& m = a.mat[at];
-          const CUtensorMap* const map_a = kind == kGram ? &m.x : &m.s;
-          const CUtensorMap* const map_b = kind == kPoly ? &m.s : &m.x;
+        for (int i = first; ok && find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &t); i += step) {
+          const Matrix& m = mat[at];
+          const CUtensorMap* const map_a = kind == kGram ? &a.map[at].x : &a.map[at].s;
+          const CUtensorMap* const map_b = kind == kPoly ? &a.map[at].s : &a.map[at].x;
           const int za = kind == kGram ? slab : kind == kPoly ? 0 : 1, zb = kind == kPoly ? 0 : slab;
           const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
           const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
@@ -658,15 +655,14 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
             if constexpr (CG == 2) bar = at_rank(bar, 0);
             const int k = kb * kBlockK;
             if (a.stall == 0) {
+              // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
+              const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
 #pragma unroll
-              for (int j = 0; j < kTileM / 64; ++j) tma_load<CG>(pa + j * 8192, map_a, k, am + j * 64, za, bar);
+              for (int j = 0; j < kTileM / 64; ++j)
+                tma_load<CG>(pa + j * 8192, map_a, ta ? am + j * 64 : k, ta ? k : am + j * 64, za, bar);
 #pragma unroll
-              for (int j = 0; j < kBCta / 64; ++j) {
-                if (kind == kApply)
-                  tma_load<CG>(pb + j * 8192, map_b, bn + j * 64, k, zb, bar);
-                else
-                  tma_load<CG>(pb + j * 8192, map_b, k, bn + j * 64, zb, bar);
-              }
+              for (int j = 0; j < kBCta / 64; ++j)
+                tma_load<CG>(pb + j * 8192, map_b, tb ? bn + j * 64 : k, tb ? k : bn + j * 64, zb, bar);
             }
             if (++stage == STAGES) stage = 0, phase_bit ^= 1;
           }
@@ -679,10 +675,9 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       }
       if (warp == 1 && lane == 0 && rank == 0) {
         // ---- products
-        const uint32_t idesc = (1u << 4) | ((kind == kApply ? 1u : 0u) << 16) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
-        const uint32_t b_step = kind == kApply ? 16 * 128 : 32, b_lbo = kind == kApply ? 8192 : 16;
-        for (int i = first; ok && find_tile<CG, BN>(a, kind, i, &at, &t); i += step) {
-          const Matrix& m = a.mat[at];
+        constexpr uint32_t idesc = (1u << 4) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
+        for (int i = first; ok && find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &t); i += step) {
+          const Matrix& m = mat[at];
           const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
           if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
           fence_after();
@@ -690,9 +685,13 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
             if (!(ok = wait(full + stage, phase_bit))) break;
             fence_after();
             const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
+            const int k = kb * kBlockK;
+            const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
+            const uint32_t a_step = ta ? 16 * 128 : 32, b_step = tb ? 16 * 128 : 32, a_lbo = ta ? 8192 : 16, b_lbo = tb ? 8192 : 16;
+            const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
 #pragma unroll
             for (int j = 0; j < kBlockK / 16; ++j)
-              mma<CG>(tmem + acc * BN, operand(pa + j * 32, 16, 1024), operand(pb + j * b_step, b_lbo, 1024), idesc, kb > 0 || j > 0);
+              mma<CG>(tmem + acc * BN, operand(pa + j * a_step, a_lbo, 1024), operand(pb + j * b_step, b_lbo, 1024), form, kb > 0 || j > 0);
             commit<CG>(empty + stage);
             if (++stage == STAGES) stage = 0, phase_bit ^= 1;
           }
@@ -714,11 +713,13 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     p.zero = p.bad = false;
     p.cols = BN / 2;
     p.ex = {exchange + (warp - 4) * kExchange, lane};
+    float* const dj = columns + (warp - 4) * (BN / 2);
     for (int ph = 0; ph < phases; ++ph) {
-      const int kind = ph % 3, k_step = ph / 3, slab = k_step & 1;
+      const int kind = ph % 3, k_step = ph / 3, slab = k_step & 1, tiles = kind == kApply ? app_tiles : sym_tiles;
+      const float ca = coef[3 * k_step], cb = coef[3 * k_step + 1], cc = coef[3 * k_step + 2];
       int at = 0;
-      for (int i = first; find_tile<CG, BN>(a, kind, i, &at, &p.tile); i += step) {
-        const Matrix& m = a.mat[at];
+      for (int i = first; find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &p.tile); i += step) {
+        const Matrix& m = mat[at];
         p.m = m.m;
         p.n = m.n;
         p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
@@ -733,19 +734,26 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           arrived();
           end_gram(m, p);
         } else if (kind == kPoly) {
-          Ahead<BN / 64> f;
-          f.fetch(p, m.fe, m.lda);
+          Ahead<4, BN / 64> f;
+          f.fetch(p, m.fb + block_at(p.row0(), p.col, p.m), p.row0() < p.m, p.m - p.col);
+          const float di = p.row < p.m ? m.dg[p.row] : 0.f;
+          // (beyond the last column F F and F are 0: D only has to be finite there)
+#pragma unroll
+          for (int c = 0; c < BN / 64; ++c) dj[32 * c + lane] = p.col + 32 * c + lane < p.m ? m.dg[p.col + 32 * c + lane] : 0.f;
+          __syncwarp();
           arrived();
-          end_poly(m, p, f, a.coef[k_step][1], a.coef[k_step][2]);
+          end_poly(m, p, f, di, dj, cb, cc);
+          __syncwarp();
         } else {
-          Ahead<BN / 64> h, l;
-          h.fetch(p, m.hi + slab * (static_cast<int64_t>(m.m) * m.ldx), m.ldx);
-          l.fetch(p, m.lo, m.ldx);
+          Ahead<8, BN / 64> x;
+          x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
+          const float factor = ca + (p.row < p.m ? m.dg[m.lda + p.row] : 0.f);
+          const int32_t status = *reinterpret_cast<const volatile int32_t*>(a.status);
           arrived();
-          if (k_step + 1 < a.steps)
-            end_next(m, p, h, l, slab, a.coef[k_step][0]);
-          else
-            end_last(m, p, h, l, a.coef[k_step][0], a.out, a.keep, a.status);
+          if (k_step + 1 < steps)
+            end_next(m, p, x, slab, factor);
+          else if (out != kUpdate || (!p.bad && status == 0))   // (otherwise p stays as it is)
+            end_last(m, p, x, factor, out, keep);
         }
         fence_before();
         __syncwarp();
@@ -840,7 +848,7 @@ adaf_status check_size(int64_t batch, int64_t rows, int64_t cols, const std::str
 
 // Bytes of a matrix in the workspace, and where its parts are.
 struct Layout {
-  size_t hi, lo, fe, dg, bytes;
+  size_t hi, xb, fe, fb, dg, bytes;
 };
 Layout layout(int64_t m, int64_t n) {
   const int64_t ldx = round_up(n, 8), lda = round_up(m, 8);
@@ -851,8 +859,9 @@ Layout layout(int64_t m, int64_t n) {
     return at;
   };
   L.hi = take(2 * m * ldx * 2);
-  L.lo = take(m * ldx * 2);
+  L.xb = take(round_up(m, 32) * round_up(n, 32) * 4);
   L.fe = take(2 * m * lda * 2);
+  L.fb = take(round_up(m, 32) * round_up(m, 32) * 2);
   L.dg = take(2 * lda * 4);
   return L;
 }
@@ -928,7 +937,8 @@ template <int CG, int BN, int STAGES, int COUNT>
 adaf_status iterate(const Call& c, const Listed* mats, int count) {
   using namespace meo::tc;
   auto* const kernel = k_muon_iterate<CG, BN, STAGES, COUNT>;
-  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes;
+  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + 3 * MUON_MAX_STEPS * 4;
+  static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   IterateArgs<COUNT> a;
   std::memset(&a, 0, sizeof a);
   a.count = count;
@@ -946,8 +956,9 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
     const Layout L = layout(z.m, z.n);
     Matrix& m = a.mat[i];
     m.hi = reinterpret_cast<__half*>(at + L.hi);
-    m.lo = reinterpret_cast<__half*>(at + L.lo);
+    m.xb = reinterpret_cast<float*>(at + L.xb);
     m.fe = reinterpret_cast<__half*>(at + L.fe);
+    m.fb = reinterpret_cast<__half*>(at + L.fb);
     m.dg = reinterpret_cast<float*>(at + L.dg);
     at += L.bytes;
     m.p = z.p;
@@ -961,8 +972,8 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
       const bool original = c.hp->adjust_lr == MUON_ADJUST_ORIGINAL;
       m.rate = static_cast<float>(c.hp->lr * (original ? std::sqrt(std::max(1.0, h / w)) : 0.2 * std::sqrt(std::max(h, w))));
     }
-    if (!make_map(&m.x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
-        !make_map(&m.s, m.fe, false, z.m, z.m, m.lda, 2, z.m * m.lda, 64))
+    if (!make_map(&a.map[i].x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
+        !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, 2, z.m * m.lda, 64))
       return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const int64_t mt = (z.m + BN - 1) / BN, nt = (z.n + BN - 1) / BN;
     m.sym0 = a.sym_tiles;
@@ -1027,7 +1038,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
     t.u = z.u;
     t.mom = z.mom;
     t.hi = reinterpret_cast<__half*>(at + L.hi);
-    t.lo = reinterpret_cast<__half*>(at + L.lo);
+    t.x = reinterpret_cast<float*>(at + L.xb);
     at += L.bytes;
     t.rows = static_cast<int32_t>(z.rows);
     t.cols = static_cast<int32_t>(z.cols);
