@@ -81,7 +81,7 @@ struct MuonArgs {
   float mu, nesterov_mu, eps;      // u = g + nesterov_mu m, or m itself (nesterov_mu < 0)
   float* part;                     // [parts of all matrices]
   int32_t* status;
-  unsigned* barrier;
+  unsigned* done;
   int32_t clear;                   // this launch clears the status word
   Item item[kMaxGroup];
 };
@@ -132,9 +132,9 @@ __device__ __forceinline__ int owner(int count, int at, First&& first) {
 template <bool STEP>
 __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ MuonArgs a) {
   __shared__ float scratch[8];
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (a.clear != 0) *a.status = 0;
-    *a.barrier = 0;
+  if (blockIdx.x == 0) {
+    if (a.clear != 0 && threadIdx.x == 0) *a.status = 0;
+    if (threadIdx.x < kMaxGroup) a.done[threadIdx.x] = 0;
   }
   const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].part0; })];
   const bool bf16 = t.flags & kBf16;
@@ -293,7 +293,7 @@ struct IterateArgs {
   float keep;
   int32_t stall;
   int32_t* status;
-  unsigned* barrier;     // arrivals of the grid's CTAs
+  unsigned* done;        // of each matrix, tiles that are done
 };
 
 using meo::tc::Part;
@@ -518,27 +518,44 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const A
 // ---- the iteration ------------------------------------------------------------------------
 // All steps for all matrices of a group, in one launch: a step is three phases
 // (x x^T, the polynomial, its product with x), each over the tiles of all
-// matrices, and between phases the grid's CTAs wait for one another (they are
-// launched together: a cooperative launch).  Fifteen launches in a row took 11 us
-// each on a matrix of 256 x 512, of which the copies and products are one or two,
-// and every matrix shape had its own.  The roles of the warps and the ring are
-// k_product's; they go on from phase to phase.
+// matrices.  All tiles of all phases are one list, which the grid's CTAs take in
+// turn; a tile waits until the phase before is done with its matrix, which a
+// counter tells (its CTAs are there: a cooperative launch; and their tiles come
+// before in the list, so they wait for nothing that waits for them).  So the last
+// tiles of one matrix's phase run beside the first of another's, and the tiles of
+// a phase need not be a multiple of the CTAs.  Fifteen launches in a row took 11 us
+// each on a matrix of 256 x 512, of which the copies and products are one or two.
+// The roles of the warps and the ring are k_product's; they go on from tile to tile.
 enum Phase : int { kGram, kPoly, kApply };
 
-// Tile number i of a phase; `at` is the matrix that the number before fell in.
+// The list of tiles: number i is of phase `kind` of step k.
+struct Place {
+  int kind, step, at;    // at: the matrix
+  int need;              // tiles of the matrix that have to be done
+};
+
+// Tile number i, going up from call to call; false beyond the last.
 template <int CG, int BN>
-__device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int tiles, int phase, int i, int* at, meo::tc::Tile* t) {
-  const bool sym = phase != kApply;
-  if (i >= tiles) return false;
-  int k = *at;
-  while (k + 1 < count && i >= (sym ? mat[k + 1].sym0 : mat[k + 1].app0)) ++k;
-  *at = k;
-  const Matrix& m = mat[k];
+__device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int steps, int sym_tiles, int app_tiles, int i, Place* w,
+                                          meo::tc::Tile* t) {
+  const int a_step = 2 * sym_tiles + app_tiles, k = i / a_step;
+  if (k >= steps) return false;
+  i -= k * a_step;
+  const int kind = i < sym_tiles ? kGram : i < 2 * sym_tiles ? kPoly : kApply;
+  i -= kind * sym_tiles;
+  if (kind != w->kind || k != w->step) w->at = 0;
+  w->kind = kind;
+  w->step = k;
+  const bool sym = kind != kApply;
+  while (w->at + 1 < count && i >= (sym ? mat[w->at + 1].sym0 : mat[w->at + 1].app0)) ++w->at;
+  const Matrix& m = mat[w->at];
   meo::tc::Shape s{};
   s.batch = 1;
   s.splits = 1;
   s.group = 8;
   const int mt = (m.m + meo::tc::kTileM * CG - 1) / (meo::tc::kTileM * CG), nt = (m.n + BN - 1) / BN;
+  const int syms = mt * (mt + 1) / 2;
+  w->need = k * (2 * syms + mt * nt) + kind * syms;
   if (sym) return meo::tc::tile_of<true>(i - m.sym0, mt, mt, s, meo::tc::kTileM * CG, BN, t);
   return meo::tc::tile_of<false>(i - m.app0, mt, nt, s, meo::tc::kTileM * CG, BN, t);
 }
@@ -607,100 +624,99 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     return true;
   };
 
-  const int phases = 3 * steps;
-  // After a phase: the grid's CTAs wait for one another.
-  auto block_barrier = [] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-  auto next_phase = [&](int ph) {
-    __syncwarp();
-    block_barrier();
-    if (ph + 1 == phases) return;
-    if (threadIdx.x == 0) {
-      const unsigned all = static_cast<unsigned>(ph + 1) * gridDim.x;
-      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.barrier) : "memory");
-      const long long from = clock64();
+  // Waits until `need` tiles of matrix `at` are done (each of a tile's warps counts).
+  auto wait_done = [&](int at, int need) -> bool {
+    const unsigned* const counter = a.done + at;
+    const unsigned all = static_cast<unsigned>(need) * (CG * kEndWarps);
+    const long long from = clock64();
+    for (;;) {
       unsigned seen;
-      for (;;) {
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(a.barrier) : "memory");
-        if (seen >= all || *off != 0) break;
-        if (clock64() - from > 4 * kWaitCycles) gave_up();
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(counter) : "memory");
+      if (seen >= all) return true;
+      if (*off != 0) return false;
+      if (clock64() - from > 4 * kWaitCycles) {
+        gave_up();
+        return false;
       }
-      asm volatile("fence.proxy.async;" ::: "memory");
     }
-    __syncwarp();
-    block_barrier();
   };
+  auto next_tile = [&](int i, Place* w, Tile* t) { return find_tile<CG, BN>(mat, count, steps, sym_tiles, app_tiles, i, w, t); };
   if (warp < 4) {
     fewer_registers();
     int stage = 0, acc = 0;
     uint32_t phase_bit = 0, acc_bit = 0;
     bool ok = true;
-    for (int ph = 0; ph < phases; ++ph) {
-      const int kind = ph % 3, slab = ph / 3 & 1, tiles = kind == kApply ? app_tiles : sym_tiles;
-      int at = 0;
-      Tile t;
-      if (warp == 0 && lane == 0) {
-        // ---- copies
-        for (int i = first; ok && find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &t); i += step) {
-          const Matrix& m = mat[at];
-          const CUtensorMap* const map_a = kind == kGram ? &a.map[at].x : &a.map[at].s;
-          const CUtensorMap* const map_b = kind == kPoly ? &a.map[at].s : &a.map[at].x;
-          const int za = kind == kGram ? slab : kind == kPoly ? 0 : 1, zb = kind == kPoly ? 0 : slab;
-          const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
-          const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
-          for (int kb = 0; kb < blocks; ++kb) {
-            if (!(ok = wait(empty + stage, phase_bit ^ 1))) break;
-            const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
-            uint32_t bar = shared_at(full + stage);
-            if (rank == 0) bar_expect(full + stage, S::kStage * CG);
-            if constexpr (CG == 2) bar = at_rank(bar, 0);
-            const int k = kb * kBlockK;
-            if (a.stall == 0) {
-              // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
-              const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
-#pragma unroll
-              for (int j = 0; j < kTileM / 64; ++j)
-                tma_load<CG>(pa + j * 8192, map_a, ta ? am + j * 64 : k, ta ? k : am + j * 64, za, bar);
-#pragma unroll
-              for (int j = 0; j < kBCta / 64; ++j)
-                tma_load<CG>(pb + j * 8192, map_b, tb ? bn + j * 64 : k, tb ? k : bn + j * 64, zb, bar);
-            }
-            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
-          }
+    Place w{-1, 0, 0, 0};
+    Tile t;
+    if (warp == 0 && lane == 0) {
+      // ---- copies
+      int known_at = -1, known = 0;
+      for (int i = first; ok && next_tile(i, &w, &t); i += step) {
+        if (w.at != known_at || w.need > known) {
+          if (!(ok = wait_done(w.at, w.need))) break;
+          known_at = w.at;
+          known = w.need;
+          asm volatile("fence.proxy.async;" ::: "memory");
         }
-        if (ph + 1 == phases)
-          for (int i = 0; ok && i < STAGES; ++i) {   // the products' last arrivals have to find the barriers there
-            ok = wait(empty + stage, phase_bit ^ 1);
-            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
-          }
-      }
-      if (warp == 1 && lane == 0 && rank == 0) {
-        // ---- products
-        constexpr uint32_t idesc = (1u << 4) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
-        for (int i = first; ok && find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &t); i += step) {
-          const Matrix& m = mat[at];
-          const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
-          if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
-          fence_after();
-          for (int kb = 0; kb < blocks; ++kb) {
-            if (!(ok = wait(full + stage, phase_bit))) break;
-            fence_after();
-            const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
-            const int k = kb * kBlockK;
+        const Matrix& m = mat[w.at];
+        const int kind = w.kind, slab = w.step & 1;
+        const CUtensorMap* const map_a = kind == kGram ? &a.map[w.at].x : &a.map[w.at].s;
+        const CUtensorMap* const map_b = kind == kPoly ? &a.map[w.at].s : &a.map[w.at].x;
+        const int za = kind == kGram ? slab : kind == kPoly ? 0 : 1, zb = kind == kPoly ? 0 : slab;
+        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!(ok = wait(empty + stage, phase_bit ^ 1))) break;
+          const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
+          uint32_t bar = shared_at(full + stage);
+          if (rank == 0) bar_expect(full + stage, S::kStage * CG);
+          if constexpr (CG == 2) bar = at_rank(bar, 0);
+          const int k = kb * kBlockK;
+          if (a.stall == 0) {
+            // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
             const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
-            const uint32_t a_step = ta ? 16 * 128 : 32, b_step = tb ? 16 * 128 : 32, a_lbo = ta ? 8192 : 16, b_lbo = tb ? 8192 : 16;
-            const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
 #pragma unroll
-            for (int j = 0; j < kBlockK / 16; ++j)
-              mma<CG>(tmem + acc * BN, operand(pa + j * a_step, a_lbo, 1024), operand(pb + j * b_step, b_lbo, 1024), form, kb > 0 || j > 0);
-            commit<CG>(empty + stage);
-            if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+            for (int j = 0; j < kTileM / 64; ++j)
+              tma_load<CG>(pa + j * 8192, map_a, ta ? am + j * 64 : k, ta ? k : am + j * 64, za, bar);
+#pragma unroll
+            for (int j = 0; j < kBCta / 64; ++j)
+              tma_load<CG>(pb + j * 8192, map_b, tb ? bn + j * 64 : k, tb ? k : bn + j * 64, zb, bar);
           }
-          if (!ok) break;
-          commit<CG>(sum_full + acc);
-          if (++acc == 2) acc = 0, acc_bit ^= 1;
+          if (++stage == STAGES) stage = 0, phase_bit ^= 1;
         }
       }
-      next_phase(ph);
+      for (int i = 0; ok && i < STAGES; ++i) {   // the products' last arrivals have to find the barriers there
+        ok = wait(empty + stage, phase_bit ^ 1);
+        if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+      }
+    }
+    if (warp == 1 && lane == 0 && rank == 0) {
+      // ---- products
+      constexpr uint32_t idesc = (1u << 4) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
+      for (int i = first; ok && next_tile(i, &w, &t); i += step) {
+        const Matrix& m = mat[w.at];
+        const int kind = w.kind;
+        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
+        fence_after();
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (!(ok = wait(full + stage, phase_bit))) break;
+          fence_after();
+          const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
+          const int k = kb * kBlockK;
+          const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
+          const uint32_t a_step = ta ? 16 * 128 : 32, b_step = tb ? 16 * 128 : 32, a_lbo = ta ? 8192 : 16, b_lbo = tb ? 8192 : 16;
+          const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
+#pragma unroll
+          for (int j = 0; j < kBlockK / 16; ++j)
+            mma<CG>(tmem + acc * BN, operand(pa + j * a_step, a_lbo, 1024), operand(pb + j * b_step, b_lbo, 1024), form, kb > 0 || j > 0);
+          commit<CG>(empty + stage);
+          if (++stage == STAGES) stage = 0, phase_bit ^= 1;
+        }
+        if (!ok) break;
+        commit<CG>(sum_full + acc);
+        if (++acc == 2) acc = 0, acc_bit ^= 1;
+      }
     }
   } else {
     // ---- endings
@@ -714,57 +730,66 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     p.cols = BN / 2;
     p.ex = {exchange + (warp - 4) * kExchange, lane};
     float* const dj = columns + (warp - 4) * (BN / 2);
-    for (int ph = 0; ph < phases; ++ph) {
-      const int kind = ph % 3, k_step = ph / 3, slab = k_step & 1, tiles = kind == kApply ? app_tiles : sym_tiles;
-      const float ca = coef[3 * k_step], cb = coef[3 * k_step + 1], cc = coef[3 * k_step + 2];
-      int at = 0;
-      for (int i = first; find_tile<CG, BN>(mat, count, tiles, kind, i, &at, &p.tile); i += step) {
-        const Matrix& m = mat[at];
-        p.m = m.m;
-        p.n = m.n;
-        p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
-        p.col = p.tile.n0 + group * p.cols;
-        p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
-        auto arrived = [&] {
-          const bool there = wait(sum_full + acc, acc_bit);
-          p.bad = __any_sync(0xffffffffu, !there) || p.bad;
-          fence_after();
-        };
-        if (kind == kGram) {
-          arrived();
-          end_gram(m, p);
-        } else if (kind == kPoly) {
-          Ahead<4, BN / 64> f;
-          f.fetch(p, m.fb + block_at(p.row0(), p.col, p.m), p.row0() < p.m, p.m - p.col);
-          const float di = p.row < p.m ? m.dg[p.row] : 0.f;
-          // (beyond the last column F F and F are 0: D only has to be finite there)
-#pragma unroll
-          for (int c = 0; c < BN / 64; ++c) dj[32 * c + lane] = p.col + 32 * c + lane < p.m ? m.dg[p.col + 32 * c + lane] : 0.f;
-          __syncwarp();
-          arrived();
-          end_poly(m, p, f, di, dj, cb, cc);
-          __syncwarp();
-        } else {
-          Ahead<8, BN / 64> x;
-          x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
-          const float factor = ca + (p.row < p.m ? m.dg[m.lda + p.row] : 0.f);
-          const int32_t status = *reinterpret_cast<const volatile int32_t*>(a.status);
-          arrived();
-          if (k_step + 1 < steps)
-            end_next(m, p, x, slab, factor);
-          else if (out != kUpdate || (!p.bad && status == 0))   // (otherwise p stays as it is)
-            end_last(m, p, x, factor, out, keep);
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
-        if (++acc == 2) acc = 0, acc_bit ^= 1;
+    Place w{-1, 0, 0, 0};
+    int known_at = -1, known = 0;
+    for (int i = first; next_tile(i, &w, &p.tile); i += step) {
+      if (w.at != known_at || w.need > known) {
+        bool done = true;
+        if (lane == 0) done = wait_done(w.at, w.need);
+        p.bad = __any_sync(0xffffffffu, !done) || p.bad;
+        known_at = w.at;
+        known = w.need;
       }
-      // what was written here is read by other CTAs' bulk copies after the barrier
+      const Matrix& m = mat[w.at];
+      const int slab = w.step & 1;
+      const float ca = coef[3 * w.step], cb = coef[3 * w.step + 1], cc = coef[3 * w.step + 2];
+      p.m = m.m;
+      p.n = m.n;
+      p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
+      p.col = p.tile.n0 + group * p.cols;
+      p.tmem = tmem + (lanes << 16) + acc * BN + group * p.cols;
+      auto arrived = [&] {
+        const bool there = wait(sum_full + acc, acc_bit);
+        p.bad = __any_sync(0xffffffffu, !there) || p.bad;
+        fence_after();
+      };
+      if (w.kind == kGram) {
+        arrived();
+        end_gram(m, p);
+      } else if (w.kind == kPoly) {
+        Ahead<4, BN / 64> f;
+        f.fetch(p, m.fb + block_at(p.row0(), p.col, p.m), p.row0() < p.m, p.m - p.col);
+        const float di = p.row < p.m ? m.dg[p.row] : 0.f;
+        // (beyond the last column F F and F are 0: D only has to be finite there)
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) dj[32 * c + lane] = p.col + 32 * c + lane < p.m ? m.dg[p.col + 32 * c + lane] : 0.f;
+        __syncwarp();
+        arrived();
+        end_poly(m, p, f, di, dj, cb, cc);
+      } else {
+        Ahead<8, BN / 64> x;
+        x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
+        const float factor = ca + (p.row < p.m ? m.dg[m.lda + p.row] : 0.f);
+        const int32_t status = *reinterpret_cast<const volatile int32_t*>(a.status);
+        arrived();
+        if (w.step + 1 < steps)
+          end_next(m, p, x, slab, factor);
+        else if (out != kUpdate || (!p.bad && status == 0))   // (otherwise p stays as it is)
+          end_last(m, p, x, factor, out, keep);
+      }
+      fence_before();
+      // what was written here is read by other CTAs' bulk copies
       asm volatile("fence.proxy.async;" ::: "memory");
-      next_phase(ph);
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.done + w.at) : "memory");
+      }
+      if (++acc == 2) acc = 0, acc_bit ^= 1;
     }
   }
+  __syncwarp();
+  __syncthreads();
   if (*off != 0 && threadIdx.x == 0) {
     // Copies and products that were under way when a wait ran out: they are done in microseconds.
     const long long from = clock64();
@@ -868,7 +893,8 @@ Layout layout(int64_t m, int64_t n) {
 int32_t parts_of(int64_t m, int64_t n) {
   return static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
 }
-constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4;   // the status word, the barrier, the sums' parts
+constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4;   // the status word, the tiles' counters; the sums' parts
+static_assert(4 + kMaxGroup * 4 <= 256, "status and counters");
 
 // Matrices are worked on in the order of their sizes, the longest sums first; a
 // group ends at so many matrices or values.
@@ -949,7 +975,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
   a.keep = c.hp != nullptr ? static_cast<float>(1.0 - c.hp->lr * c.hp->weight_decay) : 1.f;
   a.stall = t_stall ? 1 : 0;
   a.status = reinterpret_cast<int32_t*>(c.ws);
-  a.barrier = reinterpret_cast<unsigned*>(c.ws) + 1;
+  a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
   unsigned char* at = c.ws + kHead;
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
@@ -993,7 +1019,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {CG, 1, 1};
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  // Clusters that can be there together, which the barrier needs: asked for once a device.
+  // Clusters that can be there together, as the waits between tiles need: asked for once a device.
   static std::atomic<int> together[64];
   int device = 0, sms = 0;
   MUON_TRY(sm_count(&device, &sms), "current device");
@@ -1025,7 +1051,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
     a.nesterov_mu = c.hp->nesterov != 0 ? a.mu : -1.f;
   }
   a.status = reinterpret_cast<int32_t*>(c.ws);
-  a.barrier = reinterpret_cast<unsigned*>(c.ws) + 1;
+  a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
   a.part = reinterpret_cast<float*>(c.ws + 256);
   a.clear = first ? 1 : 0;
   unsigned char* at = c.ws + kHead;
