@@ -212,16 +212,39 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonA
   const void* const u = t.u;
   const float* const mom = t.mom;
   const int r0 = (turned ? bx : by) * 64, c0 = (turned ? by : bx) * 64;   // of u
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int r = r0 + (i >> 6), c = c0 + (i & 63);
-    float v = 0.f;
-    if (r < t.rows && c < t.cols) {
-      const int64_t at = static_cast<int64_t>(r) * (STEP ? t.cols : a.stride_r) + c;
-      v = value_at(u, bf16, at);
-      if (STEP) v = update_of(v, mom[at], a);
-      v *= scale;
+  const int64_t pitch = STEP ? t.cols : a.stride_r;
+  const bool quads = (pitch | t.cols) % 4 == 0 && reinterpret_cast<uintptr_t>(u) % (bf16 ? 8 : 16) == 0 &&
+                     (!STEP || reinterpret_cast<uintptr_t>(mom) % 16 == 0);
+  if (quads) {
+    // 4 values side by side, all of a thread's under way before the first is used
+    float4 v[4], m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + (threadIdx.x >> 4) + 16 * i, c = c0 + (threadIdx.x & 15) * 4;
+      v[i] = m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < t.rows && c < t.cols) {
+        v[i] = four_at(u, bf16, r * pitch + c);
+        if (STEP) m[i] = __ldcs(reinterpret_cast<const float4*>(mom + r * pitch + c));
+      }
     }
-    tile[i >> 6][i & 63] = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float* const to = &tile[(threadIdx.x >> 4) + 16 * i][(threadIdx.x & 15) * 4];
+      if (STEP) v[i] = make_float4(update_of(v[i].x, m[i].x, a), update_of(v[i].y, m[i].y, a), update_of(v[i].z, m[i].z, a), update_of(v[i].w, m[i].w, a));
+      to[0] = v[i].x * scale, to[1] = v[i].y * scale, to[2] = v[i].z * scale, to[3] = v[i].w * scale;
+    }
+  } else {
+    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+      const int r = r0 + (i >> 6), c = c0 + (i & 63);
+      float v = 0.f;
+      if (r < t.rows && c < t.cols) {
+        const int64_t at = r * pitch + c;
+        v = value_at(u, bf16, at);
+        if (STEP) v = update_of(v, mom[at], a);
+        v *= scale;
+      }
+      tile[i >> 6][i & 63] = v;
+    }
   }
   __syncthreads();
   const int x0 = by * 64, y0 = bx * 64;   // of x
@@ -552,7 +575,7 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int step
   meo::tc::Shape s{};
   s.batch = 1;
   s.splits = 1;
-  s.group = 8;
+  s.group = 16;
   const int mt = (m.m + meo::tc::kTileM * CG - 1) / (meo::tc::kTileM * CG), nt = (m.n + BN - 1) / BN;
   const int syms = mt * (mt + 1) / 2;
   w->need = k * (2 * syms + mt * nt) + kind * syms;
