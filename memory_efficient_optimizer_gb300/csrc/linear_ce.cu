@@ -38,6 +38,7 @@
 #include <cmath>
 #include <cstring>
 #include <string>
+#include <type_traits>
 
 #include "adafactor_internal.h"
 #include "linear_ce.h"
@@ -108,6 +109,7 @@ __device__ __forceinline__ int target_of(const CeArgs& a, int t) {
 
 // ---- tokens ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kScanThreads) k_lce_scan(const CeArgs a) {
+  meo::tc::next_may_begin();
   __shared__ int warps[32];
   __shared__ int total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -160,15 +162,57 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&two);
 }
 
+// Which token row i is, and how many count, by looking at all targets: for few tokens in place of
+// k_lce_scan, whose launch takes longer.
+__device__ __forceinline__ int find_token(const CeArgs& a, int i, int* n) {
+  __shared__ int warps[4], found[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int base = 0;
+  for (int t0 = 0; t0 < a.tokens; t0 += 128) {
+    const int t = t0 + static_cast<int>(threadIdx.x), y = t < a.tokens ? target_of(a, t) : kIgnored;
+    const unsigned votes = __ballot_sync(0xffffffffu, y != kIgnored);
+    if (lane == 0) warps[warp] = __popc(votes);
+    __syncthreads();
+    int at = base + __popc(votes & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += warps[w];
+    if (y != kIgnored && at == i) {
+      found[0] = t;
+      found[1] = y;
+    }
+    base += warps[0] + warps[1] + warps[2] + warps[3];
+    __syncthreads();
+  }
+  *n = base;
+  if (i >= base) return 0;
+  if (threadIdx.x == 0) {
+    a.token[i] = found[0];
+    a.target[i] = found[1];
+  }
+  return found[0];
+}
+constexpr int kFewTokens = 512;
+
 // Row i of the gathered hidden states, up to a multiple of 64 rows (zeros beyond the
 // last token), and what an ignored token i is answered.
 __global__ void __launch_bounds__(128) k_lce_gather(const CeArgs a) {
+  meo::tc::next_may_begin();
+  meo::tc::previous_done();
   const int i = blockIdx.x;
-  const int n = *a.count;
+  int n, token = 0;
+  if (a.tokens <= kFewTokens) {
+    token = find_token(a, i, &n);
+    if (i == 0 && threadIdx.x == 0) {
+      *a.count = n;
+      *a.status = 0;
+    }
+  } else {
+    n = *a.count;
+    if (i < n) token = a.token[i];
+  }
   if (i < ((n + 63) & ~63)) {
     __nv_bfloat16* const to = a.hc + static_cast<int64_t>(i) * a.ldh;
     if (i < n) {
-      const int64_t at = place(a.token[i], a.seq, a.hsb, a.hss);
+      const int64_t at = place(token, a.seq, a.hsb, a.hss);
       if (a.h_bf16) {
         const __nv_bfloat16* const from = static_cast<const __nv_bfloat16*>(a.h) + at;
         int d = 0;
@@ -207,6 +251,8 @@ __global__ void __launch_bounds__(128) k_lce_gather(const CeArgs a) {
 // The weight in bf16 with rows of a multiple of 8 values.
 __global__ void __launch_bounds__(256) k_lce_weight(const void* w, int32_t bf16, int64_t stride, int32_t vocab, int32_t dim, int32_t ld,
                                                     __nv_bfloat16* to) {
+  meo::tc::next_may_begin();
+  meo::tc::previous_done();
   for (int v = blockIdx.x; v < vocab; v += gridDim.x) {
     const int64_t at = v * stride;
     for (int k = threadIdx.x; k < ld; k += 256) {
@@ -298,10 +344,12 @@ __device__ __forceinline__ float power_of_two(float d) {   // 2^d for a whole d 
   return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
 }
 
-constexpr int kRowThreads = 256;
-
+// A row a CTA: of 1024 threads where there are few rows (16 rows of 32000 words 5 us less).
+template <int kRowThreads>
 __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
   __shared__ float s_max[kRowThreads / 32], s_sum[kRowThreads / 32];
+  meo::tc::next_may_begin();
+  meo::tc::previous_done();
   const int r = blockIdx.x;
   const int n = *a.count, live = min(a.rows, n - a.first);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -490,6 +538,8 @@ struct HiddenEnd {
 // A token's hidden gradient from its parts, in their order.
 __global__ void __launch_bounds__(256) k_lce_join(const float* parts, int32_t splits, int32_t rows, int32_t dim, const int32_t* count,
                                                   int32_t first, const HiddenEnd::Args o) {
+  meo::tc::next_may_begin();
+  meo::tc::previous_done();
   const int r = blockIdx.x;
   if (r >= *count - first) return;
   const int64_t at = place(o.token[r], o.seq, o.sb, o.ss);
@@ -555,6 +605,7 @@ struct Sum {
 
 __global__ void __launch_bounds__(1024) k_lce_loss(const CeArgs a) {
   __shared__ Sum warps[32];
+  meo::tc::previous_done();
   const int n = *a.count;
   Sum s;
   for (int i = threadIdx.x; i < n; i += 1024) s.add(a.part[i]);
@@ -745,6 +796,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (workspace == nullptr || !aligned(workspace, 256)) return invalid("workspace is NULL or not 256-byte aligned");
   if (workspace_bytes < P.bytes) return fail(ADAF_ERR_WORKSPACE_TOO_SMALL, "workspace needs " + std::to_string(P.bytes) + " bytes");
 
+  using namespace meo::tc;
   unsigned char* const ws = static_cast<unsigned char*>(workspace);
   cudaStream_t const s = static_cast<cudaStream_t>(stream);
   const bool grad = gh != nullptr || gw != nullptr;
@@ -790,17 +842,22 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   a.logp = logp;
   a.lse = lse;
 
-  LCE_TRY(g_profile.run(kSlotScan, s, [&] { k_lce_scan<<<1, kScanThreads, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_scan");
+  // (the call's first launch begins when the stream's work before it is done; the others early)
+  const bool few = tokens > 0 && tokens <= kFewTokens;
+  if (!few) LCE_TRY(g_profile.run(kSlotScan, s, [&] { k_lce_scan<<<1, kScanThreads, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_scan");
   if (P.room > 0)
-    LCE_TRY(g_profile.run(kSlotGather, s, [&] { k_lce_gather<<<static_cast<unsigned>(P.room), 128, 0, s>>>(a); return cudaGetLastError(); }),
-            "k_lce_gather");
+    LCE_TRY(g_profile.run(kSlotGather, s, [&] {
+      if (!few) return launch_early(k_lce_gather, dim3(static_cast<unsigned>(P.room)), 128, s, a);
+      k_lce_gather<<<static_cast<unsigned>(P.room), 128, 0, s>>>(a);
+      return cudaGetLastError();
+    }), "k_lce_gather");
   const void* wp = w.p;
   if (P.packed && tokens > 0) {
     wp = ws + P.w;
     LCE_TRY(g_profile.run(kSlotWeight, s, [&] {
-      k_lce_weight<<<static_cast<unsigned>(std::min<int64_t>(w.vocab, 152 * 8)), 256, 0, s>>>(
-          w.p, w.dtype == ADAF_BFLOAT16, w.stride_v, a.vocab, a.dim, static_cast<int32_t>(P.ldw), reinterpret_cast<__nv_bfloat16*>(ws + P.w));
-      return cudaGetLastError();
+      return launch_early(k_lce_weight, dim3(static_cast<unsigned>(std::min<int64_t>(w.vocab, 152 * 8))), 256, s, w.p,
+                          static_cast<int32_t>(w.dtype == ADAF_BFLOAT16), w.stride_v, a.vocab, a.dim, static_cast<int32_t>(P.ldw),
+                          reinterpret_cast<__nv_bfloat16*>(ws + P.w));
     }), "k_lce_weight");
   }
   const Factor factor{a.w.p != nullptr ? nullptr : a.count, a.scale * a.inv_t};
@@ -817,7 +874,6 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
     shape.first = a.first;
     shape.status = a.status;
     shape.stall = t_stall ? 1 : 0;
-    using namespace meo::tc;
     CUtensorMap h_k, w_k, e_k, w_n, e_m, h_n;
     bool ok = true;
     if (rows > 0) {
@@ -830,18 +886,19 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       x.k = a.dim;
       x.group = 32;
       x.m_live = a.count;
-      cudaError_t e;
-      if (grad) {
-        const LogitsEnd<true>::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
-        e = g_profile.run(kSlotLogits, s, [&] { return launch_product<2, 256, 6, false, false, true, LogitsEnd<true>>(h_k, w_k, x, end, s); });
-      } else {
-        const LogitsEnd<false>::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
-        e = g_profile.run(kSlotLogits, s, [&] { return launch_product<2, 256, 6, false, false, true, LogitsEnd<false>>(h_k, w_k, x, end, s); });
-      }
+      const auto logits = [&](auto keep) {
+        using End = LogitsEnd<decltype(keep)::value>;
+        const typename End::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
+        return g_profile.run(kSlotLogits, s, [&] {
+          if (rows <= 128) return launch_product<1, 256, 4, false, false, true, End>(h_k, w_k, x, end, s);
+          return launch_product<2, 256, 6, false, false, true, End>(h_k, w_k, x, end, s);
+        });
+      };
+      const cudaError_t e = grad ? logits(std::true_type{}) : logits(std::false_type{});
       LCE_TRY(e, "k_lce_logits");
       LCE_TRY(g_profile.run(kSlotRows, s, [&] {
-        k_lce_rows<<<static_cast<unsigned>(grad ? round_up(rows, 64) : rows), kRowThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        const dim3 grid(static_cast<unsigned>(grad ? round_up(rows, 64) : rows));
+        return rows <= 304 ? launch_early(k_lce_rows<1024>, grid, 1024, s, a) : launch_early(k_lce_rows<256>, grid, 256, s, a);
       }), "k_lce_rows");
     }
     if (gh != nullptr && rows > 0) {
@@ -863,9 +920,9 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
               "k_lce_grad_hidden");
       if (P.splits > 1)
         LCE_TRY(g_profile.run(kSlotJoin, s, [&] {
-          k_lce_join<<<dim3(static_cast<unsigned>(rows), static_cast<unsigned>(std::min<int64_t>((h.dim + 255) / 256, 16))), 256, 0, s>>>(
-              end.parts, P.splits, end.rows, a.dim, a.count, a.first, end);
-          return cudaGetLastError();
+          const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(std::min<int64_t>((h.dim + 255) / 256, 16)));
+          return launch_early(k_lce_join, grid, 256, s, static_cast<const float*>(end.parts), static_cast<int32_t>(P.splits), end.rows, a.dim,
+                              static_cast<const int32_t*>(a.count), a.first, end);
         }), "k_lce_join");
     }
     if (gw != nullptr) {
@@ -889,7 +946,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
               "k_lce_grad_weight");
     }
   }
-  LCE_TRY(g_profile.run(kSlotLoss, s, [&] { k_lce_loss<<<1, 1024, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_loss");
+  LCE_TRY(g_profile.run(kSlotLoss, s, [&] { return launch_early(k_lce_loss, dim3(1), 1024, s, a); }), "k_lce_loss");
   return ADAF_OK;
 }
 

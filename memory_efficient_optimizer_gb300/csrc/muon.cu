@@ -132,6 +132,7 @@ __device__ __forceinline__ int owner(int count, int at, First&& first) {
 template <bool STEP>
 __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ MuonArgs a) {
   __shared__ float scratch[8];
+  meo::tc::next_may_begin();
   if (blockIdx.x == 0) {
     if (a.clear != 0 && threadIdx.x == 0) *a.status = 0;
     if (threadIdx.x < kMaxGroup) a.done[threadIdx.x] = 0;
@@ -200,6 +201,7 @@ template <bool STEP>
 __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[64][65];
   __shared__ float scratch[8];
+  meo::tc::previous_done();
   const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].tile0; })];
   const int rows = t.m, cols = t.n, ldx = t.ldx;
   const int across = (cols + 63) >> 6, at_tile = blockIdx.x - t.tile0;
@@ -577,10 +579,12 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int step
   s.splits = 1;
   s.group = 16;
   const int mt = (m.m + meo::tc::kTileM * CG - 1) / (meo::tc::kTileM * CG), nt = (m.n + BN - 1) / BN;
-  const int syms = mt * (mt + 1) / 2;
+  constexpr int kRows = meo::tc::kTileM * CG;
+  const int mtn = (m.m + BN - 1) / BN;   // column tiles of the symmetric products
+  const int syms = static_cast<int>(meo::tc::sym_tiles<kRows / BN>(mtn));
   w->need = k * (2 * syms + mt * nt) + kind * syms;
-  if (sym) return meo::tc::tile_of<true>(i - m.sym0, mt, mt, s, meo::tc::kTileM * CG, BN, t);
-  return meo::tc::tile_of<false>(i - m.app0, mt, nt, s, meo::tc::kTileM * CG, BN, t);
+  if (sym) return meo::tc::tile_of<true, kRows, BN>(i - m.sym0, mt, mtn, s, t);
+  return meo::tc::tile_of<false, kRows, BN>(i - m.app0, mt, nt, s, t);
 }
 
 template <int CG, int BN, int STAGES, int COUNT>
@@ -589,7 +593,8 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   using S = Shared<CG, BN, STAGES>;
   constexpr uint32_t kCols = 2 * BN;
   constexpr int kBCta = BN / CG;
-  static_assert(kTileM * CG == BN, "square tiles");
+  constexpr int kRows = kTileM * CG;
+  static_assert(kRows == BN || kRows == 2 * BN, "tiles of the symmetric products");
   extern __shared__ unsigned char raw[];
   unsigned char* ring = raw + ((1024 - (shared_at(raw) & 1023)) & 1023);
   unsigned char* const exchange = ring + STAGES * S::kStage;
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           const int k = kb * kBlockK;
           if (a.stall == 0) {
             // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
-            const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
+            const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0 / kRows * kRows);
 #pragma unroll
             for (int j = 0; j < kTileM / 64; ++j)
               tma_load<CG>(pa + j * 8192, map_a, ta ? am + j * 64 : k, ta ? k : am + j * 64, za, bar);
@@ -727,7 +732,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           fence_after();
           const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
           const int k = kb * kBlockK;
-          const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0);
+          const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0 / kRows * kRows);
           const uint32_t a_step = ta ? 16 * 128 : 32, b_step = tb ? 16 * 128 : 32, a_lbo = ta ? 8192 : 16, b_lbo = tb ? 8192 : 16;
           const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
 #pragma unroll
@@ -1024,10 +1029,11 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
     if (!make_map(&a.map[i].x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
         !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, 2, z.m * m.lda, 64))
       return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    const int64_t mt = (z.m + BN - 1) / BN, nt = (z.n + BN - 1) / BN;
+    constexpr int kRows = kTileM * CG;
+    const int64_t mt = (z.m + kRows - 1) / kRows, nt = (z.n + BN - 1) / BN;
     m.sym0 = a.sym_tiles;
     m.app0 = a.app_tiles;
-    a.sym_tiles += static_cast<int32_t>(mt * (mt + 1) / 2);
+    a.sym_tiles += static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
     a.app_tiles += static_cast<int32_t>(mt * nt);
   }
   cudaLaunchConfig_t cfg;
@@ -1079,7 +1085,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
   a.clear = first ? 1 : 0;
   unsigned char* at = c.ws + kHead;
   int32_t parts = 0, tiles = 0;
-  int64_t big = 0;
+  int64_t big = 0, small = 0;   // tiles of 256 x 256 of a symmetric product, of 128 x 128 of the last one
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
     const Layout L = layout(z.m, z.n);
@@ -1102,17 +1108,23 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
     tiles += static_cast<int32_t>(((z.m + 63) / 64) * ((z.n + 63) / 64));
     const int64_t mt = (z.m + 255) / 256;
     big += mt * (mt + 1) / 2;
+    small += ((z.m + 127) / 128) * ((z.n + 127) / 128);
   }
   MUON_TRY(g_profile.run(kSlotMoment, c.s, [&] {
     k_muon_moment<STEP><<<static_cast<unsigned>(parts), 256, 0, c.s>>>(a);
     return cudaGetLastError();
   }), "k_muon_moment");
   MUON_TRY(g_profile.run(kSlotPack, c.s, [&] {
-    k_muon_pack<STEP><<<static_cast<unsigned>(tiles), 256, 0, c.s>>>(a);
-    return cudaGetLastError();
+    return meo::tc::launch_early(k_muon_pack<STEP>, dim3(static_cast<unsigned>(tiles)), 256, c.s, a);
   }), "k_muon_pack");
   if (big >= 64) return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count) : iterate<2, 256, 6, kMaxGroup>(c, mats, count);
-  return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count) : iterate<1, 128, 6, kMaxGroup>(c, mats, count);
+  // Narrow tiles where each of them has an SM: half as much to load and to write out a tile, for
+  // 256 x 512 102 us to 115, six matrices of 256 x 256 to 1024 126 to 140; 1403 x 777, where two
+  // rounds would be needed, 198 to 175.
+  int device = 0, sms = 0;
+  MUON_TRY(meo::tc::sm_count(&device, &sms), "current device");
+  if (2 * small > sms) return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count) : iterate<1, 128, 6, kMaxGroup>(c, mats, count);
+  return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count) : iterate<1, 64, 8, kMaxGroup>(c, mats, count);
 }
 
 template <bool STEP>

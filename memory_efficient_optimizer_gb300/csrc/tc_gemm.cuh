@@ -88,6 +88,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// A kernel launched to begin while the one before it on the stream ends waits here until that
+// one is done and what it wrote is there.
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- tcgen05 ------------------------------------------------------------------------
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -245,7 +250,6 @@ struct Shape {
 
 struct Tile {
   int32_t batch, split, m0, n0;   // the cluster tile's first row and column
-  bool mirror;                    // symmetric results: the tile above the diagonal stands for the one below too
 };
 
 // What an ending is given: a row of the result a thread, and the columns of its group.
@@ -273,32 +277,39 @@ __device__ __forceinline__ int live(const int32_t* p, int32_t first, int32_t mos
   return n < 0 ? 0 : n < most ? n : most;
 }
 
-// The tile of number i; false beyond the last.
-template <bool SYM>
-__device__ __forceinline__ bool tile_of(int64_t i, int mt, int nt, const Shape& s, int tm, int tn, Tile* t) {
-  const int64_t per = SYM ? static_cast<int64_t>(mt) * (mt + 1) / 2 : static_cast<int64_t>(mt) * nt * s.splits;
+// Tiles of a symmetric result on and above its diagonal: TM rows by TN columns, TM / TN = R
+// column tiles a row tile; column tile c has the row tiles 0 .. c / R.
+template <int R>
+__host__ __device__ constexpr int64_t sym_tiles(int64_t columns) {
+  const int64_t q = columns / R, rest = columns % R;
+  return R * (q * (q + 1) / 2) + rest * (q + 1);
+}
+
+// The tile of number i of a matrix's; false beyond the last.
+template <bool SYM, int TM, int TN>
+__device__ __forceinline__ bool tile_of(int64_t i, int mt, int nt, const Shape& s, Tile* t) {
+  constexpr int R = TM / TN;
+  const int64_t per = SYM ? sym_tiles<SYM ? R : 1>(nt) : static_cast<int64_t>(mt) * nt * s.splits;
   if (per == 0 || i >= per * s.batch) return false;
   t->batch = static_cast<int>(i / per);
   int r = static_cast<int>(i - t->batch * per);
   if constexpr (SYM) {
-    // column by column of the upper triangle: column c holds rows 0 .. c
-    int c = static_cast<int>((sqrtf(8.f * static_cast<float>(r) + 1.f) - 1.f) * 0.5f);
-    while (c * (c + 1) / 2 > r) --c;
-    while ((c + 1) * (c + 2) / 2 <= r) ++c;
-    r -= c * (c + 1) / 2;
-    t->m0 = r * tm;
-    t->n0 = c * tn;
+    // groups of R columns: group q has R (q + 1) tiles, R q (q + 1) / 2 before it
+    int q = static_cast<int>((sqrtf(8.f / R * static_cast<float>(r) + 1.f) - 1.f) * 0.5f);
+    while (R * (q * (q + 1) / 2) > r) --q;
+    while (R * ((q + 1) * (q + 2) / 2) <= r) ++q;
+    r -= R * (q * (q + 1) / 2);
+    t->m0 = r % (q + 1) * TM;
+    t->n0 = (R * q + r / (q + 1)) * TN;
     t->split = 0;
-    t->mirror = r != c;
   } else {
     t->split = r / (mt * nt);
     r -= t->split * (mt * nt);
     const int g = r / (s.group * nt);            // group of rows of tiles
     const int left = mt - g * s.group, high = left < s.group ? left : s.group;
     r -= g * s.group * nt;
-    t->n0 = r / high * tn;
-    t->m0 = (g * s.group + r % high) * tm;
-    t->mirror = false;
+    t->n0 = r / high * TN;
+    t->m0 = (g * s.group + r % high) * TM;
   }
   return true;
 }
@@ -339,10 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int64_t first = blockIdx.x / CG, step = gridDim.x / CG;
-  const int m = live(s.m_live, s.first, s.m), k_all = live(s.k_live, s.first, s.k);
-  const int mt = (m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
-  const int blocks = (k_all + kBlockK - 1) / kBlockK, per_split = (blocks + s.splits - 1) / s.splits;
-
+  next_may_begin();
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       bar_init(full + i, 1);
@@ -361,6 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_at;
+  previous_done();
+  const int m = live(s.m_live, s.first, s.m), k_all = live(s.k_live, s.first, s.k);
+  const int mt = (m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
+  const int blocks = (k_all + kBlockK - 1) / kBlockK, per_split = (blocks + s.splits - 1) / s.splits;
 
   // False if the wait ran out, or another of the CTA's had before.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       Tile t;
-      for (int64_t i = first; ok && tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &t); i += step) {
+      for (int64_t i = first; ok && tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
         const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
         const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
         for (int kb = b0; kb < b1; ++kb) {
@@ -406,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < kBCta / 64; ++j) tma_load<CG>(b + j * 64 * kBlockK * 2, &map_b, bn + j * 64, k, t.batch, bar);
             } else {
-              tma_load<CG>(b, &map_b, k, bn, t.batch, bar);
+#pragma unroll
+              for (int j = 0; j < kBCta / 128; ++j) tma_load<CG>(b + j * 128 * kBlockK * 2, &map_b, k, bn + j * 128, t.batch, bar);
             }
           }
           if (++stage == STAGES) stage = 0, phase ^= 1;
@@ -427,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       Tile t;
-      for (int64_t i = first; ok && tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &t); i += step) {
+      for (int64_t i = first; ok && tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
         const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
         if (!(ok = wait(sum_empty + acc, acc_phase ^ 1))) break;
         fence_after();
@@ -468,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.n = s.n;
     p.bad = false;
     p.ex = {exchange + (warp - 4) * kExchange, lane};
-    for (int64_t i = first; tile_of<End::kSym>(i, mt, nt, s, kTileM * CG, BN, &p.tile); i += step) {
+    for (int64_t i = first; tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &p.tile); i += step) {
       const int b0 = p.tile.split * per_split, b1 = min(blocks, b0 + per_split);
       p.zero = b1 <= b0;
       p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;

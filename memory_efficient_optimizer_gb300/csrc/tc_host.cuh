@@ -108,6 +108,23 @@ struct Profile {
   }
 };
 
+// Launches a kernel that may begin while the one before it on the stream ends (it waits for it
+// itself: previous_done).
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Launches a product over a persistent grid: as many CTAs as the device has SMs,
 // or as there are tiles.
 template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
@@ -127,7 +144,7 @@ cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Sha
     ready.fetch_or(bit);
   }
   const int64_t mt = (s.m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
-  const int64_t tiles = (End::kSym ? mt * (mt + 1) / 2 : mt * nt * s.splits) * s.batch;
+  const int64_t tiles = (End::kSym ? sym_tiles<kTileM * CG / BN>(nt) : mt * nt * s.splits) * s.batch;
   const int64_t grid = std::min<int64_t>(tiles, sms / CG) * CG;
   if (grid == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg;
@@ -136,13 +153,13 @@ cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Sha
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   cfg.attrs = at;
-  if (CG > 1) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {CG, 1, 1};
-    cfg.numAttrs = 1;
-  }
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {CG, 1, 1};
+  cfg.numAttrs = CG > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a, b, s, end);
 }
 
