@@ -272,7 +272,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 template <bool KEEP>
 struct LogitsEnd {
-  static constexpr bool kSym = false;
   static constexpr int kChunk = kSumStages;
   struct Args {
     float c_hi, c_lo;
@@ -430,12 +429,6 @@ struct Factor {
   const int32_t* count;      // NULL: nothing
   float scale;
   __device__ __forceinline__ float value() const { return count == nullptr ? 1.f : scale / static_cast<float>(max(1, *count)); }
-  __device__ __forceinline__ void apply(float (&v)[32]) const {
-    if (count == nullptr) return;
-    const float f = value();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= f;
-  }
 };
 
 // Writes the warp's 32 rows of 32 values of a result, fp32 or bf16: row i at out + row(i), of
@@ -504,30 +497,32 @@ __device__ __forceinline__ void store32(const Part& p, void* out, bool bf16, boo
 }
 
 struct HiddenEnd {
-  static constexpr bool kSym = false;
   static constexpr int kChunk = 0;
   struct Args {
     const int32_t* token;     // of the piece
     void* out;
     int64_t sb, ss;
     int32_t seq, bf16, wide;
-    float* parts;             // not NULL: [splits][rows][dim], summed by k_lce_join
-    int32_t rows;
+    float* parts;             // where sums are in several parts: [splits][rows that count][dim]
     Factor factor;
   };
   static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+    const float f = a.factor.value();
+    const bool parts = p.splits > 1;   // then summed by k_lce_join
     int64_t at[4];   // of the rows that this lane writes
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = p.row0() + p.ex.row(i);
-      at[i] = r >= p.m ? 0 : a.parts != nullptr ? (static_cast<int64_t>(p.tile.split) * a.rows + r) * p.n : place(a.token[r], a.seq, a.sb, a.ss);
+      at[i] = r >= p.m ? 0 : parts ? (static_cast<int64_t>(p.tile.split) * p.m + r) * p.n : place(a.token[r], a.seq, a.sb, a.ss);
     }
+#pragma unroll 1
     for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
       float v[32];
       p.load(c, v);
-      a.factor.apply(v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= f;
       const int j = p.col + c;
-      if (a.parts != nullptr)
+      if (parts)
         store32(p, a.parts, false, p.n % 4 == 0, false, [&](int i) { return at[i] + j; }, p.n - j, v);
       else
         store32(p, a.out, a.bf16, a.wide, false, [&](int i) { return at[i] + j; }, p.n - j, v);
@@ -536,25 +531,44 @@ struct HiddenEnd {
 };
 
 // A token's hidden gradient from its parts, in their order.
-__global__ void __launch_bounds__(256) k_lce_join(const float* parts, int32_t splits, int32_t rows, int32_t dim, const int32_t* count,
-                                                  int32_t first, const HiddenEnd::Args o) {
+__global__ void __launch_bounds__(256) k_lce_join(int32_t dim, int32_t blocks, int32_t clusters, int64_t room, const int32_t* count,
+                                                  int32_t first, int32_t most, const HiddenEnd::Args o) {
   meo::tc::next_may_begin();
   meo::tc::previous_done();
-  const int r = blockIdx.x;
-  if (r >= *count - first) return;
-  const int64_t at = place(o.token[r], o.seq, o.sb, o.ss);
-  for (int k = blockIdx.y * 256 + threadIdx.x; k < dim; k += gridDim.y * 256) {
-    float v = 0.f;
-    for (int s = 0; s < splits; ++s) v += parts[(static_cast<int64_t>(s) * rows + r) * dim + k];
-    if (o.bf16)
-      static_cast<__nv_bfloat16*>(o.out)[at + k] = __float2bfloat16_rn(v);
-    else
-      static_cast<float*>(o.out)[at + k] = v;
+  const int rows = meo::tc::live(count, first, most);
+  const int splits = meo::tc::splits_of(rows, dim, blocks, 256, 256, clusters, room);
+  if (splits == 1) return;
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t at = place(o.token[r], o.seq, o.sb, o.ss);
+    const float* const parts = o.parts + static_cast<int64_t>(r) * dim;
+    const int64_t part = static_cast<int64_t>(rows) * dim;
+    if (dim % 4 == 0 && o.wide) {
+      for (int k = 4 * (blockIdx.y * 256 + threadIdx.x); k < dim; k += 4 * gridDim.y * 256) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+          const float4 x = __ldcs(reinterpret_cast<const float4*>(parts + s * part + k));
+          v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+        }
+        if (o.bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.out) + at + k) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(o.out) + at + k) = v;
+      }
+      continue;
+    }
+    for (int k = blockIdx.y * 256 + threadIdx.x; k < dim; k += gridDim.y * 256) {
+      float v = 0.f;
+      for (int s = 0; s < splits; ++s) v += __ldcs(parts + s * part + k);
+      if (o.bf16)
+        static_cast<__nv_bfloat16*>(o.out)[at + k] = __float2bfloat16_rn(v);
+      else
+        static_cast<float*>(o.out)[at + k] = v;
+    }
   }
 }
 
 struct WeightEnd {
-  static constexpr bool kSym = false;
   static constexpr int kChunk = 0;
   struct Args {
     void* out;
@@ -566,10 +580,38 @@ struct WeightEnd {
   };
   static __device__ __forceinline__ void part(const Args& a, const Part& p) {
     if (p.zero && !a.last && (a.sum != nullptr ? a.load_sum : a.load_out)) return;   // nothing to add
+    const float f = a.factor.value();
+    const auto row_at = [&](int i) { return (p.row0() + p.ex.row(i)) * a.stride; };
+    if (a.sum == nullptr && a.bf16 && a.wide && !a.load_out && p.col + p.cols <= p.n) {
+      // the usual case: few tokens leave little time for a tile
+      const int64_t at[4] = {row_at(0), row_at(1), row_at(2), row_at(3)};
+#pragma unroll 1
+      for (int c = 0; c < p.cols; c += 64) {
+        float v[32], w[32];
+        p.load64(c, v, w);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float(&x)[32] = half == 0 ? v : w;
+          uint4 q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            q[i] = make_uint4(pack(x[8 * i] * f, x[8 * i + 1] * f), pack(x[8 * i + 2] * f, x[8 * i + 3] * f),
+                              pack(x[8 * i + 4] * f, x[8 * i + 5] * f), pack(x[8 * i + 6] * f, x[8 * i + 7] * f));
+          p.ex.to_memory(q);
+          __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + p.col + c + 32 * half + p.ex.place() / 2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (p.row0() + p.ex.row(i) < p.m) *reinterpret_cast<uint4*>(to + at[i]) = q[i];
+        }
+      }
+      return;
+    }
+#pragma unroll 1
     for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
       float v[32];
       p.load(c, v);
-      a.factor.apply(v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= f;
       const int j = p.col + c, left = p.n - j;
       if (a.sum != nullptr) {
         const auto sum_at = [&](int i) { return static_cast<int64_t>(p.row0() + p.ex.row(i)) * p.n + j; };
@@ -583,7 +625,7 @@ struct WeightEnd {
             if (i < left) v[i] += a.sum[static_cast<int64_t>(p.row) * p.n + j + i];
         }
       }
-      store32(p, a.out, a.bf16, a.wide, a.load_out, [&](int i) { return (p.row0() + p.ex.row(i)) * a.stride + j; }, left, v);
+      store32(p, a.out, a.bf16, a.wide, a.load_out, [&](int i) { return row_at(i) + j; }, left, v);
     }
   }
 };
@@ -685,7 +727,7 @@ adaf_status check_sizes(const linear_ce_hidden* h, const linear_ce_weight* w, co
 struct Plan {
   int64_t tokens, room, rows, pieces;   // room: rows of the gathered hidden states; rows: of a piece
   int64_t ldh, lde, ldw, spans;
-  int splits;                           // of the hidden gradient's sums
+  int64_t split_room;                   // values of the parts of the hidden gradient's sums
   bool packed;                          // the weight is copied
   size_t token, target, part, hc, xt, stat, e, w, parts, sum, bytes;
 };
@@ -702,8 +744,8 @@ Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_
   P.pieces = (P.tokens + P.rows - 1) / P.rows;
   P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || w.stride_v % 8 != 0;
   P.ldw = P.packed ? P.ldh : w.stride_v;
-  const int64_t tiles = ((P.rows + 255) / 256) * ((h.dim + 255) / 256), blocks = (w.vocab + 63) / 64;
-  P.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({152 / tiles, blocks / 16, 32})));
+  // up to 16 parts, of 256 MB together
+  P.split_room = std::min(P.rows * h.dim * 16, int64_t{1} << 26);
   size_t o = 256;
   auto take = [&](int64_t bytes) {
     const size_t at = o;
@@ -718,7 +760,7 @@ Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_
   P.stat = take(P.rows * P.spans * 8);
   if (grad) P.e = take(P.rows * P.lde * 2);
   if (P.packed) P.w = take(w.vocab * P.ldw * 2);
-  if (gh != nullptr && P.splits > 1) P.parts = take(P.splits * P.rows * h.dim * 4);
+  if (gh != nullptr) P.parts = take(P.split_room * 4);
   if (gw != nullptr && P.pieces > 1 && gw->dtype == ADAF_BFLOAT16) P.sum = take(w.vocab * h.dim * 4);
   P.bytes = o;
   return P;
@@ -908,22 +950,26 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       const int64_t es = size_of(gh->dtype);
       const bool wide = aligned(gh->p, 16) && (h.batch == 1 || gh->stride_b * es % 16 == 0) && (h.seq == 1 || gh->stride_s * es % 16 == 0);
       const HiddenEnd::Args end{a.token + a.first, gh->p, gh->stride_b, gh->stride_s, a.seq, a.g_bf16, wide,
-                                P.splits > 1 ? reinterpret_cast<float*>(ws + P.parts) : nullptr, static_cast<int32_t>(P.rows), factor};
+                                reinterpret_cast<float*>(ws + P.parts), factor};
       Shape x = shape;
       x.m = static_cast<int32_t>(rows);
       x.n = a.dim;
       x.k = a.vocab;
-      x.splits = P.splits;
+      x.splits = 0;
+      x.split_room = P.split_room;
       x.group = 8;
       x.m_live = a.count;
       LCE_TRY(g_profile.run(kSlotGradHidden, s, [&] { return launch_product<2, 256, 6, false, true, true, HiddenEnd>(e_k, w_n, x, end, s); }),
               "k_lce_grad_hidden");
-      if (P.splits > 1)
-        LCE_TRY(g_profile.run(kSlotJoin, s, [&] {
-          const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(std::min<int64_t>((h.dim + 255) / 256, 16)));
-          return launch_early(k_lce_join, grid, 256, s, static_cast<const float*>(end.parts), static_cast<int32_t>(P.splits), end.rows, a.dim,
-                              static_cast<const int32_t*>(a.count), a.first, end);
-        }), "k_lce_join");
+      int device = 0, sms = 0;
+      LCE_TRY(sm_count(&device, &sms), "current device");
+      const dim3 join(static_cast<unsigned>(std::min<int64_t>(rows, 1216)),
+                      static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((h.dim + 1023) / 1024, 1216 / rows))));
+      LCE_TRY(g_profile.run(kSlotJoin, s, [&] {
+        return launch_early(k_lce_join, join, 256, s, a.dim,
+                            static_cast<int32_t>((w.vocab + kBlockK - 1) / kBlockK), static_cast<int32_t>(sms / 2), P.split_room,
+                            static_cast<const int32_t*>(a.count), a.first, static_cast<int32_t>(rows), end);
+      }), "k_lce_join");
     }
     if (gw != nullptr) {
       ok = make_map(&e_m, P.e != 0 ? static_cast<void*>(a.e) : ws, true, e_rows, w.vocab, P.lde, 1, e_rows * P.lde, kBoxMN) &&

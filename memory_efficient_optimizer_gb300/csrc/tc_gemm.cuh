@@ -154,6 +154,26 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 64 columns, both halves under way together.
+__device__ __forceinline__ void tmem_load64(uint32_t at, float (&v)[32], float (&w)[32]) {
+  uint32_t r[32], q[32];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t(&t)[32] = half == 0 ? r : q;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, "
+        "%26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]), "=r"(t[3]), "=r"(t[4]), "=r"(t[5]), "=r"(t[6]), "=r"(t[7]), "=r"(t[8]), "=r"(t[9]),
+          "=r"(t[10]), "=r"(t[11]), "=r"(t[12]), "=r"(t[13]), "=r"(t[14]), "=r"(t[15]), "=r"(t[16]), "=r"(t[17]), "=r"(t[18]),
+          "=r"(t[19]), "=r"(t[20]), "=r"(t[21]), "=r"(t[22]), "=r"(t[23]), "=r"(t[24]), "=r"(t[25]), "=r"(t[26]), "=r"(t[27]),
+          "=r"(t[28]), "=r"(t[29]), "=r"(t[30]), "=r"(t[31])
+        : "r"(at + 32 * half));
+  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]), w[i] = __uint_as_float(q[i]);
+}
 __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
@@ -239,7 +259,8 @@ struct Exchange {
 struct Shape {
   int32_t m, n, k;         // of one matrix of the batch
   int32_t batch;
-  int32_t splits;          // parts of k, each a result of its own
+  int32_t splits;          // parts of k, each a result of its own; 0: as choose_splits has it
+  int64_t split_room;      // then: values that the parts' results may take
   int32_t group;           // tiles are walked in groups of so many rows of tiles
   const int32_t* m_live;   // not NULL: the rows that count (on the device) are *m_live - first, at most m
   const int32_t* k_live;   // the same for k
@@ -260,8 +281,16 @@ struct Part {
   int32_t m, n;
   uint32_t tmem;
   Exchange ex;            // of the warp
+  int32_t splits;
   bool zero, bad;         // there was nothing to sum; a wait ran out
   __device__ __forceinline__ int row0() const { return row - ex.lane; }   // the warp's first row
+  __device__ __forceinline__ void load64(int c, float (&v)[32], float (&w)[32]) const {
+    tmem_load64(tmem + c, v, w);
+    if (zero || bad) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = w[i] = bad ? __int_as_float(0x7fc00000) : 0.f;
+    }
+  }
   __device__ __forceinline__ void load(int c, float (&v)[32]) const {
     tmem_load(tmem + c, v);
     if (zero || bad) {
@@ -270,6 +299,27 @@ struct Part {
     }
   }
 };
+
+// In how many parts to sum, so that the tiles' parts come out near a multiple of the clusters that
+// work on them.  `blocks`: stages of a whole sum; a part more costs a write and a read of the result,
+// `cost` stages' time.  96 tiles on 76 clusters are two rounds; in three parts 1.3.
+__host__ __device__ inline int choose_splits(uint32_t tiles, uint32_t blocks, uint32_t clusters, uint32_t most, uint32_t cost) {
+  uint32_t best = 1, least = 0xffffffffu;
+  for (uint32_t s = 1; s <= 16 && s <= most && (s == 1 || blocks >= 16 * s); ++s) {
+    const uint32_t time = (tiles * s + clusters - 1) / clusters * ((blocks + s - 1) / s) + (s > 1 ? cost * s : 0);
+    if (time < least) least = time, best = s;
+  }
+  return static_cast<int>(best);
+}
+// The same for a result of m x n values, in tiles of tm x tn, with room for so many values.  (A
+// result so large that this overflows 32 bits is summed in one part.)
+__host__ __device__ inline int splits_of(int m, int n, int blocks, int tm, int tn, int clusters, int64_t room) {
+  const int64_t values = static_cast<int64_t>(m) * n;
+  if (values == 0 || 2 * values > room) return 1;
+  const uint32_t tiles = static_cast<uint32_t>((m + tm - 1) / tm) * static_cast<uint32_t>((n + tn - 1) / tn);
+  return choose_splits(tiles, blocks, clusters, static_cast<uint32_t>(room / values < 16 ? room / values : 16),
+                       static_cast<uint32_t>(values >> 18) + 1);
+}
 
 __device__ __forceinline__ int live(const int32_t* p, int32_t first, int32_t most) {
   if (p == nullptr) return most;
@@ -281,6 +331,7 @@ __device__ __forceinline__ int live(const int32_t* p, int32_t first, int32_t mos
 // column tiles a row tile; column tile c has the row tiles 0 .. c / R.
 template <int R>
 __host__ __device__ constexpr int64_t sym_tiles(int64_t columns) {
+  static_assert(R >= 1, "whole column tiles");
   const int64_t q = columns / R, rest = columns % R;
   return R * (q * (q + 1) / 2) + rest * (q + 1);
 }
@@ -324,7 +375,7 @@ struct Shared {
 };
 
 // End: what is done with a result tile.
-//   static constexpr bool kSym; struct Args;
+//   struct Args;
 //   static constexpr int kChunk = 0;   static __device__ void part(const Args&, const Part&)
 // or, with kChunk > 0, static __device__ void whole(const Args&, const Part&, float (&v)[BN / 2]):
 // the sums are taken out of tensor memory every kChunk stages and added up in registers.  The
@@ -332,8 +383,9 @@ struct Shared {
 // 2^-25 of itself for each of its steps of 16 values; parts of 256 values leave next to nothing.
 template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape s,
+    k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape given,
               const typename End::Args end) {
+  Shape s = given;
   using S = Shared<CG, BN, STAGES>;
   constexpr uint32_t kCols = 2 * BN;      // two accumulators
   constexpr int kBCta = BN / CG;          // rows of B (columns of the result) that a CTA loads
@@ -372,7 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   previous_done();
   const int m = live(s.m_live, s.first, s.m), k_all = live(s.k_live, s.first, s.k);
   const int mt = (m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
-  const int blocks = (k_all + kBlockK - 1) / kBlockK, per_split = (blocks + s.splits - 1) / s.splits;
+  const int blocks = (k_all + kBlockK - 1) / kBlockK;
+  if (s.splits == 0) s.splits = splits_of(m, s.n, blocks, kTileM * CG, BN, gridDim.x / CG, s.split_room);
+  const int per_split = (blocks + s.splits - 1) / s.splits;
 
   // False if the wait ran out, or another of the CTA's had before.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -397,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       Tile t;
-      for (int64_t i = first; ok && tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
+      for (int64_t i = first; ok && tile_of<false, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
         const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
         const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
         for (int kb = b0; kb < b1; ++kb) {
@@ -440,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       Tile t;
-      for (int64_t i = first; ok && tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
+      for (int64_t i = first; ok && tile_of<false, kTileM * CG, BN>(i, mt, nt, s, &t); i += step) {
         const int b0 = t.split * per_split, b1 = min(blocks, b0 + per_split);
         if (!(ok = wait(sum_empty + acc, acc_phase ^ 1))) break;
         fence_after();
@@ -479,9 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Part p;
     p.m = m;
     p.n = s.n;
+    p.splits = s.splits;
     p.bad = false;
     p.ex = {exchange + (warp - 4) * kExchange, lane};
-    for (int64_t i = first; tile_of<End::kSym, kTileM * CG, BN>(i, mt, nt, s, &p.tile); i += step) {
+    for (int64_t i = first; tile_of<false, kTileM * CG, BN>(i, mt, nt, s, &p.tile); i += step) {
       const int b0 = p.tile.split * per_split, b1 = min(blocks, b0 + per_split);
       p.zero = b1 <= b0;
       p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;

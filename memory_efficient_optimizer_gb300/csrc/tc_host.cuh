@@ -144,8 +144,8 @@ cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Sha
     ready.fetch_or(bit);
   }
   const int64_t mt = (s.m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
-  const int64_t tiles = (End::kSym ? sym_tiles<kTileM * CG / BN>(nt) : mt * nt * s.splits) * s.batch;
-  const int64_t grid = std::min<int64_t>(tiles, sms / CG) * CG;
+  const int64_t tiles = mt * nt * std::max(1, s.splits) * s.batch;
+  const int64_t grid = std::min<int64_t>(s.splits == 0 && tiles > 0 ? sms / CG : tiles, sms / CG) * CG;
   if (grid == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
