@@ -686,7 +686,7 @@ enum Slot { kSlotScan, kSlotGather, kSlotWeight, kSlotLogits, kSlotRows, kSlotGr
 meo::tc::Profile g_profile;
 thread_local bool t_stall = false;
 
-constexpr int64_t kMaxStride = int64_t{1} << 40;
+constexpr int64_t kMaxStride = int64_t{1} << 38;
 
 // [p, end) of a tensor's bytes.
 struct Extent {
@@ -711,7 +711,8 @@ adaf_status check_sizes(const linear_ce_hidden* h, const linear_ce_weight* w, co
   if (w->vocab < 1) return invalid("weight: vocab must be at least 1");
   if (h->dim > kMaxDim || w->vocab > kMaxVocab) return fail(ADAF_ERR_UNSUPPORTED, "dim above 2^16 or vocab above 2^21");
   if (h->batch > kMaxTokens || h->seq > kMaxTokens || h->batch * h->seq > kMaxTokens) return fail(ADAF_ERR_UNSUPPORTED, "more than 2^26 tokens");
-  if (w->stride_v < 0 || w->stride_v > kMaxStride || (w->vocab > 1 && w->stride_v < h->dim)) return invalid("weight: rows overlap (stride)");
+  if (w->stride_v < 0 || (w->vocab > 1 && w->stride_v < h->dim)) return invalid("weight: rows overlap (stride)");
+  if (w->stride_v > kMaxStride) return invalid("weight: strides must be 0 to 2^38");
   if (gh != nullptr) {
     if (!known(gh->dtype)) return invalid("grad_hidden: unknown dtype");
     if (gh->batch != h->batch || gh->seq != h->seq || gh->dim != h->dim) return invalid("grad_hidden: not the hidden states' size");
@@ -742,8 +743,9 @@ Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_
   P.spans = (w.vocab + kSpan - 1) / kSpan;
   P.rows = std::min(P.room, std::max<int64_t>(256, kPieceBytes / (P.lde * 2) / 256 * 256));
   P.pieces = (P.tokens + P.rows - 1) / P.rows;
-  P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || w.stride_v % 8 != 0;
-  P.ldw = P.packed ? P.ldh : w.stride_v;
+  // (a single row's stride says nothing)
+  P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || (w.vocab > 1 && w.stride_v % 8 != 0);
+  P.ldw = P.packed || w.vocab == 1 ? P.ldh : w.stride_v;
   // up to 16 parts, of 256 MB together
   P.split_room = std::min(P.rows * h.dim * 16, int64_t{1} << 26);
   size_t o = 256;
@@ -797,7 +799,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   const linear_ce_weight& w = *weight;
   const int64_t tokens = h.batch * h.seq;
   auto bad_stride = [](int64_t s) { return s < 0 || s > kMaxStride; };
-  if (bad_stride(h.stride_b) || bad_stride(h.stride_s)) return invalid("hidden: strides must be 0 to 2^40");
+  if (bad_stride(h.stride_b) || bad_stride(h.stride_s)) return invalid("hidden: strides must be 0 to 2^38");
   if (tokens > 0 && h.p == nullptr) return invalid("hidden is NULL");
   if (w.p == nullptr) return invalid("weight is NULL");
   if (!aligned(h.p, size_of(h.dtype))) return invalid("hidden is not element-aligned");
@@ -805,10 +807,10 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (targets->dtype != LOSS_INT32 && targets->dtype != LOSS_INT64) return invalid("targets: unknown dtype");
   if (tokens > 0 && targets->rows.p == nullptr) return invalid("targets is NULL");
   if (!aligned(targets->rows.p, targets->dtype == LOSS_INT64 ? 8 : 4)) return invalid("targets is not element-aligned");
-  if (bad_stride(targets->rows.stride_b) || bad_stride(targets->rows.stride_s)) return invalid("targets: strides must be 0 to 2^40");
+  if (bad_stride(targets->rows.stride_b) || bad_stride(targets->rows.stride_s)) return invalid("targets: strides must be 0 to 2^38");
   if (!aligned(args->weights.p, 4)) return invalid("weights is not element-aligned");
   if (args->weights.p != nullptr && (bad_stride(args->weights.stride_b) || bad_stride(args->weights.stride_s)))
-    return invalid("weights: strides must be 0 to 2^40");
+    return invalid("weights: strides must be 0 to 2^38");
   const double inv_t = 1.0 / args->temperature;
   if (!(args->temperature > 0.0) || !std::isfinite(args->temperature) || !std::isfinite(static_cast<float>(inv_t * 1.5)) ||
       static_cast<float>(inv_t) < FLT_MIN)
@@ -818,7 +820,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (loss == nullptr) return invalid("loss is NULL");
   if (!aligned(loss, 4) || !aligned(logp, 4) || !aligned(lse, 4)) return invalid("loss, logp or lse is not element-aligned");
   if (gh != nullptr && tokens > 0) {
-    if (bad_stride(gh->stride_b) || bad_stride(gh->stride_s)) return invalid("grad_hidden: strides must be 0 to 2^40");
+    if (bad_stride(gh->stride_b) || bad_stride(gh->stride_s)) return invalid("grad_hidden: strides must be 0 to 2^38");
     if (!aligned(gh->p, size_of(gh->dtype))) return invalid("grad_hidden is not element-aligned");
     if ((gh->seq > 1 && gh->stride_s < gh->dim) || (gh->batch > 1 && gh->stride_b < (gh->seq - 1) * gh->stride_s + gh->dim))
       return invalid("grad_hidden: rows overlap");

@@ -44,6 +44,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <string>
 #include <vector>
 
@@ -1143,43 +1144,15 @@ adaf_status run(const Call& c, std::vector<Listed>& mats) {
   return ADAF_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-void muon_default_iteration(muon_iteration* it) {
-  if (it == nullptr) return;
-  std::memset(it, 0, sizeof *it);
-  it->steps = 5;
-  for (int k = 0; k < 5; ++k) {
-    it->coef[k][0] = 3.4445;
-    it->coef[k][1] = -4.7750;
-    it->coef[k][2] = 2.0315;
-  }
-  it->eps = 1e-7;
-}
-
-adaf_status muon_validate(const muon_hparams* hp) { return check_hp(hp); }
-adaf_status muon_validate_iteration(const muon_iteration* it) { return check_iteration(it); }
-
-adaf_status muon_workspace_size(const muon_tensor* tensors, int32_t n, size_t* bytes) {
-  if (bytes == nullptr) return invalid("bytes is NULL");
-  return check_tensors(tensors, n, bytes);
-}
-
-adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t* bytes) {
-  if (bytes == nullptr) return invalid("bytes is NULL");
-  const adaf_status st = check_size(batch, rows, cols, "");
-  if (st != ADAF_OK) return st;
+// Bytes for a stack of matrices.
+size_t bytes_of(int64_t batch, int64_t rows, int64_t cols) {
   Grouping g;
   if (rows > 0 && cols > 0)
     for (int64_t b = 0; b < batch; ++b) g.add({std::max(rows, cols), std::min(rows, cols)});
-  *bytes = g.most;
-  return ADAF_OK;
+  return g.most;
 }
 
-adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes,
-                      void* stream) {
+adaf_status step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes, void* stream) {
   adaf_status st = check_hp(hp);
   if (st != ADAF_OK) return st;
   size_t need = 0;
@@ -1204,13 +1177,14 @@ adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams*
   return run<true>(c, mats);
 }
 
-adaf_status muon_orthogonalize(const muon_matrices* x, const muon_iteration* it, void* out, int32_t out_dtype, void* workspace,
-                               size_t workspace_bytes, void* stream) {
+adaf_status orthogonalize(const muon_matrices* x, const muon_iteration* it, void* out, int32_t out_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
   adaf_status st = check_iteration(it);
   if (st != ADAF_OK) return st;
   if (x == nullptr) return invalid("x is NULL");
   size_t need = 0;
-  if ((st = muon_orthogonalize_workspace_size(x->batch, x->rows, x->cols, &need)) != ADAF_OK) return st;
+  if ((st = check_size(x->batch, x->rows, x->cols, "")) != ADAF_OK) return st;
+  need = bytes_of(x->batch, x->rows, x->cols);
   if (x->dtype != ADAF_FLOAT32 && x->dtype != ADAF_BFLOAT16) return invalid("unknown dtype");
   if (out_dtype != ADAF_FLOAT32 && out_dtype != ADAF_BFLOAT16) return invalid("unknown out_dtype");
   if (need == 0) return ADAF_OK;
@@ -1235,6 +1209,58 @@ adaf_status muon_orthogonalize(const muon_matrices* x, const muon_iteration* it,
   const Call c{it, nullptr, x->rows == 1 ? x->cols : x->stride_r, os == 2 ? kBf16Out : kFp32,
                static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream)};
   return run<false>(c, mats);
+}
+
+// Nothing thrown leaves a C entry point (long lists take host memory).
+template <class Body>
+adaf_status guarded(Body&& body) {
+  try {
+    return body();
+  } catch (const std::exception&) {
+    return fail(ADAF_ERR_UNSUPPORTED, "out of host memory");
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+void muon_default_iteration(muon_iteration* it) {
+  if (it == nullptr) return;
+  std::memset(it, 0, sizeof *it);
+  it->steps = 5;
+  for (int k = 0; k < 5; ++k) {
+    it->coef[k][0] = 3.4445;
+    it->coef[k][1] = -4.7750;
+    it->coef[k][2] = 2.0315;
+  }
+  it->eps = 1e-7;
+}
+
+adaf_status muon_validate(const muon_hparams* hp) { return check_hp(hp); }
+adaf_status muon_validate_iteration(const muon_iteration* it) { return check_iteration(it); }
+
+adaf_status muon_workspace_size(const muon_tensor* tensors, int32_t n, size_t* bytes) {
+  if (bytes == nullptr) return invalid("bytes is NULL");
+  return guarded([&] { return check_tensors(tensors, n, bytes); });
+}
+
+adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t* bytes) {
+  if (bytes == nullptr) return invalid("bytes is NULL");
+  const adaf_status st = check_size(batch, rows, cols, "");
+  if (st != ADAF_OK) return st;
+  *bytes = bytes_of(batch, rows, cols);
+  return ADAF_OK;
+}
+
+adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  return guarded([&] { return step(tensors, n, hp, workspace, workspace_bytes, stream); });
+}
+
+adaf_status muon_orthogonalize(const muon_matrices* x, const muon_iteration* it, void* out, int32_t out_dtype, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return guarded([&] { return orthogonalize(x, it, out, out_dtype, workspace, workspace_bytes, stream); });
 }
 
 adaf_status muon_device_status(const void* workspace, void* stream, int32_t* status) {

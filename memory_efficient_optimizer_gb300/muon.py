@@ -77,11 +77,13 @@ def _matrices(shape):
 class MuonStep:
     """A marshalled multi-tensor Muon step: the descriptor array and the
     workspace are built once; every call is one C-library call.  Parameters
-    have two dimensions or more (leading ones: a stack)."""
+    have two dimensions or more (leading ones: a stack).  ``workspace``: uint8
+    memory to use in place of an own one, if it is large enough; steps that
+    share it must not run at the same time."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[dict], lr=1e-3,
                  momentum=0.95, nesterov=True, weight_decay=0.0, adjust_lr="original", steps=5,
-                 coefficients=COEFFICIENTS, eps=1e-7):
+                 coefficients=COEFFICIENTS, eps=1e-7, workspace: Optional[torch.Tensor] = None):
         params, grads, states = list(params), list(grads), list(states)
         if len(params) != len(grads) or len(params) != len(states):
             raise ValueError("params, grads and states must have the same length")
@@ -111,8 +113,12 @@ class MuonStep:
                                  "the param's device")
             self._tensors[k] = B.muon_tensor(_ptr(p), _ptr(g), _DTYPES[g.dtype], *_matrices(p.shape), _ptr(m))
         self.workspace_bytes = B.muon_workspace_size(self._tensors, n) if n else 0
-        self.workspace = (torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
-                          if n else None)
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+                                      or workspace.device != self.device or workspace.numel() < self.workspace_bytes):
+            workspace = None
+        if workspace is None and n:
+            workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.workspace = workspace
 
     def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         if self.n == 0:
@@ -229,6 +235,7 @@ class Muon(torch.optim.Optimizer):
                 if p.dim() < 2:
                     raise ValueError("Muon steps matrices (two dimensions or more): give the others to another optimizer")
         self._plans = {}
+        self._workspaces = {}       # by device: gigabytes for large layers, so one for all plans
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -249,11 +256,17 @@ class Muon(torch.optim.Optimizer):
             states = [self.state[p] for p in ps]
             key = (gi, tuple(p.data_ptr() for p in ps), tuple(g.data_ptr() for g in grads),
                    tuple(st["momentum"].data_ptr() for st in states), repr(sorted(hp.items())))
+            if torch.cuda.is_current_stream_capturing():
+                # memory of a graph's own pool is not kept for calls outside it
+                MuonStep(ps, grads, states, **hp)()
+                continue
             plan = self._plans.get(key)
             if plan is None:
-                plan = MuonStep(ps, grads, states, **hp)
-                if len(self._plans) > 16:
+                kept = self._workspaces.get(ps[0].device)
+                plan = MuonStep(ps, grads, states, workspace=kept, **hp)
+                if len(self._plans) > 16 or (kept is not None and plan.workspace is not kept):
                     self._plans.clear()
+                self._workspaces[ps[0].device] = plan.workspace
                 self._plans[key] = plan
             plan()
         return loss

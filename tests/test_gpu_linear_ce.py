@@ -121,6 +121,16 @@ def test_strides_and_views():
     compare(out, h, w, y, weights=share)
 
 
+@pytest.mark.parametrize("vocab", [1, 2, 130])
+def test_weights_with_aligned_gaps(vocab):
+    """Rows 16-byte aligned with gaps between them are read where they are; a single row's stride says nothing."""
+    h, w, y = make(70, 40, vocab, seed=16)
+    wide = torch.full((vocab, 56), float("nan"), dtype=BF, device="cuda")
+    for wv in (wide[:, 8:48], wide.as_strided((vocab, 40), (0 if vocab == 1 else 56, 1), 8)):
+        wv.copy_(w)
+        compare(meo.linear_cross_entropy(h.cuda(), wv, y.cuda()), h, w, y)
+
+
 def test_in_place_and_accumulated():
     h, w, y = make(150, 64, 300, seed=6)
     hc = h.cuda()

@@ -260,6 +260,27 @@ def test_optimizer_with_the_loss_of_a_model():
     assert all(torch.equal(opt.state[p]["momentum"], again.state[p]["momentum"]) for p in model.parameters())
 
 
+def test_optimizer_keeps_one_workspace():
+    """New gradient tensors every step make new plans, not new workspaces."""
+    ps = [torch.nn.Parameter(normal((40, 30), k).cuda()) for k in range(2)]
+    opt = meo.Muon([{"params": ps[:1]}, {"params": ps[1:], "lr": 0.1}], lr=0.02)
+    keep = []
+    for t in range(4):
+        for k, p in enumerate(ps):
+            p.grad = normal((40, 30), 10 * t + k).cuda()
+            keep.append(p.grad)
+        opt.step()
+    assert len({plan.workspace.data_ptr() for plan in opt._plans.values()}) == 1
+    graph = torch.cuda.CUDAGraph()
+    before = [p.detach().clone() for p in ps]
+    with torch.cuda.graph(graph):
+        opt.step()
+    assert all(torch.equal(p, b) for p, b in zip(ps, before))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not any(torch.equal(p, b) for p, b in zip(ps, before)) and all(p.isfinite().all() for p in ps)
+
+
 def test_a_copy_that_never_lands_ends_the_call():
     """A wait runs out: the call ends by itself, the status says so, the parameters stay."""
     p = normal((100, 300), 1).cuda()
