@@ -636,9 +636,11 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   fence_after();
   const uint32_t tmem = *tmem_at;
 
+  // (the status first: who learns of a tile that this CTA could not finish learns of it too)
   auto gave_up = [&] {
-    *off = 1;
     atomicOr(a.status, 1);
+    __threadfence();
+    *off = 1;
   };
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (bar_try(bar, parity)) return true;
