@@ -22,7 +22,8 @@
  * most of their size is, are kept in fp32 and multiplied apart, so a rounding
  * is relative to what a step changes and small singular values are not lost in
  * the large ones' roundings: the result is within 1e-3 of the formula
- * (2-norm of the difference over 2-norm), whatever the spectrum.
+ * (2-norm of the difference over 2-norm), whatever the spectrum, and within
+ * 3e-3 for matrices with a side of a few values.
  *
  * Values.  A matrix with NaN or infinities, or whose sum of squares overflows
  * fp32, answers NaN; a matrix of zeros stays zero.  Equal inputs give equal

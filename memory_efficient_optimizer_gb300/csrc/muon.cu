@@ -32,9 +32,11 @@
 // for decaying spectra alike, where fp16 iterates are 1.3e-3 to 1.2e-2 off and
 // bf16 ones 1e-2 to 9e-2.
 //
-// What bounds it: the tensor cores, for matrices from about 2000 on; (3 m^2 n +
-// m^3) 2 / 2 flops a step, half of what plain products of the symmetric A and B
-// would take.
+// What bounds it: the tensor cores under the power cap, for matrices from about
+// 2000 on (a decoder layer of 218 M values: 11.1 ms, 1330 TFLOP/s of the 3 m^2 n +
+// m^3 flops a step that are left when the symmetric A and B are computed by one
+// half); L2 where m is about 1000; the way from one phase to the next, 5 to 6 us,
+// for small ones.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -294,9 +296,9 @@ __device__ __forceinline__ void pack32(const float (&v)[32], uint4 (&w)[4]) {
 struct Matrix {
   __half* hi;            // [2][m][ldx]: of this step and of the next
   float* xb;             // x in blocks (block_at), updated in place
-  __half* fe;            // [2][m][lda]: F and E, the tiles on and above the diagonal
-  __half* fb;            // F in blocks
-  float* dg;             // [2][lda]: D and G
+  __half* fe;            // [kSlabs][m][lda]: symmetric matrices without their diagonals, the tiles on and above it
+  __half* fb;            // the same in blocks
+  float* dg;             // [kSlabs][lda]: the diagonals
   float* p;              // the parameter, or the result
   int32_t m, n, ldx, lda;
   int32_t flags;
@@ -306,6 +308,22 @@ struct Matrix {
 
 enum Out : int32_t { kUpdate, kFp32, kBf16Out };
 
+constexpr int kSlabs = 4;
+// Scales of the symmetric matrices' elements beside the diagonals: at most 3.9, so 2^14; a product
+// of two polynomials at most 15.5, so 2^12.
+constexpr int kSymScale = 14, kPairScale = 12;
+
+enum Kind : int32_t { kGram, kPoly, kMul, kApply };
+struct Phase {
+  int32_t kind;
+  int32_t a, b, out;     // slabs of the symmetric factors and the result; of x: 0 or 1
+  float c0, c1, c2;      // kPoly: a, b, c; kMul: factors of the product and of the diagonals' parts; kApply: of the product
+  int32_t start;         // first tile
+  int32_t syms, apps;    // phases before it, by the kind of their results
+  int32_t last;          // kApply: of the last step
+};
+constexpr int kMaxPhases = 3 * MUON_MAX_STEPS + 1;
+
 template <int COUNT>
 struct IterateArgs {
   struct {
@@ -313,8 +331,8 @@ struct IterateArgs {
   } map[COUNT];
   Matrix mat[COUNT];     // (copied to shared memory first: at every phase's first tile the constants
                          // would be asked for anew, a microsecond or two each)
-  float coef[MUON_MAX_STEPS][3];
-  int32_t count, steps, sym_tiles, app_tiles;
+  Phase phase[kMaxPhases];
+  int32_t count, phases, tiles;
   int32_t out;
   float keep;
   int32_t stall;
@@ -324,32 +342,48 @@ struct IterateArgs {
 
 using meo::tc::Part;
 
-// A = x x^T: F = A without its diagonal (scaled by 2^15), D the diagonal.
+// 32 columns of a symmetric result without its diagonal, into slab `out`.
+__device__ __forceinline__ void store_symmetric(const Matrix& t, const Part& p, int j0, int out, uint4 (&w)[4]) {
+  if (p.row0() < p.m) {
+    uint4* const to = reinterpret_cast<uint4*>(t.fb + (block_at((p.m + 31) & ~31, 0, p.m) * out + block_at(p.row0(), j0, p.m))) + p.ex.lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[32 * i] = w[i];
+  }
+  store_rows(t.fe + static_cast<int64_t>(out) * p.m * t.lda, t.lda, p, j0, w);
+}
+// The element of a lane's row that lies on the diagonal, in a block on it; and what is stored there.
+__device__ __forceinline__ float on_diagonal(const Part& p, const float (&v)[32]) {
+  float d = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) d = i == p.ex.lane ? v[i] : d;
+  return d;
+}
+__device__ __forceinline__ void clear_diagonal(const Part& p, uint4 (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint32_t& x = i % 4 == 0 ? w[i / 4].x : i % 4 == 1 ? w[i / 4].y : i % 4 == 2 ? w[i / 4].z : w[i / 4].w;
+    if (p.ex.lane == 2 * i) x &= 0xffff0000u;
+    if (p.ex.lane == 2 * i + 1) x &= 0xffffu;
+  }
+}
+
+// A = x x^T = D + F.
 __device__ __forceinline__ void end_gram(const Matrix& t, const Part& p) {
 #pragma unroll 1
   for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
     const int j0 = p.col + c;
     float v[32];
-    p.load(c, v);
+    p.load(c, v);   // A 2^30
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= 0x1p-15f;
-    if (p.row0() == j0) {
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        d = i == p.ex.lane ? v[i] : d;
-        v[i] = i == p.ex.lane ? 0.f : v[i];
-      }
-      if (p.row < p.m) t.dg[p.row] = d * 0x1p-15f;
-    }
+    for (int i = 0; i < 32; ++i) v[i] *= 0x1p-16f;
     uint4 w[4];
     pack32(v, w);
-    if (p.row0() < p.m) {
-      uint4* const to = reinterpret_cast<uint4*>(t.fb + block_at(p.row0(), j0, p.m)) + p.ex.lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[32 * i] = w[i];
+    if (p.row0() == j0) {
+      const float d = on_diagonal(p, v);
+      if (p.row < p.m) t.dg[p.row] = d * 0x1p-14f;
+      clear_diagonal(p, w);
     }
-    store_rows(t.fe, t.lda, p, j0, w);
+    store_symmetric(t, p, j0, 0, w);
   }
 }
 
@@ -370,26 +404,21 @@ struct Ahead {
   }
 };
 
-// B = b A + c A A: E without the diagonal (scaled by 2^14), G the diagonal.  di, dj: D of the row,
-// and of the columns (in the warp's shared memory).
+// P = a + b A + c A A, A = D + F.  di, dj: D of the row, and of the columns (in the warp's shared
+// memory).
 template <int CHUNKS>
-__device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, const Ahead<4, CHUNKS>& f, float di, const float* dj, float cb,
-                                         float cc) {
+__device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, const Ahead<4, CHUNKS>& f, float di, const float* dj,
+                                         const Phase& ph) {
+  const float cb = ph.c1, cc = ph.c2;
+  float* const diagonal = t.dg + static_cast<int64_t>(ph.out) * t.lda;
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int j0 = p.col + 32 * c;
     if (j0 >= p.m) break;
     float v[32];
     p.load(32 * c, v);
-    if (p.row0() == j0) {
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x = i == p.ex.lane ? v[i] : x;
-      if (p.row < p.m) t.dg[t.lda + p.row] = fmaf(cc, fmaf(di, di, x * 0x1p-30f), cb * di);
-    }
-    // ((b + c (d_i + d_j)) F + c F F) 2^14, two columns at a time; F is scaled by 2^15, F F by 2^30
-    const float2 own = make_float2(0.5f * (cb + cc * di), 0.5f * (cb + cc * di)), half_c = make_float2(0.5f * cc, 0.5f * cc),
-                 small_c = make_float2(cc * 0x1p-16f, cc * 0x1p-16f);
+    // (b + c (d_i + d_j)) F + c F F, two columns at a time; F is scaled by 2^14, F F by 2^28
+    const float2 own = make_float2(cb + cc * di, cb + cc * di), c2 = make_float2(cc, cc), small_c = make_float2(cc * 0x1p-14f, cc * 0x1p-14f);
     uint4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -399,28 +428,60 @@ __device__ __forceinline__ void end_poly(const Matrix& t, const Part& p, const A
       for (int q = 0; q < 4; ++q) {
         const float2 d = *reinterpret_cast<const float2*>(dj + 32 * c + 8 * i + 2 * q);
         const float2 x = __fmul2_rn(small_c, make_float2(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]));
-        const float2 e = __ffma2_rn(unpack(r[q]), __ffma2_rn(half_c, d, own), x);
+        const float2 e = __ffma2_rn(unpack(r[q]), __ffma2_rn(c2, d, own), x);
         o[q] = pack(e.x, e.y);
       }
       w[i] = make_uint4(o[0], o[1], o[2], o[3]);
     }
     if (p.row0() == j0) {
-      // the diagonal is G's
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t& x = i % 4 == 0 ? w[i / 4].x : i % 4 == 1 ? w[i / 4].y : i % 4 == 2 ? w[i / 4].z : w[i / 4].w;
-        if (p.ex.lane == 2 * i) x &= 0xffff0000u;
-        if (p.ex.lane == 2 * i + 1) x &= 0xffffu;
-      }
+      const float x = on_diagonal(p, v) * 0x1p-28f;
+      if (p.row < p.m) diagonal[p.row] = ph.c0 + fmaf(cc, fmaf(di, di, x), cb * di);
+      clear_diagonal(p, w);
     }
-    store_rows(t.fe + static_cast<int64_t>(p.m) * t.lda, t.lda, p, j0, w);
+    store_symmetric(t, p, j0, ph.out, w);
   }
 }
 
-// 32 columns of (a + G) x + E x, scaled by 2^15.
-__device__ __forceinline__ void applied(const Part& p, int c, const uint4 (&x)[8], float factor, float (&v)[32]) {
+// The product of two symmetric matrices that commute, U = D + E and V = D' + E': E E' + D E' + E D' + D D'.
+// di: D of the row, own: D' of the row, dj: D' of the columns.
+template <int CHUNKS>
+__device__ __forceinline__ void end_mul(const Matrix& t, const Part& p, const Ahead<4, CHUNKS>& u, const Ahead<4, CHUNKS>& f, float di,
+                                        float own, const float* dj, const Phase& ph) {
+  float* const diagonal = t.dg + static_cast<int64_t>(ph.out) * t.lda;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int j0 = p.col + 32 * c;
+    if (j0 >= p.m) break;
+    float v[32];
+    p.load(32 * c, v);
+    const float2 c0 = make_float2(ph.c0, ph.c0), c1 = make_float2(ph.c1, ph.c1), d2 = make_float2(di * ph.c1, di * ph.c1);
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t r[4] = {f.w[c][i].x, f.w[c][i].y, f.w[c][i].z, f.w[c][i].w}, s[4] = {u.w[c][i].x, u.w[c][i].y, u.w[c][i].z, u.w[c][i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 d = __fmul2_rn(c1, *reinterpret_cast<const float2*>(dj + 32 * c + 8 * i + 2 * q));
+        const float2 x = __fmul2_rn(c0, make_float2(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]));
+        const float2 e = __ffma2_rn(unpack(r[q]), d2, __ffma2_rn(unpack(s[q]), d, x));
+        o[q] = pack(e.x, e.y);
+      }
+      w[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    if (p.row0() == j0) {
+      const float x = on_diagonal(p, v) * 0x1p-28f;
+      if (p.row < p.m) diagonal[p.row] = fmaf(di, own, x);
+      clear_diagonal(p, w);
+    }
+    store_symmetric(t, p, j0, ph.out, w);
+  }
+}
+
+// 32 columns of D x + E x, scaled by 2^15; the product comes with the scale of E too.
+__device__ __forceinline__ void applied(const Part& p, int c, const uint4 (&x)[8], float factor, float scale, float (&v)[32]) {
   p.load(c, v);
-  const float2 f = make_float2(factor, factor), s = make_float2(0x1p-14f, 0x1p-14f);
+  const float2 f = make_float2(factor, factor), s = make_float2(scale, scale);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 a = __ffma2_rn(f, make_float2(__uint_as_float(x[i].x), __uint_as_float(x[i].y)), __fmul2_rn(s, make_float2(v[4 * i], v[4 * i + 1])));
@@ -431,14 +492,14 @@ __device__ __forceinline__ void applied(const Part& p, int c, const uint4 (&x)[8
 
 // x of the next step.
 template <int CHUNKS>
-__device__ __forceinline__ void end_next(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, int slab, float factor) {
+__device__ __forceinline__ void end_next(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, int slab, float factor, float scale) {
   __half* const next = t.hi + (slab ^ 1) * (static_cast<int64_t>(p.m) * t.ldx) + static_cast<int64_t>(p.row0()) * t.ldx + p.col;
   uint4* const xb = reinterpret_cast<uint4*>(t.xb + block_at(p.row0(), p.col, p.n)) + p.ex.lane;
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k) {
     if (p.col + 32 * k >= p.n) break;
     float v[32];
-    applied(p, 32 * k, x.w[k], factor, v);
+    applied(p, 32 * k, x.w[k], factor, scale, v);
     if (p.row0() < p.m) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -454,7 +515,8 @@ __device__ __forceinline__ void end_next(const Matrix& t, const Part& p, const A
 
 // The last step: the update of p, or the result.
 template <int CHUNKS>
-__device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, float factor, int out, float keep) {
+__device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const Ahead<8, CHUNKS>& x, float factor, float scale, int out,
+                                         float keep) {
   const bool turned = t.flags & kTurned;
   const bool wide = p.n % (out == kBf16Out ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(t.p) % 16 == 0;
   const float rate = t.rate * 0x1p-15f;
@@ -464,7 +526,7 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const A
     const int c = 32 * k, j0 = p.col + c;
     if (j0 >= p.n) break;
     float v[32];
-    applied(p, c, x.w[k], factor, v);
+    applied(p, c, x.w[k], factor, scale, v);
     if (turned) {
       // down a column of the parameter: the warp's lanes lie side by side there
       if (p.row >= p.m) continue;
@@ -543,8 +605,10 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const A
 
 // ---- the iteration ------------------------------------------------------------------------
 // All steps for all matrices of a group, in one launch: a step is three phases
-// (x x^T, the polynomial, its product with x), each over the tiles of all
-// matrices.  All tiles of all phases are one list, which the grid's CTAs take in
+// (A = x x^T, the polynomial P of it, P x), each over the tiles of all matrices.
+// Two steps at once are seven: with P1 of A1, the second step's A is P1 A1 P1 and
+// its P2 follows; x = P2 P1 x.  That is three more products of m x m and one each
+// less of m x m x n and of two sides of n.  All tiles of all phases are one list, which the grid's CTAs take in
 // turn; a tile waits until the phase before is done with its matrix, which a
 // counter tells (its CTAs are there: a cooperative launch; and their tiles come
 // before in the list, so they wait for nothing that waits for them).  So the last
@@ -552,38 +616,34 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const A
 // a phase need not be a multiple of the CTAs.  Fifteen launches in a row took 11 us
 // each on a matrix of 256 x 512, of which the copies and products are one or two.
 // The roles of the warps and the ring are k_product's; they go on from tile to tile.
-enum Phase : int { kGram, kPoly, kApply };
-
-// The list of tiles: number i is of phase `kind` of step k.
 struct Place {
-  int kind, step, at;    // at: the matrix
+  int phase, at;         // at: the matrix
   int need;              // tiles of the matrix that have to be done
 };
 
 // Tile number i, going up from call to call; false beyond the last.
 template <int CG, int BN>
-__device__ __forceinline__ bool find_tile(const Matrix* mat, int count, int steps, int sym_tiles, int app_tiles, int i, Place* w,
+__device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Phase* phase, int phases, int tiles, int i, Place* w,
                                           meo::tc::Tile* t) {
-  const int a_step = 2 * sym_tiles + app_tiles, k = i / a_step;
-  if (k >= steps) return false;
-  i -= k * a_step;
-  const int kind = i < sym_tiles ? kGram : i < 2 * sym_tiles ? kPoly : kApply;
-  i -= kind * sym_tiles;
-  if (kind != w->kind || k != w->step) w->at = 0;
-  w->kind = kind;
-  w->step = k;
-  const bool sym = kind != kApply;
+  if (i >= tiles) return false;
+  while (w->phase + 1 < phases && i >= phase[w->phase + 1].start) {
+    ++w->phase;
+    w->at = 0;
+  }
+  const Phase& ph = phase[w->phase];
+  i -= ph.start;
+  const bool sym = ph.kind != kApply;
   while (w->at + 1 < count && i >= (sym ? mat[w->at + 1].sym0 : mat[w->at + 1].app0)) ++w->at;
   const Matrix& m = mat[w->at];
   meo::tc::Shape s{};
   s.batch = 1;
   s.splits = 1;
   s.group = 16;
-  const int mt = (m.m + meo::tc::kTileM * CG - 1) / (meo::tc::kTileM * CG), nt = (m.n + BN - 1) / BN;
   constexpr int kRows = meo::tc::kTileM * CG;
+  const int mt = (m.m + kRows - 1) / kRows, nt = (m.n + BN - 1) / BN;
   const int mtn = (m.m + BN - 1) / BN;   // column tiles of the symmetric products
   const int syms = static_cast<int>(meo::tc::sym_tiles<kRows / BN>(mtn));
-  w->need = k * (2 * syms + mt * nt) + kind * syms;
+  w->need = ph.syms * syms + ph.apps * mt * nt;
   if (sym) return meo::tc::tile_of<true, kRows, BN>(i - m.sym0, mt, mtn, s, t);
   return meo::tc::tile_of<false, kRows, BN>(i - m.app0, mt, nt, s, t);
 }
@@ -601,8 +661,8 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   unsigned char* const exchange = ring + STAGES * S::kStage;
   float* const columns = reinterpret_cast<float*>(exchange + kEndWarps * kExchange);   // of each warp: BN / 2 values
   Matrix* const mat = reinterpret_cast<Matrix*>(columns + kEndWarps * (BN / 2));
-  float* const coef = reinterpret_cast<float*>(mat + COUNT);
-  uint64_t* full = reinterpret_cast<uint64_t*>(coef + 3 * MUON_MAX_STEPS);
+  Phase* const phase = reinterpret_cast<Phase*>(mat + COUNT);
+  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(phase + kMaxPhases) + 7) & ~uintptr_t{7});
   uint64_t* empty = full + STAGES;
   uint64_t* sum_full = empty + STAGES;
   uint64_t* sum_empty = sum_full + 2;
@@ -612,11 +672,12 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
-  const int count = a.count, steps = a.steps, sym_tiles = a.sym_tiles, app_tiles = a.app_tiles, out = a.out;
+  const int count = a.count, phases = a.phases, tiles = a.tiles, out = a.out;
   const float keep = a.keep;
   for (int i = threadIdx.x; i < count * static_cast<int>(sizeof(Matrix) / 4); i += kThreads)
     reinterpret_cast<uint32_t*>(mat)[i] = reinterpret_cast<const uint32_t*>(a.mat)[i];
-  for (int i = threadIdx.x; i < 3 * steps; i += kThreads) coef[i] = a.coef[i / 3][i % 3];
+  for (int i = threadIdx.x; i < phases * static_cast<int>(sizeof(Phase) / 4); i += kThreads)
+    reinterpret_cast<uint32_t*>(phase)[i] = reinterpret_cast<const uint32_t*>(a.phase)[i];
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       bar_init(full + i, 1);
@@ -671,31 +732,31 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       }
     }
   };
-  auto next_tile = [&](int i, Place* w, Tile* t) { return find_tile<CG, BN>(mat, count, steps, sym_tiles, app_tiles, i, w, t); };
+  auto next_tile = [&](int i, Place* w, Tile* t) { return find_tile<CG, BN>(mat, count, phase, phases, tiles, i, w, t); };
   if (warp < 4) {
     fewer_registers();
     int stage = 0, acc = 0;
     uint32_t phase_bit = 0, acc_bit = 0;
     bool ok = true;
-    Place w{-1, 0, 0, 0};
+    Place w{0, 0, 0};
     Tile t;
     if (warp == 0 && lane == 0) {
       // ---- copies
       int known_at = -1, known = 0;
       for (int i = first; ok && next_tile(i, &w, &t); i += step) {
+        const Matrix& m = mat[w.at];
+        const int kind = phase[w.phase].kind, za = phase[w.phase].a, zb = phase[w.phase].b;
+        const bool both = kind == kPoly || kind == kMul;   // both factors are symmetric
+        const CUtensorMap* const map_a = kind == kGram ? &a.map[w.at].x : &a.map[w.at].s;
+        const CUtensorMap* const map_b = both ? &a.map[w.at].s : &a.map[w.at].x;
+        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
         if (w.at != known_at || w.need > known) {
           if (!(ok = wait_done(w.at, w.need))) break;
           known_at = w.at;
           known = w.need;
           asm volatile("fence.proxy.async;" ::: "memory");
         }
-        const Matrix& m = mat[w.at];
-        const int kind = w.kind, slab = w.step & 1;
-        const CUtensorMap* const map_a = kind == kGram ? &a.map[w.at].x : &a.map[w.at].s;
-        const CUtensorMap* const map_b = kind == kPoly ? &a.map[w.at].s : &a.map[w.at].x;
-        const int za = kind == kGram ? slab : kind == kPoly ? 0 : 1, zb = kind == kPoly ? 0 : slab;
-        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
-        const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
         for (int kb = 0; kb < blocks; ++kb) {
           if (!(ok = wait(empty + stage, phase_bit ^ 1))) break;
           const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
@@ -705,7 +766,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           const int k = kb * kBlockK;
           if (a.stall == 0) {
             // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
-            const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0 / kRows * kRows);
+            const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (both && k < t.n0 / kRows * kRows);
 #pragma unroll
             for (int j = 0; j < kTileM / 64; ++j)
               tma_load<CG>(pa + j * 8192, map_a, ta ? am + j * 64 : k, ta ? k : am + j * 64, za, bar);
@@ -726,7 +787,8 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       constexpr uint32_t idesc = (1u << 4) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
       for (int i = first; ok && next_tile(i, &w, &t); i += step) {
         const Matrix& m = mat[w.at];
-        const int kind = w.kind;
+        const int kind = phase[w.phase].kind;
+        const bool both = kind == kPoly || kind == kMul;
         const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
         if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
         fence_after();
@@ -735,7 +797,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           fence_after();
           const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
           const int k = kb * kBlockK;
-          const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (kind == kPoly && k < t.n0 / kRows * kRows);
+          const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (both && k < t.n0 / kRows * kRows);
           const uint32_t a_step = ta ? 16 * 128 : 32, b_step = tb ? 16 * 128 : 32, a_lbo = ta ? 8192 : 16, b_lbo = tb ? 8192 : 16;
           const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
 #pragma unroll
@@ -761,19 +823,12 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     p.cols = BN / 2;
     p.ex = {exchange + (warp - 4) * kExchange, lane};
     float* const dj = columns + (warp - 4) * (BN / 2);
-    Place w{-1, 0, 0, 0};
+    Place w{0, 0, 0};
     int known_at = -1, known = 0;
     for (int i = first; next_tile(i, &w, &p.tile); i += step) {
-      if (w.at != known_at || w.need > known) {
-        bool done = true;
-        if (lane == 0) done = wait_done(w.at, w.need);
-        p.bad = __any_sync(0xffffffffu, !done) || p.bad;
-        known_at = w.at;
-        known = w.need;
-      }
-      const Matrix& m = mat[w.at];
-      const int slab = w.step & 1;
-      const float ca = coef[3 * w.step], cb = coef[3 * w.step + 1], cc = coef[3 * w.step + 2];
+      // (all that is known before the wait is looked up before it)
+      const Matrix m = mat[w.at];
+      const Phase ph = phase[w.phase];
       p.m = m.m;
       p.n = m.n;
       p.row = p.tile.m0 + static_cast<int>(rank) * kTileM + static_cast<int>(lanes) + lane;
@@ -784,29 +839,48 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
         p.bad = __any_sync(0xffffffffu, !there) || p.bad;
         fence_after();
       };
-      if (w.kind == kGram) {
+      // of slab z: its blocks from this tile's on; its diagonal at this row
+      const int64_t slab = block_at((p.m + 31) & ~31, 0, p.m);
+      auto blocks_of = [&](int z) { return m.fb + (slab * z + block_at(p.row0(), p.col, p.m)); };
+      auto diagonal_of = [&](int z) { return p.row < p.m ? m.dg[static_cast<int64_t>(z) * m.lda + p.row] : 0.f; };
+      if (w.at != known_at || w.need > known) {
+        bool done = true;
+        if (lane == 0) done = wait_done(w.at, w.need);
+        p.bad = __any_sync(0xffffffffu, !done) || p.bad;
+        known_at = w.at;
+        known = w.need;
+      }
+      if (ph.kind == kGram) {
         arrived();
         end_gram(m, p);
-      } else if (w.kind == kPoly) {
-        Ahead<4, BN / 64> f;
-        f.fetch(p, m.fb + block_at(p.row0(), p.col, p.m), p.row0() < p.m, p.m - p.col);
-        const float di = p.row < p.m ? m.dg[p.row] : 0.f;
-        // (beyond the last column F F and F are 0: D only has to be finite there)
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) dj[32 * c + lane] = p.col + 32 * c + lane < p.m ? m.dg[p.col + 32 * c + lane] : 0.f;
-        __syncwarp();
-        arrived();
-        end_poly(m, p, f, di, dj, cb, cc);
-      } else {
+      } else if (ph.kind == kApply) {
         Ahead<8, BN / 64> x;
         x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
-        const float factor = ca + (p.row < p.m ? m.dg[m.lda + p.row] : 0.f);
+        const float factor = diagonal_of(ph.a);
         const int32_t status = *reinterpret_cast<const volatile int32_t*>(a.status);
         arrived();
-        if (w.step + 1 < steps)
-          end_next(m, p, x, slab, factor);
+        if (ph.last == 0)
+          end_next(m, p, x, ph.b, factor, ph.c0);
         else if (out != kUpdate || (!p.bad && status == 0))   // (otherwise p stays as it is)
-          end_last(m, p, x, factor, out, keep);
+          end_last(m, p, x, factor, ph.c0, out, keep);
+      } else {
+        Ahead<4, BN / 64> f;
+        f.fetch(p, blocks_of(ph.b), p.row0() < p.m, p.m - p.col);
+        const float di = diagonal_of(ph.a), own = CG == 1 ? 0.f : diagonal_of(ph.b);
+        // (beyond the last column the products are 0: the diagonal only has to be finite there)
+        const float* const columns_of = m.dg + static_cast<int64_t>(ph.b) * m.lda;
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) dj[32 * c + lane] = p.col + 32 * c + lane < p.m ? columns_of[p.col + 32 * c + lane] : 0.f;
+        __syncwarp();
+        if (CG == 1 || ph.kind == kPoly) {   // (one CTA a tile: no two steps at once)
+          arrived();
+          end_poly(m, p, f, di, dj, ph);
+        } else {
+          Ahead<4, BN / 64> u;
+          u.fetch(p, blocks_of(ph.a), p.row0() < p.m, p.m - p.col);
+          arrived();
+          end_mul(m, p, u, f, di, own, dj, ph);
+        }
       }
       fence_before();
       // what was written here is read by other CTAs' bulk copies
@@ -916,9 +990,9 @@ Layout layout(int64_t m, int64_t n) {
   };
   L.hi = take(2 * m * ldx * 2);
   L.xb = take(round_up(m, 32) * round_up(n, 32) * 4);
-  L.fe = take(2 * m * lda * 2);
-  L.fb = take(round_up(m, 32) * round_up(m, 32) * 2);
-  L.dg = take(2 * lda * 4);
+  L.fe = take(kSlabs * m * lda * 2);
+  L.fb = take(kSlabs * round_up(m, 32) * round_up(m, 32) * 2);
+  L.dg = take(kSlabs * lda * 4);
   return L;
 }
 int32_t parts_of(int64_t m, int64_t n) {
@@ -930,20 +1004,51 @@ static_assert(4 + kMaxGroup * 4 <= 256, "status and counters");
 // Matrices are worked on in the order of their sizes, the longest sums first; a
 // group ends at so many matrices or values.
 using Size = std::pair<int64_t, int64_t>;   // n, m
-bool before(const Size& x, const Size& y) { return x > y; }
+int64_t tiles_256(const Size& z) { return meo::tc::sym_tiles<1>((z.second + 255) / 256); }
+// Matrices whose first two steps are worth taking at once, at least twice as wide as high: 4096 x
+// 14336 has 13 % fewer flops then, 1024 x 4096 14 %, 4096 x 4096 3 % more.  They make groups of their
+// own where their products fill the SMs (a list of small matrices is better off in one launch).
+bool wide(const Size& z) { return z.first >= 2 * z.second && z.second >= 1024; }
+constexpr int64_t kFullTiles = 64;
+struct Order {
+  bool apart = false;   // wide ones are apart, and come first
+  void look(const std::vector<std::pair<Size, int64_t>>& sizes) {
+    int64_t tiles = 0;
+    for (const auto& z : sizes)
+      if (wide(z.first)) tiles += tiles_256(z.first) * z.second;
+    apart = tiles >= kFullTiles;
+  }
+  bool before(const Size& x, const Size& y) const {
+    return apart && wide(x) != wide(y) ? wide(x) : x > y;
+  }
+};
 struct Grouping {
+  const Order* order;
   int64_t count = 0, values = 0;
   size_t bytes = kHead, most = 0;
-  // Whether a group that goes on with this matrix would be too large.
-  bool full(const Size& z) const { return count == kMaxGroup || (count > 0 && values + z.first * z.second > kGroupValues); }
+  bool first_wide = false;
+  // Whether a group that goes on with this matrix would be too large, or of two kinds.
+  bool full(const Size& z) const {
+    return count == kMaxGroup || (count > 0 && (values + z.first * z.second > kGroupValues || (order->apart && wide(z) != first_wide)));
+  }
   void add(const Size& z) {
-    if (full(z)) *this = Grouping{0, 0, kHead, most};
+    if (full(z)) count = values = 0, bytes = kHead;
+    if (count == 0) first_wide = wide(z);
     ++count;
     values += z.first * z.second;
     bytes += layout(z.second, z.first).bytes;
     most = std::max(most, bytes);
   }
 };
+size_t bytes_of(std::vector<std::pair<Size, int64_t>>& sizes) {
+  Order order;
+  order.look(sizes);
+  std::stable_sort(sizes.begin(), sizes.end(), [&](const auto& x, const auto& y) { return order.before(x.first, y.first); });
+  Grouping g{&order};
+  for (const auto& z : sizes)
+    for (int64_t b = 0; b < z.second; ++b) g.add(z.first);
+  return g.most;
+}
 
 adaf_status check_tensors(const muon_tensor* tensors, int32_t n, size_t* bytes) {
   if (n < 0) return invalid("n < 0");
@@ -960,11 +1065,7 @@ adaf_status check_tensors(const muon_tensor* tensors, int32_t n, size_t* bytes) 
     if ((total += t.batch) > kMaxMatrices) return fail(ADAF_ERR_UNSUPPORTED, "more than 2^20 matrices");
     sizes.push_back({{std::max(t.rows, t.cols), std::min(t.rows, t.cols)}, t.batch});
   }
-  std::stable_sort(sizes.begin(), sizes.end(), [](const auto& x, const auto& y) { return before(x.first, y.first); });
-  Grouping g;
-  for (const auto& z : sizes)
-    for (int64_t b = 0; b < z.second; ++b) g.add(z.first);
-  *bytes = g.most;
+  *bytes = bytes_of(sizes);
   return ADAF_OK;
 }
 
@@ -990,24 +1091,68 @@ struct Call {
     if (e_ != cudaSuccess) return cuda_fail(e_, what); \
   } while (0)
 
+// Whether the first two steps' polynomials stay within what a product of them may be.
+bool pair_fits(const muon_iteration& it) {
+  if (it.steps < 2) return false;
+  double top = 1.0, most = 1.0;
+  for (int k = 0; k < 2; ++k) {
+    double reach = 0.0, poly = 0.0;
+    for (int i = 0; i <= 4096; ++i) {
+      const double x = top * i / 4096, p = it.coef[k][0] + it.coef[k][1] * x * x + it.coef[k][2] * x * x * x * x;
+      reach = std::max(reach, std::fabs(p * x));
+      poly = std::max(poly, std::fabs(p));
+    }
+    top = reach;
+    most *= poly;
+  }
+  return most <= 15.5;
+}
+
+// The phases of a call; sym, app: tiles of all matrices in a symmetric product and in one with x.
+int phases_of(const muon_iteration& it, bool pair, int64_t sym, int64_t app, Phase* phase, int32_t* tiles) {
+  int n = 0, x = 0;
+  int32_t at = 0, syms = 0, apps = 0;
+  auto add = [&](int kind, int a, int b, int out, double c0, double c1, double c2, bool last) {
+    phase[n++] = {kind, a, b, out, static_cast<float>(c0), static_cast<float>(c1), static_cast<float>(c2), at, syms, apps, last ? 1 : 0};
+    at += static_cast<int32_t>(kind == kApply ? app : sym);
+    ++(kind == kApply ? apps : syms);
+  };
+  auto poly = [&](int k, int in, int out) { add(kPoly, in, in, out, it.coef[k][0], it.coef[k][1], it.coef[k][2], false); };
+  auto mul = [&](int a, int b, int out, int scale) { add(kMul, a, b, out, std::ldexp(1.0, scale - 2 * kSymScale), std::ldexp(1.0, scale - kSymScale), 0, false); };
+  for (int k = 0; k < it.steps;) {
+    add(kGram, x, x, 0, 0, 0, 0, false);
+    poly(k, 0, 1);
+    const bool two = pair && k == 0;
+    if (two) {
+      mul(1, 0, 2, kSymScale);    // P1 A1
+      mul(2, 1, 0, kSymScale);    // A2 = P1 A1 P1
+      poly(1, 0, 3);              // P2
+      mul(3, 1, 2, kPairScale);   // P2 P1
+    }
+    k += two ? 2 : 1;
+    add(kApply, two ? 2 : 1, x, 0, std::ldexp(1.0, -(two ? kPairScale : kSymScale)), 0, 0, k == it.steps);
+    x ^= 1;
+  }
+  *tiles = at;
+  return n;
+}
+
 template <int CG, int BN, int STAGES, int COUNT>
-adaf_status iterate(const Call& c, const Listed* mats, int count) {
+adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   using namespace meo::tc;
   auto* const kernel = k_muon_iterate<CG, BN, STAGES, COUNT>;
-  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + 3 * MUON_MAX_STEPS * 4;
+  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + kMaxPhases * sizeof(Phase) + 8;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   IterateArgs<COUNT> a;
   std::memset(&a, 0, sizeof a);
   a.count = count;
-  a.steps = c.it->steps;
-  for (int k = 0; k < a.steps; ++k)
-    for (int q = 0; q < 3; ++q) a.coef[k][q] = static_cast<float>(c.it->coef[k][q]);
   a.out = c.out;
   a.keep = c.hp != nullptr ? static_cast<float>(1.0 - c.hp->lr * c.hp->weight_decay) : 1.f;
   a.stall = t_stall ? 1 : 0;
   a.status = reinterpret_cast<int32_t*>(c.ws);
   a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
   unsigned char* at = c.ws + kHead;
+  int32_t sym = 0, app = 0;
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
     const Layout L = layout(z.m, z.n);
@@ -1030,15 +1175,16 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
       m.rate = static_cast<float>(c.hp->lr * (original ? std::sqrt(std::max(1.0, h / w)) : 0.2 * std::sqrt(std::max(h, w))));
     }
     if (!make_map(&a.map[i].x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
-        !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, 2, z.m * m.lda, 64))
+        !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, kSlabs, z.m * m.lda, 64))
       return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     constexpr int kRows = kTileM * CG;
     const int64_t mt = (z.m + kRows - 1) / kRows, nt = (z.n + BN - 1) / BN;
-    m.sym0 = a.sym_tiles;
-    m.app0 = a.app_tiles;
-    a.sym_tiles += static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
-    a.app_tiles += static_cast<int32_t>(mt * nt);
+    m.sym0 = sym;
+    m.app0 = app;
+    sym += static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
+    app += static_cast<int32_t>(mt * nt);
   }
+  a.phases = phases_of(*c.it, pair, sym, app, a.phase, &a.tiles);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.blockDim = dim3(kThreads);
@@ -1066,13 +1212,13 @@ adaf_status iterate(const Call& c, const Listed* mats, int count) {
     if (most < 1) return fail(ADAF_ERR_CUDA, "k_muon_iterate does not fit this device");
     if (device < 64) together[device] = most;
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(most, std::max(a.sym_tiles, a.app_tiles)) * CG));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(most, std::max(sym, app)) * CG));
   MUON_TRY(g_profile.run(kSlotIterate, c.s, [&] { return cudaLaunchKernelEx(&cfg, kernel, a); }), "k_muon_iterate");
   return ADAF_OK;
 }
 
 template <bool STEP>
-adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) {
+adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, bool apart) {
   MuonArgs a;
   std::memset(&a, 0, sizeof a);
   a.count = count;
@@ -1109,8 +1255,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
     t.tile0 = tiles;
     parts += t.parts;
     tiles += static_cast<int32_t>(((z.m + 63) / 64) * ((z.n + 63) / 64));
-    const int64_t mt = (z.m + 255) / 256;
-    big += mt * (mt + 1) / 2;
+    big += tiles_256({z.n, z.m});
     small += ((z.m + 127) / 128) * ((z.n + 127) / 128);
   }
   MUON_TRY(g_profile.run(kSlotMoment, c.s, [&] {
@@ -1120,25 +1265,33 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first) 
   MUON_TRY(g_profile.run(kSlotPack, c.s, [&] {
     return meo::tc::launch_early(k_muon_pack<STEP>, dim3(static_cast<unsigned>(tiles)), 256, c.s, a);
   }), "k_muon_pack");
-  if (big >= 64) return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count) : iterate<2, 256, 6, kMaxGroup>(c, mats, count);
+  if (big >= kFullTiles) {
+    // (a group's matrices are all wide, or none is)
+    const bool pair = apart && wide({mats[0].n, mats[0].m}) && pair_fits(*c.it);
+    return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count, pair) : iterate<2, 256, 6, kMaxGroup>(c, mats, count, pair);
+  }
   // Narrow tiles where each of them has an SM: half as much to load and to write out a tile, for
   // 256 x 512 102 us to 115, six matrices of 256 x 256 to 1024 126 to 140; 1403 x 777, where two
   // rounds would be needed, 198 to 175.
   int device = 0, sms = 0;
   MUON_TRY(meo::tc::sm_count(&device, &sms), "current device");
-  if (2 * small > sms) return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count) : iterate<1, 128, 6, kMaxGroup>(c, mats, count);
-  return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count) : iterate<1, 64, 8, kMaxGroup>(c, mats, count);
+  if (2 * small > sms) return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count, false) : iterate<1, 128, 6, kMaxGroup>(c, mats, count, false);
+  return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count, false) : iterate<1, 64, 8, kMaxGroup>(c, mats, count, false);
 }
 
 template <bool STEP>
 adaf_status run(const Call& c, std::vector<Listed>& mats) {
-  std::stable_sort(mats.begin(), mats.end(), [](const Listed& x, const Listed& y) { return before({x.n, x.m}, {y.n, y.m}); });
+  std::vector<std::pair<Size, int64_t>> sizes;
+  for (const Listed& z : mats) sizes.push_back({{z.n, z.m}, 1});
+  Order order;
+  order.look(sizes);
+  std::stable_sort(mats.begin(), mats.end(), [&](const Listed& x, const Listed& y) { return order.before({x.n, x.m}, {y.n, y.m}); });
   bool first = true;
   for (size_t i = 0; i < mats.size();) {
-    Grouping g;
+    Grouping g{&order};
     size_t j = i;
     for (; j < mats.size() && !g.full({mats[j].n, mats[j].m}); ++j) g.add({mats[j].n, mats[j].m});
-    const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(j - i), first);
+    const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(j - i), first, order.apart);
     if (st != ADAF_OK) return st;
     first = false;
     i = j;
@@ -1148,10 +1301,9 @@ adaf_status run(const Call& c, std::vector<Listed>& mats) {
 
 // Bytes for a stack of matrices.
 size_t bytes_of(int64_t batch, int64_t rows, int64_t cols) {
-  Grouping g;
-  if (rows > 0 && cols > 0)
-    for (int64_t b = 0; b < batch; ++b) g.add({std::max(rows, cols), std::min(rows, cols)});
-  return g.most;
+  std::vector<std::pair<Size, int64_t>> sizes;
+  if (batch > 0 && rows > 0 && cols > 0) sizes.push_back({{std::max(rows, cols), std::min(rows, cols)}, batch});
+  return bytes_of(sizes);
 }
 
 adaf_status step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes, void* stream) {
@@ -1251,8 +1403,10 @@ adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64
   if (bytes == nullptr) return invalid("bytes is NULL");
   const adaf_status st = check_size(batch, rows, cols, "");
   if (st != ADAF_OK) return st;
-  *bytes = bytes_of(batch, rows, cols);
-  return ADAF_OK;
+  return guarded([&] {
+    *bytes = bytes_of(batch, rows, cols);
+    return ADAF_OK;
+  });
 }
 
 adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes,

@@ -72,19 +72,54 @@ def test_small_singular_values_are_kept(shape, power):
     assert np.all(np.abs(a - b) < 4 * TOL * np.abs(b) + 1e-6)
 
 
-@pytest.mark.parametrize("shape", [(2000, 1500), (3, 1100, 2304), (4608, 520)])
-def test_large_tiles(shape):
-    """Many tiles a matrix and a CTA, in pairs of CTAs and apart, against fp64 on the GPU."""
-    x = normal(shape, 5).cuda()
+def on_gpu(x, coefficients=O.COEFFICIENTS):
+    """The formula in fp64 on the GPU, for matrices too large for the oracle."""
     want = x.double()
     want = want / want.flatten(-2).norm(dim=-1)[..., None, None]
-    turn = shape[-2] > shape[-1]
+    turn = x.shape[-2] > x.shape[-1]
     want = want.mT if turn else want
-    for a, b, c in O.COEFFICIENTS:
+    for a, b, c in coefficients:
         g = want @ want.mT
         want = a * want + (b * g + c * (g @ g)) @ want
-    want = (want.mT if turn else want).cpu().numpy()
-    assert far(meo.orthogonalize(x, dtype=torch.float32), want) < TOL
+    return (want.mT if turn else want).cpu().numpy()
+
+
+@pytest.mark.parametrize("shape", [(2000, 1500), (3, 1100, 2304), (4608, 520)])
+def test_large_tiles(shape):
+    """Many tiles a matrix and a CTA, in pairs of CTAs and apart."""
+    x = normal(shape, 5).cuda()
+    assert far(meo.orthogonalize(x, dtype=torch.float32), on_gpu(x)) < TOL
+
+
+@pytest.mark.parametrize("shape", [(7, 1024, 2048), (7, 2101, 1030), (12, 1025, 2056)])
+@pytest.mark.parametrize("spectrum", ["flat", "falling"])
+def test_two_steps_at_once(shape, spectrum):
+    """Wide matrices, enough of them: the first two steps come from one x x^T."""
+    x = normal(shape, 6).cuda()
+    if spectrum == "falling":
+        r = min(shape[-2:])
+        s = torch.arange(1, r + 1, device="cuda") ** -1.0
+        x = (normal((shape[0], shape[1], r), 7).cuda() * s) @ normal((shape[0], r, shape[2]), 8).cuda()
+    assert far(meo.orthogonalize(x, dtype=torch.float32), on_gpu(x)) < TOL
+    for co in ([O.COEFFICIENTS[0]] * 2, [O.COEFFICIENTS[0]] * 3, [(1.875, -1.25, 0.375)] * 4, [O.COEFFICIENTS[0]]):
+        got = meo.orthogonalize(x[:7], steps=len(co), coefficients=co, dtype=torch.float32)
+        assert far(got, on_gpu(x[:7], co)) < TOL
+
+
+def test_a_list_of_wide_and_square_matrices():
+    """Both kinds of group in one call."""
+    shapes = [(7, 1024, 2048), (300, 300), (2, 2100, 1024), (64, 200), (1100, 1200)]
+    params = [normal(s, k).cuda() for k, s in enumerate(shapes)]
+    grads = [normal(s, 10 + k).cuda() for k, s in enumerate(shapes)]
+    before = [p.clone() for p in params]
+    step = meo.MuonStep(params, grads, meo.init_muon_state(params), lr=0.1, adjust_lr="match_rms", nesterov=False)
+    step()
+    assert step.device_status() == 0
+    for p, b, g, s in zip(params, before, grads, shapes):
+        moved = (b - p).double() / (0.1 * 0.2 * max(s[-2:]) ** 0.5)
+        want = on_gpu(g)
+        # an fp32 rounding of p is 2^-24 of it, the update's elements are 1 / sqrt(max side) or so
+        assert far(moved, want) < TOL + 1e-3
 
 
 def test_rows_with_gaps_and_views():
