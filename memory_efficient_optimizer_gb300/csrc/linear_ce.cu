@@ -798,8 +798,13 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   const linear_ce_hidden& h = *hidden;
   const linear_ce_weight& w = *weight;
   const int64_t tokens = h.batch * h.seq;
+  // strides of rows that reach no further than 2^46 values, so that no place overflows
   auto bad_stride = [](int64_t s) { return s < 0 || s > kMaxStride; };
-  if (bad_stride(h.stride_b) || bad_stride(h.stride_s)) return invalid("hidden: strides must be 0 to 2^38");
+  auto too_far = [&](int64_t sb, int64_t ss) {
+    constexpr int64_t kReach = int64_t{1} << 46;
+    return (h.batch > 1 && sb > kReach / (h.batch - 1)) || (h.seq > 1 && ss > kReach / (h.seq - 1));
+  };
+  if (bad_stride(h.stride_b) || bad_stride(h.stride_s) || too_far(h.stride_b, h.stride_s)) return invalid("hidden: strides must be 0 to 2^38, and reach 2^46 values");
   if (tokens > 0 && h.p == nullptr) return invalid("hidden is NULL");
   if (w.p == nullptr) return invalid("weight is NULL");
   if (!aligned(h.p, size_of(h.dtype))) return invalid("hidden is not element-aligned");
@@ -807,10 +812,12 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (targets->dtype != LOSS_INT32 && targets->dtype != LOSS_INT64) return invalid("targets: unknown dtype");
   if (tokens > 0 && targets->rows.p == nullptr) return invalid("targets is NULL");
   if (!aligned(targets->rows.p, targets->dtype == LOSS_INT64 ? 8 : 4)) return invalid("targets is not element-aligned");
-  if (bad_stride(targets->rows.stride_b) || bad_stride(targets->rows.stride_s)) return invalid("targets: strides must be 0 to 2^38");
+  if (bad_stride(targets->rows.stride_b) || bad_stride(targets->rows.stride_s) || too_far(targets->rows.stride_b, targets->rows.stride_s))
+    return invalid("targets: strides must be 0 to 2^38, and reach 2^46 values");
   if (!aligned(args->weights.p, 4)) return invalid("weights is not element-aligned");
-  if (args->weights.p != nullptr && (bad_stride(args->weights.stride_b) || bad_stride(args->weights.stride_s)))
-    return invalid("weights: strides must be 0 to 2^38");
+  if (args->weights.p != nullptr && (bad_stride(args->weights.stride_b) || bad_stride(args->weights.stride_s) ||
+                                     too_far(args->weights.stride_b, args->weights.stride_s)))
+    return invalid("weights: strides must be 0 to 2^38, and reach 2^46 values");
   const double inv_t = 1.0 / args->temperature;
   if (!(args->temperature > 0.0) || !std::isfinite(args->temperature) || !std::isfinite(static_cast<float>(inv_t * 1.5)) ||
       static_cast<float>(inv_t) < FLT_MIN)
@@ -820,7 +827,8 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (loss == nullptr) return invalid("loss is NULL");
   if (!aligned(loss, 4) || !aligned(logp, 4) || !aligned(lse, 4)) return invalid("loss, logp or lse is not element-aligned");
   if (gh != nullptr && tokens > 0) {
-    if (bad_stride(gh->stride_b) || bad_stride(gh->stride_s)) return invalid("grad_hidden: strides must be 0 to 2^38");
+    if (bad_stride(gh->stride_b) || bad_stride(gh->stride_s) || too_far(gh->stride_b, gh->stride_s))
+      return invalid("grad_hidden: strides must be 0 to 2^38, and reach 2^46 values");
     if (!aligned(gh->p, size_of(gh->dtype))) return invalid("grad_hidden is not element-aligned");
     if ((gh->seq > 1 && gh->stride_s < gh->dim) || (gh->batch > 1 && gh->stride_b < (gh->seq - 1) * gh->stride_s + gh->dim))
       return invalid("grad_hidden: rows overlap");

@@ -13,10 +13,10 @@
 //                     x = a x + B x; the last one updates p, or writes the result
 //
 // Numbers.  The factors of the products are fp16, scaled by powers of two: an
-// element of x is at most its largest singular value, 1.21, so x 2^15 fits, and
-// so do A 2^15 and B 2^14, and at any size the usual elements are far above the
-// subnormal range (1 / sqrt(mn) 2^15 is 8 at 4096 x 4096).  What rounding does
-// depends on where it enters:
+// element of x is at most its largest singular value, 1.21 (1.9 with other
+// coefficients), so x 2^15 fits, and so do A 2^14 and B 2^14, and at any size the
+// usual elements are far above the subnormal range (1 / sqrt(mn) 2^15 is 8 at
+// 4096 x 4096).  What rounding does depends on where it enters:
 //   - rounding of the factors of x x^T, A A and B x acts like a multiplication
 //     of x by I + d with small d from the left or the right: directions turn by
 //     2^-12 or so, and a small singular value stays as accurate as a large one;

@@ -241,6 +241,29 @@ def test_pieces():
         gw += dx.T @ h[a:a + 100].double()
     for got in (out.grad_weight, fp.grad_weight):
         assert (got.double() - gw).norm() <= 2 ** -7 * gw.norm()
+    for dt in (BF, torch.float32):   # added to what is there, over the pieces
+        more = torch.full((vocab, dim), 0.5, device="cuda", dtype=dt)
+        meo.linear_cross_entropy(h, w, y, grad_weight=more, accumulate=True)
+        want = fp.grad_weight.double() + 0.5
+        assert ((more.double() - want).abs() <= (2 ** -8 if dt == BF else 2 ** -22) * want.abs()).all()
+    # pieces without a token that counts: all of the first, all of the last
+    for cut in (slice(0, 600), slice(500, None)):
+        y2 = y.clone()
+        y2[cut] = -100
+        a = meo.linear_cross_entropy(h, w, y2)
+        keep = (y2 != -100).nonzero()[:, 0]
+        b = meo.linear_cross_entropy(h[keep], w, y2[keep])
+        assert torch.equal(a.logp[keep], b.logp) and torch.equal(a.grad_hidden[keep], b.grad_hidden)
+        assert torch.equal(a.grad_weight, b.grad_weight) and a.grad_hidden[y2 == -100].eq(0).all()
+
+
+@pytest.mark.parametrize("n", [511, 512, 513, 1100, 9000])
+def test_masked_tokens_at_every_count(n):
+    """Tokens found by the gathering itself and by a scan of their own; masks that leave few, and none in long runs."""
+    h, w, y = make(n, 24, 60, seed=n, ignore=0.0)
+    for keep in (torch.arange(n) % 7 == 3, torch.arange(n) == n - 1, torch.arange(n) >= n // 2):
+        y2 = torch.where(keep, y, -100)
+        compare(meo.linear_cross_entropy(h.cuda(), w.cuda(), y2.cuda()), h, w, y2)
 
 
 def test_equal_bits_and_other_streams():

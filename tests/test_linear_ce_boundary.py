@@ -47,7 +47,7 @@ def call(h=None, w=None, y=None, gh=None, gw=None, loss=F, logp=F, lse=F, ws=WS,
     (dict(h=hidden(batch=-1)), "negative"), (dict(h=hidden(dim=0)), "dim"), (dict(w=weight(vocab=0)), "vocab"),
     (dict(h=hidden(p=None)), "hidden is NULL"), (dict(w=weight(p=None)), "weight is NULL"),
     (dict(h=hidden(p=H + 1)), "hidden is not element"), (dict(w=weight(p=W + 1)), "weight is not element"),
-    (dict(h=hidden(ss=-1)), "strides"), (dict(w=weight(sv=15)), "rows overlap"), (dict(ydt=4), "targets: unknown"),
+    (dict(h=hidden(ss=-1)), "strides"), (dict(gh=hidden(p=GH, sb=1 << 47)), "strides"), (dict(w=weight(sv=1 << 39)), "strides"), (dict(w=weight(sv=15)), "rows overlap"), (dict(ydt=4), "targets: unknown"),
     (dict(y=(None, 0, 0)), "targets is NULL"), (dict(y=(Y + 4, 6, 1)), "targets is not element"), (dict(y=(Y, -6, 1)), "strides"),
     (dict(rows=(F + 2, 0, 0)), "weights is not"), (dict(rows=(F, -1, 0)), "weights: strides"), (dict(t=0.0), "temperature"),
     (dict(t=-1.0), "temperature"), (dict(t=float("nan")), "temperature"), (dict(t=float("inf")), "temperature"),
@@ -90,6 +90,13 @@ def test_workspace(lib):
     assert n < (1 << 31) + (1 << 28) + (1 << 20) * (64 * 2 + 12) + 32000 * 64 * 4 + 33600 * (250 * 8 + 4) + (1 << 20)
     with pytest.raises(ValueError, match="bytes"):
         B._check(lib.linear_ce_workspace_size(hidden(), weight(), None, None, None))
+
+
+def test_rows_that_reach_too_far_are_refused(lib):
+    h, args = hidden(ss=1 << 38, seq=1 << 20, batch=1), B.linear_ce_args(B.loss_rows(None, 0, 0), 1.0, 0.0, 1.0)
+    y = B.loss_targets(B.loss_rows(Y, 0, 1), B.LOSS_INT64, -100)
+    with pytest.raises(ValueError, match="reach"):
+        B.linear_ce(h, weight(), ctypes.byref(y), ctypes.byref(args), None, None, F, None, None, WS, 1 << 40, 0)
 
 
 def test_null_structs_refused(lib):
