@@ -746,14 +746,18 @@ def muon_profile_read() -> dict:
 
 def linear_ce_workspace_size(hidden, weight, grad_hidden=None, grad_weight=None) -> int:
     out = ctypes.c_size_t()
-    _check(load().linear_ce_workspace_size(hidden, weight, grad_hidden, grad_weight, ctypes.byref(out)))
+    _check(_loss_call("linear_ce_workspace_size")(_by_address(hidden), _by_address(weight), _by_address(grad_hidden),
+                                                  _by_address(grad_weight), ctypes.byref(out)))
     return int(out.value)
 
 
 def linear_ce(hidden, weight, targets, args, grad_hidden, grad_weight, loss: int, logp: int, lse: int, workspace: int,
               workspace_bytes: int, stream: int) -> None:
-    _check(load().linear_ce(hidden, weight, targets, args, grad_hidden, grad_weight, loss, logp, lse, workspace,
-                            workspace_bytes, stream))
+    st = _loss_call("linear_ce")(_by_address(hidden), _by_address(weight), _by_address(targets), _by_address(args),
+                                 _by_address(grad_hidden), _by_address(grad_weight), loss, logp, lse, workspace,
+                                 workspace_bytes, stream)
+    if st:
+        _check(st)
 
 
 def linear_ce_debug_stall_copies(on: bool) -> None:

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
   meo::tc::next_may_begin();
   if (blockIdx.x == 0) {
     if (a.clear != 0 && threadIdx.x == 0) *a.status = 0;
-    if (threadIdx.x < kMaxGroup) a.done[threadIdx.x] = 0;
+    if (threadIdx.x < kMaxGroup + 1) a.done[threadIdx.x] = 0;   // (and the ticket behind them)
   }
   const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].part0; })];
   const bool bf16 = t.flags & kBf16;
@@ -204,6 +204,7 @@ template <bool STEP>
 __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonArgs a) {
   __shared__ float tile[64][65];
   __shared__ float scratch[8];
+  meo::tc::next_may_begin();
   meo::tc::previous_done();
   const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].tile0; })];
   const int rows = t.m, cols = t.n, ldx = t.ldx;
@@ -338,6 +339,7 @@ struct IterateArgs {
   int32_t stall;
   int32_t* status;
   unsigned* done;        // of each matrix, tiles that are done
+  unsigned* ticket;      // tiles that are taken
 };
 
 using meo::tc::Part;
@@ -608,14 +610,20 @@ __device__ __forceinline__ void end_last(const Matrix& t, const Part& p, const A
 // (A = x x^T, the polynomial P of it, P x), each over the tiles of all matrices.
 // Two steps at once are seven: with P1 of A1, the second step's A is P1 A1 P1 and
 // its P2 follows; x = P2 P1 x.  That is three more products of m x m and one each
-// less of m x m x n and of two sides of n.  All tiles of all phases are one list, which the grid's CTAs take in
-// turn; a tile waits until the phase before is done with its matrix, which a
-// counter tells (its CTAs are there: a cooperative launch; and their tiles come
-// before in the list, so they wait for nothing that waits for them).  So the last
-// tiles of one matrix's phase run beside the first of another's, and the tiles of
-// a phase need not be a multiple of the CTAs.  Fifteen launches in a row took 11 us
-// each on a matrix of 256 x 512, of which the copies and products are one or two.
-// The roles of the warps and the ring are k_product's; they go on from tile to tile.
+// less of m x m x n and of two sides of n.
+//
+// All tiles of all phases are one list, from which a cluster takes the next (an
+// atomic counter) when it begins to have room for it; a tile waits until the phase
+// before is done with its matrix, which another counter tells.  What a tile waits
+// for comes before it in the list, so clusters that run have taken it, and the
+// first tile of those that are not done waits for nothing: the clusters need not all
+// be there together.  (With tiles in fixed turns they had to be, and a cooperative
+// launch holds up the host and the launch: 256 x 512 took 100 us.)  The last tiles
+// of one matrix's phase run beside the first of another's.  Fifteen launches in a
+// row took 11 us each on a matrix of 256 x 512, of which the copies and products
+// are one or two.  The roles of the warps and the ring are k_product's; they go on
+// from tile to tile.  A tile's number goes from the first CTA's copying thread to
+// the others that work on it, in both CTAs, through a queue in shared memory.
 struct Place {
   int phase, at;         // at: the matrix
   int need;              // tiles of the matrix that have to be done
@@ -648,6 +656,8 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Ph
   return meo::tc::tile_of<false, kRows, BN>(i - m.app0, mt, nt, s, t);
 }
 
+constexpr int kQueue = 4;
+
 template <int CG, int BN, int STAGES, int COUNT>
 __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __grid_constant__ IterateArgs<COUNT> a) {
   using namespace meo::tc;
@@ -666,12 +676,14 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   uint64_t* empty = full + STAGES;
   uint64_t* sum_full = empty + STAGES;
   uint64_t* sum_empty = sum_full + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sum_empty + 2);
+  uint64_t* q_full = sum_empty + 2;
+  uint64_t* q_empty = q_full + kQueue;    // the first CTA's counts both CTAs' readers
+  int* q_tile = reinterpret_cast<int*>(q_empty + kQueue);
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(q_tile + kQueue);
   volatile int* off = reinterpret_cast<volatile int*>(tmem_at + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
   const int count = a.count, phases = a.phases, tiles = a.tiles, out = a.out;
   const float keep = a.keep;
   for (int i = threadIdx.x; i < count * static_cast<int>(sizeof(Matrix) / 4); i += kThreads)
@@ -687,6 +699,10 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       bar_init(sum_full + i, 1);
       bar_init(sum_empty + i, CG * kEndWarps);
     }
+    for (int i = 0; i < kQueue; ++i) {
+      bar_init(q_full + i, 1);
+      bar_init(q_empty + i, CG * (kEndWarps + 1));
+    }
     *off = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -696,6 +712,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
   if constexpr (CG == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_at;
+  previous_done();
 
   // (the status first: who learns of a tile that this CTA could not finish learns of it too)
   auto gave_up = [&] {
@@ -716,6 +733,24 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     return true;
   };
 
+  auto wait_cluster = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const long long from = clock64();
+    while (!bar_try_cluster(bar, parity)) {
+      if (*off != 0) return false;
+      if (clock64() - from > 4 * kWaitCycles) {   // (as long as what the other CTA may be waiting for)
+        gave_up();
+        return false;
+      }
+    }
+    return true;
+  };
+  // The queue's readers: waits for the next number; tells that it has been read (one thread of a reader).
+  auto take = [&](int q, uint32_t bit, int* i) -> bool {
+    if (!wait_cluster(q_full + q, bit)) return false;
+    *i = *reinterpret_cast<volatile int*>(q_tile + q);
+    return true;
+  };
+  auto taken = [&](int q) { bar_arrive_cluster(CG == 2 ? at_rank(shared_at(q_empty + q), 0) : shared_at(q_empty + q)); };
   // Waits until `need` tiles of matrix `at` are done (each of a tile's warps counts).
   auto wait_done = [&](int at, int need) -> bool {
     const unsigned* const counter = a.done + at;
@@ -740,10 +775,29 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     bool ok = true;
     Place w{0, 0, 0};
     Tile t;
+    int q = 0;
+    uint32_t q_bit = 0;
     if (warp == 0 && lane == 0) {
       // ---- copies
       int known_at = -1, known = 0;
-      for (int i = first; ok && next_tile(i, &w, &t); i += step) {
+      int mine = rank == 0 ? static_cast<int>(atomicAdd(a.ticket, 1u)) : 0;
+      for (;;) {
+        int i = mine;
+        if (rank == 0) {
+          if (!(ok = wait(q_empty + q, q_bit ^ 1))) break;
+          q_tile[q] = i;
+          bar_arrive(q_full + q);
+          if constexpr (CG == 2) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(shared_at(q_tile + q), 1)), "r"(i) : "memory");
+            bar_arrive_release(at_rank(shared_at(q_full + q), 1));
+          }
+        } else {
+          if (!(ok = take(q, q_bit, &i))) break;
+        }
+        const bool more = next_tile(i, &w, &t);
+        if (rank != 0) taken(q);
+        if (++q == kQueue) q = 0, q_bit ^= 1;
+        if (!more) break;
         const Matrix& m = mat[w.at];
         const int kind = phase[w.phase].kind, za = phase[w.phase].a, zb = phase[w.phase].b;
         const bool both = kind == kPoly || kind == kMul;   // both factors are symmetric
@@ -764,6 +818,8 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           if (rank == 0) bar_expect(full + stage, S::kStage * CG);
           if constexpr (CG == 2) bar = at_rank(bar, 0);
           const int k = kb * kBlockK;
+          // (the next number is there when this tile's copies have been asked for)
+          if (rank == 0 && kb == max(0, blocks - 8)) mine = static_cast<int>(atomicAdd(a.ticket, 1u));
           if (a.stall == 0) {
             // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
             const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (both && k < t.n0 / kRows * kRows);
@@ -776,6 +832,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           }
           if (++stage == STAGES) stage = 0, phase_bit ^= 1;
         }
+        if (!ok) break;
       }
       for (int i = 0; ok && i < STAGES; ++i) {   // the products' last arrivals have to find the barriers there
         ok = wait(empty + stage, phase_bit ^ 1);
@@ -785,7 +842,13 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     if (warp == 1 && lane == 0 && rank == 0) {
       // ---- products
       constexpr uint32_t idesc = (1u << 4) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
-      for (int i = first; ok && next_tile(i, &w, &t); i += step) {
+      for (;;) {
+        int i;
+        if (!(ok = take(q, q_bit, &i))) break;
+        const bool more = next_tile(i, &w, &t);
+        taken(q);
+        if (++q == kQueue) q = 0, q_bit ^= 1;
+        if (!more) break;
         const Matrix& m = mat[w.at];
         const int kind = phase[w.phase].kind;
         const bool both = kind == kPoly || kind == kMul;
@@ -824,8 +887,16 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     p.ex = {exchange + (warp - 4) * kExchange, lane};
     float* const dj = columns + (warp - 4) * (BN / 2);
     Place w{0, 0, 0};
-    int known_at = -1, known = 0;
-    for (int i = first; next_tile(i, &w, &p.tile); i += step) {
+    int known_at = -1, known = 0, q = 0;
+    uint32_t q_bit = 0;
+    for (;;) {
+      int i;
+      const bool got = take(q, q_bit, &i);
+      if (__any_sync(0xffffffffu, !got)) break;
+      const bool more = next_tile(i, &w, &p.tile);
+      if (lane == 0) taken(q);
+      if (++q == kQueue) q = 0, q_bit ^= 1;
+      if (!more) break;
       // (all that is known before the wait is looked up before it)
       const Matrix m = mat[w.at];
       const Phase ph = phase[w.phase];
@@ -902,6 +973,18 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     }
   }
   __syncthreads();
+  if (*off != 0 && out != kUpdate) {
+    // Tiles may have been left: the results say so.
+    for (int k = 0; k < count; ++k) {
+      const int64_t n = static_cast<int64_t>(mat[k].m) * mat[k].n;
+      for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+        if (out == kBf16Out)
+          reinterpret_cast<__nv_bfloat16*>(mat[k].p)[i] = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+        else
+          mat[k].p[i] = __int_as_float(0x7fc00000);
+      }
+    }
+  }
   if constexpr (CG == 2) cluster_sync();
   if (warp == 2) tmem_free<CG>(tmem, kCols);
 }
@@ -999,7 +1082,7 @@ int32_t parts_of(int64_t m, int64_t n) {
   return static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
 }
 constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4;   // the status word, the tiles' counters; the sums' parts
-static_assert(4 + kMaxGroup * 4 <= 256, "status and counters");
+static_assert(4 + (kMaxGroup + 1) * 4 <= 256, "status, counters and the ticket");
 
 // Matrices are worked on in the order of their sizes, the longest sums first; a
 // group ends at so many matrices or values.
@@ -1141,7 +1224,8 @@ template <int CG, int BN, int STAGES, int COUNT>
 adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   using namespace meo::tc;
   auto* const kernel = k_muon_iterate<CG, BN, STAGES, COUNT>;
-  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + kMaxPhases * sizeof(Phase) + 8;
+  constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + kMaxPhases * sizeof(Phase) + 8 +
+                         kQueue * 20;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   IterateArgs<COUNT> a;
   std::memset(&a, 0, sizeof a);
@@ -1151,6 +1235,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   a.stall = t_stall ? 1 : 0;
   a.status = reinterpret_cast<int32_t*>(c.ws);
   a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
+  a.ticket = a.done + kMaxGroup;
   unsigned char* at = c.ws + kHead;
   int32_t sym = 0, app = 0;
   for (int i = 0; i < count; ++i) {
@@ -1192,27 +1277,20 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   cfg.stream = c.s;
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {CG, 1, 1};
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  // Clusters that can be there together, as the waits between tiles need: asked for once a device.
-  static std::atomic<int> together[64];
+  static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
   int device = 0, sms = 0;
   MUON_TRY(sm_count(&device, &sms), "current device");
-  int most = device < 64 ? together[device].load() : 0;
-  if (most == 0) {
+  const unsigned long long bit = device < 64 ? 1ull << device : 0;
+  if (bit == 0 || (ready.load() & bit) == 0) {
     MUON_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes), "k_muon_iterate");
-    most = sms;
-    if (CG > 1) {
-      cfg.gridDim = dim3(static_cast<unsigned>(sms / CG * CG));
-      MUON_TRY(cudaOccupancyMaxActiveClusters(&most, kernel, &cfg), "k_muon_iterate");
-    }
-    if (most < 1) return fail(ADAF_ERR_CUDA, "k_muon_iterate does not fit this device");
-    if (device < 64) together[device] = most;
+    ready.fetch_or(bit);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(most, std::max(sym, app)) * CG));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms / CG, std::max(sym, app)) * CG));
   MUON_TRY(g_profile.run(kSlotIterate, c.s, [&] { return cudaLaunchKernelEx(&cfg, kernel, a); }), "k_muon_iterate");
   return ADAF_OK;
 }

@@ -18,12 +18,23 @@ on the host; the header says how bad ones show in the results.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import binding as B
-from .losses import _DTYPES, _FP32, _INDEX, _context, _raw_stream, _rows, _strides, _written
+from .losses import _DTYPES, _FP32, _INDEX, _NO_ROWS, _context, _raw_stream, _rows, _strides, _written
+
+# The C structs, packed here in one step each, as in losses.py.
+_HIDDEN = struct.Struct("@Piqqqqq")
+_WEIGHT = struct.Struct("@Piqqi4x")
+_TARGETS = struct.Struct("@Pqqiq")
+_ARGS = struct.Struct("@Pqqddd")
+for _s, _c in ((_HIDDEN, B.linear_ce_hidden), (_WEIGHT, B.linear_ce_weight), (_TARGETS, B.loss_targets),
+               (_ARGS, B.linear_ce_args)):
+    assert _s.size == ctypes.sizeof(_c), _c.__name__
 
 
 class LinearCrossEntropy(NamedTuple):
@@ -37,26 +48,40 @@ class LinearCrossEntropy(NamedTuple):
 def _hidden(name, t, shape=None, device=None):
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
-    if t.dim() not in (2, 3):
+    size, st = t.shape, t.stride()
+    if len(size) == 3:
+        batch, sb = size[0], st[0]
+    elif len(size) == 2:
+        batch, sb = 1, 0
+    else:
         raise ValueError(f"{name} must be [tokens, dim] or [batch, seq, dim]")
-    if shape is not None and (t.shape != shape or t.get_device() != device):
+    if shape is not None and (size != shape or t.get_device() != device):
         raise ValueError(f"{name} must have the hidden states' shape and device")
-    if t.shape[-1] != 1 and t.stride(-1) != 1:
+    if st[-1] != 1 and size[-1] != 1:
         raise ValueError(f"{name}: the innermost stride must be 1")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    batch, sb = (t.shape[0], t.stride(0)) if t.dim() == 3 else (1, 0)
-    return B.linear_ce_hidden(t.data_ptr(), _DTYPES[t.dtype], batch, t.shape[-2], t.shape[-1], sb, t.stride(-2))
+    return _HIDDEN.pack(t.data_ptr(), _DTYPES[t.dtype], batch, size[-2], size[-1], sb, st[-2])
 
 
 def _weight(name, t, dim, device, vocab=None, accumulate=False):
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
-    if t.dim() != 2 or t.shape[1] != dim or t.get_device() != device or (vocab is not None and t.shape[0] != vocab):
+    size, st = t.shape, t.stride()
+    if len(size) != 2 or size[1] != dim or t.get_device() != device or (vocab is not None and size[0] != vocab):
         raise ValueError(f"{name} must be [{'vocab' if vocab is None else vocab}, {dim}] on the hidden states' device")
-    if dim != 1 and t.stride(1) != 1:
+    if st[1] != 1 and dim != 1:
         raise ValueError(f"{name}: the innermost stride must be 1")
-    return B.linear_ce_weight(t.data_ptr(), _DTYPES[t.dtype], t.shape[0], t.stride(0), 1 if accumulate else 0)
+    return _WEIGHT.pack(t.data_ptr(), _DTYPES[t.dtype], size[0], st[0], 1 if accumulate else 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(tokens, dim, hidden_type, vocab, weight_type, stride, aligned, grad_hidden, grad_weight):
+    """Bytes of workspace by what they depend on; grad_hidden, grad_weight: types, or None."""
+    h = _HIDDEN.pack(0, hidden_type, 1, tokens, dim, 0, dim)
+    w = _WEIGHT.pack(0 if aligned else 8, weight_type, vocab, stride, 0)
+    return B.linear_ce_workspace_size(h, w, None if grad_hidden is None else _HIDDEN.pack(0, grad_hidden, 1, tokens, dim, 0, dim),
+                                      None if grad_weight is None else _WEIGHT.pack(0, grad_weight, vocab, dim, 0))
 
 
 def linear_cross_entropy(hidden, weight, targets, *, weights=None, z_loss: float = 0.0, temperature: float = 1.0,
@@ -92,9 +117,8 @@ def linear_cross_entropy(hidden, weight, targets, *, weights=None, z_loss: float
         raise ValueError("targets must be an int32 or int64 tensor")
     if targets.shape != shape or targets.get_device() != dev:
         raise ValueError(f"targets must have shape {list(shape)} on the hidden states' device")
-    y = B.loss_targets(B.loss_rows(targets.data_ptr(), *_strides(targets, shape)), code, ignore_index)
-    rows = B.loss_rows(*((None, 0, 0) if weights is None else _rows("weights", weights, shape, dev)))
-    args = B.linear_ce_args(rows, temperature, z_loss, grad_scale)
+    y = _TARGETS.pack(targets.data_ptr(), *_strides(targets, shape), code, ignore_index)
+    args = _ARGS.pack(*(_NO_ROWS if weights is None else _rows("weights", weights, shape, dev)), temperature, z_loss, grad_scale)
     if accumulate and grad_weight is None:
         raise ValueError("accumulate needs grad_weight")
     device = hidden.device
@@ -112,9 +136,11 @@ def linear_cross_entropy(hidden, weight, targets, *, weights=None, z_loss: float
     loss = torch.empty((), dtype=_FP32, device=device)
     logp = torch.empty(shape, dtype=_FP32, device=device)
     lse = torch.empty(shape, dtype=_FP32, device=device)
-    n = B.linear_ce_workspace_size(h, w, gh, gw)
+    n = _workspace_bytes(shape.numel(), dim, _DTYPES[hidden.dtype], weight.shape[0], _DTYPES[weight.dtype], weight.stride(0),
+                         weight.data_ptr() % 16 == 0, None if gh is None else _DTYPES[grad_hidden.dtype],
+                         None if gw is None else _DTYPES[grad_weight.dtype])
     ws = torch.empty(n, dtype=torch.uint8, device=device)
-    B.linear_ce(h, w, ctypes.byref(y), ctypes.byref(args), gh, gw, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(),
+    B.linear_ce(h, w, y, args, gh, gw, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(),
                 ws.data_ptr(), n, _raw_stream(dev))
     _written(given_h)
     _written(given_w)

@@ -12,6 +12,7 @@ leading index, as it is for the factored steps: the experts of a layer.
 """
 from __future__ import annotations
 
+import functools
 from typing import Iterable, Optional, Sequence
 
 import torch
@@ -196,11 +197,16 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS,
             out = torch.empty(x.shape, dtype=dtype, device=x.device)
         elif out.shape != x.shape or out.device != x.device or not out.is_contiguous():
             raise ValueError("out must be contiguous, with x's shape and device")
-        n = B.muon_orthogonalize_workspace_size(batch, rows, cols)
+        n = _workspace_bytes(batch, rows, cols)
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
         B.muon_orthogonalize(B.muon_matrices(_ptr(x), _DTYPES[x.dtype], batch, rows, cols, stride_b, flat.stride(-2)), it,
                              _ptr(out), _DTYPES[dtype], _ptr(ws), n, int(torch.cuda.current_stream(x.device).cuda_stream))
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(batch, rows, cols):
+    return B.muon_orthogonalize_workspace_size(batch, rows, cols)
 
 
 _iterations: dict = {}

@@ -38,7 +38,7 @@ def call(h=None, w=None, y=None, gh=None, gw=None, loss=F, logp=F, lse=F, ws=WS,
     gh, gw = gh or hidden(p=GH), gw or weight(p=GW)
     y = B.loss_targets(B.loss_rows(*(y or (Y, 6, 1))), ydt, -100)
     args = B.linear_ce_args(B.loss_rows(*rows), t, z, scale)
-    B.linear_ce(h, w, ctypes.byref(y), ctypes.byref(args), gh, gw, loss, logp, lse, ws,
+    B.linear_ce(h, w, y, args, gh, gw, loss, logp, lse, ws,
                 B.linear_ce_workspace_size(h, w, gh, gw) if n is None else n, 0)
 
 
@@ -96,7 +96,7 @@ def test_rows_that_reach_too_far_are_refused(lib):
     h, args = hidden(ss=1 << 38, seq=1 << 20, batch=1), B.linear_ce_args(B.loss_rows(None, 0, 0), 1.0, 0.0, 1.0)
     y = B.loss_targets(B.loss_rows(Y, 0, 1), B.LOSS_INT64, -100)
     with pytest.raises(ValueError, match="reach"):
-        B.linear_ce(h, weight(), ctypes.byref(y), ctypes.byref(args), None, None, F, None, None, WS, 1 << 40, 0)
+        B.linear_ce(h, weight(), y, args, None, None, F, None, None, WS, 1 << 40, 0)
 
 
 def test_null_structs_refused(lib):
