@@ -732,7 +732,6 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
     }
     return true;
   };
-
   auto wait_cluster = [&](uint64_t* bar, uint32_t parity) -> bool {
     const long long from = clock64();
     while (!bar_try_cluster(bar, parity)) {
@@ -917,6 +916,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       if (w.at != known_at || w.need > known) {
         bool done = true;
         if (lane == 0) done = wait_done(w.at, w.need);
+        __syncwarp();   // (what lane 0 has seen, all have)
         p.bad = __any_sync(0xffffffffu, !done) || p.bad;
         known_at = w.at;
         known = w.need;

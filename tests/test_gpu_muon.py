@@ -242,6 +242,26 @@ def test_equal_bits_and_other_streams():
     assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_beside_other_work():
+    """Several calls and other kernels at once: whichever SMs a call gets, and however few at first, its bits are the same."""
+    x, x2 = normal((5, 700, 1500), 1).cuda(), normal((200, 3000), 2).cuda().bfloat16()
+    h, w = normal((3000, 256), 3).cuda().bfloat16(), normal((9000, 256), 4).cuda().bfloat16() / 16
+    y = torch.randint(0, 9000, (3000,), device="cuda")
+    big = normal((4096, 4096), 5).cuda()
+    alone = meo.orthogonalize(x), meo.orthogonalize(x2), meo.linear_cross_entropy(h, w, y)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(streams[3]):
+            other = big @ big
+        a = meo.orthogonalize(x, stream=streams[0])
+        c = meo.linear_cross_entropy(h, w, y, stream=streams[2])
+        b = meo.orthogonalize(x2, stream=streams[1])
+        torch.cuda.synchronize()
+        assert torch.equal(a, alone[0]) and torch.equal(b, alone[1]) and all(torch.equal(p, q) for p, q in zip(c, alone[2]))
+        del other
+
+
 def test_captured_and_replayed():
     shapes = [(40, 64), (64, 40), (3, 200, 150)]
     params = [normal(s, k).cuda() for k, s in enumerate(shapes)]
