@@ -927,9 +927,11 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       } else if (ph.kind == kApply) {
         Ahead<8, BN / 64> x;
         x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
-        const float factor = diagonal_of(ph.a);
+        float factor = diagonal_of(ph.a);
         const int32_t status = *reinterpret_cast<const volatile int32_t*>(a.status);
         arrived();
+        // (what a tile that was not finished has gone into: NaN, also where another CTA's NaNs came first)
+        if (p.bad || status != 0) factor = __int_as_float(0x7fc00000);
         if (ph.last == 0)
           end_next(m, p, x, ph.b, factor, ph.c0);
         else if (out != kUpdate || (!p.bad && status == 0))   // (otherwise p stays as it is)

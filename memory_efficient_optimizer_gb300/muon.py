@@ -260,7 +260,7 @@ class Muon(torch.optim.Optimizer):
                     self.state[p].update(init_muon_state([p])[0])
             grads = [p.grad for p in ps]
             states = [self.state[p] for p in ps]
-            key = (gi, tuple(p.data_ptr() for p in ps), tuple(g.data_ptr() for g in grads),
+            key = (gi, tuple((p.data_ptr(), p.shape) for p in ps), tuple(g.data_ptr() for g in grads),
                    tuple(st["momentum"].data_ptr() for st in states), repr(sorted(hp.items())))
             if torch.cuda.is_current_stream_capturing():
                 # memory of a graph's own pool is not kept for calls outside it

@@ -336,6 +336,21 @@ def test_optimizer_keeps_one_workspace():
     assert not any(torch.equal(p, b) for p, b in zip(ps, before)) and all(p.isfinite().all() for p in ps)
 
 
+def test_optimizer_after_a_change_of_shape():
+    """The same memory as a matrix of another shape: another step."""
+    p, g = torch.nn.Parameter(normal((40, 60), 1).cuda()), normal((40, 60), 2).cuda()
+    opt = meo.Muon([p], lr=0.1, momentum=0.0)
+    p.grad = g
+    opt.step()
+    p.grad = None
+    p.data = p.data.view(30, 80)
+    p.grad = g.view(30, 80)
+    twin = p.detach().clone()
+    meo.muon_step([twin], [p.grad], meo.init_muon_state([twin]), lr=0.1, momentum=0.0)
+    opt.step()
+    assert torch.equal(p.detach(), twin)
+
+
 def test_a_copy_that_never_lands_ends_the_call():
     """A wait runs out: the call ends by itself, the status says so, the parameters stay."""
     p = normal((100, 300), 1).cuda()
