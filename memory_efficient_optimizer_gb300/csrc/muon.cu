@@ -62,6 +62,12 @@ constexpr int64_t kGroupValues = int64_t{1} << 28;  // their values, unless one 
 constexpr int kMaxParts = 256;                     // of a matrix's sum of squares
 constexpr int kPartValues = 8192;                  // values of a part, at least
 constexpr int64_t kMaxSide = int64_t{1} << 20;
+// x x^T of few wide matrices is summed in parts, so many tiles of them at most: one round of the SMs.
+// A part has ten stages or more (3 us); to write and join the parts takes 2 to 4 us.  64 x 20000 took
+// 570 us in one sum, 163 in 16 parts; 1024 x 4096 304, 256 in 4; 16 x 2688 127, 91 in 4.  In parts of 8
+// stages 2 x 1024 x 1024 took 193 us instead of 184.
+constexpr int kPartTiles = 144, kMostParts = 16, kPartStages = 10;
+constexpr int kMaxJoined = kPartTiles / 2 * meo::tc::kEndWarps;   // counters of the tiles' warps
 constexpr int64_t kMaxMatrices = int64_t{1} << 20;
 
 enum Flag : int32_t { kTurned = 1, kBf16 = 2 };   // x is u^T; u is bf16
@@ -85,6 +91,7 @@ struct MuonArgs {
   float* part;                     // [parts of all matrices]
   int32_t* status;
   unsigned* done;
+  unsigned* joined;
   int32_t clear;                   // this launch clears the status word
   Item item[kMaxGroup];
 };
@@ -139,6 +146,7 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
   if (blockIdx.x == 0) {
     if (a.clear != 0 && threadIdx.x == 0) *a.status = 0;
     if (threadIdx.x < kMaxGroup + 1) a.done[threadIdx.x] = 0;   // (and the ticket behind them)
+    for (int i = threadIdx.x; i < kMaxJoined; i += 256) a.joined[i] = 0;
   }
   const Item& t = a.item[owner(a.count, blockIdx.x, [&](int i) { return a.item[i].part0; })];
   const bool bf16 = t.flags & kBf16;
@@ -305,6 +313,9 @@ struct Matrix {
   int32_t flags;
   float rate;            // p = keep p - rate o
   int32_t sym0, app0;    // its first tile of the symmetric products and of the others
+  int32_t splits, gram0; // parts of the sums of x x^T; its first tile of those
+  float* parts;          // [tiles][splits][warps][32 rows x BN / 2 columns in the lanes' order]
+  unsigned* joined;      // [tiles][warps]: parts that are there
 };
 
 enum Out : int32_t { kUpdate, kFp32, kBf16Out };
@@ -369,13 +380,14 @@ __device__ __forceinline__ void clear_diagonal(const Part& p, uint4 (&w)[4]) {
   }
 }
 
-// A = x x^T = D + F.
-__device__ __forceinline__ void end_gram(const Matrix& t, const Part& p) {
+// A = x x^T = D + F.  load(c, v): 32 columns of the sums.
+template <class Load>
+__device__ __forceinline__ void end_gram(const Matrix& t, const Part& p, Load&& load) {
 #pragma unroll 1
   for (int c = 0; c < p.cols && p.col + c < p.m; c += 32) {
     const int j0 = p.col + c;
     float v[32];
-    p.load(c, v);   // A 2^30
+    load(c, v);   // A 2^30
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= 0x1p-16f;
     uint4 w[4];
@@ -387,6 +399,47 @@ __device__ __forceinline__ void end_gram(const Matrix& t, const Part& p) {
     }
     store_symmetric(t, p, j0, 0, w);
   }
+}
+
+// The same where the sums are in parts: the warp's part is written out, and the warp that brings the
+// last one adds them up in their order.  Whether that is this one; `warp`: of the tile's.
+template <int COLS>
+__device__ __forceinline__ bool end_gram_part(const Matrix& t, const Part& p, int warp) {
+  constexpr int kWords = COLS / 4 * 32;   // of 16 bytes, a warp's part
+  const int at = p.tile.batch * meo::tc::kEndWarps + warp;
+  const bool rows = p.row0() < p.m;
+  float4* const first = reinterpret_cast<float4*>(t.parts) + (static_cast<int64_t>(p.tile.batch) * t.splits * meo::tc::kEndWarps + warp) * kWords + p.ex.lane;
+  constexpr int64_t kNext = meo::tc::kEndWarps * kWords;
+#pragma unroll
+  for (int c = 0; c < COLS; c += 32) {
+    float v[32];
+    p.load(c, v);
+    if (rows && p.col + c < p.m) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) first[p.tile.split * kNext + c * 8 + 32 * i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+  }
+  __syncwarp();
+  unsigned before = 0;
+  if (p.ex.lane == 0) {
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(t.joined + at) : "memory");
+    if (before + 1 == static_cast<unsigned>(t.splits)) t.joined[at] = 0;   // (for the next step, which waits for this one)
+  }
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before + 1 != static_cast<unsigned>(t.splits)) return false;
+  end_gram(t, p, [&](int c, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    if (!rows) return;
+#pragma unroll 2
+    for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = __ldcg(first + s * kNext + c * 8 + 32 * i);
+        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+      }
+  });
+  return true;
 }
 
 // What an ending reads beside the sums.  It is asked for before the sums are there: behind the
@@ -640,8 +693,8 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Ph
   }
   const Phase& ph = phase[w->phase];
   i -= ph.start;
-  const bool sym = ph.kind != kApply;
-  while (w->at + 1 < count && i >= (sym ? mat[w->at + 1].sym0 : mat[w->at + 1].app0)) ++w->at;
+  const bool sym = ph.kind != kApply, gram = ph.kind == kGram;
+  while (w->at + 1 < count && i >= (gram ? mat[w->at + 1].gram0 : sym ? mat[w->at + 1].sym0 : mat[w->at + 1].app0)) ++w->at;
   const Matrix& m = mat[w->at];
   meo::tc::Shape s{};
   s.batch = 1;
@@ -652,6 +705,14 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Ph
   const int mtn = (m.m + BN - 1) / BN;   // column tiles of the symmetric products
   const int syms = static_cast<int>(meo::tc::sym_tiles<kRows / BN>(mtn));
   w->need = ph.syms * syms + ph.apps * mt * nt;
+  if (gram) {   // (batch: the tile's number)
+    i -= m.gram0;
+    const int tile = CG == 1 ? i / m.splits : i;
+    const bool there = meo::tc::tile_of<true, kRows, BN>(tile, mt, mtn, s, t);
+    t->batch = tile;
+    t->split = i - tile * (CG == 1 ? m.splits : 1);
+    return there;
+  }
   if (sym) return meo::tc::tile_of<true, kRows, BN>(i - m.sym0, mt, mtn, s, t);
   return meo::tc::tile_of<false, kRows, BN>(i - m.app0, mt, nt, s, t);
 }
@@ -766,6 +827,13 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       }
     }
   };
+  // The stages of a part of a sum (every part has some: there are kPartStages times as many or more).
+  auto part_of = [&](const Matrix& m, int kind, const Tile& t, int* b0, int* b1) {
+    if (CG > 1 || kind != kGram || m.splits == 1) return;
+    const int blocks = *b1;
+    *b0 = blocks * t.split / m.splits;
+    *b1 = blocks * (t.split + 1) / m.splits;
+  };
   auto next_tile = [&](int i, Place* w, Tile* t) { return find_tile<CG, BN>(mat, count, phase, phases, tiles, i, w, t); };
   if (warp < 4) {
     fewer_registers();
@@ -802,7 +870,8 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
         const bool both = kind == kPoly || kind == kMul;   // both factors are symmetric
         const CUtensorMap* const map_a = kind == kGram ? &a.map[w.at].x : &a.map[w.at].s;
         const CUtensorMap* const map_b = both ? &a.map[w.at].s : &a.map[w.at].x;
-        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        int b0 = 0, b1 = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        part_of(m, kind, t, &b0, &b1);
         const int am = t.m0 + static_cast<int>(rank) * kTileM, bn = t.n0 + static_cast<int>(rank) * kBCta;
         if (w.at != known_at || w.need > known) {
           if (!(ok = wait_done(w.at, w.need))) break;
@@ -810,7 +879,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           known = w.need;
           asm volatile("fence.proxy.async;" ::: "memory");
         }
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = b0; kb < b1; ++kb) {
           if (!(ok = wait(empty + stage, phase_bit ^ 1))) break;
           const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
           uint32_t bar = shared_at(full + stage);
@@ -818,7 +887,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           if constexpr (CG == 2) bar = at_rank(bar, 0);
           const int k = kb * kBlockK;
           // (the next number is there when this tile's copies have been asked for)
-          if (rank == 0 && kb == max(0, blocks - 8)) mine = static_cast<int>(atomicAdd(a.ticket, 1u));
+          if (rank == 0 && kb == max(b0, b1 - 8)) mine = static_cast<int>(atomicAdd(a.ticket, 1u));
           if (a.stall == 0) {
             // of a symmetric factor, what lies below its diagonal tile is read from above, transposed
             const bool ta = kind != kGram && k < t.m0, tb = kind == kApply || (both && k < t.n0 / kRows * kRows);
@@ -851,10 +920,11 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
         const Matrix& m = mat[w.at];
         const int kind = phase[w.phase].kind;
         const bool both = kind == kPoly || kind == kMul;
-        const int blocks = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        int b0 = 0, b1 = ((kind == kGram ? m.n : m.m) + kBlockK - 1) / kBlockK;
+        part_of(m, kind, t, &b0, &b1);
         if (!(ok = wait(sum_empty + acc, acc_bit ^ 1))) break;
         fence_after();
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int kb = b0; kb < b1; ++kb) {
           if (!(ok = wait(full + stage, phase_bit))) break;
           fence_after();
           const uint32_t pa = shared_at(ring + stage * S::kStage), pb = pa + S::kA;
@@ -864,7 +934,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
           const uint32_t form = idesc | ((ta ? 1u : 0u) << 15) | ((tb ? 1u : 0u) << 16);
 #pragma unroll
           for (int j = 0; j < kBlockK / 16; ++j)
-            mma<CG>(tmem + acc * BN, operand(pa + j * a_step, a_lbo, 1024), operand(pb + j * b_step, b_lbo, 1024), form, kb > 0 || j > 0);
+            mma<CG>(tmem + acc * BN, operand(pa + j * a_step, a_lbo, 1024), operand(pb + j * b_step, b_lbo, 1024), form, kb > b0 || j > 0);
           commit<CG>(empty + stage);
           if (++stage == STAGES) stage = 0, phase_bit ^= 1;
         }
@@ -921,9 +991,13 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
         known_at = w.at;
         known = w.need;
       }
+      bool done = true;
       if (ph.kind == kGram) {
         arrived();
-        end_gram(m, p);
+        if (CG == 1 && m.splits > 1)
+          done = end_gram_part<BN / 2>(m, p, warp - 4);
+        else
+          end_gram(m, p, [&](int c, float (&v)[32]) { p.load(c, v); });
       } else if (ph.kind == kApply) {
         Ahead<8, BN / 64> x;
         x.fetch(p, m.xb + block_at(p.row0(), p.col, p.n), p.row0() < p.m, p.n - p.col);
@@ -961,7 +1035,7 @@ __global__ void __launch_bounds__(meo::tc::kThreads, 1) k_muon_iterate(const __g
       __syncwarp();
       if (lane == 0) {
         bar_arrive_cluster(CG == 2 ? at_rank(shared_at(sum_empty + acc), 0) : shared_at(sum_empty + acc));
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.done + w.at) : "memory");
+        if (done) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.done + w.at) : "memory");
       }
       if (++acc == 2) acc = 0, acc_bit ^= 1;
     }
@@ -1083,7 +1157,7 @@ Layout layout(int64_t m, int64_t n) {
 int32_t parts_of(int64_t m, int64_t n) {
   return static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
 }
-constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4;   // the status word, the tiles' counters; the sums' parts
+constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4 + (kMaxJoined * 4 + 255) / 256 * 256;   // the status word, the tiles' counters; the sums' parts; x x^T's
 static_assert(4 + (kMaxGroup + 1) * 4 <= 256, "status, counters and the ticket");
 
 // Matrices are worked on in the order of their sizes, the longest sums first; a
@@ -1107,8 +1181,31 @@ struct Order {
     return apart && wide(x) != wide(y) ? wide(x) : x > y;
   }
 };
+// In how many parts x x^T of a matrix is summed, if it were alone; of `tiles` tiles of all matrices.
+int64_t parts_alone(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(kMostParts, (n + 63) / 64 / kPartStages)); }
+int64_t gram_parts(int64_t n, int64_t tiles) {
+  return 2 * tiles > kPartTiles ? 1 : std::min(parts_alone(n), kPartTiles / tiles);
+}
+// Bytes of the parts of a group, at most, in tiles of 128 x 128 and of 128 x 64.
+struct GramParts {
+  int64_t tiles[2] = {0, 0}, parts[2] = {0, 0};
+  void add(const Size& z) {
+    const int64_t of[2] = {meo::tc::sym_tiles<1>((z.second + 127) / 128), meo::tc::sym_tiles<2>((z.second + 63) / 64)};
+    for (int k = 0; k < 2; ++k) {
+      tiles[k] += of[k];
+      if (parts_alone(z.first) > 1) parts[k] += of[k] * parts_alone(z.first);
+    }
+  }
+  size_t bytes() const {
+    size_t most = 0;
+    for (int k = 0; k < 2; ++k)
+      if (2 * tiles[k] <= kPartTiles) most = std::max(most, static_cast<size_t>(std::min<int64_t>(parts[k], kPartTiles)) * (128 * (k == 0 ? 128 : 64) * 4));
+    return most;
+  }
+};
 struct Grouping {
   const Order* order;
+  GramParts parts;
   int64_t count = 0, values = 0;
   size_t bytes = kHead, most = 0;
   bool first_wide = false;
@@ -1117,12 +1214,13 @@ struct Grouping {
     return count == kMaxGroup || (count > 0 && (values + z.first * z.second > kGroupValues || (order->apart && wide(z) != first_wide)));
   }
   void add(const Size& z) {
-    if (full(z)) count = values = 0, bytes = kHead;
+    if (full(z)) count = values = 0, bytes = kHead, parts = GramParts{};
     if (count == 0) first_wide = wide(z);
     ++count;
     values += z.first * z.second;
     bytes += layout(z.second, z.first).bytes;
-    most = std::max(most, bytes);
+    parts.add(z);
+    most = std::max(most, bytes + parts.bytes());
   }
 };
 size_t bytes_of(std::vector<std::pair<Size, int64_t>>& sizes) {
@@ -1193,13 +1291,14 @@ bool pair_fits(const muon_iteration& it) {
   return most <= 15.5;
 }
 
-// The phases of a call; sym, app: tiles of all matrices in a symmetric product and in one with x.
-int phases_of(const muon_iteration& it, bool pair, int64_t sym, int64_t app, Phase* phase, int32_t* tiles) {
+// The phases of a call; gram, sym, app: tiles of all matrices in x x^T (its parts), in another
+// symmetric product and in one with x.
+int phases_of(const muon_iteration& it, bool pair, int64_t gram, int64_t sym, int64_t app, Phase* phase, int32_t* tiles) {
   int n = 0, x = 0;
   int32_t at = 0, syms = 0, apps = 0;
   auto add = [&](int kind, int a, int b, int out, double c0, double c1, double c2, bool last) {
     phase[n++] = {kind, a, b, out, static_cast<float>(c0), static_cast<float>(c1), static_cast<float>(c2), at, syms, apps, last ? 1 : 0};
-    at += static_cast<int32_t>(kind == kApply ? app : sym);
+    at += static_cast<int32_t>(kind == kApply ? app : kind == kGram ? gram : sym);
     ++(kind == kApply ? apps : syms);
   };
   auto poly = [&](int k, int in, int out) { add(kPoly, in, in, out, it.coef[k][0], it.coef[k][1], it.coef[k][2], false); };
@@ -1239,7 +1338,10 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
   a.ticket = a.done + kMaxGroup;
   unsigned char* at = c.ws + kHead;
-  int32_t sym = 0, app = 0;
+  int32_t gram = 0, sym = 0, app = 0;
+  int64_t grams = 0;   // tiles of x x^T
+  constexpr int kRows = kTileM * CG;
+  for (int i = 0; i < count; ++i) grams += sym_tiles<kRows / BN>((mats[i].m + BN - 1) / BN);
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
     const Layout L = layout(z.m, z.n);
@@ -1264,14 +1366,27 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
     if (!make_map(&a.map[i].x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
         !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, kSlabs, z.m * m.lda, 64))
       return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    constexpr int kRows = kTileM * CG;
     const int64_t mt = (z.m + kRows - 1) / kRows, nt = (z.n + BN - 1) / BN;
+    const int32_t own = static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
     m.sym0 = sym;
     m.app0 = app;
-    sym += static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
+    m.gram0 = gram;
+    m.splits = CG == 1 ? static_cast<int32_t>(gram_parts(z.n, grams)) : 1;
+    sym += own;
     app += static_cast<int32_t>(mt * nt);
+    gram += own * m.splits;
   }
-  a.phases = phases_of(*c.it, pair, sym, app, a.phase, &a.tiles);
+  unsigned* joined = reinterpret_cast<unsigned*>(c.ws + kHead) - kMaxJoined;
+  for (int i = 0; i < count; ++i) {
+    Matrix& m = a.mat[i];
+    if (m.splits == 1) continue;
+    const int64_t own = sym_tiles<kRows / BN>((m.m + BN - 1) / BN);
+    m.parts = reinterpret_cast<float*>(at);
+    m.joined = joined;
+    at += own * m.splits * (kTileM * BN * 4);
+    joined += own * kEndWarps;
+  }
+  a.phases = phases_of(*c.it, pair, gram, sym, app, a.phase, &a.tiles);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.blockDim = dim3(kThreads);
@@ -1292,7 +1407,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
     MUON_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes), "k_muon_iterate");
     ready.fetch_or(bit);
   }
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms / CG, std::max(sym, app)) * CG));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms / CG, std::max(gram, app)) * CG));
   MUON_TRY(g_profile.run(kSlotIterate, c.s, [&] { return cudaLaunchKernelEx(&cfg, kernel, a); }), "k_muon_iterate");
   return ADAF_OK;
 }
@@ -1311,6 +1426,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, 
   a.status = reinterpret_cast<int32_t*>(c.ws);
   a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
   a.part = reinterpret_cast<float*>(c.ws + 256);
+  a.joined = reinterpret_cast<unsigned*>(c.ws + kHead) - kMaxJoined;
   a.clear = first ? 1 : 0;
   unsigned char* at = c.ws + kHead;
   int32_t parts = 0, tiles = 0;

@@ -122,6 +122,47 @@ def test_a_list_of_wide_and_square_matrices():
         assert far(moved, want) < TOL + 1e-3
 
 
+@pytest.mark.parametrize("shape", [(1, 1279), (1, 1280), (1, 10301), (16, 2688), (6400, 63), (64, 20000), (65, 1281), (129, 2600),
+                                   (2, 200, 7001), (13, 16, 3584), (300, 16001), (1024, 1920), (1025, 4100), (72, 40, 1300),
+                                   (73, 40, 1300)])
+def test_long_sums_in_parts(shape):
+    """x x^T of few wide matrices is summed in parts, which are joined in their order: equal bits."""
+    x = normal(shape, 4).cuda()
+    out = meo.orthogonalize(x, dtype=torch.float32)
+    assert far(out, on_gpu(x)) < TOL
+    for _ in range(3):
+        assert torch.equal(out, meo.orthogonalize(x, dtype=torch.float32))
+
+
+def test_a_list_with_sums_in_parts_and_in_one():
+    shapes = [(64, 9000), (40, 60), (3, 16, 1400), (700, 130), (2000, 100), (256, 256), (1, 5000)]
+    params = [normal(s, k).cuda() for k, s in enumerate(shapes)]
+    grads = [normal(s, 20 + k).cuda() for k, s in enumerate(shapes)]
+    before = [p.clone() for p in params]
+    meo.muon_step(params, grads, meo.init_muon_state(params), lr=1.0, momentum=0.0)
+    for p, b, g in zip(params, before, grads):
+        want = on_gpu(g) * max(1.0, g.shape[-2] / g.shape[-1]) ** 0.5
+        # (the difference has p's own rounding too: 2^-24 of a normal value, and the update is 1 / sqrt(n) or more)
+        assert far(b - p, want) < TOL + 2e-5
+    many = [normal((64, 9000), k).cuda() for k in range(50)]   # two launches, with one workspace
+    apart = [meo.orthogonalize(m, dtype=torch.float32) for m in many]
+    zero = [torch.zeros_like(m) for m in many]
+    meo.muon_step(zero, many, meo.init_muon_state(zero), lr=1.0, momentum=0.0)
+    for z, o in zip(zero, apart):
+        assert far(-z, o.double().cpu().numpy()) < 2 * TOL
+
+
+def test_values_of_sums_in_parts():
+    x = normal((3, 32, 4000), 1).cuda()
+    want = on_gpu(x)
+    x[1, 3, 3999] = float("nan")
+    out = meo.orthogonalize(x, dtype=torch.float32)
+    assert out[1].isnan().all() and far(out[::2], want[::2]) < TOL
+    x[1] = 0
+    out = meo.orthogonalize(x, dtype=torch.float32)
+    assert out[1].eq(0).all() and far(out[::2], want[::2]) < TOL
+
+
 def test_rows_with_gaps_and_views():
     base = normal((3, 70, 100), 7).cuda()
     for x in (base[:, :, :90], base[:, 3:40], base[1:], base[:, :1], base[:, ::2, 10:63]):
@@ -368,3 +409,15 @@ def test_a_copy_that_never_lands_ends_the_call():
     step()
     torch.cuda.synchronize()
     assert step.device_status() == 0 and not torch.equal(p, before) and p.isfinite().all()
+
+
+def test_a_copy_that_never_lands_in_a_sum_in_parts():
+    x = normal((70, 3000), 1).cuda()
+    B.muon_debug_stall_copies(True)
+    try:
+        out = meo.orthogonalize(x, steps=1)
+        torch.cuda.synchronize()
+    finally:
+        B.muon_debug_stall_copies(False)
+    assert out.isnan().all()
+    assert far(meo.orthogonalize(x, dtype=torch.float32), on_gpu(x)) < TOL
