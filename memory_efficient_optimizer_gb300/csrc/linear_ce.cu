@@ -248,18 +248,34 @@ __global__ void __launch_bounds__(128) k_lce_gather(const CeArgs a) {
   }
 }
 
-// The weight in bf16 with rows of a multiple of 8 values.
+// The weight in bf16 with rows of a multiple of 8 values, 8 values a thread.  Rows whose values lie at
+// any place are read value by value, eight of a thread's under way together: 85456 x 949 in bf16 59 us
+// (5.5 TB/s; 154 with one at a time), 32000 x 4096 in fp32 118 (6.7 TB/s).
 __global__ void __launch_bounds__(256) k_lce_weight(const void* w, int32_t bf16, int64_t stride, int32_t vocab, int32_t dim, int32_t ld,
                                                     __nv_bfloat16* to) {
   meo::tc::next_may_begin();
   meo::tc::previous_done();
-  for (int v = blockIdx.x; v < vocab; v += gridDim.x) {
-    const int64_t at = v * stride;
-    for (int k = threadIdx.x; k < ld; k += 256) {
-      float x = 0.f;
-      if (k < dim) x = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at + k]) : static_cast<const float*>(w)[at + k];
-      to[static_cast<int64_t>(v) * ld + k] = __float2bfloat16_rn(x);
+  const int across = ld >> 3;
+  const int64_t vecs = static_cast<int64_t>(vocab) * across;
+  const bool wide = bf16 == 0 && stride % 4 == 0 && reinterpret_cast<uintptr_t>(w) % 16 == 0;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < vecs; i += gridDim.x * 256) {
+    // (a division of 64 bits takes as long as the copy)
+    const int64_t v = i >> 32 == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(across) : i / across;
+    const int k = static_cast<int>(i - v * across) * 8, left = dim - k;
+    const int64_t at = v * stride + k;
+    float x[8];
+    if (wide && left >= 8) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at) + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else if (bf16 != 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < left ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at + e]) : 0.f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = e < left ? static_cast<const float*>(w)[at + e] : 0.f;
     }
+    reinterpret_cast<uint4*>(to)[i] = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
   }
 }
 
@@ -907,7 +923,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (P.packed && tokens > 0) {
     wp = ws + P.w;
     LCE_TRY(g_profile.run(kSlotWeight, s, [&] {
-      return launch_early(k_lce_weight, dim3(static_cast<unsigned>(std::min<int64_t>(w.vocab, 152 * 8))), 256, s, w.p,
+      return launch_early(k_lce_weight, dim3(static_cast<unsigned>(std::min<int64_t>((w.vocab * (P.ldw >> 3) + 255) / 256, 152 * 8))), 256, s, w.p,
                           static_cast<int32_t>(w.dtype == ADAF_BFLOAT16), w.stride_v, a.vocab, a.dim, static_cast<int32_t>(P.ldw),
                           reinterpret_cast<__nv_bfloat16*>(ws + P.w));
     }), "k_lce_weight");
