@@ -1166,7 +1166,8 @@ using Size = std::pair<int64_t, int64_t>;   // n, m
 int64_t tiles_256(const Size& z) { return meo::tc::sym_tiles<1>((z.second + 255) / 256); }
 // Matrices whose first two steps are worth taking at once, at least twice as wide as high: 4096 x
 // 14336 has 13 % fewer flops then, 1024 x 4096 14 %, 4096 x 4096 3 % more.  They make groups of their
-// own where their products fill the SMs (a list of small matrices is better off in one launch).
+// own where their products fill the SMs (a list of small matrices is better off in one launch; from
+// 30 tiles on 2048 x 8192 would gain 7 %, 4 x 1024 x 2048 lose as much).
 bool wide(const Size& z) { return z.first >= 2 * z.second && z.second >= 1024; }
 constexpr int64_t kFullTiles = 64;
 struct Order {
@@ -1412,6 +1413,32 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   return ADAF_OK;
 }
 
+// About how many microseconds a step takes with tiles of `side` x `side` on `slots` SMs or pairs of
+// them: stages of a tile, each bound by its copies, and its way from and to the tiles around it.  The
+// constants are measured; of tiles of 128 and 256 it chooses the faster, or one 3 % behind, for
+// 1024 x 4096 (258 us, 281), 2048 x 2048 (335, 295), 2048 x 8192 (814, 710), 4 x 1024 x 1024 (208, 219),
+// 3 x 1024 x 4096 (430, 379), 1536 x 1536 (227, 238), 5 x 700 x 900 (205, 212), 10 x 512 x 2048 (300, 285).
+double step_time(const Listed* mats, int count, int64_t side, int slots, double stage, double ending) {
+  const auto cut = [](int64_t x, int64_t by) { return (x + by - 1) / by; };
+  int64_t grams = 0;
+  for (int i = 0; i < count; ++i) grams += meo::tc::sym_tiles<1>(cut(mats[i].m, side));
+  double sum[3] = {0, 0, 0}, most[3] = {0, 0, 0};
+  for (int i = 0; i < count; ++i) {
+    const int64_t m = mats[i].m, n = mats[i].n, sym = meo::tc::sym_tiles<1>(cut(m, side));
+    const int64_t parts = side == 128 ? gram_parts(n, grams) : 1;
+    const double tiles[3] = {static_cast<double>(sym * parts), static_cast<double>(sym), static_cast<double>(cut(m, side) * cut(n, side))};
+    const double one[3] = {static_cast<double>(cut(cut(n, 64), parts)) * stage + ending + (parts > 1 ? 3.0 : 0.0),
+                           static_cast<double>(cut(m, 64)) * stage + ending, static_cast<double>(cut(m, 64)) * stage + ending};
+    for (int k = 0; k < 3; ++k) {
+      sum[k] += tiles[k] * one[k];
+      most[k] = std::max(most[k], one[k]);
+    }
+  }
+  double time = 0;
+  for (int k = 0; k < 3; ++k) time += std::max(sum[k] / slots, most[k]);
+  return time;
+}
+
 template <bool STEP>
 adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, bool apart) {
   MuonArgs a;
@@ -1461,18 +1488,17 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, 
   MUON_TRY(g_profile.run(kSlotPack, c.s, [&] {
     return meo::tc::launch_early(k_muon_pack<STEP>, dim3(static_cast<unsigned>(tiles)), 256, c.s, a);
   }), "k_muon_pack");
-  if (big >= kFullTiles) {
-    // (a group's matrices are all wide, or none is)
-    const bool pair = apart && wide({mats[0].n, mats[0].m}) && pair_fits(*c.it);
-    return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count, pair) : iterate<2, 256, 6, kMaxGroup>(c, mats, count, pair);
-  }
+  int device = 0, sms = 0;
+  MUON_TRY(meo::tc::sm_count(&device, &sms), "current device");
+  // (a group's matrices are all wide, or none is)
+  const bool pair = apart && big >= kFullTiles && wide({mats[0].n, mats[0].m}) && pair_fits(*c.it);
   // Narrow tiles where each of them has an SM: half as much to load and to write out a tile, for
   // 256 x 512 102 us to 115, six matrices of 256 x 256 to 1024 126 to 140; 1403 x 777, where two
   // rounds would be needed, 198 to 175.
-  int device = 0, sms = 0;
-  MUON_TRY(meo::tc::sm_count(&device, &sms), "current device");
-  if (2 * small > sms) return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count, false) : iterate<1, 128, 6, kMaxGroup>(c, mats, count, false);
-  return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count, false) : iterate<1, 64, 8, kMaxGroup>(c, mats, count, false);
+  if (!pair && 2 * small <= sms) return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count, false) : iterate<1, 64, 8, kMaxGroup>(c, mats, count, false);
+  if (!pair && step_time(mats, count, 128, sms, 0.29, 1.5) < step_time(mats, count, 256, sms / 2, 0.27, 3.5))
+    return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count, false) : iterate<1, 128, 6, kMaxGroup>(c, mats, count, false);
+  return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count, pair) : iterate<2, 256, 6, kMaxGroup>(c, mats, count, pair);
 }
 
 template <bool STEP>
