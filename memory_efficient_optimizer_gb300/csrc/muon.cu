@@ -33,7 +33,7 @@
 // bf16 ones 1e-2 to 9e-2.
 //
 // What bounds it: the tensor cores under the power cap, for matrices from about
-// 2000 on (a decoder layer of 218 M values: 11.1 ms, 1330 TFLOP/s of the 3 m^2 n +
+// 2000 on (a decoder layer of 218 M values: 10.9 ms, 1340 TFLOP/s of the 3 m^2 n +
 // m^3 flops a step that are left when the symmetric A and B are computed by one
 // half); L2 where m is about 1000; the way from one phase to the next, 5 to 6 us,
 // for small ones.
