@@ -758,7 +758,7 @@ Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_
   P.lde = round_up(w.vocab, 64);
   P.spans = (w.vocab + kSpan - 1) / kSpan;
   P.rows = std::min(P.room, std::max<int64_t>(256, kPieceBytes / (P.lde * 2) / 256 * 256));
-  P.pieces = (P.tokens + P.rows - 1) / P.rows;
+  P.pieces = P.rows > 0 ? (P.tokens + P.rows - 1) / P.rows : 0;   // (no tokens, no rows)
   // (a single row's stride says nothing)
   P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || (w.vocab > 1 && w.stride_v % 8 != 0);
   P.ldw = P.packed || w.vocab == 1 ? P.ldh : w.stride_v;

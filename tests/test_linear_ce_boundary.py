@@ -121,3 +121,16 @@ def test_front_end_refuses_on_the_host():
                       ((torch.zeros(8, 4).t(), w, y), "innermost"), ((None, w, y), "float32 or bfloat16")):
         with pytest.raises(ValueError, match=msg):
             L.linear_cross_entropy(*args)
+
+
+@pytest.mark.parametrize("empty", [dict(batch=0), dict(seq=0)])
+@pytest.mark.parametrize("gh,gw", [(False, False), (True, False), (False, True), (True, True)])
+def test_without_tokens(lib, empty, gh, gw):
+    """A batch without tokens has a workspace too, and is refused one that is too small."""
+    h, w = hidden(**empty), weight()
+    gh, gw = hidden(p=GH, **empty) if gh else None, weight(p=GW) if gw else None
+    n = B.linear_ce_workspace_size(h, w, gh, gw)
+    assert 256 <= n < B.linear_ce_workspace_size(hidden(), w, gh and hidden(p=GH), gw)
+    y, args = B.loss_targets(B.loss_rows(Y, 6, 1), B.LOSS_INT64, -100), B.linear_ce_args(B.loss_rows(None, 0, 0), 1.0, 0.0, 1.0)
+    with pytest.raises(B.AdafactorError, match="workspace"):
+        B.linear_ce(h, w, y, args, gh, gw, F, F, F, WS, n - 1, 0)
