@@ -85,25 +85,34 @@ class MuonStep:
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], states: Sequence[dict], lr=1e-3,
                  momentum=0.95, nesterov=True, weight_decay=0.0, adjust_lr="original", steps=5,
                  coefficients=COEFFICIENTS, eps=1e-7, workspace: Optional[torch.Tensor] = None):
+        self._hp = make_muon_hparams(lr, momentum, nesterov, weight_decay, adjust_lr, steps, coefficients, eps)
+        self._shapes = None
+        self._take(params, grads, states)
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
+                                      or workspace.device != self.device or workspace.numel() < self.workspace_bytes):
+            workspace = None
+        if workspace is None and self.n:
+            workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
+        self.workspace = workspace
+
+    def _take(self, params, grads, states) -> None:
+        """Checks the tensors and puts them into the descriptor array."""
         params, grads, states = list(params), list(grads), list(states)
         if len(params) != len(grads) or len(params) != len(states):
             raise ValueError("params, grads and states must have the same length")
-        self._hp = make_muon_hparams(lr, momentum, nesterov, weight_decay, adjust_lr, steps, coefficients, eps)
-        self.params, self.grads, self.states = params, grads, states
         n = len(params)
-        self.n = n
-        self.device = params[0].device if n else None
-        self._tensors = (B.muon_tensor * max(1, n))()
+        device = params[0].device if n else None
+        tensors = (B.muon_tensor * max(1, n))()
         for k, (p, g, st) in enumerate(zip(params, grads, states)):
             if not isinstance(p, torch.Tensor) or p.dtype != torch.float32:
                 raise ValueError(f"tensor {k}: params must be float32 tensors")
             if p.dim() < 2:
                 raise ValueError(f"tensor {k}: Muon steps matrices (two dimensions or more); give this one to another step")
-            if p.device.type != "cuda" or g.device != p.device or p.device != self.device:
+            if p.device.type != "cuda" or g.device != p.device or p.device != device:
                 raise ValueError(f"tensor {k}: params and grads must be CUDA tensors on one device")
             if g.dtype not in _DTYPES:
                 raise ValueError(f"tensor {k}: grad dtype must be float32 or bfloat16")
-            if tuple(g.shape) != tuple(p.shape):
+            if g.shape != p.shape:
                 raise ValueError(f"tensor {k}: grad shape {tuple(g.shape)} != param shape {tuple(p.shape)}")
             if not p.is_contiguous() or not g.is_contiguous():
                 raise ValueError(f"tensor {k}: params and grads must be contiguous")
@@ -112,14 +121,13 @@ class MuonStep:
                     and m.is_contiguous() and m.numel() == p.numel()):
                 raise ValueError(f"tensor {k}: state 'momentum' must be contiguous float32 with {p.numel()} elements on "
                                  "the param's device")
-            self._tensors[k] = B.muon_tensor(_ptr(p), _ptr(g), _DTYPES[g.dtype], *_matrices(p.shape), _ptr(m))
-        self.workspace_bytes = B.muon_workspace_size(self._tensors, n) if n else 0
-        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()
-                                      or workspace.device != self.device or workspace.numel() < self.workspace_bytes):
-            workspace = None
-        if workspace is None and n:
-            workspace = torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
-        self.workspace = workspace
+            tensors[k] = B.muon_tensor(_ptr(p), _ptr(g), _DTYPES[g.dtype], *_matrices(p.shape), _ptr(m))
+        self.params, self.grads, self.states = params, grads, states
+        self.n, self.device, self._tensors = n, device, tensors
+        shapes = [p.shape for p in params]
+        if shapes != self._shapes:
+            self.workspace_bytes = B.muon_workspace_size(tensors, n) if n else 0
+            self._shapes = shapes
 
     def __call__(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         if self.n == 0:
@@ -260,22 +268,39 @@ class Muon(torch.optim.Optimizer):
                     self.state[p].update(init_muon_state([p])[0])
             grads = [p.grad for p in ps]
             states = [self.state[p] for p in ps]
-            key = (gi, tuple((p.data_ptr(), p.shape) for p in ps), tuple(g.data_ptr() for g in grads),
-                   tuple(st["momentum"].data_ptr() for st in states), repr(sorted(hp.items())))
             if torch.cuda.is_current_stream_capturing():
                 # memory of a graph's own pool is not kept for calls outside it
                 MuonStep(ps, grads, states, **hp)()
                 continue
-            plan = self._plans.get(key)
+            # A group's plan stays; the tensors are checked and put into it anew at every step (gradients
+            # come and go, on other memory or in another form), and it does not keep them.
+            plan, values = self._plans.get(gi), repr(sorted(hp.items()))
             if plan is None:
-                kept = self._workspaces.get(ps[0].device)
-                plan = MuonStep(ps, grads, states, workspace=kept, **hp)
-                if len(self._plans) > 16 or (kept is not None and plan.workspace is not kept):
-                    self._plans.clear()
-                self._workspaces[ps[0].device] = plan.workspace
-                self._plans[key] = plan
-            plan()
+                plan = MuonStep(ps, grads, states, workspace=self._workspaces.get(ps[0].device), **hp)
+                self._plans[gi] = plan
+            else:
+                plan._take(ps, grads, states)
+                if values != plan.values:
+                    plan._hp = make_muon_hparams(**hp)
+            plan.values = values
+            self._share_workspace(plan)
+            try:
+                plan()
+            finally:
+                plan.params, plan.grads, plan.states = [], [], []
         return loss
+
+    def _share_workspace(self, plan) -> None:
+        """One workspace for all plans of a device, as large as the largest of them needs."""
+        kept = self._workspaces.get(plan.device)
+        if kept is None or kept.numel() < plan.workspace_bytes:
+            kept = plan.workspace
+            if kept is None or kept.numel() < plan.workspace_bytes:
+                kept = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=plan.device)
+            self._workspaces[plan.device] = kept
+        for other in self._plans.values():
+            if other.device == plan.device:
+                other.workspace = kept
 
 
 __all__ = ["Muon", "MuonStep", "muon_step", "init_muon_state", "make_muon_hparams", "orthogonalize"]
