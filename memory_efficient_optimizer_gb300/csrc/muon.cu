@@ -88,7 +88,7 @@ struct MuonArgs {
   int32_t count;
   int64_t stride_r;                // of u
   float mu, nesterov_mu, eps;      // u = g + nesterov_mu m, or m itself (nesterov_mu < 0)
-  float* part;                     // [parts of all matrices]
+  float2* part;                    // [parts of all matrices]: the sums of u^2 and of (2^80 u)^2
   int32_t* status;
   unsigned* done;
   unsigned* joined;
@@ -118,6 +118,24 @@ __device__ __forceinline__ float4 four_at(const void* u, bool bf16, int64_t i) {
   const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
   const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
   return make_float4(a.x, a.y, b.x, b.y);
+}
+// The squares of values below 1e-19 or so are no longer normal fp32 numbers, or 0.  So the squares of 2^80 u
+// are summed beside those of u, and count where the latter's sum is below kSmallSum (what is lost of that
+// sum's terms is then below 2^-78 of it).
+constexpr float kUp = 0x1p80f, kSmallSum = 0x1p-40f, kSmallEps = 0x1p-20f;
+__device__ __forceinline__ float2 squares(float v) {
+  const float w = v * kUp;
+  return make_float2(v * v, w * w);
+}
+__device__ __forceinline__ void add_four(float2& sum, const float4& v) {
+  const float2 x = squares(v.x), y = squares(v.y), z = squares(v.z), w = squares(v.w);
+  sum.x += (x.x + y.x) + (z.x + w.x);
+  sum.y += (x.y + y.y) + (z.y + w.y);
+}
+__device__ __forceinline__ void add_one(float2& sum, float v) {
+  const float2 x = squares(v);
+  sum.x += x.x;
+  sum.y += x.y;
 }
 __device__ __forceinline__ float update_of(float g, float m, const MuonArgs& a) {
   return a.nesterov_mu < 0.f ? m : fmaf(a.nesterov_mu, m, g);
@@ -157,7 +175,7 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
   const int64_t numel = static_cast<int64_t>(t.rows) * cols;
   const int64_t per = ((numel + t.parts - 1) / t.parts + 3) & ~int64_t{3};
   const int64_t e0 = per * (blockIdx.x - t.part0), e1 = min(numel, e0 + per);
-  float sum = 0.f;
+  float2 sum = make_float2(0.f, 0.f);
   if (flat) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(u) % (bf16 ? 8 : 16) | (STEP ? reinterpret_cast<uintptr_t>(mom) % 16 : 0);
     int64_t tail = e0;
@@ -176,7 +194,7 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
           *reinterpret_cast<float4*>(mom + i) = m;
           v = make_float4(update_of(v.x, m.x, a), update_of(v.y, m.y, a), update_of(v.z, m.z, a), update_of(v.w, m.w, a));
         }
-        sum += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
+        add_four(sum, v);
       }
     }
     for (int64_t i = tail + threadIdx.x; i < e1; i += 256) {
@@ -186,16 +204,16 @@ __global__ void __launch_bounds__(256) k_muon_moment(const __grid_constant__ Muo
         mom[i] = m;
         v = update_of(v, m, a);
       }
-      sum += v * v;
+      add_one(sum, v);
     }
   } else {
     for (int64_t i = e0 + threadIdx.x; i < e1; i += 256) {
       const int r = static_cast<int>(i / cols), c = static_cast<int>(i - static_cast<int64_t>(r) * cols);
-      const float v = value_at(u, bf16, r * a.stride_r + c);
-      sum += v * v;
+      add_one(sum, value_at(u, bf16, r * a.stride_r + c));
     }
   }
-  sum = block_sum(sum, scratch);
+  sum.x = block_sum(sum.x, scratch);
+  sum.y = block_sum(sum.y, scratch);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
 }
 
@@ -218,10 +236,13 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonA
   const int rows = t.m, cols = t.n, ldx = t.ldx;
   const int across = (cols + 63) >> 6, at_tile = blockIdx.x - t.tile0;
   const int by = at_tile / across, bx = at_tile - by * across;
-  const float sum = block_sum(static_cast<int>(threadIdx.x) < t.parts ? a.part[t.part0 + threadIdx.x] : 0.f, scratch);
-  const float norm = sqrtf(sum);
+  const float2 part = static_cast<int>(threadIdx.x) < t.parts ? a.part[t.part0 + threadIdx.x] : make_float2(0.f, 0.f);
+  const float sum = block_sum(part.x, scratch), sum_up = block_sum(part.y, scratch);
+  // (both sides times 2^80; an eps above the norm needs none of it)
+  const bool small = sum < kSmallSum && a.eps < kSmallEps;
+  const float up = small ? kUp : 1.f, norm = sqrtf(small ? sum_up : sum);
   // (a norm that is not finite makes x NaN)
-  const float scale = norm <= FLT_MAX ? 32768.f / fmaxf(norm, a.eps) : __int_as_float(0x7fc00000);
+  const float scale = norm <= FLT_MAX ? 32768.f / fmaxf(norm, a.eps * up) : __int_as_float(0x7fc00000);
   const bool bf16 = t.flags & kBf16, turned = t.flags & kTurned;
   const void* const u = t.u;
   const float* const mom = t.mom;
@@ -245,7 +266,7 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonA
     for (int i = 0; i < 4; ++i) {
       float* const to = &tile[(threadIdx.x >> 4) + 16 * i][(threadIdx.x & 15) * 4];
       if (STEP) v[i] = make_float4(update_of(v[i].x, m[i].x, a), update_of(v[i].y, m[i].y, a), update_of(v[i].z, m[i].z, a), update_of(v[i].w, m[i].w, a));
-      to[0] = v[i].x * scale, to[1] = v[i].y * scale, to[2] = v[i].z * scale, to[3] = v[i].w * scale;
+      to[0] = v[i].x * up * scale, to[1] = v[i].y * up * scale, to[2] = v[i].z * up * scale, to[3] = v[i].w * up * scale;
     }
   } else {
     for (int i = threadIdx.x; i < 64 * 64; i += 256) {
@@ -255,7 +276,7 @@ __global__ void __launch_bounds__(256) k_muon_pack(const __grid_constant__ MuonA
         const int64_t at = r * pitch + c;
         v = value_at(u, bf16, at);
         if (STEP) v = update_of(v, mom[at], a);
-        v *= scale;
+        v = v * up * scale;
       }
       tile[i >> 6][i & 63] = v;
     }
@@ -1157,7 +1178,7 @@ Layout layout(int64_t m, int64_t n) {
 int32_t parts_of(int64_t m, int64_t n) {
   return static_cast<int32_t>(std::min<int64_t>(kMaxParts, (m * n + kPartValues - 1) / kPartValues));
 }
-constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 4 + (kMaxJoined * 4 + 255) / 256 * 256;   // the status word, the tiles' counters; the sums' parts; x x^T's
+constexpr size_t kHead = 256 + kMaxGroup * kMaxParts * 8 + (kMaxJoined * 4 + 255) / 256 * 256;   // the status word, the tiles' counters; the sums' parts; x x^T's
 static_assert(4 + (kMaxGroup + 1) * 4 <= 256, "status, counters and the ticket");
 
 // Matrices are worked on in the order of their sizes, the longest sums first; a
@@ -1452,7 +1473,7 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, 
   }
   a.status = reinterpret_cast<int32_t*>(c.ws);
   a.done = reinterpret_cast<unsigned*>(c.ws) + 1;
-  a.part = reinterpret_cast<float*>(c.ws + 256);
+  a.part = reinterpret_cast<float2*>(c.ws + 256);
   a.joined = reinterpret_cast<unsigned*>(c.ws + kHead) - kMaxJoined;
   a.clear = first ? 1 : 0;
   unsigned char* at = c.ws + kHead;
