@@ -446,6 +446,7 @@ __device__ __forceinline__ bool end_gram_part(const Matrix& t, const Part& p, in
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(t.joined + at) : "memory");
     if (before + 1 == static_cast<unsigned>(t.splits)) t.joined[at] = 0;   // (for the next step, which waits for this one)
   }
+  __syncwarp();   // (what lane 0 has acquired, all have: the other warps' parts)
   before = __shfl_sync(0xffffffffu, before, 0);
   if (before + 1 != static_cast<unsigned>(t.splits)) return false;
   end_gram(t, p, [&](int c, float (&v)[32]) {
