@@ -90,17 +90,27 @@ __device__ __forceinline__ bool bar_try(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Instructions that are ".aligned" are for a whole warp together: each of the functions that hold one begins
+// by bringing its lanes together, whatever branches and loops they come from.
+//
 // The endings' warps take registers over from the first four (at launch all have 168: 384
 // threads of 65536): 128 x 56 + 256 x 224 = 64512, what the block holds.  Each is
 // called by all warps of its kind at the head of their branch.
-__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
-__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void fewer_registers() {
+  __syncwarp();
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+}
+__device__ __forceinline__ void more_registers() {
+  __syncwarp();
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -115,6 +125,7 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
+  __syncwarp();
   if constexpr (CG == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_at(where)), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -125,6 +136,7 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
 }
 template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {
+  __syncwarp();
   if constexpr (CG == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
   else
@@ -155,6 +167,7 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 // 32 columns of the warp's 32 lanes (rows).
 __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
+  __syncwarp();
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -172,6 +185,7 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
 
 // 64 columns, both halves under way together.
 __device__ __forceinline__ void tmem_load64(uint32_t at, float (&v)[32], float (&w)[32]) {
+  __syncwarp();
   uint32_t r[32], q[32];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -191,6 +205,7 @@ __device__ __forceinline__ void tmem_load64(uint32_t at, float (&v)[32], float (
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]), w[i] = __uint_as_float(q[i]);
 }
 __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+  __syncwarp();
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
