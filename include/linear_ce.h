@@ -15,14 +15,16 @@
  * gradients are 0.
  *
  * Pieces.  Tokens are worked on in pieces of so many that 16 bits for each of
- * their words take 2 GB (8192 tokens of 128256 words): exp(z[j] - m) relative to
+ * their words take 2 GB (8192 tokens of 128256 words), 65536 tokens at most: exp(z[j] - m) relative to
  * a power of two of 128 words' own, which the second pass over it turns into dx
  * in bf16.  The weight's gradient over several pieces is summed in fp32.
  *
  * Types.  Hidden states and weight are bf16, or fp32, which are rounded to bf16
  * first (as under autocast); gradients have the type asked for.  exp and sums
  * are fp32; dx is rounded to bf16 once before the gradients' products, whose
- * sums are fp32 and are rounded once.
+ * sums are fp32 and are rounded once.  The tensor cores cut a sum off at each
+ * of its steps, so a gradient that one token or word makes most of comes out up
+ * to 3e-4 of itself smaller in fp32, however many tokens and words there are.
  *
  * Values.  A token with a target outside the vocabulary answers NaN (logp, the
  * loss, its hidden gradient and the weight's), and so does one with NaN or

@@ -60,6 +60,13 @@ constexpr int kSpan = 128;                          // words of one I and s
 // values take 5 % longer, 2.5 % parts of 1024.)
 constexpr int kSumStages = 16;
 constexpr double kCutOff = 0.54 / (1 << 25);
+// The gradients' sums are longer, and one that grows all the way loses more (products far below it lose
+// bits of their own): the gradient of a word that most of 2^21 tokens have as their target came out 7e-3
+// too small in one sum, those of tokens whose target comes first of 2^19 words 1.1e-3.  So a piece has at
+// most 2^16 tokens (2.0e-4), and the hidden gradient's sums go over 2^17 words at once (2.6e-4, in bf16
+// an eighth of what its rounding is).  Vocabularies of more words have an ending of their own that adds
+// up in registers (in one kernel with the usual one it cost every call 2.5 us, 1 % of 16 tokens' 220).
+constexpr int64_t kMostRows = int64_t{1} << 16, kMostWords = int64_t{1} << 17;
 constexpr int kScanThreads = 1024, kScanEach = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;                     // I of a span without words
@@ -512,17 +519,22 @@ __device__ __forceinline__ void store32(const Part& p, void* out, bool bf16, boo
   }
 }
 
+struct HiddenArgs {
+  const int32_t* token;     // of the piece
+  void* out;
+  int64_t sb, ss;
+  int32_t seq, bf16, wide;
+  float* parts;             // where sums are in several parts: [splits][rows that count][dim]
+  Factor factor;
+};
+// LONG: sums over more than kMostWords words.
+template <bool LONG>
 struct HiddenEnd {
-  static constexpr int kChunk = 0;
-  struct Args {
-    const int32_t* token;     // of the piece
-    void* out;
-    int64_t sb, ss;
-    int32_t seq, bf16, wide;
-    float* parts;             // where sums are in several parts: [splits][rows that count][dim]
-    Factor factor;
-  };
-  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+  static constexpr int kChunk = LONG ? static_cast<int>(kMostWords / meo::tc::kBlockK) : 0;
+  using Args = HiddenArgs;
+  // col32(c, v): 32 columns of the sums
+  template <class Columns>
+  static __device__ __forceinline__ void store(const Args& a, const Part& p, Columns&& col32) {
     const float f = a.factor.value();
     const bool parts = p.splits > 1;   // then summed by k_lce_join
     int64_t at[4];   // of the rows that this lane writes
@@ -534,7 +546,7 @@ struct HiddenEnd {
 #pragma unroll 1
     for (int c = 0; c < p.cols && p.col + c < p.n; c += 32) {
       float v[32];
-      p.load(c, v);
+      col32(c, v);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= f;
       const int j = p.col + c;
@@ -544,11 +556,24 @@ struct HiddenEnd {
         store32(p, a.out, a.bf16, a.wide, false, [&](int i) { return at[i] + j; }, p.n - j, v);
     }
   }
+  static __device__ __forceinline__ void part(const Args& a, const Part& p) {
+    store(a, p, [&](int c, float (&v)[32]) { p.load(c, v); });
+  }
+  static __device__ __forceinline__ void whole(const Args& a, const Part& p, float (&sum)[kSpan]) {
+    store(a, p, [&](int c, float (&v)[32]) {
+#pragma unroll
+      for (int k = 0; k < kSpan; k += 32)
+        if (c == k) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = sum[k + i];
+        }
+    });
+  }
 };
 
 // A token's hidden gradient from its parts, in their order.
 __global__ void __launch_bounds__(256) k_lce_join(int32_t dim, int32_t blocks, int32_t clusters, int64_t room, const int32_t* count,
-                                                  int32_t first, int32_t most, const HiddenEnd::Args o) {
+                                                  int32_t first, int32_t most, const HiddenArgs o) {
   meo::tc::next_may_begin();
   meo::tc::previous_done();
   const int rows = meo::tc::live(count, first, most);
@@ -757,7 +782,7 @@ Plan plan(const linear_ce_hidden& h, const linear_ce_weight& w, const linear_ce_
   P.ldh = round_up(h.dim, 8);
   P.lde = round_up(w.vocab, 64);
   P.spans = (w.vocab + kSpan - 1) / kSpan;
-  P.rows = std::min(P.room, std::max<int64_t>(256, kPieceBytes / (P.lde * 2) / 256 * 256));
+  P.rows = std::min({P.room, kMostRows, std::max<int64_t>(256, kPieceBytes / (P.lde * 2) / 256 * 256)});
   P.pieces = P.rows > 0 ? (P.tokens + P.rows - 1) / P.rows : 0;   // (no tokens, no rows)
   // (a single row's stride says nothing)
   P.packed = w.dtype != ADAF_BFLOAT16 || !aligned(w.p, 16) || (w.vocab > 1 && w.stride_v % 8 != 0);
@@ -975,7 +1000,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       if (!ok) return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
       const int64_t es = size_of(gh->dtype);
       const bool wide = aligned(gh->p, 16) && (h.batch == 1 || gh->stride_b * es % 16 == 0) && (h.seq == 1 || gh->stride_s * es % 16 == 0);
-      const HiddenEnd::Args end{a.token + a.first, gh->p, gh->stride_b, gh->stride_s, a.seq, a.g_bf16, wide,
+      const HiddenArgs end{a.token + a.first, gh->p, gh->stride_b, gh->stride_s, a.seq, a.g_bf16, wide,
                                 reinterpret_cast<float*>(ws + P.parts), factor};
       Shape x = shape;
       x.m = static_cast<int32_t>(rows);
@@ -985,8 +1010,10 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       x.split_room = P.split_room;
       x.group = 8;
       x.m_live = a.count;
-      LCE_TRY(g_profile.run(kSlotGradHidden, s, [&] { return launch_product<2, 256, 6, false, true, true, HiddenEnd>(e_k, w_n, x, end, s); }),
-              "k_lce_grad_hidden");
+      LCE_TRY(g_profile.run(kSlotGradHidden, s, [&] {
+        if (w.vocab > kMostWords) return launch_product<2, 256, 6, false, true, true, HiddenEnd<true>>(e_k, w_n, x, end, s);
+        return launch_product<2, 256, 6, false, true, true, HiddenEnd<false>>(e_k, w_n, x, end, s);
+      }), "k_lce_grad_hidden");
       int device = 0, sms = 0;
       LCE_TRY(sm_count(&device, &sms), "current device");
       const dim3 join(static_cast<unsigned>(std::min<int64_t>(rows, 1216)),

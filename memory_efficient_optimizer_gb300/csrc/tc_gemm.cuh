@@ -411,7 +411,7 @@ struct Shared {
 // or, with kChunk > 0, static __device__ void whole(const Args&, const Part&, float (&v)[BN / 2]):
 // the sums are taken out of tensor memory every kChunk stages and added up in registers.  The
 // tensor cores cut off what does not fit a sum's 24 bits, so a long sum is off toward zero by
-// 2^-25 of itself for each of its steps of 16 values; parts of 256 values leave next to nothing.
+// half of 2^-25 of itself and more for each of its steps of 16 values.
 template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
 __global__ void __launch_bounds__(kThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape given,

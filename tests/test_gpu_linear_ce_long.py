@@ -91,3 +91,67 @@ def test_long_sums_do_not_lean(dim):
     got = n64(out.logp) + n64(out.lse)
     want = (n64(h) * n64(w)[y.numpy()]).sum(1)
     assert abs(((got - want) * want).sum() / (want ** 2).sum()) < 3e-7
+
+
+# What sums of tensor memory may lose: a step cuts off at most 2^-24 or so of the sum as it is on the average of both
+# ends of a binade, and no sum has more than 2^17 values, 8192 steps: 8192 2^-24 = 4.9e-4 of a gradient, in its own direction.
+LEAN = 8192 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("vocab", [1 << 21, (1 << 20) + 77, 1 << 17])
+@pytest.mark.parametrize("weights", [False, True])
+def test_hidden_gradients_over_a_large_vocabulary(vocab, weights):
+    """The target comes first and makes most of the gradient; the other words follow in 131072 steps."""
+    n, dim = 70, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = (torch.randn(vocab, dim, device="cuda", generator=g) * 1.3 / dim ** 0.5).to(BF)
+    h = torch.randn(n, dim, device="cuda", generator=g).to(BF)
+    y = torch.arange(n, device="cuda") * 3 + torch.arange(n, device="cuda") % 2 * (vocab // 2)
+    share = torch.full((n,), 2.0 ** -6, device="cuda") if weights else None
+    out = meo.linear_cross_entropy(h, w, y, weights=share, grad_hidden=torch.empty(n, dim, device="cuda"))
+    dx = (h.double() @ w.double().T).softmax(1)
+    dx[torch.arange(n), y] -= 1
+    want = dx @ w.double() * (2.0 ** -6 if weights else 1 / n)
+    lean = ((out.grad_hidden.double() - want) * want).sum(1) / want.square().sum(1)
+    assert lean.abs().max() <= LEAN
+    assert (out.grad_hidden.double() - want).norm() <= 2.0 ** -8 * want.norm()
+
+
+@pytest.mark.parametrize("dt", [FP, BF])
+def test_weight_gradients_over_many_tokens(dt):
+    """2^21 tokens of a small vocabulary, whose hidden states have a mean."""
+    n, dim, vocab = (1 << 21) + 5, 16, 24
+    g = torch.Generator(device="cuda").manual_seed(6)
+    w = (torch.randn(vocab, dim, device="cuda", generator=g) / dim ** 0.5).to(BF)
+    h = (torch.randn(n, dim, device="cuda", generator=g) + 1).to(BF)
+    y = torch.randint(0, vocab, (n,), device="cuda", generator=g)
+    y[torch.rand(n, device="cuda", generator=g) < 0.8] = 0
+    out = meo.linear_cross_entropy(h, w, y, grad_weight=torch.empty(vocab, dim, device="cuda", dtype=dt))
+    want = torch.zeros(vocab, dim, device="cuda", dtype=torch.float64)
+    for a, b in zip(h.split(1 << 18), y.split(1 << 18)):
+        dx = (a.double() @ w.double().T).softmax(1)
+        dx[torch.arange(len(b)), b] -= 1
+        want += dx.T @ a.double() / n
+    # (a bf16 result is off by up to 2^-8 of each value, at random over a row)
+    off = LEAN + (2.0 ** -8 * 2 / dim ** 0.5 if dt == BF else 0)
+    assert abs(((out.grad_weight.double() - want)[0] * want[0]).sum() / want[0].square().sum()) <= off
+    assert (out.grad_weight.double() - want).norm() <= 2.0 ** -8 * want.norm()
+
+
+@pytest.mark.parametrize("vocab", [1 << 19, 128256])
+def test_hidden_gradients_in_one_sum_over_the_vocabulary(vocab):
+    """So many tiles that nothing is gained by sums in parts: one goes over all words, the target's first."""
+    n, dim, some = 2048, 4864, 32
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = torch.empty(vocab, dim, device="cuda", dtype=BF)
+    for c in w.split(1 << 16):
+        c.copy_(torch.randn(c.shape, device="cuda", generator=g) * 1.3 / dim ** 0.5)
+    h = torch.randn(n, dim, device="cuda", generator=g).to(BF)
+    y = torch.randint(0, 64, (n,), device="cuda", generator=g)
+    out = meo.linear_cross_entropy(h, w, y, grad_hidden=torch.empty(n, dim, device="cuda"))
+    dx = torch.cat([h[:some].double() @ c.double().T for c in w.split(1 << 16)], 1).softmax(1)
+    dx[torch.arange(some), y[:some]] -= 1
+    want = sum(d @ c.double() for d, c in zip(dx.split(1 << 16, 1), w.split(1 << 16))) / n
+    off = out.grad_hidden[:some].double() - want
+    assert (off * want).sum(1).div(want.square().sum(1)).abs().max() <= LEAN
+    assert off.norm() <= 2.0 ** -8 * want.norm()
