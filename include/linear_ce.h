@@ -27,8 +27,10 @@
  * to 3e-4 of itself smaller in fp32, however many tokens and words there are.
  *
  * Values.  A token with a target outside the vocabulary answers NaN (logp, the
- * loss, its hidden gradient and the weight's), and so does one with NaN or
- * infinite logits.  Equal inputs give equal bits.  Every call only launches
+ * loss, its hidden gradient and the weight's), and so does one with a logit of
+ * NaN or +inf, or with nothing but -inf.  A word of logit -inf has probability 0
+ * (the hidden gradient, a sum with 0 times its weight, is NaN where that is
+ * infinite; the loss of such a target is +inf).  Equal inputs give equal bits.  Every call only launches
  * kernels on the caller's stream: nothing is allocated on the device or waited
  * for, and it may be captured in a graph.  Every wait inside a kernel is
  * bounded; if one runs out, which no input brings about, the loss is NaN.

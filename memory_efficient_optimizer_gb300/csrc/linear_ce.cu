@@ -329,7 +329,7 @@ struct LogitsEnd {
       float some = 0.f;
 #pragma unroll
       for (int i = c; i < c + 32; ++i) {
-        // (a word beyond the vocabulary: -inf, and c_lo may be 0)
+        // (-inf stays -inf: c_lo is above 0)
         v[i] = i < left ? exp2_approx(fmaf(v[i], a.c_lo, fmaf(v[i], a.c_hi, shift))) : 0.f;
         some += v[i];
       }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
   }
   const float all = rest + own;
   const float log_s = log2f(all);
-  const float lse = kLn2 * (top + log_s);
+  const float lse = all > 0.f ? kLn2 * (top + log_s) : nan;   // (no word above -inf: no distribution)
   const float logp = y < 0 ? nan : own > rest ? -log1pf(rest / own) : kLn2 * (far - log_s);
   const float w = a.w.p != nullptr ? static_cast<const float*>(a.w.p)[place(t, a.seq, a.w.sb, a.w.ss)] : 1.f / static_cast<float>(n);
   if (threadIdx.x == 0) {
@@ -917,7 +917,9 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   a.spans = static_cast<int32_t>(P.spans);
   a.rows = static_cast<int32_t>(P.rows);
   const double c = 1.4426950408889634 * inv_t * (1.0 + kCutOff * static_cast<double>(std::min<int64_t>((h.dim + 15) / 16, kSumStages * 4)));
+  // c = c_hi + c_lo, rounded down: with c_lo above 0 a logit of -inf is -inf in both products
   a.c_hi = static_cast<float>(c);
+  if (static_cast<double>(a.c_hi) >= c) a.c_hi = std::nextafter(a.c_hi, 0.f);
   a.c_lo = static_cast<float>(c - static_cast<double>(a.c_hi));
   a.inv_t = static_cast<float>(inv_t);
   a.z_loss = static_cast<float>(args->z_loss);
