@@ -8,6 +8,7 @@
 //   k_lce_logits       x = h W^T.  The ending reduces a row's 128 words to a power of two 2^I >= their
 //                      largest exponential and s = sum 2^(x c - I) over the words but the target, and
 //                      keeps 2^(x c - I) in fp16 (c = log2(e) / T); the logits themselves are not kept
+//                      (for x c of millions: see kFar)
 //   k_lce_rows         a token's I and s over the vocabulary, its lse and logp, and dx in bf16 over
 //                      the exponentials: one read and one write of them
 //   k_lce_grad_hidden  dx W, in parts of the vocabulary where there are few tiles
@@ -69,7 +70,11 @@ constexpr double kCutOff = 0.54 / (1 << 25);
 constexpr int64_t kMostRows = int64_t{1} << 16, kMostWords = int64_t{1} << 17;
 constexpr int kScanThreads = 1024, kScanEach = 8;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1e30f;                     // I of a span without words
+constexpr float kNone = -FLT_MAX;                   // I of a span without words
+// From here on the whole number I (or 15 - I) and x c are too far apart for fp32: such a span's
+// exponentials are relative to 2^(top c) itself, top its largest logit, and (top, -s) is kept
+// of it in place of (I, s).
+constexpr float kFar = 4194304.f;
 constexpr int kIgnored = -1, kBad = -2;
 
 struct Rows {
@@ -322,7 +327,12 @@ struct LogitsEnd {
     }
     // (nothing but -inf or NaN leaves top at -inf: the sum is NaN or 0 then)
     const float I = top > -INFINITY ? ceilf(fmaf(top, a.c_hi, top * a.c_lo)) : kNone;
-    const float shift = 15.f - I;
+    const bool far = top > -INFINITY && fabsf(I) >= kFar;
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < kSpan; ++i) v[i] -= top;
+    }
+    const float shift = far ? 15.f : 15.f - I;
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < kSpan; c += 32) {
@@ -357,7 +367,7 @@ struct LogitsEnd {
                  (a.lde - p.col - c) * 2, w);
       }
     }
-    if (mine) a.stat[static_cast<int64_t>(p.row) * a.spans + p.col / kSpan] = make_float2(I, sum);
+    if (mine) a.stat[static_cast<int64_t>(p.row) * a.spans + p.col / kSpan] = far ? make_float2(top, -sum) : make_float2(I, sum);
   }
 };
 
@@ -366,10 +376,23 @@ __device__ __forceinline__ float power_of_two(float d) {   // 2^d for a whole d 
   return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
 }
 
+// What a row's exponentials are relative to: 2^top, or with far spans (kFar) maybe 2^(t c).
+struct Reference {
+  float top, t;
+  bool any, far;        // there are far spans; t counts
+  __device__ __forceinline__ float times(const CeArgs& a, float x, float less) const { return fmaf(x, a.c_lo, fmaf(x, a.c_hi, -less)); }
+  // A span's 2^I, or 2^(top c), over the row's.
+  __device__ __forceinline__ float scale(const CeArgs& a, const float2& s) const {
+    if (!any) return power_of_two(s.x - top);
+    if (!signbit(s.y)) return far ? exp2f(-times(a, t, s.x)) : power_of_two(s.x - top);
+    return exp2f(far ? times(a, s.x - t, 0.f) : times(a, s.x, top));
+  }
+};
+
 // A row a CTA: of 1024 threads where there are few rows (16 rows of 32000 words 5 us less).
 template <int kRowThreads>
 __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
-  __shared__ float s_max[kRowThreads / 32], s_sum[kRowThreads / 32];
+  __shared__ float s_max[kRowThreads / 32], s_far[kRowThreads / 32], s_sum[kRowThreads / 32];
   meo::tc::next_may_begin();
   meo::tc::previous_done();
   const int r = blockIdx.x;
@@ -384,18 +407,33 @@ __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
     return;
   }
   const float2* const stat = a.stat + static_cast<int64_t>(r) * a.spans;
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < a.spans; i += kRowThreads) top = fmaxf(top, stat[i].x);
+  Reference ref{-INFINITY, -INFINITY, false, false};
+  for (int i = threadIdx.x; i < a.spans; i += kRowThreads) {
+    const float2 s = stat[i];
+    float& most = signbit(s.y) ? ref.t : ref.top;
+    most = fmaxf(most, s.x);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_max[warp] = top;
+  for (int o = 16; o > 0; o >>= 1) {
+    ref.top = fmaxf(ref.top, __shfl_xor_sync(0xffffffffu, ref.top, o));
+    ref.t = fmaxf(ref.t, __shfl_xor_sync(0xffffffffu, ref.t, o));
+  }
+  if (lane == 0) {
+    s_max[warp] = ref.top;
+    s_far[warp] = ref.t;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kRowThreads / 32; ++w) top = fmaxf(top, s_max[w]);
+  for (int w = 0; w < kRowThreads / 32; ++w) {
+    ref.top = fmaxf(ref.top, s_max[w]);
+    ref.t = fmaxf(ref.t, s_far[w]);
+  }
+  ref.any = ref.t > -INFINITY;
+  ref.far = ref.any && ref.times(a, ref.t, 0.f) >= ref.top;
   float sum = 0.f;
   for (int i = threadIdx.x; i < a.spans; i += kRowThreads) {
     const float2 s = stat[i];
-    sum = fmaf(s.y, power_of_two(s.x - top), sum);
+    sum = fmaf(fabsf(s.y), ref.scale(a, s), sum);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -407,17 +445,18 @@ __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
 
   const int i = a.first + r, t = a.token[i], y = a.target[i];
   const float nan = __int_as_float(0x7fc00000);
-  // rest: the words without the target; own: the target (both over 2^top)
+  // rest: the words without the target; own: the target (both over the row's reference)
   const float rest = sum * 0x1p-15f;
   float own = 0.f, far = 0.f;
   if (y >= 0) {
     const float x = a.xt[r];
-    far = fmaf(x, a.c_lo, fmaf(x, a.c_hi, -top));
+    far = ref.far ? ref.times(a, x - ref.t, 0.f) : ref.times(a, x, ref.top);
     own = exp2f(far);
   }
   const float all = rest + own;
   const float log_s = log2f(all);
-  const float lse = all > 0.f ? kLn2 * (top + log_s) : nan;   // (no word above -inf: no distribution)
+  // (no word above -inf: no distribution)
+  const float lse = !(all > 0.f) ? nan : ref.far ? fmaf(kLn2 * ref.t, a.c_hi, kLn2 * log_s) : kLn2 * (ref.top + log_s);
   const float logp = y < 0 ? nan : own > rest ? -log1pf(rest / own) : kLn2 * (far - log_s);
   const float w = a.w.p != nullptr ? static_cast<const float*>(a.w.p)[place(t, a.seq, a.w.sb, a.w.ss)] : 1.f / static_cast<float>(n);
   if (threadIdx.x == 0) {
@@ -432,7 +471,7 @@ __global__ void __launch_bounds__(kRowThreads) k_lce_rows(const CeArgs a) {
   const float factor = y >= 0 ? d * (1.f + z) / (all * 32768.f) : nan;
   const float at_target = d * (z * own - rest) / all;
   for (int v = threadIdx.x; v < vecs; v += kRowThreads) {
-    const float f = factor * power_of_two(stat[v >> 4].x - top);
+    const float f = factor * (ref.any ? ref.scale(a, stat[v >> 4]) : power_of_two(stat[v >> 4].x - ref.top));
     const uint4 q = e[v];
     const uint32_t in[4] = {q.x, q.y, q.z, q.w};
     uint32_t out[4];

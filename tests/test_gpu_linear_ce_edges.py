@@ -67,3 +67,91 @@ def test_plus_infinity_and_nan_answer_nan(vocab):
                 out = meo.linear_cross_entropy(h, w, torch.full((4,), target, device="cuda"))
                 assert out.logp.isnan().all() and out.lse.isnan().all() and out.loss.isnan()
                 assert out.grad_hidden.isnan().all() and out.grad_weight.isnan().all()
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1e-3, 1e-5, 3e-6, 1e-6, 3e-7, 1e-7, 1e-9, 1e-20, 1e-30])
+def test_low_temperatures(temperature):
+    """Whole numbers, whose logits are exact, many of them alike: the largest share their probability at any temperature.
+
+    The logits' factor is off by 2^-25 and the tensor cores' mean, 2^-24 together, of a logarithm's size; an exponential
+    by 2^-22.  Gradients: a rounding to bf16 of the coefficient and of the result, 2^-8 each."""
+    n, dim, vocab = 60, 16, 300
+    g = torch.Generator().manual_seed(1)
+    h = torch.randint(-3, 4, (n, dim), generator=g).float()
+    w = torch.randint(-3, 4, (vocab, dim), generator=g).float()
+    w[130:260] = w[:130]                            # on both sides of a span of 128 words
+    z = h @ w.T
+    y = torch.where(torch.arange(n) % 3 > 0, z.argmax(1), torch.randint(0, vocab, (n,), generator=g))
+    out = meo.linear_cross_entropy(h.to(BF).cuda(), w.to(BF).cuda(), y.cuda(), temperature=temperature,
+                                   grad_hidden=torch.empty(n, dim, device="cuda"), grad_weight=torch.empty(vocab, dim, device="cuda"))
+    loss, gh, gw, logp, lse = O.linear_cross_entropy(n64(h), n64(w), y.numpy(), temperature=temperature)
+    for got, want in ((out.logp, logp), (out.lse, lse)):
+        assert np.all(np.abs(n64(got) - want) <= 2.0 ** -21 * (1 + np.abs(want)))
+    assert abs(out.loss.item() - loss) <= 2.0 ** -20 * (1 + abs(loss))
+    for got, want in ((out.grad_hidden, gh), (out.grad_weight, gw)):
+        assert np.linalg.norm(n64(got) - want) <= 2.0 ** -7 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("mask", [-3.3e38, -1e38, -1e30, -1e9, -1e7, -4e6, -2.9e6, -1e4])
+@pytest.mark.parametrize("temperature", [1.0, 0.5, 2.0])
+def test_masked_words_of_very_low_logits(mask, temperature):
+    """Words held down by a constant of the hidden states: alone in a span of 128 words, or beside others."""
+    n, dim, vocab = 30, 32, 400
+    g = torch.Generator().manual_seed(2)
+    h = torch.randn(n, dim, generator=g).to(BF)
+    h[:, 0] = 1
+    w = torch.randn(vocab, dim, generator=g).to(BF)
+    w[:, 0] = 0
+    w[128:256] = 0
+    w[128:256, 0] = mask
+    w[7, 0] = w[399, 0] = mask
+    y = torch.randint(0, 128, (n,), generator=g)
+    y[y == 7] = 8
+    y[3], y[4] = 140, 399
+    out = meo.linear_cross_entropy(h.cuda(), w.cuda(), y.cuda(), temperature=temperature)
+    loss, gh, gw, logp, lse = O.linear_cross_entropy(n64(h), n64(w), y.numpy(), temperature=temperature)
+    ok = np.abs(logp) < 2e38              # (what fp32 holds, before the logarithm's factor too)
+    for got, want in ((out.logp, logp), (out.lse, lse)):
+        assert np.all(np.abs(n64(got) - want)[ok] <= 2.0 ** -19 + 2.0 ** -20 * np.abs(want[ok]))
+    assert np.all(n64(out.logp)[~ok] < -1e38)
+    keep = np.ones(n, dtype=bool)
+    keep[3:5] = False
+    # (hidden gradients with 0 times the mask: finite, and whole but for the constant)
+    assert np.linalg.norm((n64(out.grad_hidden) - gh)[keep][:, 1:]) <= 2.0 ** -7 * np.linalg.norm(gh[keep][:, 1:])
+    assert np.linalg.norm(n64(out.grad_weight) - gw) <= 2.0 ** -7 * np.linalg.norm(gw)
+
+
+def test_rows_with_near_and_far_logits():
+    """Logits from thousands to a hundred million in one row, on both sides of where the exponentials change form, with the
+    largest in either form.  Whole numbers, so that the logits are exact and alike where they should be."""
+    dim, vocab = 16, 512
+    g = torch.Generator().manual_seed(3)
+    w = torch.zeros(vocab, dim)
+    w[:, 0] = torch.randint(-4, 5, (vocab,), generator=g).float()
+    w[:128, 1] = 1
+    w[128:256, 2] = 1
+    w[256:384, 3] = 1
+    w[384:, 4] = 1
+    steps = torch.tensor([0.0, 1000.0, 2.0 ** 21, 2.0 ** 21 + 2 ** 14, 2.0 ** 22, 2.0 ** 23, 2.0 ** 26, -1000.0, -2.0 ** 22, -2.0 ** 23, -2.0 ** 26])
+    rows = [[a, b, c, d] for a in steps for b in steps[::3] for c in steps[1::4] for d in steps[2::5]]
+    h = torch.zeros(len(rows), dim)
+    h[:, 0] = 1
+    h[:, 1:5] = torch.tensor(rows)
+    assert torch.equal(h.to(BF).float(), h) and torch.equal(w.to(BF).float(), w)
+    z = h.double() @ w.double().T
+    for y in (z.argmax(1), torch.randint(0, vocab, (len(rows),), generator=g)):
+        for temperature in (1.0, 2.0, 0.25):
+            out = meo.linear_cross_entropy(h.to(BF).cuda(), w.to(BF).cuda(), y.cuda(), temperature=temperature)
+            loss, gh, gw, logp, lse = O.linear_cross_entropy(n64(h), n64(w), y.numpy(), temperature=temperature)
+            # a logit near 2^26 is a whole multiple of 8 in fp32, 2^-24 of it at most off
+            far = 2.0 ** -23 * z.abs().amax(1).numpy() / temperature
+            assert np.all(np.abs(n64(out.lse) - lse) <= 2e-6 + far + 2.0 ** -22 * np.abs(lse))
+            exact = z.abs().amax(1).numpy() < 2 ** 24 - 8
+            assert np.all(np.abs(n64(out.logp) - logp)[exact] <= (2e-6 + 2.0 ** -21 * np.abs(logp))[exact])
+            assert out.grad_hidden.isfinite().all() and out.grad_weight.isfinite().all()
+            # 2^-8 of the result, and of its terms, whose roundings add up like a norm where the terms themselves cancel
+            dx = np.exp(z.numpy() / temperature - lse[:, None])
+            dx[np.arange(len(y)), y.numpy()] -= 1
+            terms = np.sqrt((dx / len(y) / temperature) ** 2 @ n64(w) ** 2)[exact]
+            got, want = n64(out.grad_hidden)[exact], gh[exact]
+            assert np.linalg.norm(got - want) <= 2.0 ** -8 * (np.linalg.norm(want) + np.linalg.norm(terms))
