@@ -18,6 +18,7 @@ from typing import Iterable, Optional, Sequence
 import torch
 
 from . import binding as B
+from .losses import _written
 
 _DTYPES = {torch.float32: B.ADAF_FLOAT32, torch.bfloat16: B.ADAF_BFLOAT16}
 
@@ -200,6 +201,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS,
     else:
         flat = x
     stride_b = flat.stride(0) if flat.dim() == 3 and batch > 1 else 0
+    given = out
     with torch.cuda.device(x.device) if stream is None else torch.cuda.stream(stream):
         if out is None:
             out = torch.empty(x.shape, dtype=dtype, device=x.device)
@@ -209,6 +211,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS,
         ws = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
         B.muon_orthogonalize(B.muon_matrices(_ptr(x), _DTYPES[x.dtype], batch, rows, cols, stride_b, flat.stride(-2)), it,
                              _ptr(out), _DTYPES[dtype], _ptr(ws), n, int(torch.cuda.current_stream(x.device).cuda_stream))
+    _written(given)
     return out
 
 

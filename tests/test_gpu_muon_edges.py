@@ -54,3 +54,16 @@ def test_an_eps_above_the_norm(eps):
         x = (x * (norm / x.double().norm())).cuda()
         want = O.orthogonalize(x.double().cpu().numpy(), eps=eps)
         assert far(meo.orthogonalize(x, eps=eps, dtype=torch.float32), want) < TOL
+
+
+def test_autograd_learns_of_a_result_over_a_tensor():
+    """A matrix that a backward pass needs, and that holds the orthogonalisation by then, is an error."""
+    w, a = (torch.nn.Parameter(normal(s, 4).cuda()) for s in ((40, 60), (60, 30)))     # (each other's gradients need both)
+    for out in (a.detach(), w.detach()):
+        y = (w @ a).square().sum()
+        meo.orthogonalize(out, out=out)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    version = a._version
+    meo.orthogonalize(a)
+    assert a._version == version
