@@ -266,12 +266,18 @@ class Muon(torch.optim.Optimizer):
             ps = [p for p in group["params"] if p.grad is not None]
             if not ps:
                 continue
+            with torch.cuda.device(ps[0].device if ps[0].is_cuda else -1):
+                capturing = torch.cuda.is_current_stream_capturing()
             for p in ps:
                 if not self.state[p]:
+                    if capturing:
+                        # its zeros would be part of the graph: every replay would forget the momentum
+                        raise RuntimeError("a first step cannot be captured: the momentum has to be there before (call "
+                                           "step() once, or load a state)")
                     self.state[p].update(init_muon_state([p])[0])
             grads = [p.grad for p in ps]
             states = [self.state[p] for p in ps]
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 # memory of a graph's own pool is not kept for calls outside it
                 MuonStep(ps, grads, states, **hp)()
                 continue

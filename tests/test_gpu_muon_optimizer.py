@@ -112,3 +112,29 @@ def test_parameters_without_a_gradient_are_left_out(calls):
         assert calls[-1][0] == want
         for p, b in zip(params, before):
             assert torch.equal(p, b) == all(p is not q for q in some)
+
+
+def test_a_first_step_is_not_captured():
+    """Its momentum would be zeroed by every replay.  Captured after a step, replays go on where it was."""
+    def grad(t):
+        return torch.randn(12, 20, generator=torch.Generator().manual_seed(t)).cuda()
+
+    p, twin = parameters((12, 20), (12, 20))
+    opt, other = meo.Muon([p], lr=0.1), meo.Muon([twin], lr=0.1)
+    p.grad, twin.grad = grad(0), grad(0)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="momentum"):
+        with torch.cuda.graph(graph):
+            opt.step()
+    assert p.eq(1).all() and not opt.state[p]
+    opt.step()
+    other.step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.step()
+    for t in range(1, 4):
+        p.grad.copy_(grad(t))
+        twin.grad.copy_(grad(t))
+        graph.replay()
+        other.step()
+        assert torch.equal(p, twin) and torch.equal(opt.state[p]["momentum"], other.state[twin]["momentum"])

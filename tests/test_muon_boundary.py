@@ -161,3 +161,10 @@ def test_front_end_refuses_on_the_host(lib):
         M.orthogonalize(w, dtype=torch.float16)
     with pytest.raises(ValueError, match="result"):
         M.orthogonalize(w, out=v.half())
+
+
+def test_optimizer_refuses_tensors_of_the_host(lib):
+    p = torch.nn.Parameter(torch.zeros(4, 6))
+    p.grad = torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="CUDA"):
+        M.Muon([p]).step()
