@@ -266,8 +266,10 @@ class Muon(torch.optim.Optimizer):
             ps = [p for p in group["params"] if p.grad is not None]
             if not ps:
                 continue
-            with torch.cuda.device(ps[0].device if ps[0].is_cuda else -1):
-                capturing = torch.cuda.is_current_stream_capturing()
+            capturing = False
+            if ps[0].is_cuda:
+                with torch.cuda.device(ps[0].device):
+                    capturing = torch.cuda.is_current_stream_capturing()
             for p in ps:
                 if not self.state[p]:
                     if capturing:
