@@ -140,6 +140,7 @@ class MuonStep:
         with torch.cuda.device(self.device):
             B.muon_step(self._tensors, self.n, self._hp, _ptr(self.workspace), self.workspace_bytes,
                         int(stream.cuda_stream))
+            self.workspace.record_stream(stream)   # (its memory is not given away while this stream works on it)
 
     def device_status(self, stream: Optional[torch.cuda.Stream] = None) -> int:
         """0, or 1 if a bounded wait inside a kernel of the last call ran out (synchronises the stream)."""

@@ -138,3 +138,25 @@ def test_a_first_step_is_not_captured():
         graph.replay()
         other.step()
         assert torch.equal(p, twin) and torch.equal(opt.state[p]["momentum"], other.state[twin]["momentum"])
+
+
+def test_a_workspace_outlives_the_work_on_another_stream():
+    """A step on a stream that is not the one its plan was made on: the plan may go before the work has begun, but not
+    its memory."""
+    p = torch.randn(200, 300, generator=torch.Generator().manual_seed(1)).cuda()
+    g = torch.randn(200, 300, generator=torch.Generator().manual_seed(2)).cuda()
+    want = p.clone()
+    meo.muon_step([want], [g], meo.init_muon_state([p]), lr=0.1)
+    state, other = meo.init_muon_state([p]), torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    plan = meo.MuonStep([p], [g], state, lr=0.1)
+    size, at = plan.workspace.numel(), plan.workspace.data_ptr()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(200_000_000)
+    plan(other)
+    del plan
+    taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert at not in [t.data_ptr() for t in taken]
+    torch.cuda.synchronize()
+    assert torch.equal(p, want)
