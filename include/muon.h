@@ -98,7 +98,9 @@ adaf_status muon_validate_iteration(const muon_iteration* it);
 adaf_status muon_workspace_size(const muon_tensor* tensors, int32_t n, size_t* bytes);
 adaf_status muon_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, size_t* bytes);
 
-/* One step over the list, enqueued on `stream`.  workspace: 256-byte aligned
+/* One step over the list, enqueued on `stream`.  All of it is stepped at once:
+ * parameters and momenta share no memory with anything else in the list (nor
+ * one tensor listed twice); gradients may with one another.  workspace: 256-byte aligned
  * device memory, not used by another call in flight. */
 adaf_status muon_step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace,
                       size_t workspace_bytes, void* stream);

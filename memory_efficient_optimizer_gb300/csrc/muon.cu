@@ -1550,12 +1550,37 @@ size_t bytes_of(int64_t batch, int64_t rows, int64_t cols) {
   return bytes_of(sizes);
 }
 
+// Tensors that share memory: a step writes p and momentum of all of them at once, and reads g beside that.
+struct Extent {
+  uintptr_t from, to;
+  int32_t tensor;
+  bool written;
+};
+adaf_status check_apart(std::vector<Extent>& all) {
+  std::sort(all.begin(), all.end(), [](const Extent& x, const Extent& y) { return x.from < y.from; });
+  // the furthest end so far, of what is written and of everything
+  const Extent *written = nullptr, *any = nullptr;
+  for (const Extent& e : all) {
+    const Extent* const other = e.written ? any : written;
+    if (other != nullptr && other->to > e.from) {
+      const int32_t lo = std::min(e.tensor, other->tensor), hi = std::max(e.tensor, other->tensor);
+      return invalid(lo == hi ? "tensor " + std::to_string(lo) + ": p, g and momentum overlap"
+                              : "tensors " + std::to_string(lo) + " and " + std::to_string(hi) + " overlap");
+    }
+    if (any == nullptr || e.to > any->to) any = &e;
+    if (e.written && (written == nullptr || e.to > written->to)) written = &e;
+  }
+  return ADAF_OK;
+}
+
 adaf_status step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, void* workspace, size_t workspace_bytes, void* stream) {
   adaf_status st = check_hp(hp);
   if (st != ADAF_OK) return st;
   size_t need = 0;
   if ((st = check_tensors(tensors, n, &need)) != ADAF_OK) return st;
   std::vector<Listed> mats;
+  std::vector<Extent> extents;
+  extents.reserve(3 * static_cast<size_t>(n));
   for (int32_t i = 0; i < n; ++i) {
     const muon_tensor& t = tensors[i];
     if (t.batch == 0 || t.rows == 0 || t.cols == 0) continue;
@@ -1564,12 +1589,20 @@ adaf_status step(const muon_tensor* tensors, int32_t n, const muon_hparams* hp, 
     const size_t es = t.grad_dtype == ADAF_BFLOAT16 ? 2 : 4;
     if (!aligned(t.p, 4) || !aligned(t.momentum, 4) || !aligned(t.g, es)) return invalid(who + " is not element-aligned");
     const int64_t numel = t.rows * t.cols;
+    const auto extent = [&](const void* p, size_t size, bool written) {
+      const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+      extents.push_back({from, from + static_cast<size_t>(t.batch * numel) * size, i, written});
+    };
+    extent(t.p, 4, true);
+    extent(t.g, es, false);
+    extent(t.momentum, 4, true);
     for (int64_t b = 0; b < t.batch; ++b)
       mats.push_back({std::min(t.rows, t.cols), std::max(t.rows, t.cols), t.rows, t.cols, t.p + b * numel,
                       static_cast<const char*>(t.g) + static_cast<size_t>(b * numel) * es, t.momentum + b * numel,
                       (t.rows > t.cols ? kTurned : 0) | (es == 2 ? kBf16 : 0)});
   }
   if (mats.empty()) return ADAF_OK;
+  if ((st = check_apart(extents)) != ADAF_OK) return st;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != ADAF_OK) return st;
   const Call c{&hp->iteration, hp, 0, kUpdate, static_cast<unsigned char*>(workspace), static_cast<cudaStream_t>(stream)};
   return run<true>(c, mats);

@@ -168,3 +168,50 @@ def test_optimizer_refuses_tensors_of_the_host(lib):
     p.grad = torch.zeros(4, 6)
     with pytest.raises(ValueError, match="CUDA"):
         M.Muon([p]).step()
+
+
+@pytest.mark.parametrize("at,msg", [
+    (dict(), "tensors 0 and 1 overlap"),                                             # one tensor listed twice
+    (dict(p=P + (1 << 20)), "tensors 0 and 1 overlap"),                              # its momentum alone
+    (dict(m=MO + (1 << 20)), "tensors 0 and 1 overlap"),                             # the parameter alone
+    (dict(p=P + 4 * (4 * 6 - 1), m=MO + (1 << 20)), "tensors 0 and 1 overlap"),      # by one value
+    (dict(p=MO, m=MO + (1 << 20)), "tensors 0 and 1 overlap"),                       # a parameter on a momentum
+    (dict(p=P + (1 << 20), m=MO + (1 << 20), g=P), "tensors 0 and 1 overlap"),       # a gradient on another's parameter
+    (dict(p=P + (1 << 20), m=P + (1 << 20) + 64), "tensor 1: p, g and momentum overlap"),
+    (dict(p=P + (1 << 20), m=MO + (1 << 20), g=P + (1 << 20)), "tensor 1: p, g and momentum overlap")])
+def test_shared_memory_in_a_list_is_refused(lib, at, msg):
+    one, other = dict(p=P, g=G, m=MO), dict(p=P, g=G, m=MO)
+    other.update(at)
+    t = (B.muon_tensor * 2)(*[B.muon_tensor(d["p"], d["g"], B.ADAF_FLOAT32, 1, 4, 6, d["m"]) for d in (one, other)])
+    with pytest.raises(ValueError, match=msg):
+        B.muon_step(t, 2, hp(), WS, 1 << 30, 0)
+
+
+def test_gradients_may_be_shared_and_tensors_may_touch(lib):
+    """Then the next check is the workspace's."""
+    t = (B.muon_tensor * 3)(*[B.muon_tensor(P + 96 * k, G, B.ADAF_FLOAT32, 1, 4, 6, P + 96 * (k + 3)) for k in (1, 0, 2)])
+    with pytest.raises(B.AdafactorError, match="workspace needs"):
+        B.muon_step(t, 3, hp(), WS, 0, 0)
+    # an empty tensor has no memory to share
+    t = (B.muon_tensor * 2)(*[B.muon_tensor(P, G, B.ADAF_FLOAT32, b, 4, 6, MO) for b in (1, 0)])
+    with pytest.raises(B.AdafactorError, match="workspace needs"):
+        B.muon_step(t, 2, hp(), WS, 0, 0)
+
+
+def test_overlaps_are_found_in_long_lists(lib):
+    """Against every pair looked at, with one overlap or none in lists in any order."""
+    import random
+    rng = random.Random(5)
+    for trial in range(60):
+        n, places = 12, list(range(40))
+        rng.shuffle(places)
+        rows = [rng.randint(1, 6) for _ in range(n)]
+        ts = [[P + 4096 * places[2 * k], G, P + 4096 * places[2 * k + 1]] for k in range(n)]
+        if trial % 2:
+            k = rng.randrange(n)
+            ts[k][rng.randrange(3)] = ts[(k + 1 + rng.randrange(n - 1)) % n][rng.choice((0, 2))] + 4 * rng.randint(0, 3)
+        ext = [(i, j, a, a + 4 * 8 * rows[i]) for i, t in enumerate(ts) for j, a in enumerate(t)]
+        meets = any(x[2] < y[3] and y[2] < x[3] and not (x[1] == y[1] == 1) for a, x in enumerate(ext) for y in ext[:a])
+        t = (B.muon_tensor * n)(*[B.muon_tensor(p, g, B.ADAF_FLOAT32, 1, r, 8, m) for (p, g, m), r in zip(ts, rows)])
+        with pytest.raises(Exception, match="overlap" if meets else "workspace needs"):
+            B.muon_step(t, n, hp(), WS, 0, 0)
