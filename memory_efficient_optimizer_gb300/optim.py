@@ -306,6 +306,15 @@ class Adafactor(torch.optim.Optimizer):
         super().__init__(params, defaults)
         self._plans = {}
 
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        # (torch gives a floating parameter's states its own type: the codes come back exactly, and the sum is taken anew)
+        for st in self.state.values():
+            for name, dtype in (("param_sq_sum", torch.float64), ("exp_avg_codes", torch.int8)):
+                if name in st:
+                    st[name] = st[name].to(dtype)
+        self._plans.clear()
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None
