@@ -16,6 +16,7 @@ from typing import Iterable, Sequence
 import torch
 
 from . import binding as B
+from .plans import check_grad, plan_for
 
 _GRAD_DTYPES = {torch.float32: B.ADAF_FLOAT32, torch.bfloat16: B.ADAF_BFLOAT16}
 
@@ -84,6 +85,14 @@ class LambStep:
         self.workspace = (torch.empty(max(self.workspace_bytes, 256), dtype=torch.uint8, device=self.device)
                           if n else None)
 
+    def take_grads(self, grads: Sequence[torch.Tensor]) -> None:
+        """Other gradients for the same parameters, of the dtypes and alignment of those before."""
+        for k, (p, g) in enumerate(zip(self.params, grads)):
+            check_grad(k, p, g, _GRAD_DTYPES)
+        for td, g in zip(self._tensors, grads):
+            td.g = _ptr(g)
+        self.grads = list(grads)
+
     def __call__(self, step: int, stream: torch.cuda.Stream | None = None) -> None:
         if self.n == 0:
             return
@@ -138,18 +147,13 @@ class Lamb(torch.optim.Optimizer):
                     st["step"] = 0
                 st["step"] += 1
                 by_step.setdefault(st["step"], []).append(p)
-            for t, ps in by_step.items():
-                grads = [p.grad for p in ps]
-                key = (gi, tuple(p.data_ptr() for p in ps), tuple(g.data_ptr() for g in grads),
-                       repr(sorted(hp.items())))
-                plan = self._plans.get(key)
-                if plan is None:
-                    states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
-                    plan = LambStep(ps, grads, states, **hp)
-                    if len(self._plans) > 16:
-                        self._plans.clear()
-                    self._plans[key] = plan
-                plan(t)
+            for i, (t, ps) in enumerate(by_step.items()):
+                states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
+                plan = plan_for(self._plans, (gi, i), ps, [p.grad for p in ps], states, hp, LambStep)
+                try:
+                    plan(t)
+                finally:
+                    plan.grads = []
         return loss
 
 

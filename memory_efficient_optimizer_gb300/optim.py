@@ -11,11 +11,13 @@ exp_avg_sq otherwise), Step 5 (the update).
 from __future__ import annotations
 
 import ctypes
+import weakref
 from typing import Iterable, Sequence
 
 import torch
 
 from . import binding as B
+from .plans import check_grad, plan_for
 
 _GRAD_DTYPES = {torch.float32: B.ADAF_FLOAT32, torch.bfloat16: B.ADAF_BFLOAT16}
 
@@ -175,6 +177,19 @@ class AdafactorStep:
                           if n else None)
         self._carry = all("param_sq_sum" in st for st in self.states)
         self._versions = None
+        self._seen = [weakref.ref(g) for g in grads]
+
+    def take_grads(self, grads: Sequence[torch.Tensor]) -> None:
+        """Other gradients for the same parameters, of the dtypes and alignment of those before."""
+        for k, (p, g) in enumerate(zip(self.params, grads)):
+            check_grad(k, p, g, _GRAD_DTYPES)
+        if not all(ref() is g for ref, g in zip(self._seen, grads)):
+            # (as for a step that is marshalled anew: sum(p^2) is not taken over from the step before)
+            self._versions = None
+        for td, g in zip(self._tensors, grads):
+            td.grad = _ptr(g)
+        self.grads = list(grads)
+        self._seen = [weakref.ref(g) for g in grads]
 
     def _carry_valid(self) -> bool:
         if not self._carry or self._versions is None:
@@ -334,16 +349,11 @@ class Adafactor(torch.optim.Optimizer):
                     st["step"] = 0
                 st["step"] += 1
                 by_step.setdefault(st["step"], []).append(p)
-            for t, ps in by_step.items():
-                grads = [p.grad for p in ps]
-                key = (gi, t if len(by_step) > 1 else None, tuple(p.data_ptr() for p in ps),
-                       tuple(g.data_ptr() for g in grads), tuple(sorted(hp.items(), key=lambda kv: kv[0])).__repr__())
-                plan = self._plans.get(key)
-                if plan is None:
-                    states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
-                    plan = AdafactorStep(ps, grads, states, **hp)
-                    if len(self._plans) > 16:
-                        self._plans.clear()
-                    self._plans[key] = plan
-                plan(t)
+            for i, (t, ps) in enumerate(by_step.items()):
+                states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
+                plan = plan_for(self._plans, (gi, i), ps, [p.grad for p in ps], states, hp, AdafactorStep)
+                try:
+                    plan(t)
+                finally:
+                    plan.grads = []
         return loss
