@@ -153,6 +153,10 @@ class Came(torch.optim.Optimizer):
                                       weight_decay=weight_decay))
         self._plans = {}
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}            # (not part of what is copied, pickled or loaded)
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None

@@ -129,6 +129,10 @@ class Lamb(torch.optim.Optimizer):
                                       bias_correction=bias_correction))
         self._plans = {}
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}            # (not part of what is copied, pickled or loaded)
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None

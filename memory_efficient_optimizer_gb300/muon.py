@@ -255,6 +255,11 @@ class Muon(torch.optim.Optimizer):
         self._plans = {}
         self._workspaces = {}       # by device: gigabytes for large layers, so one for all plans
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}            # (not part of what is copied, pickled or loaded)
+        self._workspaces = {}
+
     @torch.no_grad()
     def step(self, closure=None):
         loss = None

@@ -321,6 +321,10 @@ class Adafactor(torch.optim.Optimizer):
         super().__init__(params, defaults)
         self._plans = {}
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self._plans = {}            # (not part of what is copied, pickled or loaded)
+
     def load_state_dict(self, state_dict):
         super().load_state_dict(state_dict)
         # (torch gives a floating parameter's states its own type: the codes come back exactly, and the sum is taken anew)

@@ -1,5 +1,7 @@
 """States of the optimizer classes through a checkpoint, without a GPU."""
+import copy
 import io
+import pickle
 
 import pytest
 import torch
@@ -30,3 +32,19 @@ def test_adafactor_states_keep_their_types(kw):
                 assert got.dtype == v.dtype and got.is_contiguous() and got.shape == v.shape
                 if name != "param_sq_sum":             # (of the parameters as they are at the next step)
                     assert torch.equal(got, v)
+
+
+@pytest.mark.parametrize("make", [meo.Adafactor, meo.Lamb, lambda ps: meo.Came(ps, lr=1e-3), meo.Muon])
+def test_optimizers_can_be_copied_and_pickled(make):
+    """A copy steps its own parameters with its own states: here as far as the first check of a device."""
+    p = torch.nn.Parameter(torch.randn(4, 6))
+    opt = make([p])
+    for again in (copy.deepcopy(opt), pickle.loads(pickle.dumps(opt))):
+        q, = again.param_groups[0]["params"]
+        assert torch.equal(p, q) and q is not p
+        q.grad = torch.zeros(4, 6)
+        with pytest.raises(ValueError, match="CUDA"):
+            again.step()
+        again.load_state_dict(again.state_dict())
+        with pytest.raises(ValueError, match="CUDA"):
+            again.step()
