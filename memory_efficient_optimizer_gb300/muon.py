@@ -175,8 +175,9 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients=COEFFICIENTS,
 
     ``x`` [..., rows, cols], float32 or bfloat16, with innermost stride 1 (rows
     may have gaps; leading dimensions are a stack).  The result is bfloat16, or
-    ``dtype`` float32; it is good to 1e-3 of its norm either way.  ``out``: a
-    contiguous tensor for it, of x's shape; it may be x itself.
+    ``dtype`` float32; either way it is good to about 1e-3 of its norm (the header
+    has the bounds).  ``out``: a contiguous tensor for it, of x's shape; it may
+    be x itself.
     """
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise ValueError("x must be a float32 or bfloat16 tensor")
