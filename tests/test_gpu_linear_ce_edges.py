@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import memory_efficient_optimizer_gb300 as meo
+from memory_efficient_optimizer_gb300 import binding as B
 from oracle import linear_ce as O
 from oracle.losses import log_softmax
 
@@ -155,3 +156,34 @@ def test_rows_with_near_and_far_logits():
             terms = np.sqrt((dx / len(y) / temperature) ** 2 @ n64(w) ** 2)[exact]
             got, want = n64(out.grad_hidden)[exact], gh[exact]
             assert np.linalg.norm(got - want) <= 2.0 ** -8 * (np.linalg.norm(want) + np.linalg.norm(terms))
+
+
+@pytest.mark.parametrize("n,dim,vocab,dtype", [(70, 96, 500, BF), (70, 97, 501, torch.float32), (1, 64, 3000, BF), (700, 128, 1000, BF),
+                                               (0, 16, 40, BF), (600, 8, 1 << 21, BF)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_one_gradient_alone(n, dim, vocab, dtype, weights):
+    """The library's call for the hidden states' gradient or the weight's by itself (a frozen output layer, a frozen
+    trunk), in its own workspace, which no call has used: the same bits as both together, and the other left as it is."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    h = torch.randn(n, dim, device="cuda", generator=g).to(dtype)
+    w = (torch.randn(vocab, dim, device="cuda", generator=g) / dim ** 0.5).to(dtype)
+    y = torch.randint(0, vocab, (n,), device="cuda", generator=g)
+    y[::5] = -100
+    share = torch.rand(n, device="cuda", generator=g) if weights else None
+    both = meo.linear_cross_entropy(h, w, y, weights=share)
+    code = B.ADAF_BFLOAT16 if dtype == BF else B.ADAF_FLOAT32
+    hidden = lambda t: B.linear_ce_hidden(t.data_ptr(), code, 1, n, dim, 0, dim)
+    weight = lambda t: B.linear_ce_weight(t.data_ptr(), code, vocab, dim, 0)
+    targets = B.loss_targets(B.loss_rows(y.data_ptr(), 0, 1), B.LOSS_INT64, -100)
+    args = B.linear_ce_args(B.loss_rows(share.data_ptr() if weights else None, 0, 1), 1.0, 0.0, 1.0)
+    for only_hidden in (True, False):
+        out = torch.full_like(h if only_hidden else w, 7.0)
+        gh, gw = (hidden(out), None) if only_hidden else (None, weight(out))
+        loss, logp, lse = torch.empty((), device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        size = B.linear_ce_workspace_size(hidden(h), weight(w), gh, gw)
+        ws = torch.full((size + 4096,), 255, dtype=torch.uint8, device="cuda")
+        B.linear_ce(hidden(h), weight(w), targets, args, gh, gw, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), ws.data_ptr(), size,
+                    torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(out, both.grad_hidden if only_hidden else both.grad_weight)
+        assert torch.equal(loss, both.loss) and torch.equal(logp, both.logp) and torch.equal(lse, both.lse)
+        assert ws[size:].eq(255).all()
