@@ -1003,7 +1003,6 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
     __nv_bfloat16* const hc = a.hc + static_cast<int64_t>(a.first) * P.ldh;
     const int64_t room = std::max<int64_t>(P.room - a.first, 64), e_rows = std::max<int64_t>(P.rows, 64);
     Shape shape{};
-    shape.batch = 1;
     shape.splits = 1;
     shape.first = a.first;
     shape.status = a.status;
@@ -1024,8 +1023,8 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
         using End = LogitsEnd<decltype(keep)::value>;
         const typename End::Args end{a.c_hi, a.c_lo, a.target + a.first, a.xt, a.stat, a.e, a.lde, a.spans};
         return g_profile.run(kSlotLogits, s, [&] {
-          if (rows <= 128) return launch_product<1, 256, 4, false, false, true, End>(h_k, w_k, x, end, s);
-          return launch_product<2, 256, 6, false, false, true, End>(h_k, w_k, x, end, s);
+          if (rows <= 128) return launch_product<1, 256, 4, false, false, End>(h_k, w_k, x, end, s);
+          return launch_product<2, 256, 6, false, false, End>(h_k, w_k, x, end, s);
         });
       };
       const cudaError_t e = grad ? logits(std::true_type{}) : logits(std::false_type{});
@@ -1052,8 +1051,8 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       x.group = 8;
       x.m_live = a.count;
       LCE_TRY(g_profile.run(kSlotGradHidden, s, [&] {
-        if (w.vocab > kMostWords) return launch_product<2, 256, 6, false, true, true, HiddenEnd<true>>(e_k, w_n, x, end, s);
-        return launch_product<2, 256, 6, false, true, true, HiddenEnd<false>>(e_k, w_n, x, end, s);
+        if (w.vocab > kMostWords) return launch_product<2, 256, 6, false, true, HiddenEnd<true>>(e_k, w_n, x, end, s);
+        return launch_product<2, 256, 6, false, true, HiddenEnd<false>>(e_k, w_n, x, end, s);
       }), "k_lce_grad_hidden");
       int device = 0, sms = 0;
       LCE_TRY(sm_count(&device, &sms), "current device");
@@ -1082,7 +1081,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       x.k = static_cast<int32_t>(rows);
       x.group = std::max(1, 76 / nt_d);
       x.k_live = a.count;
-      LCE_TRY(g_profile.run(kSlotGradWeight, s, [&] { return launch_product<2, 256, 6, true, true, true, WeightEnd>(e_m, h_n, x, end, s); }),
+      LCE_TRY(g_profile.run(kSlotGradWeight, s, [&] { return launch_product<2, 256, 6, true, true, WeightEnd>(e_m, h_n, x, end, s); }),
               "k_lce_grad_weight");
     }
   }

@@ -427,9 +427,9 @@ __device__ __forceinline__ void end_gram(const Matrix& t, const Part& p, Load&& 
 template <int COLS>
 __device__ __forceinline__ bool end_gram_part(const Matrix& t, const Part& p, int warp) {
   constexpr int kWords = COLS / 4 * 32;   // of 16 bytes, a warp's part
-  const int at = p.tile.batch * meo::tc::kEndWarps + warp;
+  const int at = p.tile.number * meo::tc::kEndWarps + warp;
   const bool rows = p.row0() < p.m;
-  float4* const first = reinterpret_cast<float4*>(t.parts) + (static_cast<int64_t>(p.tile.batch) * t.splits * meo::tc::kEndWarps + warp) * kWords + p.ex.lane;
+  float4* const first = reinterpret_cast<float4*>(t.parts) + (static_cast<int64_t>(p.tile.number) * t.splits * meo::tc::kEndWarps + warp) * kWords + p.ex.lane;
   constexpr int64_t kNext = meo::tc::kEndWarps * kWords;
 #pragma unroll
   for (int c = 0; c < COLS; c += 32) {
@@ -719,7 +719,6 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Ph
   while (w->at + 1 < count && i >= (gram ? mat[w->at + 1].gram0 : sym ? mat[w->at + 1].sym0 : mat[w->at + 1].app0)) ++w->at;
   const Matrix& m = mat[w->at];
   meo::tc::Shape s{};
-  s.batch = 1;
   s.splits = 1;
   s.group = 16;
   constexpr int kRows = meo::tc::kTileM * CG;
@@ -727,11 +726,11 @@ __device__ __forceinline__ bool find_tile(const Matrix* mat, int count, const Ph
   const int mtn = (m.m + BN - 1) / BN;   // column tiles of the symmetric products
   const int syms = static_cast<int>(meo::tc::sym_tiles<kRows / BN>(mtn));
   w->need = ph.syms * syms + ph.apps * mt * nt;
-  if (gram) {   // (batch: the tile's number)
+  if (gram) {
     i -= m.gram0;
     const int tile = CG == 1 ? i / m.splits : i;
     const bool there = meo::tc::tile_of<true, kRows, BN>(tile, mt, mtn, s, t);
-    t->batch = tile;
+    t->number = tile;
     t->split = i - tile * (CG == 1 ? m.splits : 1);
     return there;
   }

@@ -1,9 +1,10 @@
 // Products of matrices on the tensor cores of sm_103a, with the work on each
 // result tile given by the caller (the "ending").
 //
-//   D[b][i, j] = sum over k of A[b][i, k] B[b][j, k]
+//   D[i, j] = sum over k of A[i, k] B[j, k]
 //
-// A and B are 16-bit (both fp16 or both bf16), each either with k innermost
+// A and B are 16-bit, both bf16 in k_product (fp16 in Muon's iteration, which has
+// the parts below in a kernel of its own), each either with k innermost
 // ("K-major") or with i or j innermost ("MN-major"); sums are fp32.
 //
 // Layout.  A tile of the result is 128 CG rows by BN columns, CG = 2: the two
@@ -288,8 +289,7 @@ struct Exchange {
 
 // ---- the product --------------------------------------------------------------------
 struct Shape {
-  int32_t m, n, k;         // of one matrix of the batch
-  int32_t batch;
+  int32_t m, n, k;
   int32_t splits;          // parts of k, each a result of its own; 0: as choose_splits has it
   int64_t split_room;      // then: values that the parts' results may take
   int32_t group;           // tiles are walked in groups of so many rows of tiles
@@ -301,7 +301,8 @@ struct Shape {
 };
 
 struct Tile {
-  int32_t batch, split, m0, n0;   // the cluster tile's first row and column
+  int32_t split, m0, n0;   // the cluster tile's first row and column
+  int32_t number;          // of the tile, where Muon's iteration needs it
 };
 
 // What an ending is given: a row of the result a thread, and the columns of its group.
@@ -372,9 +373,8 @@ template <bool SYM, int TM, int TN>
 __device__ __forceinline__ bool tile_of(int64_t i, int mt, int nt, const Shape& s, Tile* t) {
   constexpr int R = TM / TN;
   const int64_t per = SYM ? sym_tiles<SYM ? R : 1>(nt) : static_cast<int64_t>(mt) * nt * s.splits;
-  if (per == 0 || i >= per * s.batch) return false;
-  t->batch = static_cast<int>(i / per);
-  int r = static_cast<int>(i - t->batch * per);
+  if (i >= per) return false;
+  int r = static_cast<int>(i);
   if constexpr (SYM) {
     // groups of R columns: group q has R (q + 1) tiles, R q (q + 1) / 2 before it
     int q = static_cast<int>((sqrtf(8.f / R * static_cast<float>(r) + 1.f) - 1.f) * 0.5f);
@@ -412,7 +412,7 @@ struct Shared {
 // the sums are taken out of tensor memory every kChunk stages and added up in registers.  The
 // tensor cores cut off what does not fit a sum's 24 bits, so a long sum is off toward zero by
 // half of 2^-25 of itself and more for each of its steps of 16 values.
-template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
+template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, class End>
 __global__ void __launch_bounds__(kThreads, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape given,
               const typename End::Args end) {
@@ -495,16 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (s.stall == 0) {
             if constexpr (A_MN) {
 #pragma unroll
-              for (int j = 0; j < kTileM / 64; ++j) tma_load<CG>(a + j * 64 * kBlockK * 2, &map_a, am + j * 64, k, t.batch, bar);
+              for (int j = 0; j < kTileM / 64; ++j) tma_load<CG>(a + j * 64 * kBlockK * 2, &map_a, am + j * 64, k, 0, bar);
             } else {
-              tma_load<CG>(a, &map_a, k, am, t.batch, bar);
+              tma_load<CG>(a, &map_a, k, am, 0, bar);
             }
             if constexpr (B_MN) {
 #pragma unroll
-              for (int j = 0; j < kBCta / 64; ++j) tma_load<CG>(b + j * 64 * kBlockK * 2, &map_b, bn + j * 64, k, t.batch, bar);
+              for (int j = 0; j < kBCta / 64; ++j) tma_load<CG>(b + j * 64 * kBlockK * 2, &map_b, bn + j * 64, k, 0, bar);
             } else {
 #pragma unroll
-              for (int j = 0; j < kBCta / 128; ++j) tma_load<CG>(b + j * 128 * kBlockK * 2, &map_b, k, bn + j * 128, t.batch, bar);
+              for (int j = 0; j < kBCta / 128; ++j) tma_load<CG>(b + j * 128 * kBlockK * 2, &map_b, k, bn + j * 128, 0, bar);
             }
           }
           if (++stage == STAGES) stage = 0, phase ^= 1;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 1 && lane == 0 && rank == 0) {
       // ---- products
-      constexpr uint32_t idesc = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((A_MN ? 1u : 0u) << 15) |
+      constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) |
                                  ((B_MN ? 1u : 0u) << 16) | (uint32_t{BN >> 3} << 17) | (uint32_t{kTileM * CG >> 4} << 24);
       constexpr uint32_t a_step = A_MN ? 16 * 128 : 32, b_step = B_MN ? 16 * 128 : 32;   // bytes of 16 k values
       int stage = 0, acc = 0;

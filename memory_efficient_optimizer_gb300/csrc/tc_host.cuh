@@ -127,10 +127,10 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, cuda
 
 // Launches a product over a persistent grid: as many CTAs as the device has SMs,
 // or as there are tiles.
-template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, bool BF16, class End>
+template <int CG, int BN, int STAGES, bool A_MN, bool B_MN, class End>
 cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Shape& s, const typename End::Args& end,
                            cudaStream_t stream) {
-  auto* const kernel = k_product<CG, BN, STAGES, A_MN, B_MN, BF16, End>;
+  auto* const kernel = k_product<CG, BN, STAGES, A_MN, B_MN, End>;
   constexpr int kBytes = Shared<CG, BN, STAGES>::bytes;
   static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<unsigned long long> ready{0};   // devices whose limit has been raised
@@ -144,7 +144,7 @@ cudaError_t launch_product(const CUtensorMap& a, const CUtensorMap& b, const Sha
     ready.fetch_or(bit);
   }
   const int64_t mt = (s.m + kTileM * CG - 1) / (kTileM * CG), nt = (s.n + BN - 1) / BN;
-  const int64_t tiles = mt * nt * std::max(1, s.splits) * s.batch;
+  const int64_t tiles = mt * nt * std::max(1, s.splits);
   const int64_t grid = std::min<int64_t>(s.splits == 0 && tiles > 0 ? sms / CG : tiles, sms / CG) * CG;
   if (grid == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg;
