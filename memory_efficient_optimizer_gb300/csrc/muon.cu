@@ -326,9 +326,9 @@ __device__ __forceinline__ void pack32(const float (&v)[32], uint4 (&w)[4]) {
 struct Matrix {
   __half* hi;            // [2][m][ldx]: of this step and of the next
   float* xb;             // x in blocks (block_at), updated in place
-  __half* fe;            // [kSlabs][m][lda]: symmetric matrices without their diagonals, the tiles on and above it
+  __half* fe;            // [slabs][m][lda]: symmetric matrices without their diagonals, the tiles on and above it
   __half* fb;            // the same in blocks
-  float* dg;             // [kSlabs][lda]: the diagonals
+  float* dg;             // [slabs][lda]: the diagonals
   float* p;              // the parameter, or the result
   int32_t m, n, ldx, lda;
   int32_t flags;
@@ -341,7 +341,7 @@ struct Matrix {
 
 enum Out : int32_t { kUpdate, kFp32, kBf16Out };
 
-constexpr int kSlabs = 4;
+constexpr int kSlabs = 2, kPairSlabs = 4;   // symmetric matrices that are kept: A and its polynomial; for two steps at once
 // Scales of the symmetric matrices' elements beside the diagonals: at most 3.9, so 2^14; a product
 // of two polynomials at most 15.5, so 2^12.
 constexpr int kSymScale = 14, kPairScale = 12;
@@ -1160,7 +1160,7 @@ adaf_status check_size(int64_t batch, int64_t rows, int64_t cols, const std::str
 struct Layout {
   size_t hi, xb, fe, fb, dg, bytes;
 };
-Layout layout(int64_t m, int64_t n) {
+Layout layout(int64_t m, int64_t n, int slabs) {
   const int64_t ldx = round_up(n, 8), lda = round_up(m, 8);
   Layout L{};
   auto take = [&](int64_t bytes) {
@@ -1170,9 +1170,9 @@ Layout layout(int64_t m, int64_t n) {
   };
   L.hi = take(2 * m * ldx * 2);
   L.xb = take(round_up(m, 32) * round_up(n, 32) * 4);
-  L.fe = take(kSlabs * m * lda * 2);
-  L.fb = take(kSlabs * round_up(m, 32) * round_up(m, 32) * 2);
-  L.dg = take(kSlabs * lda * 4);
+  L.fe = take(slabs * m * lda * 2);
+  L.fb = take(slabs * round_up(m, 32) * round_up(m, 32) * 2);
+  L.dg = take(slabs * lda * 4);
   return L;
 }
 int32_t parts_of(int64_t m, int64_t n) {
@@ -1199,6 +1199,8 @@ struct Order {
       if (wide(z.first)) tiles += tiles_256(z.first) * z.second;
     apart = tiles >= kFullTiles;
   }
+  // Of a matrix, and of all in its group.
+  int slabs(const Size& z) const { return apart && wide(z) ? kPairSlabs : kSlabs; }
   bool before(const Size& x, const Size& y) const {
     return apart && wide(x) != wide(y) ? wide(x) : x > y;
   }
@@ -1240,7 +1242,7 @@ struct Grouping {
     if (count == 0) first_wide = wide(z);
     ++count;
     values += z.first * z.second;
-    bytes += layout(z.second, z.first).bytes;
+    bytes += layout(z.second, z.first, order->slabs(z)).bytes;
     parts.add(z);
     most = std::max(most, bytes + parts.bytes());
   }
@@ -1344,7 +1346,7 @@ int phases_of(const muon_iteration& it, bool pair, int64_t gram, int64_t sym, in
 }
 
 template <int CG, int BN, int STAGES, int COUNT>
-adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
+adaf_status iterate(const Call& c, const Listed* mats, int count, int slabs, bool pair) {
   using namespace meo::tc;
   auto* const kernel = k_muon_iterate<CG, BN, STAGES, COUNT>;
   constexpr int kBytes = Shared<CG, BN, STAGES>::bytes + kEndWarps * (BN / 2) * 4 + COUNT * sizeof(Matrix) + kMaxPhases * sizeof(Phase) + 8 +
@@ -1366,7 +1368,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
   for (int i = 0; i < count; ++i) grams += sym_tiles<kRows / BN>((mats[i].m + BN - 1) / BN);
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
-    const Layout L = layout(z.m, z.n);
+    const Layout L = layout(z.m, z.n, slabs);
     Matrix& m = a.mat[i];
     m.hi = reinterpret_cast<__half*>(at + L.hi);
     m.xb = reinterpret_cast<float*>(at + L.xb);
@@ -1386,7 +1388,7 @@ adaf_status iterate(const Call& c, const Listed* mats, int count, bool pair) {
       m.rate = static_cast<float>(c.hp->lr * (original ? std::sqrt(std::max(1.0, h / w)) : 0.2 * std::sqrt(std::max(h, w))));
     }
     if (!make_map(&a.map[i].x, m.hi, false, z.m, z.n, m.ldx, 2, z.m * m.ldx, 64) ||
-        !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, kSlabs, z.m * m.lda, 64))
+        !make_map(&a.map[i].s, m.fe, false, z.m, z.m, m.lda, slabs, z.m * m.lda, 64))
       return fail(ADAF_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     const int64_t mt = (z.m + kRows - 1) / kRows, nt = (z.n + BN - 1) / BN;
     const int32_t own = static_cast<int32_t>(sym_tiles<kRows / BN>((z.m + BN - 1) / BN));
@@ -1461,7 +1463,7 @@ double step_time(const Listed* mats, int count, int64_t side, int slots, double 
 }
 
 template <bool STEP>
-adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, bool apart) {
+adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, const Order& order) {
   MuonArgs a;
   std::memset(&a, 0, sizeof a);
   a.count = count;
@@ -1476,12 +1478,13 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, 
   a.part = reinterpret_cast<float2*>(c.ws + 256);
   a.joined = reinterpret_cast<unsigned*>(c.ws + kHead) - kMaxJoined;
   a.clear = first ? 1 : 0;
+  const int slabs = order.slabs({mats[0].n, mats[0].m});
   unsigned char* at = c.ws + kHead;
   int32_t parts = 0, tiles = 0;
   int64_t big = 0, small = 0;   // tiles of 256 x 256 of a symmetric product, of 128 x 128 of the last one
   for (int i = 0; i < count; ++i) {
     const Listed& z = mats[i];
-    const Layout L = layout(z.m, z.n);
+    const Layout L = layout(z.m, z.n, slabs);
     Item& t = a.item[i];
     t.u = z.u;
     t.mom = z.mom;
@@ -1512,14 +1515,14 @@ adaf_status run_group(const Call& c, const Listed* mats, int count, bool first, 
   int device = 0, sms = 0;
   MUON_TRY(meo::tc::sm_count(&device, &sms), "current device");
   // (a group's matrices are all wide, or none is)
-  const bool pair = apart && big >= kFullTiles && wide({mats[0].n, mats[0].m}) && pair_fits(*c.it);
+  const bool pair = slabs == kPairSlabs && big >= kFullTiles && pair_fits(*c.it);
   // Narrow tiles where each of them has an SM: half as much to load and to write out a tile, for
   // 256 x 512 102 us to 115, six matrices of 256 x 256 to 1024 126 to 140; 1403 x 777, where two
   // rounds would be needed, 198 to 175.
-  if (!pair && 2 * small <= sms) return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count, false) : iterate<1, 64, 8, kMaxGroup>(c, mats, count, false);
+  if (!pair && 2 * small <= sms) return count <= kFew ? iterate<1, 64, 8, kFew>(c, mats, count, slabs, false) : iterate<1, 64, 8, kMaxGroup>(c, mats, count, slabs, false);
   if (!pair && step_time(mats, count, 128, sms, 0.29, 1.5) < step_time(mats, count, 256, sms / 2, 0.27, 3.5))
-    return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count, false) : iterate<1, 128, 6, kMaxGroup>(c, mats, count, false);
-  return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count, pair) : iterate<2, 256, 6, kMaxGroup>(c, mats, count, pair);
+    return count <= kFew ? iterate<1, 128, 6, kFew>(c, mats, count, slabs, false) : iterate<1, 128, 6, kMaxGroup>(c, mats, count, slabs, false);
+  return count <= kFew ? iterate<2, 256, 6, kFew>(c, mats, count, slabs, pair) : iterate<2, 256, 6, kMaxGroup>(c, mats, count, slabs, pair);
 }
 
 template <bool STEP>
@@ -1534,7 +1537,7 @@ adaf_status run(const Call& c, std::vector<Listed>& mats) {
     Grouping g{&order};
     size_t j = i;
     for (; j < mats.size() && !g.full({mats[j].n, mats[j].m}); ++j) g.add({mats[j].n, mats[j].m});
-    const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(j - i), first, order.apart);
+    const adaf_status st = run_group<STEP>(c, &mats[i], static_cast<int>(j - i), first, order);
     if (st != ADAF_OK) return st;
     first = false;
     i = j;

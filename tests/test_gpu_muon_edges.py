@@ -67,3 +67,28 @@ def test_autograd_learns_of_a_result_over_a_tensor():
     version = a._version
     meo.orthogonalize(a)
     assert a._version == version
+
+
+@pytest.mark.parametrize("shapes", [[(1, 300, 300)], [(1, 40, 64)], [(2, 1500, 1500)], [(1, 64, 9000)], [(7, 1024, 2048)], [(1, 4096, 4400)],
+                                    [(7, 1024, 2048), (2, 1100, 1200), (50, 30, 20)], [(1, 2048, 4096), (1, 2049, 4100)]])
+def test_the_workspace_is_not_left(shapes):
+    """A step within the bytes that it asked for, on memory of any contents, against the oracle's formula."""
+    params = [normal(s, k).cuda() for k, s in enumerate(shapes)]
+    grads = [normal(s, 10 + k).cuda() for k, s in enumerate(shapes)]
+    before = [p.clone() for p in params]
+    states = meo.init_muon_state(params)
+    need = meo.MuonStep(params, grads, states).workspace_bytes
+    ws = torch.full((need + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+    step = meo.MuonStep(params, grads, states, lr=1.0, momentum=0.0, adjust_lr="match_rms", workspace=ws)
+    assert step.workspace is ws
+    step()
+    assert step.device_status() == 0 and ws[need:].eq(255).all()
+    for p, b, g in zip(params, before, grads):
+        x = g.double() / g.double().flatten(-2).norm(dim=-1)[..., None, None]
+        x = x if x.shape[-2] <= x.shape[-1] else x.mT
+        for c0, c1, c2 in O.COEFFICIENTS:
+            a = x @ x.mT
+            x = c0 * x + (c1 * a + c2 * (a @ a)) @ x
+        want = (x if g.shape[-2] <= g.shape[-1] else x.mT) * 0.2 * max(g.shape[-2:]) ** 0.5
+        # p's own rounding, 2^-24 of a normal value, beside an update of 0.2
+        assert far(b - p, want.cpu().numpy()) < TOL + 2.0 ** -20

@@ -215,3 +215,14 @@ def test_overlaps_are_found_in_long_lists(lib):
         t = (B.muon_tensor * n)(*[B.muon_tensor(p, g, B.ADAF_FLOAT32, 1, r, 8, m) for (p, g, m), r in zip(ts, rows)])
         with pytest.raises(Exception, match="overlap" if meets else "workspace needs"):
             B.muon_step(t, n, hp(), WS, 0, 0)
+
+
+@pytest.mark.parametrize("shape,per_value", [
+    ((1, 4096, 4096), 16), ((1, 512, 512), 16), ((7, 1000, 1000), 16),   # x twice in fp16 and in fp32; A and its polynomial, twice
+    ((1, 4096, 14336), 8 + 16 * 4096 / 14336),                           # wide: four symmetric matrices, for two steps at once
+    ((1, 1024, 4096), 8 + 8 / 4)])                                       # too few of them for that
+def test_workspace_by_value(lib, shape, per_value):
+    """Bytes for each value, but for the sums, the diagonals and the sums of x x^T in parts."""
+    values = shape[0] * shape[1] * shape[2]
+    have = B.muon_orthogonalize_workspace_size(*shape)
+    assert per_value * values <= have <= 1.05 * per_value * values + (12 << 20)
