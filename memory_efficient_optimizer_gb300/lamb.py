@@ -152,8 +152,7 @@ class Lamb(torch.optim.Optimizer):
                 st["step"] += 1
                 by_step.setdefault(st["step"], []).append(p)
             for i, (t, ps) in enumerate(by_step.items()):
-                states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
-                plan = plan_for(self._plans, (gi, i), ps, [p.grad for p in ps], states, hp, LambStep)
+                plan = plan_for(self._plans, (gi, i), ps, [self.state[p] for p in ps], hp, LambStep)
                 try:
                     plan(t)
                 finally:

@@ -183,13 +183,16 @@ class AdafactorStep:
         """Other gradients for the same parameters, of the dtypes and alignment of those before."""
         for k, (p, g) in enumerate(zip(self.params, grads)):
             check_grad(k, p, g, _GRAD_DTYPES)
-        if not all(ref() is g for ref, g in zip(self._seen, grads)):
-            # (as for a step that is marshalled anew: sum(p^2) is not taken over from the step before)
-            self._versions = None
         for td, g in zip(self._tensors, grads):
             td.grad = _ptr(g)
         self.grads = list(grads)
-        self._seen = [weakref.ref(g) for g in grads]
+
+    def note_grads(self, grads: Sequence[torch.Tensor]) -> None:
+        """Other tensors than in the step before count as a step that is marshalled anew: sum(p^2) is not taken
+        over from it."""
+        if not all(ref() is g for ref, g in zip(self._seen, grads)):
+            self._versions = None
+            self._seen = [weakref.ref(g) for g in grads]
 
     def _carry_valid(self) -> bool:
         if not self._carry or self._versions is None:
@@ -354,8 +357,8 @@ class Adafactor(torch.optim.Optimizer):
                 st["step"] += 1
                 by_step.setdefault(st["step"], []).append(p)
             for i, (t, ps) in enumerate(by_step.items()):
-                states = [{k: v for k, v in self.state[p].items() if k != "step"} for p in ps]
-                plan = plan_for(self._plans, (gi, i), ps, [p.grad for p in ps], states, hp, AdafactorStep)
+                plan = plan_for(self._plans, (gi, i), ps, [self.state[p] for p in ps], hp, AdafactorStep)
+                plan.note_grads([p.grad for p in ps])
                 try:
                     plan(t)
                 finally:
