@@ -13,6 +13,7 @@ leading index, as it is for the factored steps: the experts of a layer.
 from __future__ import annotations
 
 import functools
+from operator import is_
 from typing import Iterable, Optional, Sequence
 
 import torch
@@ -290,17 +291,23 @@ class Muon(torch.optim.Optimizer):
                 # memory of a graph's own pool is not kept for calls outside it
                 MuonStep(ps, grads, states, **hp)()
                 continue
-            # A group's plan stays; the tensors are checked and put into it anew at every step (gradients
-            # come and go, on other memory or in another form), and it does not keep them.
+            # A group's plan stays; the tensors are looked at in every step and put into it where they are others
+            # (gradients come and go, on other memory or in another form), and it does not keep them.
             plan, values = self._plans.get(gi), repr(sorted(hp.items()))
+            momenta = [st.get("momentum") for st in states]
+            seen = [(p.data_ptr(), p.shape, p.is_contiguous(), g.data_ptr(), g.shape, g.is_contiguous(), g.dtype)
+                    for p, g in zip(ps, grads)]
             if plan is None:
                 plan = MuonStep(ps, grads, states, workspace=self._workspaces.get(ps[0].device), **hp)
                 self._plans[gi] = plan
             else:
-                plan._take(ps, grads, states)
+                if seen != plan.seen or not all(map(is_, momenta, plan.momenta)):
+                    plan.seen = None
+                    plan._take(ps, grads, states)
                 if values != plan.values:
+                    plan.values = None
                     plan._hp = make_muon_hparams(**hp)
-            plan.values = values
+            plan.seen, plan.momenta, plan.values = seen, momenta, values
             self._share_workspace(plan)
             try:
                 plan()
