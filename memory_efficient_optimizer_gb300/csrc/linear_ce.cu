@@ -21,15 +21,16 @@
 // three that have to be; keeping 16 bits of it costs 4 bytes a word and token of
 // memory traffic (0.6 of 16 ms at 8192 tokens of 128256 words).
 //
-// Rounding.  An exponential is kept as 2^(x c - I + 15) in fp16: 2^-12 relative
-// down to 2^-29 of the largest of its 128 words, and below that an error of 2^-40
-// of it.  A power of two moves it to the row's scale exactly.  dx is rounded to
-// bf16 once; under a mean it is kept without the mean's factor, whose rounding
-// would lean the same way in every token's target (the gradients were up to
-// 3.3e-3 off for it, 2.1e-3 without).  The sum over the words without the target,
-// R, is kept apart from the target's exponential E: its own dx is -R / (R + E), not
-// 1 less a rounded q, and logp = -ln(1 + R / E), so a token that is nearly certain
-// has both to the last bits.
+// Rounding.  An exponential is kept as 2^(x c - I + 15) in fp16: 2^-11 relative at
+// most down to 2^-29 of the largest of its 128 words, and below that an error of
+// 2^-40 of it.  A power of two moves it to the row's scale exactly.  dx is rounded
+// to bf16 once; under a mean it is kept without the mean's factor, whose rounding
+// would lean the same way in every token's target (bf16 gradients were up to 3.3e-3
+// off for it, and are 2.0e-3 to 2.3e-3 off without; 1.7e-3 is the rounding of the
+// result alone).  Given weights are in dx, and what they are all alike in leans so.
+// The sum over the words without the target, R, is kept apart from the target's
+// exponential E: its own dx is -R / (R + E), not 1 less a rounded q, and
+// logp = -ln(1 + R / E), so a token that is nearly certain has both to the last bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -57,8 +58,9 @@ constexpr int kSpan = 128;                          // words of one I and s
 // values: measured, a sum of n steps comes out smaller by 0.54 n 2^-25 of itself (0.42 to 0.56, for
 // terms of one sign and of both, 256 to 16384 values).  4096 values at once leave logits 4e-6 off,
 // and log-probabilities 1.6e-5 of themselves.  So logits are summed in parts of 1024 values,
-// 1e-6 off, and c = log2(e) / T makes up for the mean of it: 1e-7 is left, and 5e-7 at random.  (Parts of 512
-// values take 5 % longer, 2.5 % parts of 1024.)
+// 1e-6 off, and c = log2(e) / T makes up for the mean of it: 1e-7 is left on the average, and up to 1e-6 of a
+// single logit.  (One token's log-probability over 4096 values is 1.4e-7 of itself off in the middle of 60, 1.2e-6
+// at most; in fp32 torch operations 9e-8 and 9.7e-7.  Parts of 512 values take 5 % longer, 2.5 % parts of 1024.)
 constexpr int kSumStages = 16;
 constexpr double kCutOff = 0.54 / (1 << 25);
 // The gradients' sums are longer, and one that grows all the way loses more (products far below it lose
@@ -976,6 +978,8 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   a.logp = logp;
   a.lse = lse;
 
+  int device = 0, sms = 0;
+  LCE_TRY(sm_count(&device, &sms), "current device");
   // (the call's first launch begins when the stream's work before it is done; the others early)
   const bool few = tokens > 0 && tokens <= kFewTokens;
   if (!few) LCE_TRY(g_profile.run(kSlotScan, s, [&] { k_lce_scan<<<1, kScanThreads, 0, s>>>(a); return cudaGetLastError(); }), "k_lce_scan");
@@ -989,7 +993,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
   if (P.packed && tokens > 0) {
     wp = ws + P.w;
     LCE_TRY(g_profile.run(kSlotWeight, s, [&] {
-      return launch_early(k_lce_weight, dim3(static_cast<unsigned>(std::min<int64_t>((w.vocab * (P.ldw >> 3) + 255) / 256, 152 * 8))), 256, s, w.p,
+      return launch_early(k_lce_weight, dim3(static_cast<unsigned>(std::min<int64_t>((w.vocab * (P.ldw >> 3) + 255) / 256, 8 * sms))), 256, s, w.p,
                           static_cast<int32_t>(w.dtype == ADAF_BFLOAT16), w.stride_v, a.vocab, a.dim, static_cast<int32_t>(P.ldw),
                           reinterpret_cast<__nv_bfloat16*>(ws + P.w));
     }), "k_lce_weight");
@@ -1031,7 +1035,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       LCE_TRY(e, "k_lce_logits");
       LCE_TRY(g_profile.run(kSlotRows, s, [&] {
         const dim3 grid(static_cast<unsigned>(grad ? round_up(rows, 64) : rows));
-        return rows <= 304 ? launch_early(k_lce_rows<1024>, grid, 1024, s, a) : launch_early(k_lce_rows<256>, grid, 256, s, a);
+        return rows <= 2 * sms ? launch_early(k_lce_rows<1024>, grid, 1024, s, a) : launch_early(k_lce_rows<256>, grid, 256, s, a);
       }), "k_lce_rows");
     }
     if (gh != nullptr && rows > 0) {
@@ -1054,10 +1058,8 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
         if (w.vocab > kMostWords) return launch_product<2, 256, 6, false, true, HiddenEnd<true>>(e_k, w_n, x, end, s);
         return launch_product<2, 256, 6, false, true, HiddenEnd<false>>(e_k, w_n, x, end, s);
       }), "k_lce_grad_hidden");
-      int device = 0, sms = 0;
-      LCE_TRY(sm_count(&device, &sms), "current device");
-      const dim3 join(static_cast<unsigned>(std::min<int64_t>(rows, 1216)),
-                      static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((h.dim + 1023) / 1024, 1216 / rows))));
+      const dim3 join(static_cast<unsigned>(std::min<int64_t>(rows, 8 * sms)),
+                      static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((h.dim + 1023) / 1024, 8 * sms / rows))));
       LCE_TRY(g_profile.run(kSlotJoin, s, [&] {
         return launch_early(k_lce_join, join, 256, s, a.dim,
                             static_cast<int32_t>((w.vocab + kBlockK - 1) / kBlockK), static_cast<int32_t>(sms / 2), P.split_room,
@@ -1079,7 +1081,7 @@ adaf_status linear_ce(const linear_ce_hidden* hidden, const linear_ce_weight* we
       x.m = a.vocab;
       x.n = a.dim;
       x.k = static_cast<int32_t>(rows);
-      x.group = std::max(1, 76 / nt_d);
+      x.group = std::max(1, sms / 2 / nt_d);
       x.k_live = a.count;
       LCE_TRY(g_profile.run(kSlotGradWeight, s, [&] { return launch_product<2, 256, 6, true, true, WeightEnd>(e_m, h_n, x, end, s); }),
               "k_lce_grad_weight");

@@ -7,7 +7,7 @@ parts are added in fp32, 2^-24 of the sum each.  Behind that come an exponential
 logarithm, of lse and of logp (2^-22 of their sizes).
 
 Gradients: a word's coefficient is rounded to bf16 (2^-8 at most; 2^-9 on the average of its two ends), its exponential
-to fp16 (2^-12), and the result to bf16 (2^-8) or not at all.  Independent roundings of the terms add up like a norm:
+to fp16 (2^-11), and the result to bf16 (2^-8) or not at all.  Independent roundings of the terms add up like a norm:
 (2^-8 + 2^-11) sqrt(sum of squares), of which four are allowed, and 2^-8 of the norms over all values.
 """
 import numpy as np
