@@ -19,7 +19,7 @@
 // Why exponentials are kept and not computed again: the products are all but the
 // whole time (2 T D V flops each), and to compute x twice is a fourth beside the
 // three that have to be; keeping 16 bits of it costs 4 bytes a word and token of
-// memory traffic (0.6 of 16 ms at 8192 tokens of 128256 words).
+// memory traffic (0.74 of 17 ms at 8192 tokens of 128256 words).
 //
 // Rounding.  An exponential is kept as 2^(x c - I + 15) in fp16: 2^-11 relative at
 // most down to 2^-29 of the largest of its 128 words, and below that an error of
