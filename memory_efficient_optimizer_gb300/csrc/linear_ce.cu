@@ -72,7 +72,6 @@ constexpr double kCutOff = 0.54 / (1 << 25);
 constexpr int64_t kMostRows = int64_t{1} << 16, kMostWords = int64_t{1} << 17;
 constexpr int kScanThreads = 1024, kScanEach = 8;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -FLT_MAX;                   // I of a span without words
 // From here on the whole number I (or 15 - I) and x c are too far apart for fp32: such a span's
 // exponentials are relative to 2^(top c) itself, top its largest logit, and (top, -s) is kept
 // of it in place of (I, s).
@@ -328,13 +327,14 @@ struct LogitsEnd {
         if (i == at) a.xt[p.row] = v[i];
     }
     // (nothing but -inf or NaN leaves top at -inf: the sum is NaN or 0 then)
-    const float I = top > -INFINITY ? ceilf(fmaf(top, a.c_hi, top * a.c_lo)) : kNone;
-    const bool far = top > -INFINITY && fabsf(I) >= kFar;
+    const bool none = !(top > -INFINITY);
+    const float I = ceilf(fmaf(top, a.c_hi, top * a.c_lo));   // (-inf: no words)
+    const bool far = !none && fabsf(I) >= kFar;
     if (far) {
 #pragma unroll
       for (int i = 0; i < kSpan; ++i) v[i] -= top;
     }
-    const float shift = far ? 15.f : 15.f - I;
+    const float shift = far || none ? 15.f : 15.f - I;
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < kSpan; c += 32) {

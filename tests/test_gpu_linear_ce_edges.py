@@ -187,3 +187,27 @@ def test_one_gradient_alone(n, dim, vocab, dtype, weights):
         assert torch.equal(out, both.grad_hidden if only_hidden else both.grad_weight)
         assert torch.equal(loss, both.loss) and torch.equal(logp, both.logp) and torch.equal(lse, both.lse)
         assert ws[size:].eq(255).all()
+
+
+@pytest.mark.parametrize("low", [-3.3e38, -1e38, -1e20, -1e9])
+def test_nothing_but_masked_words(low):
+    """Every word held down, some with -inf: what is left are the words of the lowest finite logits, alike."""
+    n, dim, vocab = 5, 16, 500
+    h = torch.zeros(n, dim, dtype=BF)
+    h[:, 0] = 1
+    w = torch.zeros(vocab, dim, dtype=BF)
+    w[:, 0] = low
+    w[128:256, 0] = -float("inf")
+    w[3, 0] = -float("inf")
+    left = int((w[:, 0] > -float("inf")).sum())
+    y = torch.tensor([0, 127, 499, 300, 4])
+    out = meo.linear_cross_entropy(h.cuda(), w.cuda(), y.cuda())
+    x = w[0, 0].double().item()
+    assert np.all(np.abs(n64(out.logp) + np.log(left)) <= 2.0 ** -19)
+    assert np.all(np.abs(n64(out.lse) - (x + np.log(left))) <= 2.0 ** -22 * abs(x))
+    q = np.where(n64(w[:, 0]) == -np.inf, 0.0, 1 / left)
+    target = np.zeros(vocab)
+    target[y.numpy()] = 1
+    got = n64(out.grad_weight)[:, 0] * n                     # (the hidden states' first value is 1)
+    # the mean of q - 1[y = j], each off by 2^-8, and so is the result
+    assert np.all(np.abs(got - (n * q - target)) <= 2.0 ** -7 * (n * q + target) + 1e-7)
